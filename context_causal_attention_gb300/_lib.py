@@ -16,13 +16,21 @@ CP_OK = 0
 STATUS_NAMES = {
     0: "CP_OK", 1: "CP_ERR_NULL", 2: "CP_ERR_SHAPE", 3: "CP_ERR_DIVISIBILITY", 4: "CP_ERR_DTYPE",
     5: "CP_ERR_ALIGNMENT", 6: "CP_ERR_WORKSPACE", 7: "CP_ERR_UNSUPPORTED", 8: "CP_ERR_CUDA",
-    9: "CP_ERR_DEVICE_TIMEOUT", 10: "CP_ERR_ARGUMENT",
+    9: "CP_ERR_DEVICE_TIMEOUT", 10: "CP_ERR_ARGUMENT", 11: "CP_ERR_PAGE",
 }
 CP_BF16, CP_F32 = 0, 1
 CP_ZIGZAG, CP_CONTIGUOUS = 0, 1
 CP_SEQ_TO_HEAD, CP_HEAD_TO_SEQ = 0, 1
 CP_RANK_ORDER, CP_GLOBAL_ORDER = 0, 1
 CP_RING_PREFETCH, CP_RING_FUSED_MERGE, CP_RING_TF32 = 1, 2, 4
+CP_ROPE_HALF, CP_ROPE_INTERLEAVED = 0, 1
+CP_ROPE_PLAIN, CP_ROPE_LINEAR, CP_ROPE_BASE, CP_ROPE_BY_PARTS = 0, 1, 2, 3
+
+
+class RopeStruct(ctypes.Structure):
+    """cp_rope of include/cpattn.h."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot_dim", ctypes.c_int64), ("order", ctypes.c_int),
+                ("amplitude", ctypes.c_float)]
 
 
 class CpError(RuntimeError):
@@ -92,6 +100,20 @@ def lib():
     L.cp_attn_partial_f32.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, f32, vp, vp, vp, sz, vp]
     L.cp_ring_attention_fwd_noalloc.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, f32, i32, vp, i32, vp,
                                                 vp]
+    rp = ctypes.POINTER(RopeStruct)
+    f64 = ctypes.c_double
+    L.cp_rope_phases.argtypes = [vp, i64, vp]
+    L.cp_rope_freqs.argtypes = [i64, f64, i32, f64, f64, vp, ctypes.POINTER(f32)]
+    rope = [vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64, i32, rp, vp, vp, vp]
+    L.cp_rope_fwd.argtypes = rope
+    L.cp_rope_bwd.argtypes = rope
+    L.cp_qk_norm_rope_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64, i32, i32, f32, rp,
+                                      vp, vp, vp]
+    L.cp_qk_norm_rope_bwd_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
+    L.cp_qk_norm_rope_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64, i32, i32,
+                                      f32, rp, vp, vp, vp, vp, vp, sz, vp]
+    L.cp_cache_append.argtypes = [vp, vp, vp, i64, i64, i64, i32, i64, i64, i64, i64, vp, vp, i32, f32, rp, i64, vp,
+                                  vp, i64, i64, vp, i64, i64, vp, vp, vp, vp]
     for name in header_symbols():
         if name not in ("cp_status_string", "cp_version", "cp_last_cuda_error"):
             getattr(L, name).restype = ctypes.c_int

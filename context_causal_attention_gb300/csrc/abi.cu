@@ -16,6 +16,7 @@ extern "C" const char *cp_status_string(cp_status status) {
         case CP_ERR_CUDA: return "CP_ERR_CUDA: a CUDA call or kernel launch failed";
         case CP_ERR_DEVICE_TIMEOUT: return "CP_ERR_DEVICE_TIMEOUT: a kernel gave up a bounded device wait";
         case CP_ERR_ARGUMENT: return "CP_ERR_ARGUMENT: invalid argument";
+        case CP_ERR_PAGE: return "CP_ERR_PAGE: a page number, length or count in device memory is out of range";
     }
     return "unknown cp_status";
 }

@@ -1186,11 +1186,12 @@ extern "C" cp_status cp_device_status(int *code, int clear, cudaStream_t stream)
         const int zero = 0;
         if (cudaMemcpyToSymbol(cpattn::g_cp_device_status, &zero, sizeof(int)) != cudaSuccess) return CP_ERR_CUDA;
     }
-    // the backward and tf32 kernels keep their own words (other translation units)
-    int vt = 0;
+    // the backward, tf32 and cache kernels keep their own words (other translation units)
+    int vt = 0, vc = 0;
     cp_status st = cpattn::read_bwd_device_status(&vb, clear != 0);
     if (st == CP_OK) st = cpattn::read_tf32_device_status(&vt, clear != 0);
+    if (st == CP_OK) st = cpattn::read_cache_device_status(&vc, clear != 0);
     if (st != CP_OK) return st;
-    *code = v != 0 ? v : (vb != 0 ? vb : vt);
+    *code = v != 0 ? v : (vb != 0 ? vb : (vt != 0 ? vt : vc));
     return CP_OK;
 }

@@ -1,0 +1,253 @@
+// cache.cu -- appending the keys and values of new tokens to a paged cache,
+// with the keys' norm and rotation (and the queries') on the way.
+//
+// Token j of the n_b new tokens of sequence b gets own index i = kv_len[b] -
+// n_b + j, position pos_base + i, and slot i % page_size of page
+// table[b][i / page_size].  K: norm, rotation, bf16, into that slot; V: bf16,
+// into the same slot of the other cache; Q: norm, rotation, bf16, in place
+// order.  Norm and rotation as in rope.cu.
+//
+// Memory-bound where there are many tokens and latency-bound at one token for
+// each sequence, so one launch does all three tensors: a warp takes a token
+// (or a few of its heads when there are few tokens), finds its sequence with a
+// 32-way search over the cumulative counts (one load per lane and level, two
+// levels up to 1024 sequences), works out the sines once and streams the rows.
+// Every index that comes from device memory is checked before it is used: a
+// bad one skips the token and sets the device status word.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "cp_internal.h"
+#include "cp_paged.cuh"
+#include "cp_rope.cuh"
+
+namespace cpattn {
+namespace {
+
+__device__ int g_cache_status = 0;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+struct AppendArgs {
+    const void *x[3];  // q, k, v rows
+    long long xs[3];   // elements between tokens
+    int heads[3];
+    __nv_bfloat16 *q_out, *cache[2];
+    const void *w[2];
+    int w_bf16, norm[2];
+    float eps;
+    RopeDev rope;
+    PageTable pt;
+    const int32_t *cu, *kv_len;
+    long long tokens, pos_base;
+    int chunks, hpu;
+};
+
+template <typename T, int D, int kOrder>
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs a) {
+    using Map = LaneMap<D, kOrder>;
+    constexpr int kU = sizeof(T) == 2 ? 2 : 1;
+    const int lane = threadIdx.x & 31, sub = lane / Map::L;
+    const Map map(lane, a.rope.half);
+    unsigned long long f[Map::kAng];
+    load_freqs(a.rope, lane, f);
+    const int all = a.heads[0] + a.heads[1] + a.heads[2];
+    const long long units = a.tokens * a.chunks;
+    const long long step = static_cast<long long>(gridDim.x) * kWarps;
+    for (long long u = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units; u += step) {
+        const int tok = static_cast<int>(a.chunks == 1 ? u : u / a.chunks);
+        const int first = static_cast<int>(u - static_cast<long long>(tok) * a.chunks) * a.hpu;
+        const int last = min(first + a.hpu, all);
+        int begin, count;
+        const int b = find_sequence(a.cu, a.pt.B, tok, lane, &begin, &count);
+        if (b < 0) continue;  // a row behind the last sequence
+        const long long idx = static_cast<long long>(__ldg(a.kv_len + b)) - count + (tok - begin);
+        const long long slot = a.pt.slot(b, idx);
+        if (slot < 0) {
+            if (lane == 0) atomicExch(&g_cache_status, static_cast<int>(CP_ERR_PAGE));
+            continue;
+        }
+        float c[8], s[8];
+        token_angles<D>(f, a.pos_base + idx, a.rope.amp, lane, c, s);
+#pragma unroll 1
+        for (int t = 0; t < 3; ++t) {
+            const int base = t == 0 ? 0 : (t == 1 ? a.heads[0] : a.heads[0] + a.heads[1]);
+            const int h0 = max(first - base, 0), h1 = min(last - base, a.heads[t]);
+            if (h0 >= h1) continue;
+            const T *x = static_cast<const T *>(a.x[t]) + tok * a.xs[t];
+            __nv_bfloat16 *y = t == 0 ? a.q_out + static_cast<long long>(tok) * a.heads[0] * D
+                                      : a.cache[t - 1] + slot * a.heads[1] * D;
+            const bool norm = t < 2 && a.norm[t];
+            float w[16];
+            if (norm) {
+                if (a.w_bf16) {
+                    Vec8<__nv_bfloat16> v;
+                    v.load(static_cast<const __nv_bfloat16 *>(a.w[t]) + map.c0);
+                    v.to(w);
+                    v.load(static_cast<const __nv_bfloat16 *>(a.w[t]) + map.c1);
+                    v.to(w + 8);
+                } else {
+                    Vec8<float> v;
+                    v.load(static_cast<const float *>(a.w[t]) + map.c0);
+                    v.to(w);
+                    v.load(static_cast<const float *>(a.w[t]) + map.c1);
+                    v.to(w + 8);
+                }
+            }
+            const uint32_t mask = t < 2 ? map.mask : 0u;
+            for (int hb = h0; hb < h1; hb += kU * Map::kRows) {
+                Vec8<T> v0[kU], v1[kU];
+#pragma unroll
+                for (int i = 0; i < kU; ++i) {
+                    const int h = hb + i * Map::kRows + sub;
+                    if (h < h1) {
+                        v0[i].load(x + h * D + map.c0);
+                        v1[i].load(x + h * D + map.c1);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kU; ++i) {
+                    if (hb + i * Map::kRows >= h1) break;  // uniform over the warp
+                    const int h = hb + i * Map::kRows + sub;
+                    float r[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[e] = 0.f;
+                    if (h < h1) {
+                        v0[i].to(r);
+                        v1[i].to(r + 8);
+                    }
+                    if (norm) {
+                        float q = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) q = fmaf(r[e], r[e], q);
+                        const float rstd = 1.f / sqrtf(row_sum<Map::L>(q) * (1.f / D) + a.eps);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) r[e] = r[e] * rstd * w[e];
+                    }
+                    turn_pairs<kOrder>(r, c, s, mask);
+                    if (h < h1) {
+                        store8(y + h * D + map.c0, r);
+                        store8(y + h * D + map.c1, r + 8);
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int D, int kOrder>
+cp_status launch_append(AppendArgs &a, cudaStream_t stream) {
+    constexpr int rows = LaneMap<D, kOrder>::kRows;
+    const int heads = a.heads[0] + a.heads[1] + a.heads[2], most = (heads + rows - 1) / rows;
+    // all heads of a token in one unit, fewer where there are too few tokens to give every SM 16 warps
+    long long chunks = (static_cast<long long>(sm_count()) * 16 + a.tokens - 1) / a.tokens;
+    chunks = chunks < 1 ? 1 : (chunks > most ? most : chunks);
+    a.hpu = static_cast<int>((most + chunks - 1) / chunks) * rows;
+    a.chunks = (heads + a.hpu - 1) / a.hpu;
+    const long long blocks = (a.tokens * a.chunks + kWarps - 1) / kWarps;
+    const long long cap = static_cast<long long>(sm_count()) * 4;
+    append_kernel<T, D, kOrder><<<static_cast<unsigned>(blocks < cap ? blocks : cap), kThreads, 0, stream>>>(a);
+    return last_launch_status();
+}
+
+bool misaligned(const void *p) { return p && !aligned16(p); }
+
+}  // namespace
+
+cp_status read_cache_device_status(int *code, bool clear) {
+    if (cudaMemcpyFromSymbol(code, g_cache_status, sizeof(int)) != cudaSuccess) return CP_ERR_CUDA;
+    if (clear) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_cache_status, &zero, sizeof(int)) != cudaSuccess) return CP_ERR_CUDA;
+    }
+    return CP_OK;
+}
+
+cp_status check_pages(int64_t n_pages, int64_t page_size, int64_t B, int64_t max_pages, int64_t Nkv, int64_t D) {
+    if (n_pages < 1 || n_pages > INT32_MAX || B < 1 || B > kMaxSequences || max_pages < 1 || max_pages > INT32_MAX ||
+        Nkv < 1 || Nkv > 65535)
+        return CP_ERR_SHAPE;
+    if (D != 64 && D != 128) return CP_ERR_UNSUPPORTED;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return CP_ERR_UNSUPPORTED;
+    if (n_pages * page_size > INT32_MAX || max_pages * page_size > INT32_MAX) return CP_ERR_SHAPE;
+    return CP_OK;
+}
+
+}  // namespace cpattn
+
+using namespace cpattn;
+
+extern "C" cp_status cp_cache_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                     int64_t v_stride, cp_dtype dtype, int64_t R, int64_t N, int64_t Nkv, int64_t D,
+                                     const void *wq, const void *wk, cp_dtype w_dtype, float eps, const cp_rope *rope,
+                                     int64_t pos_base, void *k_cache, void *v_cache, int64_t n_pages,
+                                     int64_t page_size, const int32_t *table, int64_t B, int64_t max_pages,
+                                     const int32_t *cu_new, const int32_t *kv_len, void *q_out, cudaStream_t stream) {
+    if (!k || !v || !k_cache || !v_cache || !table || !cu_new || !kv_len || (N > 0 && (!q || !q_out)))
+        return CP_ERR_NULL;
+    if (R < 1 || R > INT32_MAX / 2 || N < 0 || N > 65535) return CP_ERR_SHAPE;
+    cp_status st = check_pages(n_pages, page_size, B, max_pages, Nkv, D);
+    if (st != CP_OK) return st;
+    const size_t es = dtype_size(dtype);
+    if (!es || !dtype_size(w_dtype)) return CP_ERR_DTYPE;
+    if ((st = check_rope(rope, D)) != CP_OK) return st;
+    if ((N && q_stride < N * D) || k_stride < Nkv * D || v_stride < Nkv * D || q_stride > INT32_MAX ||
+        k_stride > INT32_MAX || v_stride > INT32_MAX)
+        return CP_ERR_SHAPE;
+    if ((wq || wk) && !(std::isfinite(eps) && eps >= 0.f)) return CP_ERR_ARGUMENT;
+    if (pos_base < INT32_MIN || pos_base > INT32_MAX) return CP_ERR_ARGUMENT;
+    if ((N && q_stride * es % 16) || k_stride * es % 16 || v_stride * es % 16 || misaligned(q) || misaligned(k) ||
+        misaligned(v) || misaligned(k_cache) || misaligned(v_cache) || misaligned(q_out) || misaligned(wq) ||
+        misaligned(wk) || (reinterpret_cast<uintptr_t>(table) & 3u) || (reinterpret_cast<uintptr_t>(cu_new) & 3u) ||
+        (reinterpret_cast<uintptr_t>(kv_len) & 3u))
+        return CP_ERR_ALIGNMENT;
+    if (k_cache == v_cache) return CP_ERR_ARGUMENT;
+    // q_out: dense rows; in place only where the query rows are dense bf16 themselves
+    if (N) {
+        const char *o0 = static_cast<const char *>(q_out), *o1 = o0 + R * N * D * 2;
+        auto meets = [&](const void *p, int64_t stride, int64_t heads) {
+            const char *p0 = static_cast<const char *>(p), *p1 = p0 + ((R - 1) * stride + heads * D) * es;
+            return o0 < p1 && p0 < o1;
+        };
+        const bool in_place = q == q_out && dtype == CP_BF16 && q_stride == N * D;
+        if ((!in_place && meets(q, q_stride, N)) || meets(k, k_stride, Nkv) || meets(v, v_stride, Nkv))
+            return CP_ERR_ARGUMENT;
+    }
+    AppendArgs a{};
+    a.x[0] = q, a.x[1] = k, a.x[2] = v;
+    a.xs[0] = q_stride, a.xs[1] = k_stride, a.xs[2] = v_stride;
+    a.heads[0] = static_cast<int>(N), a.heads[1] = a.heads[2] = static_cast<int>(Nkv);
+    a.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    a.cache[0] = static_cast<__nv_bfloat16 *>(k_cache);
+    a.cache[1] = static_cast<__nv_bfloat16 *>(v_cache);
+    a.w[0] = wq, a.w[1] = wk;
+    a.norm[0] = wq != nullptr, a.norm[1] = wk != nullptr;
+    a.w_bf16 = w_dtype == CP_BF16;
+    a.eps = eps;
+    if (rope) {
+        a.rope.freqs = reinterpret_cast<const unsigned long long *>(rope->freqs);
+        a.rope.half = static_cast<int>(rope->rot_dim / 2);
+        a.rope.amp = rope->amplitude;
+    }
+    a.pt.table = table;
+    a.pt.B = static_cast<int>(B);
+    a.pt.max_pages = static_cast<int>(max_pages);
+    a.pt.n_pages = static_cast<int>(n_pages);
+    a.pt.shift = __builtin_ctzll(static_cast<unsigned long long>(page_size));
+    a.cu = cu_new;
+    a.kv_len = kv_len;
+    a.tokens = R;
+    a.pos_base = pos_base;
+    const bool inter = rope && rope->order == CP_ROPE_INTERLEAVED;
+    if (dtype == CP_BF16) {
+        using T = __nv_bfloat16;
+        if (D == 128) return inter ? launch_append<T, 128, 1>(a, stream) : launch_append<T, 128, 0>(a, stream);
+        return inter ? launch_append<T, 64, 1>(a, stream) : launch_append<T, 64, 0>(a, stream);
+    }
+    if (D == 128) return inter ? launch_append<float, 128, 1>(a, stream) : launch_append<float, 128, 0>(a, stream);
+    return inter ? launch_append<float, 64, 1>(a, stream) : launch_append<float, 64, 0>(a, stream);
+}

@@ -206,4 +206,12 @@ cp_status launch_bwd(const BwdProblem &p, cudaStream_t stream);
 // Sticky device status word of the backward kernels (read and optionally cleared).
 cp_status read_bwd_device_status(int *code, bool clear);
 
+// ------------------------------------------------------------ rotation, cache
+// Checks of a rotation's description (NULL: no rotation) for head size D.
+cp_status check_rope(const cp_rope *rope, int64_t D);
+// Checks of a paged cache's sizes.
+cp_status check_pages(int64_t n_pages, int64_t page_size, int64_t B, int64_t max_pages, int64_t Nkv, int64_t D);
+// Sticky device status word of the append kernels (read and optionally cleared).
+cp_status read_cache_device_status(int *code, bool clear);
+
 }  // namespace cpattn

@@ -11,16 +11,19 @@ import torch
 
 from . import _lib
 from ._lib import (CP_BF16, CP_CONTIGUOUS, CP_F32, CP_GLOBAL_ORDER, CP_HEAD_TO_SEQ, CP_RANK_ORDER,
-                   CP_RING_FUSED_MERGE, CP_RING_PREFETCH, CP_RING_TF32, CP_SEQ_TO_HEAD, CP_ZIGZAG, CpError)
+                   CP_RING_FUSED_MERGE, CP_RING_PREFETCH, CP_RING_TF32, CP_ROPE_BASE, CP_ROPE_BY_PARTS, CP_ROPE_HALF,
+                   CP_ROPE_INTERLEAVED, CP_ROPE_LINEAR, CP_ROPE_PLAIN, CP_SEQ_TO_HEAD, CP_ZIGZAG, CpError, RopeStruct)
 
 __all__ = [
     "cp_zigzag_shard", "cp_zigzag_unshard", "cp_zigzag_positions", "cp_ulysses_relayout", "cp_attn_partial",
     "cp_attn_workspace_size",
     "cp_lse_merge", "cp_ring_workspace_size", "cp_ring_attention_fwd", "cp_ring_attention_fwd_noalloc",
     "cp_allgather_attention_fwd", "cp_ulysses_attention_fwd",
-    "cp_device_status", "cp_version",
+    "cp_device_status", "cp_version", "cp_rope_freqs", "cp_rope_phases", "cp_rope_fwd", "cp_rope_bwd",
+    "cp_qk_norm_rope_fwd", "cp_qk_norm_rope_bwd_workspace_size", "cp_qk_norm_rope_bwd", "cp_cache_append",
     "CP_BF16", "CP_F32", "CP_ZIGZAG", "CP_CONTIGUOUS", "CP_SEQ_TO_HEAD", "CP_HEAD_TO_SEQ", "CP_RANK_ORDER",
-    "CP_GLOBAL_ORDER", "CP_RING_PREFETCH", "CP_RING_FUSED_MERGE", "CP_RING_TF32", "CpError",
+    "CP_GLOBAL_ORDER", "CP_RING_PREFETCH", "CP_RING_FUSED_MERGE", "CP_RING_TF32", "CP_ROPE_HALF",
+    "CP_ROPE_INTERLEAVED", "CP_ROPE_PLAIN", "CP_ROPE_LINEAR", "CP_ROPE_BASE", "CP_ROPE_BY_PARTS", "CpRope", "CpError",
 ]
 
 _DT = {torch.bfloat16: CP_BF16, torch.float32: CP_F32}
@@ -383,6 +386,246 @@ def cp_ring_attention_fwd_noalloc(q_sh, k_sh, v_sh, pos, o, lse, scale=None, lay
                                                   _stream(stream))
     _lib.check("cp_ring_attention_fwd_noalloc", st)
     return o, lse
+
+
+class CpRope:
+    """A rotation (cp_rope of the C header): frequencies on the device, rotated
+    part, order of the pairs, amplitude.  Made by cp_rope_freqs or
+    cp_rope_phases and kept by the caller."""
+
+    def __init__(self, freqs, rot_dim, order, amplitude):
+        self.freqs, self.rot_dim, self.order, self.amplitude = freqs, rot_dim, order, amplitude
+        self._ref = ctypes.byref(RopeStruct(freqs.data_ptr(), rot_dim, order, amplitude))
+
+
+def cp_rope_freqs(rot_dim, base=10000.0, scaling=CP_ROPE_PLAIN, factor=1.0, original_len=0, order=CP_ROPE_HALF,
+                  device="cuda"):
+    """Frequencies base^(-2i/rot_dim) under one of the header's scalings -> CpRope on `device`."""
+    f = torch.empty(max(rot_dim // 2, 1), dtype=torch.int64)
+    amp = ctypes.c_float(0.0)
+    _lib.check("cp_rope_freqs", _lib.lib().cp_rope_freqs(rot_dim, base, scaling, factor, original_len, f.data_ptr(),
+                                                         ctypes.byref(amp)))
+    return CpRope(f.to(device), rot_dim, order, amp.value)
+
+
+def cp_rope_phases(inv_freq, amplitude=1.0, order=CP_ROPE_HALF, device="cuda"):
+    """Any other frequencies, in radians per position -> CpRope on `device`."""
+    w = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+    f = torch.empty(w.numel(), dtype=torch.int64)
+    _lib.check("cp_rope_phases", _lib.lib().cp_rope_phases(w.data_ptr(), w.numel(), f.data_ptr()))
+    return CpRope(f.to(device), 2 * w.numel(), order, amplitude)
+
+
+def _here(*ts):
+    """Every given tensor lies on the current CUDA device."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and not (t.is_cuda and t.device.index == dev):
+            raise ValueError("tensor must be on the current CUDA device")
+
+
+def _head_rows(t):
+    """(elements between tokens, tokens' leading shape, heads, D) of [..., heads, D] whose
+    head rows are dense and whose tokens lie at one distance from one another."""
+    if t.dim() < 3:
+        raise ValueError("expected [..., heads, D] with at least one leading dimension")
+    shape, st = t.shape, t.stride()
+    H, D = shape[-2], shape[-1]
+    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
+        raise ValueError("the head rows of a token must be dense")
+    step, n = 0, 1
+    for i in range(t.dim() - 3, -1, -1):
+        if shape[i] > 1:
+            if step == 0:
+                step = st[i]
+            elif st[i] != step * n:
+                raise ValueError("tokens must lie at one distance from one another")
+            n *= shape[i]
+    return (step if n > 1 else max(H * D, 8)), shape[:-2], H, D
+
+
+def _tokens(lead):
+    """(C, B, s) of leading dimensions [C, B, s], [B, s] or [s]."""
+    if len(lead) > 3:
+        raise ValueError("expected [C, B, s, heads, D], [B, s, heads, D] or [s, heads, D]")
+    return (1, 1, 1)[:3 - len(lead)] + tuple(lead)
+
+
+def _qk(q, k):
+    """Common description of q and k (k may be None): (C, B, s, N, Nkv, D, q stride, k stride)."""
+    qs, lead, N, D = _head_rows(q)
+    ks, Nkv = 0, 0
+    if k is not None:
+        ks, lead_k, Nkv, Dk = _head_rows(k)
+        if lead_k != lead or Dk != D or k.dtype != q.dtype:
+            raise ValueError("q and k must have the same tokens, head size and dtype")
+    C, B, s = _tokens(lead)
+    return C, B, s, N, Nkv, D, qs, ks
+
+
+def _check_pos(pos, C, s):
+    if pos.dtype != torch.int32 or pos.numel() != C * s or not pos.is_contiguous():
+        raise ValueError("pos must be contiguous int32 [C, s]")
+
+
+def _row_out(out, x):
+    """An output of x's rows: a new dense one, x itself (in place), or a dense one that was given."""
+    if x is None:
+        return None
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("an output must have its input's shape and dtype")
+    if out.data_ptr() == x.data_ptr():
+        if out.stride() != x.stride():
+            raise ValueError("an output in place must have its input's strides")
+    elif not out.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return out
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rope_call(name, q, k, pos, rope, q_out, k_out, stream):
+    C, B, s, N, Nkv, D, qs, ks = _qk(q, k)
+    _check_pos(pos, C, s)
+    q_out, k_out = _row_out(q_out, q), _row_out(k_out, k)
+    _here(q, k, pos, rope.freqs, q_out, k_out)
+    st = getattr(_lib.lib(), name)(_addr(q), _addr(k), _addr(pos), C, B, s, N, Nkv, D, qs, ks, _dtype_code(q),
+                                   rope._ref, _addr(q_out), _addr(k_out), _stream(stream))
+    _lib.check(name, st)
+    return q_out, k_out
+
+
+def cp_rope_fwd(q, k, pos, rope, q_out=None, k_out=None, stream=None):
+    """Rotate q [C,B,s,N,D] and k [C,B,s,Nkv,D] (or [B,s,..], [s,..]; k may be None) by
+    their tokens' positions pos [C,s] -> (q_out, k_out).  Rows may be strided
+    (slices of a fused projection); outputs dense, or the inputs themselves."""
+    return _rope_call("cp_rope_fwd", q, k, pos, rope, q_out, k_out, stream)
+
+
+def cp_rope_bwd(dq_out, dk_out, pos, rope, dq=None, dk=None, stream=None):
+    """Gradients of cp_rope_fwd's inputs from those of its outputs -> (dq, dk)."""
+    return _rope_call("cp_rope_bwd", dq_out, dk_out, pos, rope, dq, dk, stream)
+
+
+def _check_weights(wq, wk, D):
+    for w in (wq, wk):
+        if w is not None and (w.numel() != D or not w.is_contiguous()):
+            raise ValueError("norm weights must be contiguous [D]")
+    if wq is not None and wk is not None and wq.dtype != wk.dtype:
+        raise ValueError("wq and wk must have the same dtype")
+    w = wq if wq is not None else wk
+    return CP_F32 if w is None else _dtype_code(w)
+
+
+def cp_qk_norm_rope_fwd(q, k, wq, wk, pos, rope, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Root-mean-square norm of every head row of q and k with weights wq, wk
+    [D], then the rotation of cp_rope_fwd (rope None: norm alone) -> (q_out, k_out)."""
+    C, B, s, N, Nkv, D, qs, ks = _qk(q, k)
+    if rope is not None:
+        _check_pos(pos, C, s)
+    wd = _check_weights(wq, wk, D)
+    q_out, k_out = _row_out(q_out, q), _row_out(k_out, k)
+    _here(q, k, wq, wk, pos, None if rope is None else rope.freqs, q_out, k_out)
+    st = _lib.lib().cp_qk_norm_rope_fwd(_addr(q), _addr(k), _addr(wq), _addr(wk), _addr(pos), C, B, s, N, Nkv, D, qs,
+                                        ks, _dtype_code(q), wd, eps, None if rope is None else rope._ref,
+                                        _addr(q_out), _addr(k_out), _stream(stream))
+    _lib.check("cp_qk_norm_rope_fwd", st)
+    return q_out, k_out
+
+
+def cp_qk_norm_rope_bwd_workspace_size(C, B, s, N, Nkv, D):
+    n = ctypes.c_size_t(0)
+    _lib.check("cp_qk_norm_rope_bwd_workspace_size",
+               _lib.lib().cp_qk_norm_rope_bwd_workspace_size(C, B, s, N, Nkv, D, ctypes.byref(n)))
+    return n.value
+
+
+def cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, pos, rope, eps=1e-6, dq=None, dk=None, dwq=None, dwk=None,
+                        workspace=None, stream=None):
+    """Gradients of cp_qk_norm_rope_fwd -> (dq, dk, dwq fp32 [D], dwk fp32 [D])
+    from the dense gradients of its outputs and its inputs."""
+    C, B, s, N, Nkv, D, qs, ks = _qk(q, k)
+    if rope is not None:
+        _check_pos(pos, C, s)
+    wd = _check_weights(wq, wk, D)
+    for g, x in ((dq_out, q), (dk_out, k)):
+        if (g is None) != (x is None) or (g is not None and (g.shape != x.shape or g.dtype != x.dtype or
+                                                             not g.is_contiguous())):
+            raise ValueError("the gradients must be dense, of the inputs' shapes and dtype")
+    dq = dq_out if dq is dq_out else _row_out(dq, q)
+    dk = dk_out if dk is dk_out else _row_out(dk, k)
+    if dwq is None:
+        dwq = torch.empty(D, dtype=torch.float32, device=q.device)
+    if dwk is None and k is not None:
+        dwk = torch.empty(D, dtype=torch.float32, device=q.device)
+    for w in (dwq, dwk):
+        if w is not None and (w.dtype != torch.float32 or w.numel() != D or not w.is_contiguous()):
+            raise ValueError("weight gradients must be contiguous fp32 [D]")
+    if workspace is None:
+        workspace = torch.empty(max(256, cp_qk_norm_rope_bwd_workspace_size(C, B, s, N, Nkv, D)), dtype=torch.uint8,
+                                device=q.device)
+    _here(dq_out, dk_out, q, k, wq, wk, pos, None if rope is None else rope.freqs, dq, dk, dwq, dwk, workspace)
+    st = _lib.lib().cp_qk_norm_rope_bwd(_addr(dq_out), _addr(dk_out), _addr(q), _addr(k), _addr(wq), _addr(wk),
+                                        _addr(pos), C, B, s, N, Nkv, D, qs, ks, _dtype_code(q), wd, eps,
+                                        None if rope is None else rope._ref, _addr(dq), _addr(dk), _addr(dwq),
+                                        _addr(dwk), _addr(workspace), workspace.numel() * workspace.element_size(),
+                                        _stream(stream))
+    _lib.check("cp_qk_norm_rope_bwd", st)
+    return dq, dk, dwq, dwk
+
+
+def _check_cache(k_cache, v_cache, table, cu_new, kv_len):
+    """(n_pages, page_size, Nkv, D, B, max_pages) of a paged cache and its lists."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("the caches must be [n_pages, page_size, Nkv, D], both alike")
+    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
+        raise TypeError("the caches must be bf16")
+    if table.dim() != 2 or kv_len.dim() != 1 or cu_new.dim() != 1 or kv_len.numel() != table.shape[0] or \
+            cu_new.numel() != table.shape[0] + 1:
+        raise ValueError("table [B, max_pages], cu_new [B + 1] and kv_len [B] must agree")
+    for t in (table, cu_new, kv_len):
+        if t.dtype != torch.int32:
+            raise TypeError("table, cu_new and kv_len must be int32")
+    for t in (k_cache, v_cache, table, cu_new, kv_len):
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+    return tuple(k_cache.shape) + tuple(table.shape)
+
+
+def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=None, q_out=None, wq=None, wk=None,
+                    eps=1e-6, pos_base=0, stream=None):
+    """Append the new tokens' k, v [R,Nkv,D] to the pages of their sequences,
+    k normed (wk) and rotated (rope) on the way; q [R,N,D], if given, likewise into
+    q_out bf16 [R,N,D].  kv_len counts each sequence's tokens after the call.
+    Returns q_out (None without q)."""
+    n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
+    if k.dim() != 3 or v.dim() != 3 or k.shape != v.shape or k.shape[1] != Nkv or k.shape[2] != D or \
+            v.dtype != k.dtype:
+        raise ValueError("k and v must be [R, Nkv, D] of the cache's heads, of one dtype")
+    ks, vs = _head_rows(k)[0], _head_rows(v)[0]
+    R, qs, N = k.shape[0], 0, 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != R or q.shape[2] != D or q.dtype != k.dtype:
+            raise ValueError("q must be [R, N, D] of k's tokens and dtype")
+        qs, N = _head_rows(q)[0], q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((R, N, D), dtype=torch.bfloat16, device=q.device)
+        elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous bf16 [R, N, D]")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    wd = _check_weights(wq, wk, D)
+    _here(q, k, v, k_cache, v_cache, table, cu_new, kv_len, wq, wk, None if rope is None else rope.freqs, q_out)
+    st = _lib.lib().cp_cache_append(_addr(q), _addr(k), _addr(v), qs, ks, vs, _dtype_code(k), R, N, Nkv, D, _addr(wq),
+                                    _addr(wk), wd, eps, None if rope is None else rope._ref, pos_base, _addr(k_cache),
+                                    _addr(v_cache), n_pages, page, _addr(table), B, max_pages, _addr(cu_new),
+                                    _addr(kv_len), _addr(q_out), _stream(stream))
+    _lib.check("cp_cache_append", st)
+    return q_out
 
 
 def cp_selftest_stalled_producer(q, k, v, pos, o, lse, timeout_ns, stream=None):

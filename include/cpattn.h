@@ -52,13 +52,22 @@ typedef enum cp_status {
     CP_ERR_UNSUPPORTED = 7,   /* e.g. D not in {64, 128} for attention */
     CP_ERR_CUDA = 8,          /* a CUDA runtime call or launch failed */
     CP_ERR_DEVICE_TIMEOUT = 9,/* a kernel gave up a bounded wait (see cp_device_status) */
-    CP_ERR_ARGUMENT = 10      /* any other invalid argument (scale, enum, event count) */
+    CP_ERR_ARGUMENT = 10,     /* any other invalid argument (scale, enum, event count) */
+    CP_ERR_PAGE = 11          /* a page number, length or count in device memory is out of range
+                                 (device status word only, see cp_device_status) */
 } cp_status;
 
 typedef enum cp_dtype { CP_BF16 = 0, CP_F32 = 1 } cp_dtype;
 typedef enum cp_layout { CP_ZIGZAG = 0, CP_CONTIGUOUS = 1 } cp_layout;
 typedef enum cp_dir { CP_SEQ_TO_HEAD = 0, CP_HEAD_TO_SEQ = 1 } cp_dir;
 typedef enum cp_seq_order { CP_RANK_ORDER = 0, CP_GLOBAL_ORDER = 1 } cp_seq_order;
+typedef enum cp_rope_order { CP_ROPE_HALF = 0, CP_ROPE_INTERLEAVED = 1 } cp_rope_order;
+typedef enum cp_rope_scaling {
+    CP_ROPE_PLAIN = 0,
+    CP_ROPE_LINEAR = 1,
+    CP_ROPE_BASE = 2,
+    CP_ROPE_BY_PARTS = 3
+} cp_rope_scaling;
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *cp_status_string(cp_status status);
@@ -420,6 +429,146 @@ cp_status cp_ring_attention_bwd(const void *q_sh, const void *k_sh, const void *
                                 cudaStream_t stream);
 
 /*
+ * cp_rope -- a rotation of head rows by their token's position.  The first
+ * rot_dim values of a row of D form rot_dim/2 pairs, which at position t become
+ *   a' = A (a cos t theta_i - b sin t theta_i)
+ *   b' = A (b cos t theta_i + a sin t theta_i)
+ * and the other D - rot_dim values stay as they are.
+ *   freqs     : device uint64 [rot_dim/2], turns per position in 64-bit fixed
+ *               point, theta_i / (2 pi) * 2^64 modulo 2^64 (cp_rope_freqs, cp_rope_phases,
+ *               copied to the device by the caller and kept as long as calls use
+ *               it); positions of any size lose no precision
+ *   order     : CP_ROPE_HALF pairs value i with value i + rot_dim/2,
+ *               CP_ROPE_INTERLEAVED pairs 2i with 2i + 1
+ *   rot_dim   : even, 2 .. D; a multiple of 16 for CP_ROPE_HALF
+ *               (CP_ERR_UNSUPPORTED else)
+ *   amplitude : A, finite (1 unless the scaling says otherwise)
+ * The struct itself is read on the host during the call.
+ */
+typedef struct cp_rope {
+    const uint64_t *freqs;
+    int64_t rot_dim;
+    cp_rope_order order;
+    float amplitude;
+} cp_rope;
+
+/*
+ * cp_rope_freqs / cp_rope_phases -- frequencies of a rotation, into host memory.
+ * cp_rope_freqs: theta_i = base^(-2i/rot_dim), i < rot_dim/2, and for a context
+ * `factor` (>= 1) times longer than the one trained on
+ *   CP_ROPE_PLAIN    : as they are (factor and original_len are not read)
+ *   CP_ROPE_LINEAR   : theta_i / factor (positions interpolated)
+ *   CP_ROPE_BASE     : base * factor^(rot_dim/(rot_dim-2)) in the place of base
+ *   CP_ROPE_BY_PARTS : theta_i / factor for pairs that turn less than once over
+ *                      original_len positions, theta_i for those that turn more
+ *                      than 32 times, a linear ramp over the number of turns
+ *                      between; *amplitude = 0.1 ln(factor) + 1
+ * *amplitude is 1 for the others.  cp_rope_phases: any other rule, from n
+ * angular frequencies in radians per position (each finite, at most 2 pi in
+ * size, n <= 4096).  Both compute in fp64.
+ */
+cp_status cp_rope_freqs(int64_t rot_dim, double base, cp_rope_scaling scaling, double factor, double original_len,
+                        uint64_t *freqs, float *amplitude);
+cp_status cp_rope_phases(const double *inv_freq, int64_t n, uint64_t *freqs);
+
+/*
+ * cp_rope_fwd / cp_rope_bwd -- rotate the rows of q and k by their positions
+ * before the attention ([OCP] Introduction: apply_rope(q, k, local_positions)),
+ * and rotate gradients back (dx = A R(-t) dy).
+ *   q, k  : device, rows of N and Nkv heads of D values (`dtype`), token
+ *           ((c*B + b)*s + i) at element offset token * q_stride (k_stride);
+ *           dense shards [C][B][s][N][D] have q_stride = N*D, q and k inside
+ *           the rows of a fused projection have its row length.  Either may be
+ *           left out (NULL with N = 0 or Nkv = 0).
+ *   pos   : device int32 [C][s], the position of token (c, b, i) is pos[c][i]
+ *           (cp_zigzag_positions for shards; C = B = 1: one per token); any value
+ *   q_out, k_out : device, `dtype`; written dense, or in place where the
+ *           pointer equals q (k), then with its stride.  Any other overlap with
+ *           q, k or one another is refused (CP_ERR_ARGUMENT).
+ *   cp_rope_bwd takes the gradients of the rotated rows and writes those of
+ *   the unrotated ones; the same arguments.
+ * Strides are multiples of 16 bytes; pointers 16-byte aligned (pos 4); D in
+ * {64, 128}.  Computed in fp32 and rounded once.
+ */
+cp_status cp_rope_fwd(const void *q, const void *k, const int32_t *pos, int64_t C, int64_t B, int64_t s, int64_t N,
+                      int64_t Nkv, int64_t D, int64_t q_stride, int64_t k_stride, cp_dtype dtype,
+                      const cp_rope *rope, void *q_out, void *k_out, cudaStream_t stream);
+cp_status cp_rope_bwd(const void *dq_out, const void *dk_out, const int32_t *pos, int64_t C, int64_t B, int64_t s,
+                      int64_t N, int64_t Nkv, int64_t D, int64_t q_stride, int64_t k_stride, cp_dtype dtype,
+                      const cp_rope *rope, void *dq, void *dk, cudaStream_t stream);
+
+/*
+ * cp_qk_norm_rope_fwd -- the root-mean-square norm of every head row of q and
+ * k, its weights, and the rotation of cp_rope_fwd in the same pass:
+ *   y = A R(t) (w . x r),  r = (mean_j x_j^2 + eps)^(-1/2)
+ *   wq, wk  : device [D] of w_dtype, one weight vector for all heads of q (k)
+ *   eps     : finite, >= 0
+ *   rope    : NULL for the norm alone (pos is not read then)
+ * Everything else as for cp_rope_fwd.
+ */
+cp_status cp_qk_norm_rope_fwd(const void *q, const void *k, const void *wq, const void *wk, const int32_t *pos,
+                              int64_t C, int64_t B, int64_t s, int64_t N, int64_t Nkv, int64_t D, int64_t q_stride,
+                              int64_t k_stride, cp_dtype dtype, cp_dtype w_dtype, float eps, const cp_rope *rope,
+                              void *q_out, void *k_out, cudaStream_t stream);
+
+/*
+ * cp_qk_norm_rope_bwd -- gradients of cp_qk_norm_rope_fwd.  With g = A R(-t) dy
+ * and xh = x r:
+ *   u = w . g,  dx = r (u - xh mean_j(u_j xh_j)),  dw = sum over rows of g . xh
+ *   dq_out, dk_out : device, `dtype`, dense: gradients of q_out and k_out
+ *   q, k           : the inputs of the forward call, with their strides
+ *   dq, dk         : device, `dtype`, written dense, or in place of q (k) with its stride, or in
+ *                    place of dq_out (dk_out)
+ *   dwq, dwk       : device fp32 [D], written (sums in fp32, in a fixed order: the same
+ *                    from run to run)
+ *   workspace      : device, >= cp_qk_norm_rope_bwd_workspace_size bytes,
+ *                    256-byte aligned; overwritten (stream-ordered), not read back
+ */
+cp_status cp_qk_norm_rope_bwd_workspace_size(int64_t C, int64_t B, int64_t s, int64_t N, int64_t Nkv, int64_t D,
+                                             size_t *bytes);
+cp_status cp_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k, const void *wq,
+                              const void *wk, const int32_t *pos, int64_t C, int64_t B, int64_t s, int64_t N,
+                              int64_t Nkv, int64_t D, int64_t q_stride, int64_t k_stride, cp_dtype dtype,
+                              cp_dtype w_dtype, float eps, const cp_rope *rope, void *dq, void *dk, float *dwq,
+                              float *dwk, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * cp_cache_append -- put the keys and values of new tokens into a paged cache,
+ * with the keys normed and rotated on the way, and the queries of the same
+ * tokens in the same launch.
+ *   k, v    : device rows of Nkv heads of D values (`dtype`), token r at element offset
+ *             r * k_stride (v_stride); q the same with N heads (NULL with N = 0)
+ *   cu_new  : device int32 [B+1], non-decreasing from 0: rows cu_new[b] ..
+ *             cu_new[b+1]-1 are the n_b new tokens of sequence b (n_b may be 0);
+ *             rows from cu_new[B] up to R are padding, and neither they nor
+ *             their part of q_out are touched
+ *   kv_len  : device int32 [B], tokens of each sequence in the cache AFTER the
+ *             call: new token j of sequence b gets index i = kv_len[b] - n_b + j,
+ *             goes to slot i % page_size of page table[b][i / page_size], and
+ *             has position pos_base + i (pos_base: the length of a shared
+ *             prefix that stands before every sequence, 0 without one)
+ *   k_cache, v_cache : device bf16 [n_pages][page_size][Nkv][D]
+ *   table   : device int32 [B][max_pages]; only the entries that the new tokens fall into are
+ *             read.  Two new tokens must not share a slot.
+ *   wq, wk  : device [D] of w_dtype, or NULL: no norm of q (k); eps as above
+ *   rope    : NULL for no rotation
+ *   q_out   : device bf16 [R][N][D], the normed and rotated queries (may be q itself when q is
+ *             dense bf16)
+ * The prefix itself is appended as a sequence with its own table.
+ * page_size in {16, 32, 64, 128, 256} and D in {64, 128} (else
+ * CP_ERR_UNSUPPORTED); B <= 4096; n_pages * page_size and max_pages *
+ * page_size < 2^31.  cu_new, kv_len and table are read on the device: a token
+ * whose index or page number is out of range is skipped and the device status
+ * word becomes CP_ERR_PAGE.
+ */
+cp_status cp_cache_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                          int64_t v_stride, cp_dtype dtype, int64_t R, int64_t N, int64_t Nkv, int64_t D,
+                          const void *wq, const void *wk, cp_dtype w_dtype, float eps, const cp_rope *rope,
+                          int64_t pos_base, void *k_cache, void *v_cache, int64_t n_pages, int64_t page_size,
+                          const int32_t *table, int64_t B, int64_t max_pages, const int32_t *cu_new,
+                          const int32_t *kv_len, void *q_out, cudaStream_t stream);
+
+/*
  * cp_selftest_stalled_producer -- failure-detection self-test of the bounded
  * device-side waits (no counterpart on the pages).  Launches the attention
  * kernel on a [1][128][1][64] problem (q, k, v device bf16 [128][64], pos
@@ -496,8 +645,9 @@ cp_status cp_ring_attention_fwd_noalloc(const void *q_sh, const void *k_sh, cons
 /*
  * cp_device_status -- synchronise `stream`, then read (and, if clear != 0,
  * reset) the library's device status word on the current device.
- * *code receives CP_OK, or CP_ERR_DEVICE_TIMEOUT if a kernel of this library
- * gave up a bounded wait since the last reset.  Host-blocking.
+ * *code receives CP_OK, CP_ERR_DEVICE_TIMEOUT if a kernel of this library
+ * gave up a bounded wait since the last reset, or CP_ERR_PAGE if one met a page
+ * number, length or count out of range.  Host-blocking.
  */
 cp_status cp_device_status(int *code, int clear, cudaStream_t stream);
 

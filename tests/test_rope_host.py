@@ -1,0 +1,152 @@
+"""Frequencies, and what the rotation, norm and append calls refuse on the host
+before anything is launched (no GPU needed)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import rows_ref as R
+from context_causal_attention_gb300 import _lib
+from context_causal_attention_gb300 import ops as F
+
+FAKE = 1 << 20  # aligned, never read
+FAR = [FAKE + (i << 32) for i in range(12)]
+
+
+@pytest.mark.parametrize("scaling", ["plain", "linear", "base", "by_parts"])
+def test_frequencies(cplib, scaling):
+    kind = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}[scaling]
+    for rot in (16, 64, 128):
+        r = F.cp_rope_freqs(rot, 10000.0, kind, 8.0, 4096, device="cpu")
+        th, amp = R.thetas(rot, 10000.0, scaling, 8.0, 4096.0)
+        turns = r.freqs.numpy().view(np.uint64).astype(np.float64) / 2.0 ** 64
+        assert np.abs(turns - th / (2 * np.pi)).max() <= 2.0 ** -52
+        assert abs(r.amplitude - amp) <= amp * 2.0 ** -23
+
+
+def test_phases_keep_the_fraction_of_a_turn(cplib):
+    r = F.cp_rope_phases([2 * np.pi, np.pi, -np.pi / 2, 0.0], device="cpu")
+    assert r.rot_dim == 8
+    got = r.freqs.numpy().view(np.uint64)
+    assert got.tolist() == [0, 1 << 63, 3 << 62, 0]
+
+
+def test_frequency_refusals(cplib):
+    f = np.zeros(64, np.uint64)
+    a = ctypes.c_float(0)
+    call = lambda rot=64, base=1e4, kind=0, factor=1.0, length=1.0: cplib.cp_rope_freqs(  # noqa: E731
+        rot, base, kind, factor, length, f.ctypes.data, ctypes.byref(a))
+    assert call() == 0
+    assert call(rot=0) == 2 and call(rot=7) == 2 and call(rot=2, kind=2, factor=2.0) == 2
+    assert call(base=0.5) == 10 and call(base=float("nan")) == 10 and call(kind=4) == 10
+    assert call(kind=1, factor=0.5) == 10 and call(kind=3, factor=2.0, length=0.0) == 10
+    assert call(kind=2, factor=1e300, rot=4) == 10
+    assert cplib.cp_rope_freqs(64, 1e4, 0, 1.0, 1.0, None, ctypes.byref(a)) == 1
+    w = np.array([7.0, np.inf])
+    assert cplib.cp_rope_phases(w[:1].ctypes.data, 1, f.ctypes.data) == 10
+    assert cplib.cp_rope_phases(w[1:].ctypes.data, 1, f.ctypes.data) == 10
+    assert cplib.cp_rope_phases(w.ctypes.data, 0, f.ctypes.data) == 2
+    assert cplib.cp_rope_phases(None, 1, f.ctypes.data) == 1
+
+
+def spec(freqs=FAKE, rot=64, order=0, amp=1.0):
+    return ctypes.byref(_lib.RopeStruct(freqs, rot, order, amp))
+
+
+def rope(cplib, name="cp_rope_fwd", q=FAR[0], k=FAR[1], pos=FAKE, C=2, B=1, s=8, N=4, Nkv=2, D=64, qs=256, ks=128,
+         dt=0, r="default", qo=FAR[2], ko=FAR[3]):
+    return getattr(cplib, name)(q, k, pos, C, B, s, N, Nkv, D, qs, ks, dt, spec() if r == "default" else r, qo, ko,
+                                None)
+
+
+@pytest.mark.parametrize("name", ["cp_rope_fwd", "cp_rope_bwd"])
+def test_rope_refusals(cplib, name):
+    bad = lambda **kw: rope(cplib, name, **kw)  # noqa: E731
+    for kw in (dict(q=None), dict(k=None), dict(pos=None), dict(qo=None), dict(ko=None), dict(r=None),
+               dict(r=spec(freqs=None))):
+        assert bad(**kw) == 1, kw
+    for kw in (dict(C=0), dict(B=0), dict(s=0), dict(N=-1), dict(N=0, Nkv=0), dict(qs=255), dict(ks=120),
+               dict(s=1 << 31), dict(C=1 << 16, s=1 << 16), dict(r=spec(rot=0)), dict(r=spec(rot=66)),
+               dict(r=spec(rot=33)), dict(N=70000, qs=70000 * 64)):
+        assert bad(**kw) == 2, kw
+    for kw in (dict(D=96, qs=384, ks=192), dict(D=256, qs=1024, ks=512), dict(r=spec(rot=24))):
+        assert bad(**kw) == 7, kw
+    assert bad(dt=2) == 4
+    for kw in (dict(r=spec(order=2)), dict(r=spec(amp=float("inf"))), dict(qo=FAR[0] + 16), dict(qo=FAR[1]),
+               dict(ko=FAR[0]), dict(qo=FAR[2], ko=FAR[2] + 64), dict(q=FAR[0], k=FAR[1], ko=FAR[1] - 16)):
+        assert bad(**kw) == 10, kw
+    for kw in (dict(q=FAR[0] + 8), dict(qo=FAR[2] + 4), dict(pos=FAKE + 2), dict(qs=260), dict(r=spec(freqs=FAKE + 4))):
+        assert bad(**kw) == 5, kw
+
+
+def test_norm_refusals(cplib):
+    def fwd(q=FAR[0], wq=FAKE, wk=FAKE, pos=FAKE, r="default", eps=1e-6, wd=1, dt=0):
+        return cplib.cp_qk_norm_rope_fwd(q, FAR[1], wq, wk, pos, 1, 1, 8, 4, 2, 64, 256, 128, dt, wd, eps,
+                                         spec() if r == "default" else r, FAR[2], FAR[3], None)
+
+    assert fwd(q=None) == 1 and fwd(wq=None) == 1 and fwd(wk=None) == 1 and fwd(pos=None) == 1
+    assert fwd(eps=-1.0) == 10 and fwd(eps=float("nan")) == 10 and fwd(wd=3) == 4 and fwd(dt=3) == 4
+    assert fwd(wq=FAKE + 4) == 5 and fwd(r=spec(rot=24)) == 7
+    n = ctypes.c_size_t(0)
+    size = cplib.cp_qk_norm_rope_bwd_workspace_size
+    assert size(1, 1, 8, 4, 2, 64, ctypes.byref(n)) == 0 and n.value > 0
+    assert size(1, 1, 8, 4, 2, 64, None) == 1 and size(1, 1, 0, 4, 2, 64, ctypes.byref(n)) == 2
+    assert size(1, 1, 8, 4, 2, 80, ctypes.byref(n)) == 7
+
+    def bwd(gq=FAR[4], gk=FAR[5], dq=FAR[2], dk=FAR[3], dwq=FAR[6], dwk=FAR[7], ws=FAR[8], nb=n.value, wq=FAKE):
+        return cplib.cp_qk_norm_rope_bwd(gq, gk, FAR[0], FAR[1], wq, FAKE, FAKE, 1, 1, 8, 4, 2, 64, 256, 128, 0, 1,
+                                         1e-6, spec(), dq, dk, dwq, dwk, ws, nb, None)
+
+    for kw in (dict(gq=None), dict(gk=None), dict(dwq=None), dict(dwk=None), dict(wq=None), dict(dq=None)):
+        assert bwd(**kw) == 1, kw
+    assert bwd(ws=None) == 6 and bwd(nb=n.value - 1) == 6
+    assert bwd(ws=FAR[8] + 128) == 5 and bwd(dwq=FAR[6] + 2) == 5 and bwd(gq=FAR[4] + 8) == 5
+    assert bwd(dq=FAR[4] + 16) == 10 and bwd(dq=FAR[5]) == 10 and bwd(dk=FAR[4]) == 10
+
+
+def test_append_refusals(cplib):
+    def app(q=FAR[0], k=FAR[1], v=FAR[2], qs=256, ks=128, vs=128, dt=0, R_=8, N=4, Nkv=2, D=64, wq=None, wk=None, wd=1,
+            eps=1e-6, r="default", base=0, kc=FAR[3], vc=FAR[4], pages=10, page=16, table=FAKE, B=2, most=4, cu=FAKE,
+            ln=FAKE, qo=FAR[5]):
+        return cplib.cp_cache_append(q, k, v, qs, ks, vs, dt, R_, N, Nkv, D, wq, wk, wd, eps,
+                                     spec() if r == "default" else r, base, kc, vc, pages, page, table, B, most, cu,
+                                     ln, qo, None)
+
+    for kw in (dict(k=None), dict(v=None), dict(kc=None), dict(vc=None), dict(table=None), dict(cu=None),
+               dict(ln=None), dict(q=None), dict(qo=None), dict(r=spec(freqs=None))):
+        assert app(**kw) == 1, kw
+    for kw in (dict(R_=0), dict(R_=1 << 31), dict(N=-1), dict(Nkv=0), dict(pages=0), dict(B=0), dict(B=4097),
+               dict(most=0), dict(pages=1 << 28), dict(most=1 << 28), dict(qs=255), dict(ks=64), dict(vs=64),
+               dict(r=spec(rot=65))):
+        assert app(**kw) == 2, kw
+    for kw in (dict(D=96, qs=384, ks=192, vs=192), dict(page=8), dict(page=48), dict(page=512), dict(r=spec(rot=24))):
+        assert app(**kw) == 7, kw
+    assert app(dt=5) == 4 and app(wd=5) == 4
+    for kw in (dict(wk=FAKE, eps=-1.0), dict(base=1 << 31), dict(vc=FAR[3]), dict(qo=FAR[1]), dict(qo=FAR[0] + 16),
+               dict(qo=FAR[0], dt=1), dict(qo=FAR[0], qs=512)):
+        assert app(**kw) == 10, kw
+    for kw in (dict(k=FAR[1] + 8), dict(cu=FAKE + 2), dict(ks=132), dict(wq=FAKE + 4), dict(kc=FAR[3] + 8)):
+        assert app(**kw) == 5, kw
+
+
+def test_binding_refusals(cplib):
+    """Shapes, strides and devices that the binding refuses before the call."""
+    rope = F.cp_rope_freqs(64, device="cpu")
+    pos = torch.zeros(5, dtype=torch.int32)
+    q = torch.zeros(5, 2, 64)
+    for bad in (q[:, :, ::2], q.transpose(0, 1), q.transpose(1, 2), q[0]):
+        with pytest.raises(ValueError):
+            F.cp_rope_fwd(bad, None, pos, rope)
+    with pytest.raises(ValueError):
+        F.cp_rope_fwd(torch.zeros(2, 6, 2, 64)[:, :5], None, pos, rope)  # tokens at two distances
+    with pytest.raises(ValueError):
+        F.cp_rope_fwd(q, torch.zeros(4, 2, 64), pos, rope)
+    with pytest.raises(ValueError):
+        F.cp_rope_fwd(q, None, pos.long(), rope)
+    with pytest.raises(ValueError):
+        F.cp_rope_fwd(q, None, pos[:4], rope)
+    with pytest.raises(ValueError):
+        F.cp_rope_fwd(q, None, pos, rope, q_out=torch.zeros(5, 2, 64, dtype=torch.bfloat16))
+    with pytest.raises((ValueError, RuntimeError, AssertionError)):
+        F.cp_rope_fwd(q, None, pos, rope)  # not on a GPU
