@@ -114,6 +114,9 @@ def lib():
                                       f32, rp, vp, vp, vp, vp, vp, sz, vp]
     L.cp_cache_append.argtypes = [vp, vp, vp, i64, i64, i64, i32, i64, i64, i64, i64, vp, vp, i32, f32, rp, i64, vp,
                                   vp, i64, i64, vp, i64, i64, vp, vp, vp, vp]
+    L.cp_prefix_attn_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
+    L.cp_prefix_attn_fwd.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i64, i64, i64, i64, i64, f32,
+                                     vp, i32, vp, vp, sz, vp]
     for name in header_symbols():
         if name not in ("cp_status_string", "cp_version", "cp_last_cuda_error"):
             getattr(L, name).restype = ctypes.c_int

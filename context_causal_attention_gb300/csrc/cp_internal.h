@@ -213,5 +213,7 @@ cp_status check_rope(const cp_rope *rope, int64_t D);
 cp_status check_pages(int64_t n_pages, int64_t page_size, int64_t B, int64_t max_pages, int64_t Nkv, int64_t D);
 // Sticky device status word of the append kernels (read and optionally cleared).
 cp_status read_cache_device_status(int *code, bool clear);
+// Sticky device status word of the shared-prefix attention.
+cp_status read_prefix_device_status(int *code, bool clear);
 
 }  // namespace cpattn

@@ -21,6 +21,7 @@ __all__ = [
     "cp_allgather_attention_fwd", "cp_ulysses_attention_fwd",
     "cp_device_status", "cp_version", "cp_rope_freqs", "cp_rope_phases", "cp_rope_fwd", "cp_rope_bwd",
     "cp_qk_norm_rope_fwd", "cp_qk_norm_rope_bwd_workspace_size", "cp_qk_norm_rope_bwd", "cp_cache_append",
+    "cp_prefix_attn_workspace_size", "cp_prefix_attn_fwd",
     "CP_BF16", "CP_F32", "CP_ZIGZAG", "CP_CONTIGUOUS", "CP_SEQ_TO_HEAD", "CP_HEAD_TO_SEQ", "CP_RANK_ORDER",
     "CP_GLOBAL_ORDER", "CP_RING_PREFETCH", "CP_RING_FUSED_MERGE", "CP_RING_TF32", "CP_ROPE_HALF",
     "CP_ROPE_INTERLEAVED", "CP_ROPE_PLAIN", "CP_ROPE_LINEAR", "CP_ROPE_BASE", "CP_ROPE_BY_PARTS", "CpRope", "CpError",
@@ -626,6 +627,48 @@ def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=
                                     _addr(kv_len), _addr(q_out), _stream(stream))
     _lib.check("cp_cache_append", st)
     return q_out
+
+
+def cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page_size, max_pages):
+    n = ctypes.c_size_t(0)
+    _lib.check("cp_prefix_attn_workspace_size",
+               _lib.lib().cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page_size, max_pages,
+                                                        ctypes.byref(n)))
+    return n.value
+
+
+def cp_prefix_attn_fwd(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale=None,
+                       o_dtype=CP_BF16, o=None, lse=None, workspace=None, stream=None):
+    """Attention of the new tokens q bf16 [R,N,D] over the shared prefix and their own sequences'
+    pages -> (o [R,N,D], lse fp32 [N,R]); see the C header.  max_new: the
+    largest number of new tokens of a sequence (chooses the tiles only)."""
+    n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
+    if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be contiguous bf16 [R, N, D]")
+    R, N = q.shape[0], q.shape[1]
+    if prefix_len and (prefix_pages.dtype != torch.int32 or not prefix_pages.is_contiguous() or
+                       prefix_pages.numel() * page < prefix_len):
+        raise ValueError("prefix_pages must be contiguous int32 and cover prefix_len tokens")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if o is None:
+        o = torch.empty((R, N, D), dtype=torch.float32 if o_dtype == CP_F32 else torch.bfloat16, device=q.device)
+    elif o.shape != q.shape or not o.is_contiguous():
+        raise ValueError("o must be contiguous [R, N, D]")
+    if lse is None:
+        lse = torch.empty((N, R), dtype=torch.float32, device=q.device)
+    elif lse.shape != (N, R) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [N, R]")
+    if workspace is None:
+        workspace = torch.empty(max(256, cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page,
+                                                                       max_pages)), dtype=torch.uint8, device=q.device)
+    _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, o, lse, workspace)
+    st = _lib.lib().cp_prefix_attn_fwd(_addr(q), _addr(k_cache), _addr(v_cache), n_pages, page, _addr(prefix_pages),
+                                       prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), max_new,
+                                       R, N, Nkv, D, scale, _addr(o), _dtype_code(o), _addr(lse), _addr(workspace),
+                                       workspace.numel() * workspace.element_size(), _stream(stream))
+    _lib.check("cp_prefix_attn_fwd", st)
+    return o, lse
 
 
 def cp_selftest_stalled_producer(q, k, v, pos, o, lse, timeout_ns, stream=None):

@@ -569,6 +569,48 @@ cp_status cp_cache_append(const void *q, const void *k, const void *v, int64_t q
                           const int32_t *kv_len, void *q_out, cudaStream_t stream);
 
 /*
+ * cp_prefix_attn_workspace_size / cp_prefix_attn_fwd -- attention of a batch of
+ * sequences that share a prefix, over a paged cache filled by cp_cache_append.
+ * Query row r (a new token of sequence b with own index i) sees the
+ * prefix_len keys of the prefix and its own sequence's keys 0 .. i:
+ *   s_j = scale <q_r, k_j>,  lse_r = ln sum_j e^{s_j},  o_r = sum_j e^{s_j - lse_r} v_j
+ * The prefix is read once for all rows ([DAY74] How do partial softmax results
+ * combine?; the two parts join as in cp_lse_merge).  One call serves single
+ * tokens, drafts and prompts, mixed in one batch.
+ *   q       : device bf16 [R][N][D], dense; query head h reads KV head h/(N/Nkv)
+ *   k_cache, v_cache : device bf16 [n_pages][page_size][Nkv][D]
+ *   prefix_pages : device int32 [ceil(prefix_len/page_size)], the prefix's pages
+ *             (may be NULL when prefix_len is 0)
+ *   table, cu_new, kv_len, B, max_pages : as for cp_cache_append, after it: new token j of
+ *             sequence b has own index kv_len[b] - n_b + j (a negative index sees
+ *             the prefix alone)
+ *   max_new : about the largest n_b, 1 .. R: chooses the tiles only, every n_b is right
+ *   o       : device [R][N][D] of o_dtype; a row that sees no key gets o = 0
+ *   lse     : device fp32 [N][R] (cp_lse_merge's layout for B = 1), -inf for such a row
+ *             Rows from cu_new[B] to R are padding: neither o nor lse is touched there.
+ *   workspace : device, >= cp_prefix_attn_workspace_size bytes, 256-byte
+ *             aligned; overwritten (stream-ordered), not read back.  Calls that
+ *             may overlap need one each.
+ * Products are bf16 with fp32 accumulation; the softmax weights are rounded to
+ * bf16 before the second product (off by 2^-9 of themselves at most, whatever
+ * o_dtype is), lse is not.  Keys that no row of the call sees are not read into
+ * a result whatever they hold; a NaN or infinity in a V row that some row sees
+ * may reach other rows of its sequence.
+ * D in {64, 128}, page_size in {16, 32, 64, 128, 256}; N % Nkv == 0; scale
+ * finite and > 0.  The lists are read on the device: a page number, length or
+ * count out of range sets the device status word to CP_ERR_PAGE, is never
+ * followed, and leaves its rows' results unspecified.
+ */
+cp_status cp_prefix_attn_workspace_size(int64_t R, int64_t B, int64_t max_new, int64_t prefix_len, int64_t N,
+                                        int64_t Nkv, int64_t D, int64_t page_size, int64_t max_pages, size_t *bytes);
+cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, const void *v_cache, int64_t n_pages,
+                             int64_t page_size, const int32_t *prefix_pages, int64_t prefix_len,
+                             const int32_t *table, int64_t B, int64_t max_pages, const int32_t *cu_new,
+                             const int32_t *kv_len, int64_t max_new, int64_t R, int64_t N, int64_t Nkv, int64_t D,
+                             float scale, void *o, cp_dtype o_dtype, float *lse, void *workspace, size_t ws_bytes,
+                             cudaStream_t stream);
+
+/*
  * cp_selftest_stalled_producer -- failure-detection self-test of the bounded
  * device-side waits (no counterpart on the pages).  Launches the attention
  * kernel on a [1][128][1][64] problem (q, k, v device bf16 [128][64], pos

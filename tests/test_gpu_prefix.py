@@ -1,0 +1,283 @@
+"""Attention over a shared prefix and paged sequences, against the 64-bit form of
+rows_ref.py.
+
+Tolerance.  Scores: products of bf16 values are exact in fp32, and a sum of D of
+them is off by at most D u sum|q k| (u = 2^-24); with unit-normal values and scale
+1/sqrt(D) that is under 2^-14 in the score for D = 128, so every weight, and lse,
+is right to 2^-13 with the exponential's own 2^-22 and the sums' length / 2^24
+(lengths here stay under 2^10 tiles a thread).  Each weight is then rounded to
+bf16: at most 2^-8 / 2 (half a step) of itself, so o is off by at most (2^-8 + 2^-12)
+sum p|v| / sum p, and by half a step of its own type."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import rows_ref as R
+from context_causal_attention_gb300 import ops as F
+from test_gpu_cache import Batch
+from test_gpu_rope import f64, rand, rope_of, within
+
+pytestmark = pytest.mark.gpu
+
+
+class Call:
+    """A batch with caches, prefix and queries, on the device, and its 64-bit result."""
+
+    def __init__(self, seed, new, length, prefix, N, Nkv, D, page, pad=0, garbage=None, gain=1.0):
+        g = torch.Generator().manual_seed(seed)
+        # the prefix is one more list of the batch's pages
+        b = Batch(g, list(new) + [0], list(length) + [prefix], page)
+        self.b, self.N, self.Nkv, self.D, self.prefix, self.new, self.length = b, N, Nkv, D, prefix, new, length
+        self.rows, self.R = sum(new), sum(new) + pad
+        self.k, self.v = (rand(g, (b.total, page, Nkv, D), "bf16") for _ in range(2))
+        self.q = rand(g, (self.R, N, D), "bf16", gain)
+        used = np.zeros(b.total * page, bool)
+        for s, m in enumerate(b.length):
+            used[b.slots(s, 0, m)] = True
+        if garbage is not None:
+            free = torch.tensor(~used).view(b.total, page)
+            self.k[free], self.v[free] = garbage, garbage
+            self.q[self.rows:] = garbage
+        self.table = b.table[:-1].contiguous()
+        self.pages = b.table[-1, :max(1, -(-prefix // page))].contiguous()
+        self.cu, self.kv_len = b.cu[:-1].contiguous(), b.kv_len[:-1].contiguous()
+
+    def run(self, dev, **kw):
+        self.dev = [t.to(dev) for t in (self.q, self.k, self.v, self.pages, self.table, self.cu, self.kv_len)]
+        q, k, v, pages, table, cu, kv_len = self.dev
+        return F.cp_prefix_attn_fwd(q, k, v, pages, self.prefix, table, cu, kv_len,
+                                    max(1, max(self.new)), **kw)
+
+    def want(self):
+        b, n, P = self.b, len(self.new), self.prefix
+        k, v = f64(self.k).reshape(-1, self.Nkv, self.D), f64(self.v).reshape(-1, self.Nkv, self.D)
+        o, a = (np.zeros((self.rows, self.N, self.D)) for _ in range(2))
+        lse, r = np.zeros((self.N, self.rows)), 0
+        for s in range(n):
+            at = b.slots(n, 0, P) + b.slots(s, 0, self.length[s])
+            m, L = self.new[s], self.length[s]
+            seen = np.ones((m, P + L), bool)
+            seen[:, P:] = np.arange(L) <= np.arange(L - m, L)[:, None]
+            o[r:r + m], lse[:, r:r + m], a[r:r + m] = R.attention(f64(self.q[r:r + m]), k[at], v[at], seen,
+                                                                 1 / math.sqrt(self.D))
+            r += m
+        return o, lse, a
+
+    def check(self, o, lse, dt="bf16", what="", gain=1.0):
+        wo, wl, a = self.want()
+        n = self.rows
+        within(o[:n], wo, dt, (2.0 ** -8 + 2.0 ** -12 * gain) * a, what + " o")
+        got = f64(lse)[:, :n]
+        empty = np.isneginf(wl)
+        assert np.array_equal(np.isneginf(got), empty)
+        assert (f64(o[:n]).transpose(1, 0, 2)[empty] == 0).all()
+        assert np.abs(got - wl)[~empty].max(initial=0) <= 2.0 ** -12 * gain, what + " lse"
+
+
+# new tokens, own lengths, prefix, N, Nkv, D, page, padding
+CASES = {
+    "one_key": ([1], [1], 0, 1, 1, 64, 16, 0),
+    "one_and_prefix": ([1], [1], 1, 4, 1, 128, 16, 0),
+    "tile_edges": ([1, 1, 1, 1], [63, 64, 65, 128], 64, 8, 2, 64, 64, 0),
+    "page_edges": ([1, 1, 1], [15, 16, 17], 33, 8, 8, 128, 16, 0),
+    "draft": ([5, 1, 3, 5], [5, 700, 3, 130], 1000, 12, 4, 64, 32, 3),
+    "odd_groups": ([2, 1, 4], [2, 90, 400], 257, 21, 3, 128, 128, 0),
+    "one_kv_head": ([3, 3], [3, 77], 500, 40, 1, 64, 256, 0),
+    "no_prefix": ([1, 7, 0, 2], [1000, 7, 12, 33], 0, 16, 4, 128, 16, 1),
+    "empty_sequences": ([0, 1, 0, 0], [0, 9, 300, 0], 70, 4, 2, 64, 16, 2),
+    "prompts": ([150, 1, 64, 33], [150, 40, 264, 33], 300, 8, 2, 128, 64, 5),
+    "many": ([1] * 300, list(range(1, 301)), 200, 4, 2, 64, 16, 0),
+    "long": ([1, 2], [3000, 9000], 20000, 8, 2, 128, 64, 0),
+}
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_against_64_bits(cuda_dev, name, dt):
+    new, length, prefix, N, Nkv, D, page, pad = CASES[name]
+    c = Call(len(name), new, length, prefix, N, Nkv, D, page, pad)
+    T = {"bf16": torch.bfloat16, "fp32": torch.float32}[dt]
+    o = torch.full((c.R, N, D), 7.0, dtype=T, device=cuda_dev)
+    lse = torch.full((N, c.R), 7.0, device=cuda_dev)
+    c.run(cuda_dev, o=o, lse=lse)
+    c.check(o, lse, dt, name)
+    assert (o[c.rows:] == 7).all() and (lse[:, c.rows:] == 7).all()
+
+
+@pytest.mark.parametrize("garbage", [float("nan"), float("inf"), 3e38])
+@pytest.mark.parametrize("name", ["draft", "page_edges", "prompts", "one_key"])
+def test_what_unused_slots_hold_does_not_matter(cuda_dev, name, garbage):
+    """Slots past a length (in a used page too), spare pages and padding queries hold
+    NaN, infinities or the largest values: the same bits come out."""
+    new, length, prefix, N, Nkv, D, page, pad = CASES[name]
+    clean = Call(3, new, length, prefix, N, Nkv, D, page, pad)
+    dirty = Call(3, new, length, prefix, N, Nkv, D, page, pad, garbage=garbage)
+    n = clean.rows
+    a, b = clean.run(cuda_dev), dirty.run(cuda_dev)
+    assert torch.equal(a[0][:n], b[0][:n]) and torch.equal(a[1][:, :n], b[1][:, :n])
+    clean.check(*a)
+
+
+def test_rows_that_see_nothing(cuda_dev):
+    """Fewer cached tokens than new ones: rows with a negative index see the prefix
+    alone, and without one nothing (o = 0, lse = -inf)."""
+    for prefix in (0, 40):
+        c = Call(4, [6, 1], [6, 20], prefix, 4, 2, 64, 16)
+        c.kv_len[0] = 2
+        c.length = [2, 20]
+        o, lse = c.run(cuda_dev)
+        k, v = f64(c.k).reshape(-1, 2, 64), f64(c.v).reshape(-1, 2, 64)
+        at = c.b.slots(2, 0, prefix) + c.b.slots(0, 0, 2)
+        seen = np.ones((6, prefix + 2), bool)
+        seen[:, prefix:] = np.arange(2) <= (np.arange(6) - 4)[:, None]
+        wo, wl, a = R.attention(f64(c.q[:6]), k[at], v[at], seen, 0.125)
+        within(o[:6], wo, "bf16", (2.0 ** -8 + 2.0 ** -12) * a, "few keys")
+        none = np.isneginf(wl)
+        assert none.sum() == (16 if prefix == 0 else 0)
+        assert np.array_equal(np.isneginf(f64(lse)[:, :6]), none)
+        assert np.abs(f64(lse)[:, :6] - wl)[~none].max() <= 2.0 ** -12
+        c = None
+    # no key at all anywhere
+    c = Call(5, [1], [1], 0, 2, 1, 128, 16)
+    c.kv_len[0] = 0
+    o, lse = c.run(cuda_dev)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("gain", [30.0, 300.0])
+def test_large_scores(cuda_dev, gain):
+    """Scores in the hundreds and thousands, growing along the keys: the running
+    maximum moves.  The score's error scales with the queries (the bound of the
+    header times the gain), which the weights share."""
+    c = Call(6, [2, 1], [500, 900], 1500, 8, 4, 64, 16, gain=gain)
+    # keys grow along the sequence
+    for s, m in enumerate(c.b.length):
+        at = c.b.slots(s, 0, m)
+        k = c.k.view(-1, 4, 64)
+        k[at] = (k[at].float() * torch.linspace(0.01, 1, max(m, 1)).view(-1, 1, 1)).to(torch.bfloat16)
+    o, lse = c.run(cuda_dev, o_dtype=F.CP_F32)
+    c.check(o, lse, "fp32", "gain", gain)
+
+
+def test_same_bits_twice_and_by_graph(cuda_dev):
+    """The same call twice, on another stream, and as a captured graph whose lists
+    and caches change between replays: each the bits of an eager call."""
+    c = Call(7, [1, 3, 2], [200, 400, 61], 3000, 16, 4, 128, 16)
+    a = c.run(cuda_dev)
+    b = c.run(cuda_dev)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    q, k, v, pages, table, cu, kv_len = c.dev
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        d = F.cp_prefix_attn_fwd(q, k, v, pages, 3000, table, cu, kv_len, 3)
+    s.synchronize()
+    assert torch.equal(a[0], d[0]) and torch.equal(a[1], d[1])
+    o, lse = torch.empty_like(a[0]), torch.empty_like(a[1])
+    ws = torch.empty(F.cp_prefix_attn_workspace_size(6, 3, 3, 3000, 16, 4, 128, 16, table.shape[1]), dtype=torch.uint8,
+                     device=cuda_dev)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        F.cp_prefix_attn_fwd(q, k, v, pages, 3000, table, cu, kv_len, 3, o=o, lse=lse, workspace=ws)
+    for step in range(3):
+        ws.random_(0, 256)
+        kv_len.copy_(torch.tensor([200 - 50 * step, 400 - 133 * step, 61 - step], dtype=torch.int32))
+        q.copy_(q.flip(0))
+        graph.replay()
+        want = F.cp_prefix_attn_fwd(q, k, v, pages, 3000, table, cu, kv_len, 3)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), step
+
+
+def test_outputs_and_workspace_stay_in_bounds(cuda_dev):
+    c = Call(8, [3, 40, 1], [3, 300, 77], 130, 6, 2, 64, 16, pad=2)
+    c.run(cuda_dev)
+    q, k, v, pages, table, cu, kv_len = c.dev
+    need = F.cp_prefix_attn_workspace_size(c.R, 3, 40, 130, 6, 2, 64, 16, table.shape[1])
+    ws = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device=cuda_dev)
+    o = torch.full((c.R + 2, 6, 64), 7.0, device=cuda_dev)
+    lse = torch.full((6 * c.R + 8,), 7.0, device=cuda_dev)
+    F.cp_prefix_attn_fwd(q, k, v, pages, 130, table, cu, kv_len, 40, o=o[1:-1], lse=lse[4:-4].view(6, c.R),
+                         workspace=ws[256:256 + need])
+    torch.cuda.synchronize()
+    assert (o[0] == 7).all() and (o[-1] == 7).all() and (lse[:4] == 7).all() and (lse[-4:] == 7).all()
+    assert (ws[:256] == 0xA5).all() and (ws[256 + need:] == 0xA5).all()
+    c.check(o[1:-1], lse[4:-4].view(6, c.R), "fp32")
+
+
+@pytest.mark.parametrize("what", ["page", "prefix_page", "length", "negative_length", "counts", "counts_past_rows"])
+def test_bad_lists_are_reported(cuda_dev, what):
+    """Lists out of range are reported and not followed; a sequence that they do not
+    touch keeps its result."""
+    c = Call(9, [2, 3], [50, 40], 70, 4, 2, 64, 16)
+    good = c.run(cuda_dev)
+    torch.cuda.synchronize()
+    if what == "page":
+        c.table[0, 1] = c.b.total + 5
+    elif what == "prefix_page":
+        c.pages[2] = -1
+    elif what == "length":
+        c.kv_len[0] = 16 * c.table.shape[1] + 1
+    elif what == "negative_length":
+        c.kv_len[0] = -3
+    elif what == "counts":
+        c.cu[1] = -2
+    else:
+        c.cu[2] = 6
+    o, lse = c.run(cuda_dev)
+    assert F.cp_device_status() == 11
+    assert F.cp_device_status() == 0
+    if what in ("page", "length", "negative_length"):
+        assert torch.equal(o[2:], good[0][2:]) and torch.equal(lse[:, 2:], good[1][:, 2:])
+
+
+def test_append_then_attend_decodes_like_one_causal_attention(cuda_dev):
+    """The operators together: a prefix and two prompts are appended (norm, rotation),
+    then tokens one at a time; every step's attention equals the 64-bit causal
+    attention of the whole sequence so far (inputs rounded where the cache rounds)."""
+    g = torch.Generator().manual_seed(10)
+    N, Nkv, D, page, P = 8, 2, 64, 16, 37
+    prompt, steps, total = [21, 5], 4, 40
+    b = Batch(g, [0, 0, 0], [prompt[0] + steps, prompt[1] + steps, P], page)
+    rope, th, amp = rope_of(D, "half")
+    kc, vc = (torch.full((b.total, page, Nkv, D), float("nan"), dtype=torch.bfloat16, device=cuda_dev) for _ in range(2))
+    wq, wk = (1 + 0.2 * torch.randn(D, generator=g) for _ in range(2))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda_dev)  # noqa: E731
+    table, pages = b.table[:2].to(cuda_dev), b.table[2:, :-(-P // page)].contiguous().to(cuda_dev)
+    hist = [[], []]  # each sequence's (q, k, v) rows, as drawn
+
+    def draw(n):
+        return [rand(g, (n, h, D), "bf16") for h in (N, Nkv, Nkv)]
+
+    def append(rows, tab, cu, lens, base):
+        q, k, v = (t.to(cuda_dev) for t in rows)
+        return F.cp_cache_append(k, v, kc, vc, tab, cu, lens, rope=rope, q=q, wq=wq.to(cuda_dev), wk=wk.to(cuda_dev),
+                                 pos_base=base)
+
+    shared = draw(P)
+    append(shared, pages, i32(0, P), i32(P), 0)
+    lens = [0, 0]
+    for step in range(steps + 1):
+        n = prompt if step == 0 else [1, 1]
+        rows = [draw(x) for x in n]
+        for h, r in zip(hist, rows):
+            h.append(r)
+        lens = [x + y for x, y in zip(lens, n)]
+        cat = [torch.cat([r[i] for r in rows]) for i in range(3)]
+        cu, kv_len = i32(0, n[0], n[0] + n[1]), i32(*lens)
+        q = append(cat, table, cu, kv_len, P)
+        o, lse = F.cp_prefix_attn_fwd(q, kc, vc, pages.flatten(), P, table, cu, kv_len, max(n))
+        at = 0
+        for s in range(2):
+            every = [torch.cat([shared[i]] + [r[i] for r in hist[s]]) for i in range(3)]
+            pos = np.arange(P + lens[s])
+            qr, kr = (R.bf16(R.turn(R.norm(f64(every[i]), f64(w), 1e-6), pos, th, amp, "half"))
+                      for i, w in ((0, wq), (1, wk)))
+            seen = pos <= pos[-n[s]:, None]
+            wo, wl, a = R.attention(qr[-n[s]:], kr, f64(every[2]), seen, 1 / math.sqrt(D))
+            # a value next to a rounding border may go the other way in q or k: half a
+            # step (2^-8) of single values, 2^-5 in a score of size sum|q k| scale < 8
+            assert np.abs(f64(lse)[:, at:at + n[s]] - wl).max() <= 2.0 ** -5
+            within(o[at:at + n[s]], wo, "bf16", (2.0 ** -8 + 2.0 ** -4) * a, "decode")
+            at += n[s]
