@@ -1,0 +1,239 @@
+// cp_prefix.cuh -- how the shared-prefix attention lays its work on a line and
+// cuts it into equal shares (prefix.cu, prefix_tc.cuh).
+//
+// A launch works on problems: the prefix with the rows of all sequences, the
+// sequences with their own rows and keys, or both.  For one KV head the rows of
+// a problem are its tokens times the G query heads of that KV head (row i =
+// token i / G, head i % G), cut into tiles of TM rows; an item is one row tile
+// of one KV head of one problem.  The items lie end to end on a line, each
+// ceil(keys / KT) long, and block c works on [c share, (c + 1) share).
+//
+// The row tiles of a causal problem need fewer keys than its length: a stretch
+// [n0, n1) of an item of nominal length T that needs K tiles stands for tiles
+// [n0 K / T, n1 K / T).  Row tiles from the beginning and the end take turns on
+// the line, so neighbours cost about the average.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "cp_paged.cuh"
+
+namespace cpattn {
+
+struct PrefixArgs {
+    const __nv_bfloat16 *q, *k, *v;
+    PageTable own, pre;  // the sequences' pages; the prefix as a table of one row
+    const int32_t *cu, *kv_len;
+    int R, B, N, Nkv, G;
+    long long P;
+    float scale_log2;
+    int with_prefix, with_own;  // the problems of this launch
+    int *status;
+    unsigned long long timeout_ns;
+    // what the launch leaves for the join
+    long long *head;      // [0]: tiles of a share
+    long long *base_tile; // [B] first tile of each sequence
+    int *base_item;       // [B] first item of each sequence
+    float2 *slot_ml;      // [slots][TM]: exponent, sum
+    float *slot_o;        // [slots][TM][D], not divided by the sum
+    int slots;
+};
+
+__device__ __forceinline__ void report(int *status, cp_status code) { atomicExch(status, static_cast<int>(code)); }
+
+// One problem's shape.
+struct Problem {
+    int tok0, n;     // rows' tokens
+    long long keys;  // keys in all
+    int row_tiles;
+    long long key_tiles;  // nominal length of an item
+};
+
+// Sequence b as the device lists give it; a list that makes no sense is cut to
+// what can be read and reported.
+template <int TM, int KT>
+__device__ __forceinline__ Problem sequence_problem(const PrefixArgs &a, int b) {
+    Problem p;
+    const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+    long long len = __ldg(a.kv_len + b);
+    const long long most = static_cast<long long>(a.own.max_pages) << a.own.shift;
+    p.tok0 = c0;
+    p.n = c1 - c0;
+    if (c0 < 0 || c1 < c0 || c1 > a.R) {
+        p.n = 0;
+        report(a.status, CP_ERR_PAGE);
+    }
+    if (len < 0 || len > most) {
+        len = len < 0 ? 0 : most;
+        report(a.status, CP_ERR_PAGE);
+    }
+    p.keys = len;
+    p.row_tiles = (p.n * a.G + TM - 1) / TM;
+    p.key_tiles = p.n ? (len + KT - 1) / KT : 0;
+    return p;
+}
+template <int TM, int KT>
+__device__ __forceinline__ Problem prefix_problem(const PrefixArgs &a) {
+    Problem p;
+    p.tok0 = 0;
+    p.n = min(max(__ldg(a.cu + a.B), 0), a.R);
+    p.keys = a.P;
+    p.row_tiles = (p.n * a.G + TM - 1) / TM;
+    p.key_tiles = p.n ? (a.P + KT - 1) / KT : 0;
+    return p;
+}
+
+// Row tile at place w of a problem's turn order, and back.
+__device__ __forceinline__ int tile_at(int w, int tiles) { return w & 1 ? tiles - 1 - (w >> 1) : w >> 1; }
+__device__ __forceinline__ int place_of(int j, int tiles) {
+    return j < (tiles + 1) / 2 ? 2 * j : 2 * (tiles - 1 - j) + 1;
+}
+
+// Where every problem's tiles and items begin on the line: sums over runs of
+// sequences (entry i + 1: run i; entry 0: the prefix), scanned over the block.
+constexpr int kRuns = 128;
+struct Line {
+    long long tile[kRuns + 1];
+    int item[kRuns + 1];
+};
+
+template <int TM, int KT>
+__device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, bool publish) {
+    const int tid = threadIdx.x, run = (a.B + kRuns - 1) / kRuns;
+    const int b0 = min(tid * run, a.B), b1 = a.with_own ? min(b0 + run, a.B) : b0;
+    if (tid < kRuns) {
+        long long tiles = 0;
+        int items = 0;
+        for (int b = b0; b < b1; ++b) {
+            const Problem p = sequence_problem<TM, KT>(a, b);
+            tiles += static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles;
+            items += a.Nkv * p.row_tiles;
+        }
+        line.tile[tid + 1] = tiles;
+        line.item[tid + 1] = items;
+        if (tid == 0) {
+            const Problem p = prefix_problem<TM, KT>(a);
+            line.tile[0] = a.with_prefix ? static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles : 0;
+            line.item[0] = a.with_prefix ? a.Nkv * p.row_tiles : 0;
+        }
+    }
+    __syncthreads();
+    if (tid < 32) {
+        // inclusive scan of 128 entries, 4 to a lane
+        long long t[4];
+        int n[4];
+        for (int i = 0; i < 4; ++i) {
+            t[i] = line.tile[1 + 4 * tid + i] + (i ? t[i - 1] : 0);
+            n[i] = line.item[1 + 4 * tid + i] + (i ? n[i - 1] : 0);
+        }
+        long long ts = t[3];
+        int ns = n[3];
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long tv = __shfl_up_sync(0xffffffffu, ts, o);
+            const int nv = __shfl_up_sync(0xffffffffu, ns, o);
+            if (tid >= o) ts += tv, ns += nv;
+        }
+        const long long t0 = ts - t[3] + line.tile[0];
+        const int n0 = ns - n[3] + line.item[0];
+        for (int i = 0; i < 4; ++i) {
+            line.tile[1 + 4 * tid + i] = t0 + t[i];
+            line.item[1 + 4 * tid + i] = n0 + n[i];
+        }
+    }
+    __syncthreads();
+    if (publish && tid < kRuns) {
+        long long t = line.tile[tid];
+        int n = line.item[tid];
+        for (int b = b0; b < b1; ++b) {
+            const Problem p = sequence_problem<TM, KT>(a, b);
+            a.base_tile[b] = t;
+            a.base_item[b] = n;
+            t += static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles;
+            n += a.Nkv * p.row_tiles;
+        }
+    }
+}
+
+// A block's share of the line; false if it has none.
+__device__ __forceinline__ bool share_of(const PrefixArgs &a, const Line &line, long long *t0, long long *t1) {
+    const long long total = line.tile[kRuns];
+    const long long share = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = share;
+    *t0 = share * blockIdx.x;
+    *t1 = min(*t0 + share, total);
+    return *t0 < *t1;
+}
+
+// A stretch of one item that a block works on.
+struct Piece {
+    int b;                // sequence, -1: the prefix
+    int item;             // index on the line
+    int kvh, tok0, rows;  // rows of the problem
+    int row0;             // first row of the tile
+    long long keys;       // keys of the problem
+    long long off;        // rows of token i see keys [0, off + i] (prefix: all)
+    long long k0, k1;     // key tiles [k0, k1), may be none
+    long long next;       // where the next piece begins on the line
+};
+
+// Keys that row `row` of the problem sees: [0, limit).
+__device__ __forceinline__ long long row_limit(const PrefixArgs &a, const Piece &x, int row) {
+    return x.b < 0 ? x.keys : max(0ll, x.off + row / a.G + 1);
+}
+
+// The piece that begins at place t of the line (t < end), cut at `end`.
+template <int TM, int KT>
+__device__ __forceinline__ Piece find_piece(const PrefixArgs &a, const Line &line, long long t, long long end) {
+    Piece x;
+    Problem p;
+    long long base = 0;
+    int item = 0;
+    if (t < line.tile[0]) {
+        p = prefix_problem<TM, KT>(a);
+        x.b = -1;
+    } else {
+        // the run that holds t: the last entry with tile <= t
+        int lo = 0, hi = kRuns - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (line.tile[mid] <= t) lo = mid; else hi = mid - 1;
+        }
+        base = line.tile[lo];
+        item = line.item[lo];
+        int b = lo * ((a.B + kRuns - 1) / kRuns);
+        for (; b < a.B; ++b) {
+            p = sequence_problem<TM, KT>(a, b);
+            const long long all = static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles;
+            if (t < base + all) break;
+            base += all;
+            item += a.Nkv * p.row_tiles;
+        }
+        x.b = b;
+        if (b >= a.B) {
+            // only when the lists were changed under the launch: a stretch without work
+            x = Piece{};
+            x.next = end;
+            return x;
+        }
+    }
+    const long long at = t - base, which = at / p.key_tiles;
+    x.kvh = static_cast<int>(which / p.row_tiles);
+    const int j = tile_at(static_cast<int>(which - static_cast<long long>(x.kvh) * p.row_tiles), p.row_tiles);
+    x.item = item + static_cast<int>(which);
+    x.row0 = j * TM;
+    x.tok0 = p.tok0;
+    x.rows = p.n * a.G;
+    x.keys = p.keys;
+    x.off = p.keys - p.n;
+    const long long n0 = at - which * p.key_tiles;
+    const long long n1 = min(n0 + (end - t), p.key_tiles);
+    const long long need = (min(p.keys, row_limit(a, x, min(x.row0 + TM, x.rows) - 1)) + KT - 1) / KT;
+    x.k0 = n0 * need / p.key_tiles;
+    x.k1 = n1 * need / p.key_tiles;
+    x.next = t + (n1 - n0);
+    return x;
+}
+
+}  // namespace cpattn

@@ -38,201 +38,22 @@
 
 #include "cp_internal.h"
 #include "cp_paged.cuh"
+#include "cp_prefix.cuh"
 #include "cp_ptx.cuh"
+#include "prefix_tc.cuh"
 
 namespace cpattn {
 namespace {
 
 __device__ int g_prefix_status = 0;
 
+// A problem whose rows for one KV head are more than this runs in tiles of 256
+// rows on the tensor memory, else in tiles of 16.
+constexpr int kTcRows = 16;
+
 constexpr int kThreads = 128;
+constexpr int kTM = 16;  // rows of a tile
 constexpr int kKT = 64;  // keys of a stage
-
-struct PrefixArgs {
-    const __nv_bfloat16 *q, *k, *v;
-    PageTable own, pre;  // the sequences' pages; the prefix as a table of one row
-    const int32_t *cu, *kv_len;
-    int R, B, N, Nkv, G;
-    long long P;
-    float scale_log2;
-    void *o;
-    int o_bf16;
-    float *lse;
-    // workspace
-    long long *head;        // [0]: tiles of a share
-    long long *base_tile;   // [B] first tile of each sequence
-    int *base_item;         // [B]
-    float *slot_ml;         // [slots][TM][2]
-    float *slot_o;          // [slots][TM][D]
-    int slots;
-};
-
-// One problem's shape.
-struct Problem {
-    int tok0, n;        // rows' tokens
-    long long keys;     // keys in all
-    int row_tiles;
-    long long key_tiles;
-};
-
-// Sequence b as the device lists give it; a list that makes no sense is cut to
-// what can be read and reported.
-__device__ __forceinline__ Problem sequence_problem(const PrefixArgs &a, int b, int tm) {
-    Problem p;
-    const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
-    long long len = __ldg(a.kv_len + b);
-    const long long most = static_cast<long long>(a.own.max_pages) << a.own.shift;
-    p.tok0 = c0;
-    p.n = c1 - c0;
-    if (c0 < 0 || c1 < c0 || c1 > a.R) {
-        p.n = 0;
-        atomicExch(&g_prefix_status, static_cast<int>(CP_ERR_PAGE));
-    }
-    if (len < 0 || len > most) {
-        len = len < 0 ? 0 : most;
-        atomicExch(&g_prefix_status, static_cast<int>(CP_ERR_PAGE));
-    }
-    p.keys = len;
-    p.row_tiles = (p.n * a.G + tm - 1) / tm;
-    p.key_tiles = p.n ? (len + kKT - 1) / kKT : 0;
-    return p;
-}
-__device__ __forceinline__ Problem prefix_problem(const PrefixArgs &a, int tm) {
-    Problem p;
-    p.tok0 = 0;
-    p.n = min(max(__ldg(a.cu + a.B), 0), a.R);
-    p.keys = a.P;
-    p.row_tiles = (p.n * a.G + tm - 1) / tm;
-    p.key_tiles = p.n ? (a.P + kKT - 1) / kKT : 0;
-    return p;
-}
-
-// Where every problem's tiles and items begin on the line: sums over the
-// thread's run of sequences, scanned over the block (128 entries in shared
-// memory however many sequences there are).
-struct Line {
-    long long tile[kThreads + 1];
-    int item[kThreads + 1];
-};
-
-__device__ __forceinline__ void scan_line(const PrefixArgs &a, int tm, Line &line, bool publish) {
-    const int tid = threadIdx.x, run = (a.B + kThreads - 1) / kThreads;
-    const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
-    long long tiles = 0;
-    int items = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Problem p = sequence_problem(a, b, tm);
-        tiles += static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles;
-        items += a.Nkv * p.row_tiles;
-    }
-    line.tile[tid + 1] = tiles;
-    line.item[tid + 1] = items;
-    if (tid == 0) {
-        const Problem p = prefix_problem(a, tm);
-        line.tile[0] = static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles;
-        line.item[0] = a.Nkv * p.row_tiles;
-    }
-    __syncthreads();
-    if (tid < 32) {
-        // inclusive scan of 128 entries, 4 to a lane
-        long long t[4];
-        int n[4];
-        for (int i = 0; i < 4; ++i) {
-            t[i] = line.tile[1 + 4 * tid + i] + (i ? t[i - 1] : 0);
-            n[i] = line.item[1 + 4 * tid + i] + (i ? n[i - 1] : 0);
-        }
-        long long ts = t[3];
-        int ns = n[3];
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long tv = __shfl_up_sync(0xffffffffu, ts, o);
-            const int nv = __shfl_up_sync(0xffffffffu, ns, o);
-            if (tid >= o) ts += tv, ns += nv;
-        }
-        const long long t0 = ts - t[3] + line.tile[0];
-        const int n0 = ns - n[3] + line.item[0];
-        for (int i = 0; i < 4; ++i) {
-            line.tile[1 + 4 * tid + i] = t0 + t[i];
-            line.item[1 + 4 * tid + i] = n0 + n[i];
-        }
-    }
-    __syncthreads();
-    if (publish) {
-        long long t = line.tile[tid];
-        int n = line.item[tid];
-        for (int b = b0; b < b1; ++b) {
-            const Problem p = sequence_problem(a, b, tm);
-            a.base_tile[b] = t;
-            a.base_item[b] = n;
-            t += static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles;
-            n += a.Nkv * p.row_tiles;
-        }
-    }
-}
-
-// A stretch of one item that a block works on.
-struct Piece {
-    int b;               // sequence, -1: the prefix
-    int item;            // index on the line
-    int kvh, tok0, rows; // rows of the problem
-    int row0;            // first row of the tile
-    long long keys;      // keys of the problem
-    long long off;       // rows of token i see keys [0, off + i] (prefix: all)
-    long long k0, k1;    // key tiles [k0, k1)
-};
-
-// The piece that begins at tile t of the line (t < end), cut at `end`.
-__device__ __forceinline__ Piece find_piece(const PrefixArgs &a, int tm, const Line &line, long long t, long long end) {
-    Piece x;
-    Problem p;
-    long long base = 0;
-    int item = 0;
-    if (t < line.tile[0]) {
-        p = prefix_problem(a, tm);
-        x.b = -1;
-    } else {
-        // the thread run that holds t: the last entry with tile <= t
-        int lo = 0, hi = kThreads - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (line.tile[mid] <= t) lo = mid; else hi = mid - 1;
-        }
-        const int run = (a.B + kThreads - 1) / kThreads;
-        base = line.tile[lo];
-        item = line.item[lo];
-        int b = lo * run;
-        for (; b < a.B; ++b) {
-            p = sequence_problem(a, b, tm);
-            const long long all = static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles;
-            if (t < base + all) break;
-            base += all;
-            item += a.Nkv * p.row_tiles;
-        }
-        x.b = b;
-        if (b >= a.B) {
-            // only when the lists were changed under the launch: a stretch without rows
-            x = Piece{};
-            x.k1 = end - t;
-            return x;
-        }
-    }
-    const long long at = t - base, which = at / p.key_tiles;
-    x.item = item + static_cast<int>(which);
-    x.kvh = static_cast<int>(which / p.row_tiles);
-    x.row0 = static_cast<int>(which - static_cast<long long>(x.kvh) * p.row_tiles) * tm;
-    x.tok0 = p.tok0;
-    x.rows = p.n * a.G;
-    x.keys = p.keys;
-    x.off = x.b < 0 ? a.P : p.keys - p.n;
-    x.k0 = at - which * p.key_tiles;
-    x.k1 = x.k0 + (end - t) < p.key_tiles ? x.k0 + (end - t) : p.key_tiles;
-    return x;
-}
-
-// Keys that row i of the problem sees: [0, limit).
-__device__ __forceinline__ long long row_limit(const PrefixArgs &a, const Piece &x, int row) {
-    if (row >= x.rows) return 0;
-    return x.b < 0 ? x.keys : x.off + row / a.G + 1;
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     const int n = valid ? 16 : 0;
@@ -264,7 +85,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 
 template <int D>
 struct MmaCfg {
-    static constexpr int kTM = 16;
     static constexpr int kRowBytes = D * 2;
     static constexpr int kTileBytes = kKT * kRowBytes;     // K or V of a stage
     static constexpr int kStages = D == 128 ? 2 : 4;
@@ -291,23 +111,23 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_mma_kernel(const PrefixArg
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
 
-    scan_line(a, C::kTM, line, blockIdx.x == 0);
-    const long long total = line.tile[kThreads];
-    long long share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < 1) share = 1;
-    if (blockIdx.x == 0 && tid == 0) a.head[0] = share;
-    const long long t0 = share * blockIdx.x, t1 = min(t0 + share, total);
-    if (t0 >= t1) return;
+    scan_line<kTM, kKT>(a, line, blockIdx.x == 0);
+    long long t0, t1;
+    if (!share_of(a, line, &t0, &t1)) return;
 
     // loads run ahead of the products over the tiles of all the block's pieces
-    Piece lp = find_piece(a, C::kTM, line, t0, t1);
-    long long lt = t0, lk = lp.k0;
+    Piece lp = find_piece<kTM, kKT>(a, line, t0, t1);
+    long long lk = lp.k0;
     int lstage = 0;
     auto load_next = [&]() {
-        if (lt < t1) {
+        while (lk == lp.k1 && lp.next < t1) {
+            lp = find_piece<kTM, kKT>(a, line, lp.next, t1);
+            lk = lp.k0;
+        }
+        if (lk < lp.k1) {
             const PageTable &pt = lp.b < 0 ? a.pre : a.own;
-            const int last_row = min(lp.row0 + C::kTM, lp.rows) - 1;
-            const long long limit = row_limit(a, lp, last_row);  // keys that any row of the tile sees
+            // keys that any row of the tile sees
+            const long long limit = min(lp.keys, row_limit(a, lp, min(lp.row0 + kTM, lp.rows) - 1));
             const uint32_t ks = sbase + lstage * 2 * C::kTileBytes, vs = ks + C::kTileBytes;
             constexpr int kChunks = D / 8, kStep = kThreads / kChunks;  // rows between a thread's chunks
             const int c = tid % kChunks;
@@ -317,18 +137,14 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_mma_kernel(const PrefixArg
                 long long slot = -1;
                 if (key < limit) {
                     slot = pt.slot(lp.b < 0 ? 0 : lp.b, key);
-                    if (slot < 0 && c == 0) atomicExch(&g_prefix_status, static_cast<int>(CP_ERR_PAGE));
+                    if (slot < 0 && c == 0) report(a.status, CP_ERR_PAGE);
                 }
                 const long long off = slot < 0 ? 0 : (slot * a.Nkv + lp.kvh) * D + c * 8;
                 cp_async16(ks + tile_off<D>(r, c), a.k + off, slot >= 0);
                 cp_async16(vs + tile_off<D>(r, c), a.v + off, slot >= 0);
             }
             lstage = lstage + 1 == C::kStages ? 0 : lstage + 1;
-            ++lt;
-            if (++lk == lp.k1 && lt < t1) {
-                lp = find_piece(a, C::kTM, line, lt, t1);
-                lk = lp.k0;
-            }
+            ++lk;
         }
         cp_async_commit();
     };
@@ -338,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_mma_kernel(const PrefixArg
     const int g = lane >> 2, t4 = lane & 3;  // accumulator row (and row + 8), column pair
     int stage = 0;
     for (long long t = t0; t < t1;) {
-        const Piece x = find_piece(a, C::kTM, line, t, t1);
+        const Piece x = find_piece<kTM, kKT>(a, line, t, t1);
+        t = x.next;
         // this warp's copy of the rows as A operands
         uint32_t qf[D / 16][4];
 #pragma unroll
@@ -354,16 +171,17 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_mma_kernel(const PrefixArg
                 qf[kk][2 + h] = ok ? __ldg(reinterpret_cast<const uint32_t *>(qp + kk * 16 + 8 + 2 * t4)) : 0u;
             }
         }
-        const long long lim0 = row_limit(a, x, x.row0 + g), lim1 = row_limit(a, x, x.row0 + g + 8);
+        const long long lim0 = x.row0 + g < x.rows ? min(x.keys, row_limit(a, x, x.row0 + g)) : 0;
+        const long long lim1 = x.row0 + g + 8 < x.rows ? min(x.keys, row_limit(a, x, x.row0 + g + 8)) : 0;
         // tiles from the first that some row does not see whole on are masked
-        const long long whole = x.row0 + C::kTM <= x.rows ? row_limit(a, x, x.row0) : 0;
+        const long long whole = x.row0 + kTM <= x.rows ? min(x.keys, row_limit(a, x, x.row0)) : 0;
         float o[D / 8][4];
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        for (long long kt = x.k0; kt < x.k1; ++kt, ++t) {
+        for (long long kt = x.k0; kt < x.k1; ++kt) {
             load_next();
             cp_async_wait<C::kStages - 1>();
             __syncthreads();
@@ -481,22 +299,37 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_mma_kernel(const PrefixArg
                 }
                 *reinterpret_cast<float4 *>(dst + c) = v;
             }
-            if (c0 == 0) {
-                a.slot_ml[(static_cast<long long>(slot) * 16 + row) * 2] = mx;
-                a.slot_ml[(static_cast<long long>(slot) * 16 + row) * 2 + 1] = ls;
-            }
+            if (c0 == 0) a.slot_ml[static_cast<long long>(slot) * 16 + row] = make_float2(mx, ls);
         } else if (tid == 0) {
-            atomicExch(&g_prefix_status, static_cast<int>(CP_ERR_PAGE));
+            report(a.status, CP_ERR_PAGE);
         }
         __syncthreads();
     }
     cp_async_wait<0>();
 }
 
+// What a launch left, as the join reads it.
+struct JoinPart {
+    const long long *head, *base_tile;
+    const int *base_item;
+    const float2 *slot_ml;
+    const float *slot_o;
+    int slots, tm, kt;
+};
+struct JoinArgs {
+    JoinPart part[2];  // the prefix; the sequences
+    const int32_t *cu, *kv_len;
+    int R, B, N, Nkv, G;
+    long long P, most;  // most: keys that a sequence's table can hold
+    void *o;
+    int o_bf16;
+    float *lse;
+};
+
 // One warp joins the pieces of one output row (token, head).
 template <int D>
-__global__ void __launch_bounds__(128) prefix_join_kernel(const PrefixArgs a) {
-    constexpr int TM = MmaCfg<D>::kTM, kV = D / 32;
+__global__ void __launch_bounds__(128) prefix_join_kernel(const JoinArgs a) {
+    constexpr int kV = D / 32;
     const int lane = threadIdx.x & 31;
     const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (row >= static_cast<long long>(a.R) * a.N) return;
@@ -505,40 +338,30 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PrefixArgs a) {
     int begin, count;
     const int b = find_sequence(a.cu, a.B, tok, lane, &begin, &count);
     if (b < 0) return;
-    const long long share = a.head[0];
-    // the stretch of the line and the slots of the row's two items
-    long long first[2], last[2];
-    int item[2], r[2];
-    {
-        const Problem p = prefix_problem(a, TM);
-        const int i = tok * a.G + gh;
-        const long long at = static_cast<long long>(kvh) * p.row_tiles + i / TM;
-        item[0] = static_cast<int>(at);
-        first[0] = at * p.key_tiles;
-        last[0] = first[0] + p.key_tiles;
-        r[0] = i % TM;
-    }
-    {
-        const Problem p = sequence_problem(a, b, TM);
-        const int i = (tok - begin) * a.G + gh;
-        const long long at = static_cast<long long>(kvh) * p.row_tiles + i / TM;
-        item[1] = __ldg(a.base_item + b) + static_cast<int>(at);
-        first[1] = __ldg(a.base_tile + b) + at * p.key_tiles;
-        last[1] = first[1] + p.key_tiles;
-        r[1] = i % TM;
-    }
     float mx = -INFINITY, ls = 0.f, acc[kV];
 #pragma unroll
     for (int e = 0; e < kV; ++e) acc[e] = 0.f;
-    for (int part = 0; part < 2; ++part) {
-        if (first[part] >= last[part]) continue;
-        const int c0 = static_cast<int>(first[part] / share), c1 = static_cast<int>((last[part] - 1) / share);
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const JoinPart &p = a.part[which];
+        // the row's item: its stretch of the line, its pieces' slots and its row in them
+        const int n = which ? count : min(max(__ldg(a.cu + a.B), 0), a.R);
+        const long long keys = which ? min(max(static_cast<long long>(__ldg(a.kv_len + b)), 0ll), a.most) : a.P;
+        const long long key_tiles = (keys + p.kt - 1) / p.kt;
+        if (key_tiles == 0) continue;
+        const int row_tiles = (n * a.G + p.tm - 1) / p.tm, i = (tok - (which ? begin : 0)) * a.G + gh, r = i % p.tm;
+        if (i >= n * a.G) continue;
+        const long long at = static_cast<long long>(kvh) * row_tiles + place_of(i / p.tm, row_tiles);
+        const int item = (which ? __ldg(p.base_item + b) : 0) + static_cast<int>(at);
+        const long long first = (which ? __ldg(p.base_tile + b) : 0) + at * key_tiles;
+        const long long share = __ldg(p.head);
+        const int c0 = static_cast<int>(first / share), c1 = static_cast<int>((first + key_tiles - 1) / share);
         for (int cb = c0; cb <= c1; cb += 32) {
             // up to 32 pieces: their (m, l) side by side, then their rows one after another
-            const int slot = item[part] + cb + lane;
+            const int slot = item + cb + lane;
             float pm = -INFINITY, pl = 0.f;
-            if (cb + lane <= c1 && slot < a.slots) {
-                const float2 ml = __ldg(reinterpret_cast<const float2 *>(a.slot_ml) + static_cast<long long>(slot) * TM + r[part]);
+            if (cb + lane <= c1 && slot < p.slots) {
+                const float2 ml = __ldg(p.slot_ml + static_cast<long long>(slot) * p.tm + r);
                 pm = ml.x;
                 pl = ml.y;
             }
@@ -558,11 +381,11 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PrefixArgs a) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
             ls += add;
-            const int n = min(32, c1 - cb + 1);
+            const int m = min(32, c1 - cb + 1);
 #pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                const float f = __shfl_sync(0xffffffffu, w, i);
-                const float *src = a.slot_o + (static_cast<long long>(item[part] + cb + i) * TM + r[part]) * D + lane * kV;
+            for (int k = 0; k < m; ++k) {
+                const float f = __shfl_sync(0xffffffffu, w, k);
+                const float *src = p.slot_o + (static_cast<long long>(item + cb + k) * p.tm + r) * D + lane * kV;
                 if (f != 0.f) {
                     if (kV == 4) {
                         const float4 y = __ldg(reinterpret_cast<const float4 *>(src));
@@ -592,40 +415,96 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PrefixArgs a) {
 }
 
 // ---------------------------------------------------------------- host side
-int grid_blocks() { return 2 * sm_count(); }
+constexpr int kMaxBlocks = 320;  // of a launch (a slot more for each)
 
-struct Layout {
-    size_t base_tile, base_item, slot_ml, slot_o, bytes;
-    long long slots;
+// How a call is cut: which launches it makes and where they leave their pieces.
+struct Shape {
+    bool tc_prefix, tc_own;  // tensor-memory tiles of 256 rows, else tiles of 16 rows
+    long long slots[2];      // of the 16-row launch and the 256-row launch (0: not made)
+    size_t head[2], base_tile[2], base_item[2], slot_ml[2], slot_o[2], bytes;
 };
-Layout layout_of(int64_t R, int64_t B, int64_t N, int64_t Nkv, int64_t D) {
-    const long long G = N / Nkv, tiles = (R * G + 15) / 16;
-    Layout l;
-    // every row tile of the prefix, of the sequences (each may end a tile early), and a cut for each block
-    l.slots = Nkv * (2 * tiles + B) + 2 * 160;
-    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-    l.base_tile = 256;
-    l.base_item = up(l.base_tile + B * 8);
-    l.slot_ml = up(l.base_item + B * 4);
-    l.slot_o = up(l.slot_ml + static_cast<size_t>(l.slots) * 16 * 8);
-    l.bytes = up(l.slot_o + static_cast<size_t>(l.slots) * 16 * D * 4);
-    return l;
+
+Shape shape_of(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int64_t Nkv, int64_t D) {
+    const long long G = N / Nkv;
+    Shape s{};
+    s.tc_prefix = R * G > kTcRows;
+    s.tc_own = max_new * G > kTcRows;
+    size_t at = 0;
+    auto take = [&at](size_t n) {
+        const size_t x = at;
+        at = (at + n + 255) & ~size_t(255);
+        return x;
+    };
+    for (int k = 0; k < 2; ++k) {
+        const bool pre = P > 0 && s.tc_prefix == (k == 1), own = s.tc_own == (k == 1);
+        const long long tm = k ? kTcTM : kTM, tiles = (R * G + tm - 1) / tm;
+        if (!pre && !own) continue;
+        // every row tile of the prefix and of the sequences (each may end a tile early), and a cut for each block
+        s.slots[k] = Nkv * ((pre ? tiles : 0) + (own ? tiles + (B < R ? B : R) : 0)) + kMaxBlocks;
+        s.head[k] = take(8);
+        s.base_tile[k] = take(B * 8);
+        s.base_item[k] = take(B * 4);
+        s.slot_ml[k] = take(static_cast<size_t>(s.slots[k]) * tm * 8);
+        s.slot_o[k] = take(static_cast<size_t>(s.slots[k]) * tm * D * 4);
+    }
+    s.bytes = at;
+    return s;
 }
 
 template <int D>
-cp_status launch_typed(const PrefixArgs &a, cudaStream_t stream) {
+cp_status launch_mma(const PrefixArgs &a, cudaStream_t stream) {
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [] {
         err = cudaFuncSetAttribute(prefix_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, MmaCfg<D>::kSmem);
     });
     if (err != cudaSuccess) return cuda_status(err);
-    const int grid = grid_blocks() < 320 ? grid_blocks() : 320;
+    const int grid = 2 * sm_count() < kMaxBlocks ? 2 * sm_count() : kMaxBlocks;
     prefix_mma_kernel<D><<<grid, kThreads, MmaCfg<D>::kSmem, stream>>>(a);
-    cp_status st = last_launch_status();
-    if (st != CP_OK) return st;
+    return last_launch_status();
+}
+
+template <int D>
+cp_status launch_tc(const PrefixArgs &a, int64_t slots, int box_rows, cudaStream_t stream) {
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<D>::kSmem);
+    });
+    if (err != cudaSuccess) return cuda_status(err);
+    CUtensorMap mk, mv;
+    if (!make_map(&mk, a.k, D, a.Nkv, slots, 1, box_rows) || !make_map(&mv, a.v, D, a.Nkv, slots, 1, box_rows))
+        return CP_ERR_CUDA;
+    const int grid = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
+    prefix_tc_kernel<D><<<grid, kTcThreads, TcCfg<D>::kSmem, stream>>>(mk, mv, a);
+    return last_launch_status();
+}
+
+template <int D>
+cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cudaStream_t stream) {
+    const int64_t slots = static_cast<int64_t>(a.own.n_pages) << a.own.shift;
+    const int box_rows = a.own.shift < 7 ? 1 << a.own.shift : 128;
+    // the wide launch first: it has the prefix, the longer work
+    for (int k = 1; k >= 0; --k) {
+        if (!s.slots[k]) continue;
+        a.with_prefix = a.P > 0 && s.tc_prefix == (k == 1);
+        a.with_own = s.tc_own == (k == 1);
+        a.head = reinterpret_cast<long long *>(w + s.head[k]);
+        a.base_tile = reinterpret_cast<long long *>(w + s.base_tile[k]);
+        a.base_item = reinterpret_cast<int *>(w + s.base_item[k]);
+        a.slot_ml = reinterpret_cast<float2 *>(w + s.slot_ml[k]);
+        a.slot_o = reinterpret_cast<float *>(w + s.slot_o[k]);
+        a.slots = static_cast<int>(s.slots[k]);
+        const cp_status st = k ? launch_tc<D>(a, slots, box_rows, stream) : launch_mma<D>(a, stream);
+        if (st != CP_OK) return st;
+        for (int which = 0; which < 2; ++which)
+            if (which ? a.with_own : a.with_prefix)
+                j.part[which] = JoinPart{a.head, a.base_tile, a.base_item, a.slot_ml, a.slot_o, a.slots,
+                                         k ? kTcTM : kTM, k ? kTcKT : kKT};
+    }
+    if (a.P == 0) j.part[0] = j.part[1];  // not read into a result: no keys
     const long long rows = static_cast<long long>(a.R) * a.N;
-    prefix_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(a);
+    prefix_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(j);
     return last_launch_status();
 }
 
@@ -639,6 +518,14 @@ cp_status check_sizes(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t 
     return CP_OK;
 }
 
+}  // namespace
+
+namespace {
+// Device address of the status word in the current context (looked up at each
+// call: a new context has another).
+cp_status status_word(int **p) {
+    return cuda_status(cudaGetSymbolAddress(reinterpret_cast<void **>(p), g_prefix_status));
+}
 }  // namespace
 
 cp_status read_prefix_device_status(int *code, bool clear) {
@@ -660,7 +547,7 @@ extern "C" cp_status cp_prefix_attn_workspace_size(int64_t R, int64_t B, int64_t
     if (!bytes) return CP_ERR_NULL;
     const cp_status st = check_sizes(R, B, max_new, prefix_len, N, Nkv, D, page_size, max_pages);
     if (st != CP_OK) return st;
-    *bytes = layout_of(R, B, N, Nkv, D).bytes;
+    *bytes = shape_of(R, B, max_new, prefix_len, N, Nkv, D).bytes;
     return CP_OK;
 }
 
@@ -681,10 +568,13 @@ extern "C" cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, cons
     if (odd(q, 16) || odd(k_cache, 16) || odd(v_cache, 16) || odd(o, 16) || odd(lse, 4) || odd(table, 4) ||
         odd(prefix_pages, 4) || odd(cu_new, 4) || odd(kv_len, 4))
         return CP_ERR_ALIGNMENT;
-    const Layout l = layout_of(R, B, N, Nkv, D);
-    if (!workspace || ws_bytes < l.bytes) return CP_ERR_WORKSPACE;
+    const Shape s = shape_of(R, B, max_new, prefix_len, N, Nkv, D);
+    if (!workspace || ws_bytes < s.bytes) return CP_ERR_WORKSPACE;
     if (odd(workspace, 256)) return CP_ERR_ALIGNMENT;
+    if (s.slots[0] > INT32_MAX || s.slots[1] > INT32_MAX) return CP_ERR_SHAPE;
     PrefixArgs a{};
+    if ((st = status_word(&a.status)) != CP_OK) return st;
+    a.timeout_ns = 2000000000ull;
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.k = static_cast<const __nv_bfloat16 *>(k_cache);
     a.v = static_cast<const __nv_bfloat16 *>(v_cache);
@@ -706,15 +596,15 @@ extern "C" cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, cons
     a.G = static_cast<int>(N / Nkv);
     a.P = prefix_len;
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-    a.o = o;
-    a.o_bf16 = o_dtype == CP_BF16;
-    a.lse = lse;
+    JoinArgs j{};
+    j.cu = cu_new;
+    j.kv_len = kv_len;
+    j.R = a.R, j.B = a.B, j.N = a.N, j.Nkv = a.Nkv, j.G = a.G;
+    j.P = prefix_len;
+    j.most = max_pages * page_size;
+    j.o = o;
+    j.o_bf16 = o_dtype == CP_BF16;
+    j.lse = lse;
     uint8_t *w = static_cast<uint8_t *>(workspace);
-    a.head = reinterpret_cast<long long *>(w);
-    a.base_tile = reinterpret_cast<long long *>(w + l.base_tile);
-    a.base_item = reinterpret_cast<int *>(w + l.base_item);
-    a.slot_ml = reinterpret_cast<float *>(w + l.slot_ml);
-    a.slot_o = reinterpret_cast<float *>(w + l.slot_o);
-    a.slots = static_cast<int>(l.slots);
-    return D == 128 ? launch_typed<128>(a, stream) : launch_typed<64>(a, stream);
+    return D == 128 ? launch_call<128>(a, s, w, j, stream) : launch_call<64>(a, s, w, j, stream);
 }

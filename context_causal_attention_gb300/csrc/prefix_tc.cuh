@@ -1,0 +1,391 @@
+// prefix_tc.cuh -- the shared-prefix attention's kernel for many rows: tiles of
+// 2 x 128 rows on tcgen05 (S and O in tensor memory, K and V pages by TMA).
+//
+// One block on an SM works through its share of the line (cp_prefix.cuh) with
+// 12 warps:
+//   warp 0      loads: the page numbers of a 128-key tile side by side in its
+//               lanes, one tile ahead; each lane starts the copies of its page
+//               (64 columns x a page's rows a copy, 128-byte swizzle) into a
+//               ring of K and V stages.  A page number out of range becomes a
+//               coordinate outside the tensor, which TMA fills with zeros.
+//   warp 1      tensor memory (512 columns: S0 | S1 | O0 | O1) and MMA issue:
+//               S_i = Q_i K^T, O_i += P_i V with P_i in tensor memory.
+//   warps 4-7   softmax of rows 0..127, warps 8-11 of rows 128..255: one thread
+//               a row, in the log2 domain with an integer running maximum that
+//               moves only when a tile's sum passes 2^64 (as in attn.cu).
+// The rows of a tile are query heads of the same KV head from one or many
+// sequences, so the softmax threads gather Q themselves (a thread its row, into
+// the swizzled layout) instead of TMA.  A tile of up to 128 rows leaves the
+// second half idle.  Keys past the problem's length lie in a page's tail or in
+// pages that were not loaded: their scores become -inf, and their V rows are
+// zeroed in shared memory before the product reads them, so nothing that they
+// hold (NaN included) is multiplied.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "cp_prefix.cuh"
+#include "cp_ptx.cuh"
+#include "cp_softmax.cuh"
+
+namespace cpattn {
+namespace {
+
+constexpr int kTcThreads = 384;
+constexpr int kTcTM = 256;  // rows of a tile
+constexpr int kTcKT = 128;  // keys of a stage
+
+template <int D>
+struct TcCfg {
+    static constexpr int kAtom = 128 * 128;  // 128 rows x 64 columns
+    static constexpr int kAtoms = D / 64;
+    static constexpr int kTile = kAtom * kAtoms;
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = 2 * kTile;
+    static constexpr int kOffV = kOffK + kStages * kTile;
+    static constexpr int kOffLine = kOffV + kStages * kTile;
+    static constexpr int kOffBar = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
+    // q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain, k_full[S], v_full[S], k_empty[S], v_empty[S]
+    static constexpr int kBars = 11 + 4 * kStages;
+    static constexpr int kOffMisc = kOffBar + kBars * 8;
+    static constexpr int kSmem = kOffMisc + 16 + 1024;  // + alignment slack
+    static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ void fence_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Scores of columns c0 .. c0+63 that the row does not see (column >= lim) become -inf.
+__device__ __forceinline__ void hide_columns(int c0, int lim, uint32_t (&h)[64]) {
+#pragma unroll
+    for (int c = 0; c < 64; ++c)
+        if (c0 + c >= lim) h[c] = 0xff800000u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const PrefixArgs a) {
+    using C = TcCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    Line &line = *reinterpret_cast<Line *>(smem + C::kOffLine);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint64_t *q_full = bar, *s_full = bar + 2, *p_full = bar + 4, *o_full = bar + 6, *o_empty = bar + 8;
+    uint64_t *drain = bar + 10, *k_full = bar + 11, *v_full = k_full + C::kStages, *k_empty = v_full + C::kStages,
+             *v_empty = k_empty + C::kStages;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
+
+    if (tid == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 4);
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4);
+            mbar_init(o_full + i, 1);
+            mbar_init(o_empty + i, 4);
+        }
+        mbar_init(drain, 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(k_full + s, 1);
+            mbar_init(v_full + s, 1);
+            mbar_init(k_empty + s, 1);
+            mbar_init(v_empty + s, 1);
+        }
+        fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    scan_line<kTcTM, kTcKT>(a, line, blockIdx.x == 0);
+    long long t0, t1;
+    if (!share_of(a, line, &t0, &t1)) return;
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    uint8_t *sQ = smem + C::kOffQ, *sK = smem + C::kOffK, *sV = smem + C::kOffV;
+
+    if (warp == 0) {
+        // -------------------------------------------------------- loads
+        const int shift = a.own.shift, rows = min(128, 1 << shift);  // rows of a copy
+        const int per_tile = 128 / rows;                             // copies of a tile and 64 columns
+        const int nowhere = a.own.n_pages << shift;                  // a row outside the tensor
+        uint32_t k_it = 0, v_it = 0, k_par = 0, v_par = 0, k_issued = 0, v_issued = 0;
+        bool ok = true;
+        // cache row of this lane's copy of tile kt (-1: past the keys)
+        auto page_row = [&](const Piece &x, long long kt) -> int {
+            const long long key = kt * 128 + lane * rows;
+            if (lane >= per_tile || key >= x.keys) return -1;
+            const long long slot = (x.b < 0 ? a.pre : a.own).slot(x.b < 0 ? 0 : x.b, key);
+            if (slot < 0) report(a.status, CP_ERR_PAGE);
+            return slot < 0 ? nowhere : static_cast<int>(slot);
+        };
+        auto load = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *full, uint64_t *empty, uint32_t &it,
+                        uint32_t &par, uint32_t &issued, int row, int kvh) -> bool {
+            const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
+            if (!mbar_wait_warp(empty + st, ph ^ 1u, abort_flag, a.timeout_ns)) return false;
+            const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(full + st, n * rows * 128 * C::kAtoms);
+            __syncwarp();
+            if (row >= 0)
+                for (int at = 0; at < C::kAtoms; ++at)
+                    tma_load_4d(dst + st * C::kTile + at * C::kAtom + lane * rows * 128, map, full + st, 64 * at, kvh,
+                                row, 0);
+            issued |= 1u << st;
+            par = (par & ~(1u << st)) | (ph << st);
+            ++it;
+            return true;
+        };
+        // K runs one tile ahead of V: a K stage is free after the tile's scores, a
+        // V stage only after its weights have been used
+        bool pend = false;
+        int pend_row = -1, pend_kvh = 0;
+        for (long long t = t0; t < t1 && ok;) {
+            const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
+            t = x.next;
+            if (x.k0 >= x.k1) continue;
+            int row = page_row(x, x.k0);
+            for (long long kt = x.k0; kt < x.k1; ++kt) {
+                const int next = kt + 1 < x.k1 ? page_row(x, kt + 1) : -1;
+                if (!load(&tmK, sK, k_full, k_empty, k_it, k_par, k_issued, row, x.kvh) ||
+                    (pend && !load(&tmV, sV, v_full, v_empty, v_it, v_par, v_issued, pend_row, pend_kvh))) {
+                    ok = false;
+                    break;
+                }
+                pend = true;
+                pend_row = row;
+                pend_kvh = x.kvh;
+                row = next;
+            }
+        }
+        if (ok && pend && !load(&tmV, sV, v_full, v_empty, v_it, v_par, v_issued, pend_row, pend_kvh)) ok = false;
+        if (!ok && lane == 0) {
+            // let every copy already issued land before shared memory goes away
+            volatile int no_abort = 0;
+            for (int st = 0; st < C::kStages; ++st) {
+                if ((k_issued >> st) & 1u) mbar_wait(k_full + st, (k_par >> st) & 1u, &no_abort, 100000000ull);
+                if ((v_issued >> st) & 1u) mbar_wait(v_full + st, (v_par >> st) & 1u, &no_abort, 100000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // -------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
+            constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);
+            const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+            const uint64_t dq1 = smem_desc_sw128(smem_u32(sQ) + C::kTile, 16, 1024);
+            const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
+            const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), C::kAtom, 1024);
+            constexpr uint64_t kStageDesc = C::kTile >> 4;
+            uint32_t kv = 0, items[2] = {0, 0}, tiles[2] = {0, 0};
+            bool ok = true;
+            // P V of the tile before `kv` for half i
+            auto pv = [&](int i, int last, bool first_of_item, uint32_t acc) -> bool {
+                const uint32_t st = (kv - 1) % C::kStages, ph = ((kv - 1) / C::kStages) & 1u;
+                if (i == 0 && !mbar_wait(v_full + st, ph, abort_flag, a.timeout_ns)) return false;
+                if (first_of_item && !mbar_wait(o_empty + i, (items[i] & 1u) ^ 1u, abort_flag, a.timeout_ns)) return false;
+                if (!mbar_wait(p_full + i, tiles[i] & 1u, abort_flag, a.timeout_ns)) return false;
+                tc_fence_after();
+                ++tiles[i];
+                umma_pv_group(tmem + 256 + i * D, tmem + i * 128 + 64, dv0 + st * kStageDesc, kIdescPV, acc);
+                if (i == last) umma_commit(v_empty + st);
+                return true;
+            };
+            for (long long t = t0; t < t1 && ok;) {
+                const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
+                t = x.next;
+                if (x.k0 >= x.k1) continue;
+                const int last = x.rows - x.row0 > 128;  // the second half has rows
+                for (int i = 0; i <= last && ok; ++i) ok = mbar_wait(q_full + i, items[i] & 1u, abort_flag, a.timeout_ns);
+                if (!ok) break;
+                tc_fence_after();
+                const long long n = x.k1 - x.k0;
+                for (long long j = 0; j < n && ok; ++j) {
+                    const uint32_t st = kv % C::kStages, ph = (kv / C::kStages) & 1u;
+                    if (!mbar_wait(k_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
+                    tc_fence_after();
+                    for (int i = 0; i <= last; ++i) {
+                        if (j > 0 && !pv(i, last, j == 1, j > 1)) { ok = false; break; }
+                        umma_qk_group<D / 16>(tmem + i * 128, i ? dq1 : dq0, dk0 + st * kStageDesc, kIdescQK);
+                        umma_commit(s_full + i);
+                    }
+                    if (!ok) break;
+                    umma_commit(k_empty + st);
+                    ++kv;
+                }
+                for (int i = 0; i <= last && ok; ++i) {
+                    if (!pv(i, last, n == 1, n > 1)) { ok = false; break; }
+                    umma_commit(o_full + i);
+                    ++items[i];
+                }
+            }
+            // no MMA may still be running when tensor memory is released
+            umma_commit(drain);
+            volatile int no_abort = 0;
+            mbar_wait(drain, 0, &no_abort, 100000000ull);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // -------------------------------------------------------- softmax
+        const int half = (warp - 4) >> 2, in_tile = (warp & 3) * 32 + lane;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_off + half * 128, tO = tmem + lane_off + 256 + half * D;
+        const float sl2 = a.scale_log2;
+        uint32_t tiles = 0, items = 0, kv = 0;
+        bool ok = true;
+        for (long long t = t0; t < t1 && ok;) {
+            const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
+            const int row = x.row0 + half * 128 + in_tile;
+            const bool valid = row < x.rows;
+            const int slot = x.item + static_cast<int>(blockIdx.x);
+            const bool write = valid && slot < a.slots;
+            if (slot >= a.slots && in_tile == 0) report(a.status, CP_ERR_PAGE);
+            t = x.next;
+            if (x.k0 >= x.k1) {
+                if (write) a.slot_ml[static_cast<long long>(slot) * kTcTM + half * 128 + in_tile] = make_float2(-INFINITY, 0.f);
+                continue;
+            }
+            if (x.row0 + half * 128 >= x.rows) {
+                kv += static_cast<uint32_t>(x.k1 - x.k0);
+                continue;  // no rows in this half
+            }
+            // this thread's row of Q, swizzled as TMA would (the last item's products have all read the tile: o_full)
+            {
+                const int tok = valid ? row / a.G : 0;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.q + (static_cast<long long>(x.tok0 + tok) * a.N + x.kvh * a.G + (valid ? row - tok * a.G : 0)) * D);
+                uint8_t *dst = sQ + half * C::kTile + in_tile * 128;
+                uint4 v[D / 8];
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) v[c] = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kAtom + (((c & 7) ^ (in_tile & 7)) << 4)) = v[c];
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full + half);
+            }
+            const long long limit = valid ? min(x.keys, row_limit(a, x, row)) : x.keys;
+            const long long whole = min(x.keys, row_limit(a, x, x.row0 + half * 128));  // seen by every row
+            float m_run = -INFINITY, l_run = 0.f;
+            for (long long kt = x.k0; kt < x.k1; ++kt, ++kv, ++tiles) {
+                const long long past = x.keys - kt * 128;
+                if (half == 0 && past < 128) {
+                    const uint32_t st = kv % C::kStages, ph = (kv / C::kStages) & 1u;
+                    if (!mbar_wait_warp(v_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
+                    if (in_tile >= past) {
+                        uint8_t *dst = sV + st * C::kTile + in_tile * 128;
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kAtom + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_async_shared();
+                }
+                if (!mbar_wait_warp(s_full + half, tiles & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                tc_fence_after();
+                const bool mask = kt * 128 + 128 > whole;
+                const int lim = static_cast<int>(min(128ll, max(0ll, limit - kt * 128)));
+                uint32_t sa[64], sb[64], pa[32], pb[32];
+                tmem_ld64_nowait(tS, sa);
+                tmem_wait_ld(sa);
+                tmem_ld64_nowait(tS + 64, sb);
+                if (mask) hide_columns(0, lim, sa);
+                const bool first = !__all_sync(0xffffffffu, m_run != -INFINITY);
+                if (first) {
+                    // rows without a running maximum yet: set it
+                    tmem_wait_ld(sb);
+                    if (mask) hide_columns(64, lim, sb);
+                    if (m_run == -INFINITY) {
+                        const float top = row_max128(sa, sb) * sl2;
+                        if (top > -INFINITY) m_run = ceilf(top);
+                    }
+                }
+                const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+                const float s0 = exp_pack64(sa, sl2, neg_m, pa);
+                tmem_wait_ld(sb);  // columns 64..127 are read: P may overwrite them
+                tmem_st32_nowait(tS + 64, pa);
+                if (mask && !first) hide_columns(64, lim, sb);
+                const float s1 = exp_pack64(sb, sl2, neg_m, pb);
+                tmem_st32_nowait(tS + 96, pb);
+                float sum = s0 + s1;
+                const bool big = !(sum <= 0x1p64f);  // also for inf and NaN
+                tmem_wait_st();
+                if (__any_sync(0xffffffffu, big)) {
+                    // rare: the scores grew by more than 2^64 over the running maximum.
+                    // Columns 0..63 of S are still in tensor memory, 64..127 in sb.
+                    tmem_ld64(tS, sa);
+                    if (mask) hide_columns(0, lim, sa);
+                    float f = 1.f;
+                    if (big) {
+                        const float m_new = ceilf(row_max128(sa, sb) * sl2), d = m_run - m_new;
+                        f = d >= -126.f ? __int_as_float((127 + static_cast<int>(d)) << 23) : 0.f;
+                        l_run *= f;
+                        m_run = m_new;
+                    }
+                    exp_pack128(sa, sb, sl2, m_run == -INFINITY ? 0.f : -m_run, pa, pb, &sum);
+                    tmem_st64(tS + 64, pa, pb);
+                    // O is quiet: this tile's product waits for p_full below
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO + c0, ov);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * f);
+                        tmem_st32(tO + c0, ov);
+                    }
+                }
+                l_run += sum;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + half);
+            }
+            if (!ok || !mbar_wait_warp(o_full + half, items & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+            tc_fence_after();
+            ++items;
+            uint32_t ov[D / 32][32];
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) tmem_ld32_nowait(tO + 32 * c, ov[c]);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) tmem_wait_ld32(ov[c]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_empty + half);
+            if (write) {
+                const long long at = static_cast<long long>(slot) * kTcTM + half * 128 + in_tile;
+                float *dst = a.slot_o + at * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        st_global_v8(dst + 32 * c + e, __uint_as_float(ov[c][e]), __uint_as_float(ov[c][e + 1]),
+                                     __uint_as_float(ov[c][e + 2]), __uint_as_float(ov[c][e + 3]),
+                                     __uint_as_float(ov[c][e + 4]), __uint_as_float(ov[c][e + 5]),
+                                     __uint_as_float(ov[c][e + 6]), __uint_as_float(ov[c][e + 7]));
+                a.slot_ml[at] = make_float2(m_run, l_run);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0 && *abort_flag) report(a.status, CP_ERR_DEVICE_TIMEOUT);
+}
+
+}  // namespace
+}  // namespace cpattn
