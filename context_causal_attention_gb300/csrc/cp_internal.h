@@ -135,8 +135,10 @@ cp_status ulysses_relayout_groups(const void *in, void *out, int64_t B, int64_t 
 // TMA descriptors.  make_map: 4-D bf16 map over [outer][rows][heads][D],
 // box 64 columns x 1 head x box_rows rows x 1, 128-byte swizzle.
 // make_map_f32_rows: 2-D fp32 map over [rows][cols], box box_cols x 1.
+// l2_bytes: how much a miss brings into L2 (256; 128 where the neighbouring
+// 128 bytes belong to another head and are not wanted).
 bool make_map(CUtensorMap *map, const void *base, int64_t D, int64_t heads, int64_t rows, int64_t outer,
-              int box_rows);
+              int box_rows, int l2_bytes = 256);
 bool make_map_f32_rows(CUtensorMap *map, const float *base, int64_t cols, int64_t rows, int box_cols);
 // 4-D fp32 map over [d3][d2][d1][d0] (d0 innermost), box b0 x b1 x b2 x 1,
 // 128-byte swizzle.

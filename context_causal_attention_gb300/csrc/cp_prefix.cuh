@@ -156,10 +156,16 @@ __device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, bool 
     }
 }
 
+// a / b for 0 <= a, 0 < b, by a 32-bit division where both fit.
+__device__ __forceinline__ long long div_floor(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // A block's share of the line; false if it has none.
 __device__ __forceinline__ bool share_of(const PrefixArgs &a, const Line &line, long long *t0, long long *t1) {
     const long long total = line.tile[kRuns];
-    const long long share = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+    const long long share = max(1ll, div_floor(total + gridDim.x - 1, gridDim.x));
     if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = share;
     *t0 = share * blockIdx.x;
     *t1 = min(*t0 + share, total);
@@ -218,8 +224,8 @@ __device__ __forceinline__ Piece find_piece(const PrefixArgs &a, const Line &lin
             return x;
         }
     }
-    const long long at = t - base, which = at / p.key_tiles;
-    x.kvh = static_cast<int>(which / p.row_tiles);
+    const long long at = t - base, which = div_floor(at, p.key_tiles);
+    x.kvh = static_cast<int>(div_floor(which, p.row_tiles));
     const int j = tile_at(static_cast<int>(which - static_cast<long long>(x.kvh) * p.row_tiles), p.row_tiles);
     x.item = item + static_cast<int>(which);
     x.row0 = j * TM;
@@ -230,8 +236,8 @@ __device__ __forceinline__ Piece find_piece(const PrefixArgs &a, const Line &lin
     const long long n0 = at - which * p.key_tiles;
     const long long n1 = min(n0 + (end - t), p.key_tiles);
     const long long need = (min(p.keys, row_limit(a, x, min(x.row0 + TM, x.rows) - 1)) + KT - 1) / KT;
-    x.k0 = n0 * need / p.key_tiles;
-    x.k1 = n1 * need / p.key_tiles;
+    x.k0 = need == p.key_tiles ? n0 : n0 * need / p.key_tiles;
+    x.k1 = need == p.key_tiles ? n1 : n1 * need / p.key_tiles;
     x.next = t + (n1 - n0);
     return x;
 }

@@ -21,14 +21,18 @@
 // no counter.  A second launch joins the pieces of every row in their order:
 // the result does not depend on timing.
 //
-// Inside a block: 4 warps share a double-buffered 64-key stage filled by
-// cp.async (page numbers checked, keys past the length zero-filled, so stale
-// values in the last page never meet an MMA); each warp owns 16 of the 64 keys,
-// so every byte of K and V passes from shared memory to registers once.  Both
-// products run on mma.sync m16n8k16: at 16 rows the tensor work is a tenth of
-// what the SM can do while it waits for memory.  Running maximum and sum stay in
-// fp32 registers; P is rounded to bf16 for the second product (2^-9 of each
-// weight at most, as in cp_attn_partial).
+// Inside a block of the 16-row kernel: one warp starts TMA copies of the pages
+// (a lane a copy) into a ring of 64-key stages, two groups of 4 warps take the
+// block's pieces in turn, so that one group's epilogue and next queries run
+// under the other's products and the ring never waits for them.  Each warp owns 16
+// of a stage's 64 keys: every byte of K and V passes from shared memory to
+// registers once.  Both products run on mma.sync m16n8k16: at 16 rows the tensor
+// work is a tenth of what the SM can do while it waits for memory.  Running
+// maximum and sum stay in fp32 registers; P is rounded to bf16 for the second
+// product (2^-9 of each weight at most, as in cp_attn_partial).  Keys past the
+// length are hidden by their index and their V rows zeroed, whatever the page
+// holds there.  Problems of more rows run in prefix_tc.cuh.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -51,19 +55,9 @@ __device__ int g_prefix_status = 0;
 // rows on the tensor memory, else in tiles of 16.
 constexpr int kTcRows = 16;
 
-constexpr int kThreads = 128;
 constexpr int kTM = 16;  // rows of a tile
 constexpr int kKT = 64;  // keys of a stage
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-    const int n = valid ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -83,229 +77,296 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+constexpr int kGroups = 2;                    // consumer groups of 4 warps
+constexpr int kMmaThreads = 32 + kGroups * 128;
+
 template <int D>
 struct MmaCfg {
-    static constexpr int kRowBytes = D * 2;
-    static constexpr int kTileBytes = kKT * kRowBytes;     // K or V of a stage
-    static constexpr int kStages = D == 128 ? 2 : 4;
-    static constexpr int kOffOut = kStages * 2 * kTileBytes;  // [4 warps][16 rows][D] fp32
-    static constexpr int kOffMl = kOffOut + 4 * 16 * D * 4;   // [4][16][2]
-    static constexpr int kOffLine = kOffMl + 4 * 16 * 2 * 4;
-    static constexpr int kSmem = kOffLine + static_cast<int>(sizeof(Line));
+    static constexpr int kAtoms = D / 64;
+    static constexpr int kAtom = kKT * 128;                // 64 rows x 64 columns, 128-byte swizzle
+    static constexpr int kTile = kAtom * kAtoms;           // K or V of a stage
+    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kOffOut = kStages * 2 * kTile;    // [groups][4 warps][16 rows][D] fp32
+    static constexpr int kOffMl = kOffOut + kGroups * 4 * 16 * D * 4;  // [groups][4][16] (m, l)
+    static constexpr int kOffLine = kOffMl + kGroups * 4 * 16 * 8;
+    static constexpr int kOffBar = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
+    static constexpr int kOffMisc = kOffBar + kStages * 16 + kGroups * 8;
+    static constexpr int kSmem = kOffMisc + 16 + 1024;     // + alignment slack
+    static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-// Byte offset of 16-byte chunk c of row r in a stage tile: chunks are permuted
-// by the row's low bits, so the 8 rows of an ldmatrix phase hit 8 bank groups.
+// Shared-memory address of 16-byte chunk c (of D/8) of row r in a stage tile.
 template <int D>
-__device__ __forceinline__ uint32_t tile_off(int r, int c) {
-    return r * (D * 2) + ((c ^ (r & 7)) << 4);
+__device__ __forceinline__ uint32_t tile_at_chunk(uint32_t base, int r, int c) {
+    return base + (c >> 3) * MmaCfg<D>::kAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory");
+}
+
+// group_sync that also tells every thread whether any of them has `v`.
+__device__ __forceinline__ bool group_any(int group, bool v) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\tbar.red.or.pred p, %1, 128, q;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(group + 1), "r"(static_cast<int>(v))
+        : "memory");
+    return r != 0;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) prefix_mma_kernel(const PrefixArgs a) {
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    prefix_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const PrefixArgs a) {
     using C = MmaCfg<D>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Line &line = *reinterpret_cast<Line *>(smem + C::kOffLine);
-    float *out_s = reinterpret_cast<float *>(smem + C::kOffOut);
-    float *ml_s = reinterpret_cast<float *>(smem + C::kOffMl);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t sbase = smem_u32(smem);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *empty = full + C::kStages, *go = empty + C::kStages;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+    if (tid == 0) {
+        *abort_flag = 0;
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 4);
+        }
+        for (int i = 0; i < kGroups; ++i) mbar_init(go + i, 4);
+        fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
     scan_line<kTM, kKT>(a, line, blockIdx.x == 0);
     long long t0, t1;
     if (!share_of(a, line, &t0, &t1)) return;
 
-    // loads run ahead of the products over the tiles of all the block's pieces
-    Piece lp = find_piece<kTM, kKT>(a, line, t0, t1);
-    long long lk = lp.k0;
-    int lstage = 0;
-    auto load_next = [&]() {
-        while (lk == lp.k1 && lp.next < t1) {
-            lp = find_piece<kTM, kKT>(a, line, lp.next, t1);
-            lk = lp.k0;
+    if (warp == 0) {
+        // -------------------------------------------------------- loads
+        // lane = (page of the tile, K or V, 64-column half): one copy each
+        const int shift = a.own.shift, rows = min(kKT, 1 << shift);
+        const int per_tile = kKT / rows, nowhere = a.own.n_pages << shift;
+        const int page = lane / (2 * C::kAtoms), is_v = (lane / C::kAtoms) & 1, at = lane % C::kAtoms;
+        uint32_t it = 0;
+        bool ok = true;
+        auto page_row = [&](const Piece &x, long long kt) -> int {
+            const long long key = kt * kKT + page * rows;
+            if (page >= per_tile || key >= x.keys) return -1;
+            const long long slot = (x.b < 0 ? a.pre : a.own).slot(x.b < 0 ? 0 : x.b, key);
+            if (slot < 0) report(a.status, CP_ERR_PAGE);
+            return slot < 0 ? nowhere : static_cast<int>(slot);
+        };
+        for (long long t = t0; t < t1 && ok;) {
+            const Piece x = find_piece<kTM, kKT>(a, line, t, t1);
+            t = x.next;
+            if (x.k0 >= x.k1) continue;
+            int row = page_row(x, x.k0);
+            for (long long kt = x.k0; kt < x.k1; ++kt, ++it) {
+                const int next = kt + 1 < x.k1 ? page_row(x, kt + 1) : -1;
+                const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
+                if (!mbar_wait_warp(empty + st, ph ^ 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                if (lane == 0) mbar_arrive_expect_tx(full + st, n * rows * 128);
+                __syncwarp();
+                if (row >= 0)
+                    tma_load_4d(smem + (st * 2 + is_v) * C::kTile + at * C::kAtom + page * rows * 128, is_v ? &tmV : &tmK,
+                                full + st, 64 * at, x.kvh, row, 0);
+                row = next;
+            }
         }
-        if (lk < lp.k1) {
-            const PageTable &pt = lp.b < 0 ? a.pre : a.own;
-            // keys that any row of the tile sees
-            const long long limit = min(lp.keys, row_limit(a, lp, min(lp.row0 + kTM, lp.rows) - 1));
-            const uint32_t ks = sbase + lstage * 2 * C::kTileBytes, vs = ks + C::kTileBytes;
-            constexpr int kChunks = D / 8, kStep = kThreads / kChunks;  // rows between a thread's chunks
-            const int c = tid % kChunks;
+        // let every copy already issued land before shared memory goes away
+        if (!ok && lane == 0) {
+            volatile int no_abort = 0;
+            for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
+                mbar_wait(full + i % C::kStages, (i / C::kStages) & 1u, &no_abort, 100000000ull);
+        }
+        __syncwarp();
+    } else {
+        // -------------------------------------------------------- products
+        const int group = (warp - 1) >> 2, w = (warp - 1) & 3, gtid = tid - 32 - group * 128;
+        const int g = lane >> 2, t4 = lane & 3;  // accumulator row (and row + 8), column pair
+        float *out_s = reinterpret_cast<float *>(smem + C::kOffOut) + group * 4 * 16 * D;
+        float2 *ml_s = reinterpret_cast<float2 *>(smem + C::kOffMl) + group * 4 * 16;
+        const uint32_t sbase = smem_u32(smem);
+        uint32_t it = 0, gone = 0;
+        int turn = 0;
+        bool ok = true;
+        for (long long t = t0; t < t1 && ok; turn ^= 1) {
+            const bool first = t == t0;
+            const Piece x = find_piece<kTM, kKT>(a, line, t, t1);
+            t = x.next;
+            if (turn != group) {
+                // the other group's piece
+                it += static_cast<uint32_t>(x.k1 - x.k0);
+                continue;
+            }
+            // this warp's copy of the rows as A operands
+            uint32_t qf[D / 16][4];
 #pragma unroll
-            for (int r = tid / kChunks; r < kKT; r += kStep) {
-                const long long key = lk * kKT + r;
-                long long slot = -1;
-                if (key < limit) {
-                    slot = pt.slot(lp.b < 0 ? 0 : lp.b, key);
-                    if (slot < 0 && c == 0) report(a.status, CP_ERR_PAGE);
+            for (int h = 0; h < 2; ++h) {
+                const int row = x.row0 + g + 8 * h;
+                const bool in = row < x.rows;
+                const int tok = row / a.G;
+                const __nv_bfloat16 *qp = a.q + (static_cast<long long>(x.tok0 + (in ? tok : 0)) * a.N + x.kvh * a.G +
+                                                 (in ? row - tok * a.G : 0)) * D;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    qf[kk][h] = in ? __ldg(reinterpret_cast<const uint32_t *>(qp + kk * 16 + 2 * t4)) : 0u;
+                    qf[kk][2 + h] = in ? __ldg(reinterpret_cast<const uint32_t *>(qp + kk * 16 + 8 + 2 * t4)) : 0u;
                 }
-                const long long off = slot < 0 ? 0 : (slot * a.Nkv + lp.kvh) * D + c * 8;
-                cp_async16(ks + tile_off<D>(r, c), a.k + off, slot >= 0);
-                cp_async16(vs + tile_off<D>(r, c), a.v + off, slot >= 0);
             }
-            lstage = lstage + 1 == C::kStages ? 0 : lstage + 1;
-            ++lk;
-        }
-        cp_async_commit();
-    };
+            const long long lim0 = x.row0 + g < x.rows ? min(x.keys, row_limit(a, x, x.row0 + g)) : 0;
+            const long long lim1 = x.row0 + g + 8 < x.rows ? min(x.keys, row_limit(a, x, x.row0 + g + 8)) : 0;
+            // tiles from the first that some row does not see whole on are masked
+            const long long whole = x.row0 + kTM <= x.rows ? min(x.keys, row_limit(a, x, x.row0)) : 0;
+            float o[D / 8][4];
 #pragma unroll
-    for (int s = 0; s < C::kStages - 1; ++s) load_next();
-
-    const int g = lane >> 2, t4 = lane & 3;  // accumulator row (and row + 8), column pair
-    int stage = 0;
-    for (long long t = t0; t < t1;) {
-        const Piece x = find_piece<kTM, kKT>(a, line, t, t1);
-        t = x.next;
-        // this warp's copy of the rows as A operands
-        uint32_t qf[D / 16][4];
+            for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = x.row0 + g + 8 * h;
-            const bool ok = row < x.rows;
-            const int tok = row / a.G;
-            const __nv_bfloat16 *qp =
-                a.q + (static_cast<long long>(x.tok0 + (ok ? tok : 0)) * a.N + x.kvh * a.G + (ok ? row - tok * a.G : 0)) * D;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                qf[kk][h] = ok ? __ldg(reinterpret_cast<const uint32_t *>(qp + kk * 16 + 2 * t4)) : 0u;
-                qf[kk][2 + h] = ok ? __ldg(reinterpret_cast<const uint32_t *>(qp + kk * 16 + 8 + 2 * t4)) : 0u;
-            }
-        }
-        const long long lim0 = x.row0 + g < x.rows ? min(x.keys, row_limit(a, x, x.row0 + g)) : 0;
-        const long long lim1 = x.row0 + g + 8 < x.rows ? min(x.keys, row_limit(a, x, x.row0 + g + 8)) : 0;
-        // tiles from the first that some row does not see whole on are masked
-        const long long whole = x.row0 + kTM <= x.rows ? min(x.keys, row_limit(a, x, x.row0)) : 0;
-        float o[D / 8][4];
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        for (long long kt = x.k0; kt < x.k1; ++kt) {
-            load_next();
-            cp_async_wait<C::kStages - 1>();
-            __syncthreads();
-            const uint32_t ks = sbase + stage * 2 * C::kTileBytes, vs = ks + C::kTileBytes;
-            const int key0 = warp * 16;
-            float s[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t b[4];
-                // lanes 0-7: keys 0-7, low 8 columns; 8-15: high; 16-31: keys 8-15
-                ldsm4(ks + tile_off<D>(key0 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)), b);
-                mma16816(s[0], qf[kk], b[0], b[1]);
-                mma16816(s[1], qf[kk], b[2], b[3]);
-            }
-            const long long kb = kt * kKT + key0 + 2 * t4;
-            const bool masked = kt * kKT + kKT > whole;
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[n][e] *= a.scale_log2;
-                    if (masked && kb + 8 * n + (e & 1) >= ((e & 2) ? lim1 : lim0)) s[n][e] = -INFINITY;
+                for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            // the other group has used up the stages before these: a wait for a stage
+            // is then never more than one of its phases ahead
+            if (!first && !mbar_wait_warp(go + group, gone++ & 1u, abort_flag, a.timeout_ns)) ok = false;
+            for (long long kt = x.k0; kt < x.k1 && ok; ++kt, ++it) {
+                const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
+                if (!mbar_wait_warp(full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
+                const uint32_t ks = sbase + st * 2 * C::kTile, vs = ks + C::kTile;
+                const int key0 = w * 16;
+                const long long past = x.keys - kt * kKT - key0;  // keys of this warp's 16 that exist
+                if (past < 16) {
+                    // what lies behind the last key must not meet a product
+                    for (int i = lane; i < 16 * (D / 8); i += 32) {
+                        const int r = i / (D / 8);
+                        if (r >= past) {
+                            const uint32_t dst = tile_at_chunk<D>(vs, key0 + r, i % (D / 8));
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+                        }
+                    }
+                    __syncwarp();
                 }
-            // the maximum is an integer, set by the first keys that a row sees and
-            // moved only when a weight would pass 2^30: rescaling is exact and rare
-            const float top0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-            const float top1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-            if (__any_sync(0xffffffffu, top0 > m[0] + 30.f || top1 > m[1] + 30.f)) {
-                float top[2] = {top0, top1};
+                float s[2][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-                    if (top[h] > m[h] + 30.f) {
-                        const float mn = ceilf(top[h]), f = fast_exp2(m[h] - mn);  // 0 from -inf
-                        m[h] = mn;
-                        l[h] *= f;
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int n = 0; n < D / 8; ++n) {
-                            o[n][2 * h] *= f;
-                            o[n][2 * h + 1] *= f;
+                    for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t b[4];
+                    // lanes 0-7: keys 0-7, low 8 columns; 8-15: high; 16-31: keys 8-15
+                    ldsm4(tile_at_chunk<D>(ks, key0 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)), b);
+                    mma16816(s[0], qf[kk], b[0], b[1]);
+                    mma16816(s[1], qf[kk], b[2], b[3]);
+                }
+                const long long kb = kt * kKT + key0 + 2 * t4;
+                const bool masked = kt * kKT + kKT > whole;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[n][e] *= a.scale_log2;
+                        if (masked && kb + 8 * n + (e & 1) >= ((e & 2) ? lim1 : lim0)) s[n][e] = -INFINITY;
+                    }
+                // the maximum is an integer, set by the first keys that a row sees and
+                // moved only when a weight would pass 2^30: rescaling is exact and rare
+                const float top0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+                const float top1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+                if (__any_sync(0xffffffffu, top0 > m[0] + 30.f || top1 > m[1] + 30.f)) {
+                    float top[2] = {top0, top1};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+                        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+                        if (top[h] > m[h] + 30.f) {
+                            const float mn = ceilf(top[h]), f = fast_exp2(m[h] - mn);  // 0 from -inf
+                            m[h] = mn;
+                            l[h] *= f;
+#pragma unroll
+                            for (int n = 0; n < D / 8; ++n) {
+                                o[n][2 * h] *= f;
+                                o[n][2 * h + 1] *= f;
+                            }
                         }
                     }
                 }
-            }
-            const float n0 = m[0] == -INFINITY ? 0.f : m[0], n1 = m[1] == -INFINITY ? 0.f : m[1];
-            uint32_t pf[4];
+                const float n0 = m[0] == -INFINITY ? 0.f : m[0], n1 = m[1] == -INFINITY ? 0.f : m[1];
+                uint32_t pf[4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float p0 = fast_exp2(s[n][0] - n0), p1 = fast_exp2(s[n][1] - n0);
-                const float p2 = fast_exp2(s[n][2] - n1), p3 = fast_exp2(s[n][3] - n1);
-                l[0] += p0 + p1;
-                l[1] += p2 + p3;
-                pf[2 * n] = pack_bf16x2(p0, p1);
-                pf[2 * n + 1] = pack_bf16x2(p2, p3);
-            }
-#pragma unroll
-            for (int n = 0; n < D / 16; ++n) {
-                uint32_t b[4];
-                // lanes 0-7: keys 0-7, 8-15: keys 8-15 of the low 8 columns; 16-31: of the high
-                ldsm4t(vs + tile_off<D>(key0 + (lane & 15), 2 * n + (lane >> 4)), b);
-                mma16816(o[2 * n], pf, b[0], b[1]);
-                mma16816(o[2 * n + 1], pf, b[2], b[3]);
-            }
-            __syncthreads();  // the stage may be filled again
-            stage = stage + 1 == C::kStages ? 0 : stage + 1;
-        }
-        // join the four warps' keys and leave the piece's partial
-        const int slot = x.item + static_cast<int>(blockIdx.x);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (t4 == 0) {
-                ml_s[(warp * 16 + g + 8 * h) * 2] = m[h];
-                ml_s[(warp * 16 + g + 8 * h) * 2 + 1] = l[h];
-            }
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-                *reinterpret_cast<float2 *>(out_s + (warp * 16 + g + 8 * h) * D + ((8 * n + 2 * t4) ^ ((g & 3) << 3))) =
-                    make_float2(o[n][2 * h], o[n][2 * h + 1]);
-        }
-        __syncthreads();
-        if (slot < a.slots) {
-            constexpr int kPer = 16 * D / kThreads;  // values of a thread: part of one row
-            const int row = tid / (kThreads / 16), c0 = (tid % (kThreads / 16)) * kPer;
-            float mw[4], f[4], mx = -INFINITY, ls = 0.f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                mw[w] = ml_s[(w * 16 + row) * 2];
-                mx = fmaxf(mx, mw[w]);
-            }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                f[w] = mw[w] == -INFINITY ? 0.f : fast_exp2(mw[w] - mx);
-                ls += f[w] * ml_s[(w * 16 + row) * 2 + 1];
-            }
-            float *dst = a.slot_o + (static_cast<long long>(slot) * 16 + row) * D;
-#pragma unroll
-            for (int c = c0; c < c0 + kPer; c += 4) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const float4 y = *reinterpret_cast<const float4 *>(out_s + (w * 16 + row) * D + (c ^ ((row & 3) << 3)));
-                    if (f[w] != 0.f) {  // a warp that saw nothing holds zeros
-                        v.x += f[w] * y.x;
-                        v.y += f[w] * y.y;
-                        v.z += f[w] * y.z;
-                        v.w += f[w] * y.w;
-                    }
+                for (int n = 0; n < 2; ++n) {
+                    const float p0 = fast_exp2(s[n][0] - n0), p1 = fast_exp2(s[n][1] - n0);
+                    const float p2 = fast_exp2(s[n][2] - n1), p3 = fast_exp2(s[n][3] - n1);
+                    l[0] += p0 + p1;
+                    l[1] += p2 + p3;
+                    pf[2 * n] = pack_bf16x2(p0, p1);
+                    pf[2 * n + 1] = pack_bf16x2(p2, p3);
                 }
-                *reinterpret_cast<float4 *>(dst + c) = v;
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n) {
+                    uint32_t b[4];
+                    // lanes 0-7: keys 0-7, 8-15: keys 8-15 of the low 8 columns; 16-31: of the high
+                    ldsm4t(tile_at_chunk<D>(vs, key0 + (lane & 15), 2 * n + (lane >> 4)), b);
+                    mma16816(o[2 * n], pf, b[0], b[1]);
+                    mma16816(o[2 * n + 1], pf, b[2], b[3]);
+                }
+                if (past < 16) fence_async_shared();  // the zeros before the next copy into the stage
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + st);
             }
-            if (c0 == 0) a.slot_ml[static_cast<long long>(slot) * 16 + row] = make_float2(mx, ls);
-        } else if (tid == 0) {
-            report(a.status, CP_ERR_PAGE);
+            if (lane == 0) mbar_arrive(go + (group ^ 1));
+            // join the four warps' keys and leave the piece's partial (a warp that gave
+            // up a wait takes part, so that the group stays together, and all leave below)
+            const int slot = x.item + static_cast<int>(blockIdx.x);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+                if (t4 == 0) ml_s[w * 16 + g + 8 * h] = make_float2(m[h], l[h]);
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    *reinterpret_cast<float2 *>(out_s + (w * 16 + g + 8 * h) * D + ((8 * n + 2 * t4) ^ ((g & 3) << 3))) =
+                        make_float2(o[n][2 * h], o[n][2 * h + 1]);
+            }
+            group_sync(group);
+            const int row = gtid >> 3, c0 = (gtid & 7) * 4;  // 8 threads a row, 4 values at a time
+            if (x.row0 + row < x.rows && slot < a.slots) {
+                float2 ml[4];
+                float f[4], mx = -INFINITY, ls = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ml[i] = ml_s[i * 16 + row];
+                    mx = fmaxf(mx, ml[i].x);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[i] = ml[i].x == -INFINITY ? 0.f : fast_exp2(ml[i].x - mx);
+                    ls += f[i] * ml[i].y;
+                }
+                const long long at = static_cast<long long>(slot) * kTM + row;
+#pragma unroll
+                for (int c = c0; c < D; c += 32) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 y = *reinterpret_cast<const float4 *>(out_s + (i * 16 + row) * D + (c ^ ((row & 3) << 3)));
+                        if (f[i] != 0.f) {  // a warp that saw nothing holds zeros
+                            v.x += f[i] * y.x;
+                            v.y += f[i] * y.y;
+                            v.z += f[i] * y.z;
+                            v.w += f[i] * y.w;
+                        }
+                    }
+                    *reinterpret_cast<float4 *>(a.slot_o + at * D + c) = v;
+                }
+                if (c0 == 0) a.slot_ml[at] = make_float2(mx, ls);
+            }
+            if (slot >= a.slots && gtid == 0) report(a.status, CP_ERR_PAGE);
+            if (group_any(group, !ok)) ok = false;
         }
-        __syncthreads();
     }
-    cp_async_wait<0>();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) report(a.status, CP_ERR_DEVICE_TIMEOUT);
 }
 
 // What a launch left, as the join reads it.
@@ -326,48 +387,102 @@ struct JoinArgs {
     float *lse;
 };
 
-// One warp joins the pieces of one output row (token, head).
+// Where the pieces of a row of head h lie: the slots first .. first + n - 1, row r of each.
+struct RowPieces {
+    int first, n, r;
+};
+
+// A part of one token's rows, for all its heads.
+struct TokenPart {
+    const float2 *slot_ml;
+    const float *slot_o;
+    long long base_tile, key_tiles, share;
+    int base_item, row_tiles, row0, tm, slots;
+    // which: 0 the prefix, 1 the sequence b that begins at row `begin` with `count` new tokens
+    __device__ __forceinline__ TokenPart(const JoinArgs &a, int which, int b, int tok, int begin, int count) {
+        const JoinPart &p = a.part[which];
+        const int n = which ? count : min(max(__ldg(a.cu + a.B), 0), a.R);
+        const long long keys = which ? min(max(static_cast<long long>(__ldg(a.kv_len + b)), 0ll), a.most) : a.P;
+        slot_ml = p.slot_ml;
+        slot_o = p.slot_o;
+        slots = p.slots;
+        tm = p.tm;
+        key_tiles = div_floor(keys + p.kt - 1, p.kt);
+        row_tiles = (n * a.G + tm - 1) / tm;
+        row0 = (tok - (which ? begin : 0)) * a.G;
+        base_tile = which ? p.base_tile[b] : 0;
+        base_item = which ? p.base_item[b] : 0;
+        share = p.head[0];
+        if (row0 >= n * a.G) key_tiles = 0;
+    }
+    __device__ __forceinline__ RowPieces row(int kvh, int gh) const {
+        if (key_tiles == 0) return RowPieces{0, 0, 0};
+        const int i = row0 + gh;
+        const long long at = static_cast<long long>(kvh) * row_tiles + place_of(i / tm, row_tiles);
+        const long long first = base_tile + at * key_tiles;
+        const int c0 = static_cast<int>(div_floor(first, share));
+        const int c1 = static_cast<int>(div_floor(first + key_tiles - 1, share));
+        const int slot = base_item + static_cast<int>(at) + c0;
+        return RowPieces{slot, min(c1 - c0 + 1, slots - slot), i % tm};
+    }
+};
+
+template <int kV>
+__device__ __forceinline__ void store_row(const JoinArgs &a, long long row, int lane, const float (&v)[kV], float f) {
+    const long long at = row * (32 * kV) + lane * kV;
+    if (a.o_bf16) {
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.o) + at);
+#pragma unroll
+        for (int e = 0; e < kV; e += 2) dst[e / 2] = pack_bf16x2(v[e] * f, v[e + 1] * f);
+    } else {
+        float *dst = static_cast<float *>(a.o) + at;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) dst[e] = v[e] * f;
+    }
+}
+template <int kV>
+__device__ __forceinline__ void add_row(float (&acc)[kV], const float *src, float f) {
+    if (kV == 4) {
+        const float4 y = *reinterpret_cast<const float4 *>(src);
+        acc[0] += f * y.x, acc[1] += f * y.y, acc[2 % kV] += f * y.z, acc[3 % kV] += f * y.w;
+    } else {
+        const float2 y = *reinterpret_cast<const float2 *>(src);
+        acc[0] += f * y.x, acc[1] += f * y.y;
+    }
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+// Few rows of many pieces: a warp joins the pieces of one row, a lane a piece's
+// (m, l), then the pieces' rows one after another.
 template <int D>
-__global__ void __launch_bounds__(128) prefix_join_kernel(const JoinArgs a) {
+__global__ void __launch_bounds__(128) join_row_kernel(const JoinArgs a) {
     constexpr int kV = D / 32;
     const int lane = threadIdx.x & 31;
     const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (row >= static_cast<long long>(a.R) * a.N) return;
     const int tok = static_cast<int>(row / a.N), h = static_cast<int>(row - static_cast<long long>(tok) * a.N);
-    const int kvh = h / a.G, gh = h - kvh * a.G;
     int begin, count;
     const int b = find_sequence(a.cu, a.B, tok, lane, &begin, &count);
     if (b < 0) return;
     float mx = -INFINITY, ls = 0.f, acc[kV];
 #pragma unroll
     for (int e = 0; e < kV; ++e) acc[e] = 0.f;
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        const JoinPart &p = a.part[which];
-        // the row's item: its stretch of the line, its pieces' slots and its row in them
-        const int n = which ? count : min(max(__ldg(a.cu + a.B), 0), a.R);
-        const long long keys = which ? min(max(static_cast<long long>(__ldg(a.kv_len + b)), 0ll), a.most) : a.P;
-        const long long key_tiles = (keys + p.kt - 1) / p.kt;
-        if (key_tiles == 0) continue;
-        const int row_tiles = (n * a.G + p.tm - 1) / p.tm, i = (tok - (which ? begin : 0)) * a.G + gh, r = i % p.tm;
-        if (i >= n * a.G) continue;
-        const long long at = static_cast<long long>(kvh) * row_tiles + place_of(i / p.tm, row_tiles);
-        const int item = (which ? __ldg(p.base_item + b) : 0) + static_cast<int>(at);
-        const long long first = (which ? __ldg(p.base_tile + b) : 0) + at * key_tiles;
-        const long long share = __ldg(p.head);
-        const int c0 = static_cast<int>(first / share), c1 = static_cast<int>((first + key_tiles - 1) / share);
-        for (int cb = c0; cb <= c1; cb += 32) {
-            // up to 32 pieces: their (m, l) side by side, then their rows one after another
-            const int slot = item + cb + lane;
-            float pm = -INFINITY, pl = 0.f;
-            if (cb + lane <= c1 && slot < p.slots) {
-                const float2 ml = __ldg(p.slot_ml + static_cast<long long>(slot) * p.tm + r);
-                pm = ml.x;
-                pl = ml.y;
-            }
-            float top = pm;
+    const int kvh = h / a.G;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int which = 0; which < 2; ++which) {
+        const TokenPart p(a, which, b, tok, begin, count);
+        const RowPieces x = p.row(kvh, h - kvh * a.G);
+        for (int cb = 0; cb < x.n; cb += 32) {
+            const float2 ml = cb + lane < x.n ? p.slot_ml[static_cast<long long>(x.first + cb + lane) * p.tm + x.r]
+                                              : make_float2(-INFINITY, 0.f);
+            const float top = warp_max(ml.x);
             if (top == -INFINITY) continue;
             if (top > mx) {
                 const float f = mx == -INFINITY ? 0.f : fast_exp2(mx - top);
@@ -376,46 +491,95 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const JoinArgs a) {
                 for (int e = 0; e < kV; ++e) acc[e] *= f;
                 mx = top;
             }
-            const float w = pm == -INFINITY ? 0.f : fast_exp2(pm - mx);
-            float add = w * pl;
+            const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mx);
+            float add = w * ml.y;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
             ls += add;
-            const int m = min(32, c1 - cb + 1);
-#pragma unroll 4
-            for (int k = 0; k < m; ++k) {
+            const int n = min(32, x.n - cb);
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
                 const float f = __shfl_sync(0xffffffffu, w, k);
-                const float *src = p.slot_o + (static_cast<long long>(item + cb + k) * p.tm + r) * D + lane * kV;
-                if (f != 0.f) {
-                    if (kV == 4) {
-                        const float4 y = __ldg(reinterpret_cast<const float4 *>(src));
-                        acc[0] += f * y.x, acc[1] += f * y.y, acc[2 % kV] += f * y.z, acc[3 % kV] += f * y.w;
-                    } else {
-                        const float2 y = __ldg(reinterpret_cast<const float2 *>(src));
-                        acc[0] += f * y.x, acc[1] += f * y.y;
-                    }
-                }
+                if (f != 0.f)
+                    add_row<kV>(acc, p.slot_o + (static_cast<long long>(x.first + cb + k) * p.tm + x.r) * D + lane * kV, f);
             }
         }
     }
-    const float inv = mx == -INFINITY ? 0.f : 1.f / ls;
-    const long long at = row * D + lane * kV;
-    if (a.o_bf16) {
-        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.o) + at);
-#pragma unroll
-        for (int e = 0; e < kV; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    } else {
-        float *dst = static_cast<float *>(a.o) + at;
-#pragma unroll
-        for (int e = 0; e < kV; ++e) dst[e] = acc[e] * inv;
+    store_row<kV>(a, row, lane, acc, mx == -INFINITY ? 0.f : 1.f / ls);
+    if (lane == 0) a.lse[static_cast<long long>(h) * a.R + tok] = lse_of(mx, ls);
+}
+
+// Many rows of few pieces: a warp joins up to 32 heads of one token, a lane a
+// head's (m, l), then four heads' rows at a time with their loads in flight together.
+template <int D>
+__global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
+    constexpr int kV = D / 32;
+    const int lane = threadIdx.x & 31, blocks = (a.N + 31) / 32;
+    const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const int tok = static_cast<int>(unit / blocks), h0 = static_cast<int>(unit - static_cast<long long>(tok) * blocks) * 32;
+    if (tok >= a.R) return;
+    int begin, count;
+    const int b = find_sequence(a.cu, a.B, tok, lane, &begin, &count);
+    if (b < 0) return;
+    const int h = h0 + lane, kvh = h / a.G, heads = min(32, a.N - h0);
+    const TokenPart p0(a, 0, b, tok, begin, count), p1(a, 1, b, tok, begin, count);
+    const RowPieces x0 = h < a.N ? p0.row(kvh, h - kvh * a.G) : RowPieces{0, 0, 0};
+    const RowPieces x1 = h < a.N ? p1.row(kvh, h - kvh * a.G) : RowPieces{0, 0, 0};
+    const float2 *s0 = p0.slot_ml + static_cast<long long>(x0.first) * p0.tm + x0.r;
+    const float2 *s1 = p1.slot_ml + static_cast<long long>(x1.first) * p1.tm + x1.r;
+    float mx = -INFINITY, ls = 0.f;
+    for (int i = 0; i < x0.n; ++i) mx = fmaxf(mx, s0[static_cast<long long>(i) * p0.tm].x);
+    for (int i = 0; i < x1.n; ++i) mx = fmaxf(mx, s1[static_cast<long long>(i) * p1.tm].x);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    for (int i = 0; i < x0.n; ++i) {
+        const float2 ml = s0[static_cast<long long>(i) * p0.tm];
+        ls += fast_exp2(ml.x - ref) * ml.y;
     }
-    if (lane == 0)
-        a.lse[static_cast<long long>(h) * a.R + tok] =
-            mx == -INFINITY ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994530942f;
+    for (int i = 0; i < x1.n; ++i) {
+        const float2 ml = s1[static_cast<long long>(i) * p1.tm];
+        ls += fast_exp2(ml.x - ref) * ml.y;
+    }
+    const float inv = mx == -INFINITY ? 0.f : 1.f / ls;
+    if (h < a.N) a.lse[static_cast<long long>(h) * a.R + tok] = lse_of(mx, ls);
+    for (int k0 = 0; k0 < heads; k0 += 4) {
+        float acc[4][kV];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < kV; ++e) acc[k][e] = 0.f;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const TokenPart &p = which ? p1 : p0;
+            const RowPieces &x = which ? x1 : x0;
+            const float2 *s = which ? s1 : s0;
+            int n[4], most = 0;
+            const float *src[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                n[k] = __shfl_sync(0xffffffffu, x.n, (k0 + k) & 31);
+                if (k0 + k >= heads) n[k] = 0;
+                most = max(most, n[k]);
+                src[k] = p.slot_o + (static_cast<long long>(__shfl_sync(0xffffffffu, x.first, (k0 + k) & 31)) * p.tm +
+                                     __shfl_sync(0xffffffffu, x.r, (k0 + k) & 31)) * D + lane * kV;
+            }
+            for (int i = 0; i < most; ++i) {
+                const float w = i < x.n ? fast_exp2(s[static_cast<long long>(i) * p.tm].x - ref) * inv : 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float f = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+                    if (i < n[k] && f != 0.f) add_row<kV>(acc[k], src[k] + static_cast<long long>(i) * p.tm * D, f);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k0 + k < heads) store_row<kV>(a, static_cast<long long>(tok) * a.N + h0 + k0 + k, lane, acc[k], 1.f);
+    }
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kMaxBlocks = 320;  // of a launch (a slot more for each)
+constexpr int kMaxBlocks = 320;          // of a launch (a slot more for each)
+constexpr long long kJoinRows = 16384;  // up to this many rows a warp joins one, beyond it a token's heads
 
 // How a call is cut: which launches it makes and where they leave their pieces.
 struct Shape {
@@ -452,38 +616,32 @@ Shape shape_of(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int6
 }
 
 template <int D>
-cp_status launch_mma(const PrefixArgs &a, cudaStream_t stream) {
+cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [] {
         err = cudaFuncSetAttribute(prefix_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, MmaCfg<D>::kSmem);
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<D>::kSmem);
     });
     if (err != cudaSuccess) return cuda_status(err);
-    const int grid = 2 * sm_count() < kMaxBlocks ? 2 * sm_count() : kMaxBlocks;
-    prefix_mma_kernel<D><<<grid, kThreads, MmaCfg<D>::kSmem, stream>>>(a);
-    return last_launch_status();
-}
-
-template <int D>
-cp_status launch_tc(const PrefixArgs &a, int64_t slots, int box_rows, cudaStream_t stream) {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<D>::kSmem);
-    });
-    if (err != cudaSuccess) return cuda_status(err);
+    const int64_t rows = static_cast<int64_t>(a.own.n_pages) << a.own.shift;
+    const int page = 1 << a.own.shift, tile = tc ? kTcKT : kKT, box = page < tile ? page : tile;
+    // at D = 64 a head's row is 128 bytes and its neighbour another head's
+    const int l2 = D == 64 ? 128 : 256;
     CUtensorMap mk, mv;
-    if (!make_map(&mk, a.k, D, a.Nkv, slots, 1, box_rows) || !make_map(&mv, a.v, D, a.Nkv, slots, 1, box_rows))
+    if (!make_map(&mk, a.k, D, a.Nkv, rows, 1, box, l2) || !make_map(&mv, a.v, D, a.Nkv, rows, 1, box, l2))
         return CP_ERR_CUDA;
     const int grid = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
-    prefix_tc_kernel<D><<<grid, kTcThreads, TcCfg<D>::kSmem, stream>>>(mk, mv, a);
+    if (tc)
+        prefix_tc_kernel<D><<<grid, kTcThreads, TcCfg<D>::kSmem, stream>>>(mk, mv, a);
+    else
+        prefix_mma_kernel<D><<<grid, kMmaThreads, MmaCfg<D>::kSmem, stream>>>(mk, mv, a);
     return last_launch_status();
 }
 
 template <int D>
 cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cudaStream_t stream) {
-    const int64_t slots = static_cast<int64_t>(a.own.n_pages) << a.own.shift;
-    const int box_rows = a.own.shift < 7 ? 1 << a.own.shift : 128;
     // the wide launch first: it has the prefix, the longer work
     for (int k = 1; k >= 0; --k) {
         if (!s.slots[k]) continue;
@@ -495,7 +653,7 @@ cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cuda
         a.slot_ml = reinterpret_cast<float2 *>(w + s.slot_ml[k]);
         a.slot_o = reinterpret_cast<float *>(w + s.slot_o[k]);
         a.slots = static_cast<int>(s.slots[k]);
-        const cp_status st = k ? launch_tc<D>(a, slots, box_rows, stream) : launch_mma<D>(a, stream);
+        const cp_status st = launch_main<D>(a, k == 1, stream);
         if (st != CP_OK) return st;
         for (int which = 0; which < 2; ++which)
             if (which ? a.with_own : a.with_prefix)
@@ -504,7 +662,12 @@ cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cuda
     }
     if (a.P == 0) j.part[0] = j.part[1];  // not read into a result: no keys
     const long long rows = static_cast<long long>(a.R) * a.N;
-    prefix_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(j);
+    if (rows <= kJoinRows) {
+        join_row_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(j);
+    } else {
+        const long long units = static_cast<long long>(a.R) * ((a.N + 31) / 32);
+        join_token_kernel<D><<<static_cast<unsigned>((units + 3) / 4), 128, 0, stream>>>(j);
+    }
     return last_launch_status();
 }
 

@@ -418,31 +418,42 @@ def cp_rope_phases(inv_freq, amplitude=1.0, order=CP_ROPE_HALF, device="cuda"):
 
 
 def _here(*ts):
-    """Every given tensor lies on the current CUDA device."""
+    """Every given tensor lies on the current CUDA device, which is returned."""
     dev = torch.cuda.current_device()
     for t in ts:
-        if t is not None and not (t.is_cuda and t.device.index == dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensor must be on the current CUDA device")
+    return dev
+
+
+def _raw_stream(stream, dev):
+    """Handle of `stream`, or of the device's current stream (without making a Stream object: these
+    calls are short)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _head_rows(t):
     """(elements between tokens, tokens' leading shape, heads, D) of [..., heads, D] whose
     head rows are dense and whose tokens lie at one distance from one another."""
-    if t.dim() < 3:
+    shape = t.shape
+    n = len(shape)
+    if n < 3:
         raise ValueError("expected [..., heads, D] with at least one leading dimension")
-    shape, st = t.shape, t.stride()
     H, D = shape[-2], shape[-1]
+    if t.is_contiguous():
+        return H * D, shape[:-2], H, D
+    st = t.stride()
     if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
         raise ValueError("the head rows of a token must be dense")
-    step, n = 0, 1
-    for i in range(t.dim() - 3, -1, -1):
+    step, count = 0, 1
+    for i in range(n - 3, -1, -1):
         if shape[i] > 1:
             if step == 0:
                 step = st[i]
-            elif st[i] != step * n:
+            elif st[i] != step * count:
                 raise ValueError("tokens must lie at one distance from one another")
-            n *= shape[i]
-    return (step if n > 1 else max(H * D, 8)), shape[:-2], H, D
+            count *= shape[i]
+    return (step if count > 1 else H * D), shape[:-2], H, D
 
 
 def _tokens(lead):
@@ -493,9 +504,9 @@ def _rope_call(name, q, k, pos, rope, q_out, k_out, stream):
     C, B, s, N, Nkv, D, qs, ks = _qk(q, k)
     _check_pos(pos, C, s)
     q_out, k_out = _row_out(q_out, q), _row_out(k_out, k)
-    _here(q, k, pos, rope.freqs, q_out, k_out)
+    dev = _here(q, k, pos, rope.freqs, q_out, k_out)
     st = getattr(_lib.lib(), name)(_addr(q), _addr(k), _addr(pos), C, B, s, N, Nkv, D, qs, ks, _dtype_code(q),
-                                   rope._ref, _addr(q_out), _addr(k_out), _stream(stream))
+                                   rope._ref, _addr(q_out), _addr(k_out), _raw_stream(stream, dev))
     _lib.check(name, st)
     return q_out, k_out
 
@@ -530,10 +541,10 @@ def cp_qk_norm_rope_fwd(q, k, wq, wk, pos, rope, eps=1e-6, q_out=None, k_out=Non
         _check_pos(pos, C, s)
     wd = _check_weights(wq, wk, D)
     q_out, k_out = _row_out(q_out, q), _row_out(k_out, k)
-    _here(q, k, wq, wk, pos, None if rope is None else rope.freqs, q_out, k_out)
+    dev = _here(q, k, wq, wk, pos, None if rope is None else rope.freqs, q_out, k_out)
     st = _lib.lib().cp_qk_norm_rope_fwd(_addr(q), _addr(k), _addr(wq), _addr(wk), _addr(pos), C, B, s, N, Nkv, D, qs,
                                         ks, _dtype_code(q), wd, eps, None if rope is None else rope._ref,
-                                        _addr(q_out), _addr(k_out), _stream(stream))
+                                        _addr(q_out), _addr(k_out), _raw_stream(stream, dev))
     _lib.check("cp_qk_norm_rope_fwd", st)
     return q_out, k_out
 
@@ -569,12 +580,12 @@ def cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, pos, rope, eps=1e-6, dq=No
     if workspace is None:
         workspace = torch.empty(max(256, cp_qk_norm_rope_bwd_workspace_size(C, B, s, N, Nkv, D)), dtype=torch.uint8,
                                 device=q.device)
-    _here(dq_out, dk_out, q, k, wq, wk, pos, None if rope is None else rope.freqs, dq, dk, dwq, dwk, workspace)
+    dev = _here(dq_out, dk_out, q, k, wq, wk, pos, None if rope is None else rope.freqs, dq, dk, dwq, dwk, workspace)
     st = _lib.lib().cp_qk_norm_rope_bwd(_addr(dq_out), _addr(dk_out), _addr(q), _addr(k), _addr(wq), _addr(wk),
                                         _addr(pos), C, B, s, N, Nkv, D, qs, ks, _dtype_code(q), wd, eps,
                                         None if rope is None else rope._ref, _addr(dq), _addr(dk), _addr(dwq),
                                         _addr(dwk), _addr(workspace), workspace.numel() * workspace.element_size(),
-                                        _stream(stream))
+                                        _raw_stream(stream, dev))
     _lib.check("cp_qk_norm_rope_bwd", st)
     return dq, dk, dwq, dwk
 
@@ -620,11 +631,11 @@ def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=
     elif q_out is not None:
         raise ValueError("q_out without q")
     wd = _check_weights(wq, wk, D)
-    _here(q, k, v, k_cache, v_cache, table, cu_new, kv_len, wq, wk, None if rope is None else rope.freqs, q_out)
+    dev = _here(q, k, v, k_cache, v_cache, table, cu_new, kv_len, wq, wk, None if rope is None else rope.freqs, q_out)
     st = _lib.lib().cp_cache_append(_addr(q), _addr(k), _addr(v), qs, ks, vs, _dtype_code(k), R, N, Nkv, D, _addr(wq),
                                     _addr(wk), wd, eps, None if rope is None else rope._ref, pos_base, _addr(k_cache),
                                     _addr(v_cache), n_pages, page, _addr(table), B, max_pages, _addr(cu_new),
-                                    _addr(kv_len), _addr(q_out), _stream(stream))
+                                    _addr(kv_len), _addr(q_out), _raw_stream(stream, dev))
     _lib.check("cp_cache_append", st)
     return q_out
 
@@ -662,11 +673,11 @@ def cp_prefix_attn_fwd(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_
     if workspace is None:
         workspace = torch.empty(max(256, cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page,
                                                                        max_pages)), dtype=torch.uint8, device=q.device)
-    _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, o, lse, workspace)
+    dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, o, lse, workspace)
     st = _lib.lib().cp_prefix_attn_fwd(_addr(q), _addr(k_cache), _addr(v_cache), n_pages, page, _addr(prefix_pages),
                                        prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), max_new,
                                        R, N, Nkv, D, scale, _addr(o), _dtype_code(o), _addr(lse), _addr(workspace),
-                                       workspace.numel() * workspace.element_size(), _stream(stream))
+                                       workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
     _lib.check("cp_prefix_attn_fwd", st)
     return o, lse
 
