@@ -6,7 +6,12 @@
 // a problem are its tokens times the G query heads of that KV head (row i =
 // token i / G, head i % G), cut into tiles of TM rows; an item is one row tile
 // of one KV head of one problem.  The items lie end to end on a line, each
-// ceil(keys / KT) long, and block c works on [c share, (c + 1) share).
+// ceil(keys / KT) long, and worker c of W works on [c share, (c + 1) share).
+//
+// The KV heads of a token lie side by side in memory, and their work is the
+// same, so blocks that run side by side take the same stretch of the line for
+// neighbouring heads: block x is worker x / lanes of lane x % lanes, and the line
+// of a lane holds heads lane, lane + lanes, ...  (a.heads of them).
 //
 // The row tiles of a causal problem need fewer keys than its length: a stretch
 // [n0, n1) of an item of nominal length T that needs K tiles stands for tiles
@@ -29,6 +34,7 @@ struct PrefixArgs {
     int R, B, N, Nkv, G;
     long long P;
     float scale_log2;
+    int lanes, heads;           // Nkv = lanes x heads
     int with_prefix, with_own;  // the problems of this launch
     int *status;
     unsigned long long timeout_ns;
@@ -38,7 +44,7 @@ struct PrefixArgs {
     int *base_item;       // [B] first item of each sequence
     float2 *slot_ml;      // [slots][TM]: exponent, sum
     float *slot_o;        // [slots][TM][D], not divided by the sum
-    int slots;
+    int slots;            // of a lane
 };
 
 __device__ __forceinline__ void report(int *status, cp_status code) { atomicExch(status, static_cast<int>(code)); }
@@ -51,13 +57,26 @@ struct Problem {
     long long key_tiles;  // nominal length of an item
 };
 
+// The lists of the first kListed sequences and where every problem's tiles and
+// items begin on the line (entry i + 1: run i of the sequences; entry 0: the
+// prefix), in shared memory.
+constexpr int kRuns = 128;
+constexpr int kListed = 1024;
+struct Line {
+    long long tile[kRuns + 1];
+    int item[kRuns + 1];
+    int rows_end;  // cu[B]
+    int cu[kListed + 1], len[kListed];
+};
+
 // Sequence b as the device lists give it; a list that makes no sense is cut to
 // what can be read and reported.
 template <int TM, int KT>
-__device__ __forceinline__ Problem sequence_problem(const PrefixArgs &a, int b) {
+__device__ __forceinline__ Problem sequence_problem(const PrefixArgs &a, const Line &line, int b) {
     Problem p;
-    const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
-    long long len = __ldg(a.kv_len + b);
+    const bool listed = b < kListed;
+    const int c0 = listed ? line.cu[b] : __ldg(a.cu + b), c1 = listed ? line.cu[b + 1] : __ldg(a.cu + b + 1);
+    long long len = listed ? line.len[b] : __ldg(a.kv_len + b);
     const long long most = static_cast<long long>(a.own.max_pages) << a.own.shift;
     p.tok0 = c0;
     p.n = c1 - c0;
@@ -75,10 +94,10 @@ __device__ __forceinline__ Problem sequence_problem(const PrefixArgs &a, int b) 
     return p;
 }
 template <int TM, int KT>
-__device__ __forceinline__ Problem prefix_problem(const PrefixArgs &a) {
+__device__ __forceinline__ Problem prefix_problem(const PrefixArgs &a, const Line &line) {
     Problem p;
     p.tok0 = 0;
-    p.n = min(max(__ldg(a.cu + a.B), 0), a.R);
+    p.n = min(max(line.rows_end, 0), a.R);
     p.keys = a.P;
     p.row_tiles = (p.n * a.G + TM - 1) / TM;
     p.key_tiles = p.n ? (a.P + KT - 1) / KT : 0;
@@ -91,32 +110,33 @@ __device__ __forceinline__ int place_of(int j, int tiles) {
     return j < (tiles + 1) / 2 ? 2 * j : 2 * (tiles - 1 - j) + 1;
 }
 
-// Where every problem's tiles and items begin on the line: sums over runs of
-// sequences (entry i + 1: run i; entry 0: the prefix), scanned over the block.
-constexpr int kRuns = 128;
-struct Line {
-    long long tile[kRuns + 1];
-    int item[kRuns + 1];
-};
-
+// Fills `line`: the lists (one load a thread and list for up to a block's
+// threads of sequences), sums over runs of sequences, and their scan.  `lead`
+// is true in the block that leaves the sequences' places for the join.
 template <int TM, int KT>
-__device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, bool publish) {
+__device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, bool lead) {
     const int tid = threadIdx.x, run = (a.B + kRuns - 1) / kRuns;
+    if (tid == 0) line.rows_end = __ldg(a.cu + a.B);
+    for (int b = tid; b <= min(a.B, kListed); b += blockDim.x) {
+        line.cu[b] = __ldg(a.cu + b);
+        if (b < min(a.B, kListed)) line.len[b] = __ldg(a.kv_len + b);
+    }
+    __syncthreads();
     const int b0 = min(tid * run, a.B), b1 = a.with_own ? min(b0 + run, a.B) : b0;
     if (tid < kRuns) {
         long long tiles = 0;
         int items = 0;
         for (int b = b0; b < b1; ++b) {
-            const Problem p = sequence_problem<TM, KT>(a, b);
-            tiles += static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles;
-            items += a.Nkv * p.row_tiles;
+            const Problem p = sequence_problem<TM, KT>(a, line, b);
+            tiles += static_cast<long long>(a.heads) * p.row_tiles * p.key_tiles;
+            items += a.heads * p.row_tiles;
         }
         line.tile[tid + 1] = tiles;
         line.item[tid + 1] = items;
         if (tid == 0) {
-            const Problem p = prefix_problem<TM, KT>(a);
-            line.tile[0] = a.with_prefix ? static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles : 0;
-            line.item[0] = a.with_prefix ? a.Nkv * p.row_tiles : 0;
+            const Problem p = prefix_problem<TM, KT>(a, line);
+            line.tile[0] = a.with_prefix ? static_cast<long long>(a.heads) * p.row_tiles * p.key_tiles : 0;
+            line.item[0] = a.with_prefix ? a.heads * p.row_tiles : 0;
         }
     }
     __syncthreads();
@@ -124,12 +144,14 @@ __device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, bool 
         // inclusive scan of 128 entries, 4 to a lane
         long long t[4];
         int n[4];
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
             t[i] = line.tile[1 + 4 * tid + i] + (i ? t[i - 1] : 0);
             n[i] = line.item[1 + 4 * tid + i] + (i ? n[i - 1] : 0);
         }
         long long ts = t[3];
         int ns = n[3];
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long tv = __shfl_up_sync(0xffffffffu, ts, o);
             const int nv = __shfl_up_sync(0xffffffffu, ns, o);
@@ -137,21 +159,22 @@ __device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, bool 
         }
         const long long t0 = ts - t[3] + line.tile[0];
         const int n0 = ns - n[3] + line.item[0];
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
             line.tile[1 + 4 * tid + i] = t0 + t[i];
             line.item[1 + 4 * tid + i] = n0 + n[i];
         }
     }
     __syncthreads();
-    if (publish && tid < kRuns) {
+    if (lead && tid < kRuns) {
         long long t = line.tile[tid];
         int n = line.item[tid];
         for (int b = b0; b < b1; ++b) {
-            const Problem p = sequence_problem<TM, KT>(a, b);
+            const Problem p = sequence_problem<TM, KT>(a, line, b);
             a.base_tile[b] = t;
             a.base_item[b] = n;
-            t += static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles;
-            n += a.Nkv * p.row_tiles;
+            t += static_cast<long long>(a.heads) * p.row_tiles * p.key_tiles;
+            n += a.heads * p.row_tiles;
         }
     }
 }
@@ -162,12 +185,13 @@ __device__ __forceinline__ long long div_floor(long long a, long long b) {
     return a / b;
 }
 
-// A block's share of the line; false if it has none.
+// A block's share of its lane's line; false if it has none.
 __device__ __forceinline__ bool share_of(const PrefixArgs &a, const Line &line, long long *t0, long long *t1) {
     const long long total = line.tile[kRuns];
-    const long long share = max(1ll, div_floor(total + gridDim.x - 1, gridDim.x));
+    const int workers = gridDim.x / a.lanes;
+    const long long share = max(1ll, div_floor(total + workers - 1, workers));
     if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = share;
-    *t0 = share * blockIdx.x;
+    *t0 = share * (blockIdx.x / a.lanes);
     *t1 = min(*t0 + share, total);
     return *t0 < *t1;
 }
@@ -175,7 +199,7 @@ __device__ __forceinline__ bool share_of(const PrefixArgs &a, const Line &line, 
 // A stretch of one item that a block works on.
 struct Piece {
     int b;                // sequence, -1: the prefix
-    int item;             // index on the line
+    int slot;             // where the piece's partial goes, -1: nowhere
     int kvh, tok0, rows;  // rows of the problem
     int row0;             // first row of the tile
     long long keys;       // keys of the problem
@@ -197,7 +221,7 @@ __device__ __forceinline__ Piece find_piece(const PrefixArgs &a, const Line &lin
     long long base = 0;
     int item = 0;
     if (t < line.tile[0]) {
-        p = prefix_problem<TM, KT>(a);
+        p = prefix_problem<TM, KT>(a, line);
         x.b = -1;
     } else {
         // the run that holds t: the last entry with tile <= t
@@ -210,24 +234,27 @@ __device__ __forceinline__ Piece find_piece(const PrefixArgs &a, const Line &lin
         item = line.item[lo];
         int b = lo * ((a.B + kRuns - 1) / kRuns);
         for (; b < a.B; ++b) {
-            p = sequence_problem<TM, KT>(a, b);
-            const long long all = static_cast<long long>(a.Nkv) * p.row_tiles * p.key_tiles;
+            p = sequence_problem<TM, KT>(a, line, b);
+            const long long all = static_cast<long long>(a.heads) * p.row_tiles * p.key_tiles;
             if (t < base + all) break;
             base += all;
-            item += a.Nkv * p.row_tiles;
+            item += a.heads * p.row_tiles;
         }
         x.b = b;
         if (b >= a.B) {
             // only when the lists were changed under the launch: a stretch without work
             x = Piece{};
+            x.slot = -1;
             x.next = end;
             return x;
         }
     }
     const long long at = t - base, which = div_floor(at, p.key_tiles);
-    x.kvh = static_cast<int>(div_floor(which, p.row_tiles));
-    const int j = tile_at(static_cast<int>(which - static_cast<long long>(x.kvh) * p.row_tiles), p.row_tiles);
-    x.item = item + static_cast<int>(which);
+    const int pass = static_cast<int>(div_floor(which, p.row_tiles)), lane = blockIdx.x % a.lanes;
+    const int j = tile_at(static_cast<int>(which - static_cast<long long>(pass) * p.row_tiles), p.row_tiles);
+    const int slot = item + static_cast<int>(which) + static_cast<int>(blockIdx.x / a.lanes);
+    x.kvh = pass * a.lanes + lane;
+    x.slot = slot < a.slots ? lane * a.slots + slot : -1;
     x.row0 = j * TM;
     x.tok0 = p.tok0;
     x.rows = p.n * a.G;
@@ -241,5 +268,47 @@ __device__ __forceinline__ Piece find_piece(const PrefixArgs &a, const Line &lin
     x.next = t + (n1 - n0);
     return x;
 }
+
+// The page numbers of a piece, for the warp that starts its copies: 32 entries
+// of the page list side by side in the lanes and the next 32 on their way, so no
+// tile waits for its page numbers.
+struct PageWindow {
+    const int32_t *list;
+    int n, n_pages, shift;  // entries, pages of the cache
+    int base, cur, next;    // first entry of `cur`
+    __device__ __forceinline__ int fetch(int first, int lane) const {
+        return first + lane < n ? __ldg(list + first + lane) : -1;
+    }
+    __device__ __forceinline__ void begin(const PrefixArgs &a, const Piece &x, int first, int lane) {
+        const PageTable &t = x.b < 0 ? a.pre : a.own;
+        list = t.table + static_cast<long long>(max(x.b, 0)) * t.max_pages;
+        n = static_cast<int>(min(static_cast<long long>(t.max_pages), (x.keys + (1ll << t.shift) - 1) >> t.shift));
+        n_pages = t.n_pages;
+        shift = t.shift;
+        base = first;
+        cur = fetch(base, lane);
+        next = fetch(base + 32, lane);
+    }
+    // Moves on so that entry `first` lies in the window (first never goes back). Warp-wide.
+    __device__ __forceinline__ void advance(int first, int lane) {
+        while (first >= base + 32) {
+            base += 32;
+            cur = next;
+            next = fetch(base + 32, lane);
+        }
+    }
+    // Cache row of key `key` (uniform over the warp, of an entry in the window:
+    // 32 is a multiple of a tile's pages, and the window began at a tile's
+    // first); the row after the last page for a page number out of range.
+    __device__ __forceinline__ int row(const PrefixArgs &a, long long key) const {
+        const int e = static_cast<int>(key >> shift);
+        const int page = __shfl_sync(0xffffffffu, cur, (e - base) & 31);
+        if (page < 0 || page >= n_pages) {
+            report(a.status, CP_ERR_PAGE);
+            return n_pages << shift;
+        }
+        return (page << shift) + static_cast<int>(key & ((1 << shift) - 1));
+    }
+};
 
 }  // namespace cpattn

@@ -78,7 +78,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 constexpr int kGroups = 2;                    // consumer groups of 4 warps
-constexpr int kMmaThreads = 32 + kGroups * 128;
+constexpr int kMmaThreads = 64 + kGroups * 128;  // and two loading warps
 
 template <int D>
 struct MmaCfg {
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     if (tid == 0) {
         *abort_flag = 0;
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(full + s, 1);
+            mbar_init(full + s, 2);
             mbar_init(empty + s, 4);
         }
         for (int i = 0; i < kGroups; ++i) mbar_init(go + i, 4);
@@ -143,37 +143,36 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     long long t0, t1;
     if (!share_of(a, line, &t0, &t1)) return;
 
-    if (warp == 0) {
-        // -------------------------------------------------------- loads
-        // lane = (page of the tile, K or V, 64-column half): one copy each
+    if (warp < 2) {
+        // -------------------------------------------------------- loads: K by warp 0, V by warp 1
+        // The copies are started by one lane in a loop over the tile's pages with
+        // uniform operands, about 30 cycles each; a lane for each page took 90,
+        // the instruction being issued lane after lane.
+        const CUtensorMap *map = warp ? &tmV : &tmK;
         const int shift = a.own.shift, rows = min(kKT, 1 << shift);
-        const int per_tile = kKT / rows, nowhere = a.own.n_pages << shift;
-        const int page = lane / (2 * C::kAtoms), is_v = (lane / C::kAtoms) & 1, at = lane % C::kAtoms;
         uint32_t it = 0;
         bool ok = true;
-        auto page_row = [&](const Piece &x, long long kt) -> int {
-            const long long key = kt * kKT + page * rows;
-            if (page >= per_tile || key >= x.keys) return -1;
-            const long long slot = (x.b < 0 ? a.pre : a.own).slot(x.b < 0 ? 0 : x.b, key);
-            if (slot < 0) report(a.status, CP_ERR_PAGE);
-            return slot < 0 ? nowhere : static_cast<int>(slot);
-        };
         for (long long t = t0; t < t1 && ok;) {
             const Piece x = find_piece<kTM, kKT>(a, line, t, t1);
             t = x.next;
             if (x.k0 >= x.k1) continue;
-            int row = page_row(x, x.k0);
+            PageWindow win;
+            win.begin(a, x, static_cast<int>((x.k0 * kKT) >> shift), lane);
             for (long long kt = x.k0; kt < x.k1; ++kt, ++it) {
-                const int next = kt + 1 < x.k1 ? page_row(x, kt + 1) : -1;
+                const long long key = kt * kKT;
+                win.advance(static_cast<int>(key >> shift), lane);
+                const int n = static_cast<int>(min(static_cast<long long>(kKT), x.keys - key) + rows - 1) / rows;
                 const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
                 if (!mbar_wait_warp(empty + st, ph ^ 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
-                const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
-                if (lane == 0) mbar_arrive_expect_tx(full + st, n * rows * 128);
-                __syncwarp();
-                if (row >= 0)
-                    tma_load_4d(smem + (st * 2 + is_v) * C::kTile + at * C::kAtom + page * rows * 128, is_v ? &tmV : &tmK,
-                                full + st, 64 * at, x.kvh, row, 0);
-                row = next;
+                uint8_t *dst = smem + (st * 2 + warp) * C::kTile;
+                if (lane == 0) mbar_arrive_expect_tx(full + st, n * rows * 128 * C::kAtoms);
+                for (int i = 0; i < n; ++i) {
+                    const int row = win.row(a, key + i * rows);
+                    if (lane == 0)
+#pragma unroll
+                        for (int at = 0; at < C::kAtoms; ++at)
+                            tma_load_4d(dst + at * C::kAtom + i * rows * 128, map, full + st, 64 * at, x.kvh, row, 0);
+                }
             }
         }
         // let every copy already issued land before shared memory goes away
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------- products
-        const int group = (warp - 1) >> 2, w = (warp - 1) & 3, gtid = tid - 32 - group * 128;
+        const int group = (warp - 2) >> 2, w = (warp - 2) & 3, gtid = tid - 64 - group * 128;
         const int g = lane >> 2, t4 = lane & 3;  // accumulator row (and row + 8), column pair
         float *out_s = reinterpret_cast<float *>(smem + C::kOffOut) + group * 4 * 16 * D;
         float2 *ml_s = reinterpret_cast<float2 *>(smem + C::kOffMl) + group * 4 * 16;
@@ -317,7 +316,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             if (lane == 0) mbar_arrive(go + (group ^ 1));
             // join the four warps' keys and leave the piece's partial (a warp that gave
             // up a wait takes part, so that the group stays together, and all leave below)
-            const int slot = x.item + static_cast<int>(blockIdx.x);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -330,7 +328,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             }
             group_sync(group);
             const int row = gtid >> 3, c0 = (gtid & 7) * 4;  // 8 threads a row, 4 values at a time
-            if (x.row0 + row < x.rows && slot < a.slots) {
+            if (x.row0 + row < x.rows && x.slot >= 0) {
                 float2 ml[4];
                 float f[4], mx = -INFINITY, ls = 0.f;
 #pragma unroll
@@ -343,7 +341,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     f[i] = ml[i].x == -INFINITY ? 0.f : fast_exp2(ml[i].x - mx);
                     ls += f[i] * ml[i].y;
                 }
-                const long long at = static_cast<long long>(slot) * kTM + row;
+                const long long at = static_cast<long long>(x.slot) * kTM + row;
 #pragma unroll
                 for (int c = c0; c < D; c += 32) {
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -361,7 +359,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 }
                 if (c0 == 0) a.slot_ml[at] = make_float2(mx, ls);
             }
-            if (slot >= a.slots && gtid == 0) report(a.status, CP_ERR_PAGE);
+            if (x.slot < 0 && gtid == 0) report(a.status, CP_ERR_PAGE);
             if (group_any(group, !ok)) ok = false;
         }
     }
@@ -375,7 +373,7 @@ struct JoinPart {
     const int *base_item;
     const float2 *slot_ml;
     const float *slot_o;
-    int slots, tm, kt;
+    int slots, tm, kt, lanes;  // slots: of a lane
 };
 struct JoinArgs {
     JoinPart part[2];  // the prefix; the sequences
@@ -397,7 +395,7 @@ struct TokenPart {
     const float2 *slot_ml;
     const float *slot_o;
     long long base_tile, key_tiles, share;
-    int base_item, row_tiles, row0, tm, slots;
+    int base_item, row_tiles, row0, tm, slots, lanes;
     // which: 0 the prefix, 1 the sequence b that begins at row `begin` with `count` new tokens
     __device__ __forceinline__ TokenPart(const JoinArgs &a, int which, int b, int tok, int begin, int count) {
         const JoinPart &p = a.part[which];
@@ -406,6 +404,7 @@ struct TokenPart {
         slot_ml = p.slot_ml;
         slot_o = p.slot_o;
         slots = p.slots;
+        lanes = p.lanes;
         tm = p.tm;
         key_tiles = div_floor(keys + p.kt - 1, p.kt);
         row_tiles = (n * a.G + tm - 1) / tm;
@@ -417,13 +416,13 @@ struct TokenPart {
     }
     __device__ __forceinline__ RowPieces row(int kvh, int gh) const {
         if (key_tiles == 0) return RowPieces{0, 0, 0};
-        const int i = row0 + gh;
-        const long long at = static_cast<long long>(kvh) * row_tiles + place_of(i / tm, row_tiles);
+        const int i = row0 + gh, pass = kvh / lanes;
+        const long long at = static_cast<long long>(pass) * row_tiles + place_of(i / tm, row_tiles);
         const long long first = base_tile + at * key_tiles;
         const int c0 = static_cast<int>(div_floor(first, share));
         const int c1 = static_cast<int>(div_floor(first + key_tiles - 1, share));
         const int slot = base_item + static_cast<int>(at) + c0;
-        return RowPieces{slot, min(c1 - c0 + 1, slots - slot), i % tm};
+        return RowPieces{(kvh - pass * lanes) * slots + slot, min(c1 - c0 + 1, slots - slot), i % tm};
     }
 };
 
@@ -459,8 +458,8 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
-// Few rows of many pieces: a warp joins the pieces of one row, a lane a piece's
-// (m, l), then the pieces' rows one after another.
+// Few rows of many pieces: a warp joins the pieces of one row, those of both
+// parts in one list: a lane a piece's (m, l), then the pieces' rows, eight loads in flight.
 template <int D>
 __global__ void __launch_bounds__(128) join_row_kernel(const JoinArgs a) {
     constexpr int kV = D / 32;
@@ -475,34 +474,47 @@ __global__ void __launch_bounds__(128) join_row_kernel(const JoinArgs a) {
 #pragma unroll
     for (int e = 0; e < kV; ++e) acc[e] = 0.f;
     const int kvh = h / a.G;
+    const TokenPart p0(a, 0, b, tok, begin, count), p1(a, 1, b, tok, begin, count);
+    const RowPieces x0 = p0.row(kvh, h - kvh * a.G), x1 = p1.row(kvh, h - kvh * a.G);
+    for (int cb = 0; cb < x0.n + x1.n; cb += 32) {
+        const int i = cb + lane;
+        const bool one = i >= x0.n;
+        const TokenPart &p = one ? p1 : p0;
+        const long long at = static_cast<long long>(one ? x1.first + i - x0.n : x0.first + i) * p.tm + (one ? x1.r : x0.r);
+        const bool in = i < x0.n + x1.n;
+        const float2 ml = in ? p.slot_ml[at] : make_float2(-INFINITY, 0.f);
+        const float *mine = in ? p.slot_o + at * D : nullptr;
+        const float top = warp_max(ml.x);
+        if (top == -INFINITY) continue;
+        if (top > mx) {
+            const float f = mx == -INFINITY ? 0.f : fast_exp2(mx - top);
+            ls *= f;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const TokenPart p(a, which, b, tok, begin, count);
-        const RowPieces x = p.row(kvh, h - kvh * a.G);
-        for (int cb = 0; cb < x.n; cb += 32) {
-            const float2 ml = cb + lane < x.n ? p.slot_ml[static_cast<long long>(x.first + cb + lane) * p.tm + x.r]
-                                              : make_float2(-INFINITY, 0.f);
-            const float top = warp_max(ml.x);
-            if (top == -INFINITY) continue;
-            if (top > mx) {
-                const float f = mx == -INFINITY ? 0.f : fast_exp2(mx - top);
-                ls *= f;
+            for (int e = 0; e < kV; ++e) acc[e] *= f;
+            mx = top;
+        }
+        const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mx);
+        float add = w * ml.y;
 #pragma unroll
-                for (int e = 0; e < kV; ++e) acc[e] *= f;
-                mx = top;
+        for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+        ls += add;
+        const int n = min(32, x0.n + x1.n - cb);
+        for (int k0 = 0; k0 < n; k0 += 8) {
+            float v[8][kV], f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                f[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+                const float *src = reinterpret_cast<const float *>(__shfl_sync(
+                    0xffffffffu, reinterpret_cast<unsigned long long>(mine), (k0 + k) & 31));
+                if (k0 + k >= n) f[k] = 0.f;
+#pragma unroll
+                for (int e = 0; e < kV; ++e) v[k][e] = 0.f;
+                if (f[k] != 0.f) add_row<kV>(v[k], src + lane * kV, 1.f);
             }
-            const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mx);
-            float add = w * ml.y;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
-            ls += add;
-            const int n = min(32, x.n - cb);
-#pragma unroll 8
-            for (int k = 0; k < n; ++k) {
-                const float f = __shfl_sync(0xffffffffu, w, k);
-                if (f != 0.f)
-                    add_row<kV>(acc, p.slot_o + (static_cast<long long>(x.first + cb + k) * p.tm + x.r) * D + lane * kV, f);
-            }
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int e = 0; e < kV; ++e) acc[e] += f[k] * v[k][e];
         }
     }
     store_row<kV>(a, row, lane, acc, mx == -INFINITY ? 0.f : 1.f / ls);
@@ -584,7 +596,8 @@ constexpr long long kJoinRows = 16384;  // up to this many rows a warp joins one
 // How a call is cut: which launches it makes and where they leave their pieces.
 struct Shape {
     bool tc_prefix, tc_own;  // tensor-memory tiles of 256 rows, else tiles of 16 rows
-    long long slots[2];      // of the 16-row launch and the 256-row launch (0: not made)
+    int lanes;               // of KV heads
+    long long slots[2];      // of a lane of the 16-row launch and the 256-row launch (0: not made)
     size_t head[2], base_tile[2], base_item[2], slot_ml[2], slot_o[2], bytes;
 };
 
@@ -593,6 +606,10 @@ Shape shape_of(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int6
     Shape s{};
     s.tc_prefix = R * G > kTcRows;
     s.tc_own = max_new * G > kTcRows;
+    // as many lanes as leave nearly no SM without work
+    const int sms = sm_count();
+    for (int d = 1; d <= Nkv && d <= sms; ++d)
+        if (Nkv % d == 0 && sms / d * d * 25LL >= sms * 24LL) s.lanes = d;
     size_t at = 0;
     auto take = [&at](size_t n) {
         const size_t x = at;
@@ -604,12 +621,12 @@ Shape shape_of(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int6
         const long long tm = k ? kTcTM : kTM, tiles = (R * G + tm - 1) / tm;
         if (!pre && !own) continue;
         // every row tile of the prefix and of the sequences (each may end a tile early), and a cut for each block
-        s.slots[k] = Nkv * ((pre ? tiles : 0) + (own ? tiles + (B < R ? B : R) : 0)) + kMaxBlocks;
+        s.slots[k] = Nkv / s.lanes * ((pre ? tiles : 0) + (own ? tiles + (B < R ? B : R) : 0)) + kMaxBlocks / s.lanes;
         s.head[k] = take(8);
         s.base_tile[k] = take(B * 8);
         s.base_item[k] = take(B * 4);
-        s.slot_ml[k] = take(static_cast<size_t>(s.slots[k]) * tm * 8);
-        s.slot_o[k] = take(static_cast<size_t>(s.slots[k]) * tm * D * 4);
+        s.slot_ml[k] = take(static_cast<size_t>(s.slots[k]) * s.lanes * tm * 8);
+        s.slot_o[k] = take(static_cast<size_t>(s.slots[k]) * s.lanes * tm * D * 4);
     }
     s.bytes = at;
     return s;
@@ -632,7 +649,8 @@ cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
     CUtensorMap mk, mv;
     if (!make_map(&mk, a.k, D, a.Nkv, rows, 1, box, l2) || !make_map(&mv, a.v, D, a.Nkv, rows, 1, box, l2))
         return CP_ERR_CUDA;
-    const int grid = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
+    const int sms = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
+    const int grid = sms / a.lanes * a.lanes;
     if (tc)
         prefix_tc_kernel<D><<<grid, kTcThreads, TcCfg<D>::kSmem, stream>>>(mk, mv, a);
     else
@@ -658,7 +676,7 @@ cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cuda
         for (int which = 0; which < 2; ++which)
             if (which ? a.with_own : a.with_prefix)
                 j.part[which] = JoinPart{a.head, a.base_tile, a.base_item, a.slot_ml, a.slot_o, a.slots,
-                                         k ? kTcTM : kTM, k ? kTcKT : kKT};
+                                         k ? kTcTM : kTM, k ? kTcKT : kKT, a.lanes};
     }
     if (a.P == 0) j.part[0] = j.part[1];  // not read into a result: no keys
     const long long rows = static_cast<long long>(a.R) * a.N;
@@ -734,7 +752,7 @@ extern "C" cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, cons
     const Shape s = shape_of(R, B, max_new, prefix_len, N, Nkv, D);
     if (!workspace || ws_bytes < s.bytes) return CP_ERR_WORKSPACE;
     if (odd(workspace, 256)) return CP_ERR_ALIGNMENT;
-    if (s.slots[0] > INT32_MAX || s.slots[1] > INT32_MAX) return CP_ERR_SHAPE;
+    if (s.slots[0] * s.lanes > INT32_MAX || s.slots[1] * s.lanes > INT32_MAX) return CP_ERR_SHAPE;
     PrefixArgs a{};
     if ((st = status_word(&a.status)) != CP_OK) return st;
     a.timeout_ns = 2000000000ull;
@@ -757,6 +775,8 @@ extern "C" cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, cons
     a.N = static_cast<int>(N);
     a.Nkv = static_cast<int>(Nkv);
     a.G = static_cast<int>(N / Nkv);
+    a.lanes = s.lanes;
+    a.heads = static_cast<int>(Nkv / s.lanes);
     a.P = prefix_len;
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
     JoinArgs j{};

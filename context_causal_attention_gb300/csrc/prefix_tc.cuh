@@ -3,10 +3,10 @@
 //
 // One block on an SM works through its share of the line (cp_prefix.cuh) with
 // 12 warps:
-//   warp 0      loads: the page numbers of a 128-key tile side by side in its
-//               lanes, one tile ahead; each lane starts the copies of its page
-//               (64 columns x a page's rows a copy, 128-byte swizzle) into a
-//               ring of K and V stages.  A page number out of range becomes a
+//   warps 0, 2  loads of K and of V: the page numbers of 32 pages side by side in
+//               the lanes, the next 32 on their way; a copy (64 columns x a
+//               page's rows, 128-byte swizzle) for each page and column half
+//               into a ring of stages.  A page number out of range becomes a
 //               coordinate outside the tensor, which TMA fills with zeros.
 //   warp 1      tensor memory (512 columns: S0 | S1 | O0 | O1) and MMA issue:
 //               S_i = Q_i K^T, O_i += P_i V with P_i in tensor memory.
@@ -116,67 +116,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t tmem = *tmem_slot;
     uint8_t *sQ = smem + C::kOffQ, *sK = smem + C::kOffK, *sV = smem + C::kOffV;
 
-    if (warp == 0) {
-        // -------------------------------------------------------- loads
-        const int shift = a.own.shift, rows = min(128, 1 << shift);  // rows of a copy
-        const int per_tile = 128 / rows;                             // copies of a tile and 64 columns
-        const int nowhere = a.own.n_pages << shift;                  // a row outside the tensor
-        uint32_t k_it = 0, v_it = 0, k_par = 0, v_par = 0, k_issued = 0, v_issued = 0;
+    if (warp == 0 || warp == 2) {
+        // -------------------------------------------------------- loads: K by warp 0, V by warp 2
+        const CUtensorMap *map = warp ? &tmV : &tmK;
+        uint64_t *full = warp ? v_full : k_full, *empty = warp ? v_empty : k_empty;
+        uint8_t *ring = warp ? sV : sK;
+        const int shift = a.own.shift, rows = min(kTcKT, 1 << shift);  // rows of a copy
+        uint32_t it = 0;
         bool ok = true;
-        // cache row of this lane's copy of tile kt (-1: past the keys)
-        auto page_row = [&](const Piece &x, long long kt) -> int {
-            const long long key = kt * 128 + lane * rows;
-            if (lane >= per_tile || key >= x.keys) return -1;
-            const long long slot = (x.b < 0 ? a.pre : a.own).slot(x.b < 0 ? 0 : x.b, key);
-            if (slot < 0) report(a.status, CP_ERR_PAGE);
-            return slot < 0 ? nowhere : static_cast<int>(slot);
-        };
-        auto load = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *full, uint64_t *empty, uint32_t &it,
-                        uint32_t &par, uint32_t &issued, int row, int kvh) -> bool {
-            const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
-            if (!mbar_wait_warp(empty + st, ph ^ 1u, abort_flag, a.timeout_ns)) return false;
-            const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
-            if (lane == 0) mbar_arrive_expect_tx(full + st, n * rows * 128 * C::kAtoms);
-            __syncwarp();
-            if (row >= 0)
-                for (int at = 0; at < C::kAtoms; ++at)
-                    tma_load_4d(dst + st * C::kTile + at * C::kAtom + lane * rows * 128, map, full + st, 64 * at, kvh,
-                                row, 0);
-            issued |= 1u << st;
-            par = (par & ~(1u << st)) | (ph << st);
-            ++it;
-            return true;
-        };
-        // K runs one tile ahead of V: a K stage is free after the tile's scores, a
-        // V stage only after its weights have been used
-        bool pend = false;
-        int pend_row = -1, pend_kvh = 0;
         for (long long t = t0; t < t1 && ok;) {
             const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
             t = x.next;
             if (x.k0 >= x.k1) continue;
-            int row = page_row(x, x.k0);
-            for (long long kt = x.k0; kt < x.k1; ++kt) {
-                const int next = kt + 1 < x.k1 ? page_row(x, kt + 1) : -1;
-                if (!load(&tmK, sK, k_full, k_empty, k_it, k_par, k_issued, row, x.kvh) ||
-                    (pend && !load(&tmV, sV, v_full, v_empty, v_it, v_par, v_issued, pend_row, pend_kvh))) {
-                    ok = false;
-                    break;
+            PageWindow win;
+            win.begin(a, x, static_cast<int>((x.k0 * kTcKT) >> shift), lane);
+            for (long long kt = x.k0; kt < x.k1; ++kt, ++it) {
+                const long long key = kt * kTcKT;
+                win.advance(static_cast<int>(key >> shift), lane);
+                const int n = static_cast<int>(min(static_cast<long long>(kTcKT), x.keys - key) + rows - 1) / rows;
+                const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
+                if (!mbar_wait_warp(empty + st, ph ^ 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(full + st, n * rows * 128 * C::kAtoms);
+                for (int i = 0; i < n; ++i) {
+                    const int row = win.row(a, key + i * rows);
+                    if (lane == 0)
+#pragma unroll
+                        for (int at = 0; at < C::kAtoms; ++at)
+                            tma_load_4d(ring + st * C::kTile + at * C::kAtom + i * rows * 128, map, full + st, 64 * at,
+                                        x.kvh, row, 0);
                 }
-                pend = true;
-                pend_row = row;
-                pend_kvh = x.kvh;
-                row = next;
             }
         }
-        if (ok && pend && !load(&tmV, sV, v_full, v_empty, v_it, v_par, v_issued, pend_row, pend_kvh)) ok = false;
         if (!ok && lane == 0) {
             // let every copy already issued land before shared memory goes away
             volatile int no_abort = 0;
-            for (int st = 0; st < C::kStages; ++st) {
-                if ((k_issued >> st) & 1u) mbar_wait(k_full + st, (k_par >> st) & 1u, &no_abort, 100000000ull);
-                if ((v_issued >> st) & 1u) mbar_wait(v_full + st, (v_par >> st) & 1u, &no_abort, 100000000ull);
-            }
+            for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
+                mbar_wait(full + i % C::kStages, (i / C::kStages) & 1u, &no_abort, 100000000ull);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -249,12 +224,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
             const int row = x.row0 + half * 128 + in_tile;
             const bool valid = row < x.rows;
-            const int slot = x.item + static_cast<int>(blockIdx.x);
-            const bool write = valid && slot < a.slots;
-            if (slot >= a.slots && in_tile == 0) report(a.status, CP_ERR_PAGE);
+            const bool write = valid && x.slot >= 0;
+            if (x.slot < 0 && in_tile == 0) report(a.status, CP_ERR_PAGE);
             t = x.next;
             if (x.k0 >= x.k1) {
-                if (write) a.slot_ml[static_cast<long long>(slot) * kTcTM + half * 128 + in_tile] = make_float2(-INFINITY, 0.f);
+                if (write) a.slot_ml[static_cast<long long>(x.slot) * kTcTM + half * 128 + in_tile] = make_float2(-INFINITY, 0.f);
                 continue;
             }
             if (x.row0 + half * 128 >= x.rows) {
@@ -363,7 +337,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(o_empty + half);
             if (write) {
-                const long long at = static_cast<long long>(slot) * kTcTM + half * 128 + in_tile;
+                const long long at = static_cast<long long>(x.slot) * kTcTM + half * 128 + in_tile;
                 float *dst = a.slot_o + at * D;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c)
