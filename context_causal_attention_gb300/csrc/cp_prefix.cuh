@@ -24,6 +24,7 @@
 #include <cstdint>
 
 #include "cp_paged.cuh"
+#include "cp_ptx.cuh"
 
 namespace cpattn {
 
@@ -117,7 +118,7 @@ template <int TM, int KT>
 __device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, bool lead) {
     const int tid = threadIdx.x, run = (a.B + kRuns - 1) / kRuns;
     if (tid == 0) line.rows_end = __ldg(a.cu + a.B);
-    for (int b = tid; b <= min(a.B, kListed); b += blockDim.x) {
+    for (int b = a.with_own ? tid : kListed + 1; b <= min(a.B, kListed); b += blockDim.x) {
         line.cu[b] = __ldg(a.cu + b);
         if (b < min(a.B, kListed)) line.len[b] = __ldg(a.kv_len + b);
     }
@@ -202,15 +203,15 @@ struct Piece {
     int slot;             // where the piece's partial goes, -1: nowhere
     int kvh, tok0, rows;  // rows of the problem
     int row0;             // first row of the tile
-    long long keys;       // keys of the problem
-    long long off;        // rows of token i see keys [0, off + i] (prefix: all)
-    long long k0, k1;     // key tiles [k0, k1), may be none
+    int keys;             // keys of the problem
+    int off;              // rows of token i see keys [0, off + i] (prefix: all)
+    int k0, k1;           // key tiles [k0, k1), may be none
     long long next;       // where the next piece begins on the line
 };
 
 // Keys that row `row` of the problem sees: [0, limit).
-__device__ __forceinline__ long long row_limit(const PrefixArgs &a, const Piece &x, int row) {
-    return x.b < 0 ? x.keys : max(0ll, x.off + row / a.G + 1);
+__device__ __forceinline__ int row_limit(const PrefixArgs &a, const Piece &x, int row) {
+    return x.b < 0 ? x.keys : min(x.keys, max(0, x.off + row / a.G + 1));
 }
 
 // The piece that begins at place t of the line (t < end), cut at `end`.
@@ -258,13 +259,13 @@ __device__ __forceinline__ Piece find_piece(const PrefixArgs &a, const Line &lin
     x.row0 = j * TM;
     x.tok0 = p.tok0;
     x.rows = p.n * a.G;
-    x.keys = p.keys;
-    x.off = p.keys - p.n;
+    x.keys = static_cast<int>(p.keys);
+    x.off = x.keys - p.n;
     const long long n0 = at - which * p.key_tiles;
     const long long n1 = min(n0 + (end - t), p.key_tiles);
-    const long long need = (min(p.keys, row_limit(a, x, min(x.row0 + TM, x.rows) - 1)) + KT - 1) / KT;
-    x.k0 = need == p.key_tiles ? n0 : n0 * need / p.key_tiles;
-    x.k1 = need == p.key_tiles ? n1 : n1 * need / p.key_tiles;
+    const long long need = (static_cast<long long>(row_limit(a, x, min(x.row0 + TM, x.rows) - 1)) + KT - 1) / KT;
+    x.k0 = static_cast<int>(need == p.key_tiles ? n0 : n0 * need / p.key_tiles);
+    x.k1 = static_cast<int>(need == p.key_tiles ? n1 : n1 * need / p.key_tiles);
     x.next = t + (n1 - n0);
     return x;
 }
@@ -282,7 +283,7 @@ struct PageWindow {
     __device__ __forceinline__ void begin(const PrefixArgs &a, const Piece &x, int first, int lane) {
         const PageTable &t = x.b < 0 ? a.pre : a.own;
         list = t.table + static_cast<long long>(max(x.b, 0)) * t.max_pages;
-        n = static_cast<int>(min(static_cast<long long>(t.max_pages), (x.keys + (1ll << t.shift) - 1) >> t.shift));
+        n = min(t.max_pages, static_cast<int>((static_cast<long long>(x.keys) + (1 << t.shift) - 1) >> t.shift));
         n_pages = t.n_pages;
         shift = t.shift;
         base = first;
@@ -300,15 +301,51 @@ struct PageWindow {
     // Cache row of key `key` (uniform over the warp, of an entry in the window:
     // 32 is a multiple of a tile's pages, and the window began at a tile's
     // first); the row after the last page for a page number out of range.
-    __device__ __forceinline__ int row(const PrefixArgs &a, long long key) const {
-        const int e = static_cast<int>(key >> shift);
+    __device__ __forceinline__ int row(const PrefixArgs &a, int key) const {
+        const int e = key >> shift;
         const int page = __shfl_sync(0xffffffffu, cur, (e - base) & 31);
         if (page < 0 || page >= n_pages) {
             report(a.status, CP_ERR_PAGE);
             return n_pages << shift;
         }
-        return (page << shift) + static_cast<int>(key & ((1 << shift) - 1));
+        return (page << shift) + (key & ((1 << shift) - 1));
     }
 };
+
+// Starts the copies of one tile of KT keys of a piece (K or V) into shared
+// memory, 64-column atoms of kAtom bytes, rows of 128 bytes, 128-byte swizzle, by
+// one warp with 16-byte cp.async: a warp instruction moves whole head rows of D
+// values, the page is looked up once for 16 rows, and keys past the piece's are
+// filled with zeros.  TMA tiles of a small page are slower: a copy of 16 rows of
+// 128 bytes holds the TMA unit for about 90 cycles, which ends at 3.4 TB/s over
+// the GPU with two issuing warps and 4.4 with four, where this reaches 5.9.
+template <int D, int KT, int kAtom>
+__device__ __forceinline__ void copy_tile(const PrefixArgs &a, const Piece &x, const PageWindow &win,
+                                          const __nv_bfloat16 *cache, uint32_t dst, int key0, int lane) {
+    constexpr int kChunks = D / 8, kRpi = 32 / kChunks;  // 16-byte chunks of a row, rows of an instruction
+    const int r = lane / kChunks, c = lane % kChunks;
+    const long long step = static_cast<long long>(kRpi) * a.Nkv * D;
+    const uint32_t lane_dst = dst + (c >> 3) * kAtom + r * 128, sw = ((c & 7) ^ r) << 4;
+#pragma unroll
+    for (int g = 0; g < KT / 16; ++g) {
+        const int key = key0 + 16 * g, left = min(16, x.keys - key);
+        const int row = left > 0 ? win.row(a, key) : 0;
+        const bool there = row < win.n_pages << win.shift;  // else a bad page: zeros
+        const __nv_bfloat16 *src =
+            cache + ((static_cast<long long>(there ? row + r : 0)) * a.Nkv + x.kvh) * D + c * 8;
+#pragma unroll
+        for (int i = 0; i < 16 / kRpi; ++i) {
+            const int n = there && i * kRpi + r < left ? 16 : 0;
+            const uint32_t at = lane_dst + (16 * g + i * kRpi) * 128 + (sw ^ (((i * kRpi) & 7) << 4));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(n ? src + i * step : cache), "r"(n)
+                         : "memory");
+        }
+    }
+}
+// Arrives on `bar` (count: one for each lane) when the lane's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copies_drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 }  // namespace cpattn

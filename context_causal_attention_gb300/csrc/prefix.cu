@@ -21,8 +21,8 @@
 // no counter.  A second launch joins the pieces of every row in their order:
 // the result does not depend on timing.
 //
-// Inside a block of the 16-row kernel: one warp starts TMA copies of the pages
-// (a lane a copy) into a ring of 64-key stages, two groups of 4 warps take the
+// Inside a block of the 16-row kernel: two warps copy K and V into a ring of
+// 64-key stages (16-byte cp.async: pages are small), two groups of 4 warps take the
 // block's pieces in turn, so that one group's epilogue and next queries run
 // under the other's products and the ring never waits for them.  Each warp owns 16
 // of a stage's 64 keys: every byte of K and V passes from shared memory to
@@ -30,8 +30,7 @@
 // work is a tenth of what the SM can do while it waits for memory.  Running
 // maximum and sum stay in fp32 registers; P is rounded to bf16 for the second
 // product (2^-9 of each weight at most, as in cp_attn_partial).  Keys past the
-// length are hidden by their index and their V rows zeroed, whatever the page
-// holds there.  Problems of more rows run in prefix_tc.cuh.
+// length are never copied (zeros in their place), whatever the page holds there.  Problems of more rows run in prefix_tc.cuh.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -118,8 +117,7 @@ __device__ __forceinline__ bool group_any(int group, bool v) {
 
 template <int D>
 __global__ void __launch_bounds__(kMmaThreads, 1)
-    prefix_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                      const PrefixArgs a) {
+    prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
     using C = MmaCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -131,13 +129,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     if (tid == 0) {
         *abort_flag = 0;
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(full + s, 2);
+            mbar_init(full + s, 64);
             mbar_init(empty + s, 4);
         }
         for (int i = 0; i < kGroups; ++i) mbar_init(go + i, 4);
         fence_mbar_init();
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
     }
     scan_line<kTM, kKT>(a, line, blockIdx.x == 0);
     long long t0, t1;
@@ -145,11 +141,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 
     if (warp < 2) {
         // -------------------------------------------------------- loads: K by warp 0, V by warp 1
-        // The copies are started by one lane in a loop over the tile's pages with
-        // uniform operands, about 30 cycles each; a lane for each page took 90,
-        // the instruction being issued lane after lane.
-        const CUtensorMap *map = warp ? &tmV : &tmK;
-        const int shift = a.own.shift, rows = min(kKT, 1 << shift);
+        const __nv_bfloat16 *cache = warp ? a.v : a.k;
+        const int shift = a.own.shift;
+        const uint32_t ring = smem_u32(smem) + warp * C::kTile;
         uint32_t it = 0;
         bool ok = true;
         for (long long t = t0; t < t1 && ok;) {
@@ -157,31 +151,16 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             t = x.next;
             if (x.k0 >= x.k1) continue;
             PageWindow win;
-            win.begin(a, x, static_cast<int>((x.k0 * kKT) >> shift), lane);
-            for (long long kt = x.k0; kt < x.k1; ++kt, ++it) {
-                const long long key = kt * kKT;
-                win.advance(static_cast<int>(key >> shift), lane);
-                const int n = static_cast<int>(min(static_cast<long long>(kKT), x.keys - key) + rows - 1) / rows;
+            win.begin(a, x, (x.k0 * kKT) >> shift, lane);
+            for (int kt = x.k0; kt < x.k1; ++kt, ++it) {
+                win.advance((kt * kKT) >> shift, lane);
                 const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
                 if (!mbar_wait_warp(empty + st, ph ^ 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
-                uint8_t *dst = smem + (st * 2 + warp) * C::kTile;
-                if (lane == 0) mbar_arrive_expect_tx(full + st, n * rows * 128 * C::kAtoms);
-                for (int i = 0; i < n; ++i) {
-                    const int row = win.row(a, key + i * rows);
-                    if (lane == 0)
-#pragma unroll
-                        for (int at = 0; at < C::kAtoms; ++at)
-                            tma_load_4d(dst + at * C::kAtom + i * rows * 128, map, full + st, 64 * at, x.kvh, row, 0);
-                }
+                copy_tile<D, kKT, C::kAtom>(a, x, win, cache, ring + st * 2 * C::kTile, kt * kKT, lane);
+                copies_arrive(full + st);
             }
         }
-        // let every copy already issued land before shared memory goes away
-        if (!ok && lane == 0) {
-            volatile int no_abort = 0;
-            for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
-                mbar_wait(full + i % C::kStages, (i / C::kStages) & 1u, &no_abort, 100000000ull);
-        }
-        __syncwarp();
+        copies_drain();  // also where a wait was given up: no copy may land after the block is gone
     } else {
         // -------------------------------------------------------- products
         const int group = (warp - 2) >> 2, w = (warp - 2) & 3, gtid = tid - 64 - group * 128;
@@ -216,10 +195,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     qf[kk][2 + h] = in ? __ldg(reinterpret_cast<const uint32_t *>(qp + kk * 16 + 8 + 2 * t4)) : 0u;
                 }
             }
-            const long long lim0 = x.row0 + g < x.rows ? min(x.keys, row_limit(a, x, x.row0 + g)) : 0;
-            const long long lim1 = x.row0 + g + 8 < x.rows ? min(x.keys, row_limit(a, x, x.row0 + g + 8)) : 0;
+            const int lim0 = x.row0 + g < x.rows ? row_limit(a, x, x.row0 + g) : 0;
+            const int lim1 = x.row0 + g + 8 < x.rows ? row_limit(a, x, x.row0 + g + 8) : 0;
             // tiles from the first that some row does not see whole on are masked
-            const long long whole = x.row0 + kTM <= x.rows ? min(x.keys, row_limit(a, x, x.row0)) : 0;
+            const int whole = x.row0 + kTM <= x.rows ? row_limit(a, x, x.row0) : 0;
             float o[D / 8][4];
 #pragma unroll
             for (int n = 0; n < D / 8; ++n)
@@ -229,23 +208,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             // the other group has used up the stages before these: a wait for a stage
             // is then never more than one of its phases ahead
             if (!first && !mbar_wait_warp(go + group, gone++ & 1u, abort_flag, a.timeout_ns)) ok = false;
-            for (long long kt = x.k0; kt < x.k1 && ok; ++kt, ++it) {
+            for (int kt = x.k0; kt < x.k1 && ok; ++kt, ++it) {
                 const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
                 if (!mbar_wait_warp(full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
                 const uint32_t ks = sbase + st * 2 * C::kTile, vs = ks + C::kTile;
                 const int key0 = w * 16;
-                const long long past = x.keys - kt * kKT - key0;  // keys of this warp's 16 that exist
-                if (past < 16) {
-                    // what lies behind the last key must not meet a product
-                    for (int i = lane; i < 16 * (D / 8); i += 32) {
-                        const int r = i / (D / 8);
-                        if (r >= past) {
-                            const uint32_t dst = tile_at_chunk<D>(vs, key0 + r, i % (D / 8));
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
-                        }
-                    }
-                    __syncwarp();
-                }
                 float s[2][4];
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
@@ -259,8 +226,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     mma16816(s[0], qf[kk], b[0], b[1]);
                     mma16816(s[1], qf[kk], b[2], b[3]);
                 }
-                const long long kb = kt * kKT + key0 + 2 * t4;
-                const bool masked = kt * kKT + kKT > whole;
+                const int kb = kt * kKT + key0 + 2 * t4;
+                const bool masked = whole - kt * kKT < kKT;
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -309,7 +276,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     mma16816(o[2 * n], pf, b[0], b[1]);
                     mma16816(o[2 * n + 1], pf, b[2], b[3]);
                 }
-                if (past < 16) fence_async_shared();  // the zeros before the next copy into the stage
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + st);
             }
@@ -639,22 +605,30 @@ cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
     std::call_once(once, [] {
         err = cudaFuncSetAttribute(prefix_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, MmaCfg<D>::kSmem);
         if (err == cudaSuccess)
-            err = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<D>::kSmem);
+            err = cudaFuncSetAttribute(prefix_tc_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       TcCfg<D>::kSmem);
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(prefix_tc_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       TcCfg<D>::kSmem);
     });
     if (err != cudaSuccess) return cuda_status(err);
+    const int sms = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
+    const int grid = sms / a.lanes * a.lanes;
+    if (!tc) {
+        prefix_mma_kernel<D><<<grid, kMmaThreads, MmaCfg<D>::kSmem, stream>>>(a);
+        return last_launch_status();
+    }
     const int64_t rows = static_cast<int64_t>(a.own.n_pages) << a.own.shift;
-    const int page = 1 << a.own.shift, tile = tc ? kTcKT : kKT, box = page < tile ? page : tile;
+    const int page = 1 << a.own.shift, box = page < kTcKT ? page : kTcKT;
     // at D = 64 a head's row is 128 bytes and its neighbour another head's
     const int l2 = D == 64 ? 128 : 256;
     CUtensorMap mk, mv;
     if (!make_map(&mk, a.k, D, a.Nkv, rows, 1, box, l2) || !make_map(&mv, a.v, D, a.Nkv, rows, 1, box, l2))
         return CP_ERR_CUDA;
-    const int sms = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
-    const int grid = sms / a.lanes * a.lanes;
-    if (tc)
-        prefix_tc_kernel<D><<<grid, kTcThreads, TcCfg<D>::kSmem, stream>>>(mk, mv, a);
+    if (page >= kTmaPage)
+        prefix_tc_kernel<D, true><<<grid, kTcThreads, TcCfg<D>::kSmem, stream>>>(mk, mv, a);
     else
-        prefix_mma_kernel<D><<<grid, kMmaThreads, MmaCfg<D>::kSmem, stream>>>(mk, mv, a);
+        prefix_tc_kernel<D, false><<<grid, kTcThreads, TcCfg<D>::kSmem, stream>>>(mk, mv, a);
     return last_launch_status();
 }
 

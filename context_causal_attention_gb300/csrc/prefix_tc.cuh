@@ -4,22 +4,22 @@
 // One block on an SM works through its share of the line (cp_prefix.cuh) with
 // 12 warps:
 //   warps 0, 2  loads of K and of V: the page numbers of 32 pages side by side in
-//               the lanes, the next 32 on their way; a copy (64 columns x a
-//               page's rows, 128-byte swizzle) for each page and column half
-//               into a ring of stages.  A page number out of range becomes a
-//               coordinate outside the tensor, which TMA fills with zeros.
+//               the lanes, the next 32 on their way; pages of 64 tokens or more
+//               by TMA (64 columns x a page's rows a copy), smaller ones by
+//               cp.async (cp_prefix.cuh), into a ring of stages.  A page number
+//               out of range becomes a coordinate outside the tensor, which TMA
+//               fills with zeros.
+//   warp 3      gathers Q: the rows of a tile are query heads of one KV head
+//               from one or many sequences (16-byte cp.async, swizzled)
 //   warp 1      tensor memory (512 columns: S0 | S1 | O0 | O1) and MMA issue:
 //               S_i = Q_i K^T, O_i += P_i V with P_i in tensor memory.
 //   warps 4-7   softmax of rows 0..127, warps 8-11 of rows 128..255: one thread
 //               a row, in the log2 domain with an integer running maximum that
 //               moves only when a tile's sum passes 2^64 (as in attn.cu).
-// The rows of a tile are query heads of the same KV head from one or many
-// sequences, so the softmax threads gather Q themselves (a thread its row, into
-// the swizzled layout) instead of TMA.  A tile of up to 128 rows leaves the
-// second half idle.  Keys past the problem's length lie in a page's tail or in
+// A tile of up to 128 rows leaves the second half idle.  Keys past the problem's length lie in a page's tail or in
 // pages that were not loaded: their scores become -inf, and their V rows are
-// zeroed in shared memory before the product reads them, so nothing that they
-// hold (NaN included) is multiplied.
+// zeros before the product reads them (zeroed in shared memory behind TMA, never
+// copied by cp.async), so nothing that they hold (NaN included) is multiplied.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -37,6 +37,9 @@ namespace {
 constexpr int kTcThreads = 384;
 constexpr int kTcTM = 256;  // rows of a tile
 constexpr int kTcKT = 128;  // keys of a stage
+// Pages of this many tokens or more are copied by TMA, smaller ones by cp.async
+// (see copy_tile).
+constexpr int kTmaPage = 64;
 
 template <int D>
 struct TcCfg {
@@ -67,10 +70,11 @@ __device__ __forceinline__ void hide_columns(int c0, int lim, uint32_t (&h)[64])
         if (c0 + c >= lim) h[c] = 0xff800000u;
 }
 
-template <int D>
+// tma: the pages are copied by TMA, else by cp.async.
+template <int D, bool tma>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const PrefixArgs a) {
+                     const __grid_constant__ PrefixArgs a) {
     using C = TcCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (tid == 0) {
         *abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + i, 4);
+            mbar_init(q_full + i, 32);
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 4);
             mbar_init(o_full + i, 1);
@@ -94,8 +98,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         mbar_init(drain, 1);
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(k_full + s, 1);
-            mbar_init(v_full + s, 1);
+            mbar_init(k_full + s, tma ? 1 : 32);
+            mbar_init(v_full + s, tma ? 1 : 32);
             mbar_init(k_empty + s, 1);
             mbar_init(v_empty + s, 1);
         }
@@ -129,13 +133,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             t = x.next;
             if (x.k0 >= x.k1) continue;
             PageWindow win;
-            win.begin(a, x, static_cast<int>((x.k0 * kTcKT) >> shift), lane);
-            for (long long kt = x.k0; kt < x.k1; ++kt, ++it) {
-                const long long key = kt * kTcKT;
-                win.advance(static_cast<int>(key >> shift), lane);
-                const int n = static_cast<int>(min(static_cast<long long>(kTcKT), x.keys - key) + rows - 1) / rows;
+            win.begin(a, x, (x.k0 * kTcKT) >> shift, lane);
+            for (int kt = x.k0; kt < x.k1; ++kt, ++it) {
+                const int key = kt * kTcKT;
+                win.advance(key >> shift, lane);
+                const int n = (min(kTcKT, x.keys - key) + rows - 1) / rows;
                 const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
                 if (!mbar_wait_warp(empty + st, ph ^ 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                if (!tma) {
+                    copy_tile<D, kTcKT, C::kAtom>(a, x, win, warp ? a.v : a.k, smem_u32(ring) + st * C::kTile, key, lane);
+                    copies_arrive(full + st);
+                    continue;
+                }
                 if (lane == 0) mbar_arrive_expect_tx(full + st, n * rows * 128 * C::kAtoms);
                 for (int i = 0; i < n; ++i) {
                     const int row = win.row(a, key + i * rows);
@@ -147,7 +156,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
         }
-        if (!ok && lane == 0) {
+        copies_drain();
+        if (!ok && tma && lane == 0) {
             // let every copy already issued land before shared memory goes away
             volatile int no_abort = 0;
             for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
@@ -169,7 +179,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // P V of the tile before `kv` for half i
             auto pv = [&](int i, int last, bool first_of_item, uint32_t acc) -> bool {
                 const uint32_t st = (kv - 1) % C::kStages, ph = ((kv - 1) / C::kStages) & 1u;
-                if (i == 0 && !mbar_wait(v_full + st, ph, abort_flag, a.timeout_ns)) return false;
+                if (i == 0) {
+                    if (!mbar_wait(v_full + st, ph, abort_flag, a.timeout_ns)) return false;
+                    if (!tma) fence_async_shared();  // written by cp.async, read by the tensor core
+                }
                 if (first_of_item && !mbar_wait(o_empty + i, (items[i] & 1u) ^ 1u, abort_flag, a.timeout_ns)) return false;
                 if (!mbar_wait(p_full + i, tiles[i] & 1u, abort_flag, a.timeout_ns)) return false;
                 tc_fence_after();
@@ -185,11 +198,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int last = x.rows - x.row0 > 128;  // the second half has rows
                 for (int i = 0; i <= last && ok; ++i) ok = mbar_wait(q_full + i, items[i] & 1u, abort_flag, a.timeout_ns);
                 if (!ok) break;
+                fence_async_shared();  // written by cp.async, read by the tensor core
                 tc_fence_after();
-                const long long n = x.k1 - x.k0;
-                for (long long j = 0; j < n && ok; ++j) {
+                const int n = x.k1 - x.k0;
+                for (int j = 0; j < n && ok; ++j) {
                     const uint32_t st = kv % C::kStages, ph = (kv / C::kStages) & 1u;
                     if (!mbar_wait(k_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
+                    if (!tma) fence_async_shared();
                     tc_fence_after();
                     for (int i = 0; i <= last; ++i) {
                         if (j > 0 && !pv(i, last, j == 1, j > 1)) { ok = false; break; }
@@ -212,6 +227,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_wait(drain, 0, &no_abort, 100000000ull);
         }
         __syncwarp();
+    } else if (warp == 3) {
+        // -------------------------------------------------------- Q: rows gathered, swizzled as TMA would
+        uint32_t items[2] = {0, 0};
+        bool ok = true;
+        for (long long t = t0; t < t1 && ok;) {
+            const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
+            t = x.next;
+            if (x.k0 >= x.k1) continue;
+            for (int i = 0; i < 2 && x.row0 + i * 128 < x.rows; ++i) {
+                // the products of the half's last item have read its tile
+                if (items[i] && !mbar_wait_warp(o_full + i, (items[i] - 1) & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                constexpr int kChunks = D / 8, kRpi = 32 / kChunks;  // 16-byte chunks of a row, rows of an instruction
+                const int c = lane % kChunks, r0 = lane / kChunks;
+                const uint32_t dst = smem_u32(sQ) + i * C::kTile + (c >> 3) * C::kAtom + r0 * 128;
+                for (int g = 0; g < 4; ++g) {
+                    // element offset of row 32 g + lane, handed to the lanes that copy it
+                    const int row = x.row0 + i * 128 + 32 * g + lane, tok = row / a.G;
+                    const long long mine =
+                        row < x.rows ? (static_cast<long long>(x.tok0 + tok) * a.N + x.kvh * a.G + row - tok * a.G) * D : -1;
+#pragma unroll 8
+                    for (int j = 0; j < 32 / kRpi; ++j) {
+                        const long long at = __shfl_sync(0xffffffffu, mine, j * kRpi + r0);
+                        const uint32_t to = dst + (32 * g + j * kRpi) * 128 + (((c & 7) ^ ((j * kRpi + r0) & 7)) << 4);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                                     "l"(a.q + (at < 0 ? 0 : at + c * 8)), "r"(at < 0 ? 0 : 16)
+                                     : "memory");
+                    }
+                }
+                copies_arrive(q_full + i);
+                ++items[i];
+            }
+        }
+        copies_drain();
     } else if (warp >= 4) {
         // -------------------------------------------------------- softmax
         const int half = (warp - 4) >> 2, in_tile = (warp & 3) * 32 + lane;
@@ -235,28 +283,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 kv += static_cast<uint32_t>(x.k1 - x.k0);
                 continue;  // no rows in this half
             }
-            // this thread's row of Q, swizzled as TMA would (the last item's products have all read the tile: o_full)
-            {
-                const int tok = valid ? row / a.G : 0;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    a.q + (static_cast<long long>(x.tok0 + tok) * a.N + x.kvh * a.G + (valid ? row - tok * a.G : 0)) * D);
-                uint8_t *dst = sQ + half * C::kTile + in_tile * 128;
-                uint4 v[D / 8];
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) v[c] = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kAtom + (((c & 7) ^ (in_tile & 7)) << 4)) = v[c];
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full + half);
-            }
-            const long long limit = valid ? min(x.keys, row_limit(a, x, row)) : x.keys;
-            const long long whole = min(x.keys, row_limit(a, x, x.row0 + half * 128));  // seen by every row
+            // counted from the current tile: keys of the problem, that this row sees, that all rows see
+            int past = x.keys - x.k0 * 128, limit = (valid ? row_limit(a, x, row) : x.keys) - x.k0 * 128;
+            int whole = row_limit(a, x, x.row0 + half * 128) - x.k0 * 128;
             float m_run = -INFINITY, l_run = 0.f;
-            for (long long kt = x.k0; kt < x.k1; ++kt, ++kv, ++tiles) {
-                const long long past = x.keys - kt * 128;
-                if (half == 0 && past < 128) {
+            for (int n = x.k1 - x.k0; n > 0; --n, ++kv, ++tiles, past -= 128, limit -= 128, whole -= 128) {
+                if (tma && half == 0 && past < 128) {
                     const uint32_t st = kv % C::kStages, ph = (kv / C::kStages) & 1u;
                     if (!mbar_wait_warp(v_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
                     if (in_tile >= past) {
@@ -269,8 +301,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 if (!mbar_wait_warp(s_full + half, tiles & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
                 tc_fence_after();
-                const bool mask = kt * 128 + 128 > whole;
-                const int lim = static_cast<int>(min(128ll, max(0ll, limit - kt * 128)));
+                const bool mask = whole < 128;
+                const int lim = limit;
                 uint32_t sa[64], sb[64], pa[32], pb[32];
                 tmem_ld64_nowait(tS, sa);
                 tmem_wait_ld(sa);
