@@ -16,10 +16,15 @@
 //   warps 4-7   softmax of rows 0..127, warps 8-11 of rows 128..255: one thread
 //               a row, in the log2 domain with an integer running maximum that
 //               moves only when a tile's sum passes 2^64 (as in attn.cu).
-// A tile of up to 128 rows leaves the second half idle.  Keys past the problem's length lie in a page's tail or in
-// pages that were not loaded: their scores become -inf, and their V rows are
-// zeros before the product reads them (zeroed in shared memory behind TMA, never
-// copied by cp.async), so nothing that they hold (NaN included) is multiplied.
+// The two halves keep the tensor cores and the exponentials busy in turn.  In a
+// tile of up to 128 rows both hold the same rows and take the key tiles in turn;
+// the first half joins the two results at the end (with one half alone the scores,
+// the exponentials and the second product of a tile follow one another: 35 rows
+// ran at half of this speed).
+// Keys past the problem's length lie in a page's tail or in pages that were not
+// loaded: their scores become -inf, and their V rows are zeros before the product
+// reads them (zeroed in shared memory behind TMA, never copied by cp.async), so
+// nothing that they hold (NaN included) is multiplied.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -52,10 +57,11 @@ struct TcCfg {
     static constexpr int kOffV = kOffK + kStages * kTile;
     static constexpr int kOffLine = kOffV + kStages * kTile;
     static constexpr int kOffBar = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
-    // q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain, k_full[S], v_full[S], k_empty[S], v_empty[S]
-    static constexpr int kBars = 11 + 4 * kStages;
+    // q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain, ml_full, k_full[S], v_full[S], k_empty[S], v_empty[S]
+    static constexpr int kBars = 12 + 4 * kStages;
     static constexpr int kOffMisc = kOffBar + kBars * 8;
-    static constexpr int kSmem = kOffMisc + 16 + 1024;  // + alignment slack
+    static constexpr int kOffMl = kOffMisc + 16;        // [128] (m, l) of the second half
+    static constexpr int kSmem = kOffMl + 128 * 8 + 1024;  // + alignment slack
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -82,7 +88,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Line &line = *reinterpret_cast<Line *>(smem + C::kOffLine);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *q_full = bar, *s_full = bar + 2, *p_full = bar + 4, *o_full = bar + 6, *o_empty = bar + 8;
-    uint64_t *drain = bar + 10, *k_full = bar + 11, *v_full = k_full + C::kStages, *k_empty = v_full + C::kStages,
+    uint64_t *drain = bar + 10, *ml_full = bar + 11, *k_full = bar + 12, *v_full = k_full + C::kStages, *k_empty = v_full + C::kStages,
              *v_empty = k_empty + C::kStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
@@ -97,6 +103,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(o_empty + i, 4);
         }
         mbar_init(drain, 1);
+        mbar_init(ml_full, 4);
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(k_full + s, tma ? 1 : 32);
             mbar_init(v_full + s, tma ? 1 : 32);
@@ -174,51 +181,81 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
             const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), C::kAtom, 1024);
             constexpr uint64_t kStageDesc = C::kTile >> 4;
-            uint32_t kv = 0, items[2] = {0, 0}, tiles[2] = {0, 0};
+            uint32_t kv = 0, items[2] = {0, 0}, tiles[2] = {0, 0}, queries[2] = {0, 0};
             bool ok = true;
-            // P V of the tile before `kv` for half i
-            auto pv = [&](int i, int last, bool first_of_item, uint32_t acc) -> bool {
-                const uint32_t st = (kv - 1) % C::kStages, ph = ((kv - 1) / C::kStages) & 1u;
-                if (i == 0) {
+            // S_i = Q K^T of the tile in K stage st
+            auto qk = [&](int i, uint64_t dq, uint32_t st) {
+                umma_qk_group<D / 16>(tmem + i * 128, dq, dk0 + st * kStageDesc, kIdescQK);
+                umma_commit(s_full + i);
+            };
+            // O_i (+)= P_i V of tile `at`; the tile's V is awaited with `await`, given back with `release`
+            auto pv = [&](int i, uint32_t at, bool await, bool release, bool first) -> bool {
+                const uint32_t st = at % C::kStages, ph = (at / C::kStages) & 1u;
+                if (await) {
                     if (!mbar_wait(v_full + st, ph, abort_flag, a.timeout_ns)) return false;
                     if (!tma) fence_async_shared();  // written by cp.async, read by the tensor core
                 }
-                if (first_of_item && !mbar_wait(o_empty + i, (items[i] & 1u) ^ 1u, abort_flag, a.timeout_ns)) return false;
+                if (first && !mbar_wait(o_empty + i, (items[i] & 1u) ^ 1u, abort_flag, a.timeout_ns)) return false;
                 if (!mbar_wait(p_full + i, tiles[i] & 1u, abort_flag, a.timeout_ns)) return false;
                 tc_fence_after();
                 ++tiles[i];
-                umma_pv_group(tmem + 256 + i * D, tmem + i * 128 + 64, dv0 + st * kStageDesc, kIdescPV, acc);
-                if (i == last) umma_commit(v_empty + st);
+                umma_pv_group(tmem + 256 + i * D, tmem + i * 128 + 64, dv0 + st * kStageDesc, kIdescPV, first ? 0u : 1u);
+                if (release) umma_commit(v_empty + st);
+                return true;
+            };
+            auto k_wait = [&]() -> bool {
+                if (!mbar_wait(k_full + kv % C::kStages, (kv / C::kStages) & 1u, abort_flag, a.timeout_ns)) return false;
+                if (!tma) fence_async_shared();
+                tc_fence_after();
                 return true;
             };
             for (long long t = t0; t < t1 && ok;) {
                 const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
                 t = x.next;
-                if (x.k0 >= x.k1) continue;
-                const int last = x.rows - x.row0 > 128;  // the second half has rows
-                for (int i = 0; i <= last && ok; ++i) ok = mbar_wait(q_full + i, items[i] & 1u, abort_flag, a.timeout_ns);
+                const int n = x.k1 - x.k0;
+                if (n <= 0) continue;
+                const bool paired = x.rows - x.row0 <= 128;
+                for (int i = 0; i < (paired ? 1 : 2) && ok; ++i)
+                    ok = mbar_wait(q_full + i, queries[i]++ & 1u, abort_flag, a.timeout_ns);
                 if (!ok) break;
                 fence_async_shared();  // written by cp.async, read by the tensor core
                 tc_fence_after();
-                const int n = x.k1 - x.k0;
-                for (int j = 0; j < n && ok; ++j) {
-                    const uint32_t st = kv % C::kStages, ph = (kv / C::kStages) & 1u;
-                    if (!mbar_wait(k_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
-                    if (!tma) fence_async_shared();
-                    tc_fence_after();
-                    for (int i = 0; i <= last; ++i) {
-                        if (j > 0 && !pv(i, last, j == 1, j > 1)) { ok = false; break; }
-                        umma_qk_group<D / 16>(tmem + i * 128, i ? dq1 : dq0, dk0 + st * kStageDesc, kIdescQK);
-                        umma_commit(s_full + i);
+                if (paired) {
+                    // tile j belongs to half j & 1; its weights are used when tile j + 2 comes
+                    for (int j = 0; j < n + 2 && ok; ++j) {
+                        const int i = j & 1;
+                        if (j >= 2) {
+                            ok = pv(i, kv - (j < n ? 2 : n + 2 - j), true, true, j < 4);
+                            if (ok && j >= n) {
+                                umma_commit(o_full + i);
+                                ++items[i];
+                            }
+                        }
+                        if (j < n && ok && (ok = k_wait())) {
+                            const uint32_t st = kv % C::kStages;
+                            qk(i, dq0, st);
+                            umma_commit(k_empty + st);
+                            ++kv;
+                        }
+                        if (n == 1) ++j;  // no tile for the second half
                     }
-                    if (!ok) break;
-                    umma_commit(k_empty + st);
-                    ++kv;
-                }
-                for (int i = 0; i <= last && ok; ++i) {
-                    if (!pv(i, last, n == 1, n > 1)) { ok = false; break; }
-                    umma_commit(o_full + i);
-                    ++items[i];
+                } else {
+                    for (int j = 0; j < n && ok; ++j) {
+                        if (!k_wait()) { ok = false; break; }
+                        const uint32_t st = kv % C::kStages;
+                        for (int i = 0; i < 2 && ok; ++i) {
+                            if (j > 0 && !pv(i, kv - 1, i == 0, i == 1, j == 1)) { ok = false; break; }
+                            qk(i, i ? dq1 : dq0, st);
+                        }
+                        if (!ok) break;
+                        umma_commit(k_empty + st);
+                        ++kv;
+                    }
+                    for (int i = 0; i < 2 && ok; ++i) {
+                        if (!pv(i, kv - 1, i == 0, i == 1, n == 1)) { ok = false; break; }
+                        umma_commit(o_full + i);
+                        ++items[i];
+                    }
                 }
             }
             // no MMA may still be running when tensor memory is released
@@ -229,15 +266,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
     } else if (warp == 3) {
         // -------------------------------------------------------- Q: rows gathered, swizzled as TMA would
-        uint32_t items[2] = {0, 0};
-        bool ok = true;
-        for (long long t = t0; t < t1 && ok;) {
+        uint32_t items = 0;
+        for (long long t = t0; t < t1;) {
             const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
             t = x.next;
             if (x.k0 >= x.k1) continue;
+            // the last item's scores have all been computed (o_full[0] is committed after the last of them)
+            if (items && !mbar_wait_warp(o_full, (items - 1) & 1u, abort_flag, a.timeout_ns)) break;
+            ++items;
             for (int i = 0; i < 2 && x.row0 + i * 128 < x.rows; ++i) {
-                // the products of the half's last item have read its tile
-                if (items[i] && !mbar_wait_warp(o_full + i, (items[i] - 1) & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
                 constexpr int kChunks = D / 8, kRpi = 32 / kChunks;  // 16-byte chunks of a row, rows of an instruction
                 const int c = lane % kChunks, r0 = lane / kChunks;
                 const uint32_t dst = smem_u32(sQ) + i * C::kTile + (c >> 3) * C::kAtom + r0 * 128;
@@ -256,7 +293,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 }
                 copies_arrive(q_full + i);
-                ++items[i];
             }
         }
         copies_drain();
@@ -266,30 +302,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + half * 128, tO = tmem + lane_off + 256 + half * D;
         const float sl2 = a.scale_log2;
-        uint32_t tiles = 0, items = 0, kv = 0;
+        float2 *ml_s = reinterpret_cast<float2 *>(smem + C::kOffMl);
+        uint32_t tiles = 0, items = 0, kv = 0, joins = 0, other = 0;  // other: items of the other half
         bool ok = true;
         for (long long t = t0; t < t1 && ok;) {
             const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
-            const int row = x.row0 + half * 128 + in_tile;
-            const bool valid = row < x.rows;
-            const bool write = valid && x.slot >= 0;
-            if (x.slot < 0 && in_tile == 0) report(a.status, CP_ERR_PAGE);
             t = x.next;
-            if (x.k0 >= x.k1) {
-                if (write) a.slot_ml[static_cast<long long>(x.slot) * kTcTM + half * 128 + in_tile] = make_float2(-INFINITY, 0.f);
+            // up to 128 rows: both halves hold the same rows, tile j of the piece is half j & 1's
+            const bool paired = x.rows - x.row0 <= 128;
+            const int first_row = x.row0 + (paired ? 0 : half * 128), row = first_row + in_tile, all = x.k1 - x.k0;
+            const bool valid = row < x.rows, write = valid && x.slot >= 0 && !(paired && half);
+            const long long at = static_cast<long long>(max(x.slot, 0)) * kTcTM + row - x.row0;
+            if (x.slot < 0 && in_tile == 0) report(a.status, CP_ERR_PAGE);
+            if (all <= 0) {
+                if (write) a.slot_ml[at] = make_float2(-INFINITY, 0.f);
                 continue;
             }
-            if (x.row0 + half * 128 >= x.rows) {
-                kv += static_cast<uint32_t>(x.k1 - x.k0);
-                continue;  // no rows in this half
-            }
+            const int begin = paired ? half : 0, step = paired ? 2 : 1;
+            uint32_t tile = kv + begin;
+            kv += all;
+            if (begin >= all) continue;  // one tile: nothing for the second half
             // counted from the current tile: keys of the problem, that this row sees, that all rows see
-            int past = x.keys - x.k0 * 128, limit = (valid ? row_limit(a, x, row) : x.keys) - x.k0 * 128;
-            int whole = row_limit(a, x, x.row0 + half * 128) - x.k0 * 128;
+            int past = x.keys - (x.k0 + begin) * 128;
+            int limit = (valid ? row_limit(a, x, row) : x.keys) - (x.k0 + begin) * 128;
+            int whole = row_limit(a, x, first_row) - (x.k0 + begin) * 128;
             float m_run = -INFINITY, l_run = 0.f;
-            for (int n = x.k1 - x.k0; n > 0; --n, ++kv, ++tiles, past -= 128, limit -= 128, whole -= 128) {
-                if (tma && half == 0 && past < 128) {
-                    const uint32_t st = kv % C::kStages, ph = (kv / C::kStages) & 1u;
+            for (int n = begin; n < all; n += step, tile += step, ++tiles, past -= 128 * step, limit -= 128 * step,
+                     whole -= 128 * step) {
+                if (tma && (paired || half == 0) && past < 128) {
+                    const uint32_t st = tile % C::kStages, ph = (tile / C::kStages) & 1u;
                     if (!mbar_wait_warp(v_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
                     if (in_tile >= past) {
                         uint8_t *dst = sV + st * C::kTile + in_tile * 128;
@@ -360,27 +401,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok || !mbar_wait_warp(o_full + half, items & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
             tc_fence_after();
             ++items;
-            uint32_t ov[D / 32][32];
+            if (paired && half) {
+                // the first half joins the two; this thread's row is the same lane of tensor memory there
+                ml_s[in_tile] = make_float2(m_run, l_run);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_full);
+                continue;
+            }
+            const bool join = paired && all > 1;
+            float f0 = 1.f, f1 = 0.f;
+            if (join) {
+                if (!mbar_wait_warp(ml_full, joins++ & 1u, abort_flag, a.timeout_ns) ||
+                    !mbar_wait_warp(o_full + 1, other & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                tc_fence_after();
+                const float2 other = ml_s[in_tile];
+                const float m = fmaxf(m_run, other.x);
+                f0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m);
+                f1 = other.x == -INFINITY ? 0.f : fast_exp2(other.x - m);
+                l_run = f0 * l_run + f1 * other.y;
+                m_run = m;
+            }
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) tmem_ld32_nowait(tO + 32 * c, ov[c]);
+            for (int c = 0; c < D; c += 32) {
+                uint32_t ov[32], ow[32];
+                tmem_ld32(tO + c, ov);
+                if (join) {
+                    tmem_ld32(tO + D + c, ow);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) tmem_wait_ld32(ov[c]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(o_empty + half);
-            if (write) {
-                const long long at = static_cast<long long>(x.slot) * kTcTM + half * 128 + in_tile;
-                float *dst = a.slot_o + at * D;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c)
+                    for (int e = 0; e < 32; ++e)
+                        ov[e] = __float_as_uint(f0 * __uint_as_float(ov[e]) + f1 * __uint_as_float(ow[e]));
+                }
+                if (c + 32 == D) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(o_empty + half);
+                    if (lane == 0 && join) mbar_arrive(o_empty + 1);
+                }
+                if (write) {
+                    float *dst = a.slot_o + at * D + c;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
-                        st_global_v8(dst + 32 * c + e, __uint_as_float(ov[c][e]), __uint_as_float(ov[c][e + 1]),
-                                     __uint_as_float(ov[c][e + 2]), __uint_as_float(ov[c][e + 3]),
-                                     __uint_as_float(ov[c][e + 4]), __uint_as_float(ov[c][e + 5]),
-                                     __uint_as_float(ov[c][e + 6]), __uint_as_float(ov[c][e + 7]));
-                a.slot_ml[at] = make_float2(m_run, l_run);
+                        st_global_v8(dst + e, __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
+                                     __uint_as_float(ov[e + 3]), __uint_as_float(ov[e + 4]), __uint_as_float(ov[e + 5]),
+                                     __uint_as_float(ov[e + 6]), __uint_as_float(ov[e + 7]));
+                }
             }
+            if (write) a.slot_ml[at] = make_float2(m_run, l_run);
+            if (!paired || join) ++other;
         }
     }
 

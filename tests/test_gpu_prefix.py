@@ -89,6 +89,9 @@ CASES = {
     "empty_sequences": ([0, 1, 0, 0], [0, 9, 300, 0], 70, 4, 2, 64, 16, 2),
     "prompts": ([150, 1, 64, 33], [150, 40, 264, 33], 300, 8, 2, 128, 64, 5),
     "many": ([1] * 300, list(range(1, 301)), 200, 4, 2, 64, 16, 0),
+    "half_tile": ([5, 5], [5, 9], 100, 8, 2, 64, 16, 0),
+    "half_tile_long": ([6, 1], [70, 2900], 5000, 24, 3, 128, 64, 0),
+    "half_tiles_mixed": ([70, 20, 1, 90], [900, 20, 333, 1200], 400, 16, 4, 64, 32, 3),
     "long": ([1, 2], [3000, 9000], 20000, 8, 2, 128, 64, 0),
 }
 
