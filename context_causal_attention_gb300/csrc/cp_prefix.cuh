@@ -10,8 +10,8 @@
 //
 // The KV heads of a token lie side by side in memory, and their work is the
 // same, so blocks that run side by side take the same stretch of the line for
-// neighbouring heads: block x is worker x / lanes of lane x % lanes, and the line
-// of a lane holds heads lane, lane + lanes, ...  (a.heads of them).
+// neighbouring heads: block (x, y) is worker y of lane x, and the line of a lane
+// holds heads lane, lane + lanes, ...  (a.heads of them).
 //
 // The row tiles of a causal problem need fewer keys than its length: a stretch
 // [n0, n1) of an item of nominal length T that needs K tiles stands for tiles
@@ -25,6 +25,7 @@
 
 #include "cp_paged.cuh"
 #include "cp_ptx.cuh"
+#include "cp_sched.cuh"
 
 namespace cpattn {
 
@@ -33,6 +34,7 @@ struct PrefixArgs {
     PageTable own, pre;  // the sequences' pages; the prefix as a table of one row
     const int32_t *cu, *kv_len;
     int R, B, N, Nkv, G;
+    FastDiv div_g;              // by G
     long long P;
     float scale_log2;
     int lanes, heads;           // Nkv = lanes x heads
@@ -189,10 +191,9 @@ __device__ __forceinline__ long long div_floor(long long a, long long b) {
 // A block's share of its lane's line; false if it has none.
 __device__ __forceinline__ bool share_of(const PrefixArgs &a, const Line &line, long long *t0, long long *t1) {
     const long long total = line.tile[kRuns];
-    const int workers = gridDim.x / a.lanes;
-    const long long share = max(1ll, div_floor(total + workers - 1, workers));
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = share;
-    *t0 = share * (blockIdx.x / a.lanes);
+    const long long share = max(1ll, div_floor(total + gridDim.y - 1, gridDim.y));
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.head[0] = share;
+    *t0 = share * blockIdx.y;
     *t1 = min(*t0 + share, total);
     return *t0 < *t1;
 }
@@ -206,69 +207,107 @@ struct Piece {
     int keys;             // keys of the problem
     int off;              // rows of token i see keys [0, off + i] (prefix: all)
     int k0, k1;           // key tiles [k0, k1), may be none
-    long long next;       // where the next piece begins on the line
 };
 
 // Keys that row `row` of the problem sees: [0, limit).
 __device__ __forceinline__ int row_limit(const PrefixArgs &a, const Piece &x, int row) {
-    return x.b < 0 ? x.keys : min(x.keys, max(0, x.off + row / a.G + 1));
+    return x.b < 0 ? x.keys
+                   : min(x.keys, max(0, x.off + static_cast<int>(fdiv(static_cast<uint32_t>(row), a.div_g)) + 1));
 }
 
-// The piece that begins at place t of the line (t < end), cut at `end`.
+// Where a block's share begins: the item and the place in it.
+struct Start {
+    int b, pass, w, item;  // problem, head of the lane, row tile's place, index on the line
+    long long n0;
+};
+
+// Finds the place t of the line.  By one whole warp; the caller shares `s`.
 template <int TM, int KT>
-__device__ __forceinline__ Piece find_piece(const PrefixArgs &a, const Line &line, long long t, long long end) {
-    Piece x;
+__device__ __forceinline__ void find_start(const PrefixArgs &a, const Line &line, long long t, Start *s) {
+    const int lane = threadIdx.x & 31;
+    // runs that begin at or before t (their beginnings do not go back)
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kRuns / 32; ++i) n += line.tile[lane * (kRuns / 32) + i] <= t;
+    const int lo = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n))) - 1;
+    if (lane) return;
     Problem p;
     long long base = 0;
-    int item = 0;
+    int item = 0, b = -1;
     if (t < line.tile[0]) {
         p = prefix_problem<TM, KT>(a, line);
-        x.b = -1;
     } else {
-        // the run that holds t: the last entry with tile <= t
-        int lo = 0, hi = kRuns - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (line.tile[mid] <= t) lo = mid; else hi = mid - 1;
-        }
         base = line.tile[lo];
         item = line.item[lo];
-        int b = lo * ((a.B + kRuns - 1) / kRuns);
-        for (; b < a.B; ++b) {
+        const int run = (a.B + kRuns - 1) / kRuns;
+        for (b = lo * run; b < a.B; ++b) {
             p = sequence_problem<TM, KT>(a, line, b);
             const long long all = static_cast<long long>(a.heads) * p.row_tiles * p.key_tiles;
             if (t < base + all) break;
             base += all;
             item += a.heads * p.row_tiles;
         }
-        x.b = b;
-        if (b >= a.B) {
-            // only when the lists were changed under the launch: a stretch without work
-            x = Piece{};
-            x.slot = -1;
-            x.next = end;
-            return x;
-        }
     }
+    s->b = b;
+    if (b >= a.B) return;  // only when the lists were changed under the launch
     const long long at = t - base, which = div_floor(at, p.key_tiles);
-    const int pass = static_cast<int>(div_floor(which, p.row_tiles)), lane = blockIdx.x % a.lanes;
-    const int j = tile_at(static_cast<int>(which - static_cast<long long>(pass) * p.row_tiles), p.row_tiles);
-    const int slot = item + static_cast<int>(which) + static_cast<int>(blockIdx.x / a.lanes);
-    x.kvh = pass * a.lanes + lane;
-    x.slot = slot < a.slots ? lane * a.slots + slot : -1;
-    x.row0 = j * TM;
-    x.tok0 = p.tok0;
-    x.rows = p.n * a.G;
-    x.keys = static_cast<int>(p.keys);
-    x.off = x.keys - p.n;
-    const long long n0 = at - which * p.key_tiles;
-    const long long n1 = min(n0 + (end - t), p.key_tiles);
-    const long long need = (static_cast<long long>(row_limit(a, x, min(x.row0 + TM, x.rows) - 1)) + KT - 1) / KT;
-    x.k0 = static_cast<int>(need == p.key_tiles ? n0 : n0 * need / p.key_tiles);
-    x.k1 = static_cast<int>(need == p.key_tiles ? n1 : n1 * need / p.key_tiles);
-    x.next = t + (n1 - n0);
-    return x;
+    s->pass = static_cast<int>(div_floor(which, p.row_tiles));
+    s->w = static_cast<int>(which - static_cast<long long>(s->pass) * p.row_tiles);
+    s->item = item + static_cast<int>(which);
+    s->n0 = at - which * p.key_tiles;
 }
+
+// Walks a block's pieces.  Every role of a kernel walks for itself, from the
+// block's Start; a step is a few additions.
+template <int TM, int KT>
+struct Walk {
+    Problem p;
+    Start s;
+    long long left;  // nominal tiles of the share that are left
+    __device__ __forceinline__ Walk(const PrefixArgs &a, const Line &line, const Start &start, long long share)
+        : s(start), left(share) {
+        if (s.b >= a.B) left = 0;
+        else p = s.b < 0 ? prefix_problem<TM, KT>(a, line) : sequence_problem<TM, KT>(a, line, s.b);
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ Piece next(const PrefixArgs &a, const Line &line) {
+        Piece x;
+        const int lane = blockIdx.x, slot = s.item + static_cast<int>(blockIdx.y);
+        x.b = s.b;
+        x.kvh = s.pass * a.lanes + lane;
+        x.slot = slot < a.slots ? lane * a.slots + slot : -1;
+        x.row0 = tile_at(s.w, p.row_tiles) * TM;
+        x.tok0 = p.tok0;
+        x.rows = p.n * a.G;
+        x.keys = static_cast<int>(p.keys);
+        x.off = x.keys - p.n;
+        const long long n1 = min(s.n0 + left, p.key_tiles);
+        const long long need = (static_cast<long long>(row_limit(a, x, min(x.row0 + TM, x.rows) - 1)) + KT - 1) / KT;
+        // the part [n0, n1) of the nominal length, scaled to the tiles that the rows need
+        x.k0 = static_cast<int>(s.n0 == 0 || need == p.key_tiles ? min(s.n0, need) : s.n0 * need / p.key_tiles);
+        x.k1 = static_cast<int>(n1 == p.key_tiles || need == p.key_tiles ? min(n1, need) : n1 * need / p.key_tiles);
+        left -= n1 - s.n0;
+        s.n0 = 0;
+        ++s.item;
+        if (++s.w == p.row_tiles) {
+            s.w = 0;
+            if (++s.pass == a.heads) {
+                s.pass = 0;
+                // the next problem with work; the prefix comes before sequence 0
+                while (left > 0) {
+                    if (++s.b >= a.B) {
+                        left = 0;  // only when the lists were changed under the launch
+                        break;
+                    }
+                    p = sequence_problem<TM, KT>(a, line, s.b);
+                    if (p.row_tiles > 0 && p.key_tiles > 0) break;
+                    s.item += a.heads * p.row_tiles;
+                }
+            }
+        }
+        return x;
+    }
+};
 
 // The page numbers of a piece, for the warp that starts its copies: 32 entries
 // of the page list side by side in the lanes and the next 32 on their way, so no
@@ -298,6 +337,18 @@ struct PageWindow {
             next = fetch(base + 32, lane);
         }
     }
+    // Cache row of each lane's key `key` (of an entry in the window), -1 for a key
+    // past the last or a page number out of range.  Warp-wide.
+    __device__ __forceinline__ int rows16(const PrefixArgs &a, int key, int keys) const {
+        const int e = key >> shift;
+        const int page = __shfl_sync(0xffffffffu, cur, (e - base) & 31);
+        if (key >= keys) return -1;
+        if (page < 0 || page >= n_pages) {
+            report(a.status, CP_ERR_PAGE);
+            return -1;
+        }
+        return (page << shift) + (key & ((1 << shift) - 1));
+    }
     // Cache row of key `key` (uniform over the warp, of an entry in the window:
     // 32 is a multiple of a tile's pages, and the window began at a tile's
     // first); the row after the last page for a page number out of range.
@@ -312,6 +363,17 @@ struct PageWindow {
     }
 };
 
+// Rows kI, kI + kRpi, ... up to 16 of a group, whole (kRpi rows an instruction).
+template <int kRpi, int kI>
+__device__ __forceinline__ void copy_rows(uint32_t at, uint32_t sw, const char *src, long long step) {
+    if constexpr (kI < 16) {
+        asm volatile("cp.async.cg.shared.global [%0 + %2], [%1], 16;" ::"r"(at + (sw ^ ((kI & 7) << 4))), "l"(src),
+                     "n"(kI * 128)
+                     : "memory");
+        copy_rows<kRpi, kI + kRpi>(at, sw, src + step, step);
+    }
+}
+
 // Starts the copies of one tile of KT keys of a piece (K or V) into shared
 // memory, 64-column atoms of kAtom bytes, rows of 128 bytes, 128-byte swizzle, by
 // one warp with 16-byte cp.async: a warp instruction moves whole head rows of D
@@ -319,26 +381,34 @@ struct PageWindow {
 // filled with zeros.  TMA tiles of a small page are slower: a copy of 16 rows of
 // 128 bytes holds the TMA unit for about 90 cycles, which ends at 3.4 TB/s over
 // the GPU with two issuing warps and 4.4 with four, where this reaches 5.9.
-template <int D, int KT, int kAtom>
+// (The loop over 16-row groups is not unrolled: a block copies few tiles, and code
+// that is read for the first time costs more than the loop.)
+template <int D, int KT, int kAtom>  // KT: a multiple of 16, here also a part of a tile
 __device__ __forceinline__ void copy_tile(const PrefixArgs &a, const Piece &x, const PageWindow &win,
                                           const __nv_bfloat16 *cache, uint32_t dst, int key0, int lane) {
     constexpr int kChunks = D / 8, kRpi = 32 / kChunks;  // 16-byte chunks of a row, rows of an instruction
     const int r = lane / kChunks, c = lane % kChunks;
-    const long long step = static_cast<long long>(kRpi) * a.Nkv * D;
-    const uint32_t lane_dst = dst + (c >> 3) * kAtom + r * 128, sw = ((c & 7) ^ r) << 4;
-#pragma unroll
-    for (int g = 0; g < KT / 16; ++g) {
-        const int key = key0 + 16 * g, left = min(16, x.keys - key);
-        const int row = left > 0 ? win.row(a, key) : 0;
-        const bool there = row < win.n_pages << win.shift;  // else a bad page: zeros
-        const __nv_bfloat16 *src =
-            cache + ((static_cast<long long>(there ? row + r : 0)) * a.Nkv + x.kvh) * D + c * 8;
-#pragma unroll
-        for (int i = 0; i < 16 / kRpi; ++i) {
-            const int n = there && i * kRpi + r < left ? 16 : 0;
-            const uint32_t at = lane_dst + (16 * g + i * kRpi) * 128 + (sw ^ (((i * kRpi) & 7) << 4));
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(n ? src + i * step : cache), "r"(n)
-                         : "memory");
+    const long long row_bytes = static_cast<long long>(a.Nkv) * D * 2, step = kRpi * row_bytes;
+    const char *lane_src = reinterpret_cast<const char *>(cache) + r * row_bytes + (x.kvh * D + c * 8) * 2;
+    uint32_t at = dst + (c >> 3) * kAtom + r * 128;
+    const uint32_t sw = ((c & 7) ^ r) << 4;
+    // lane g looks up the rows 16 g .. 16 g + 15: where they begin, -1 for none (a bad page or no keys)
+    const int mine = win.rows16(a, key0 + 16 * (lane % (KT / 16)), x.keys);
+#pragma unroll 2
+    for (int g = 0; g < KT / 16; ++g, at += 16 * 128) {
+        const int left = x.keys - key0 - 16 * g, row = __shfl_sync(0xffffffffu, mine, g);
+        const bool there = row >= 0;
+        const char *src = lane_src + (there ? row : 0) * row_bytes;
+        if (there && left >= 16) {
+            copy_rows<kRpi, 0>(at, sw, src, step);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 16; i += kRpi, src += step) {
+                const bool in = there && i + r < left;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + i * 128 + (sw ^ ((i & 7) << 4))),
+                             "l"(in ? src : reinterpret_cast<const char *>(cache)), "r"(in ? 16 : 0)
+                             : "memory");
+            }
         }
     }
 }

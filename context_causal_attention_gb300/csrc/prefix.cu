@@ -77,7 +77,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 constexpr int kGroups = 2;                    // consumer groups of 4 warps
-constexpr int kMmaThreads = 64 + kGroups * 128;  // and two loading warps
+constexpr int kLoaders = 4;  // warps: K and V, the first and second half of a stage
+constexpr int kMmaThreads = kLoaders * 32 + kGroups * 128;
 
 template <int D>
 struct MmaCfg {
@@ -88,7 +89,8 @@ struct MmaCfg {
     static constexpr int kOffOut = kStages * 2 * kTile;    // [groups][4 warps][16 rows][D] fp32
     static constexpr int kOffMl = kOffOut + kGroups * 4 * 16 * D * 4;  // [groups][4][16] (m, l)
     static constexpr int kOffLine = kOffMl + kGroups * 4 * 16 * 8;
-    static constexpr int kOffBar = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
+    static constexpr int kOffStart = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
+    static constexpr int kOffBar = (kOffStart + static_cast<int>(sizeof(Start)) + 15) & ~15;
     static constexpr int kOffMisc = kOffBar + kStages * 16 + kGroups * 8;
     static constexpr int kSmem = kOffMisc + 16 + 1024;     // + alignment slack
     static_assert(kSmem <= 232448, "shared memory budget");
@@ -122,6 +124,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Line &line = *reinterpret_cast<Line *>(smem + C::kOffLine);
+    Start &start = *reinterpret_cast<Start *>(smem + C::kOffStart);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *empty = full + C::kStages, *go = empty + C::kStages;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -129,26 +132,29 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     if (tid == 0) {
         *abort_flag = 0;
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(full + s, 64);
+            mbar_init(full + s, 32 * kLoaders);
             mbar_init(empty + s, 4);
         }
         for (int i = 0; i < kGroups; ++i) mbar_init(go + i, 4);
         fence_mbar_init();
     }
-    scan_line<kTM, kKT>(a, line, blockIdx.x == 0);
+    scan_line<kTM, kKT>(a, line, blockIdx.x == 0 && blockIdx.y == 0);
     long long t0, t1;
     if (!share_of(a, line, &t0, &t1)) return;
+    if (warp == 0) find_start<kTM, kKT>(a, line, t0, &start);
+    __syncthreads();
 
-    if (warp < 2) {
-        // -------------------------------------------------------- loads: K by warp 0, V by warp 1
-        const __nv_bfloat16 *cache = warp ? a.v : a.k;
-        const int shift = a.own.shift;
-        const uint32_t ring = smem_u32(smem) + warp * C::kTile;
+    if (warp < kLoaders) {
+        // -------------------------------------------------------- loads
+        constexpr int kPart = kKT * 2 / kLoaders;  // keys of a warp
+        const bool is_v = warp & 1;
+        const __nv_bfloat16 *cache = is_v ? a.v : a.k;
+        const int shift = a.own.shift, part = (warp >> 1) * kPart;
+        const uint32_t ring = smem_u32(smem) + is_v * C::kTile + part * 128;
         uint32_t it = 0;
         bool ok = true;
-        for (long long t = t0; t < t1 && ok;) {
-            const Piece x = find_piece<kTM, kKT>(a, line, t, t1);
-            t = x.next;
+        for (Walk<kTM, kKT> walk(a, line, start, t1 - t0); walk.more() && ok;) {
+            const Piece x = walk.next(a, line);
             if (x.k0 >= x.k1) continue;
             PageWindow win;
             win.begin(a, x, (x.k0 * kKT) >> shift, lane);
@@ -156,14 +162,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 win.advance((kt * kKT) >> shift, lane);
                 const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
                 if (!mbar_wait_warp(empty + st, ph ^ 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
-                copy_tile<D, kKT, C::kAtom>(a, x, win, cache, ring + st * 2 * C::kTile, kt * kKT, lane);
+                copy_tile<D, kPart, C::kAtom>(a, x, win, cache, ring + st * 2 * C::kTile, kt * kKT + part, lane);
                 copies_arrive(full + st);
             }
         }
         copies_drain();  // also where a wait was given up: no copy may land after the block is gone
     } else {
         // -------------------------------------------------------- products
-        const int group = (warp - 2) >> 2, w = (warp - 2) & 3, gtid = tid - 64 - group * 128;
+        const int group = (warp - kLoaders) >> 2, w = (warp - kLoaders) & 3, gtid = tid - kLoaders * 32 - group * 128;
         const int g = lane >> 2, t4 = lane & 3;  // accumulator row (and row + 8), column pair
         float *out_s = reinterpret_cast<float *>(smem + C::kOffOut) + group * 4 * 16 * D;
         float2 *ml_s = reinterpret_cast<float2 *>(smem + C::kOffMl) + group * 4 * 16;
@@ -171,10 +177,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         uint32_t it = 0, gone = 0;
         int turn = 0;
         bool ok = true;
-        for (long long t = t0; t < t1 && ok; turn ^= 1) {
-            const bool first = t == t0;
-            const Piece x = find_piece<kTM, kKT>(a, line, t, t1);
-            t = x.next;
+        bool first = true;
+        for (Walk<kTM, kKT> walk(a, line, start, t1 - t0); walk.more() && ok; turn ^= 1, first = false) {
+            const Piece x = walk.next(a, line);
             if (turn != group) {
                 // the other group's piece
                 it += static_cast<uint32_t>(x.k1 - x.k0);
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             for (int h = 0; h < 2; ++h) {
                 const int row = x.row0 + g + 8 * h;
                 const bool in = row < x.rows;
-                const int tok = row / a.G;
+                const int tok = static_cast<int>(fdiv(static_cast<uint32_t>(row), a.div_g));
                 const __nv_bfloat16 *qp = a.q + (static_cast<long long>(x.tok0 + (in ? tok : 0)) * a.N + x.kvh * a.G +
                                                  (in ? row - tok * a.G : 0)) * D;
 #pragma unroll
@@ -613,7 +618,7 @@ cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
     });
     if (err != cudaSuccess) return cuda_status(err);
     const int sms = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
-    const int grid = sms / a.lanes * a.lanes;
+    const dim3 grid(a.lanes, sms / a.lanes);
     if (!tc) {
         prefix_mma_kernel<D><<<grid, kMmaThreads, MmaCfg<D>::kSmem, stream>>>(a);
         return last_launch_status();
@@ -749,6 +754,7 @@ extern "C" cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, cons
     a.N = static_cast<int>(N);
     a.Nkv = static_cast<int>(Nkv);
     a.G = static_cast<int>(N / Nkv);
+    a.div_g = make_fastdiv(static_cast<uint32_t>(a.G));
     a.lanes = s.lanes;
     a.heads = static_cast<int>(Nkv / s.lanes);
     a.P = prefix_len;

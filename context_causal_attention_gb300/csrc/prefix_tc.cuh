@@ -56,7 +56,8 @@ struct TcCfg {
     static constexpr int kOffK = 2 * kTile;
     static constexpr int kOffV = kOffK + kStages * kTile;
     static constexpr int kOffLine = kOffV + kStages * kTile;
-    static constexpr int kOffBar = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
+    static constexpr int kOffStart = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
+    static constexpr int kOffBar = (kOffStart + static_cast<int>(sizeof(Start)) + 15) & ~15;
     // q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain, ml_full, k_full[S], v_full[S], k_empty[S], v_empty[S]
     static constexpr int kBars = 12 + 4 * kStages;
     static constexpr int kOffMisc = kOffBar + kBars * 8;
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Line &line = *reinterpret_cast<Line *>(smem + C::kOffLine);
+    Start &start = *reinterpret_cast<Start *>(smem + C::kOffStart);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *q_full = bar, *s_full = bar + 2, *p_full = bar + 4, *o_full = bar + 6, *o_empty = bar + 8;
     uint64_t *drain = bar + 10, *ml_full = bar + 11, *k_full = bar + 12, *v_full = k_full + C::kStages, *k_empty = v_full + C::kStages,
@@ -114,13 +116,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    scan_line<kTcTM, kTcKT>(a, line, blockIdx.x == 0);
+    scan_line<kTcTM, kTcKT>(a, line, blockIdx.x == 0 && blockIdx.y == 0);
     long long t0, t1;
     if (!share_of(a, line, &t0, &t1)) return;
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
+    if (warp == 0) find_start<kTcTM, kTcKT>(a, line, t0, &start);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -135,9 +138,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int shift = a.own.shift, rows = min(kTcKT, 1 << shift);  // rows of a copy
         uint32_t it = 0;
         bool ok = true;
-        for (long long t = t0; t < t1 && ok;) {
-            const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
-            t = x.next;
+        for (Walk<kTcTM, kTcKT> walk(a, line, start, t1 - t0); walk.more() && ok;) {
+            const Piece x = walk.next(a, line);
             if (x.k0 >= x.k1) continue;
             PageWindow win;
             win.begin(a, x, (x.k0 * kTcKT) >> shift, lane);
@@ -209,9 +211,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_after();
                 return true;
             };
-            for (long long t = t0; t < t1 && ok;) {
-                const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
-                t = x.next;
+            for (Walk<kTcTM, kTcKT> walk(a, line, start, t1 - t0); walk.more() && ok;) {
+                const Piece x = walk.next(a, line);
                 const int n = x.k1 - x.k0;
                 if (n <= 0) continue;
                 const bool paired = x.rows - x.row0 <= 128;
@@ -267,9 +268,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp == 3) {
         // -------------------------------------------------------- Q: rows gathered, swizzled as TMA would
         uint32_t items = 0;
-        for (long long t = t0; t < t1;) {
-            const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
-            t = x.next;
+        for (Walk<kTcTM, kTcKT> walk(a, line, start, t1 - t0); walk.more();) {
+            const Piece x = walk.next(a, line);
             if (x.k0 >= x.k1) continue;
             // the last item's scores have all been computed (o_full[0] is committed after the last of them)
             if (items && !mbar_wait_warp(o_full, (items - 1) & 1u, abort_flag, a.timeout_ns)) break;
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint32_t dst = smem_u32(sQ) + i * C::kTile + (c >> 3) * C::kAtom + r0 * 128;
                 for (int g = 0; g < 4; ++g) {
                     // element offset of row 32 g + lane, handed to the lanes that copy it
-                    const int row = x.row0 + i * 128 + 32 * g + lane, tok = row / a.G;
+                    const int row = x.row0 + i * 128 + 32 * g + lane, tok = static_cast<int>(fdiv(static_cast<uint32_t>(row), a.div_g));
                     const long long mine =
                         row < x.rows ? (static_cast<long long>(x.tok0 + tok) * a.N + x.kvh * a.G + row - tok * a.G) * D : -1;
 #pragma unroll 8
@@ -305,9 +305,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float2 *ml_s = reinterpret_cast<float2 *>(smem + C::kOffMl);
         uint32_t tiles = 0, items = 0, kv = 0, joins = 0, other = 0;  // other: items of the other half
         bool ok = true;
-        for (long long t = t0; t < t1 && ok;) {
-            const Piece x = find_piece<kTcTM, kTcKT>(a, line, t, t1);
-            t = x.next;
+        for (Walk<kTcTM, kTcKT> walk(a, line, start, t1 - t0); walk.more() && ok;) {
+            const Piece x = walk.next(a, line);
             // up to 128 rows: both halves hold the same rows, tile j of the piece is half j & 1's
             const bool paired = x.rows - x.row0 <= 128;
             const int first_row = x.row0 + (paired ? 0 : half * 128), row = first_row + in_tile, all = x.k1 - x.k0;
