@@ -60,16 +60,16 @@ struct Problem {
     long long key_tiles;  // nominal length of an item
 };
 
-// The lists of the first kListed sequences and where every problem's tiles and
-// items begin on the line (entry i + 1: run i of the sequences; entry 0: the
-// prefix), in shared memory.
+// Where every problem's tiles and items begin on the line (entry i + 1: run i of
+// the sequences; entry 0: the prefix), in shared memory, and the lists of the
+// first `listed` sequences where a kernel has room for them there.
 constexpr int kRuns = 128;
-constexpr int kListed = 1024;
 struct Line {
     long long tile[kRuns + 1];
     int item[kRuns + 1];
     int rows_end;  // cu[B]
-    int cu[kListed + 1], len[kListed];
+    int listed;
+    int *cu, *len;  // [listed + 1], [listed]
 };
 
 // Sequence b as the device lists give it; a list that makes no sense is cut to
@@ -77,7 +77,7 @@ struct Line {
 template <int TM, int KT>
 __device__ __forceinline__ Problem sequence_problem(const PrefixArgs &a, const Line &line, int b) {
     Problem p;
-    const bool listed = b < kListed;
+    const bool listed = b < line.listed;
     const int c0 = listed ? line.cu[b] : __ldg(a.cu + b), c1 = listed ? line.cu[b + 1] : __ldg(a.cu + b + 1);
     long long len = listed ? line.len[b] : __ldg(a.kv_len + b);
     const long long most = static_cast<long long>(a.own.max_pages) << a.own.shift;
@@ -113,16 +113,20 @@ __device__ __forceinline__ int place_of(int j, int tiles) {
     return j < (tiles + 1) / 2 ? 2 * j : 2 * (tiles - 1 - j) + 1;
 }
 
-// Fills `line`: the lists (one load a thread and list for up to a block's
-// threads of sequences), sums over runs of sequences, and their scan.  `lead`
+// Fills `line`: the lists of up to `room` sequences (`lists`: 2 room + 1 values), sums over runs of sequences, and their scan.  `lead`
 // is true in the block that leaves the sequences' places for the join.
 template <int TM, int KT>
-__device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, bool lead) {
-    const int tid = threadIdx.x, run = (a.B + kRuns - 1) / kRuns;
-    if (tid == 0) line.rows_end = __ldg(a.cu + a.B);
-    for (int b = a.with_own ? tid : kListed + 1; b <= min(a.B, kListed); b += blockDim.x) {
-        line.cu[b] = __ldg(a.cu + b);
-        if (b < min(a.B, kListed)) line.len[b] = __ldg(a.kv_len + b);
+__device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, int *lists, int room, bool lead) {
+    const int tid = threadIdx.x, run = (a.B + kRuns - 1) / kRuns, listed = a.with_own ? min(a.B, room) : 0;
+    if (tid == 0) {
+        line.rows_end = __ldg(a.cu + a.B);
+        line.listed = listed;
+        line.cu = lists;
+        line.len = lists + room + 1;
+    }
+    for (int b = listed ? tid : 1; b <= listed; b += blockDim.x) {
+        lists[b] = __ldg(a.cu + b);
+        if (b < listed) lists[room + 1 + b] = __ldg(a.kv_len + b);
     }
     __syncthreads();
     const int b0 = min(tid * run, a.B), b1 = a.with_own ? min(b0 + run, a.B) : b0;

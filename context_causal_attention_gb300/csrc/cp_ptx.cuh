@@ -479,6 +479,14 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
 
+// ---------------------------------------------------------------- dependent launches
+// Lets the next kernel of the stream start its blocks as soon as SMs have room,
+// if it was launched with programmatic stream serialization.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until the kernel before this one is complete and its writes are visible
+// (at once if this one was launched normally).
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- misc
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;

@@ -89,7 +89,9 @@ struct MmaCfg {
     static constexpr int kOffOut = kStages * 2 * kTile;    // [groups][4 warps][16 rows][D] fp32
     static constexpr int kOffMl = kOffOut + kGroups * 4 * 16 * D * 4;  // [groups][4][16] (m, l)
     static constexpr int kOffLine = kOffMl + kGroups * 4 * 16 * 8;
-    static constexpr int kOffStart = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
+    static constexpr int kListed = 1024;                   // sequences whose lists are kept here
+    static constexpr int kOffLists = kOffLine + static_cast<int>(sizeof(Line));
+    static constexpr int kOffStart = (kOffLists + (2 * kListed + 1) * 4 + 15) & ~15;
     static constexpr int kOffBar = (kOffStart + static_cast<int>(sizeof(Start)) + 15) & ~15;
     static constexpr int kOffMisc = kOffBar + kStages * 16 + kGroups * 8;
     static constexpr int kSmem = kOffMisc + 16 + 1024;     // + alignment slack
@@ -129,6 +131,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+    launch_dependents();
     if (tid == 0) {
         *abort_flag = 0;
         for (int s = 0; s < C::kStages; ++s) {
@@ -138,9 +141,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         for (int i = 0; i < kGroups; ++i) mbar_init(go + i, 4);
         fence_mbar_init();
     }
-    scan_line<kTM, kKT>(a, line, blockIdx.x == 0 && blockIdx.y == 0);
+    scan_line<kTM, kKT>(a, line, reinterpret_cast<int *>(smem + C::kOffLists), C::kListed,
+                        blockIdx.x == 0 && blockIdx.y == 0);
     long long t0, t1;
-    if (!share_of(a, line, &t0, &t1)) return;
+    if (!share_of(a, line, &t0, &t1)) {
+        if (tid == 0) wait_for_previous();
+        return;
+    }
     if (warp == 0) find_start<kTM, kKT>(a, line, t0, &start);
     __syncthreads();
 
@@ -336,6 +343,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     __syncthreads();
     if (tid == 0 && *abort_flag) report(a.status, CP_ERR_DEVICE_TIMEOUT);
+    // It reads nothing of the 256-row launch before it, but is not complete before
+    // that one is: the join waits for this launch alone.
+    if (tid == 0) wait_for_previous();
 }
 
 // What a launch left, as the join reads it.
@@ -440,6 +450,7 @@ __global__ void __launch_bounds__(128) join_row_kernel(const JoinArgs a) {
     const int tok = static_cast<int>(row / a.N), h = static_cast<int>(row - static_cast<long long>(tok) * a.N);
     int begin, count;
     const int b = find_sequence(a.cu, a.B, tok, lane, &begin, &count);
+    wait_for_previous();
     if (b < 0) return;
     float mx = -INFINITY, ls = 0.f, acc[kV];
 #pragma unroll
@@ -503,6 +514,7 @@ __global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
     if (tok >= a.R) return;
     int begin, count;
     const int b = find_sequence(a.cu, a.B, tok, lane, &begin, &count);
+    wait_for_previous();
     if (b < 0) return;
     const int h = h0 + lane, kvh = h / a.G, heads = min(32, a.N - h0);
     const TokenPart p0(a, 0, b, tok, begin, count), p1(a, 1, b, tok, begin, count);
@@ -603,8 +615,28 @@ Shape shape_of(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int6
     return s;
 }
 
+// Launches `kernel`; `after`: its blocks may start before the kernel before it in
+// the stream is complete (it waits for itself, wait_for_previous).
+template <typename... P, typename... A>
+cp_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool after, cudaStream_t stream, const A &...args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = after ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
+    if (e != cudaSuccess) cudaGetLastError();
+    return cuda_status(e);
+}
+
+// `after`: the call's other main launch came before this one.
 template <int D>
-cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
+cp_status launch_main(const PrefixArgs &a, bool tc, bool after, cudaStream_t stream) {
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [] {
@@ -619,10 +651,7 @@ cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
     if (err != cudaSuccess) return cuda_status(err);
     const int sms = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
     const dim3 grid(a.lanes, sms / a.lanes);
-    if (!tc) {
-        prefix_mma_kernel<D><<<grid, kMmaThreads, MmaCfg<D>::kSmem, stream>>>(a);
-        return last_launch_status();
-    }
+    if (!tc) return launch(prefix_mma_kernel<D>, grid, kMmaThreads, MmaCfg<D>::kSmem, after, stream, a);
     const int64_t rows = static_cast<int64_t>(a.own.n_pages) << a.own.shift;
     const int page = 1 << a.own.shift, box = page < kTcKT ? page : kTcKT;
     // at D = 64 a head's row is 128 bytes and its neighbour another head's
@@ -631,10 +660,8 @@ cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
     if (!make_map(&mk, a.k, D, a.Nkv, rows, 1, box, l2) || !make_map(&mv, a.v, D, a.Nkv, rows, 1, box, l2))
         return CP_ERR_CUDA;
     if (page >= kTmaPage)
-        prefix_tc_kernel<D, true><<<grid, kTcThreads, TcCfg<D>::kSmem, stream>>>(mk, mv, a);
-    else
-        prefix_tc_kernel<D, false><<<grid, kTcThreads, TcCfg<D>::kSmem, stream>>>(mk, mv, a);
-    return last_launch_status();
+        return launch(prefix_tc_kernel<D, true>, grid, kTcThreads, TcCfg<D>::kSmem, false, stream, mk, mv, a);
+    return launch(prefix_tc_kernel<D, false>, grid, kTcThreads, TcCfg<D>::kSmem, false, stream, mk, mv, a);
 }
 
 template <int D>
@@ -650,7 +677,7 @@ cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cuda
         a.slot_ml = reinterpret_cast<float2 *>(w + s.slot_ml[k]);
         a.slot_o = reinterpret_cast<float *>(w + s.slot_o[k]);
         a.slots = static_cast<int>(s.slots[k]);
-        const cp_status st = launch_main<D>(a, k == 1, stream);
+        const cp_status st = launch_main<D>(a, k == 1, k == 0 && s.slots[1], stream);
         if (st != CP_OK) return st;
         for (int which = 0; which < 2; ++which)
             if (which ? a.with_own : a.with_prefix)
@@ -659,13 +686,10 @@ cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cuda
     }
     if (a.P == 0) j.part[0] = j.part[1];  // not read into a result: no keys
     const long long rows = static_cast<long long>(a.R) * a.N;
-    if (rows <= kJoinRows) {
-        join_row_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(j);
-    } else {
-        const long long units = static_cast<long long>(a.R) * ((a.N + 31) / 32);
-        join_token_kernel<D><<<static_cast<unsigned>((units + 3) / 4), 128, 0, stream>>>(j);
-    }
-    return last_launch_status();
+    const bool few = rows <= kJoinRows;
+    const long long units = few ? rows : static_cast<long long>(a.R) * ((a.N + 31) / 32);
+    return launch(few ? join_row_kernel<D> : join_token_kernel<D>, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0,
+                  true, stream, j);
 }
 
 cp_status check_sizes(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int64_t Nkv, int64_t D,

@@ -51,18 +51,22 @@ struct TcCfg {
     static constexpr int kAtom = 128 * 128;  // 128 rows x 64 columns
     static constexpr int kAtoms = D / 64;
     static constexpr int kTile = kAtom * kAtoms;
-    static constexpr int kStages = D == 128 ? 2 : 4;
+    // Stages of K and of V.  The scores of the second half hold a K stage until its
+    // exponentials of the tile before are done, so K is asked for late: a third
+    // stage of it (all that shared memory has left beside Q) took 64 decoding
+    // sequences behind 32768 keys from V_OLD to V_NEW us.
+    static constexpr int kStagesK = D == 128 ? 3 : 6, kStagesV = D == 128 ? 2 : 6;
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = 2 * kTile;
-    static constexpr int kOffV = kOffK + kStages * kTile;
-    static constexpr int kOffLine = kOffV + kStages * kTile;
+    static constexpr int kOffV = kOffK + kStagesK * kTile;
+    static constexpr int kOffLine = kOffV + kStagesV * kTile;
     static constexpr int kOffStart = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
     static constexpr int kOffBar = (kOffStart + static_cast<int>(sizeof(Start)) + 15) & ~15;
-    // q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain, ml_full, k_full[S], v_full[S], k_empty[S], v_empty[S]
-    static constexpr int kBars = 12 + 4 * kStages;
+    // q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain, ml_full, k_full[], v_full[], k_empty[], v_empty[]
+    static constexpr int kBars = 12 + 2 * (kStagesK + kStagesV);
     static constexpr int kOffMisc = kOffBar + kBars * 8;
     static constexpr int kOffMl = kOffMisc + 16;        // [128] (m, l) of the second half
-    static constexpr int kSmem = kOffMl + 128 * 8 + 1024;  // + alignment slack
+    static constexpr int kSmem = kOffMl + 128 * 8;
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -83,18 +87,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PrefixArgs a) {
     using C = TcCfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // (no room to align by hand; a block without static shared memory begins at 1024)
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (smem_u32(smem) & 1023u) {
+        if (tid == 0) report(a.status, CP_ERR_ALIGNMENT);
+        return;
+    }
     Line &line = *reinterpret_cast<Line *>(smem + C::kOffLine);
     Start &start = *reinterpret_cast<Start *>(smem + C::kOffStart);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *q_full = bar, *s_full = bar + 2, *p_full = bar + 4, *o_full = bar + 6, *o_empty = bar + 8;
-    uint64_t *drain = bar + 10, *ml_full = bar + 11, *k_full = bar + 12, *v_full = k_full + C::kStages, *k_empty = v_full + C::kStages,
-             *v_empty = k_empty + C::kStages;
+    uint64_t *drain = bar + 10, *ml_full = bar + 11, *k_full = bar + 12, *v_full = k_full + C::kStagesK,
+             *k_empty = v_full + C::kStagesV, *v_empty = k_empty + C::kStagesK;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
 
+    launch_dependents();
     if (tid == 0) {
         *abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
@@ -106,17 +115,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         mbar_init(drain, 1);
         mbar_init(ml_full, 4);
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < C::kStagesK; ++s) {
             mbar_init(k_full + s, tma ? 1 : 32);
-            mbar_init(v_full + s, tma ? 1 : 32);
             mbar_init(k_empty + s, 1);
+        }
+        for (int s = 0; s < C::kStagesV; ++s) {
+            mbar_init(v_full + s, tma ? 1 : 32);
             mbar_init(v_empty + s, 1);
         }
         fence_mbar_init();
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    scan_line<kTcTM, kTcKT>(a, line, blockIdx.x == 0 && blockIdx.y == 0);
+    scan_line<kTcTM, kTcKT>(a, line, nullptr, 0, blockIdx.x == 0 && blockIdx.y == 0);
     long long t0, t1;
     if (!share_of(a, line, &t0, &t1)) return;
     if (warp == 1) {
@@ -135,6 +146,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const CUtensorMap *map = warp ? &tmV : &tmK;
         uint64_t *full = warp ? v_full : k_full, *empty = warp ? v_empty : k_empty;
         uint8_t *ring = warp ? sV : sK;
+        const uint32_t stages = warp ? C::kStagesV : C::kStagesK;
+        uint32_t st = 0, ph = 0;  // stage and phase of tile `it`
         const int shift = a.own.shift, rows = min(kTcKT, 1 << shift);  // rows of a copy
         uint32_t it = 0;
         bool ok = true;
@@ -147,7 +160,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int key = kt * kTcKT;
                 win.advance(key >> shift, lane);
                 const int n = (min(kTcKT, x.keys - key) + rows - 1) / rows;
-                const uint32_t st = it % C::kStages, ph = (it / C::kStages) & 1u;
+                if (it) {
+                    if (++st == stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
                 if (!mbar_wait_warp(empty + st, ph ^ 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
                 if (!tma) {
                     copy_tile<D, kTcKT, C::kAtom>(a, x, win, warp ? a.v : a.k, smem_u32(ring) + st * C::kTile, key, lane);
@@ -169,8 +187,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok && tma && lane == 0) {
             // let every copy already issued land before shared memory goes away
             volatile int no_abort = 0;
-            for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
-                mbar_wait(full + i % C::kStages, (i / C::kStages) & 1u, &no_abort, 100000000ull);
+            for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
+                mbar_wait(full + i % stages, (i / stages) & 1u, &no_abort, 100000000ull);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -192,7 +210,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             // O_i (+)= P_i V of tile `at`; the tile's V is awaited with `await`, given back with `release`
             auto pv = [&](int i, uint32_t at, bool await, bool release, bool first) -> bool {
-                const uint32_t st = at % C::kStages, ph = (at / C::kStages) & 1u;
+                const uint32_t st = at % C::kStagesV, ph = (at / C::kStagesV) & 1u;
                 if (await) {
                     if (!mbar_wait(v_full + st, ph, abort_flag, a.timeout_ns)) return false;
                     if (!tma) fence_async_shared();  // written by cp.async, read by the tensor core
@@ -206,7 +224,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 return true;
             };
             auto k_wait = [&]() -> bool {
-                if (!mbar_wait(k_full + kv % C::kStages, (kv / C::kStages) & 1u, abort_flag, a.timeout_ns)) return false;
+                if (!mbar_wait(k_full + kv % C::kStagesK, (kv / C::kStagesK) & 1u, abort_flag, a.timeout_ns)) return false;
                 if (!tma) fence_async_shared();
                 tc_fence_after();
                 return true;
@@ -233,7 +251,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                         if (j < n && ok && (ok = k_wait())) {
-                            const uint32_t st = kv % C::kStages;
+                            const uint32_t st = kv % C::kStagesK;
                             qk(i, dq0, st);
                             umma_commit(k_empty + st);
                             ++kv;
@@ -243,7 +261,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 } else {
                     for (int j = 0; j < n && ok; ++j) {
                         if (!k_wait()) { ok = false; break; }
-                        const uint32_t st = kv % C::kStages;
+                        const uint32_t st = kv % C::kStagesK;
                         for (int i = 0; i < 2 && ok; ++i) {
                             if (j > 0 && !pv(i, kv - 1, i == 0, i == 1, j == 1)) { ok = false; break; }
                             qk(i, i ? dq1 : dq0, st);
@@ -329,7 +347,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int n = begin; n < all; n += step, tile += step, ++tiles, past -= 128 * step, limit -= 128 * step,
                      whole -= 128 * step) {
                 if (tma && (paired || half == 0) && past < 128) {
-                    const uint32_t st = tile % C::kStages, ph = (tile / C::kStages) & 1u;
+                    const uint32_t st = tile % C::kStagesV, ph = (tile / C::kStagesV) & 1u;
                     if (!mbar_wait_warp(v_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
                     if (in_tile >= past) {
                         uint8_t *dst = sV + st * C::kTile + in_tile * 128;
