@@ -62,8 +62,8 @@ struct TcCfg {
     static constexpr int kOffLine = kOffV + kStagesV * kTile;
     static constexpr int kOffStart = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
     static constexpr int kOffBar = (kOffStart + static_cast<int>(sizeof(Start)) + 15) & ~15;
-    // q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain, ml_full, k_full[], v_full[], k_empty[], v_empty[]
-    static constexpr int kBars = 12 + 2 * (kStagesK + kStagesV);
+    // q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain, ml_full, q_empty, k_full[], v_full[], k_empty[], v_empty[]
+    static constexpr int kBars = 13 + 2 * (kStagesK + kStagesV);
     static constexpr int kOffMisc = kOffBar + kBars * 8;
     static constexpr int kOffMl = kOffMisc + 16;        // [128] (m, l) of the second half
     static constexpr int kSmem = kOffMl + 128 * 8;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Start &start = *reinterpret_cast<Start *>(smem + C::kOffStart);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *q_full = bar, *s_full = bar + 2, *p_full = bar + 4, *o_full = bar + 6, *o_empty = bar + 8;
-    uint64_t *drain = bar + 10, *ml_full = bar + 11, *k_full = bar + 12, *v_full = k_full + C::kStagesK,
+    uint64_t *drain = bar + 10, *ml_full = bar + 11, *q_empty = bar + 12, *k_full = bar + 13, *v_full = k_full + C::kStagesK,
              *k_empty = v_full + C::kStagesV, *v_empty = k_empty + C::kStagesK;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         mbar_init(drain, 1);
         mbar_init(ml_full, 4);
+        mbar_init(q_empty, 1);
         for (int s = 0; s < C::kStagesK; ++s) {
             mbar_init(k_full + s, tma ? 1 : 32);
             mbar_init(k_empty + s, 1);
@@ -234,11 +235,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int n = x.k1 - x.k0;
                 if (n <= 0) continue;
                 const bool paired = x.rows - x.row0 <= 128;
-                for (int i = 0; i < (paired ? 1 : 2) && ok; ++i)
-                    ok = mbar_wait(q_full + i, queries[i]++ & 1u, abort_flag, a.timeout_ns);
-                if (!ok) break;
-                fence_async_shared();  // written by cp.async, read by the tensor core
-                tc_fence_after();
+                auto q_wait = [&](int i) -> bool {
+                    if (!mbar_wait(q_full + i, queries[i]++ & 1u, abort_flag, a.timeout_ns)) return false;
+                    fence_async_shared();  // written by cp.async, read by the tensor core
+                    tc_fence_after();
+                    return true;
+                };
+                if (!q_wait(0)) { ok = false; break; }
                 if (paired) {
                     // tile j belongs to half j & 1; its weights are used when tile j + 2 comes
                     for (int j = 0; j < n + 2 && ok; ++j) {
@@ -254,6 +257,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const uint32_t st = kv % C::kStagesK;
                             qk(i, dq0, st);
                             umma_commit(k_empty + st);
+                            if (j == n - 1) umma_commit(q_empty);
                             ++kv;
                         }
                         if (n == 1) ++j;  // no tile for the second half
@@ -264,10 +268,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const uint32_t st = kv % C::kStagesK;
                         for (int i = 0; i < 2 && ok; ++i) {
                             if (j > 0 && !pv(i, kv - 1, i == 0, i == 1, j == 1)) { ok = false; break; }
+                            if (j == 0 && i == 1 && !q_wait(1)) { ok = false; break; }
                             qk(i, i ? dq1 : dq0, st);
                         }
                         if (!ok) break;
                         umma_commit(k_empty + st);
+                        if (j == n - 1) umma_commit(q_empty);
                         ++kv;
                     }
                     for (int i = 0; i < 2 && ok; ++i) {
@@ -289,8 +295,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (Walk<kTcTM, kTcKT> walk(a, line, start, t1 - t0); walk.more();) {
             const Piece x = walk.next(a, line);
             if (x.k0 >= x.k1) continue;
-            // the last item's scores have all been computed (o_full[0] is committed after the last of them)
-            if (items && !mbar_wait_warp(o_full, (items - 1) & 1u, abort_flag, a.timeout_ns)) break;
+            // the last item's scores have all been computed
+            if (items && !mbar_wait_warp(q_empty, (items - 1) & 1u, abort_flag, a.timeout_ns)) break;
             ++items;
             for (int i = 0; i < 2 && x.row0 + i * 128 < x.rows; ++i) {
                 constexpr int kChunks = D / 8, kRpi = 32 / kChunks;  // 16-byte chunks of a row, rows of an instruction
@@ -323,6 +329,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float2 *ml_s = reinterpret_cast<float2 *>(smem + C::kOffMl);
         uint32_t tiles = 0, items = 0, kv = 0, joins = 0, other = 0;  // other: items of the other half
         bool ok = true;
+        // The first pass through the code of a tile is made on what tensor memory
+        // happens to hold, while the first copies are under way: read cold, that
+        // code took 8000 cycles, four times a tile's time.  Nothing is written in it and
+        // no barrier touched.
+        bool dry = true;
         for (Walk<kTcTM, kTcKT> walk(a, line, start, t1 - t0); walk.more() && ok;) {
             const Piece x = walk.next(a, line);
             // up to 128 rows: both halves hold the same rows, tile j of the piece is half j & 1's
@@ -344,9 +355,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             int limit = (valid ? row_limit(a, x, row) : x.keys) - (x.k0 + begin) * 128;
             int whole = row_limit(a, x, first_row) - (x.k0 + begin) * 128;
             float m_run = -INFINITY, l_run = 0.f;
-            for (int n = begin; n < all; n += step, tile += step, ++tiles, past -= 128 * step, limit -= 128 * step,
-                     whole -= 128 * step) {
-                if (tma && (paired || half == 0) && past < 128) {
+            for (int n = begin; n < all;) {
+                if (!dry && tma && (paired || half == 0) && past < 128) {
                     const uint32_t st = tile % C::kStagesV, ph = (tile / C::kStagesV) & 1u;
                     if (!mbar_wait_warp(v_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
                     if (in_tile >= past) {
@@ -357,7 +367,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     fence_async_shared();
                 }
-                if (!mbar_wait_warp(s_full + half, tiles & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                if (!dry && !mbar_wait_warp(s_full + half, tiles & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
                 tc_fence_after();
                 const bool mask = whole < 128;
                 const int lim = limit;
@@ -379,14 +389,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
                 const float s0 = exp_pack64(sa, sl2, neg_m, pa);
                 tmem_wait_ld(sb);  // columns 64..127 are read: P may overwrite them
-                tmem_st32_nowait(tS + 64, pa);
+                if (!dry) tmem_st32_nowait(tS + 64, pa);
                 if (mask && !first) hide_columns(64, lim, sb);
                 const float s1 = exp_pack64(sb, sl2, neg_m, pb);
-                tmem_st32_nowait(tS + 96, pb);
+                if (!dry) tmem_st32_nowait(tS + 96, pb);
                 float sum = s0 + s1;
                 const bool big = !(sum <= 0x1p64f);  // also for inf and NaN
                 tmem_wait_st();
-                if (__any_sync(0xffffffffu, big)) {
+                if (__any_sync(0xffffffffu, big) && !dry) {
                     // rare: the scores grew by more than 2^64 over the running maximum.
                     // Columns 0..63 of S are still in tensor memory, 64..127 in sb.
                     tmem_ld64(tS, sa);
@@ -413,7 +423,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 l_run += sum;
                 tc_fence_before();
                 __syncwarp();
+                if (dry) {
+                    dry = false;
+                    m_run = -INFINITY;
+                    l_run = 0.f;
+                    continue;
+                }
                 if (lane == 0) mbar_arrive(p_full + half);
+                n += step;
+                tile += step;
+                ++tiles;
+                past -= 128 * step;
+                limit -= 128 * step;
+                whole -= 128 * step;
             }
             if (!ok || !mbar_wait_warp(o_full + half, items & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
             tc_fence_after();
