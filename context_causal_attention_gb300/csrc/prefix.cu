@@ -54,8 +54,6 @@ __device__ int g_prefix_status = 0;
 // rows on the tensor memory, else in tiles of 16.
 constexpr int kTcRows = 16;
 
-constexpr int kTM = 16;  // rows of a tile
-constexpr int kKT = 64;  // keys of a stage
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -671,6 +669,11 @@ cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cuda
         if (!s.slots[k]) continue;
         a.with_prefix = a.P > 0 && s.tc_prefix == (k == 1);
         a.with_own = s.tc_own == (k == 1);
+        // measured cycles of a tile (256 rows or up to 128 rows of 128 keys; 16 rows of 64 keys)
+        const bool both = s.slots[0] && s.slots[1];
+        const bool half = static_cast<int64_t>(a.R) * a.G <= 128;
+        a.cost_prefix = !both ? 0 : D == 128 ? (half ? 2300 : 4600) : (half ? 2300 : 3300);
+        a.cost_own = !both ? 0 : D == 128 ? 1250 : 800;
         a.head = reinterpret_cast<long long *>(w + s.head[k]);
         a.base_tile = reinterpret_cast<long long *>(w + s.base_tile[k]);
         a.base_item = reinterpret_cast<int *>(w + s.base_item[k]);

@@ -40,8 +40,6 @@ namespace cpattn {
 namespace {
 
 constexpr int kTcThreads = 384;
-constexpr int kTcTM = 256;  // rows of a tile
-constexpr int kTcKT = 128;  // keys of a stage
 // Pages of this many tokens or more are copied by TMA, smaller ones by cp.async
 // (see copy_tile).
 constexpr int kTmaPage = 64;
@@ -51,11 +49,8 @@ struct TcCfg {
     static constexpr int kAtom = 128 * 128;  // 128 rows x 64 columns
     static constexpr int kAtoms = D / 64;
     static constexpr int kTile = kAtom * kAtoms;
-    // Stages of K and of V.  The scores of the second half hold a K stage until its
-    // exponentials of the tile before are done, so K is asked for late: a third
-    // stage of it (all that shared memory has left beside Q) took 64 decoding
-    // sequences behind 32768 keys from V_OLD to V_NEW us.
-    static constexpr int kStagesK = D == 128 ? 3 : 6, kStagesV = D == 128 ? 2 : 6;
+    // Stages of K and of V: a third of K (D = 128) or six of both (D = 64) measured the same.
+    static constexpr int kStagesK = D == 128 ? 2 : 4, kStagesV = D == 128 ? 2 : 4;
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = 2 * kTile;
     static constexpr int kOffV = kOffK + kStagesK * kTile;
