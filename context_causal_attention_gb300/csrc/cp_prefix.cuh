@@ -296,21 +296,36 @@ __device__ __forceinline__ void find_start(const PrefixArgs &a, const Line &line
     s->n0 = at - which * p.key_tiles;
 }
 
-// Walks a block's pieces.  Every role of a kernel walks for itself, from the
-// block's Start; a step is a few additions.
+// Walks a block's pieces.  Every warp walks for itself, from the block's Start; a
+// step is a few additions.  The walk and the piece it has come to lie in shared
+// memory: they are looked at once in many tiles, and the registers of the tile
+// loops are scarce.
 template <int TM, int KT>
 struct Walk {
     Problem p;
     Start s;
     long long left;  // nominal tiles of the share that are left
-    __device__ __forceinline__ Walk(const PrefixArgs &a, const Line &line, const Start &start, long long share)
-        : s(start), left(share) {
-        if (s.b >= a.B) left = 0;
-        else p = s.b < 0 ? prefix_problem<TM, KT>(a, line) : sequence_problem<TM, KT>(a, line, s.b);
+    Piece x;         // the piece come to
+    // Warp-wide.
+    __device__ __forceinline__ void begin(const PrefixArgs &a, const Line &line, const Start &start, long long share) {
+        if ((threadIdx.x & 31) == 0) {
+            s = start;
+            left = share;
+            if (s.b >= a.B) left = 0;
+            else p = s.b < 0 ? prefix_problem<TM, KT>(a, line) : sequence_problem<TM, KT>(a, line, s.b);
+        }
+        __syncwarp();
     }
-    __device__ __forceinline__ bool more() const { return left > 0; }
-    __device__ __forceinline__ Piece next(const PrefixArgs &a, const Line &line) {
-        Piece x;
+    // Comes to the next piece; false if there is none.  Warp-wide.
+    __device__ __forceinline__ bool next(const PrefixArgs &a, const Line &line) {
+        __syncwarp();
+        const bool more = left > 0;
+        __syncwarp();
+        if (more && (threadIdx.x & 31) == 0) step(a, line);
+        __syncwarp();
+        return more;
+    }
+    __device__ __forceinline__ void step(const PrefixArgs &a, const Line &line) {
         const int lane = blockIdx.x, slot = s.item + static_cast<int>(blockIdx.y);
         x.b = s.b;
         x.kvh = s.pass * a.lanes + lane;
@@ -344,7 +359,6 @@ struct Walk {
                 }
             }
         }
-        return x;
     }
 };
 

@@ -92,7 +92,8 @@ struct MmaCfg {
     static constexpr int kOffStart = (kOffLists + (2 * kListed + 1) * 4 + 15) & ~15;
     static constexpr int kOffBar = (kOffStart + static_cast<int>(sizeof(Start)) + 15) & ~15;
     static constexpr int kOffMisc = kOffBar + kStages * 16 + kGroups * 8;
-    static constexpr int kSmem = kOffMisc + 16 + 1024;     // + alignment slack
+    static constexpr int kOffWalk = (kOffMisc + 16 + 15) & ~15;  // [warps]
+    static constexpr int kSmem = kOffWalk + kMmaThreads / 32 * static_cast<int>(sizeof(Walk<kTM, kKT>)) + 1024;  // + alignment slack
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -149,6 +150,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     if (warp == 0) find_start<kTM, kKT>(a, line, t0, &start);
     __syncthreads();
 
+    Walk<kTM, kKT> &walk = reinterpret_cast<Walk<kTM, kKT> *>(smem + C::kOffWalk)[warp];
+    const Piece &x = walk.x;
+    walk.begin(a, line, start, t1 - t0);
     if (warp < kLoaders) {
         // -------------------------------------------------------- loads
         constexpr int kPart = kKT * 2 / kLoaders;  // keys of a warp
@@ -158,8 +162,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         const uint32_t ring = smem_u32(smem) + is_v * C::kTile + part * 128;
         uint32_t it = 0;
         bool ok = true;
-        for (Walk<kTM, kKT> walk(a, line, start, t1 - t0); walk.more() && ok;) {
-            const Piece x = walk.next(a, line);
+        while (ok && walk.next(a, line)) {
             if (x.k0 >= x.k1) continue;
             PageWindow win;
             win.begin(a, x, (x.k0 * kKT) >> shift, lane);
@@ -183,8 +186,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         int turn = 0;
         bool ok = true;
         bool first = true;
-        for (Walk<kTM, kKT> walk(a, line, start, t1 - t0); walk.more() && ok; turn ^= 1, first = false) {
-            const Piece x = walk.next(a, line);
+        for (; ok && walk.next(a, line); turn ^= 1, first = false) {
             if (turn != group) {
                 // the other group's piece
                 it += static_cast<uint32_t>(x.k1 - x.k0);

@@ -9,10 +9,10 @@
 //               cp.async (cp_prefix.cuh), into a ring of stages.  A page number
 //               out of range becomes a coordinate outside the tensor, which TMA
 //               fills with zeros.
-//   warp 3      gathers Q: the rows of a tile are query heads of one KV head
-//               from one or many sequences (16-byte cp.async, swizzled)
-//   warp 1      tensor memory (512 columns: S0 | S1 | O0 | O1) and MMA issue:
-//               S_i = Q_i K^T, O_i += P_i V with P_i in tensor memory.
+//               Warp 2 also gathers Q: the rows of a tile are query heads of one
+//               KV head from one or many sequences (16-byte cp.async, swizzled).
+//   warps 1, 3  MMA issue of the two halves: S_i = Q_i K^T, O_i += P_i V with P_i
+//               in tensor memory (512 columns: S0 | S1 | O0 | O1).
 //   warps 4-7   softmax of rows 0..127, warps 8-11 of rows 128..255: one thread
 //               a row, in the log2 domain with an integer running maximum that
 //               moves only when a tile's sum passes 2^64 (as in attn.cu).
@@ -57,11 +57,13 @@ struct TcCfg {
     static constexpr int kOffLine = kOffV + kStagesV * kTile;
     static constexpr int kOffStart = (kOffLine + static_cast<int>(sizeof(Line)) + 15) & ~15;
     static constexpr int kOffBar = (kOffStart + static_cast<int>(sizeof(Start)) + 15) & ~15;
-    // q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain, ml_full, q_empty, k_full[], v_full[], k_empty[], v_empty[]
-    static constexpr int kBars = 13 + 2 * (kStagesK + kStagesV);
+    // q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain[2], ml_full, q_empty, turn[2], k_full[], v_full[], k_empty[], v_empty[]
+    static constexpr int kWalks = kTcThreads / 32;
+    static constexpr int kBars = 16 + 2 * (kStagesK + kStagesV);
     static constexpr int kOffMisc = kOffBar + kBars * 8;
-    static constexpr int kOffMl = kOffMisc + 16;        // [128] (m, l) of the second half
-    static constexpr int kSmem = kOffMl + 128 * 8;
+    static constexpr int kOffMl = (kOffMisc + 16 + 15) & ~15;        // [128] (m, l) of the second half
+    static constexpr int kOffWalk = kOffMl + 128 * 8;   // [warps]
+    static constexpr int kSmem = kOffWalk + kWalks * static_cast<int>(sizeof(Walk<kTcTM, kTcKT>)) + 1024;  // + alignment slack
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -76,24 +78,75 @@ __device__ __forceinline__ void hide_columns(int c0, int lim, uint32_t (&h)[64])
         if (c0 + c >= lim) h[c] = 0xff800000u;
 }
 
+// One lane of the warp (non-zero there), the same at every call.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+// D (+)= A B, one K step of 16, A and B in shared memory; takes effect where `lead`.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, bool acc, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(lead)
+        : "memory");
+}
+// The same with A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint64_t db, uint32_t idesc, bool acc, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(ta), "l"(db), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(lead)
+        : "memory");
+}
+// umma_commit where `lead`.
+__device__ __forceinline__ void commit(uint64_t *bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
+        "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+
+// Starts the gather of 128 rows of a piece, the first of them row0, into a Q tile
+// swizzled as TMA would (zeros behind the piece's rows).  By one warp.
+template <int D, int kAtom>
+__device__ __forceinline__ void copy_queries(const PrefixArgs &a, const Piece &x, int row0, uint32_t tile, int lane) {
+    constexpr int kChunks = D / 8, kRpi = 32 / kChunks;  // 16-byte chunks of a row, rows of an instruction
+    const int c = lane % kChunks, r0 = lane / kChunks;
+    const uint32_t dst = tile + (c >> 3) * kAtom + r0 * 128;
+#pragma unroll 1
+    for (int g = 0; g < 128; g += 32) {
+        // element offset of row g + lane, handed to the lanes that copy it
+        const int row = row0 + g + lane, tok = static_cast<int>(fdiv(static_cast<uint32_t>(row), a.div_g));
+        const long long mine =
+            row < x.rows ? (static_cast<long long>(x.tok0 + tok) * a.N + x.kvh * a.G + row - tok * a.G) * D : -1;
+#pragma unroll 8
+        for (int j = 0; j < 32 / kRpi; ++j) {
+            const long long at = __shfl_sync(0xffffffffu, mine, j * kRpi + r0);
+            const uint32_t to = dst + (g + j * kRpi) * 128 + (((c & 7) ^ ((j * kRpi + r0) & 7)) << 4);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                         "l"(a.q + (at < 0 ? 0 : at + c * 8)), "r"(at < 0 ? 0 : 16)
+                         : "memory");
+        }
+    }
+}
+
 // tma: the pages are copied by TMA, else by cp.async.
 template <int D, bool tma>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PrefixArgs a) {
     using C = TcCfg<D>;
-    // (no room to align by hand; a block without static shared memory begins at 1024)
-    extern __shared__ __align__(1024) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (smem_u32(smem) & 1023u) {
-        if (tid == 0) report(a.status, CP_ERR_ALIGNMENT);
-        return;
-    }
     Line &line = *reinterpret_cast<Line *>(smem + C::kOffLine);
     Start &start = *reinterpret_cast<Start *>(smem + C::kOffStart);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *q_full = bar, *s_full = bar + 2, *p_full = bar + 4, *o_full = bar + 6, *o_empty = bar + 8;
-    uint64_t *drain = bar + 10, *ml_full = bar + 11, *q_empty = bar + 12, *k_full = bar + 13, *v_full = k_full + C::kStagesK,
+    uint64_t *drain = bar + 10, *ml_full = bar + 12, *q_empty = bar + 13, *turn = bar + 14, *k_full = bar + 16, *v_full = k_full + C::kStagesK,
              *k_empty = v_full + C::kStagesV, *v_empty = k_empty + C::kStagesK;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
@@ -107,17 +160,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(p_full + i, 4);
             mbar_init(o_full + i, 1);
             mbar_init(o_empty + i, 4);
+            mbar_init(drain + i, 1);
+            mbar_init(turn + i, 4);
         }
-        mbar_init(drain, 1);
         mbar_init(ml_full, 4);
-        mbar_init(q_empty, 1);
+        mbar_init(q_empty, 2);
         for (int s = 0; s < C::kStagesK; ++s) {
             mbar_init(k_full + s, tma ? 1 : 32);
-            mbar_init(k_empty + s, 1);
+            mbar_init(k_empty + s, 2);
         }
         for (int s = 0; s < C::kStagesV; ++s) {
             mbar_init(v_full + s, tma ? 1 : 32);
-            mbar_init(v_empty + s, 1);
+            mbar_init(v_empty + s, 2);
         }
         fence_mbar_init();
         tma_prefetch_desc(&tmK);
@@ -137,19 +191,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t tmem = *tmem_slot;
     uint8_t *sQ = smem + C::kOffQ, *sK = smem + C::kOffK, *sV = smem + C::kOffV;
 
+    Walk<kTcTM, kTcKT> &walk = reinterpret_cast<Walk<kTcTM, kTcKT> *>(smem + C::kOffWalk)[warp];
+    const Piece &x = walk.x;
+    walk.begin(a, line, start, t1 - t0);
     if (warp == 0 || warp == 2) {
-        // -------------------------------------------------------- loads: K by warp 0, V by warp 2
+        // -------------------------------------------------------- loads: K by warp 0, Q and V by warp 2
         const CUtensorMap *map = warp ? &tmV : &tmK;
         uint64_t *full = warp ? v_full : k_full, *empty = warp ? v_empty : k_empty;
         uint8_t *ring = warp ? sV : sK;
         const uint32_t stages = warp ? C::kStagesV : C::kStagesK;
         uint32_t st = 0, ph = 0;  // stage and phase of tile `it`
         const int shift = a.own.shift, rows = min(kTcKT, 1 << shift);  // rows of a copy
-        uint32_t it = 0;
+        uint32_t it = 0, items = 0;
         bool ok = true;
-        for (Walk<kTcTM, kTcKT> walk(a, line, start, t1 - t0); walk.more() && ok;) {
-            const Piece x = walk.next(a, line);
+        while (ok && walk.next(a, line)) {
             if (x.k0 >= x.k1) continue;
+            if (warp == 2) {
+                // Q, gathered: the last item's scores have all been computed
+                if (items && !mbar_wait_warp(q_empty, (items - 1) & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                ++items;
+                for (int i = 0; i < 2 && x.row0 + i * 128 < x.rows; ++i) {
+                    copy_queries<D, C::kAtom>(a, x, x.row0 + i * 128, smem_u32(sQ) + i * C::kTile, lane);
+                    copies_arrive(q_full + i);
+                }
+            }
             PageWindow win;
             win.begin(a, x, (x.k0 * kTcKT) >> shift, lane);
             for (int kt = x.k0; kt < x.k1; ++kt, ++it) {
@@ -187,134 +252,87 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_wait(full + i % stages, (i / stages) & 1u, &no_abort, 100000000ull);
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // -------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
-            constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);
-            const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-            const uint64_t dq1 = smem_desc_sw128(smem_u32(sQ) + C::kTile, 16, 1024);
-            const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
-            const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), C::kAtom, 1024);
-            constexpr uint64_t kStageDesc = C::kTile >> 4;
-            uint32_t kv = 0, items[2] = {0, 0}, tiles[2] = {0, 0}, queries[2] = {0, 0};
-            bool ok = true;
-            // S_i = Q K^T of the tile in K stage st
-            auto qk = [&](int i, uint64_t dq, uint32_t st) {
-                umma_qk_group<D / 16>(tmem + i * 128, dq, dk0 + st * kStageDesc, kIdescQK);
-                umma_commit(s_full + i);
+    } else if (warp < 4) {
+        // -------------------------------------------------------- MMA issue: half 0 by warp 1, half 1 by warp 3
+        // One warp for both halves spent 1000 cycles on the instructions of a half's
+        // tile (waits, 8 + 8 MMAs, commits) and was what a tile waited for.  The warp
+        // runs whole and one lane's instructions take effect, so that the operands
+        // stay in uniform registers.
+        const int i = warp >> 1;
+        const uint32_t lead = elect_lane();
+        const uint32_t tS = tmem + i * 128, tP = tS + 64, tO = tmem + 256 + i * D;
+        constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0), kIdescPV = idesc_bf16_f32(128, D, 0, 1);
+        constexpr uint64_t kStageDesc = C::kTile >> 4;
+        const uint64_t dq = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t dk = smem_desc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dv = smem_desc_sw128(smem_u32(sV), C::kAtom, 1024);
+        uint32_t kv = 0, items = 0, tiles = 0, pieces = 0, wide = 0;  // wide: pieces of more than 128 rows
+        bool ok = true;
+        while (ok && walk.next(a, line)) {
+            const int n = x.k1 - x.k0;
+            if (n <= 0) continue;
+            // up to 128 rows: the halves take the key tiles in turn, both with Q's first tile
+            const bool paired = x.rows - x.row0 <= 128;
+            const int begin = paired ? i : 0, step = paired ? 2 : 1;
+            const uint32_t base = kv;
+            kv += n;
+            // The waits that do not hang on the softmax come first, so that the
+            // products follow its weights at once.
+            auto v_wait = [&](uint32_t at) -> bool {
+                return mbar_wait_warp(v_full + at % C::kStagesV, (at / C::kStagesV) & 1u, abort_flag, a.timeout_ns);
             };
-            // O_i (+)= P_i V of tile `at`; the tile's V is awaited with `await`, given back with `release`
-            auto pv = [&](int i, uint32_t at, bool await, bool release, bool first) -> bool {
-                const uint32_t st = at % C::kStagesV, ph = (at / C::kStagesV) & 1u;
-                if (await) {
-                    if (!mbar_wait(v_full + st, ph, abort_flag, a.timeout_ns)) return false;
-                    if (!tma) fence_async_shared();  // written by cp.async, read by the tensor core
-                }
-                if (first && !mbar_wait(o_empty + i, (items[i] & 1u) ^ 1u, abort_flag, a.timeout_ns)) return false;
-                if (!mbar_wait(p_full + i, tiles[i] & 1u, abort_flag, a.timeout_ns)) return false;
+            // O (+)= P V of tile `at`
+            auto pv = [&](uint32_t at, bool first) -> bool {
+                const uint32_t st = at % C::kStagesV;
+                if (first && !mbar_wait_warp(o_empty + i, (items & 1u) ^ 1u, abort_flag, a.timeout_ns)) return false;
+                if (!mbar_wait_warp(p_full + i, tiles & 1u, abort_flag, a.timeout_ns)) return false;
                 tc_fence_after();
-                ++tiles[i];
-                umma_pv_group(tmem + 256 + i * D, tmem + i * 128 + 64, dv0 + st * kStageDesc, kIdescPV, first ? 0u : 1u);
-                if (release) umma_commit(v_empty + st);
+                ++tiles;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ts(tO, tP + 8 * k, dv + st * kStageDesc + 128 * k, kIdescPV, !first || k > 0, lead);
+                commit(v_empty + st, lead);
+                if (paired) commit(v_empty + st, lead);  // for the other half
                 return true;
             };
-            auto k_wait = [&]() -> bool {
-                if (!mbar_wait(k_full + kv % C::kStagesK, (kv / C::kStagesK) & 1u, abort_flag, a.timeout_ns)) return false;
-                if (!tma) fence_async_shared();
-                tc_fence_after();
-                return true;
-            };
-            for (Walk<kTcTM, kTcKT> walk(a, line, start, t1 - t0); walk.more() && ok;) {
-                const Piece x = walk.next(a, line);
-                const int n = x.k1 - x.k0;
-                if (n <= 0) continue;
-                const bool paired = x.rows - x.row0 <= 128;
-                auto q_wait = [&](int i) -> bool {
-                    if (!mbar_wait(q_full + i, queries[i]++ & 1u, abort_flag, a.timeout_ns)) return false;
-                    fence_async_shared();  // written by cp.async, read by the tensor core
-                    tc_fence_after();
-                    return true;
-                };
-                if (!q_wait(0)) { ok = false; break; }
-                if (paired) {
-                    // tile j belongs to half j & 1; its weights are used when tile j + 2 comes
-                    for (int j = 0; j < n + 2 && ok; ++j) {
-                        const int i = j & 1;
-                        if (j >= 2) {
-                            ok = pv(i, kv - (j < n ? 2 : n + 2 - j), true, true, j < 4);
-                            if (ok && j >= n) {
-                                umma_commit(o_full + i);
-                                ++items[i];
-                            }
-                        }
-                        if (j < n && ok && (ok = k_wait())) {
-                            const uint32_t st = kv % C::kStagesK;
-                            qk(i, dq0, st);
-                            umma_commit(k_empty + st);
-                            if (j == n - 1) umma_commit(q_empty);
-                            ++kv;
-                        }
-                        if (n == 1) ++j;  // no tile for the second half
+            const uint32_t q_phase = paired || i == 0 ? pieces : wide;
+            ++pieces;
+            if (!paired) ++wide;
+            if (begin < n) {
+                if (!mbar_wait_warp(q_full + (paired ? 0 : i), q_phase & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                const uint64_t dqi = dq + (paired ? 0 : i) * kStageDesc;
+                for (int j = begin; j < n && ok; j += step) {
+                    const uint32_t st = (base + j) % C::kStagesK, ph = ((base + j) / C::kStagesK) & 1u;
+                    if (!mbar_wait_warp(k_full + st, ph, abort_flag, a.timeout_ns) || (j > begin && !v_wait(base + j - step))) {
+                        ok = false;
+                        break;
                     }
-                } else {
-                    for (int j = 0; j < n && ok; ++j) {
-                        if (!k_wait()) { ok = false; break; }
-                        const uint32_t st = kv % C::kStagesK;
-                        for (int i = 0; i < 2 && ok; ++i) {
-                            if (j > 0 && !pv(i, kv - 1, i == 0, i == 1, j == 1)) { ok = false; break; }
-                            if (j == 0 && i == 1 && !q_wait(1)) { ok = false; break; }
-                            qk(i, i ? dq1 : dq0, st);
-                        }
-                        if (!ok) break;
-                        umma_commit(k_empty + st);
-                        if (j == n - 1) umma_commit(q_empty);
-                        ++kv;
-                    }
-                    for (int i = 0; i < 2 && ok; ++i) {
-                        if (!pv(i, kv - 1, i == 0, i == 1, n == 1)) { ok = false; break; }
-                        umma_commit(o_full + i);
-                        ++items[i];
-                    }
+                    fence_async_shared();  // Q (and without TMA K and V) was written by cp.async
+                    if (j > begin && !pv(base + j - step, j == begin + step)) { ok = false; break; }
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(tS, dqi + (k / 4) * (C::kAtom >> 4) + (k % 4) * 2,
+                               dk + st * kStageDesc + (k / 4) * (C::kAtom >> 4) + (k % 4) * 2, kIdescQK, k > 0, lead);
+                    commit(s_full + i, lead);
+                    commit(k_empty + st, lead);
+                    if (paired) commit(k_empty + st, lead);  // for the other half
+                    if (j + step >= n) commit(q_empty, lead);
                 }
+                const int last = begin + (n - 1 - begin) / step * step;
+                if (!ok || !v_wait(base + last)) { ok = false; break; }
+                fence_async_shared();
+                if (!pv(base + last, last == begin)) { ok = false; break; }
+                commit(o_full + i, lead);
+                ++items;
+            } else {
+                commit(q_empty, lead);
             }
-            // no MMA may still be running when tensor memory is released
-            umma_commit(drain);
-            volatile int no_abort = 0;
-            mbar_wait(drain, 0, &no_abort, 100000000ull);
         }
+        // no MMA may still be running when tensor memory is released
+        commit(drain + i, lead);
+        volatile int no_abort = 0;
+        mbar_wait(drain + i, 0, &no_abort, 100000000ull);
         __syncwarp();
-    } else if (warp == 3) {
-        // -------------------------------------------------------- Q: rows gathered, swizzled as TMA would
-        uint32_t items = 0;
-        for (Walk<kTcTM, kTcKT> walk(a, line, start, t1 - t0); walk.more();) {
-            const Piece x = walk.next(a, line);
-            if (x.k0 >= x.k1) continue;
-            // the last item's scores have all been computed
-            if (items && !mbar_wait_warp(q_empty, (items - 1) & 1u, abort_flag, a.timeout_ns)) break;
-            ++items;
-            for (int i = 0; i < 2 && x.row0 + i * 128 < x.rows; ++i) {
-                constexpr int kChunks = D / 8, kRpi = 32 / kChunks;  // 16-byte chunks of a row, rows of an instruction
-                const int c = lane % kChunks, r0 = lane / kChunks;
-                const uint32_t dst = smem_u32(sQ) + i * C::kTile + (c >> 3) * C::kAtom + r0 * 128;
-                for (int g = 0; g < 4; ++g) {
-                    // element offset of row 32 g + lane, handed to the lanes that copy it
-                    const int row = x.row0 + i * 128 + 32 * g + lane, tok = static_cast<int>(fdiv(static_cast<uint32_t>(row), a.div_g));
-                    const long long mine =
-                        row < x.rows ? (static_cast<long long>(x.tok0 + tok) * a.N + x.kvh * a.G + row - tok * a.G) * D : -1;
-#pragma unroll 8
-                    for (int j = 0; j < 32 / kRpi; ++j) {
-                        const long long at = __shfl_sync(0xffffffffu, mine, j * kRpi + r0);
-                        const uint32_t to = dst + (32 * g + j * kRpi) * 128 + (((c & 7) ^ ((j * kRpi + r0) & 7)) << 4);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
-                                     "l"(a.q + (at < 0 ? 0 : at + c * 8)), "r"(at < 0 ? 0 : 16)
-                                     : "memory");
-                    }
-                }
-                copies_arrive(q_full + i);
-            }
-        }
-        copies_drain();
     } else if (warp >= 4) {
         // -------------------------------------------------------- softmax
         const int half = (warp - 4) >> 2, in_tile = (warp & 3) * 32 + lane;
@@ -329,8 +347,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // code took 8000 cycles, four times a tile's time.  Nothing is written in it and
         // no barrier touched.
         bool dry = true;
-        for (Walk<kTcTM, kTcKT> walk(a, line, start, t1 - t0); walk.more() && ok;) {
-            const Piece x = walk.next(a, line);
+        // The first half's k-th turn (k > 0) follows the second half's turn k - 1,
+        // which follows the first half's.
+        uint32_t turns = half ? 0u : 0xffffffffu;
+        auto my_turn = [&]() -> bool {
+            const uint32_t k = turns++;
+            return k == 0xffffffffu || mbar_wait_warp(turn + half, k & 1u, abort_flag, a.timeout_ns);
+        };
+        auto pass_turn = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(turn + (half ^ 1));
+        };
+        while (ok && walk.next(a, line)) {
             // up to 128 rows: both halves hold the same rows, tile j of the piece is half j & 1's
             const bool paired = x.rows - x.row0 <= 128;
             const int first_row = x.row0 + (paired ? 0 : half * 128), row = first_row + in_tile, all = x.k1 - x.k0;
@@ -344,14 +372,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int begin = paired ? half : 0, step = paired ? 2 : 1;
             uint32_t tile = kv + begin;
             kv += all;
-            if (begin >= all) continue;  // one tile: nothing for the second half
+            if (begin >= all) {  // one tile: nothing for the second half but its turn
+                if (!my_turn()) { ok = false; break; }
+                pass_turn();
+                continue;
+            }
             // counted from the current tile: keys of the problem, that this row sees, that all rows see
             int past = x.keys - (x.k0 + begin) * 128;
             int limit = (valid ? row_limit(a, x, row) : x.keys) - (x.k0 + begin) * 128;
             int whole = row_limit(a, x, first_row) - (x.k0 + begin) * 128;
             float m_run = -INFINITY, l_run = 0.f;
             for (int n = begin; n < all;) {
-                if (!dry && tma && (paired || half == 0) && past < 128) {
+                if (!dry && tma && past < 128) {
                     const uint32_t st = tile % C::kStagesV, ph = (tile / C::kStagesV) & 1u;
                     if (!mbar_wait_warp(v_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
                     if (in_tile >= past) {
@@ -363,6 +395,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     fence_async_shared();
                 }
                 if (!dry && !mbar_wait_warp(s_full + half, tiles & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                // The halves take turns at the exponentials: left alone they fall into
+                // step, and the tensor cores wait while both compute and the other way round.
+                if (!dry && !my_turn()) { ok = false; break; }
                 tc_fence_after();
                 const bool mask = whole < 128;
                 const int lim = limit;
@@ -390,6 +425,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!dry) tmem_st32_nowait(tS + 96, pb);
                 float sum = s0 + s1;
                 const bool big = !(sum <= 0x1p64f);  // also for inf and NaN
+                if (!dry) pass_turn();
                 tmem_wait_st();
                 if (__any_sync(0xffffffffu, big) && !dry) {
                     // rare: the scores grew by more than 2^64 over the running maximum.
@@ -431,6 +467,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 past -= 128 * step;
                 limit -= 128 * step;
                 whole -= 128 * step;
+            }
+            // a piece of an odd number of tiles: the second half's last turn is empty
+            if (ok && paired && half && (all & 1)) {
+                ok = my_turn();
+                pass_turn();
             }
             if (!ok || !mbar_wait_warp(o_full + half, items & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
             tc_fence_after();
