@@ -24,6 +24,12 @@
 #include "cp_paged.cuh"
 #include "cp_rope.cuh"
 
+#ifndef VM
+#define VM 2
+#endif
+#ifndef VU
+#define VU 2
+#endif
 namespace cpattn {
 namespace {
 
@@ -48,9 +54,9 @@ struct AppendArgs {
 };
 
 template <typename T, int D, int kOrder>
-__global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, VM) append_kernel(const AppendArgs a) {
     using Map = LaneMap<D, kOrder>;
-    constexpr int kU = sizeof(T) == 2 ? 2 : 1;
+    constexpr int kU = sizeof(T) == 2 ? VU : VU / 2;
     const int lane = threadIdx.x & 31, sub = lane / Map::L;
     const Map map(lane, a.rope.half);
     unsigned long long f[Map::kAng];
@@ -124,11 +130,11 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs a)
                         float q = 0.f;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) q = fmaf(r[e], r[e], q);
-                        const float rstd = 1.f / sqrtf(row_sum<Map::L>(q) * (1.f / D) + a.eps);
+                        const float rstd = rsqrtf(row_sum<Map::L>(q) * (1.f / D) + a.eps);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) r[e] = r[e] * rstd * w[e];
                     }
-                    turn_pairs<kOrder>(r, c, s, mask);
+                    turn_pairs<kOrder, false>(r, c, s, mask);
                     if (h < h1) {
                         store8(y + h * D + map.c0, r);
                         store8(y + h * D + map.c1, r + 8);

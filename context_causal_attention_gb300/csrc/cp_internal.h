@@ -5,6 +5,9 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime_api.h>
+#ifdef __CUDACC__
+#include <cuda_runtime.h>
+#endif
 
 #include "../../include/cpattn.h"
 
@@ -31,6 +34,28 @@ inline cp_status cuda_status(cudaError_t e) {
 
 // Reads and clears the sticky launch error of this thread.
 inline cp_status last_launch_status() { return cuda_status(cudaGetLastError()); }
+
+#ifdef __CUDACC__
+// Launches `kernel`; `after`: its blocks may start before the kernel before it in
+// the stream is complete (it waits for itself, wait_for_previous).
+template <typename... P, typename... A>
+cp_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool after, cudaStream_t stream,
+                 const A &...args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = after ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+    if (e != cudaSuccess) cudaGetLastError();
+    return cuda_status(e);
+}
+#endif
 
 // Number of SMs of the current device (cached per device).
 int sm_count();

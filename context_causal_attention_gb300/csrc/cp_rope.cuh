@@ -38,6 +38,7 @@ template <>
 struct Vec8<__nv_bfloat16> {
     uint4 r;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void load_pieces(const uint4 *p, int) { r = *p; }
     __device__ __forceinline__ void to(float *x) const {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -53,6 +54,11 @@ struct Vec8<float> {
     __device__ __forceinline__ void load(const float *p) {
         a = *reinterpret_cast<const float4 *>(p);
         b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    // The two 16-byte pieces `apart` places from one another.
+    __device__ __forceinline__ void load_pieces(const uint4 *p, int apart) {
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + apart);
     }
     __device__ __forceinline__ void to(float *x) const {
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
@@ -142,14 +148,14 @@ template <int kOrder>
 __device__ __forceinline__ constexpr int ib(int e) { return kOrder == 0 ? 8 + e : 2 * e + 1; }
 
 // Rotates the lane's 8 pairs in place.  Values outside the rotated part stay
-// as they are, bit for bit.
-template <int kOrder>
+// as they are, bit for bit (kAll: there are none).
+template <int kOrder, bool kAll>
 __device__ __forceinline__ void turn_pairs(float (&x)[16], const float (&c)[8], const float (&s)[8], uint32_t mask) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float a = x[ia<kOrder>(e)], b = x[ib<kOrder>(e)];
         const float ra = a * c[e] - b * s[e], rb = b * c[e] + a * s[e];
-        const bool t = (mask >> e) & 1u;
+        const bool t = kAll || ((mask >> e) & 1u);
         x[ia<kOrder>(e)] = t ? ra : a;
         x[ib<kOrder>(e)] = t ? rb : b;
     }

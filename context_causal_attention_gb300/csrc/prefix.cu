@@ -366,6 +366,8 @@ struct JoinArgs {
     float *lse;
 };
 
+constexpr int kJoinHeads = 16;
+
 // Where the pieces of a row of head h lie: the slots first .. first + n - 1, row r of each.
 struct RowPieces {
     int first, n, r;
@@ -503,23 +505,23 @@ __global__ void __launch_bounds__(128) join_row_kernel(const JoinArgs a) {
     if (lane == 0) a.lse[static_cast<long long>(h) * a.R + tok] = lse_of(mx, ls);
 }
 
-// Many rows of few pieces: a warp joins up to 32 heads of one token, a lane a
+// Many rows of few pieces: a warp joins kJoinHeads heads of one token, a lane a
 // head's (m, l), then four heads' rows at a time with their loads in flight together.
 template <int D>
 __global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
     constexpr int kV = D / 32;
-    const int lane = threadIdx.x & 31, blocks = (a.N + 31) / 32;
+    const int lane = threadIdx.x & 31, blocks = (a.N + kJoinHeads - 1) / kJoinHeads;
     const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int tok = static_cast<int>(unit / blocks), h0 = static_cast<int>(unit - static_cast<long long>(tok) * blocks) * 32;
+    const int tok = static_cast<int>(unit / blocks), h0 = static_cast<int>(unit - static_cast<long long>(tok) * blocks) * kJoinHeads;
     if (tok >= a.R) return;
     int begin, count;
     const int b = find_sequence(a.cu, a.B, tok, lane, &begin, &count);
     wait_for_previous();
     if (b < 0) return;
-    const int h = h0 + lane, kvh = h / a.G, heads = min(32, a.N - h0);
+    const int heads = min(kJoinHeads, a.N - h0), h = h0 + min(lane, heads - 1), kvh = h / a.G;
     const TokenPart p0(a, 0, b, tok, begin, count), p1(a, 1, b, tok, begin, count);
-    const RowPieces x0 = h < a.N ? p0.row(kvh, h - kvh * a.G) : RowPieces{0, 0, 0};
-    const RowPieces x1 = h < a.N ? p1.row(kvh, h - kvh * a.G) : RowPieces{0, 0, 0};
+    const RowPieces x0 = p0.row(kvh, h - kvh * a.G);
+    const RowPieces x1 = p1.row(kvh, h - kvh * a.G);
     const float2 *s0 = p0.slot_ml + static_cast<long long>(x0.first) * p0.tm + x0.r;
     const float2 *s1 = p1.slot_ml + static_cast<long long>(x1.first) * p1.tm + x1.r;
     float mx = -INFINITY, ls = 0.f;
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
         ls += fast_exp2(ml.x - ref) * ml.y;
     }
     const float inv = mx == -INFINITY ? 0.f : 1.f / ls;
-    if (h < a.N) a.lse[static_cast<long long>(h) * a.R + tok] = lse_of(mx, ls);
+    if (lane < heads) a.lse[static_cast<long long>(h) * a.R + tok] = lse_of(mx, ls);
     for (int k0 = 0; k0 < heads; k0 += 4) {
         float acc[4][kV];
 #pragma unroll
@@ -615,25 +617,6 @@ Shape shape_of(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int6
     return s;
 }
 
-// Launches `kernel`; `after`: its blocks may start before the kernel before it in
-// the stream is complete (it waits for itself, wait_for_previous).
-template <typename... P, typename... A>
-cp_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool after, cudaStream_t stream, const A &...args) {
-    cudaLaunchConfig_t c{};
-    c.gridDim = grid;
-    c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
-    c.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &at;
-    c.numAttrs = after ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
-    if (e != cudaSuccess) cudaGetLastError();
-    return cuda_status(e);
-}
-
 // `after`: the call's other main launch came before this one.
 template <int D>
 cp_status launch_main(const PrefixArgs &a, bool tc, bool after, cudaStream_t stream) {
@@ -692,7 +675,7 @@ cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cuda
     if (a.P == 0) j.part[0] = j.part[1];  // not read into a result: no keys
     const long long rows = static_cast<long long>(a.R) * a.N;
     const bool few = rows <= kJoinRows;
-    const long long units = few ? rows : static_cast<long long>(a.R) * ((a.N + 31) / 32);
+    const long long units = few ? rows : static_cast<long long>(a.R) * ((a.N + kJoinHeads - 1) / kJoinHeads);
     return launch(few ? join_row_kernel<D> : join_token_kernel<D>, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0,
                   true, stream, j);
 }

@@ -20,6 +20,8 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
+#include <type_traits>
 
 #include "cp_internal.h"
 #include "cp_rope.cuh"
@@ -74,10 +76,10 @@ __device__ __forceinline__ void load_weights(const void *w, int bf16, const Map 
     }
 }
 
-template <typename T, int D, int kOrder, bool kNorm>
-__global__ void __launch_bounds__(kThreads, 3) rows_fwd_kernel(const RowsArgs a) {
+template <typename T, int D, int kOrder, bool kNorm, bool kAll>
+__global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(const RowsArgs a) {
     using Map = LaneMap<D, kOrder>;
-    constexpr int kU = sizeof(T) == 2 ? 2 : 1;  // rows of a lane in flight
+    constexpr int kU = sizeof(T) == 2 ? 4 : 2;  // rows of a lane in flight
     const int lane = threadIdx.x & 31, sub = lane / Map::L;
     const Map map(lane, a.rope.half);
     unsigned long long f[Map::kAng];
@@ -126,11 +128,11 @@ __global__ void __launch_bounds__(kThreads, 3) rows_fwd_kernel(const RowsArgs a)
                         float q = 0.f;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) q = fmaf(r[e], r[e], q);
-                        const float rstd = 1.f / sqrtf(row_sum<Map::L>(q) * (1.f / D) + a.eps);
+                        const float rstd = rsqrtf(row_sum<Map::L>(q) * (1.f / D) + a.eps);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) r[e] = r[e] * rstd * w[e];
                     }
-                    turn_pairs<kOrder>(r, c, s, map.mask);
+                    turn_pairs<kOrder, kAll>(r, c, s, map.mask);
                     if (h < h1) {
                         store8(y + h * D + map.c0, r);
                         store8(y + h * D + map.c1, r + 8);
@@ -142,72 +144,128 @@ __global__ void __launch_bounds__(kThreads, 3) rows_fwd_kernel(const RowsArgs a)
 }
 
 // The first `split` blocks take the rows of q, the others those of k, so that a
-// thread keeps one set of weights and of weight gradients.
-template <typename T, int D, int kOrder>
+// thread keeps one set of weights and of weight gradients.  Those and a row's
+// values fill the registers, so the rows to come wait in shared memory: a lane
+// copies the pieces that it will read itself (cp.async, kAhead rows ahead, over the
+// ends of tokens), so no barrier is needed.  S=32768, 32 + 8 heads of 128, bf16, with
+// the sums: one row ahead in registers 197 us, two in shared memory 179 us (1.01 GB).
+constexpr int kAhead = 2;
+template <typename T>
+constexpr int kBwdSmem = (kAhead + 1) * kThreads * 4 * 8 * static_cast<int>(sizeof(T));
+
+template <typename T, int D, int kOrder, bool kAll>
 __global__ void __launch_bounds__(kThreads, 2) norm_bwd_kernel(const RowsArgs a) {
     using Map = LaneMap<D, kOrder>;
+    constexpr int kStages = kAhead + 1;
+    constexpr int kPieces = sizeof(T) / 2;  // 16-byte pieces of 8 values
+    launch_dependents();
+    extern __shared__ __align__(16) uint4 stage_s[];  // [stage][x0, x1, g0, g1: pieces][thread]
     __shared__ float red[kWarps][D];
     const int lane = threadIdx.x & 31, sub = lane / Map::L, warp = threadIdx.x >> 5;
     const Map map(lane, a.rope.half);
     const int t = static_cast<int>(blockIdx.x) >= a.split;
     const int block = blockIdx.x - (t ? a.split : 0), blocks = t ? gridDim.x - a.split : a.split;
     const int heads = a.heads[t], chunks = t ? a.kchunks : a.chunks;
+    const long long units = a.tokens * chunks;
+    const long long step = static_cast<long long>(blocks) * kWarps;
+    // A place in the warp's rows: unit u of token tok, rows hb .. hb + kRows - 1 of its heads up to h1.
+    struct At {
+        long long u, tok;
+        int hb, h1;
+    };
+    auto open = [&](At &p) {
+        p.tok = chunks == 1 ? p.u : p.u / chunks;
+        p.hb = static_cast<int>(p.u - p.tok * chunks) * a.hpu;
+        p.h1 = min(p.hb + a.hpu, heads);
+    };
+    auto advance = [&](At &p) {
+        p.hb += Map::kRows;
+        if (p.hb >= p.h1) {
+            p.u += step;
+            if (p.u < units) open(p);
+        }
+    };
+    At next;
+    next.u = static_cast<long long>(block) * kWarps + warp;
+    if (next.u < units) open(next);
+    At cur = next;
+    int in = 0;
+    auto copy_next = [&]() {
+        if (next.u < units) {
+            const int h = next.hb + sub;
+            if (h < next.h1) {
+                const T *x = static_cast<const T *>(a.x[t]) + next.tok * a.xs[t] + h * D;
+                const T *g = static_cast<const T *>(a.g[t]) + next.tok * a.gs[t] + h * D;
+                const T *src[4] = {x + map.c0, x + map.c1, g + map.c0, g + map.c1};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int k = 0; k < kPieces; ++k)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         smem_u32(stage_s + ((in * 4 + i) * kPieces + k) * kThreads + threadIdx.x)),
+                                     "l"(src[i] + k * (16 / sizeof(T)))
+                                     : "memory");
+            }
+            advance(next);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        in = in + 1 == kStages ? 0 : in + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) copy_next();
     unsigned long long f[Map::kAng];
     load_freqs(a.rope, lane, f);
-    float w[16], dw[16];
+    float w[16], dw[16], c[8], s[8];
     load_weights(a.w[t], a.w_bf16, map, w);
 #pragma unroll
     for (int e = 0; e < 16; ++e) dw[e] = 0.f;
-    const long long units = a.tokens * chunks;
-    const long long step = static_cast<long long>(blocks) * kWarps;
-    for (long long u = static_cast<long long>(block) * kWarps + warp; u < units; u += step) {
-        const long long tok = chunks == 1 ? u : u / chunks;
-        const int h0 = static_cast<int>(u - tok * chunks) * a.hpu, h1 = min(h0 + a.hpu, heads);
-        float c[8], s[8];
-        token_angles<D>(f, token_position(a, tok), a.rope.amp, lane, c, s);
+    long long tok = -1;
+    for (int out = 0; cur.u < units; advance(cur), out = out + 1 == kStages ? 0 : out + 1) {
+        copy_next();
+        if (cur.tok != tok) {
+            tok = cur.tok;
+            token_angles<D>(f, token_position(a, tok), a.rope.amp, lane, c, s);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] = -s[e];
-        const T *x = static_cast<const T *>(a.x[t]) + tok * a.xs[t];
-        const T *g = static_cast<const T *>(a.g[t]) + tok * a.gs[t];
-        T *y = static_cast<T *>(a.y[t]) + tok * a.ys[t];
-        for (int hb = h0; hb < h1; hb += Map::kRows) {
-            const int h = hb + sub;
-            float r[16], d[16];
+            for (int e = 0; e < 8; ++e) s[e] = -s[e];
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+        const int h = cur.hb + sub;
+        const bool in_row = h < cur.h1;
+        float r[16], d[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = d[e] = 0.f;
-            if (h < h1) {
-                Vec8<T> x0, x1, g0, g1;
-                x0.load(x + h * D + map.c0);
-                x1.load(x + h * D + map.c1);
-                g0.load(g + h * D + map.c0);
-                g1.load(g + h * D + map.c1);
-                x0.to(r);
-                x1.to(r + 8);
-                g0.to(d);
-                g1.to(d + 8);
-            }
-            turn_pairs<kOrder>(d, c, s, map.mask);
-            float q = 0.f;
+        for (int e = 0; e < 16; ++e) r[e] = d[e] = 0.f;
+        if (in_row) {
+            const uint4 *mine = stage_s + out * 4 * kPieces * kThreads + threadIdx.x;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) q = fmaf(r[e], r[e], q);
-            const float rstd = 1.f / sqrtf(row_sum<Map::L>(q) * (1.f / D) + a.eps);
-            float m = 0.f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                r[e] *= rstd;
-                if (h < h1) dw[e] = fmaf(d[e], r[e], dw[e]);
-                d[e] *= w[e];
-                m = fmaf(d[e], r[e], m);
-            }
-            m = row_sum<Map::L>(m) * (1.f / D);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) d[e] = rstd * (d[e] - r[e] * m);
-            if (h < h1) {
-                store8(y + h * D + map.c0, d);
-                store8(y + h * D + map.c1, d + 8);
+            for (int i = 0; i < 4; ++i) {
+                Vec8<T> v;
+                v.load_pieces(mine + i * kPieces * kThreads, kThreads);
+                v.to((i < 2 ? r : d) + 8 * (i & 1));
             }
         }
+        turn_pairs<kOrder, kAll>(d, c, s, map.mask);
+        float q = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) q = fmaf(r[e], r[e], q);
+        const float rstd = rsqrtf(row_sum<Map::L>(q) * (1.f / D) + a.eps);
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            r[e] *= rstd;
+            if (in_row) dw[e] = fmaf(d[e], r[e], dw[e]);
+            d[e] *= w[e];
+            m = fmaf(d[e], r[e], m);
+        }
+        m = row_sum<Map::L>(m) * (1.f / D);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) d[e] = rstd * (d[e] - r[e] * m);
+        if (in_row) {
+            T *y = static_cast<T *>(a.y[t]) + tok * a.ys[t] + h * D;
+            store8(y + map.c0, d);
+            store8(y + map.c1, d + 8);
+        }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     // over the rows that the warp held side by side, then over the block's warps
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
@@ -227,21 +285,23 @@ __global__ void __launch_bounds__(kThreads, 2) norm_bwd_kernel(const RowsArgs a)
 
 // dw[t][j] = sum over the partials of q's blocks (t = 0: the first `split`) or
 // k's, in a fixed order; 32 columns to a block.
-__global__ void __launch_bounds__(kThreads) dw_sum_kernel(const float *__restrict__ part, int split, int n, int D,
-                                                          float *dwq, float *dwk) {
-    __shared__ float red[kWarps][32];
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32) dw_sum_kernel(const float *part, int split, int n, int D, float *dwq,
+                                                                float *dwk) {
+    __shared__ float red[kSumWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.y, col = blockIdx.x * 32 + lane;
+    wait_for_previous();
     float v = 0.f;
-    for (int i = (t ? split : 0) + warp; i < (t ? n : split); i += kWarps)
-        v += __ldg(part + static_cast<long long>(i) * D + col);
+#pragma unroll 4
+    for (int i = (t ? split : 0) + warp; i < (t ? n : split); i += kSumWarps)
+        v += part[static_cast<long long>(i) * D + col];
     red[warp][lane] = v;
     __syncthreads();
-    if (warp) return;
-    v = 0.f;
+    v = red[lane][warp];  // column `warp`: its 32 partial sums across the lanes
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) v += red[k][lane];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     float *out = t ? dwk : dwq;
-    if (out) out[col] = v;
+    if (out && lane == 0) out[blockIdx.x * 32 + warp] = v;
 }
 
 // ---------------------------------------------------------------- host side
@@ -333,29 +393,45 @@ int plan_units(RowsArgs *a, int rows, int warps_per_sm) {
     return static_cast<int>(blocks < kMaxGrid ? blocks : kMaxGrid);
 }
 
-template <typename T, int D, int kOrder>
+template <typename T, int D, int kOrder, bool kAll>
 cp_status launch_fwd(RowsArgs &a, bool norm, cudaStream_t stream) {
     const int grid = plan_units(&a, LaneMap<D, kOrder>::kRows, 16);
     if (norm)
-        rows_fwd_kernel<T, D, kOrder, true><<<grid, kThreads, 0, stream>>>(a);
+        rows_fwd_kernel<T, D, kOrder, true, kAll><<<grid, kThreads, 0, stream>>>(a);
     else
-        rows_fwd_kernel<T, D, kOrder, false><<<grid, kThreads, 0, stream>>>(a);
+        rows_fwd_kernel<T, D, kOrder, false, kAll><<<grid, kThreads, 0, stream>>>(a);
     return last_launch_status();
 }
 
-cp_status run_fwd(RowsArgs &a, bool norm, int64_t D, cp_dtype dtype, const cp_rope *rope, cudaStream_t stream) {
-    const bool inter = rope && rope->order == CP_ROPE_INTERLEAVED;
-    if (dtype == CP_BF16) {
-        using T = __nv_bfloat16;
-        if (D == 128) return inter ? launch_fwd<T, 128, 1>(a, norm, stream) : launch_fwd<T, 128, 0>(a, norm, stream);
-        return inter ? launch_fwd<T, 64, 1>(a, norm, stream) : launch_fwd<T, 64, 0>(a, norm, stream);
+// Calls f<T, D, order, all>() of the call's dtype, head size, order and whether the whole head turns.
+template <typename F>
+cp_status dispatch(int64_t D, cp_dtype dtype, const cp_rope *rope, F f) {
+    const bool inter = rope && rope->order == CP_ROPE_INTERLEAVED, all = rope && rope->rot_dim == D;
+    auto with = [&](auto t, auto d) -> cp_status {
+        using T = decltype(t);
+        constexpr int kD = decltype(d)::value;
+        if (inter) return all ? f.template operator()<T, kD, 1, true>() : f.template operator()<T, kD, 1, false>();
+        return all ? f.template operator()<T, kD, 0, true>() : f.template operator()<T, kD, 0, false>();
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (dtype == CP_BF16) return D == 128 ? with(__nv_bfloat16{}, D128{}) : with(__nv_bfloat16{}, D64{});
+    return D == 128 ? with(float{}, D128{}) : with(float{}, D64{});
+}
+struct Fwd {
+    RowsArgs &a;
+    bool norm;
+    cudaStream_t stream;
+    template <typename T, int D, int kOrder, bool kAll>
+    cp_status operator()() const {
+        return launch_fwd<T, D, kOrder, kAll>(a, norm, stream);
     }
-    if (D == 128)
-        return inter ? launch_fwd<float, 128, 1>(a, norm, stream) : launch_fwd<float, 128, 0>(a, norm, stream);
-    return inter ? launch_fwd<float, 64, 1>(a, norm, stream) : launch_fwd<float, 64, 0>(a, norm, stream);
+};
+cp_status run_fwd(RowsArgs &a, bool norm, int64_t D, cp_dtype dtype, const cp_rope *rope, cudaStream_t stream) {
+    return dispatch(D, dtype, rope, Fwd{a, norm, stream});
 }
 
-template <typename T, int D, int kOrder>
+template <typename T, int D, int kOrder, bool kAll>
 cp_status launch_bwd_typed(RowsArgs &a, float *dwq, float *dwk, cudaStream_t stream) {
     constexpr int rows = LaneMap<D, kOrder>::kRows;
     plan_units(&a, rows, 16);
@@ -376,13 +452,29 @@ cp_status launch_bwd_typed(RowsArgs &a, float *dwq, float *dwk, cudaStream_t str
     }
     a.split = static_cast<int>(gq);
     const int grid = static_cast<int>(gq + gk);
-    norm_bwd_kernel<T, D, kOrder><<<grid, kThreads, 0, stream>>>(a);
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(norm_bwd_kernel<T, D, kOrder, kAll>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   kBwdSmem<T>);
+    });
+    if (err != cudaSuccess) return cuda_status(err);
+    norm_bwd_kernel<T, D, kOrder, kAll><<<grid, kThreads, kBwdSmem<T>, stream>>>(a);
     const cp_status st = last_launch_status();
     if (st != CP_OK) return st;
-    dw_sum_kernel<<<dim3(D / 32, 2), kThreads, 0, stream>>>(a.part, a.split, grid, D, nq ? dwq : nullptr,
-                                                            nk ? dwk : nullptr);
-    return last_launch_status();
+    return launch(dw_sum_kernel, dim3(D / 32, 2), kSumWarps * 32, 0, true, stream, a.part, a.split, grid, D,
+                  nq ? dwq : nullptr, nk ? dwk : nullptr);
 }
+
+struct Bwd {
+    RowsArgs &a;
+    float *dwq, *dwk;
+    cudaStream_t stream;
+    template <typename T, int D, int kOrder, bool kAll>
+    cp_status operator()() const {
+        return launch_bwd_typed<T, D, kOrder, kAll>(a, dwq, dwk, stream);
+    }
+};
 
 cp_status rope_call(const void *q, const void *k, const int32_t *pos, int64_t C, int64_t B, int64_t s, int64_t N,
                     int64_t Nkv, int64_t D, int64_t qs, int64_t ks, cp_dtype dtype, const cp_rope *rope, void *qo,
@@ -524,18 +616,5 @@ extern "C" cp_status cp_qk_norm_rope_bwd(const void *dq_out, const void *dk_out,
     a.w_bf16 = w_dtype == CP_BF16;
     a.eps = eps;
     a.part = static_cast<float *>(workspace);
-    const bool inter = rope && rope->order == CP_ROPE_INTERLEAVED;
-    if (dtype == CP_BF16) {
-        using T = __nv_bfloat16;
-        if (D == 128)
-            return inter ? launch_bwd_typed<T, 128, 1>(a, dwq, dwk, stream)
-                         : launch_bwd_typed<T, 128, 0>(a, dwq, dwk, stream);
-        return inter ? launch_bwd_typed<T, 64, 1>(a, dwq, dwk, stream)
-                     : launch_bwd_typed<T, 64, 0>(a, dwq, dwk, stream);
-    }
-    if (D == 128)
-        return inter ? launch_bwd_typed<float, 128, 1>(a, dwq, dwk, stream)
-                     : launch_bwd_typed<float, 128, 0>(a, dwq, dwk, stream);
-    return inter ? launch_bwd_typed<float, 64, 1>(a, dwq, dwk, stream)
-                 : launch_bwd_typed<float, 64, 0>(a, dwq, dwk, stream);
+    return dispatch(D, dtype, rope, Bwd{a, dwq, dwk, stream});
 }
