@@ -24,12 +24,6 @@
 #include "cp_paged.cuh"
 #include "cp_rope.cuh"
 
-#ifndef VM
-#define VM 2
-#endif
-#ifndef VU
-#define VU 2
-#endif
 namespace cpattn {
 namespace {
 
@@ -50,94 +44,101 @@ struct AppendArgs {
     PageTable pt;
     const int32_t *cu, *kv_len;
     long long tokens, pos_base;
-    int chunks, hpu;
+    int group, chunks, hpu;
 };
 
+// Sequence b's new token `tok` (the b-th begins at row `begin` and has `count`): its own index, and its slot or -1.
+__device__ __forceinline__ long long slot_of(const AppendArgs &a, int b, int tok, int begin, int count, long long *idx) {
+    *idx = static_cast<long long>(__ldg(a.kv_len + b)) - count + (tok - begin);
+    const long long slot = a.pt.slot(b, *idx);
+    if (slot < 0) atomicExch(&g_cache_status, static_cast<int>(CP_ERR_PAGE));
+    return slot;
+}
+
+// A unit is `group` tokens in a row with all their heads, or (group 1) `hpu` heads
+// of one token.  The rows of q, k and v of a token make one list, so that four rows
+// of a lane are in flight whichever tensor they belong to.
 template <typename T, int D, int kOrder>
-__global__ void __launch_bounds__(kThreads, VM) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs a) {
     using Map = LaneMap<D, kOrder>;
-    constexpr int kU = sizeof(T) == 2 ? VU : VU / 2;
+    constexpr int kU = sizeof(T) == 2 ? 4 : 2;
     const int lane = threadIdx.x & 31, sub = lane / Map::L;
     const Map map(lane, a.rope.half);
     unsigned long long f[Map::kAng];
     load_freqs(a.rope, lane, f);
-    const int all = a.heads[0] + a.heads[1] + a.heads[2];
-    const long long units = a.tokens * a.chunks;
+    const int nq = a.heads[0], nk = a.heads[1], all = nq + 2 * nk;
+    const long long units = (a.tokens + a.group - 1) / a.group * a.chunks;
     const long long step = static_cast<long long>(gridDim.x) * kWarps;
     for (long long u = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units; u += step) {
-        const int tok = static_cast<int>(a.chunks == 1 ? u : u / a.chunks);
-        const int first = static_cast<int>(u - static_cast<long long>(tok) * a.chunks) * a.hpu;
+        const int tok0 = static_cast<int>(a.chunks == 1 ? u * a.group : u / a.chunks);
+        const int first = a.chunks == 1 ? 0 : static_cast<int>(u - static_cast<long long>(tok0) * a.chunks) * a.hpu;
         const int last = min(first + a.hpu, all);
-        int begin, count;
-        const int b = find_sequence(a.cu, a.pt.B, tok, lane, &begin, &count);
-        if (b < 0) continue;  // a row behind the last sequence
-        const long long idx = static_cast<long long>(__ldg(a.kv_len + b)) - count + (tok - begin);
-        const long long slot = a.pt.slot(b, idx);
-        if (slot < 0) {
-            if (lane == 0) atomicExch(&g_cache_status, static_cast<int>(CP_ERR_PAGE));
-            continue;
-        }
-        float c[8], s[8];
-        token_angles<D>(f, a.pos_base + idx, a.rope.amp, lane, c, s);
-#pragma unroll 1
-        for (int t = 0; t < 3; ++t) {
-            const int base = t == 0 ? 0 : (t == 1 ? a.heads[0] : a.heads[0] + a.heads[1]);
-            const int h0 = max(first - base, 0), h1 = min(last - base, a.heads[t]);
-            if (h0 >= h1) continue;
-            const T *x = static_cast<const T *>(a.x[t]) + tok * a.xs[t];
-            __nv_bfloat16 *y = t == 0 ? a.q_out + static_cast<long long>(tok) * a.heads[0] * D
-                                      : a.cache[t - 1] + slot * a.heads[1] * D;
-            const bool norm = t < 2 && a.norm[t];
-            float w[16];
-            if (norm) {
-                if (a.w_bf16) {
-                    Vec8<__nv_bfloat16> v;
-                    v.load(static_cast<const __nv_bfloat16 *>(a.w[t]) + map.c0);
-                    v.to(w);
-                    v.load(static_cast<const __nv_bfloat16 *>(a.w[t]) + map.c1);
-                    v.to(w + 8);
-                } else {
-                    Vec8<float> v;
-                    v.load(static_cast<const float *>(a.w[t]) + map.c0);
-                    v.to(w);
-                    v.load(static_cast<const float *>(a.w[t]) + map.c1);
-                    v.to(w + 8);
-                }
+        // lane i looks up token tok0 + i
+        long long idx = 0, slot = -1;
+        if (a.group == 1) {
+            int begin, count;
+            const int b = find_sequence(a.cu, a.pt.B, tok0, lane, &begin, &count);
+            if (b < 0) continue;  // a row behind the last sequence
+            slot = slot_of(a, b, tok0, begin, count, &idx);
+        } else if (lane < a.group && tok0 + lane < a.tokens) {
+            const int tok = tok0 + lane;
+            int lo = 0, hi = a.pt.B - 1;  // the last sequence that begins at or before tok
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (__ldg(a.cu + mid) <= tok) lo = mid; else hi = mid - 1;
             }
-            const uint32_t mask = t < 2 ? map.mask : 0u;
-            for (int hb = h0; hb < h1; hb += kU * Map::kRows) {
+            const int begin = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1);
+            if (tok >= begin && tok < end) slot = slot_of(a, lo, tok, begin, end - begin, &idx);
+        }
+        for (int i = 0; i < a.group; ++i) {
+            const long long to = __shfl_sync(0xffffffffu, slot, i), at = __shfl_sync(0xffffffffu, idx, i);
+            const int tok = tok0 + i;
+            if (to < 0) continue;  // behind the last sequence, or reported
+            float c[8], s[8];
+            if (a.rope.half) token_angles<D>(f, a.pos_base + at, a.rope.amp, lane, c, s);
+            for (int hb = first; hb < last; hb += kU * Map::kRows) {
                 Vec8<T> v0[kU], v1[kU];
 #pragma unroll
-                for (int i = 0; i < kU; ++i) {
-                    const int h = hb + i * Map::kRows + sub;
-                    if (h < h1) {
-                        v0[i].load(x + h * D + map.c0);
-                        v1[i].load(x + h * D + map.c1);
+                for (int k = 0; k < kU; ++k) {
+                    const int h = hb + k * Map::kRows + sub;
+                    if (h < last) {
+                        const int t = h < nq ? 0 : (h < nq + nk ? 1 : 2);
+                        const T *x = static_cast<const T *>(a.x[t]) + tok * a.xs[t] + (h - (t == 0 ? 0 : nq + (t - 1) * nk)) * D;
+                        v0[k].load(x + map.c0);
+                        v1[k].load(x + map.c1);
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < kU; ++i) {
-                    if (hb + i * Map::kRows >= h1) break;  // uniform over the warp
-                    const int h = hb + i * Map::kRows + sub;
+                for (int k = 0; k < kU; ++k) {
+                    if (hb + k * Map::kRows >= last) break;  // uniform over the warp
+                    const int h = hb + k * Map::kRows + sub;
+                    const int t = h < nq ? 0 : (h < nq + nk ? 1 : 2);
                     float r[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) r[e] = 0.f;
-                    if (h < h1) {
-                        v0[i].to(r);
-                        v1[i].to(r + 8);
+                    if (h < last) {
+                        v0[k].to(r);
+                        v1[k].to(r + 8);
                     }
-                    if (norm) {
+                    const bool norm = t < 2 && a.norm[t];
+                    if (__any_sync(0xffffffffu, norm)) {
                         float q = 0.f;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) q = fmaf(r[e], r[e], q);
                         const float rstd = rsqrtf(row_sum<Map::L>(q) * (1.f / D) + a.eps);
+                        if (norm) {
+                            float w[16];
+                            load_weights(a.w[t], a.w_bf16, map, w);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) r[e] = r[e] * rstd * w[e];
+                            for (int e = 0; e < 16; ++e) r[e] = r[e] * rstd * w[e];
+                        }
                     }
-                    turn_pairs<kOrder, false>(r, c, s, mask);
-                    if (h < h1) {
-                        store8(y + h * D + map.c0, r);
-                        store8(y + h * D + map.c1, r + 8);
+                    if (a.rope.half) turn_pairs<kOrder, false>(r, c, s, t < 2 ? map.mask : 0u);
+                    if (h < last) {
+                        __nv_bfloat16 *y = t == 0 ? a.q_out + (static_cast<long long>(tok) * nq + h) * D
+                                                  : a.cache[t - 1] + (to * nk + h - nq - (t - 1) * nk) * D;
+                        store8(y + map.c0, r);
+                        store8(y + map.c1, r + 8);
                     }
                 }
             }
@@ -149,12 +150,16 @@ template <typename T, int D, int kOrder>
 cp_status launch_append(AppendArgs &a, cudaStream_t stream) {
     constexpr int rows = LaneMap<D, kOrder>::kRows;
     const int heads = a.heads[0] + a.heads[1] + a.heads[2], most = (heads + rows - 1) / rows;
-    // all heads of a token in one unit, fewer where there are too few tokens to give every SM 16 warps
-    long long chunks = (static_cast<long long>(sm_count()) * 16 + a.tokens - 1) / a.tokens;
+    // as many tokens to a unit (their lookups go side by side) as leave every SM 16
+    // warps, up to 32; where there are fewer tokens than that, fewer heads of one
+    const long long warps = static_cast<long long>(sm_count()) * 16;
+    const long long group = (a.tokens + warps - 1) / warps;
+    a.group = static_cast<int>(group < 32 ? group : 32);
+    long long chunks = (warps + a.tokens - 1) / a.tokens;
     chunks = chunks < 1 ? 1 : (chunks > most ? most : chunks);
     a.hpu = static_cast<int>((most + chunks - 1) / chunks) * rows;
     a.chunks = (heads + a.hpu - 1) / a.hpu;
-    const long long blocks = (a.tokens * a.chunks + kWarps - 1) / kWarps;
+    const long long blocks = ((a.tokens + a.group - 1) / a.group * a.chunks + kWarps - 1) / kWarps;
     const long long cap = static_cast<long long>(sm_count()) * 4;
     append_kernel<T, D, kOrder><<<static_cast<unsigned>(blocks < cap ? blocks : cap), kThreads, 0, stream>>>(a);
     return last_launch_status();

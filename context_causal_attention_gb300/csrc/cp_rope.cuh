@@ -161,6 +161,24 @@ __device__ __forceinline__ void turn_pairs(float (&x)[16], const float (&c)[8], 
     }
 }
 
+// This lane's 16 weights.
+template <typename Map>
+__device__ __forceinline__ void load_weights(const void *w, int bf16, const Map &m, float (&o)[16]) {
+    if (bf16) {
+        Vec8<__nv_bfloat16> v;
+        v.load(static_cast<const __nv_bfloat16 *>(w) + m.c0);
+        v.to(o);
+        v.load(static_cast<const __nv_bfloat16 *>(w) + m.c1);
+        v.to(o + 8);
+    } else {
+        Vec8<float> v;
+        v.load(static_cast<const float *>(w) + m.c0);
+        v.to(o);
+        v.load(static_cast<const float *>(w) + m.c1);
+        v.to(o + 8);
+    }
+}
+
 // Sum over the L lanes of a row.
 template <int L>
 __device__ __forceinline__ float row_sum(float v) {

@@ -58,24 +58,6 @@ __device__ __forceinline__ long long token_position(const RowsArgs &a, long long
     return __ldg(a.pos + static_cast<long long>(u / static_cast<uint32_t>(a.B)) * a.s + (t - u * a.s));
 }
 
-// This lane's 16 weights.
-template <typename Map>
-__device__ __forceinline__ void load_weights(const void *w, int bf16, const Map &m, float (&o)[16]) {
-    if (bf16) {
-        Vec8<__nv_bfloat16> v;
-        v.load(static_cast<const __nv_bfloat16 *>(w) + m.c0);
-        v.to(o);
-        v.load(static_cast<const __nv_bfloat16 *>(w) + m.c1);
-        v.to(o + 8);
-    } else {
-        Vec8<float> v;
-        v.load(static_cast<const float *>(w) + m.c0);
-        v.to(o);
-        v.load(static_cast<const float *>(w) + m.c1);
-        v.to(o + 8);
-    }
-}
-
 template <typename T, int D, int kOrder, bool kNorm, bool kAll>
 __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(const RowsArgs a) {
     using Map = LaneMap<D, kOrder>;
