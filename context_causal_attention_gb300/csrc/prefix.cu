@@ -130,7 +130,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    launch_dependents();
     if (tid == 0) {
         *abort_flag = 0;
         for (int s = 0; s < C::kStages; ++s) {
@@ -140,6 +139,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         for (int i = 0; i < kGroups; ++i) mbar_init(go + i, 4);
         fence_mbar_init();
     }
+    // As the call's only main launch it follows the kernels that made its inputs;
+    // behind the 256-row launch it starts when that one has seen them complete.
+    if (!a.cost_own) wait_for_previous();
+    launch_dependents();
     scan_line<kTM, kKT>(a, line, reinterpret_cast<int *>(smem + C::kOffLists), C::kListed,
                         blockIdx.x == 0 && blockIdx.y == 0);
     long long t0, t1;
@@ -617,9 +620,8 @@ Shape shape_of(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int6
     return s;
 }
 
-// `after`: the call's other main launch came before this one.
 template <int D>
-cp_status launch_main(const PrefixArgs &a, bool tc, bool after, cudaStream_t stream) {
+cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [] {
@@ -634,7 +636,7 @@ cp_status launch_main(const PrefixArgs &a, bool tc, bool after, cudaStream_t str
     if (err != cudaSuccess) return cuda_status(err);
     const int sms = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
     const dim3 grid(a.lanes, sms / a.lanes);
-    if (!tc) return launch(prefix_mma_kernel<D>, grid, kMmaThreads, MmaCfg<D>::kSmem, after, stream, a);
+    if (!tc) return launch(prefix_mma_kernel<D>, grid, kMmaThreads, MmaCfg<D>::kSmem, true, stream, a);
     const int64_t rows = static_cast<int64_t>(a.own.n_pages) << a.own.shift;
     const int page = 1 << a.own.shift, box = page < kTcKT ? page : kTcKT;
     // at D = 64 a head's row is 128 bytes and its neighbour another head's
@@ -643,8 +645,8 @@ cp_status launch_main(const PrefixArgs &a, bool tc, bool after, cudaStream_t str
     if (!make_map(&mk, a.k, D, a.Nkv, rows, 1, box, l2) || !make_map(&mv, a.v, D, a.Nkv, rows, 1, box, l2))
         return CP_ERR_CUDA;
     if (page >= kTmaPage)
-        return launch(prefix_tc_kernel<D, true>, grid, kTcThreads, TcCfg<D>::kSmem, false, stream, mk, mv, a);
-    return launch(prefix_tc_kernel<D, false>, grid, kTcThreads, TcCfg<D>::kSmem, false, stream, mk, mv, a);
+        return launch(prefix_tc_kernel<D, true>, grid, kTcThreads, TcCfg<D>::kSmem, true, stream, mk, mv, a);
+    return launch(prefix_tc_kernel<D, false>, grid, kTcThreads, TcCfg<D>::kSmem, true, stream, mk, mv, a);
 }
 
 template <int D>
@@ -665,7 +667,7 @@ cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cuda
         a.slot_ml = reinterpret_cast<float2 *>(w + s.slot_ml[k]);
         a.slot_o = reinterpret_cast<float *>(w + s.slot_o[k]);
         a.slots = static_cast<int>(s.slots[k]);
-        const cp_status st = launch_main<D>(a, k == 1, k == 0 && s.slots[1], stream);
+        const cp_status st = launch_main<D>(a, k == 1, stream);
         if (st != CP_OK) return st;
         for (int which = 0; which < 2; ++which)
             if (which ? a.with_own : a.with_prefix)

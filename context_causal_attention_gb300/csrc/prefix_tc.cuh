@@ -151,7 +151,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
 
-    launch_dependents();
     if (tid == 0) {
         *abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
@@ -177,6 +176,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
+    // its blocks may have started under the kernels that made its inputs
+    wait_for_previous();
+    launch_dependents();
     scan_line<kTcTM, kTcKT>(a, line, nullptr, 0, blockIdx.x == 0 && blockIdx.y == 0);
     long long t0, t1;
     if (!share_of(a, line, &t0, &t1)) return;
