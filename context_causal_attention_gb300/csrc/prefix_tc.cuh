@@ -209,8 +209,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         while (ok && walk.next(a, line)) {
             if (x.k0 >= x.k1) continue;
             if (warp == 2) {
-                // Q, gathered: the last item's scores have all been computed
+                // Q, gathered: the last piece's scores have all been computed, and its V has
+                // landed (its K has, or they would not)
                 if (items && !mbar_wait_warp(q_empty, (items - 1) & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                for (uint32_t i = it > stages ? it - stages : 0; i < it && ok; ++i)
+                    ok = mbar_wait_warp(full + i % stages, (i / stages) & 1u, abort_flag, a.timeout_ns);
+                if (!ok) break;
                 ++items;
                 for (int i = 0; i < 2 && x.row0 + i * 128 < x.rows; ++i) {
                     copy_queries<D, C::kAtom>(a, x, x.row0 + i * 128, smem_u32(sQ) + i * C::kTile, lane);
@@ -297,11 +301,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (paired) commit(v_empty + st, lead);  // for the other half
                 return true;
             };
+            // Also with no tile for this half (a piece of one tile): Q of a piece is
+            // loaded when both halves are done with the last one's, so that neither
+            // waits for a stage or a query tile more than one phase ahead, where the
+            // parity would tell it the opposite.
             const uint32_t q_phase = paired || i == 0 ? pieces : wide;
             ++pieces;
             if (!paired) ++wide;
+            if (!mbar_wait_warp(q_full + (paired ? 0 : i), q_phase & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
             if (begin < n) {
-                if (!mbar_wait_warp(q_full + (paired ? 0 : i), q_phase & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
                 const uint64_t dqi = dq + (paired ? 0 : i) * kStageDesc;
                 for (int j = begin; j < n && ok; j += step) {
                     const uint32_t st = (base + j) % C::kStagesK, ph = ((base + j) / C::kStagesK) & 1u;

@@ -92,6 +92,13 @@ CASES = {
     "half_tile": ([5, 5], [5, 9], 100, 8, 2, 64, 16, 0),
     "half_tile_long": ([6, 1], [70, 2900], 5000, 24, 3, 128, 64, 0),
     "half_tiles_mixed": ([70, 20, 1, 90], [900, 20, 333, 1200], 400, 16, 4, 64, 32, 3),
+    # more pieces than blocks: every block goes from piece to piece, of one, of an odd
+    # and of an even number of key tiles, of up to 128 and of more rows
+    "short_prompts": ([20] * 400, [20 + 7 * i % 109 for i in range(400)], 100, 4, 1, 64, 16, 0),
+    "mixed_prompts": ([1 + 13 * i % 60 for i in range(300)], [61 + 37 * i % 700 for i in range(300)], 130, 4, 1, 128,
+                      64, 2),
+    "mixed_prompts_small_pages": ([1 + 29 * i % 90 for i in range(200)], [91 + 53 * i % 500 for i in range(200)], 0, 6,
+                                  2, 64, 16, 0),
     "long": ([1, 2], [3000, 9000], 20000, 8, 2, 128, 64, 0),
 }
 
