@@ -51,6 +51,8 @@ struct TcCfg {
     static constexpr int kTile = kAtom * kAtoms;
     // Stages of K and of V: a third of K (D = 128) or six of both (D = 64) measured the same.
     static constexpr int kStagesK = D == 128 ? 2 : 4, kStagesV = D == 128 ? 2 : 4;
+    // even: a stage then serves the same half through a piece whose halves take turns
+    static_assert(kStagesK % 2 == 0 && kStagesV % 2 == 0, "stages");
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = 2 * kTile;
     static constexpr int kOffV = kOffK + kStagesK * kTile;
@@ -305,10 +307,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // loaded when both halves are done with the last one's, so that neither
             // waits for a stage or a query tile more than one phase ahead, where the
             // parity would tell it the opposite.
-            const uint32_t q_phase = paired || i == 0 ? pieces : wide;
-            ++pieces;
-            if (!paired) ++wide;
-            if (!mbar_wait_warp(q_full + (paired ? 0 : i), q_phase & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+            if (!mbar_wait_warp(q_full, pieces++ & 1u, abort_flag, a.timeout_ns) ||
+                (!paired && i && !mbar_wait_warp(q_full + 1, wide++ & 1u, abort_flag, a.timeout_ns))) {
+                ok = false;
+                break;
+            }
             if (begin < n) {
                 const uint64_t dqi = dq + (paired ? 0 : i) * kStageDesc;
                 for (int j = begin; j < n && ok; j += step) {
@@ -393,17 +396,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             int whole = row_limit(a, x, first_row) - (x.k0 + begin) * 128;
             float m_run = -INFINITY, l_run = 0.f;
             for (int n = begin; n < all;) {
-                if (!dry && tma && past < 128) {
-                    const uint32_t st = tile % C::kStagesV, ph = (tile / C::kStagesV) & 1u;
-                    if (!mbar_wait_warp(v_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
-                    if (in_tile >= past) {
-                        uint8_t *dst = sV + st * C::kTile + in_tile * 128;
-#pragma unroll
-                        for (int c = 0; c < D / 8; ++c)
-                            *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kAtom + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_async_shared();
-                }
                 if (!dry && !mbar_wait_warp(s_full + half, tiles & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
                 // The halves take turns at the exponentials: left alone they fall into
                 // step, and the tensor cores wait while both compute and the other way round.
@@ -470,6 +462,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     l_run = 0.f;
                     continue;
                 }
+                if (tma && past < 128) {
+                    // The scores of this tile came after the product of the stage's last tile was
+                    // issued, so that one's V has landed: the wait is for this tile's phase.
+                    const uint32_t st = tile % C::kStagesV, ph = (tile / C::kStagesV) & 1u;
+                    if (!mbar_wait_warp(v_full + st, ph, abort_flag, a.timeout_ns)) { ok = false; break; }
+                    if (in_tile >= past) {
+                        uint8_t *dst = sV + st * C::kTile + in_tile * 128;
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kAtom + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_async_shared();
+                }
+                __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + half);
                 n += step;
                 tile += step;

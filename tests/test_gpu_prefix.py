@@ -200,6 +200,35 @@ def test_same_bits_twice_and_by_graph(cuda_dev):
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), step
 
 
+@pytest.mark.parametrize("new,N,Nkv,D,page", [(6, 64, 8, 128, 64), (21, 40, 8, 128, 128), (6, 64, 8, 128, 16),
+                                               (40, 16, 4, 64, 64)])
+def test_repeated_calls_agree(cuda_dev, new, N, Nkv, D, page):
+    """Many blocks, pieces and last tiles that are not full, over and over with other work
+    between: the bits never change (a wait that passes too early shows as a
+    call that differs now and then), and they are right."""
+    g = torch.Generator().manual_seed(new * page)
+    lens = [new + int(x) for x in torch.randint(0, 1300, (24,), generator=g)]
+    c = Call(11, [1 + (new - 1) * (i % 3) // 2 for i in range(24)], lens, 777, N, Nkv, D, page)
+    o, lse = c.run(cuda_dev)
+    c.check(o, lse)
+    junk = torch.empty(64 << 20, device=cuda_dev)
+    q, k, v, pages, table, cu, kv_len = c.dev
+    for i in range(40):
+        if i % 2:
+            junk.fill_(i)
+        o2, lse2 = F.cp_prefix_attn_fwd(q, k, v, pages, 777, table, cu, kv_len, new)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2), i
+
+
+@pytest.mark.parametrize("hint", [1, 3, 40])
+def test_any_hint_is_right(cuda_dev, hint):
+    """max_new chooses the tiles only: one that is far off changes no result but by rounding."""
+    c = Call(12, [40, 1, 0, 17], [300, 5, 9, 17], 200, 8, 2, 64, 32)
+    c.run(cuda_dev)
+    q, k, v, pages, table, cu, kv_len = c.dev
+    c.check(*F.cp_prefix_attn_fwd(q, k, v, pages, 200, table, cu, kv_len, hint))
+
+
 def test_outputs_and_workspace_stay_in_bounds(cuda_dev):
     c = Call(8, [3, 40, 1], [3, 300, 77], 130, 6, 2, 64, 16, pad=2)
     c.run(cuda_dev)
