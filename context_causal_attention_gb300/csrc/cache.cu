@@ -184,7 +184,7 @@ cp_status check_pages(int64_t n_pages, int64_t page_size, int64_t B, int64_t max
         return CP_ERR_SHAPE;
     if (D != 64 && D != 128) return CP_ERR_UNSUPPORTED;
     if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return CP_ERR_UNSUPPORTED;
-    if (n_pages * page_size > INT32_MAX || max_pages * page_size > INT32_MAX) return CP_ERR_SHAPE;
+    if (n_pages * page_size > kMaxKeys || max_pages * page_size > kMaxKeys) return CP_ERR_SHAPE;
     return CP_OK;
 }
 

@@ -7,7 +7,8 @@
 
 namespace cpattn {
 
-constexpr int kMaxSequences = 4096;  // sequences of one call
+constexpr int kMaxSequences = 4096;          // sequences of one call
+constexpr long long kMaxKeys = 0x7fffff00ll;  // slots of a cache, of a list or of a prefix: the end of the last tile fits 31 bits
 
 // The page lists of B sequences.  Every page number is checked where it is
 // read, so a wrong table never leads outside the cache.

@@ -58,6 +58,9 @@ struct PrefixArgs {
 
 __device__ __forceinline__ void report(int *status, cp_status code) { atomicExch(status, static_cast<int>(code)); }
 
+// The lists, tables and queries are read past L1 (__ldcg): a launch's blocks may
+// have started while the kernel that writes them was still running.
+
 // One problem's shape.
 struct Problem {
     int tok0, n;     // rows' tokens
@@ -85,8 +88,8 @@ template <int TM, int KT>
 __device__ __forceinline__ Problem sequence_problem(const PrefixArgs &a, const Line &line, int b) {
     Problem p;
     const bool listed = b < line.listed;
-    const int c0 = listed ? line.cu[b] : __ldg(a.cu + b), c1 = listed ? line.cu[b + 1] : __ldg(a.cu + b + 1);
-    long long len = listed ? line.len[b] : __ldg(a.kv_len + b);
+    const int c0 = listed ? line.cu[b] : __ldcg(a.cu + b), c1 = listed ? line.cu[b + 1] : __ldcg(a.cu + b + 1);
+    long long len = listed ? line.len[b] : __ldcg(a.kv_len + b);
     const long long most = static_cast<long long>(a.own.max_pages) << a.own.shift;
     p.tok0 = c0;
     p.n = c1 - c0;
@@ -131,21 +134,22 @@ __device__ __forceinline__ int prefix_workers(const PrefixArgs &a, long long pre
     return min(workers - 1, max(1, static_cast<int>(workers * (p / (p + o)) + 0.5f)));
 }
 
-// Fills `line`: the lists of up to `room` sequences (`lists`: 2 room + 1 values), sums over runs of sequences, and their scan.  `lead`
-// is true in the block that leaves the sequences' places for the join.
+// Fills `line`: the lists of up to `room` sequences (`lists`: 2 room + 1 values),
+// sums over runs of sequences, and their scan.  `lead` is true in the block that
+// leaves the sequences' places for the join.
 template <int TM, int KT>
 __device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, int *lists, int room, bool lead) {
     const int tid = threadIdx.x, run = (a.B + kRuns - 1) / kRuns, listed = a.with_own ? min(a.B, room) : 0;
     if (tid == 0) {
-        line.rows_end = __ldg(a.cu + a.B);
+        line.rows_end = __ldcg(a.cu + a.B);
         line.own = 0;
         line.listed = listed;
         line.cu = lists;
         line.len = lists + room + 1;
     }
     for (int b = listed ? tid : 1; b <= listed; b += blockDim.x) {
-        lists[b] = __ldg(a.cu + b);
-        if (b < listed) lists[room + 1 + b] = __ldg(a.kv_len + b);
+        lists[b] = __ldcg(a.cu + b);
+        if (b < listed) lists[room + 1 + b] = __ldcg(a.kv_len + b);
     }
     __syncthreads();
     const int b0 = min(tid * run, a.B), b1 = a.with_own ? min(b0 + run, a.B) : b0;
@@ -370,7 +374,7 @@ struct PageWindow {
     int n, n_pages, shift;  // entries, pages of the cache
     int base, cur, next;    // first entry of `cur`
     __device__ __forceinline__ int fetch(int first, int lane) const {
-        return first + lane < n ? __ldg(list + first + lane) : -1;
+        return first + lane < n ? __ldcg(list + first + lane) : -1;
     }
     __device__ __forceinline__ void begin(const PrefixArgs &a, const Piece &x, int first, int lane) {
         const PageTable &t = x.b < 0 ? a.pre : a.own;

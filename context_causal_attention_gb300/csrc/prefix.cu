@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                                                  (in ? row - tok * a.G : 0)) * D;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    qf[kk][h] = in ? __ldg(reinterpret_cast<const uint32_t *>(qp + kk * 16 + 2 * t4)) : 0u;
-                    qf[kk][2 + h] = in ? __ldg(reinterpret_cast<const uint32_t *>(qp + kk * 16 + 8 + 2 * t4)) : 0u;
+                    qf[kk][h] = in ? __ldcg(reinterpret_cast<const uint32_t *>(qp + kk * 16 + 2 * t4)) : 0u;
+                    qf[kk][2 + h] = in ? __ldcg(reinterpret_cast<const uint32_t *>(qp + kk * 16 + 8 + 2 * t4)) : 0u;
                 }
             }
             const int lim0 = x.row0 + g < x.rows ? row_limit(a, x, x.row0 + g) : 0;
@@ -684,7 +684,7 @@ cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cuda
 
 cp_status check_sizes(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int64_t Nkv, int64_t D,
                       int64_t page_size, int64_t max_pages) {
-    if (R < 1 || N < 1 || N > 65535 || max_new < 1 || max_new > R || P < 0 || P > INT32_MAX) return CP_ERR_SHAPE;
+    if (R < 1 || N < 1 || N > 65535 || max_new < 1 || max_new > R || P < 0 || P > kMaxKeys) return CP_ERR_SHAPE;
     const cp_status st = check_pages(1, page_size, B, max_pages, Nkv, D);
     if (st != CP_OK) return st;
     if (N % Nkv) return CP_ERR_DIVISIBILITY;

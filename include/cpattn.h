@@ -557,7 +557,7 @@ cp_status cp_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void
  * The prefix itself is appended as a sequence with its own table.
  * page_size in {16, 32, 64, 128, 256} and D in {64, 128} (else
  * CP_ERR_UNSUPPORTED); B <= 4096; n_pages * page_size and max_pages *
- * page_size < 2^31.  cu_new, kv_len and table are read on the device: a token
+ * page_size at most 2^31 - 256.  cu_new, kv_len and table are read on the device: a token
  * whose index or page number is out of range is skipped and the device status
  * word becomes CP_ERR_PAGE.
  */
@@ -597,7 +597,9 @@ cp_status cp_cache_append(const void *q, const void *k, const void *v, int64_t q
  * a result whatever they hold; a NaN or infinity in a V row that some row sees
  * may reach other rows of its sequence.
  * D in {64, 128}, page_size in {16, 32, 64, 128, 256}; N % Nkv == 0; scale
- * finite and > 0.  The lists are read on the device: a page number, length or
+ * finite and > 0; prefix_len at most 2^31 - 256.  Its launches overlap one another and the end of
+ * the kernel before them on the stream, never one that the caller puts behind.
+ * Make the first call of a process outside a stream capture.  The lists are read on the device: a page number, length or
  * count out of range sets the device status word to CP_ERR_PAGE, is never
  * followed, and leaves its rows' results unspecified.
  */

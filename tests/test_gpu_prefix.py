@@ -99,6 +99,8 @@ CASES = {
                       64, 2),
     "mixed_prompts_small_pages": ([1 + 29 * i % 90 for i in range(200)], [91 + 53 * i % 500 for i in range(200)], 0, 6,
                                   2, 64, 16, 0),
+    "most_sequences": ([1] * 4096, [1 + i % 40 for i in range(4096)], 30, 2, 1, 64, 16, 0),
+    "most_sequences_wide": ([i % 4 for i in range(4096)], [3 + i % 40 for i in range(4096)], 0, 8, 1, 64, 32, 0),
     "long": ([1, 2], [3000, 9000], 20000, 8, 2, 128, 64, 0),
 }
 

@@ -150,3 +150,57 @@ def test_binding_refusals(cplib):
         F.cp_rope_fwd(q, None, pos, rope, q_out=torch.zeros(5, 2, 64, dtype=torch.bfloat16))
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         F.cp_rope_fwd(q, None, pos, rope)  # not on a GPU
+
+
+def test_prefix_attention_refusals(cplib):
+    n = ctypes.c_size_t(0)
+
+    def size(R_=8, B=2, new=4, P=100, N=8, Nkv=2, D=64, page=16, most=4, out=ctypes.byref(n)):
+        return cplib.cp_prefix_attn_workspace_size(R_, B, new, P, N, Nkv, D, page, most, out)
+
+    assert size() == 0 and n.value > 0
+    need = n.value
+    assert size(P=0) == 0 and size(R_=1, new=1, B=1) == 0 and size(B=4096) == 0
+    assert size(out=None) == 1
+    for kw in (dict(R_=0), dict(B=0), dict(B=4097), dict(new=0), dict(new=9), dict(P=-1), dict(P=(1 << 31) - 255),
+               dict(N=0), dict(Nkv=0), dict(most=0), dict(most=1 << 27), dict(R_=1 << 28, N=64)):
+        assert size(**kw) == 2, kw
+    assert size(N=9) == 3
+    for kw in (dict(D=96), dict(D=256), dict(page=8), dict(page=24), dict(page=512)):
+        assert size(**kw) == 7, kw
+
+    def call(q=FAR[0], k=FAR[1], v=FAR[2], pages=10, page=16, pp=FAKE, P=100, table=FAKE, B=2, most=4, cu=FAKE, ln=FAKE,
+             new=4, R_=8, N=8, Nkv=2, D=64, scale=0.125, o=FAR[3], od=0, lse=FAKE, ws=FAR[4], nb=need):
+        return cplib.cp_prefix_attn_fwd(q, k, v, pages, page, pp, P, table, B, most, cu, ln, new, R_, N, Nkv, D, scale,
+                                        o, od, lse, ws, nb, None)
+
+    for kw in (dict(q=None), dict(k=None), dict(v=None), dict(pp=None), dict(table=None), dict(cu=None), dict(ln=None),
+               dict(o=None), dict(lse=None)):
+        assert call(**kw) == 1, kw
+    for kw in (dict(pages=0), dict(pages=1 << 27), dict(R_=0), dict(new=0), dict(new=9)):
+        assert call(**kw) == 2, kw
+    assert call(N=9) == 3 and call(od=2) == 4
+    for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf"))):
+        assert call(**kw) == 10, kw
+    for kw in (dict(q=FAR[0] + 8), dict(k=FAR[1] + 8), dict(o=FAR[3] + 8), dict(lse=FAKE + 2), dict(cu=FAKE + 1),
+               dict(pp=FAKE + 2), dict(ws=FAR[4] + 128)):
+        assert call(**kw) == 5, kw
+    assert call(ws=None) == 6 and call(nb=need - 1) == 6
+    assert call(D=96) == 7 and call(page=48) == 7
+
+
+def test_prefix_binding_refusals(cplib):
+    bf, i32 = torch.bfloat16, torch.int32
+    kc = torch.zeros(4, 16, 2, 64, dtype=bf)
+    q, pages, table = torch.zeros(3, 8, 64, dtype=bf), torch.zeros(2, dtype=i32), torch.zeros(1, 2, dtype=i32)
+    cu, ln = torch.tensor([0, 3], dtype=i32), torch.tensor([3], dtype=i32)
+    ok = dict(q=q, k_cache=kc, v_cache=kc.clone(), prefix_pages=pages, prefix_len=20, table=table, cu_new=cu, kv_len=ln,
+              max_new=3)
+    for kw in (dict(q=q.float()), dict(q=q[:, ::2]), dict(q=q[0]), dict(prefix_pages=pages[:1]),
+               dict(prefix_pages=pages.long()), dict(cu_new=cu[:1]), dict(o=torch.zeros(3, 8, 32, dtype=bf)),
+               dict(lse=torch.zeros(3, 8)), dict(v_cache=kc[:3])):
+        with pytest.raises(ValueError):
+            F.cp_prefix_attn_fwd(**dict(ok, **kw))
+    for kw in (dict(table=table.long()), dict(k_cache=kc.float(), v_cache=kc.float())):
+        with pytest.raises(TypeError):
+            F.cp_prefix_attn_fwd(**dict(ok, **kw))
