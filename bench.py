@@ -69,7 +69,7 @@ def attn_source_hash():
     """Hash of the attention kernel's code (comments and whitespace ignored), so
     a recorded traffic figure stays valid across comment edits only."""
     h = hashlib.sha256()
-    for f in ("attn.cu", "cp_ptx.cuh", "cp_sched.cuh"):
+    for f in ("attn.cu", "cp_ptx.cuh", "cp_sched.cuh", "cp_softmax.cuh"):
         with open(os.path.join(ROOT, "context_causal_attention_gb300", "csrc", f)) as fh:
             h.update(_code_only(fh.read()).encode())
     return h.hexdigest()[:16]
