@@ -21,16 +21,21 @@
 // no counter.  A second launch joins the pieces of every row in their order:
 // the result does not depend on timing.
 //
-// Inside a block of the 16-row kernel: two warps copy K and V into a ring of
-// 64-key stages (16-byte cp.async: pages are small), two groups of 4 warps take the
-// block's pieces in turn, so that one group's epilogue and next queries run
-// under the other's products and the ring never waits for them.  Each warp owns 16
+// Inside a block of the 16-row kernel: four warps copy K and V into a ring of
+// 64-key stages (16-byte cp.async, two warps for each of K and V), two groups of
+// 4 warps take the block's pieces in turn, so that one group's epilogue and next
+// queries run under the other's products and the ring never waits for them.  Each warp owns 16
 // of a stage's 64 keys: every byte of K and V passes from shared memory to
 // registers once.  Both products run on mma.sync m16n8k16: at 16 rows the tensor
 // work is a tenth of what the SM can do while it waits for memory.  Running
 // maximum and sum stay in fp32 registers; P is rounded to bf16 for the second
 // product (2^-9 of each weight at most, as in cp_attn_partial).  Keys past the
-// length are never copied (zeros in their place), whatever the page holds there.  Problems of more rows run in prefix_tc.cuh.
+// length are never copied (zeros in their place), whatever the page holds there.
+// Problems of more rows run in prefix_tc.cuh.
+//
+// What bounds it: few rows read each key and value once, so the bytes of the
+// pages.  64 single-token sequences of 4096 keys and 8 KV heads of 128 (1.07 GB)
+// take 185 us, 5.8 TB/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -51,9 +56,13 @@ namespace {
 __device__ int g_prefix_status = 0;
 
 // A problem whose rows for one KV head are more than this runs in tiles of 256
-// rows on the tensor memory, else in tiles of 16.
+// rows on the tensor memory, else in tiles of 16.  A second 16-row tile reads
+// every key again: 16 sequences of 4096 keys (8 KV heads of 128) take 72.8 us with
+// 16 rows each (75.9 on the wide tiles), 112.8 with 32 (wide: 76.9) and 185 with
+// 64 (81.0); a prefix of 32768 keys 50.3 us with 16 rows (52.4), 66.7 with 32
+// (56.4).  At D = 64 the same: prefix of 16 rows 31.9 (40.0), 32 rows of 4096 keys
+// 70.8 (50.3).
 constexpr int kTcRows = 16;
-
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -75,7 +84,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 constexpr int kGroups = 2;                    // consumer groups of 4 warps
-constexpr int kLoaders = 4;  // warps: K and V, the first and second half of a stage
+constexpr int kLoaders = 4;                   // warps: K and V, the first and second half of a stage
 constexpr int kMmaThreads = kLoaders * 32 + kGroups * 128;
 
 template <int D>
@@ -369,6 +378,9 @@ struct JoinArgs {
     float *lse;
 };
 
+// Heads of a token that one warp of join_token_kernel takes: 4, 8, 16 and 32
+// measured 1260, 1255, 1250 and 1264 us for 8 ragged prompts of up to 1024 tokens
+// (32 heads of 128) over a prefix of 16384 keys, the whole call.
 constexpr int kJoinHeads = 16;
 
 // Where the pieces of a row of head h lie: the slots first .. first + n - 1, row r of each.
@@ -579,7 +591,11 @@ __global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
 
 // ---------------------------------------------------------------- host side
 constexpr int kMaxBlocks = 320;          // of a launch (a slot more for each)
-constexpr long long kJoinRows = 16384;  // up to this many rows a warp joins one, beyond it a token's heads
+// Up to this many rows (tokens x heads) a warp joins one, beyond it kJoinHeads heads
+// of a token.  Few rows have many pieces: a call of 64 tokens of 32 heads takes
+// 103 us with a warp for a token's heads and 92 with one for a row.  Many rows have
+// few: the prompts above 1250 us by tokens and 1329 by rows.
+constexpr long long kJoinRows = 16384;
 
 // How a call is cut: which launches it makes and where they leave their pieces.
 struct Shape {
@@ -656,7 +672,10 @@ cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cuda
         if (!s.slots[k]) continue;
         a.with_prefix = a.P > 0 && s.tc_prefix == (k == 1);
         a.with_own = s.tc_own == (k == 1);
-        // measured cycles of a tile (256 rows or up to 128 rows of 128 keys; 16 rows of 64 keys)
+        // Measured cycles of a tile (256 rows or up to 128 rows of 128 keys; 16 rows of
+        // 64 keys); the blocks of the two launches share the SMs by their sum.  A
+        // prefix of 32768 keys and 64 sequences of up to 2048: 113.9 us at 2600 for a
+        // wide tile, 102.9 at 3100, 92 to 95 from 3600 to 5000, 104 at 5600.
         const bool both = s.slots[0] && s.slots[1];
         const bool half = static_cast<int64_t>(a.R) * a.G <= 128;
         a.cost_prefix = !both ? 0 : D == 128 ? (half ? 2300 : 4600) : (half ? 2300 : 3300);

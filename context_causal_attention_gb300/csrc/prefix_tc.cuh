@@ -41,7 +41,9 @@ namespace {
 
 constexpr int kTcThreads = 384;
 // Pages of this many tokens or more are copied by TMA, smaller ones by cp.async
-// (see copy_tile).
+// (see copy_tile).  64 rows over 32768 keys: pages of 64 take 58.5 us by TMA and
+// 60.5 by cp.async (D = 64: 44.1 and 46.2), pages of 16 62.6 and 60.5; prompts
+// over pages of 16 392 us and 384.
 constexpr int kTmaPage = 64;
 
 template <int D>

@@ -592,20 +592,19 @@ def cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, pos, rope, eps=1e-6, dq=No
 
 def _check_cache(k_cache, v_cache, table, cu_new, kv_len):
     """(n_pages, page_size, Nkv, D, B, max_pages) of a paged cache and its lists."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    shape, tab = k_cache.shape, table.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("the caches must be [n_pages, page_size, Nkv, D], both alike")
-    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
+    if k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16:
         raise TypeError("the caches must be bf16")
-    if table.dim() != 2 or kv_len.dim() != 1 or cu_new.dim() != 1 or kv_len.numel() != table.shape[0] or \
-            cu_new.numel() != table.shape[0] + 1:
+    if len(tab) != 2 or kv_len.shape != (tab[0],) or cu_new.shape != (tab[0] + 1,):
         raise ValueError("table [B, max_pages], cu_new [B + 1] and kv_len [B] must agree")
-    for t in (table, cu_new, kv_len):
-        if t.dtype != torch.int32:
-            raise TypeError("table, cu_new and kv_len must be int32")
-    for t in (k_cache, v_cache, table, cu_new, kv_len):
-        if not t.is_contiguous():
-            raise ValueError("tensor must be contiguous")
-    return tuple(k_cache.shape) + tuple(table.shape)
+    if not (table.dtype is cu_new.dtype is kv_len.dtype is torch.int32):
+        raise TypeError("table, cu_new and kv_len must be int32")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and table.is_contiguous() and
+            cu_new.is_contiguous() and kv_len.is_contiguous()):
+        raise ValueError("tensor must be contiguous")
+    return (*shape, *tab)
 
 
 def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=None, q_out=None, wq=None, wk=None,
@@ -615,15 +614,15 @@ def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=
     q_out bf16 [R,N,D].  kv_len counts each sequence's tokens after the call.
     Returns q_out (None without q)."""
     n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
-    if k.dim() != 3 or v.dim() != 3 or k.shape != v.shape or k.shape[1] != Nkv or k.shape[2] != D or \
-            v.dtype != k.dtype:
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or v.shape != shape or shape[1] != Nkv or shape[2] != D or v.dtype is not dtype:
         raise ValueError("k and v must be [R, Nkv, D] of the cache's heads, of one dtype")
     ks, vs = _head_rows(k)[0], _head_rows(v)[0]
-    R, qs, N = k.shape[0], 0, 0
+    R, qs, N = shape[0], 0, 0
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != R or q.shape[2] != D or q.dtype != k.dtype:
+        qs, lead, N, Dq = _head_rows(q)
+        if lead != shape[:1] or Dq != D or q.dtype is not dtype:
             raise ValueError("q must be [R, N, D] of k's tokens and dtype")
-        qs, N = _head_rows(q)[0], q.shape[1]
         if q_out is None:
             q_out = torch.empty((R, N, D), dtype=torch.bfloat16, device=q.device)
         elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous():
