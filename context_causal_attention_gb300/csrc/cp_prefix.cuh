@@ -126,12 +126,13 @@ __device__ __forceinline__ int place_of(int j, int tiles) {
 // The 256-row launch of the prefix is bound by its arithmetic and the 16-row
 // launch of the sequences by memory, so where a call makes both they share the
 // SMs: the first takes as many of the `workers` of a lane as its part of the
-// estimated cycles, the second the others.  Both find the same number from the lists.
+// estimated cycles, the second the others (a lane of one worker: both that one).
+// Both find the same number from the lists.
 __device__ __forceinline__ int prefix_workers(const PrefixArgs &a, long long prefix_tiles, long long own_tiles,
                                               int workers) {
     const float p = static_cast<float>(prefix_tiles) * a.cost_prefix, o = static_cast<float>(own_tiles) * a.cost_own;
     if (own_tiles == 0) return workers;
-    return min(workers - 1, max(1, static_cast<int>(workers * (p / (p + o)) + 0.5f)));
+    return max(1, min(workers - 1, static_cast<int>(workers * (p / (p + o)) + 0.5f)));
 }
 
 // Fills `line`: the lists of up to `room` sequences (`lists`: 2 room + 1 values),
@@ -239,6 +240,12 @@ __device__ __forceinline__ bool share_of(const PrefixArgs &a, const Line &line, 
     *t0 = share * blockIdx.y;
     *t1 = min(*t0 + share, total);
     return *t0 < *t1;
+}
+
+// A row's (exponent, sum) as a piece leaves it.  A row whose scores so far are all
+// NaN has no exponent, but must not pass for one that saw no key.
+__device__ __forceinline__ float2 left_ml(float m, float l) {
+    return make_float2(m == -INFINITY && l != l ? INFINITY : m, l);
 }
 
 // A stretch of one item that a block works on.

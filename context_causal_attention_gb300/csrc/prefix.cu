@@ -29,7 +29,7 @@
 // registers once.  Both products run on mma.sync m16n8k16: at 16 rows the tensor
 // work is a tenth of what the SM can do while it waits for memory.  Running
 // maximum and sum stay in fp32 registers; P is rounded to bf16 for the second
-// product (2^-9 of each weight at most, as in cp_attn_partial).  Keys past the
+// product (off by 2^-8 of each weight at most, as in cp_attn_partial).  Keys past the
 // length are never copied (zeros in their place), whatever the page holds there.
 // Problems of more rows run in prefix_tc.cuh.
 //
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     }
                     *reinterpret_cast<float4 *>(a.slot_o + at * D + c) = v;
                 }
-                if (c0 == 0) a.slot_ml[at] = make_float2(mx, ls);
+                if (c0 == 0) a.slot_ml[at] = left_ml(mx, ls);
             }
             if (x.slot < 0 && gtid == 0) report(a.status, CP_ERR_PAGE);
             if (group_any(group, !ok)) ok = false;
@@ -420,7 +420,8 @@ struct TokenPart {
         const int c0 = static_cast<int>(div_floor(first, share));
         const int c1 = static_cast<int>(div_floor(first + key_tiles - 1, share));
         const int slot = base_item + static_cast<int>(at) + c0;
-        return RowPieces{(kvh - pass * lanes) * slots + slot, min(c1 - c0 + 1, slots - slot), i % tm};
+        if (slot < 0) return RowPieces{0, 0, 0};  // lists that make no sense (reported)
+        return RowPieces{(kvh - pass * lanes) * slots + slot, max(0, min(c1 - c0 + 1, slots - slot)), i % tm};
     }
 };
 

@@ -445,9 +445,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     exp_pack128(sa, sb, sl2, m_run == -INFINITY ? 0.f : -m_run, pa, pb, &sum);
                     tmem_st64(tS + 64, pa, pb);
-                    // O is quiet: this tile's product waits for p_full below
+                    // O is quiet: this tile's product waits for p_full below.  Before a
+                    // piece's first product (NaN or infinite scores) it is still the last
+                    // piece's, which the first half may be joining.
 #pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 32) {
+                    for (int c0 = 0; c0 < D && n != begin; c0 += 32) {
                         uint32_t ov[32];
                         tmem_ld32(tO + c0, ov);
 #pragma unroll
@@ -539,7 +541,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                      __uint_as_float(ov[e + 6]), __uint_as_float(ov[e + 7]));
                 }
             }
-            if (write) a.slot_ml[at] = make_float2(m_run, l_run);
+            if (write) a.slot_ml[at] = left_ml(m_run, l_run);
             if (!paired || join) ++other;
         }
     }

@@ -592,7 +592,7 @@ cp_status cp_cache_append(const void *q, const void *k, const void *v, int64_t q
  *             aligned; overwritten (stream-ordered), not read back.  Calls that
  *             may overlap need one each.
  * Products are bf16 with fp32 accumulation; the softmax weights are rounded to
- * bf16 before the second product (off by 2^-9 of themselves at most, whatever
+ * bf16 before the second product (off by 2^-8 of themselves at most, whatever
  * o_dtype is), lse is not.  Keys that no row of the call sees are not read into
  * a result whatever they hold; a NaN or infinity in a V row that some row sees
  * may reach other rows of its sequence.

@@ -6,7 +6,7 @@ them is off by at most D u sum|q k| (u = 2^-24); with unit-normal values and sca
 1/sqrt(D) that is under 2^-14 in the score for D = 128, so every weight, and lse,
 is right to 2^-13 with the exponential's own 2^-22 and the sums' length / 2^24
 (lengths here stay under 2^10 tiles a thread).  Each weight is then rounded to
-bf16: at most 2^-8 / 2 (half a step) of itself, so o is off by at most (2^-8 + 2^-12)
+bf16: off by at most 2^-8 (half a step) of itself, so o is off by at most (2^-8 + 2^-12)
 sum p|v| / sum p, and by half a step of its own type."""
 import math
 
@@ -102,6 +102,10 @@ CASES = {
     "most_sequences": ([1] * 4096, [1 + i % 40 for i in range(4096)], 30, 2, 1, 64, 16, 0),
     "most_sequences_wide": ([i % 4 for i in range(4096)], [3 + i % 40 for i in range(4096)], 0, 8, 1, 64, 32, 0),
     "long": ([1, 2], [3000, 9000], 20000, 8, 2, 128, 64, 0),
+    # a KV head for nearly every SM: one or two blocks work on a head's line, of both launches
+    "heads_152": ([1] * 20, [1 + 9 * i for i in range(20)], 300, 152, 152, 64, 16, 0),
+    "heads_76": ([1, 2] * 6, [2 + 9 * i for i in range(12)], 200, 152, 76, 128, 32, 1),
+    "heads_157": ([1] * 18, [1 + 9 * i for i in range(18)], 130, 157, 157, 64, 64, 0),
 }
 
 
@@ -156,6 +160,39 @@ def test_rows_that_see_nothing(cuda_dev):
     c.kv_len[0] = 0
     o, lse = c.run(cuda_dev)
     assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["draft", "page_edges", "prompts", "half_tile_long", "short_prompts", "mixed_prompts",
+                                  "heads_152", "no_prefix"])
+def test_a_query_that_is_not_a_number_stays_alone(cuda_dev, name, value):
+    """Every score of a query row of NaN (or of infinities of both signs) is NaN: so are its o and
+    lse, and no other row's.  The rows that share its warp may take the sums l of their
+    weights in another order: two sums of positive values, each off by at most 34
+    additions of u = 2^-24 a tile, so l moves by 68 u < 2^-17 of itself.  o = sum_i f_i o_i / l over
+    the pieces: the quotient moves by as much, and each of the products and sums
+    rounds relative to its own size, which is at most sum p|v| / sum p, not |o| (pieces of
+    opposite sign cancel): a few u of that.  Together under 2^-17 + 2^-21 of sum p|v| / sum p."""
+    new, length, prefix, N, Nkv, D, page, pad = CASES[name]
+    c = Call(13, new, length, prefix, N, Nkv, D, page, pad)
+    n = c.rows
+    good = [t.clone() for t in c.run(cuda_dev, o_dtype=F.CP_F32)]
+    size = torch.from_numpy(c.want()[2]).to(cuda_dev)
+    at = [(r, (7 * r) % N) for r in range(0, n, 11)]
+    for r, h in at:
+        c.q[r, h] = value
+        c.q[r, h, ::2] *= -1
+    o, lse = c.run(cuda_dev, o_dtype=F.CP_F32)
+    sick = torch.zeros((n, N), dtype=torch.bool, device=cuda_dev)
+    for r, h in at:
+        sick[r, h] = True
+    sick &= ~torch.isneginf(good[1][:, :n].T)  # a row that sees no key has no score
+    assert sick.any()
+    o, lse, wo, wl = o[:n], lse[:, :n].T, good[0][:n], good[1][:, :n].T
+    assert torch.isnan(o[sick]).all() and torch.isnan(lse[sick]).all()
+    assert ((o[~sick] - wo[~sick]).abs() <= (2.0 ** -17 + 2.0 ** -21) * size[~sick]).all()
+    same = torch.isneginf(wl) & torch.isneginf(lse)
+    assert ((lse - wl).abs() <= 2.0 ** -17)[~sick & ~same].all()
 
 
 @pytest.mark.parametrize("gain", [30.0, 300.0])
