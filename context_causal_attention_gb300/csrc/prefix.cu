@@ -658,11 +658,12 @@ cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
     const int page = 1 << a.own.shift, box = page < kTcKT ? page : kTcKT;
     // at D = 64 a head's row is 128 bytes and its neighbour another head's
     const int l2 = D == 64 ? 128 : 256;
-    CUtensorMap mk, mv;
-    if (!make_map(&mk, a.k, D, a.Nkv, rows, 1, box, l2) || !make_map(&mv, a.v, D, a.Nkv, rows, 1, box, l2))
-        return CP_ERR_CUDA;
-    if (page >= kTmaPage)
+    CUtensorMap mk{}, mv{};  // read only with TMA
+    if (page >= kTmaPage) {
+        if (!make_map(&mk, a.k, D, a.Nkv, rows, 1, box, l2) || !make_map(&mv, a.v, D, a.Nkv, rows, 1, box, l2))
+            return CP_ERR_CUDA;
         return launch(prefix_tc_kernel<D, true>, grid, kTcThreads, TcCfg<D>::kSmem, true, stream, mk, mv, a);
+    }
     return launch(prefix_tc_kernel<D, false>, grid, kTcThreads, TcCfg<D>::kSmem, true, stream, mk, mv, a);
 }
 

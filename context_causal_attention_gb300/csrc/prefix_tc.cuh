@@ -177,8 +177,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(v_empty + s, 2);
         }
         fence_mbar_init();
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
+        if (tma) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
     }
     // its blocks may have started under the kernels that made its inputs
     wait_for_previous();
