@@ -6,7 +6,8 @@
 // a problem are its tokens times the G query heads of that KV head (row i =
 // token i / G, head i % G), cut into tiles of TM rows; an item is one row tile
 // of one KV head of one problem.  The items lie end to end on a line, each
-// ceil(keys / KT) long, and worker c of W works on [c share, (c + 1) share).
+// ceil(keys / KT) + E long (E: what beginning and ending it costs, in tiles), and
+// worker c of W works on [c share, (c + 1) share).
 //
 // The KV heads of a token lie side by side in memory, and their work is the
 // same, so blocks that run side by side take the same stretch of the line for
@@ -31,6 +32,15 @@ namespace cpattn {
 
 constexpr int kTM = 16, kKT = 64;       // rows and keys of a tile of the 16-row launch
 constexpr int kTcTM = 256, kTcKT = 128;  // of the 256-row launch
+// What an item costs beside its tiles (queries, first scores, its partial), in
+// tiles, for the shares of the line.  A 16-row item costs about 4600 cycles
+// against 1250 a tile, a 256-row one of few rows 8 us against 2.  Without (0 and
+// 0) a block that gets short sequences works on after the others are done: 32768
+// prefix keys and 64 sequences of 32 heads, one own key each, 169 us (71 with 3 and
+// 3); 16384 prefix keys and 64 prompts of 20 tokens 495 us (315), 32 of 64 tokens 632
+// (482), 8 of 512 tokens 1042 (879).  More than 3 for 256 rows gains nothing (64
+// prompts of 20 tokens 321 us with 4, 334 with 6).
+constexpr int kExtra = 3;
 
 struct PrefixArgs {
     const __nv_bfloat16 *q, *k, *v;
@@ -103,7 +113,7 @@ __device__ __forceinline__ Problem sequence_problem(const PrefixArgs &a, const L
     }
     p.keys = len;
     p.row_tiles = (p.n * a.G + TM - 1) / TM;
-    p.key_tiles = p.n ? (len + KT - 1) / KT : 0;
+    p.key_tiles = p.n && len ? (len + KT - 1) / KT + kExtra : 0;
     return p;
 }
 template <int TM, int KT>
@@ -113,7 +123,7 @@ __device__ __forceinline__ Problem prefix_problem(const PrefixArgs &a, const Lin
     p.n = min(max(line.rows_end, 0), a.R);
     p.keys = a.P;
     p.row_tiles = (p.n * a.G + TM - 1) / TM;
-    p.key_tiles = p.n ? (a.P + KT - 1) / KT : 0;
+    p.key_tiles = p.n && a.P ? (a.P + KT - 1) / KT + kExtra : 0;
     return p;
 }
 

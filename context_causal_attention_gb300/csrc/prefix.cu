@@ -404,7 +404,7 @@ struct TokenPart {
         slots = p.slots;
         lanes = p.lanes;
         tm = p.tm;
-        key_tiles = div_floor(keys + p.kt - 1, p.kt);
+        key_tiles = keys ? div_floor(keys + p.kt - 1, p.kt) + kExtra : 0;
         row_tiles = (n * a.G + tm - 1) / tm;
         row0 = (tok - (which ? begin : 0)) * a.G;
         base_tile = which ? p.base_tile[b] : 0;
