@@ -52,9 +52,7 @@ struct PrefixArgs {
     float scale_log2;
     int lanes, heads;           // Nkv = lanes x heads
     int with_prefix, with_own;  // the problems of this launch
-    // Cycles of a tile of the prefix in the 256-row launch and of the sequences in
-    // the 16-row launch where the call makes both (0 else): they run side by side.
-    int cost_prefix, cost_own;
+    float cost;                 // cycles of a tile, where both kinds of tiles share a launch
     int *status;
     unsigned long long timeout_ns;
     // what the launch leaves for the join
@@ -86,8 +84,8 @@ constexpr int kRuns = 128;
 struct Line {
     long long tile[kRuns + 1];
     int item[kRuns + 1];
-    unsigned long long own;  // tiles of the other launch's sequences
-    int rows_end;            // cu[B]
+    int worker, workers;  // this block's share, of how many
+    int rows_end;         // cu[B]
     int listed;
     int *cu, *len;  // [listed + 1], [listed]
 };
@@ -133,27 +131,15 @@ __device__ __forceinline__ int place_of(int j, int tiles) {
     return j < (tiles + 1) / 2 ? 2 * j : 2 * (tiles - 1 - j) + 1;
 }
 
-// The 256-row launch of the prefix is bound by its arithmetic and the 16-row
-// launch of the sequences by memory, so where a call makes both they share the
-// SMs: the first takes as many of the `workers` of a lane as its part of the
-// estimated cycles, the second the others (a lane of one worker: both that one).
-// Both find the same number from the lists.
-__device__ __forceinline__ int prefix_workers(const PrefixArgs &a, long long prefix_tiles, long long own_tiles,
-                                              int workers) {
-    const float p = static_cast<float>(prefix_tiles) * a.cost_prefix, o = static_cast<float>(own_tiles) * a.cost_own;
-    if (own_tiles == 0) return workers;
-    return max(1, min(workers - 1, static_cast<int>(workers * (p / (p + o)) + 0.5f)));
-}
-
 // Fills `line`: the lists of up to `room` sequences (`lists`: 2 room + 1 values),
-// sums over runs of sequences, and their scan.  `lead` is true in the block that
-// leaves the sequences' places for the join.
+// sums over runs of sequences, and their scan.
 template <int TM, int KT>
-__device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, int *lists, int room, bool lead) {
+__device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, int *lists, int room) {
     const int tid = threadIdx.x, run = (a.B + kRuns - 1) / kRuns, listed = a.with_own ? min(a.B, room) : 0;
     if (tid == 0) {
         line.rows_end = __ldcg(a.cu + a.B);
-        line.own = 0;
+        line.worker = blockIdx.y;
+        line.workers = gridDim.y;
         line.listed = listed;
         line.cu = lists;
         line.len = lists + room + 1;
@@ -179,14 +165,6 @@ __device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, int *
             line.tile[0] = a.with_prefix ? static_cast<long long>(a.heads) * p.row_tiles * p.key_tiles : 0;
             line.item[0] = a.with_prefix ? a.heads * p.row_tiles : 0;
         }
-    }
-    if (a.cost_own && !a.with_own) {
-        unsigned long long tiles = 0;
-        for (int b = tid; b < a.B; b += blockDim.x) {
-            const Problem p = sequence_problem<kTM, kKT>(a, line, b);
-            tiles += static_cast<unsigned long long>(a.heads) * p.row_tiles * p.key_tiles;
-        }
-        if (tiles) atomicAdd(&line.own, tiles);
     }
     __syncthreads();
     if (tid < 32) {
@@ -215,7 +193,14 @@ __device__ __forceinline__ void scan_line(const PrefixArgs &a, Line &line, int *
         }
     }
     __syncthreads();
-    if (lead && tid < kRuns) {
+}
+
+// Leaves the sequences' places for the join; by one block of the launch.
+template <int TM, int KT>
+__device__ __forceinline__ void leave_places(const PrefixArgs &a, const Line &line) {
+    const int tid = threadIdx.x, run = (a.B + kRuns - 1) / kRuns;
+    if (a.with_own && tid < kRuns) {
+        const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
         long long t = line.tile[tid];
         int n = line.item[tid];
         for (int b = b0; b < b1; ++b) {
@@ -237,17 +222,9 @@ __device__ __forceinline__ long long div_floor(long long a, long long b) {
 // A block's share of its lane's line; false if it has none.
 __device__ __forceinline__ bool share_of(const PrefixArgs &a, const Line &line, long long *t0, long long *t1) {
     const long long total = line.tile[kRuns];
-    int workers = gridDim.y;
-    if (a.cost_own && a.with_prefix)
-        workers = prefix_workers(a, total, static_cast<long long>(line.own), workers);
-    else if (a.cost_own) {
-        const Problem p = prefix_problem<kTcTM, kTcKT>(a, line);
-        workers -= prefix_workers(a, static_cast<long long>(a.heads) * p.row_tiles * p.key_tiles, total, workers);
-        workers = max(workers, 1);
-    }
-    const long long share = max(1ll, div_floor(total + workers - 1, workers));
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.head[0] = share;
-    *t0 = share * blockIdx.y;
+    const long long share = max(1ll, div_floor(total + line.workers - 1, line.workers));
+    if (blockIdx.x == 0 && line.worker == 0 && threadIdx.x == 0) a.head[0] = share;
+    *t0 = share * line.worker;
     *t1 = min(*t0 + share, total);
     return *t0 < *t1;
 }
@@ -347,7 +324,7 @@ struct Walk {
         return more;
     }
     __device__ __forceinline__ void step(const PrefixArgs &a, const Line &line) {
-        const int lane = blockIdx.x, slot = s.item + static_cast<int>(blockIdx.y);
+        const int lane = blockIdx.x, slot = s.item + line.worker;
         x.b = s.b;
         x.kvh = s.pass * a.lanes + lane;
         x.slot = slot < a.slots ? lane * a.slots + slot : -1;

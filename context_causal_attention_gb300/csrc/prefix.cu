@@ -83,6 +83,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+constexpr int kMaxBlocks = 320;               // of a launch (a slot more for each)
 constexpr int kGroups = 2;                    // consumer groups of 4 warps
 constexpr int kLoaders = 4;                   // warps: K and V, the first and second half of a stage
 constexpr int kMmaThreads = kLoaders * 32 + kGroups * 128;
@@ -127,38 +128,38 @@ __device__ __forceinline__ bool group_any(int group, bool v) {
     return r != 0;
 }
 
+// Barriers of a block's pipeline.  By one thread; a __syncthreads follows in mma_work.
 template <int D>
-__global__ void __launch_bounds__(kMmaThreads, 1)
-    prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
+__device__ __forceinline__ void mma_init(uint8_t *smem) {
     using C = MmaCfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *empty = full + C::kStages, *go = empty + C::kStages;
+    *reinterpret_cast<volatile int *>(smem + C::kOffMisc) = 0;  // abort flag
+    for (int s = 0; s < C::kStages; ++s) {
+        mbar_init(full + s, 32 * kLoaders);
+        mbar_init(empty + s, 4);
+    }
+    for (int i = 0; i < kGroups; ++i) mbar_init(go + i, 4);
+    fence_mbar_init();
+}
+template <int D>
+__device__ __forceinline__ void mma_scan(const PrefixArgs &a, uint8_t *smem) {
+    using C = MmaCfg<D>;
+    scan_line<kTM, kKT>(a, *reinterpret_cast<Line *>(smem + C::kOffLine), reinterpret_cast<int *>(smem + C::kOffLists),
+                        C::kListed);
+}
+
+// A block's share, behind mma_scan.
+template <int D>
+__device__ __forceinline__ void mma_work(const PrefixArgs &a, uint8_t *smem) {
+    using C = MmaCfg<D>;
     Line &line = *reinterpret_cast<Line *>(smem + C::kOffLine);
     Start &start = *reinterpret_cast<Start *>(smem + C::kOffStart);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *empty = full + C::kStages, *go = empty + C::kStages;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    if (tid == 0) {
-        *abort_flag = 0;
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(full + s, 32 * kLoaders);
-            mbar_init(empty + s, 4);
-        }
-        for (int i = 0; i < kGroups; ++i) mbar_init(go + i, 4);
-        fence_mbar_init();
-    }
-    // As the call's only main launch it follows the kernels that made its inputs;
-    // behind the 256-row launch it starts when that one has seen them complete.
-    if (!a.cost_own) wait_for_previous();
-    launch_dependents();
-    scan_line<kTM, kKT>(a, line, reinterpret_cast<int *>(smem + C::kOffLists), C::kListed,
-                        blockIdx.x == 0 && blockIdx.y == 0);
     long long t0, t1;
-    if (!share_of(a, line, &t0, &t1)) {
-        if (tid == 0) wait_for_previous();
-        return;
-    }
+    if (!share_of(a, line, &t0, &t1)) return;
     if (warp == 0) find_start<kTM, kKT>(a, line, t0, &start);
     __syncthreads();
 
@@ -355,9 +356,96 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     __syncthreads();
     if (tid == 0 && *abort_flag) report(a.status, CP_ERR_DEVICE_TIMEOUT);
-    // It reads nothing of the 256-row launch before it, but is not complete before
-    // that one is: the join waits for this launch alone.
-    if (tid == 0) wait_for_previous();
+}
+
+__device__ __forceinline__ uint8_t *aligned_shared() {
+    extern __shared__ uint8_t smem_raw[];
+    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
+    uint8_t *smem = aligned_shared();
+    if (threadIdx.x == 0) mma_init<D>(smem);
+    // its blocks may have started under the kernels that made its inputs
+    wait_for_previous();
+    launch_dependents();
+    mma_scan<D>(a, smem);
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        leave_places<kTM, kKT>(a, *reinterpret_cast<Line *>(smem + MmaCfg<D>::kOffLine));
+    mma_work<D>(a, smem);
+}
+
+// A block's beginning and end in cycles (lists, pages, queries, first tiles; the last
+// rows' partials): a wide block had its first scores after 13 us and its last 6 us
+// before its end, a narrow one its first tile after 6.6.
+constexpr float kAroundWide = 36000.f, kAroundNarrow = 15000.f;
+
+// Workers of a lane for the prefix, so that the slower of the two kinds is done
+// soonest.  With the wide tile's cost (D = 128, small pages: 4250 cycles) a prefix of
+// 32768 keys and 64 sequences of up to 2048, 32 / 8 heads, take 87 us; at 2600 114, at
+// 3100 103, at 5600 104 (of the two-launch form, 93 at its best).  In proportion
+// to the costs alone (without what lies around the tiles, rounded) five tokens each
+// of 7 sequences behind 100003 keys, 16 heads of 64, got one worker where they need
+// two: 101 us, 95 so.  Warp-wide; at least two workers.
+__device__ __forceinline__ int prefix_workers(float prefix, float own, int workers) {
+    if (own == 0.f) return workers;
+    uint32_t best = 0xffffffffu;
+    for (int w = 1 + (threadIdx.x & 31); w < workers; w += 32) {
+        const float t = fmaxf(kAroundWide + prefix / w, kAroundNarrow + own / (workers - w));
+        best = min(best, (__float_as_uint(t) & ~511u) | w);  // t > 0: its bits are in its order
+    }
+    return static_cast<int>(__reduce_min_sync(0xffffffffu, best) & 511u);
+}
+
+// The prefix in tiles of 256 rows and the sequences in tiles of 16, side by side:
+// the first are bound by their arithmetic and the second by memory, so a block does
+// one kind (prefix_workers).  As two launches, each leaving the other's blocks idle, the
+// idle blocks of the second waited for the first and the join for them: 93 us
+// where this takes 87.  a: the prefix; b: the sequences.
+template <int D, bool tma>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    prefix_both_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ PrefixArgs a, const __grid_constant__ PrefixArgs b) {
+    static_assert(kMmaThreads == kTcThreads && kMaxBlocks < 512, "one launch");
+    uint8_t *smem = aligned_shared();
+    wait_for_previous();
+    launch_dependents();
+    mma_scan<D>(b, smem);
+    Line &line = *reinterpret_cast<Line *>(smem + MmaCfg<D>::kOffLine);
+    const Problem p = prefix_problem<kTcTM, kTcKT>(a, line);
+    const int items = a.heads * p.row_tiles;
+    const long long tiles = items * p.key_tiles;
+    const int w = prefix_workers(static_cast<float>(tiles) * a.cost, static_cast<float>(line.tile[kRuns]) * b.cost, gridDim.y);
+    const int y = blockIdx.y, rows_end = line.rows_end;
+    __syncthreads();
+    if (y >= w) {
+        if (threadIdx.x == 0) {
+            mma_init<D>(smem);
+            line.worker = y - w;
+            line.workers = gridDim.y - w;
+        }
+        __syncthreads();
+        if (blockIdx.x == 0 && y == w) leave_places<kTM, kKT>(b, line);
+        mma_work<D>(b, smem);
+        return;
+    }
+    // the prefix alone makes a line of one problem
+    Line &own = *reinterpret_cast<Line *>(smem + TcCfg<D>::kOffLine);
+    if (threadIdx.x <= kRuns) {
+        own.tile[threadIdx.x] = tiles;
+        own.item[threadIdx.x] = items;
+    }
+    if (threadIdx.x == 0) {
+        own.worker = y;
+        own.workers = w;
+        own.rows_end = rows_end;
+        own.listed = 0;
+        tc_init<D, tma>(smem, tmK, tmV);
+    }
+    __syncthreads();
+    tc_work<D, tma>(tmK, tmV, a, smem);
 }
 
 // What a launch left, as the join reads it.
@@ -591,12 +679,14 @@ __global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kMaxBlocks = 320;          // of a launch (a slot more for each)
 // Up to this many rows (tokens x heads) a warp joins one, beyond it kJoinHeads heads
 // of a token.  Few rows have many pieces: a call of 64 tokens of 32 heads takes
 // 103 us with a warp for a token's heads and 92 with one for a row.  Many rows have
 // few: the prompts above 1250 us by tokens and 1329 by rows.
 constexpr long long kJoinRows = 16384;
+
+// Blocks of a launch for each lane.
+int workers_of(int lanes) { return (sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks) / lanes; }
 
 // How a call is cut: which launches it makes and where they leave their pieces.
 struct Shape {
@@ -637,8 +727,12 @@ Shape shape_of(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int6
     return s;
 }
 
+// One launch: `wide` in tiles of 256 rows, `narrow` in tiles of 16, or both (either
+// may be null).
 template <int D>
-cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
+cp_status launch_main(const PrefixArgs *wide, const PrefixArgs *narrow, cudaStream_t stream) {
+    constexpr int both_smem = TcCfg<D>::kSmem > MmaCfg<D>::kSmem ? TcCfg<D>::kSmem : MmaCfg<D>::kSmem;
+    const PrefixArgs &a = wide ? *wide : *narrow;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [] {
@@ -649,11 +743,14 @@ cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
         if (err == cudaSuccess)
             err = cudaFuncSetAttribute(prefix_tc_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        TcCfg<D>::kSmem);
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(prefix_both_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, both_smem);
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(prefix_both_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, both_smem);
     });
     if (err != cudaSuccess) return cuda_status(err);
-    const int sms = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
-    const dim3 grid(a.lanes, sms / a.lanes);
-    if (!tc) return launch(prefix_mma_kernel<D>, grid, kMmaThreads, MmaCfg<D>::kSmem, true, stream, a);
+    const dim3 grid(a.lanes, workers_of(a.lanes));
+    if (!wide) return launch(prefix_mma_kernel<D>, grid, kMmaThreads, MmaCfg<D>::kSmem, true, stream, a);
     const int64_t rows = static_cast<int64_t>(a.own.n_pages) << a.own.shift;
     const int page = 1 << a.own.shift, box = page < kTcKT ? page : kTcKT;
     // at D = 64 a head's row is 128 bytes and its neighbour another head's
@@ -662,43 +759,52 @@ cp_status launch_main(const PrefixArgs &a, bool tc, cudaStream_t stream) {
     if (page >= kTmaPage) {
         if (!make_map(&mk, a.k, D, a.Nkv, rows, 1, box, l2) || !make_map(&mv, a.v, D, a.Nkv, rows, 1, box, l2))
             return CP_ERR_CUDA;
+        if (narrow) return launch(prefix_both_kernel<D, true>, grid, kTcThreads, both_smem, true, stream, mk, mv, a, *narrow);
         return launch(prefix_tc_kernel<D, true>, grid, kTcThreads, TcCfg<D>::kSmem, true, stream, mk, mv, a);
     }
+    if (narrow) return launch(prefix_both_kernel<D, false>, grid, kTcThreads, both_smem, true, stream, mk, mv, a, *narrow);
     return launch(prefix_tc_kernel<D, false>, grid, kTcThreads, TcCfg<D>::kSmem, true, stream, mk, mv, a);
 }
 
 template <int D>
-cp_status launch_call(PrefixArgs a, const Shape &s, uint8_t *w, JoinArgs j, cudaStream_t stream) {
-    // the wide launch first: it has the prefix, the longer work
-    for (int k = 1; k >= 0; --k) {
+cp_status launch_call(const PrefixArgs &call, const Shape &s, uint8_t *w, JoinArgs j, cudaStream_t stream) {
+    PrefixArgs args[2];  // tiles of 16 rows, of 256
+    for (int k = 0; k < 2; ++k) {
         if (!s.slots[k]) continue;
+        PrefixArgs &a = args[k];
+        a = call;
         a.with_prefix = a.P > 0 && s.tc_prefix == (k == 1);
         a.with_own = s.tc_own == (k == 1);
-        // Measured cycles of a tile (256 rows or up to 128 rows of 128 keys; 16 rows of
-        // 64 keys); the blocks of the two launches share the SMs by their sum.  A
-        // prefix of 32768 keys and 64 sequences of up to 2048: 113.9 us at 2600 for a
-        // wide tile, 102.9 at 3100, 92 to 95 from 3600 to 5000, 104 at 5600.
-        const bool both = s.slots[0] && s.slots[1];
-        const bool half = static_cast<int64_t>(a.R) * a.G <= 128;
-        a.cost_prefix = !both ? 0 : D == 128 ? (half ? 2300 : 4600) : (half ? 2300 : 3300);
-        a.cost_own = !both ? 0 : D == 128 ? 1250 : 800;
+        // Measured cycles of a tile, for the blocks' shares where both kinds run (a tile
+        // of up to 128 rows by both halves in turn; small pages by cp.async).
+        const bool half = static_cast<int64_t>(a.R) * a.G <= 128, small = (1 << a.own.shift) < kTmaPage;
+        a.cost = !k ? (D == 128 ? 1200.f : 780.f)
+                    : D == 128 ? (half ? (small ? 3400.f : 2900.f) : (small ? 4250.f : 4000.f))
+                               : (half ? (small ? 2050.f : 1450.f) : 2700.f);
         a.head = reinterpret_cast<long long *>(w + s.head[k]);
         a.base_tile = reinterpret_cast<long long *>(w + s.base_tile[k]);
         a.base_item = reinterpret_cast<int *>(w + s.base_item[k]);
         a.slot_ml = reinterpret_cast<float2 *>(w + s.slot_ml[k]);
         a.slot_o = reinterpret_cast<float *>(w + s.slot_o[k]);
         a.slots = static_cast<int>(s.slots[k]);
-        const cp_status st = launch_main<D>(a, k == 1, stream);
-        if (st != CP_OK) return st;
         for (int which = 0; which < 2; ++which)
             if (which ? a.with_own : a.with_prefix)
                 j.part[which] = JoinPart{a.head, a.base_tile, a.base_item, a.slot_ml, a.slot_o, a.slots,
                                          k ? kTcTM : kTM, k ? kTcKT : kKT, a.lanes};
     }
-    if (a.P == 0) j.part[0] = j.part[1];  // not read into a result: no keys
-    const long long rows = static_cast<long long>(a.R) * a.N;
+    if (call.P == 0) j.part[0] = j.part[1];  // not read into a result: no keys
+    const PrefixArgs *narrow = s.slots[0] ? &args[0] : nullptr, *wide = s.slots[1] ? &args[1] : nullptr;
+    cp_status st = CP_OK;
+    if (narrow && wide && workers_of(s.lanes) < 2) {
+        // a lane of one worker has none to share
+        st = launch_main<D>(wide, nullptr, stream);
+        wide = nullptr;
+    }
+    if (st == CP_OK) st = launch_main<D>(wide, narrow, stream);
+    if (st != CP_OK) return st;
+    const long long rows = static_cast<long long>(call.R) * call.N;
     const bool few = rows <= kJoinRows;
-    const long long units = few ? rows : static_cast<long long>(a.R) * ((a.N + kJoinHeads - 1) / kJoinHeads);
+    const long long units = few ? rows : static_cast<long long>(call.R) * ((call.N + kJoinHeads - 1) / kJoinHeads);
     return launch(few ? join_row_kernel<D> : join_token_kernel<D>, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0,
                   true, stream, j);
 }

@@ -137,14 +137,47 @@ __device__ __forceinline__ void copy_queries(const PrefixArgs &a, const Piece &x
     }
 }
 
-// tma: the pages are copied by TMA, else by cp.async.
+// Barriers of a block's pipeline.  By one thread; a __syncthreads follows in tc_work.
 template <int D, bool tma>
-__global__ void __launch_bounds__(kTcThreads, 1)
-    prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ PrefixArgs a) {
+__device__ __forceinline__ void tc_init(uint8_t *smem, const CUtensorMap &tmK, const CUtensorMap &tmV) {
     using C = TcCfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint64_t *q_full = bar, *s_full = bar + 2, *p_full = bar + 4, *o_full = bar + 6, *o_empty = bar + 8;
+    uint64_t *drain = bar + 10, *ml_full = bar + 12, *q_empty = bar + 13, *turn = bar + 14, *k_full = bar + 16,
+             *v_full = k_full + C::kStagesK, *k_empty = v_full + C::kStagesV, *v_empty = k_empty + C::kStagesK;
+    *reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4) = 0;  // abort flag
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(q_full + i, 32);
+        mbar_init(s_full + i, 1);
+        mbar_init(p_full + i, 4);
+        mbar_init(o_full + i, 1);
+        mbar_init(o_empty + i, 4);
+        mbar_init(drain + i, 1);
+        mbar_init(turn + i, 4);
+    }
+    mbar_init(ml_full, 4);
+    mbar_init(q_empty, 2);
+    for (int s = 0; s < C::kStagesK; ++s) {
+        mbar_init(k_full + s, tma ? 1 : 32);
+        mbar_init(k_empty + s, 2);
+    }
+    for (int s = 0; s < C::kStagesV; ++s) {
+        mbar_init(v_full + s, tma ? 1 : 32);
+        mbar_init(v_empty + s, 2);
+    }
+    fence_mbar_init();
+    if (tma) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+}
+
+// A block's share, behind the scan of its line.  tma: the pages are copied by TMA,
+// else by cp.async.
+template <int D, bool tma>
+__device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMap &tmV, const PrefixArgs &a,
+                                        uint8_t *smem) {
+    using C = TcCfg<D>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Line &line = *reinterpret_cast<Line *>(smem + C::kOffLine);
     Start &start = *reinterpret_cast<Start *>(smem + C::kOffStart);
@@ -155,37 +188,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
 
-    if (tid == 0) {
-        *abort_flag = 0;
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + i, 32);
-            mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 4);
-            mbar_init(o_full + i, 1);
-            mbar_init(o_empty + i, 4);
-            mbar_init(drain + i, 1);
-            mbar_init(turn + i, 4);
-        }
-        mbar_init(ml_full, 4);
-        mbar_init(q_empty, 2);
-        for (int s = 0; s < C::kStagesK; ++s) {
-            mbar_init(k_full + s, tma ? 1 : 32);
-            mbar_init(k_empty + s, 2);
-        }
-        for (int s = 0; s < C::kStagesV; ++s) {
-            mbar_init(v_full + s, tma ? 1 : 32);
-            mbar_init(v_empty + s, 2);
-        }
-        fence_mbar_init();
-        if (tma) {
-            tma_prefetch_desc(&tmK);
-            tma_prefetch_desc(&tmV);
-        }
-    }
-    // its blocks may have started under the kernels that made its inputs
-    wait_for_previous();
-    launch_dependents();
-    scan_line<kTcTM, kTcKT>(a, line, nullptr, 0, blockIdx.x == 0 && blockIdx.y == 0);
     long long t0, t1;
     if (!share_of(a, line, &t0, &t1)) return;
     if (warp == 1) {
@@ -555,6 +557,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_dealloc(tmem, 512);
     }
     if (tid == 0 && *abort_flag) report(a.status, CP_ERR_DEVICE_TIMEOUT);
+}
+
+template <int D, bool tma>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ PrefixArgs a) {
+    using C = TcCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Line &line = *reinterpret_cast<Line *>(smem + C::kOffLine);
+    if (threadIdx.x == 0) tc_init<D, tma>(smem, tmK, tmV);
+    // its blocks may have started under the kernels that made its inputs
+    wait_for_previous();
+    launch_dependents();
+    scan_line<kTcTM, kTcKT>(a, line, nullptr, 0);
+    if (blockIdx.x == 0 && blockIdx.y == 0) leave_places<kTcTM, kTcKT>(a, line);
+    tc_work<D, tma>(tmK, tmV, a, smem);
 }
 
 }  // namespace
