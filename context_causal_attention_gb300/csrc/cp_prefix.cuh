@@ -30,8 +30,8 @@
 
 namespace cpattn {
 
-constexpr int kTM = 16, kKT = 64;       // rows and keys of a tile of the 16-row launch
-constexpr int kTcTM = 256, kTcKT = 128;  // of the 256-row launch
+constexpr int kTM = 16, kKT = 64;        // rows and keys of a narrow tile (mma.sync)
+constexpr int kTcTM = 256, kTcKT = 128;  // of a wide one (tcgen05)
 // What an item costs beside its tiles (queries, first scores, its partial), in
 // tiles, for the shares of the line.  A 16-row item costs about 4600 cycles
 // against 1250 a tile, a 256-row one of few rows 8 us against 2.  Without (0 and
