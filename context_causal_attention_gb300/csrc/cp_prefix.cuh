@@ -34,12 +34,11 @@ constexpr int kTM = 16, kKT = 64;        // rows and keys of a narrow tile (mma.
 constexpr int kTcTM = 256, kTcKT = 128;  // of a wide one (tcgen05)
 // What an item costs beside its tiles (queries, first scores, its partial), in
 // tiles, for the shares of the line.  A 16-row item costs about 4600 cycles
-// against 1250 a tile, a 256-row one of few rows 8 us against 2.  Without (0 and
-// 0) a block that gets short sequences works on after the others are done: 32768
-// prefix keys and 64 sequences of 32 heads, one own key each, 169 us (71 with 3 and
-// 3); 16384 prefix keys and 64 prompts of 20 tokens 495 us (315), 32 of 64 tokens 632
-// (482), 8 of 512 tokens 1042 (879).  More than 3 for 256 rows gains nothing (64
-// prompts of 20 tokens 321 us with 4, 334 with 6).
+// against 1200 a tile, a 256-row one of few rows 8 us against 2.  Without (0) a
+// block that gets short sequences works on after the others are done: 32768 prefix
+// keys and 64 sequences of 32 heads, one own key each, 167 us (71 with 3, 75 with 6);
+// 16384 prefix keys and 64 prompts of 20 tokens 495 us (316, 331), 32 of 64 tokens
+// 632 (488, 454), 8 of 512 tokens 1046 (886, 898).
 constexpr int kExtra = 3;
 
 struct PrefixArgs {

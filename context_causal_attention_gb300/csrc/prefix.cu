@@ -35,7 +35,9 @@
 //
 // What bounds it: few rows read each key and value once, so the bytes of the
 // pages.  64 single-token sequences of 4096 keys and 8 KV heads of 128 (1.07 GB)
-// take 185 us, 5.8 TB/s.
+// take 190 us from a cold L2, 5.6 TB/s.  A call of one token over 4400 keys is latency:
+// 15 us, of them 3.7 until the place on the line is found, 3 for the first tile,
+// 6 for the join.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -58,10 +60,12 @@ __device__ int g_prefix_status = 0;
 // A problem whose rows for one KV head are more than this runs in tiles of 256
 // rows on the tensor memory, else in tiles of 16.  A second 16-row tile reads
 // every key again: 16 sequences of 4096 keys (8 KV heads of 128) take 72.8 us with
-// 16 rows each (75.9 on the wide tiles), 112.8 with 32 (wide: 76.9) and 185 with
-// 64 (81.0); a prefix of 32768 keys 50.3 us with 16 rows (52.4), 66.7 with 32
-// (56.4).  At D = 64 the same: prefix of 16 rows 31.9 (40.0), 32 rows of 4096 keys
-// 70.8 (50.3).
+// 16 rows each (74.9 on the wide tiles), 115.8 with 32 (wide: 78.9) and 187.5 with
+// 64 (83.1); 64 single tokens 191.6 (199.8), 16 rows over a prefix of 32768 keys
+// 48.3 (50.3).  At D = 64 the same: that prefix 33.9 (38.0), 32 rows of 4096 keys
+// 70.8 (50.3).  Where the prefix is wide and the sequences are narrow but next to
+// nothing (four of 64 keys), wide tiles for both would win: 52.4 against 60.5; the
+// lengths are not known here.
 constexpr int kTcRows = 16;
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -384,8 +388,8 @@ constexpr float kAroundWide = 36000.f, kAroundNarrow = 15000.f;
 
 // Workers of a lane for the prefix, so that the slower of the two kinds is done
 // soonest.  With the wide tile's cost (D = 128, small pages: 4250 cycles) a prefix of
-// 32768 keys and 64 sequences of up to 2048, 32 / 8 heads, take 87 us; at 2600 114, at
-// 3100 103, at 5600 104 (of the two-launch form, 93 at its best).  In proportion
+// 32768 keys and 64 sequences of up to 2048, 32 / 8 heads, take 86 us; at 3000 98.6, at
+// 3600 92.4, at 5000 86, at 5600 92.5.  In proportion
 // to the costs alone (without what lies around the tiles, rounded) five tokens each
 // of 7 sequences behind 100003 keys, 16 heads of 64, got one worker where they need
 // two: 101 us, 95 so.  Warp-wide; at least two workers.
@@ -403,7 +407,7 @@ __device__ __forceinline__ int prefix_workers(float prefix, float own, int worke
 // the first are bound by their arithmetic and the second by memory, so a block does
 // one kind (prefix_workers).  As two launches, each leaving the other's blocks idle, the
 // idle blocks of the second waited for the first and the join for them: 93 us
-// where this takes 87.  a: the prefix; b: the sequences.
+// where this took 87.  a: the prefix; b: the sequences.
 template <int D, bool tma>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_both_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -467,7 +471,7 @@ struct JoinArgs {
 };
 
 // Heads of a token that one warp of join_token_kernel takes: 4, 8, 16 and 32
-// measured 1260, 1255, 1250 and 1264 us for 8 ragged prompts of up to 1024 tokens
+// measured 1220, 1206, 1208 and 1223 us for 8 ragged prompts of up to 1024 tokens
 // (32 heads of 128) over a prefix of 16384 keys, the whole call.
 constexpr int kJoinHeads = 16;
 
@@ -689,8 +693,8 @@ __global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
 // ---------------------------------------------------------------- host side
 // Up to this many rows (tokens x heads) a warp joins one, beyond it kJoinHeads heads
 // of a token.  Few rows have many pieces: a call of 64 tokens of 32 heads takes
-// 103 us with a warp for a token's heads and 92 with one for a row.  Many rows have
-// few: the prompts above 1250 us by tokens and 1329 by rows.
+// 145 us with a warp for a token's heads and 86 with one for a row.  Many rows have
+// few: the prompts above 1208 us by tokens and 1335 by rows.
 constexpr long long kJoinRows = 16384;
 
 // Blocks of a launch for each lane.
