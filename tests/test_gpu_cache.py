@@ -120,7 +120,6 @@ def test_slots_past_32_bits_of_offset(cuda_dev):
     neighbours and the places an overflow would reach are not."""
     pages, page, Nkv, D = 20500, 256, 8, 128  # 5.4e9 elements
     kc = torch.zeros(pages, page, Nkv, D, dtype=torch.bfloat16, device=cuda_dev)
-    vc = torch.zeros(1, device=cuda_dev).to(torch.bfloat16).expand(1)
     vc = torch.zeros_like(kc)
     k, v = (torch.ones(2, Nkv, D, dtype=torch.bfloat16, device=cuda_dev) * x for x in (3, 5))
     i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda_dev)  # noqa: E731

@@ -154,7 +154,6 @@ def test_rows_that_see_nothing(cuda_dev):
         assert none.sum() == (16 if prefix == 0 else 0)
         assert np.array_equal(np.isneginf(f64(lse)[:, :6]), none)
         assert np.abs(f64(lse)[:, :6][~none] - wl[~none]).max() <= 2.0 ** -12
-        c = None
     # no key at all anywhere
     c = Call(5, [1], [1], 0, 2, 1, 128, 16)
     c.kv_len[0] = 0
@@ -257,6 +256,72 @@ def test_repeated_calls_agree(cuda_dev, new, N, Nkv, D, page):
             junk.fill_(i)
         o2, lse2 = F.cp_prefix_attn_fwd(q, k, v, pages, 777, table, cu, kv_len, new)
         assert torch.equal(o, o2) and torch.equal(lse, lse2), i
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("new", [1, 40])
+def test_pages_past_32_bits_of_offset(cuda_dev, page, new):
+    """Caches of 2.7e9 elements each (byte offsets past 2^32), the pages in use at their
+    end: the bits of the same call over small caches."""
+    c = Call(14, [new, 1, new], [300 + new, 90, new], 700, 16, 4, 128, page)
+    want = c.run(cuda_dev)
+    q, k, v, pages, table, cu, kv_len = c.dev
+    extra = int(2.7e9) // (page * 4 * 128)
+    big = []
+    for small in (k, v):
+        t = torch.empty(extra + c.b.total, page, 4, 128, dtype=torch.bfloat16, device=cuda_dev)
+        t[:2 * c.b.total] = float("nan")  # where a wrapped offset would lead
+        t[extra:] = small
+        big.append(t)
+    ws = torch.empty(F.cp_prefix_attn_workspace_size(c.R, 3, new, 700, 16, 4, 128, page, table.shape[1]),
+                     dtype=torch.uint8, device=cuda_dev)
+    got = F.cp_prefix_attn_fwd(q, *big, pages + extra, 700, torch.where(table < 0, table, table + extra), cu, kv_len, new,
+                               workspace=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("name", ["draft", "prompts", "page_edges"])
+def test_two_calls_at_once(cuda_dev, name):
+    """Two streams, a workspace each, the same caches: both get their own calls' bits.  Then
+    two graphs that share a workspace, replayed one after the other."""
+    new, length, prefix, N, Nkv, D, page, pad = CASES[name]
+    c = Call(15, new, length, prefix, N, Nkv, D, page, pad)
+    c.run(cuda_dev)
+    q, k, v, pages, table, cu, kv_len = c.dev
+    qs = [q, q.flip(1).contiguous()]
+    need = F.cp_prefix_attn_workspace_size(c.R, len(new), max(new), prefix, N, Nkv, D, page, table.shape[1])
+    ws = [torch.empty(need, dtype=torch.uint8, device=cuda_dev) for _ in range(2)]
+    outs = [(torch.zeros_like(q), torch.zeros(N, c.R, device=cuda_dev)) for _ in range(2)]
+
+    def call(i, w):
+        F.cp_prefix_attn_fwd(qs[i], k, v, pages, prefix, table, cu, kv_len, max(new), o=outs[i][0], lse=outs[i][1],
+                             workspace=ws[w])
+
+    want = []
+    for i in range(2):
+        call(i, 0)
+        want.append([t.clone() for t in outs[i]])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                for t in outs[i]:
+                    t.zero_()
+                call(i, i)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i]))
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            call(i, 0)
+    for _ in range(10):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i]))
 
 
 @pytest.mark.parametrize("hint", [1, 3, 40])
