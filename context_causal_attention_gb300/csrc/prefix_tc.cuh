@@ -9,9 +9,8 @@
 //               cp.async (cp_prefix.cuh), into a ring of stages.  A page number
 //               out of range becomes a coordinate outside the tensor, which TMA
 //               fills with zeros.
-//               Warp 2 also gathers Q (a block's first by warps 1 and 3): the rows of
-//               a tile are query heads of one KV head from one or many sequences
-//               (16-byte cp.async, swizzled).
+//               Warp 2 also gathers Q: the rows of a tile are query heads of one
+//               KV head from one or many sequences (16-byte cp.async, swizzled).
 //   warps 1, 3  MMA issue of the two halves: S_i = Q_i K^T, O_i += P_i V with P_i
 //               in tensor memory (512 columns: S0 | S1 | O0 | O1).
 //   warps 4-7   softmax of rows 0..127, warps 8-11 of rows 128..255: one thread
@@ -227,12 +226,11 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                 for (uint32_t i = it > stages ? it - stages : 0; i < it && ok; ++i)
                     ok = mbar_wait_warp(full + i % stages, (i / stages) & 1u, abort_flag, a.timeout_ns);
                 if (!ok) break;
-                // (the first piece's: the MMA warps)
-                for (int i = 0; i < 2 && items && x.row0 + i * 128 < x.rows; ++i) {
+                ++items;
+                for (int i = 0; i < 2 && x.row0 + i * 128 < x.rows; ++i) {
                     copy_queries<D, C::kAtom>(a, x, x.row0 + i * 128, smem_u32(sQ) + i * C::kTile, lane);
                     copies_arrive(q_full + i);
                 }
-                ++items;
             }
             PageWindow win;
             win.begin(a, x, (x.k0 * kTcKT) >> shift, lane);
@@ -314,12 +312,6 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                 if (paired) commit(v_empty + st, lead);  // for the other half
                 return true;
             };
-            // The first piece's queries: nothing else to do yet, and one warp took 5.5 us to
-            // start the copies of 256 rows.
-            if (!pieces && x.row0 + i * 128 < x.rows) {
-                copy_queries<D, C::kAtom>(a, x, x.row0 + i * 128, smem_u32(sQ) + i * C::kTile, lane);
-                copies_arrive(q_full + i);
-            }
             // Also with no tile for this half (a piece of one tile): Q of a piece is
             // loaded when both halves are done with the last one's, so that neither
             // waits for a stage or a query tile more than one phase ahead, where the
@@ -358,7 +350,6 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                 commit(q_empty, lead);
             }
         }
-        copies_drain();
         // no MMA may still be running when tensor memory is released
         commit(drain + i, lead);
         volatile int no_abort = 0;
