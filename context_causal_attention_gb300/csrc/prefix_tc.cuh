@@ -346,8 +346,11 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                 if (!pv(base + last, last == begin)) { ok = false; break; }
                 commit(o_full + i, lead);
                 ++items;
-            } else {
-                commit(q_empty, lead);
+            } else if (lane == 0) {
+                // It multiplied nothing here and has nothing to wait for.  (With a commit in
+                // this place, none of the warp's own products on the way, the loader was seen to
+                // bring the next queries before the other half had read these.)
+                mbar_arrive(q_empty);
             }
         }
         // no MMA may still be running when tensor memory is released

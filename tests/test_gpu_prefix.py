@@ -258,6 +258,26 @@ def test_repeated_calls_agree(cuda_dev, new, N, Nkv, D, page):
         assert torch.equal(o, o2) and torch.equal(lse, lse2), i
 
 
+@pytest.mark.parametrize("B,top,most,N,Nkv,D,page,prefix,hint", [
+    (300, 200, 2, 24, 8, 64, 16, 0, 196), (300, 200, 2, 128, 8, 128, 128, 127, 2), (130, 190, 1, 85, 5, 128, 128, 3151, 1),
+    (300, 30, 4, 21, 3, 128, 128, 2573, 4), (300, 190, 4, 16, 16, 128, 256, 1000, 400), (300, 20, 4, 9, 3, 64, 64, 0, 400)])
+def test_many_short_sequences_on_wide_tiles(cuda_dev, B, top, most, N, Nkv, D, page, prefix, hint):
+    """Blocks that go through many pieces of one key tile, where only one half has work,
+    and a few of two: each piece has its own queries, over and over."""
+    g = torch.Generator().manual_seed(B + N)
+    new = torch.randint(0, most + 1, (B,), generator=g).tolist()
+    c = Call(16, new, [n + int(x) for n, x in zip(new, torch.randint(0, top, (B,), generator=g))], prefix, N, Nkv, D, page, 3)
+    c.run(cuda_dev)
+    q, k, v, pages, table, cu, kv_len = c.dev
+    first = F.cp_prefix_attn_fwd(q, k, v, pages, prefix, table, cu, kv_len, hint)
+    c.check(*first)
+    n = c.rows
+    for _ in range(10):
+        o, lse = F.cp_prefix_attn_fwd(q, k, v, pages, prefix, table, cu, kv_len, hint)
+        assert torch.equal(o[:n], first[0][:n]) and torch.equal(lse[:, :n], first[1][:, :n])
+    assert F.cp_device_status() == 0
+
+
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("new", [1, 40])
 def test_pages_past_32_bits_of_offset(cuda_dev, page, new):
