@@ -388,8 +388,8 @@ constexpr float kAroundWide = 36000.f, kAroundNarrow = 15000.f;
 
 // Workers of a lane for the prefix, so that the slower of the two kinds is done
 // soonest.  With the wide tile's cost (D = 128, small pages: 4250 cycles) a prefix of
-// 32768 keys and 64 sequences of up to 2048, 32 / 8 heads, take 86 us; at 3000 98.6, at
-// 3600 92.4, at 5000 86, at 5600 92.5.  In proportion
+// 32768 keys and 64 sequences of up to 2048, 32 / 8 heads, take 88 us; at 3000 100, at
+// 3600 93.6, at 5000 88, at 5600 93.  In proportion
 // to the costs alone (without what lies around the tiles, rounded) five tokens each
 // of 7 sequences behind 100003 keys, 16 heads of 64, got one worker where they need
 // two: 101 us, 95 so.  Warp-wide; at least two workers.
@@ -407,7 +407,7 @@ __device__ __forceinline__ int prefix_workers(float prefix, float own, int worke
 // the first are bound by their arithmetic and the second by memory, so a block does
 // one kind (prefix_workers).  As two launches, each leaving the other's blocks idle, the
 // idle blocks of the second waited for the first and the join for them: 93 us
-// where this took 87.  a: the prefix; b: the sequences.
+// where this took 88.  a: the prefix; b: the sequences.
 template <int D, bool tma>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_both_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
 // ---------------------------------------------------------------- host side
 // Up to this many rows (tokens x heads) a warp joins one, beyond it kJoinHeads heads
 // of a token.  Few rows have many pieces: a call of 64 tokens of 32 heads takes
-// 145 us with a warp for a token's heads and 86 with one for a row.  Many rows have
+// 141 us with a warp for a token's heads and 88 with one for a row.  Many rows have
 // few: the prompts above 1208 us by tokens and 1335 by rows.
 constexpr long long kJoinRows = 16384;
 
