@@ -36,11 +36,10 @@ inline cp_status cuda_status(cudaError_t e) {
 inline cp_status last_launch_status() { return cuda_status(cudaGetLastError()); }
 
 #ifdef __CUDACC__
-// Launches `kernel`; `after`: its blocks may start before the kernel before it in
-// the stream is complete (it waits for itself, wait_for_previous).
+// Launches a `kernel` whose blocks may start before the kernel before it in the
+// stream is complete (it waits for that itself, wait_for_previous).
 template <typename... P, typename... A>
-cp_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool after, cudaStream_t stream,
-                 const A &...args) {
+cp_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args) {
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
     c.blockDim = dim3(threads);
@@ -50,7 +49,7 @@ cp_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &at;
-    c.numAttrs = after ? 1 : 0;
+    c.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
     if (e != cudaSuccess) cudaGetLastError();
     return cuda_status(e);

@@ -762,7 +762,7 @@ cp_status launch_main(const PrefixArgs *wide, const PrefixArgs *narrow, cudaStre
     });
     if (err != cudaSuccess) return cuda_status(err);
     const dim3 grid(a.lanes, workers_of(a.lanes));
-    if (!wide) return launch(prefix_mma_kernel<D>, grid, kMmaThreads, MmaCfg<D>::kSmem, true, stream, a);
+    if (!wide) return launch(prefix_mma_kernel<D>, grid, kMmaThreads, MmaCfg<D>::kSmem, stream, a);
     const int64_t rows = static_cast<int64_t>(a.own.n_pages) << a.own.shift;
     const int page = 1 << a.own.shift, box = page < kTcKT ? page : kTcKT;
     // at D = 64 a head's row is 128 bytes and its neighbour another head's
@@ -771,11 +771,11 @@ cp_status launch_main(const PrefixArgs *wide, const PrefixArgs *narrow, cudaStre
     if (page >= kTmaPage) {
         if (!make_map(&mk, a.k, D, a.Nkv, rows, 1, box, l2) || !make_map(&mv, a.v, D, a.Nkv, rows, 1, box, l2))
             return CP_ERR_CUDA;
-        if (narrow) return launch(prefix_both_kernel<D, true>, grid, kTcThreads, both_smem, true, stream, mk, mv, a, *narrow);
-        return launch(prefix_tc_kernel<D, true>, grid, kTcThreads, TcCfg<D>::kSmem, true, stream, mk, mv, a);
+        if (narrow) return launch(prefix_both_kernel<D, true>, grid, kTcThreads, both_smem, stream, mk, mv, a, *narrow);
+        return launch(prefix_tc_kernel<D, true>, grid, kTcThreads, TcCfg<D>::kSmem, stream, mk, mv, a);
     }
-    if (narrow) return launch(prefix_both_kernel<D, false>, grid, kTcThreads, both_smem, true, stream, mk, mv, a, *narrow);
-    return launch(prefix_tc_kernel<D, false>, grid, kTcThreads, TcCfg<D>::kSmem, true, stream, mk, mv, a);
+    if (narrow) return launch(prefix_both_kernel<D, false>, grid, kTcThreads, both_smem, stream, mk, mv, a, *narrow);
+    return launch(prefix_tc_kernel<D, false>, grid, kTcThreads, TcCfg<D>::kSmem, stream, mk, mv, a);
 }
 
 template <int D>
@@ -818,7 +818,7 @@ cp_status launch_call(const PrefixArgs &call, const Shape &s, uint8_t *w, JoinAr
     const bool few = rows <= kJoinRows;
     const long long units = few ? rows : static_cast<long long>(call.R) * ((call.N + kJoinHeads - 1) / kJoinHeads);
     return launch(few ? join_row_kernel<D> : join_token_kernel<D>, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0,
-                  true, stream, j);
+                  stream, j);
 }
 
 cp_status check_sizes(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t N, int64_t Nkv, int64_t D,

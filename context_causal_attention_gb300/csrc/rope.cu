@@ -450,7 +450,7 @@ cp_status launch_bwd_typed(RowsArgs &a, float *dwq, float *dwk, cudaStream_t str
     norm_bwd_kernel<T, D, kOrder, kAll><<<grid, kThreads, kBwdSmem<T>, stream>>>(a);
     const cp_status st = last_launch_status();
     if (st != CP_OK) return st;
-    return launch(dw_sum_kernel, dim3(D / 32, 2), kSumWarps * 32, 0, true, stream, a.part, a.split, grid, D,
+    return launch(dw_sum_kernel, dim3(D / 32, 2), kSumWarps * 32, 0, stream, a.part, a.split, grid, D,
                   nq ? dwq : nullptr, nk ? dwk : nullptr);
 }
 
