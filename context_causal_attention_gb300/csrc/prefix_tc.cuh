@@ -68,6 +68,7 @@ struct TcCfg {
     static constexpr int kWalks = kTcThreads / 32;
     static constexpr int kBars = 16 + 2 * (kStagesK + kStagesV);
     static constexpr int kOffMisc = kOffBar + kBars * 8;
+    static_assert(kOffMisc % 16 == 0, "tensor memory's address is left on 16 bytes");
     static constexpr int kOffMl = (kOffMisc + 16 + 15) & ~15;        // [128] (m, l) of the second half
     static constexpr int kOffWalk = kOffMl + 128 * 8;   // [warps]
     static constexpr int kSmem = kOffWalk + kWalks * static_cast<int>(sizeof(Walk<kTcTM, kTcKT>)) + 1024;  // + alignment slack
