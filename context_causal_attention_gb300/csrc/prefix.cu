@@ -480,6 +480,18 @@ struct RowPieces {
     int first, n, r;
 };
 
+// Keys of sequence b, whose `count` new tokens begin at row `begin`, as the launch
+// before the join takes them (sequence_problem): where the counts make no sense
+// it has no rows there, and so no keys here (reported there).
+__device__ __forceinline__ long long own_keys(const JoinArgs &a, int b, int *begin, int *count) {
+    if (b < 0) return 0;
+    if (*begin < 0 || *count > a.R - *begin) {
+        *begin = *count = 0;
+        return 0;
+    }
+    return min(max(static_cast<long long>(__ldg(a.kv_len + b)), 0ll), a.most);
+}
+
 // A part of one token's rows, for all its heads.
 struct TokenPart {
     const float2 *slot_ml;
@@ -563,7 +575,7 @@ __global__ void __launch_bounds__(128) join_row_kernel(const JoinArgs a) {
     const int b = find_sequence(a.cu, a.B, tok, lane, &begin, &count);
     // inputs, as the search: before the wait
     const int all = min(max(__ldg(a.cu + a.B), 0), a.R);
-    const long long len = b < 0 ? 0 : min(max(static_cast<long long>(__ldg(a.kv_len + b)), 0ll), a.most);
+    const long long len = own_keys(a, b, &begin, &count);
     wait_for_previous();
     if (b < 0) return;
     float mx = -INFINITY, ls = 0.f, acc[kV];
@@ -631,7 +643,7 @@ __global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
     const int b = find_sequence(a.cu, a.B, tok, lane, &begin, &count);
     // inputs, as the search: before the wait
     const int all = min(max(__ldg(a.cu + a.B), 0), a.R);
-    const long long len = b < 0 ? 0 : min(max(static_cast<long long>(__ldg(a.kv_len + b)), 0ll), a.most);
+    const long long len = own_keys(a, b, &begin, &count);
     wait_for_previous();
     if (b < 0) return;
     const int heads = min(kJoinHeads, a.N - h0), h = h0 + min(lane, heads - 1), kvh = h / a.G;

@@ -395,6 +395,22 @@ def test_bad_lists_are_reported(cuda_dev, what):
         assert torch.equal(o[2:], good[0][2:]) and torch.equal(lse[:, 2:], good[1][:, 2:])
 
 
+@pytest.mark.parametrize("first,N", [(-(2 ** 29 - 31), 8), (-(2 ** 31), 8), (-(2 ** 31) + 101, 32), (-1, 8)])
+def test_counts_far_out_of_range_are_not_followed(cuda_dev, first, N):
+    """Counts whose products with the heads of a KV head pass 32 bits: reported, and
+    nothing outside the workspace is read into a result (NaN lies around it)."""
+    c = Call(17, [100], [200], 70, N, 1, 64, 16)
+    c.cu[0] = first
+    need = F.cp_prefix_attn_workspace_size(100, 1, 100, 70, N, 1, 64, 16, c.table.shape[1])
+    ws = torch.full((need + 8192,), 0xFF, dtype=torch.uint8, device=cuda_dev)
+    for _ in range(2):  # the second time, over what the first left
+        o, lse = c.run(cuda_dev, workspace=ws[4096:4096 + need])
+        assert F.cp_device_status() == 11
+        assert F.cp_device_status() == 0
+        assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    assert (ws[:4096] == 0xFF).all() and (ws[4096 + need:] == 0xFF).all()
+
+
 def test_append_then_attend_decodes_like_one_causal_attention(cuda_dev):
     """The operators together: a prefix and two prompts are appended (norm, rotation),
     then tokens one at a time; every step's attention equals the 64-bit causal
