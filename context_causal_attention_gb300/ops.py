@@ -448,9 +448,10 @@ def _head_rows(t):
     step, count = 0, 1
     for i in range(n - 3, -1, -1):
         if shape[i] > 1:
-            if step == 0:
+            if count == 1:
                 step = st[i]
-            elif st[i] != step * count:
+            # (an expanded dimension repeats its tokens: no distance at all)
+            if st[i] != step * count or step == 0:
                 raise ValueError("tokens must lie at one distance from one another")
             count *= shape[i]
     return (step if count > 1 else H * D), shape[:-2], H, D

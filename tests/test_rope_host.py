@@ -152,6 +152,20 @@ def test_binding_refusals(cplib):
         F.cp_rope_fwd(q, None, pos, rope)  # not on a GPU
 
 
+def test_repeated_tokens_are_refused(cplib):
+    """Rows that an expanded dimension repeats lie at no distance from one another: read as
+    tokens at the outer dimension's distance they would end far behind the tensor."""
+    assert F._head_rows(torch.zeros(3, 2, 4, 64)) == (256, (3, 2), 4, 64)
+    assert F._head_rows(torch.zeros(3, 1, 9, 64)[:, :, :4].expand(3, 1, 4, 64)) == (576, (3, 1), 4, 64)
+    for lead in ((3, 2), (2, 3, 2), (1, 3, 5)):
+        x = torch.zeros(*lead[:-1], 1, 4, 64).expand(*lead, 4, 64)
+        with pytest.raises(ValueError, match="one distance"):
+            F._head_rows(x)
+    for x in (torch.zeros(1, 2, 4, 64).expand(3, 2, 4, 64), torch.zeros(4, 64).expand(5, 4, 64)):
+        with pytest.raises(ValueError, match="one distance"):
+            F._head_rows(x)
+
+
 def test_prefix_attention_refusals(cplib):
     n = ctypes.c_size_t(0)
 
