@@ -292,13 +292,21 @@ __global__ void __launch_bounds__(kSumWarps * 32) dw_sum_kernel(const float *par
 // ---------------------------------------------------------------- host side
 bool misaligned(const void *p) { return p && !aligned16(p); }
 
-// One of q and k: `rows` tokens of `heads` head rows, `stride` elements apart.
+// One of q and k: `tokens` rows of heads * D values, `stride` elements apart.
 struct Rows {
     const char *p;
     long long bytes;  // from the first row to the end of the last
+    long long step, row;
     Rows(const void *q, long long tokens, long long stride, long long heads, long long D, size_t es)
-        : p(static_cast<const char *>(q)), bytes(q && heads ? ((tokens - 1) * stride + heads * D) * (long long)es : 0) {}
-    bool meets(const Rows &o) const { return bytes && o.bytes && p < o.p + o.bytes && o.p < p + bytes; }
+        : p(static_cast<const char *>(q)), bytes(q && heads ? ((tokens - 1) * stride + heads * D) * (long long)es : 0),
+          step(stride * (long long)es), row(heads * D * (long long)es) {}
+    // Whether any value belongs to both (false for slices side by side in the rows of one buffer).
+    bool meets(const Rows &o) const {
+        if (!bytes || !o.bytes || p >= o.p + o.bytes || o.p >= p + bytes) return false;
+        if (step != o.step) return true;
+        const long long at = ((o.p - p) % step + step) % step;  // o's rows begin so far behind these
+        return at < row || at + o.row > step;
+    }
 };
 
 cp_status check_sizes(int64_t C, int64_t B, int64_t s, int64_t N, int64_t Nkv, int64_t D) {
@@ -344,9 +352,8 @@ cp_status fill_rows(RowsArgs *a, const void *q, const void *k, void *qo, void *k
     const bool in_q = N && q == qo, in_k = Nkv && k == ko;
     const Rows rq(q, tokens, qs, N, D, es), rk(k, tokens, ks, Nkv, D, es);
     const Rows oq(qo, tokens, in_q ? qs : N * D, N, D, es), ok(ko, tokens, in_k ? ks : Nkv * D, Nkv, D, es);
-    if (!in_q && (oq.meets(rq) || oq.meets(rk))) return CP_ERR_ARGUMENT;
-    if (!in_k && (ok.meets(rq) || ok.meets(rk))) return CP_ERR_ARGUMENT;
-    if ((!in_q || !in_k) && oq.meets(ok)) return CP_ERR_ARGUMENT;
+    if ((!in_q && oq.meets(rq)) || (!in_k && ok.meets(rk)) || oq.meets(rk) || ok.meets(rq) || oq.meets(ok))
+        return CP_ERR_ARGUMENT;
     *a = RowsArgs{};
     a->x[0] = q, a->x[1] = k;
     a->y[0] = qo, a->y[1] = ko;

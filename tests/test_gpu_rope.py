@@ -140,6 +140,36 @@ def test_strided_rows_and_in_place(cuda_dev, dt, call):
     assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(qkv[:, :, N + Nkv:], v)
 
 
+@pytest.mark.parametrize("which", ["q", "k", "both"])
+@pytest.mark.parametrize("order", ["qkv", "kvq", "one_token"])
+def test_one_of_two_slices_in_place(cuda_dev, which, order):
+    """Slices of one buffer lie side by side, so either may be turned in place while the
+    other goes elsewhere; the heads between them stay."""
+    g = torch.Generator().manual_seed(12)
+    N, Nkv, D = 3, 2, 64
+    rows = rand(g, (1 if order == "one_token" else 41, N + 2 * Nkv, D), "bf16").to(cuda_dev)
+    at = (2 * Nkv, 0) if order == "kvq" else (0, N)
+    cut = lambda t: (t[:, at[0]:at[0] + N], t[:, at[1]:at[1] + Nkv])  # noqa: E731
+    pos = torch.arange(len(rows), dtype=torch.int32, device=cuda_dev)
+    rope, _, _ = rope_of(32, "half")
+    w = [1 + 0.1 * torch.randn(D, generator=g).to(cuda_dev) for _ in range(2)]
+    grads = [rand(g, (len(rows), h, D), "bf16").to(cuda_dev) for h in (N, Nkv)]
+    calls = [lambda a, b, x=None, y=None: F.cp_rope_fwd(a, b, pos, rope, x, y),
+             lambda a, b, x=None, y=None: F.cp_qk_norm_rope_fwd(a, b, *w, pos, rope, q_out=x, k_out=y),
+             lambda a, b, x=None, y=None: F.cp_qk_norm_rope_bwd(*grads, a, b, *w, pos, rope, dq=x, dk=y)]
+    for i, call in enumerate(calls):
+        want = call(*(t.contiguous() for t in cut(rows)))
+        buf = rows.clone()
+        q, k = cut(buf)
+        got = call(q, k, q if which != "k" else None, k if which != "q" else None)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+        kept = torch.ones(N + 2 * Nkv, dtype=torch.bool, device=cuda_dev)
+        for t, n in ((0, N), (1, Nkv)):
+            if which in ("both", "qk"[t]):
+                kept[at[t]:at[t] + n] = False
+        assert torch.equal(buf[:, kept], rows[:, kept]), i
+
+
 def test_backward_in_place_and_bf16_weights(cuda_dev):
     g = torch.Generator().manual_seed(6)
     q, k, gq, gk = (rand(g, (1, 1, 50, h, 64), "bf16").to(cuda_dev) for h in (4, 2, 4, 2))

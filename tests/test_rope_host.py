@@ -80,6 +80,25 @@ def test_rope_refusals(cplib, name):
         assert bad(**kw) == 5, kw
 
 
+def test_rows_written_over_other_rows_are_refused(cplib):
+    """In place is where an output is its own input; an output over the other tensor's rows
+    (q and k the same rows, or slices of one buffer that share heads) is not."""
+    one, four = 64 * 2, 4 * 64 * 2  # bytes of a head, of q's row
+    same = dict(N=4, Nkv=4, ks=256)
+    for name in ("cp_rope_fwd", "cp_rope_bwd"):
+        for kw in (
+                dict(q=FAR[0], k=FAR[0], qo=FAR[0], ko=FAR[0], **same),       # both in place of the same rows
+                dict(q=FAR[0], k=FAR[0], qo=FAR[0], ko=FAR[3], **same),       # q in place, k reads those rows
+                dict(q=FAR[0], k=FAR[0], qo=FAR[2], ko=FAR[0], **same),
+                dict(q=FAR[0], k=FAR[0] + one, qo=FAR[0], ko=FAR[0] + one, qs=512, ks=512),
+                dict(q=FAR[0], k=FAR[0] + four - one, qo=FAR[0], ko=FAR[0] + four - one, qs=512, ks=512),
+                dict(q=FAR[0] + one, k=FAR[0], qo=FAR[0] + one, ko=FAR[0], qs=512, ks=512),
+                # k's last head is q's first of the next token
+                dict(q=FAR[0], k=FAR[0] + 7 * one, qo=FAR[0], ko=FAR[0] + 7 * one, qs=512, ks=512),
+                dict(q=FAR[0], k=FAR[0] + four, qo=FAR[0], ko=FAR[0] + four, qs=512, ks=384)):
+            assert rope(cplib, name, **kw) == 10, kw
+
+
 def test_norm_refusals(cplib):
     def fwd(q=FAR[0], wq=FAKE, wk=FAKE, pos=FAKE, r="default", eps=1e-6, wd=1, dt=0):
         return cplib.cp_qk_norm_rope_fwd(q, FAR[1], wq, wk, pos, 1, 1, 8, 4, 2, 64, 256, 128, dt, wd, eps,
