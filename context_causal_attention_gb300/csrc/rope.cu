@@ -601,6 +601,9 @@ extern "C" cp_status cp_qk_norm_rope_bwd(const void *dq_out, const void *dk_out,
     const bool same_q = dq == dq_out && a.ys[0] == N * D, same_k = dk == dk_out && a.ys[1] == Nkv * D;
     if ((!same_q && oq.meets(gq)) || (!same_k && ok.meets(gk)) || oq.meets(gk) || ok.meets(gq))
         return CP_ERR_ARGUMENT;
+    // one buffer for both sums would keep one of them
+    const Rows wq_sum(dwq, 1, D, N ? 1 : 0, D, sizeof(float)), wk_sum(dwk, 1, D, Nkv ? 1 : 0, D, sizeof(float));
+    if (wq_sum.meets(wk_sum)) return CP_ERR_ARGUMENT;
     size_t need = 0;
     cp_qk_norm_rope_bwd_workspace_size(C, B, s, N, Nkv, D, &need);
     if (!workspace || ws_bytes < need) return CP_ERR_WORKSPACE;

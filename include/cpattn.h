@@ -520,7 +520,8 @@ cp_status cp_qk_norm_rope_fwd(const void *q, const void *k, const void *wq, cons
  *   dq, dk         : device, `dtype`, written dense, or in place of q (k) with its stride, or in
  *                    place of dq_out (dk_out)
  *   dwq, dwk       : device fp32 [D], written (sums in fp32, in a fixed order: the same
- *                    from run to run)
+ *                    from run to run); apart from one another (CP_ERR_ARGUMENT else), also where wq
+ *                    and wk are one vector, whose gradient is their sum
  *   workspace      : device, >= cp_qk_norm_rope_bwd_workspace_size bytes,
  *                    256-byte aligned; overwritten (stream-ordered), not read back
  */

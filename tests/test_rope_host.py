@@ -124,6 +124,15 @@ def test_norm_refusals(cplib):
     assert bwd(dq=FAR[4] + 16) == 10 and bwd(dq=FAR[5]) == 10 and bwd(dk=FAR[4]) == 10
 
 
+def test_weight_gradients_that_share_memory_are_refused(cplib):
+    def bwd(dwq, dwk):
+        return cplib.cp_qk_norm_rope_bwd(FAR[4], FAR[5], FAR[0], FAR[1], FAKE, FAKE, FAKE, 1, 1, 8, 4, 2, 64, 256, 128,
+                                         0, 1, 1e-6, spec(), FAR[2], FAR[3], dwq, dwk, FAR[8], 1 << 30, None)
+
+    for off in (0, 4, 252, -4, -252):
+        assert bwd(FAR[6], FAR[6] + off) == 10, off
+
+
 def test_append_refusals(cplib):
     def app(q=FAR[0], k=FAR[1], v=FAR[2], qs=256, ks=128, vs=128, dt=0, R_=8, N=4, Nkv=2, D=64, wq=None, wk=None, wd=1,
             eps=1e-6, r="default", base=0, kc=FAR[3], vc=FAR[4], pages=10, page=16, table=FAKE, B=2, most=4, cu=FAKE,
