@@ -219,7 +219,9 @@ extern "C" cp_status cp_cache_append(const void *q, const void *k, const void *v
         misaligned(wk) || (reinterpret_cast<uintptr_t>(table) & 3u) || (reinterpret_cast<uintptr_t>(cu_new) & 3u) ||
         (reinterpret_cast<uintptr_t>(kv_len) & 3u))
         return CP_ERR_ALIGNMENT;
-    if (k_cache == v_cache) return CP_ERR_ARGUMENT;
+    const char *kc = static_cast<const char *>(k_cache), *vc = static_cast<const char *>(v_cache);
+    const int64_t cache = n_pages * page_size * Nkv * D * 2;
+    if (kc < vc + cache && vc < kc + cache) return CP_ERR_ARGUMENT;
     // q_out: dense rows; in place only where the query rows are dense bf16 themselves
     if (N) {
         const char *o0 = static_cast<const char *>(q_out), *o1 = o0 + R * N * D * 2;
@@ -230,6 +232,7 @@ extern "C" cp_status cp_cache_append(const void *q, const void *k, const void *v
         const bool in_place = q == q_out && dtype == CP_BF16 && q_stride == N * D;
         if ((!in_place && meets(q, q_stride, N)) || meets(k, k_stride, Nkv) || meets(v, v_stride, Nkv))
             return CP_ERR_ARGUMENT;
+        if ((o0 < kc + cache && kc < o1) || (o0 < vc + cache && vc < o1)) return CP_ERR_ARGUMENT;
     }
     AppendArgs a{};
     a.x[0] = q, a.x[1] = k, a.x[2] = v;

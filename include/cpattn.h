@@ -554,7 +554,8 @@ cp_status cp_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void
  *   wq, wk  : device [D] of w_dtype, or NULL: no norm of q (k); eps as above
  *   rope    : NULL for no rotation
  *   q_out   : device bf16 [R][N][D], the normed and rotated queries (may be q itself when q is
- *             dense bf16)
+ *             dense bf16; any other overlap with the rows or the caches, and of the caches
+ *             with one another, is refused: CP_ERR_ARGUMENT)
  * The prefix itself is appended as a sequence with its own table.
  * page_size in {16, 32, 64, 128, 256} and D in {64, 128} (else
  * CP_ERR_UNSUPPORTED); B <= 4096; n_pages * page_size and max_pages *

@@ -158,6 +158,20 @@ def test_append_refusals(cplib):
         assert app(**kw) == 5, kw
 
 
+def test_append_refuses_caches_that_overlap(cplib):
+    size = 10 * 16 * 2 * 64 * 2  # bytes of a cache
+
+    def app(kc=FAR[3], vc=FAR[4], qo=FAR[5]):
+        return cplib.cp_cache_append(FAR[0], FAR[1], FAR[2], 256, 128, 128, 0, 8, 4, 2, 64, None, None, 1, 1e-6, spec(),
+                                     0, kc, vc, 10, 16, FAKE, 2, 4, FAKE, FAKE, qo, None)
+
+    for off in (0, 16, size - 16, -16, 16 - size):
+        assert app(vc=FAR[3] + off) == 10, off
+    for cache in (FAR[3], FAR[4]):
+        for off in (0, size - 16, 16 - 8 * 4 * 64 * 2):
+            assert app(qo=cache + off) == 10, off
+
+
 def test_binding_refusals(cplib):
     """Shapes, strides and devices that the binding refuses before the call."""
     rope = F.cp_rope_freqs(64, device="cpu")
