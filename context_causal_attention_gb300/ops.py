@@ -2,7 +2,9 @@
 
 Argument marshalling only: shapes and pointers are read from torch tensors,
 outputs are allocated with torch when not given, and the call is enqueued on
-the current torch CUDA stream.  All arithmetic happens in the CUDA library.
+the current torch CUDA stream, or on `stream` (a torch.cuda.Stream) where one is
+given: outputs and scratch then come out of that stream's memory, and the caller
+orders the streams.  All arithmetic happens in the CUDA library.
 """
 import ctypes
 import math
@@ -60,6 +62,28 @@ def cp_version():
     return _lib.lib().cp_version().decode()
 
 
+def _scratch(nbytes, device, stream):
+    """A call's scratch on `stream`, out of that stream's memory: it goes back there when the call
+    returns, so nothing but later work of the same stream is given it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _new(shape, dtype, device, stream):
+    """An output of a call on `stream`, out of that stream's memory: nothing that is still at work
+    on another stream used the place before, and an output that is dropped early goes to later work
+    of that stream only.  The current stream, which will read it, is waited for then too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def cp_zigzag_shard(x, C, layout=CP_ZIGZAG, out=None, stream=None):
     """x [B,S,N,D] -> rank-major shards [C,B,S/C,N,D] (bit-exact permutation).
 
@@ -68,7 +92,7 @@ def cp_zigzag_shard(x, C, layout=CP_ZIGZAG, out=None, stream=None):
     B, S, N, D = x.shape
     if out is None:
         dev = x.device if x.is_cuda else torch.device("cuda", torch.cuda.current_device())
-        out = torch.empty((C, B, S // C, N, D), dtype=x.dtype, device=dev)
+        out = _new((C, B, S // C, N, D), x.dtype, dev, stream)
     st = _lib.lib().cp_zigzag_shard(_ptr(x, host_ok=True), _ptr(out), B, S, N, D, C, _dtype_code(x), layout,
                                     _stream(stream))
     _lib.check("cp_zigzag_shard", st)
@@ -82,7 +106,7 @@ def cp_zigzag_unshard(x_sh, layout=CP_ZIGZAG, out=None, stream=None):
     host link (unshard and device-to-host copy in one pass)."""
     C, B, s, N, D = x_sh.shape
     if out is None:
-        out = torch.empty((B, C * s, N, D), dtype=x_sh.dtype, device=x_sh.device)
+        out = _new((B, C * s, N, D), x_sh.dtype, x_sh.device, stream)
     st = _lib.lib().cp_zigzag_unshard(_ptr(x_sh), _ptr(out, host_ok=True), B, C * s, N, D, C, _dtype_code(x_sh),
                                       layout, _stream(stream))
     _lib.check("cp_zigzag_unshard", st)
@@ -93,7 +117,7 @@ def cp_zigzag_positions(S, C, layout=CP_ZIGZAG, device="cuda", out=None, stream=
     """int32 [C, S/C] global positions of every local token."""
     dev = torch.device(device)
     if out is None:
-        out = torch.empty((C, S // C), dtype=torch.int32, device=dev)
+        out = _new((C, S // C), torch.int32, dev, stream)
     on_dev = 1 if out.is_cuda else 0
     st = _lib.lib().cp_zigzag_positions(_ptr(out, host_ok=True), S, C, layout, on_dev,
                                         _stream(stream) if on_dev else None)
@@ -114,7 +138,7 @@ def cp_ulysses_relayout(x, C, direction=CP_SEQ_TO_HEAD, order=CP_RANK_ORDER, out
     if Cx != C:
         raise ValueError("leading dimension must be C")
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _new(shape, x.dtype, x.device, stream)
     st = _lib.lib().cp_ulysses_relayout(_ptr(x), _ptr(out), B, S, N, D, C, _dtype_code(x), direction, order,
                                         _stream(stream))
     _lib.check("cp_ulysses_relayout", st)
@@ -136,9 +160,9 @@ def cp_attn_partial(q, k, v, q_pos, k_pos, scale=None, o=None, lse=None, workspa
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if o is None:
-        o = torch.empty((B, Sq, N, D), dtype=torch.float32, device=q.device)
+        o = _new((B, Sq, N, D), torch.float32, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, N, Sq), dtype=torch.float32, device=q.device)
+        lse = _new((B, N, Sq), torch.float32, q.device, stream)
     L = _lib.lib()
     need = cp_attn_workspace_size(B, Sq, Sk, N, Nkv, D)
     if need == 0 and workspace is None:
@@ -147,7 +171,7 @@ def cp_attn_partial(q, k, v, q_pos, k_pos, scale=None, o=None, lse=None, workspa
         _lib.check("cp_attn_partial", st)
         return o, lse
     if workspace is None:
-        workspace = torch.empty(max(256, need), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(256, need), q.device, stream)
     st = L.cp_attn_partial_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(q_pos), _ptr(k_pos), B, Sq, Sk, N, Nkv, D, float(scale),
                               _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                               _stream(stream))
@@ -163,14 +187,14 @@ def cp_attn_partial_f32(q, k, v, q_pos, k_pos, scale=None, o=None, lse=None, wor
         scale = 1.0 / math.sqrt(D)
     dev = q.device
     if o is None:
-        o = torch.empty((B, Sq, N, D), dtype=torch.float32, device=dev)
+        o = _new((B, Sq, N, D), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((B, N, Sq), dtype=torch.float32, device=dev)
+        lse = _new((B, N, Sq), torch.float32, dev, stream)
     L = _lib.lib()
     n = ctypes.c_size_t(0)
     _lib.check("cp_attn_f32_workspace_size", L.cp_attn_f32_workspace_size(B, Sq, Sk, N, Nkv, D, ctypes.byref(n)))
     if workspace is None:
-        workspace = torch.empty(max(256, n.value), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(256, n.value), dev, stream)
     st = L.cp_attn_partial_f32(_ptr(q), _ptr(k), _ptr(v), _ptr(q_pos), _ptr(k_pos), B, Sq, Sk, N, Nkv, D, float(scale),
                                _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                _stream(stream))
@@ -214,12 +238,12 @@ def cp_ring_attention_fwd(q_sh, k_sh, v_sh, pos, scale=None, layout=CP_ZIGZAG, p
         scale = 1.0 / math.sqrt(D)
     dev = q_sh.device
     if o is None:
-        o = torch.empty((C, B, s, N, D), dtype=torch.float32 if o_dtype == CP_F32 else torch.bfloat16, device=dev)
+        o = _new((C, B, s, N, D), torch.float32 if o_dtype == CP_F32 else torch.bfloat16, dev, stream)
     if lse is None:
-        lse = torch.empty((C, B, N, s), dtype=torch.float32, device=dev)
+        lse = _new((C, B, N, s), torch.float32, dev, stream)
     need = cp_ring_workspace_size(B, S, N, Nkv, D, C, prefetch, o_dtype, fused_merge, tf32)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(need, 256), dev, stream)
     L = _lib.lib()
     args = [_ptr(q_sh), _ptr(k_sh), _ptr(v_sh), _ptr(pos), B, S, N, Nkv, D, C, float(scale), layout,
             _ring_flags(prefetch, fused_merge, tf32),
@@ -245,14 +269,14 @@ def cp_allgather_attention_fwd(q_sh, k_sh, v_sh, pos, scale=None, layout=CP_ZIGZ
         scale = 1.0 / math.sqrt(D)
     dev = q_sh.device
     if o is None:
-        o = torch.empty((C, B, s, N, D), dtype=torch.float32, device=dev)
+        o = _new((C, B, s, N, D), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((C, B, N, s), dtype=torch.float32, device=dev)
+        lse = _new((C, B, N, s), torch.float32, dev, stream)
     L = _lib.lib()
     n = ctypes.c_size_t(0)
     _lib.check("cp_allgather_workspace_size", L.cp_allgather_workspace_size(B, S, N, Nkv, D, C, ctypes.byref(n)))
     if workspace is None:
-        workspace = torch.empty(max(256, n.value), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(256, n.value), dev, stream)
     st = L.cp_allgather_attention_fwd(_ptr(q_sh), _ptr(k_sh), _ptr(v_sh), _ptr(pos), B, S, N, Nkv, D, C,
                                       float(scale), layout, _ptr(o), _ptr(lse), _ptr(workspace),
                                       workspace.numel() * workspace.element_size(), _stream(stream))
@@ -270,14 +294,14 @@ def cp_ulysses_attention_fwd(q_sh, k_sh, v_sh, scale=None, layout=CP_ZIGZAG, wor
         scale = 1.0 / math.sqrt(D)
     dev = q_sh.device
     if o is None:
-        o = torch.empty((C, B, s, N, D), dtype=torch.float32, device=dev)
+        o = _new((C, B, s, N, D), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((C, B, N // C, S), dtype=torch.float32, device=dev)
+        lse = _new((C, B, N // C, S), torch.float32, dev, stream)
     L = _lib.lib()
     n = ctypes.c_size_t(0)
     _lib.check("cp_ulysses_workspace_size", L.cp_ulysses_workspace_size(B, S, N, Nkv, D, C, ctypes.byref(n)))
     if workspace is None:
-        workspace = torch.empty(max(256, n.value), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(256, n.value), dev, stream)
     st = L.cp_ulysses_attention_fwd(_ptr(q_sh), _ptr(k_sh), _ptr(v_sh), B, S, N, Nkv, D, C, float(scale), layout,
                                     _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                     _stream(stream))
@@ -306,12 +330,12 @@ def cp_mesh_attention_fwd(q_sh, k_sh, v_sh, pos, A, R, scale=None, layout=CP_ZIG
         scale = 1.0 / math.sqrt(D)
     dev = q_sh.device
     if o is None:
-        o = torch.empty((C, B, s, N, D), dtype=torch.float32, device=dev)
+        o = _new((C, B, s, N, D), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((R, A, B, N // A, S // R), dtype=torch.float32, device=dev)
+        lse = _new((R, A, B, N // A, S // R), torch.float32, dev, stream)
     need = cp_mesh_workspace_size(B, S, N, Nkv, D, A, R, prefetch, fused_merge)
     if workspace is None:
-        workspace = torch.empty(max(256, need), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(256, need), dev, stream)
     st = _lib.lib().cp_mesh_attention_fwd(_ptr(q_sh), _ptr(k_sh), _ptr(v_sh), _ptr(pos), B, S, N, Nkv, D, A, R,
                                           float(scale), layout, _ring_flags(prefetch, fused_merge), _ptr(o),
                                           _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -329,14 +353,14 @@ def cp_attn_bwd_partial(q, k, v, o, dout, lse, q_pos, k_pos, scale=None, dq=None
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     dev = q.device
-    dq = torch.empty((B, Sq, N, D), dtype=torch.float32, device=dev) if dq is None else dq
-    dk = torch.empty((B, Sk, Nkv, D), dtype=torch.float32, device=dev) if dk is None else dk
-    dv = torch.empty((B, Sk, Nkv, D), dtype=torch.float32, device=dev) if dv is None else dv
+    dq = _new((B, Sq, N, D), torch.float32, dev, stream) if dq is None else dq
+    dk = _new((B, Sk, Nkv, D), torch.float32, dev, stream) if dk is None else dk
+    dv = _new((B, Sk, Nkv, D), torch.float32, dev, stream) if dv is None else dv
     L = _lib.lib()
     n = ctypes.c_size_t(0)
     _lib.check("cp_attn_bwd_workspace_size", L.cp_attn_bwd_workspace_size(B, Sq, Sk, N, ctypes.byref(n)))
     if workspace is None:
-        workspace = torch.empty(max(256, n.value), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(256, n.value), dev, stream)
     st = L.cp_attn_bwd_partial(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(q_pos), _ptr(k_pos), B,
                                Sq, Sk, N, Nkv, D, float(scale), _ptr(dq), _ptr(dk), _ptr(dv), 1 if accumulate else 0,
                                _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
@@ -359,11 +383,11 @@ def cp_ring_attention_bwd(q_sh, k_sh, v_sh, o_sh, lse_sh, do_sh, pos, scale=None
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     dev = q_sh.device
-    dq = torch.empty((C, B, s, N, D), dtype=torch.float32, device=dev) if dq is None else dq
-    dk = torch.empty((C, B, s, Nkv, D), dtype=torch.float32, device=dev) if dk is None else dk
-    dv = torch.empty((C, B, s, Nkv, D), dtype=torch.float32, device=dev) if dv is None else dv
+    dq = _new((C, B, s, N, D), torch.float32, dev, stream) if dq is None else dq
+    dk = _new((C, B, s, Nkv, D), torch.float32, dev, stream) if dk is None else dk
+    dv = _new((C, B, s, Nkv, D), torch.float32, dev, stream) if dv is None else dv
     if workspace is None:
-        workspace = torch.empty(max(256, cp_ring_bwd_workspace_size(B, S, N, C)), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(256, cp_ring_bwd_workspace_size(B, S, N, C)), dev, stream)
     st = _lib.lib().cp_ring_attention_bwd(_ptr(q_sh), _ptr(k_sh), _ptr(v_sh), _ptr(o_sh), _ptr(lse_sh), _ptr(do_sh),
                                           _ptr(pos), B, S, N, Nkv, D, C, float(scale), layout, _ptr(dq), _ptr(dk),
                                           _ptr(dv), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -481,12 +505,12 @@ def _check_pos(pos, C, s):
         raise ValueError("pos must be contiguous int32 [C, s]")
 
 
-def _row_out(out, x):
+def _row_out(out, x, stream):
     """An output of x's rows: a new dense one, x itself (in place), or a dense one that was given."""
     if x is None:
         return None
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return _new(x.shape, x.dtype, x.device, stream)
     if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("an output must have its input's shape and dtype")
     if out.data_ptr() == x.data_ptr():
@@ -504,7 +528,7 @@ def _addr(t):
 def _rope_call(name, q, k, pos, rope, q_out, k_out, stream):
     C, B, s, N, Nkv, D, qs, ks = _qk(q, k)
     _check_pos(pos, C, s)
-    q_out, k_out = _row_out(q_out, q), _row_out(k_out, k)
+    q_out, k_out = _row_out(q_out, q, stream), _row_out(k_out, k, stream)
     dev = _here(q, k, pos, rope.freqs, q_out, k_out)
     st = getattr(_lib.lib(), name)(_addr(q), _addr(k), _addr(pos), C, B, s, N, Nkv, D, qs, ks, _dtype_code(q),
                                    rope._ref, _addr(q_out), _addr(k_out), _raw_stream(stream, dev))
@@ -541,7 +565,7 @@ def cp_qk_norm_rope_fwd(q, k, wq, wk, pos, rope, eps=1e-6, q_out=None, k_out=Non
     if rope is not None:
         _check_pos(pos, C, s)
     wd = _check_weights(wq, wk, D)
-    q_out, k_out = _row_out(q_out, q), _row_out(k_out, k)
+    q_out, k_out = _row_out(q_out, q, stream), _row_out(k_out, k, stream)
     dev = _here(q, k, wq, wk, pos, None if rope is None else rope.freqs, q_out, k_out)
     st = _lib.lib().cp_qk_norm_rope_fwd(_addr(q), _addr(k), _addr(wq), _addr(wk), _addr(pos), C, B, s, N, Nkv, D, qs,
                                         ks, _dtype_code(q), wd, eps, None if rope is None else rope._ref,
@@ -569,18 +593,17 @@ def cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, pos, rope, eps=1e-6, dq=No
         if (g is None) != (x is None) or (g is not None and (g.shape != x.shape or g.dtype != x.dtype or
                                                              not g.is_contiguous())):
             raise ValueError("the gradients must be dense, of the inputs' shapes and dtype")
-    dq = dq_out if dq is dq_out else _row_out(dq, q)
-    dk = dk_out if dk is dk_out else _row_out(dk, k)
+    dq = dq_out if dq is dq_out else _row_out(dq, q, stream)
+    dk = dk_out if dk is dk_out else _row_out(dk, k, stream)
     if dwq is None:
-        dwq = torch.empty(D, dtype=torch.float32, device=q.device)
+        dwq = _new(D, torch.float32, q.device, stream)
     if dwk is None and k is not None:
-        dwk = torch.empty(D, dtype=torch.float32, device=q.device)
+        dwk = _new(D, torch.float32, q.device, stream)
     for w in (dwq, dwk):
         if w is not None and (w.dtype != torch.float32 or w.numel() != D or not w.is_contiguous()):
             raise ValueError("weight gradients must be contiguous fp32 [D]")
     if workspace is None:
-        workspace = torch.empty(max(256, cp_qk_norm_rope_bwd_workspace_size(C, B, s, N, Nkv, D)), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _scratch(max(256, cp_qk_norm_rope_bwd_workspace_size(C, B, s, N, Nkv, D)), q.device, stream)
     dev = _here(dq_out, dk_out, q, k, wq, wk, pos, None if rope is None else rope.freqs, dq, dk, dwq, dwk, workspace)
     st = _lib.lib().cp_qk_norm_rope_bwd(_addr(dq_out), _addr(dk_out), _addr(q), _addr(k), _addr(wq), _addr(wk),
                                         _addr(pos), C, B, s, N, Nkv, D, qs, ks, _dtype_code(q), wd, eps,
@@ -625,7 +648,7 @@ def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=
         if lead != shape[:1] or Dq != D or q.dtype is not dtype:
             raise ValueError("q must be [R, N, D] of k's tokens and dtype")
         if q_out is None:
-            q_out = torch.empty((R, N, D), dtype=torch.bfloat16, device=q.device)
+            q_out = _new((R, N, D), torch.bfloat16, q.device, stream)
         elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous bf16 [R, N, D]")
     elif q_out is not None:
@@ -663,16 +686,16 @@ def cp_prefix_attn_fwd(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if o is None:
-        o = torch.empty((R, N, D), dtype=torch.float32 if o_dtype == CP_F32 else torch.bfloat16, device=q.device)
+        o = _new((R, N, D), torch.float32 if o_dtype == CP_F32 else torch.bfloat16, q.device, stream)
     elif o.shape != q.shape or not o.is_contiguous():
         raise ValueError("o must be contiguous [R, N, D]")
     if lse is None:
-        lse = torch.empty((N, R), dtype=torch.float32, device=q.device)
+        lse = _new((N, R), torch.float32, q.device, stream)
     elif lse.shape != (N, R) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [N, R]")
     if workspace is None:
-        workspace = torch.empty(max(256, cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page,
-                                                                       max_pages)), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(256, cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page,
+                                                                    max_pages)), q.device, stream)
     dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, o, lse, workspace)
     st = _lib.lib().cp_prefix_attn_fwd(_addr(q), _addr(k_cache), _addr(v_cache), n_pages, page, _addr(prefix_pages),
                                        prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), max_new,
@@ -699,7 +722,7 @@ def cp_selftest_stalled_kernel(kernel, timeout_ns, scratch=None, device="cuda", 
     (backward: its dK/dV and dQ launches), on a tiny problem laid out in
     `scratch` (allocated here unless given)."""
     if scratch is None:
-        scratch = torch.empty(CP_SELFTEST_SCRATCH_BYTES, dtype=torch.uint8, device=device)
+        scratch = _scratch(CP_SELFTEST_SCRATCH_BYTES, device, stream)
     st = _lib.lib().cp_selftest_stalled_kernel(int(kernel), _ptr(scratch), scratch.numel() * scratch.element_size(),
                                                int(timeout_ns), _stream(stream))
     _lib.check("cp_selftest_stalled_kernel", st)

@@ -118,3 +118,71 @@ def test_two_host_threads_run_rings_at_once(cuda_dev):
         for o, l in out[i]:
             assert torch.equal(o, ref[i][0]) and torch.equal(l, ref[i][1])
     assert F.cp_device_status() == 0
+
+
+def _side_calls(dev):
+    """Calls that allocate outputs and scratch: name -> (call(stream), bytes of its scratch)."""
+    g = torch.Generator().manual_seed(9)
+    mk = lambda *shape: torch.randn(*shape, generator=g).to(torch.bfloat16).to(dev)  # noqa: E731
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    q, k, v = mk(1, 512, 4, 64), mk(1, 512, 2, 64), mk(1, 512, 2, 64)
+    pos = torch.arange(512, dtype=torch.int32, device=dev)
+    w = [torch.ones(64, device=dev) for _ in range(2)]
+    rope = F.cp_rope_freqs(64, device=dev)
+    kc, vc = mk(64, 16, 2, 64), mk(64, 16, 2, 64)
+    table = torch.arange(64, dtype=torch.int32, device=dev).view(2, 32)
+    cu, kv_len, new = i32(0, 20, 40), i32(400, 500), mk(40, 8, 64)
+    pages = i32(*range(64))
+    qs, ks, vs = (F.cp_zigzag_shard(t, 4) for t in (q, k, v))
+    zz = F.cp_zigzag_positions(512, 4, device=dev)
+    o, lse = F.cp_attn_partial(q, k, v, pos, pos)
+    return {
+        "shard": (lambda s: F.cp_zigzag_shard(q, 4, stream=s), 0),
+        "rope": (lambda s: F.cp_rope_fwd(q, k, pos, rope, stream=s), 0),
+        "norm_bwd": (lambda s: F.cp_qk_norm_rope_bwd(q, k, q, k, *w, pos, rope, stream=s),
+                     F.cp_qk_norm_rope_bwd_workspace_size(1, 1, 512, 4, 2, 64)),
+        "append": (lambda s: F.cp_cache_append(new[:, :2], new[:, 2:4], kc, vc, table, cu, kv_len, rope=rope, q=new,
+                                               stream=s), 0),
+        "prefix": (lambda s: F.cp_prefix_attn_fwd(new, kc, vc, pages, 1000, table, cu, kv_len, 20, stream=s),
+                   F.cp_prefix_attn_workspace_size(40, 2, 20, 1000, 8, 2, 64, 16, 32)),
+        "ring": (lambda s: F.cp_ring_attention_fwd(qs, ks, vs, zz, prefetch=1, stream=s),
+                 F.cp_ring_workspace_size(1, 512, 4, 2, 64, 4, 1)),
+        "bwd": (lambda s: F.cp_attn_bwd_partial(q, k, v, o, q, lse, pos, pos, stream=s), 256),
+    }
+
+
+@pytest.mark.parametrize("keep", [True, False])
+@pytest.mark.parametrize("name", ["shard", "rope", "norm_bwd", "append", "prefix", "ring", "bwd"])
+def test_memory_of_a_call_on_another_stream(cuda_dev, name, keep):
+    """stream= with nothing given to write into.  The other stream is held back: what the
+    current one allocates after the call (the sizes of its outputs, dropped or not, and of its
+    scratch) is not what the call still uses.  Then the current stream is held back:
+    what it has yet to read is not what the call writes into, though it has been given back."""
+    call, scratch = _side_calls(cuda_dev)[name]
+    many = lambda x: [t for t in (x if isinstance(x, (tuple, list)) else [x]) if t is not None]  # noqa: E731
+    want = [t.clone() for t in many(call(None))]
+    sizes = [t.numel() * t.element_size() for t in want] + [max(256, scratch)] * 2
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+        got = many(call(s))
+        if not keep:
+            got = None
+        after = [torch.full((n,), 0xA5, dtype=torch.uint8, device=cuda_dev) for n in sizes]
+        torch.cuda.synchronize()
+        assert all((t == 0xA5).all() for t in after)
+        assert not keep or all(torch.equal(a, b) for a, b in zip(got, want))
+        del after, got
+        torch.cuda.synchronize()
+        before = [torch.full((n,), i + 1, dtype=torch.uint8, device=cuda_dev) for i, n in enumerate(sizes)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        late = [t.clone() for t in before]
+        del before
+        got = many(call(s))
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        torch.cuda.synchronize()
+        assert all((t == i + 1).all() for i, t in enumerate(late))
