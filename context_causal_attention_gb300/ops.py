@@ -501,7 +501,7 @@ def _qk(q, k):
 
 
 def _check_pos(pos, C, s):
-    if pos.dtype != torch.int32 or pos.numel() != C * s or not pos.is_contiguous():
+    if pos is not None and (pos.dtype != torch.int32 or pos.numel() != C * s or not pos.is_contiguous()):
         raise ValueError("pos must be contiguous int32 [C, s]")
 
 
@@ -529,9 +529,9 @@ def _rope_call(name, q, k, pos, rope, q_out, k_out, stream):
     C, B, s, N, Nkv, D, qs, ks = _qk(q, k)
     _check_pos(pos, C, s)
     q_out, k_out = _row_out(q_out, q, stream), _row_out(k_out, k, stream)
-    dev = _here(q, k, pos, rope.freqs, q_out, k_out)
+    dev = _here(q, k, pos, None if rope is None else rope.freqs, q_out, k_out)
     st = getattr(_lib.lib(), name)(_addr(q), _addr(k), _addr(pos), C, B, s, N, Nkv, D, qs, ks, _dtype_code(q),
-                                   rope._ref, _addr(q_out), _addr(k_out), _raw_stream(stream, dev))
+                                   None if rope is None else rope._ref, _addr(q_out), _addr(k_out), _raw_stream(stream, dev))
     _lib.check(name, st)
     return q_out, k_out
 
@@ -680,8 +680,10 @@ def cp_prefix_attn_fwd(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_
     if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be contiguous bf16 [R, N, D]")
     R, N = q.shape[0], q.shape[1]
-    if prefix_len and (prefix_pages.dtype != torch.int32 or not prefix_pages.is_contiguous() or
-                       prefix_pages.numel() * page < prefix_len):
+    # (a list that is missing is the library's to refuse)
+    if prefix_len and prefix_pages is not None and (prefix_pages.dtype != torch.int32 or
+                                                    not prefix_pages.is_contiguous() or
+                                                    prefix_pages.numel() * page < prefix_len):
         raise ValueError("prefix_pages must be contiguous int32 and cover prefix_len tokens")
     if scale is None:
         scale = 1.0 / math.sqrt(D)

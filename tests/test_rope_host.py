@@ -260,3 +260,24 @@ def test_prefix_binding_refusals(cplib):
     for kw in (dict(table=table.long()), dict(k_cache=kc.float(), v_cache=kc.float())):
         with pytest.raises(TypeError):
             F.cp_prefix_attn_fwd(**dict(ok, **kw))
+
+
+def test_missing_lists_get_the_librarys_error(cplib, monkeypatch):
+    """What is left out where it is needed reaches the library, which refuses it (on
+    the host, before anything is launched)."""
+    monkeypatch.setattr(F, "_here", lambda *ts: 0)
+    monkeypatch.setattr(F, "_raw_stream", lambda stream, dev: None)
+    bf, i32 = torch.bfloat16, torch.int32
+    kc = torch.zeros(4, 16, 2, 64, dtype=bf)
+    q, table = torch.zeros(3, 8, 64, dtype=bf), torch.zeros(1, 2, dtype=i32)
+    cu, ln = torch.tensor([0, 3], dtype=i32), torch.tensor([3], dtype=i32)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    rope, pos, w = F.cp_rope_freqs(64, device="cpu"), torch.zeros(3, dtype=i32), torch.ones(64)
+    for call in (lambda: F.cp_prefix_attn_fwd(q, kc, kc.clone(), None, 20, table, cu, ln, 3, workspace=ws),
+                 lambda: F.cp_rope_fwd(q, None, None, rope), lambda: F.cp_rope_bwd(q, None, pos, None),
+                 lambda: F.cp_qk_norm_rope_fwd(q, None, w, None, None, rope),
+                 lambda: F.cp_qk_norm_rope_fwd(q, q, w, None, pos, rope),
+                 lambda: F.cp_qk_norm_rope_bwd(q, None, q, None, w, None, None, rope, workspace=ws)):
+        with pytest.raises(F.CpError) as e:
+            call()
+        assert e.value.status == 1
