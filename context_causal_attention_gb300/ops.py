@@ -416,11 +416,19 @@ def cp_ring_attention_fwd_noalloc(q_sh, k_sh, v_sh, pos, o, lse, scale=None, lay
 class CpRope:
     """A rotation (cp_rope of the C header): frequencies on the device, rotated
     part, order of the pairs, amplitude.  Made by cp_rope_freqs or
-    cp_rope_phases and kept by the caller."""
+    cp_rope_phases and kept by the caller; another rotation is another object."""
 
     def __init__(self, freqs, rot_dim, order, amplitude):
-        self.freqs, self.rot_dim, self.order, self.amplitude = freqs, rot_dim, order, amplitude
+        if freqs.dtype != torch.int64 or not freqs.is_contiguous() or 2 * freqs.numel() < rot_dim:
+            raise ValueError("freqs must be contiguous int64 [rot_dim / 2]")
+        self._freqs, self._rest = freqs, (rot_dim, order, amplitude)
         self._ref = ctypes.byref(RopeStruct(freqs.data_ptr(), rot_dim, order, amplitude))
+
+    # read only: calls use the struct above
+    freqs = property(lambda self: self._freqs)
+    rot_dim = property(lambda self: self._rest[0])
+    order = property(lambda self: self._rest[1])
+    amplitude = property(lambda self: self._rest[2])
 
 
 def cp_rope_freqs(rot_dim, base=10000.0, scaling=CP_ROPE_PLAIN, factor=1.0, original_len=0, order=CP_ROPE_HALF,

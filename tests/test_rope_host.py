@@ -50,6 +50,21 @@ def test_frequency_refusals(cplib):
     assert cplib.cp_rope_phases(None, 1, f.ctypes.data) == 1
 
 
+def test_a_rotation_stays_with_its_frequencies(cplib):
+    """A list shorter than the rotated part is refused (the kernels read rot_dim / 2 entries),
+    and what calls would not follow cannot be set."""
+    f = torch.zeros(16, dtype=torch.int64)
+    assert F.CpRope(f, 32, 0, 1.0).freqs is f and F.CpRope(f, 16, 1, 0.5).rot_dim == 16
+    for bad, rot in ((f, 34), (f, 128), (f.int(), 32), (f.double(), 32), (torch.zeros(32, dtype=torch.int64)[::2], 32)):
+        with pytest.raises(ValueError):
+            F.CpRope(bad, rot, 0, 1.0)
+    r = F.cp_rope_freqs(64, device="cpu")
+    for name, value in (("freqs", f), ("rot_dim", 16), ("order", 1), ("amplitude", 2.0)):
+        with pytest.raises(AttributeError):
+            setattr(r, name, value)
+    assert (r.rot_dim, r.order, r.amplitude) == (64, F.CP_ROPE_HALF, 1.0)
+
+
 def spec(freqs=FAKE, rot=64, order=0, amp=1.0):
     return ctypes.byref(_lib.RopeStruct(freqs, rot, order, amp))
 
