@@ -160,7 +160,7 @@ __device__ __forceinline__ void tc_init(uint8_t *smem, const CUtensorMap &tmK, c
         mbar_init(turn + i, 4);
     }
     mbar_init(ml_full, 4);
-    mbar_init(q_empty, 2);
+    mbar_init(q_empty, 2);  // the MMA warps, each when it has seen that its half's products with Q are done
     for (int s = 0; s < C::kStagesK; ++s) {
         mbar_init(k_full + s, tma ? 1 : 32);
         mbar_init(k_empty + s, 2);
@@ -339,18 +339,19 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                     commit(s_full + i, lead);
                     commit(k_empty + st, lead);
                     if (paired) commit(k_empty + st, lead);  // for the other half
-                    if (j + step >= n) commit(q_empty, lead);
                 }
+                // Q has been read when the last scores are there.  (The weights that this warp
+                // waits for next come after them, so the wait costs nothing.)
+                if (!ok || !mbar_wait_warp(s_full + i, tiles & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
+                if (lane == 0) mbar_arrive(q_empty);
                 const int last = begin + (n - 1 - begin) / step * step;
-                if (!ok || !v_wait(base + last)) { ok = false; break; }
+                if (!v_wait(base + last)) { ok = false; break; }
                 fence_async_shared();
                 if (!pv(base + last, last == begin)) { ok = false; break; }
                 commit(o_full + i, lead);
                 ++items;
             } else if (lane == 0) {
-                // It multiplied nothing here and has nothing to wait for.  (With a commit in
-                // this place, none of the warp's own products on the way, the loader was seen to
-                // bring the next queries before the other half had read these.)
+                // it multiplied nothing here and has nothing to wait for
                 mbar_arrive(q_empty);
             }
         }
