@@ -186,3 +186,52 @@ def test_append_in_a_graph_reads_new_lengths(cuda_dev):
     for s, (rv, rk) in want.items():
         assert torch.equal(fv[s], rv)
         within(fk[s], rk, "bf16", 8 * R.U32 * 10, "keys")
+
+
+LONG = {
+    # new tokens (empty sequences among them, beginnings and the padding's inside units of several tokens), what
+    # was there before, heads of q and of k, D, page, padding
+    "units_of_2": ([700, 0, 1, 0, 999, 3, 0, 820], 5, 3, 2, 64, 16, 7),
+    "units_of_10": ([4096, 1, 0, 4095, 33, 4000, 0, 0, 2, 4001, 4096, 3053], 90, 2, 1, 128, 32, 1),
+    "units_of_10_keys_alone": ([4096, 1, 0, 4095, 33, 4000, 0, 0, 2, 4001, 4096, 3053], 0, 0, 3, 64, 128, 3),
+    "units_of_32": ([30001, 0, 0, 31, 1, 49000, 97, 2000], 3, 1, 1, 64, 256, 19),
+    # more units than all warps take at once
+    "units_of_32_in_rounds": ([60001, 7, 0, 70000, 32, 31, 33, 30011], 0, 1, 1, 64, 64, 5),
+}
+
+
+@pytest.mark.parametrize("name", sorted(LONG))
+@pytest.mark.parametrize("dt,order,norm", [("bf16", "half", True), ("fp32", "interleaved", False)])
+def test_append_of_many_tokens(cuda_dev, name, dt, order, norm):
+    """Prompts so long that a warp takes several tokens: every key, value and query against
+    64 bits, the slots that got no token and the padding as they were."""
+    new, before, N, Nkv, D, page, pad = LONG[name]
+    g = torch.Generator().manual_seed(len(name))
+    b = Batch(g, new, [n + (before if i % 3 else 0) for i, n in enumerate(new)], page)
+    rows, base = sum(new), 1234567
+    rope, th, amp = rope_of(D, order, "by_parts")
+    x = rand(g, (rows + pad, N + 2 * Nkv, D), dt, 2.0)
+    wq, wk = [1 + 0.3 * torch.randn(D, generator=g) for _ in range(2)]
+    d = x.to(cuda_dev)
+    kc, vc = (torch.full((b.total, page, Nkv, D), 9.0, dtype=torch.bfloat16, device=cuda_dev) for _ in range(2))
+    qo = torch.full((rows + pad, N, D), 7.0, dtype=torch.bfloat16, device=cuda_dev) if N else None
+    w = dict(wq=wq.to(cuda_dev) if N else None, wk=wk.to(cuda_dev)) if norm else {}
+    F.cp_cache_append(d[:, N:N + Nkv], d[:, N + Nkv:], kc, vc, b.table.to(cuda_dev), b.cu.to(cuda_dev),
+                      b.kv_len.to(cuda_dev), rope=rope, q=d[:, :N] if N else None, q_out=qo, eps=1e-5, pos_base=base, **w)
+    assert F.cp_device_status() == 0
+    at, pos = np.array(b.new_slots()), b.new_index() + base
+    rest = np.ones(b.total * page, bool)
+    rest[at] = False
+    keys, values = (c.view(-1, Nkv, D).cpu() for c in (kc, vc))
+    assert (keys[rest] == 9).all() and (values[rest] == 9).all()
+    assert torch.equal(values[at], x[:rows, N + Nkv:].to(torch.bfloat16))
+
+    def check(got, cut, w, what):
+        y = f64(x[:rows, cut])
+        y = R.norm(y, f64(w), 1e-5) if norm else y
+        within(got, R.turn(y, pos, th, amp, order), "bf16", 24 * R.U32 * amp * R.pair_size(y, th, order), what)
+
+    check(keys[at], slice(N, N + Nkv), wk, "keys")
+    if N:
+        check(qo[:rows], slice(0, N), wq, "queries")
+        assert (qo[rows:] == 7).all()

@@ -280,3 +280,57 @@ def test_outputs_stay_in_bounds(cuda_dev):
     F.cp_qk_norm_rope_bwd(q, None, q, None, w, None, pos, rope, dq=big[1:78], dwq=dw[16:80], workspace=ws[256:256 + need])
     assert (big[0] == 7).all() and (big[78] == 7).all() and (dw[:16] == 7).all() and (dw[80:] == 7).all()
     assert (ws[:256] == 0xA5).all() and (ws[256 + need:] == 0xA5).all()
+
+
+# more units than all resident warps take at once (608 blocks of 8 warps forward, 304 backward), in odd
+# numbers; several heads to a lane's walk; B > 1, where positions repeat; one tensor alone
+MANY = [(2, 3, 1667, 5, 2, 64, 64), (1, 1, 9001, 20, 3, 64, 32), (3, 1, 2111, 9, 1, 128, 128), (1, 2, 5003, 3, 0, 128, 64),
+        (1, 1, 4999, 33, 7, 128, 96)]
+
+
+@pytest.mark.parametrize("shape", MANY)
+@pytest.mark.parametrize("dt,order", [("bf16", "half"), ("bf16", "interleaved"), ("fp32", "half"), ("fp32", "interleaved")])
+def test_many_rows(cuda_dev, shape, dt, order):
+    """Rotation and norm, both directions, where a warp goes from token to token: every
+    value against 64 bits, and the same bits on another stream.  dw: a thread adds the rows
+    of its own tokens one after the other, then 3 shuffles, 8 warps, at most 10 blocks a warp and 5
+    shuffles follow: (rows of a thread + 26) u of sum |g xh| in the place of all rows, and the
+    40 u of the terms."""
+    C, B, s, N, Nkv, D, rot = shape
+    g = torch.Generator().manual_seed(s)
+    rope, th, amp = rope_of(rot, order, "by_parts")
+    pos = torch.randint(-9, 1 << 20, (C, s), generator=g, dtype=torch.int32)
+    p, eps, u = pos.numpy()[:, None].repeat(B, 1), 1e-5, R.U32
+    heads = [h for h in (N, Nkv) if h]
+    pad = [None] * (2 - len(heads))
+    xs, gs = ([rand(g, (C, B, s, h, D), dt, x) for h in heads] for x in (3.0, 1.0))
+    ws = [1 + 0.3 * torch.randn(D, generator=g) for _ in heads]
+    xd, gd, wd = ([t.to(cuda_dev) for t in l] + pad for l in (xs, gs, ws))
+    pd = pos.to(cuda_dev)
+
+    def calls():
+        return [F.cp_rope_fwd(*xd, pd, rope), F.cp_rope_bwd(*gd, pd, rope),
+                F.cp_qk_norm_rope_fwd(*xd, *wd, pd, rope, eps=eps), F.cp_qk_norm_rope_bwd(*gd, *xd, *wd, pd, rope, eps=eps)]
+
+    fwd, bwd, nf, nb = got = calls()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = calls()
+    side.synchronize()
+    assert all(a is b or torch.equal(a, b) for x, y in zip(got, again) for a, b in zip(x, y))
+    for t, h in enumerate(heads):
+        x, gr, w = f64(xs[t]), f64(gs[t]), f64(ws[t])
+        what = "qk"[t]
+        within(fwd[t], R.turn(x, p, th, amp, order), dt, 8 * u * amp * R.pair_size(x, th, order), what + " rotated")
+        back, pair = R.turn(gr, p, th, amp, order, True), amp * R.pair_size(gr, th, order)
+        within(bwd[t], back, dt, 8 * u * pair, what + " rotated back")
+        y = R.norm(x, w, eps)
+        within(nf[t], R.turn(y, p, th, amp, order), dt, 24 * u * amp * R.pair_size(y, th, order), what + " normed")
+        dx, dw = R.norm_bwd(x, w, back, eps)
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+        xh, size = np.abs(x * r), np.abs(w) * pair
+        within(nb[t], dx, dt, 48 * u * r * (size + xh * (size * xh).mean(-1, keepdims=True)), what + " norm gradient")
+        blocks = 304 * h // (N + Nkv) - 1  # at least
+        mine = -(-C * B * s // (8 * blocks)) * -(-h // (512 // D))
+        within(nb[2 + t], dw, "fp32", (mine + 66) * u * (pair * xh).reshape(-1, D).sum(0), what + " weight gradient")
