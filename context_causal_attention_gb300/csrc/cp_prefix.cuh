@@ -335,8 +335,8 @@ struct Walk {
         const long long n1 = min(s.n0 + left, p.key_tiles);
         const long long need = (static_cast<long long>(row_limit(a, x, min(x.row0 + TM, x.rows) - 1)) + KT - 1) / KT;
         // the part [n0, n1) of the nominal length, scaled to the tiles that the rows need
-        x.k0 = static_cast<int>(s.n0 == 0 || need == p.key_tiles ? min(s.n0, need) : s.n0 * need / p.key_tiles);
-        x.k1 = static_cast<int>(n1 == p.key_tiles || need == p.key_tiles ? min(n1, need) : n1 * need / p.key_tiles);
+        x.k0 = static_cast<int>(s.n0 == 0 ? 0 : s.n0 * need / p.key_tiles);
+        x.k1 = static_cast<int>(n1 == p.key_tiles ? need : n1 * need / p.key_tiles);
         left -= n1 - s.n0;
         s.n0 = 0;
         ++s.item;

@@ -15,9 +15,11 @@
 //
 // Work split.  Few rows and many keys: the parallelism is in the keys.  All
 // (problem, KV head, row tile) items are laid end to end, each as long as its
-// 64-key tiles, and every block takes an equal share of that line, whatever the
-// lengths are.  A share that covers part of an item leaves a partial; the k-th
-// piece of the line has slot (item + block), which is unique, so the slots need
+// key tiles and kExtra more (cp_prefix.cuh), and every block takes an equal share of
+// that line, whatever the lengths are.  Where a call has both kinds of tiles there are
+// two lines, and the blocks are divided between them by their estimated cycles
+// (prefix_workers).  A share that covers part of an item leaves a partial; the
+// k-th piece of a line has slot (item + block), which is unique, so the slots need
 // no counter.  A second launch joins the pieces of every row in their order:
 // the result does not depend on timing.
 //
