@@ -502,12 +502,14 @@ extern "C" cp_status cp_rope_phases(const double *inv_freq, int64_t n, uint64_t 
     for (int64_t i = 0; i < n; ++i)
         if (!(std::isfinite(inv_freq[i]) && std::fabs(inv_freq[i]) <= 6.2831853071795864769)) return CP_ERR_ARGUMENT;
     for (int64_t i = 0; i < n; ++i) {
-        // turns per position, then its fraction in units of 2^-64 (a double holds 53 bits of it)
-        double t = inv_freq[i] / 6.2831853071795864769;
+        // turns per position, then its fraction in units of 2^-64 (a double holds 53 bits of
+        // it, those of a negative frequency before its complement is taken)
+        double t = std::fabs(inv_freq[i]) / 6.2831853071795864769;
         t -= std::floor(t);
         const double hi = std::floor(t * 4294967296.0);  // top 32 bits, exact
         const double lo = (t * 4294967296.0 - hi) * 4294967296.0;
-        freqs[i] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(std::llrint(lo));
+        const uint64_t f = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(std::llrint(lo));
+        freqs[i] = inv_freq[i] < 0.0 ? 0 - f : f;
     }
     return CP_OK;
 }

@@ -437,7 +437,9 @@ cp_status cp_ring_attention_bwd(const void *q_sh, const void *k_sh, const void *
  *   freqs     : device uint64 [rot_dim/2], turns per position in 64-bit fixed
  *               point, theta_i / (2 pi) * 2^64 modulo 2^64 (cp_rope_freqs, cp_rope_phases,
  *               copied to the device by the caller and kept as long as calls use
- *               it); positions of any size lose no precision
+ *               it).  The fraction of a turn of pos * freqs[i] is formed exactly at any
+ *               position; freqs[i] comes from an fp64 quotient, so the angle is off by
+ *               at most |pos| (theta_i 2^-52 + 2^-62) radians (under 3e-7 measured at 2^31)
  *   order     : CP_ROPE_HALF pairs value i with value i + rot_dim/2,
  *               CP_ROPE_INTERLEAVED pairs 2i with 2i + 1
  *   rot_dim   : even, 2 .. D; a multiple of 16 for CP_ROPE_HALF

@@ -1,6 +1,7 @@
 """Frequencies, and what the rotation, norm and append calls refuse on the host
 before anything is launched (no GPU needed)."""
 import ctypes
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -30,6 +31,18 @@ def test_phases_keep_the_fraction_of_a_turn(cplib):
     assert r.rot_dim == 8
     got = r.freqs.numpy().view(np.uint64)
     assert got.tolist() == [0, 1 << 63, 3 << 62, 0]
+
+
+def test_phases_are_as_near_as_stated(cplib):
+    """The stored turns against the given frequencies in exact fractions: within theta 2^-52 + 2^-62
+    radians a position, modulo a turn (pi to 60 digits)."""
+    turn = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494")
+    w = [10000.0 ** (-i / 64) for i in range(64)] + [6.283185307179586, -6.283185307179586, 3.0, -0.1, 1e-12, -1e-300]
+    got = F.cp_rope_phases(w, device="cpu").freqs.numpy().view(np.uint64)
+    for x, f in zip(w, got):
+        off = (Fraction(int(f), 1 << 64) * turn - Fraction(x)) % turn
+        off = min(off, turn - off)
+        assert off <= abs(Fraction(x)) / 2 ** 52 + Fraction(1, 1 << 62), x
 
 
 def test_frequency_refusals(cplib):
