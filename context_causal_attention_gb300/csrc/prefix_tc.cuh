@@ -263,8 +263,9 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
             }
         }
         copies_drain();
-        if (!ok && tma && lane == 0) {
-            // let every copy already issued land before shared memory goes away
+        if (tma && lane == 0) {
+            // Every copy already issued lands before shared memory goes away, also where this
+            // warp has issued all of its own and a wait of another warp ends the block.
             volatile int no_abort = 0;
             for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
                 mbar_wait(full + i % stages, (i / stages) & 1u, &no_abort, 100000000ull);
