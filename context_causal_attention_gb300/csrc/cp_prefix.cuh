@@ -24,6 +24,7 @@
 
 #include <cstdint>
 
+#include "cp_hold.cuh"
 #include "cp_paged.cuh"
 #include "cp_ptx.cuh"
 #include "cp_sched.cuh"
@@ -54,6 +55,7 @@ struct PrefixArgs {
     float cost;                 // cycles of a tile, where both kinds of tiles share a launch
     int *status;
     unsigned long long timeout_ns;
+    const int *hold;  // self-test: the loads wait for this word (null: they do not)
     // what the launch leaves for the join
     long long *head;      // [0]: tiles of a share
     long long *base_tile; // [B] first tile of each sequence
@@ -67,6 +69,11 @@ __device__ __forceinline__ void report(int *status, cp_status code) { atomicExch
 
 // The lists, tables and queries are read past L1 (__ldcg): a launch's blocks may
 // have started while the kernel that writes them was still running.
+
+// The self-test's wait, by one whole warp: true at once without one.
+__device__ __forceinline__ bool released(const PrefixArgs &a, volatile int *abort_flag) {
+    return !a.hold || __all_sync(0xffffffffu, hold_wait(a.hold, a.timeout_ns, abort_flag));
+}
 
 // One problem's shape.
 struct Problem {

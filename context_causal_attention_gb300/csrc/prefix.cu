@@ -58,6 +58,7 @@ namespace cpattn {
 namespace {
 
 __device__ int g_prefix_status = 0;
+__device__ int g_prefix_hold = 0;  // never set
 
 // A problem whose rows for one KV head are more than this runs in tiles of 256
 // rows on the tensor memory, else in tiles of 16.  A second 16-row tile reads
@@ -180,7 +181,7 @@ __device__ __forceinline__ void mma_work(const PrefixArgs &a, uint8_t *smem) {
         const int shift = a.own.shift, part = (warp >> 1) * kPart;
         const uint32_t ring = smem_u32(smem) + is_v * C::kTile + part * 128;
         uint32_t it = 0;
-        bool ok = true;
+        bool ok = warp != 0 || released(a, abort_flag);
         while (ok && walk.next(a, line)) {
             if (x.k0 >= x.k1) continue;
             PageWindow win;
@@ -878,12 +879,13 @@ extern "C" cp_status cp_prefix_attn_workspace_size(int64_t R, int64_t B, int64_t
     return CP_OK;
 }
 
-extern "C" cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, const void *v_cache, int64_t n_pages,
-                                        int64_t page_size, const int32_t *prefix_pages, int64_t prefix_len,
-                                        const int32_t *table, int64_t B, int64_t max_pages, const int32_t *cu_new,
-                                        const int32_t *kv_len, int64_t max_new, int64_t R, int64_t N, int64_t Nkv,
-                                        int64_t D, float scale, void *o, cp_dtype o_dtype, float *lse,
-                                        void *workspace, size_t ws_bytes, cudaStream_t stream) {
+namespace {
+// cp_prefix_attn_fwd, with the limit of its waits; stalled: its loads wait for a word that nothing sets.
+cp_status prefix_call(const void *q, const void *k_cache, const void *v_cache, int64_t n_pages, int64_t page_size,
+                      const int32_t *prefix_pages, int64_t prefix_len, const int32_t *table, int64_t B,
+                      int64_t max_pages, const int32_t *cu_new, const int32_t *kv_len, int64_t max_new, int64_t R,
+                      int64_t N, int64_t Nkv, int64_t D, float scale, void *o, cp_dtype o_dtype, float *lse,
+                      void *workspace, size_t ws_bytes, uint64_t timeout_ns, bool stalled, cudaStream_t stream) {
     if (!q || !k_cache || !v_cache || !table || !cu_new || !kv_len || !o || !lse || (prefix_len > 0 && !prefix_pages))
         return CP_ERR_NULL;
     cp_status st = check_sizes(R, B, max_new, prefix_len, N, Nkv, D, page_size, max_pages);
@@ -901,7 +903,12 @@ extern "C" cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, cons
     if (s.slots[0] * s.lanes > INT32_MAX || s.slots[1] * s.lanes > INT32_MAX) return CP_ERR_SHAPE;
     PrefixArgs a{};
     if ((st = status_word(&a.status)) != CP_OK) return st;
-    a.timeout_ns = 2000000000ull;
+    a.timeout_ns = timeout_ns;
+    if (stalled) {
+        void *hold = nullptr;
+        if ((st = cuda_status(cudaGetSymbolAddress(&hold, g_prefix_hold))) != CP_OK) return st;
+        a.hold = static_cast<const int *>(hold);
+    }
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.k = static_cast<const __nv_bfloat16 *>(k_cache);
     a.v = static_cast<const __nv_bfloat16 *>(v_cache);
@@ -937,4 +944,28 @@ extern "C" cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, cons
     j.lse = lse;
     uint8_t *w = static_cast<uint8_t *>(workspace);
     return D == 128 ? launch_call<128>(a, s, w, j, stream) : launch_call<64>(a, s, w, j, stream);
+}
+}  // namespace
+
+extern "C" cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, const void *v_cache, int64_t n_pages,
+                                        int64_t page_size, const int32_t *prefix_pages, int64_t prefix_len,
+                                        const int32_t *table, int64_t B, int64_t max_pages, const int32_t *cu_new,
+                                        const int32_t *kv_len, int64_t max_new, int64_t R, int64_t N, int64_t Nkv,
+                                        int64_t D, float scale, void *o, cp_dtype o_dtype, float *lse,
+                                        void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    return prefix_call(q, k_cache, v_cache, n_pages, page_size, prefix_pages, prefix_len, table, B, max_pages, cu_new,
+                       kv_len, max_new, R, N, Nkv, D, scale, o, o_dtype, lse, workspace, ws_bytes, 2000000000ull, false,
+                       stream);
+}
+
+extern "C" cp_status cp_selftest_stalled_prefix_attn(
+    const void *q, const void *k_cache, const void *v_cache, int64_t n_pages, int64_t page_size,
+    const int32_t *prefix_pages, int64_t prefix_len, const int32_t *table, int64_t B, int64_t max_pages,
+    const int32_t *cu_new, const int32_t *kv_len, int64_t max_new, int64_t R, int64_t N, int64_t Nkv, int64_t D,
+    float scale, void *o, cp_dtype o_dtype, float *lse, void *workspace, size_t ws_bytes, uint64_t timeout_ns,
+    cudaStream_t stream) {
+    if (timeout_ns < 1000000ull || timeout_ns > 2000000000ull) return CP_ERR_ARGUMENT;
+    return prefix_call(q, k_cache, v_cache, n_pages, page_size, prefix_pages, prefix_len, table, B, max_pages, cu_new,
+                       kv_len, max_new, R, N, Nkv, D, scale, o, o_dtype, lse, workspace, ws_bytes, timeout_ns, true,
+                       stream);
 }

@@ -217,7 +217,7 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
         uint32_t st = 0, ph = 0;  // stage and phase of tile `it`
         const int shift = a.own.shift, rows = min(kTcKT, 1 << shift);  // rows of a copy
         uint32_t it = 0, items = 0;
-        bool ok = true;
+        bool ok = warp != 0 || released(a, abort_flag);
         while (ok && walk.next(a, line)) {
             if (x.k0 >= x.k1) continue;
             if (warp == 2) {

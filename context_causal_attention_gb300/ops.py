@@ -679,11 +679,8 @@ def cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page_siz
     return n.value
 
 
-def cp_prefix_attn_fwd(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale=None,
-                       o_dtype=CP_BF16, o=None, lse=None, workspace=None, stream=None):
-    """Attention of the new tokens q bf16 [R,N,D] over the shared prefix and their own sequences'
-    pages -> (o [R,N,D], lse fp32 [N,R]); see the C header.  max_new: the
-    largest number of new tokens of a sequence (chooses the tiles only)."""
+def _prefix_call(name, more, q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale,
+                 o_dtype, o, lse, workspace, stream):
     n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
     if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be contiguous bf16 [R, N, D]")
@@ -707,12 +704,29 @@ def cp_prefix_attn_fwd(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_
         workspace = _scratch(max(256, cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page,
                                                                     max_pages)), q.device, stream)
     dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, o, lse, workspace)
-    st = _lib.lib().cp_prefix_attn_fwd(_addr(q), _addr(k_cache), _addr(v_cache), n_pages, page, _addr(prefix_pages),
-                                       prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), max_new,
-                                       R, N, Nkv, D, scale, _addr(o), _dtype_code(o), _addr(lse), _addr(workspace),
-                                       workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
-    _lib.check("cp_prefix_attn_fwd", st)
+    st = getattr(_lib.lib(), name)(_addr(q), _addr(k_cache), _addr(v_cache), n_pages, page, _addr(prefix_pages),
+                                   prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), max_new, R, N,
+                                   Nkv, D, scale, _addr(o), _dtype_code(o), _addr(lse), _addr(workspace),
+                                   workspace.numel() * workspace.element_size(), *more, _raw_stream(stream, dev))
+    _lib.check(name, st)
     return o, lse
+
+
+def cp_prefix_attn_fwd(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale=None,
+                       o_dtype=CP_BF16, o=None, lse=None, workspace=None, stream=None):
+    """Attention of the new tokens q bf16 [R,N,D] over the shared prefix and their own sequences'
+    pages -> (o [R,N,D], lse fp32 [N,R]); see the C header.  max_new: the
+    largest number of new tokens of a sequence (chooses the tiles only)."""
+    return _prefix_call("cp_prefix_attn_fwd", (), q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len,
+                        max_new, scale, o_dtype, o, lse, workspace, stream)
+
+
+def cp_selftest_stalled_prefix_attn(timeout_ns, q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len,
+                                    max_new, workspace=None, stream=None):
+    """The self-test of the shared-prefix attention's bounded waits: a call whose loads are held on a word
+    that nothing sets (see the C header); read the outcome with cp_device_status."""
+    _prefix_call("cp_selftest_stalled_prefix_attn", (int(timeout_ns),), q, k_cache, v_cache, prefix_pages, prefix_len,
+                 table, cu_new, kv_len, max_new, None, CP_BF16, None, None, workspace, stream)
 
 
 def cp_selftest_stalled_producer(q, k, v, pos, o, lse, timeout_ns, stream=None):

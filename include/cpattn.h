@@ -650,6 +650,21 @@ cp_status cp_selftest_stalled_kernel(int kernel, void *scratch, size_t scratch_b
                                      cudaStream_t stream);
 
 /*
+ * cp_selftest_stalled_prefix_attn -- the same self-test of the shared-prefix attention:
+ * the arguments of cp_prefix_attn_fwd, which choose the kernels as they do there, with
+ * every block's first loads held on a word that nothing sets and every
+ * bounded wait limited to timeout_ns (1 ms .. 2 s, else CP_ERR_ARGUMENT).  The
+ * blocks give up, unwind and record CP_ERR_DEVICE_TIMEOUT; o and lse are
+ * unspecified.
+ */
+cp_status cp_selftest_stalled_prefix_attn(const void *q, const void *k_cache, const void *v_cache, int64_t n_pages,
+                                          int64_t page_size, const int32_t *prefix_pages, int64_t prefix_len,
+                                          const int32_t *table, int64_t B, int64_t max_pages, const int32_t *cu_new,
+                                          const int32_t *kv_len, int64_t max_new, int64_t R, int64_t N, int64_t Nkv,
+                                          int64_t D, float scale, void *o, cp_dtype o_dtype, float *lse,
+                                          void *workspace, size_t ws_bytes, uint64_t timeout_ns, cudaStream_t stream);
+
+/*
  * cp_ring_attention_fwd_noalloc -- cp_ring_attention_fwd for callers that
  * cannot allocate device memory.  The source pages have no counterpart: this
  * entry point exists for callers that may not call cudaMalloc or cannot hand

@@ -82,3 +82,31 @@ def test_every_kernel_gives_up_a_stalled_wait(cuda_dev, kernel):
             for got, r in zip((dq, dk, dv), ref):
                 assert np.max(np.abs(f(got) - r)) <= 1e-2 * np.max(np.abs(r))
     assert F.cp_device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form", ["narrow", "wide_tma", "wide_small_pages", "both_tma", "both_small_pages"])
+def test_prefix_attention_gives_up_a_stalled_wait(cuda_dev, form, D):
+    """Every kernel of the shared-prefix attention, its loads held on a word that nothing sets: it
+    gives up after 10 ms, the status word says so, nothing outside the workspace is written,
+    and the same call computes correctly afterwards, in the workspace that was left."""
+    from test_gpu_prefix import Call
+    new, length, prefix, page = {
+        "narrow": ([1], [300], 1000, 16), "wide_tma": ([40, 9], [300, 900], 500, 64),
+        "wide_small_pages": ([40, 9], [300, 900], 500, 16), "both_tma": ([1] * 20, [90 + 9 * i for i in range(20)], 1000, 64),
+        "both_small_pages": ([1] * 20, [90 + 9 * i for i in range(20)], 1000, 32)}[form]
+    c = Call(21, new, length, prefix, 8, 2, D, page)
+    o, lse = c.run(cuda_dev)
+    c.check(o, lse)
+    assert F.cp_device_status() == 0
+    q, k, v, pages, table, cu, kv_len = c.dev
+    need = F.cp_prefix_attn_workspace_size(c.R, len(new), max(new), prefix, 8, 2, D, page, table.shape[1])
+    ws = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device=cuda_dev)
+    lists = (q, k, v, pages, prefix, table, cu, kv_len, max(new))
+    F.cp_selftest_stalled_prefix_attn(10_000_000, *lists, workspace=ws[256:256 + need])
+    assert F.cp_device_status() == CP_ERR_DEVICE_TIMEOUT
+    assert F.cp_device_status() == 0
+    o2, lse2 = F.cp_prefix_attn_fwd(*lists, workspace=ws[256:256 + need])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert (ws[:256] == 0xA5).all() and (ws[256 + need:] == 0xA5).all()
+    assert F.cp_device_status() == 0

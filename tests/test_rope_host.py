@@ -273,6 +273,16 @@ def test_prefix_attention_refusals(cplib):
     assert call(D=96) == 7 and call(page=48) == 7
 
 
+def test_stalled_prefix_attention_checks_as_the_call_does(cplib):
+    def call(q=FAR[0], ns=10_000_000, nb=1 << 40, ws=FAR[4]):
+        return cplib.cp_selftest_stalled_prefix_attn(q, FAR[1], FAR[2], 10, 16, FAKE, 100, FAKE, 2, 4, FAKE, FAKE, 4, 8, 8,
+                                                     2, 64, 0.125, FAR[3], 0, FAKE, ws, nb, ns, None)
+
+    for ns in (0, 999_999, 2_000_000_001):
+        assert call(ns=ns) == 10, ns
+    assert call(q=None) == 1 and call(nb=1) == 6 and call(ws=None) == 6 and call(q=FAR[0] + 8) == 5
+
+
 def test_prefix_binding_refusals(cplib):
     bf, i32 = torch.bfloat16, torch.int32
     kc = torch.zeros(4, 16, 2, 64, dtype=bf)
