@@ -1124,13 +1124,14 @@ extern "C" cp_status cp_device_status(int *code, int clear, cudaStream_t stream)
         const int zero = 0;
         if (cudaMemcpyToSymbol(cpattn::g_cp_device_status, &zero, sizeof(int)) != cudaSuccess) return CP_ERR_CUDA;
     }
-    // the backward, tf32 and cache kernels keep their own words (other translation units)
+    // the backward, tf32 and cache kernels keep their own words (other translation units); the
+    // append's, which waits for nothing, comes last: a wait that ran out is not hidden by a bad list
     int vt = 0, vc = 0, vp = 0;
     cp_status st = cpattn::read_bwd_device_status(&vb, clear != 0);
     if (st == CP_OK) st = cpattn::read_tf32_device_status(&vt, clear != 0);
     if (st == CP_OK) st = cpattn::read_cache_device_status(&vc, clear != 0);
     if (st == CP_OK) st = cpattn::read_prefix_device_status(&vp, clear != 0);
     if (st != CP_OK) return st;
-    *code = v != 0 ? v : (vb != 0 ? vb : (vt != 0 ? vt : (vc != 0 ? vc : vp)));
+    *code = v != 0 ? v : (vb != 0 ? vb : (vt != 0 ? vt : (vp != 0 ? vp : vc)));
     return CP_OK;
 }

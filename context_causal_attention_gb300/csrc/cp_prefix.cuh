@@ -65,7 +65,13 @@ struct PrefixArgs {
     int slots;            // of a lane
 };
 
-__device__ __forceinline__ void report(int *status, cp_status code) { atomicExch(status, static_cast<int>(code)); }
+// A bad list never hides that a wait ran out.
+__device__ __forceinline__ void report(int *status, cp_status code) {
+    if (code == CP_ERR_DEVICE_TIMEOUT)
+        atomicExch(status, static_cast<int>(code));
+    else
+        atomicCAS(status, static_cast<int>(CP_OK), static_cast<int>(code));
+}
 
 // The lists, tables and queries are read past L1 (__ldcg): a launch's blocks may
 // have started while the kernel that writes them was still running.

@@ -709,7 +709,7 @@ cp_status cp_ring_attention_fwd_noalloc(const void *q_sh, const void *k_sh, cons
  * cp_device_status -- synchronise `stream`, then read (and, if clear != 0,
  * reset) the library's device status word on the current device.
  * *code receives CP_OK, CP_ERR_DEVICE_TIMEOUT if a kernel of this library
- * gave up a bounded wait since the last reset, or CP_ERR_PAGE if one met a page
+ * gave up a bounded wait since the last reset, or else CP_ERR_PAGE if one met a page
  * number, length or count out of range.  Host-blocking.
  */
 cp_status cp_device_status(int *code, int clear, cudaStream_t stream);

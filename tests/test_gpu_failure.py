@@ -110,3 +110,31 @@ def test_prefix_attention_gives_up_a_stalled_wait(cuda_dev, form, D):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     assert (ws[:256] == 0xA5).all() and (ws[256 + need:] == 0xA5).all()
     assert F.cp_device_status() == 0
+
+
+@pytest.mark.parametrize("order", ["wait_first", "list_first"])
+def test_a_bad_list_does_not_hide_a_wait_that_ran_out(cuda_dev, order):
+    """A stalled call and calls with a page number out of range (the append's and the
+    attention's), in either order: the status word is the wait's; without it, the list's."""
+    from test_gpu_prefix import Call
+    c = Call(22, [1, 1], [40, 70], 100, 4, 2, 64, 16)
+    c.run(cuda_dev)
+    q, k, v, pages, table, cu, kv_len = c.dev
+    bad = table.clone()
+    bad[:, :3] = c.b.total
+
+    def lists():
+        F.cp_cache_append(k[0, :2], v[0, :2], k.clone(), v.clone(), bad, cu, kv_len)
+        F.cp_prefix_attn_fwd(q, k, v, pages, 100, bad, cu, kv_len, 1)
+
+    def stall():
+        F.cp_selftest_stalled_prefix_attn(5_000_000, q, k, v, pages, 100, table, cu, kv_len, 1)
+
+    for call in (stall, lists) if order == "wait_first" else (lists, stall):
+        call()
+    assert F.cp_device_status(clear=False) == CP_ERR_DEVICE_TIMEOUT
+    assert F.cp_device_status() == CP_ERR_DEVICE_TIMEOUT
+    assert F.cp_device_status() == 0
+    lists()
+    assert F.cp_device_status() == 11
+    assert F.cp_device_status() == 0
