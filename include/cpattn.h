@@ -506,6 +506,8 @@ cp_status cp_rope_bwd(const void *dq_out, const void *dk_out, const int32_t *pos
  *   wq, wk  : device [D] of w_dtype, one weight vector for all heads of q (k)
  *   eps     : finite, >= 0
  *   rope    : NULL for the norm alone (pos is not read then)
+ * The mean square is formed in fp32: a row of values above 1.6e18 overflows it
+ * (its r is 0), and with eps = 0 a row below 1e-19 falls under it (its r is infinite).
  * Everything else as for cp_rope_fwd.
  */
 cp_status cp_qk_norm_rope_fwd(const void *q, const void *k, const void *wq, const void *wk, const int32_t *pos,
@@ -560,7 +562,7 @@ cp_status cp_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void
  *             with one another, is refused: CP_ERR_ARGUMENT)
  * The prefix itself is appended as a sequence with its own table.
  * page_size in {16, 32, 64, 128, 256} and D in {64, 128} (else
- * CP_ERR_UNSUPPORTED); B <= 4096; n_pages * page_size and max_pages *
+ * CP_ERR_UNSUPPORTED); R >= 1; B <= 4096; n_pages * page_size and max_pages *
  * page_size at most 2^31 - 256.  cu_new, kv_len and table are read on the device: a token
  * whose index or page number is out of range is skipped and the device status
  * word becomes CP_ERR_PAGE.
@@ -601,11 +603,11 @@ cp_status cp_cache_append(const void *q, const void *k, const void *v, int64_t q
  * a result whatever they hold; a NaN or infinity in a V row that some row sees
  * may reach other rows of its sequence.
  * D in {64, 128}, page_size in {16, 32, 64, 128, 256}; N % Nkv == 0; scale
- * finite and > 0; prefix_len at most 2^31 - 256.  Its launches overlap one another and the end of
- * the kernel before them on the stream, never one that the caller puts behind.
- * Make the first call of a process outside a stream capture.  The lists are read on the device: a page number, length or
- * count out of range sets the device status word to CP_ERR_PAGE, is never
- * followed, and leaves its rows' results unspecified.
+ * finite and > 0; prefix_len at most 2^31 - 256; R >= 1 (a step without new tokens
+ * makes no call).  Its launches overlap one another and the end of the kernel before them on
+ * the stream, never one that the caller puts behind.  The lists are read on the
+ * device: a page number, length or count out of range sets the device status word to
+ * CP_ERR_PAGE, is never followed, and leaves its rows' results unspecified.
  */
 cp_status cp_prefix_attn_workspace_size(int64_t R, int64_t B, int64_t max_new, int64_t prefix_len, int64_t N,
                                         int64_t Nkv, int64_t D, int64_t page_size, int64_t max_pages, size_t *bytes);

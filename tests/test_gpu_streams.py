@@ -10,12 +10,15 @@ ring adds a pooled side stream joined back with events.  These tests check that
   * two host threads running prefetched rings at once on their own streams each
     get exactly their single-threaded results (no shared side stream or event).
 """
+import subprocess
+import sys
 import threading
 
 import pytest
 import torch
 
 import cp_synth as SY
+from conftest import ROOT
 from context_causal_attention_gb300 import ops as F
 
 pytestmark = pytest.mark.gpu
@@ -186,3 +189,61 @@ def test_memory_of_a_call_on_another_stream(cuda_dev, name, keep):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         torch.cuda.synchronize()
         assert all((t == i + 1).all() for i, t in enumerate(late))
+
+
+@pytest.mark.parametrize("name", ["rope", "norm_bwd", "append", "prefix", "ring"])
+def test_stream_argument_inside_a_capture(cuda_dev, name):
+    """A call on a side stream of a capture, its outputs and scratch allocated there: each replay
+    gives the eager bits, over whatever the memory held."""
+    call, _ = _side_calls(cuda_dev)[name]
+    many = lambda x: [t for t in (x if isinstance(x, (tuple, list)) else [x]) if t is not None]  # noqa: E731
+    want = [t.clone() for t in many(call(None))]
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        call(s)  # dropped: its memory goes to later work of s
+        got = many(call(s))
+        torch.cuda.current_stream().wait_stream(s)
+    for _ in range(3):
+        for t in got:
+            t.fill_(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+FIRST = """
+import sys, torch
+from context_causal_attention_gb300 import ops as F
+dev, bf, i32 = "cuda", torch.bfloat16, torch.int32
+q, k = (torch.randn(40, h, 64, device=dev).to(bf) for h in (8, 2))
+pos = torch.arange(40, dtype=i32, device=dev)
+w = [torch.ones(64, device=dev)] * 2
+rope = F.cp_rope_freqs(64, device=dev)
+kc, vc = (torch.randn(64, 16, 2, 64, device=dev).to(bf) for _ in range(2))
+table, pages = torch.arange(64, dtype=i32, device=dev).view(2, 32), torch.arange(64, dtype=i32, device=dev)
+cu, kv_len = torch.tensor([0, 20, 40], dtype=i32, device=dev), torch.tensor([300, 400], dtype=i32, device=dev)
+calls = {
+    "norm_bwd": lambda: F.cp_qk_norm_rope_bwd(q, k, q, k, *w, pos, rope),
+    "append": lambda: (F.cp_cache_append(k, k, kc, vc, table, cu, kv_len, rope=rope, q=q),),
+    "prefix": lambda: F.cp_prefix_attn_fwd(q, kc, vc, pages, 1000, table, cu, kv_len, 20),
+}
+call = calls[sys.argv[1]]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = call()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, call()))
+print("same")
+"""
+
+
+@pytest.mark.parametrize("name", ["norm_bwd", "append", "prefix"])
+def test_first_call_of_a_process_may_be_captured(cuda_dev, name):
+    """What a kernel sets up at its first call is allowed inside a capture."""
+    r = subprocess.run([sys.executable, "-c", FIRST, name], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
