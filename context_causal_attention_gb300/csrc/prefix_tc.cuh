@@ -342,7 +342,8 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                     if (paired) commit(k_empty + st, lead);  // for the other half
                 }
                 // Q has been read when the last scores are there.  (The weights that this warp
-                // waits for next come after them, so the wait costs nothing.)
+                // waits for next come after them.  Against a commit on q_empty in this place: 300
+                // sequences of 30 tokens 174 and 171 us, 64 of 20 behind 16384 keys 312 and 312.)
                 if (!ok || !mbar_wait_warp(s_full + i, tiles & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
                 if (lane == 0) mbar_arrive(q_empty);
                 const int last = begin + (n - 1 - begin) / step * step;

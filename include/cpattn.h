@@ -507,7 +507,8 @@ cp_status cp_rope_bwd(const void *dq_out, const void *dk_out, const int32_t *pos
  *   eps     : finite, >= 0
  *   rope    : NULL for the norm alone (pos is not read then)
  * The mean square is formed in fp32: a row of values above 1.6e18 overflows it
- * (its r is 0), and with eps = 0 a row below 1e-19 falls under it (its r is infinite).
+ * (its r is 0), and with eps = 0 a row below 1e-19 loses bits of it, below 1e-23 all (its r
+ * is infinite).
  * Everything else as for cp_rope_fwd.
  */
 cp_status cp_qk_norm_rope_fwd(const void *q, const void *k, const void *wq, const void *wk, const int32_t *pos,
