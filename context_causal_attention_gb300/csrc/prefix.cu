@@ -707,9 +707,11 @@ __global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
 
 // ---------------------------------------------------------------- host side
 // Up to this many rows (tokens x heads) a warp joins one, beyond it kJoinHeads heads
-// of a token.  Few rows have many pieces: a call of 64 tokens of 32 heads takes
-// 141 us with a warp for a token's heads and 88 with one for a row.  Many rows have
-// few: the prompts above 1208 us by tokens and 1335 by rows.
+// of a token.  Few rows have many pieces, many rows few.  The whole call, by rows and by
+// tokens, 32 heads of 128, tokens of one behind 32768 keys: 2048 rows 106 and 163 us,
+// 8192 237 and 263, 16384 362 and 374, 32768 594 and 575, 65536 (16384 keys) 767 and 692;
+// prompts behind 16384 keys: 8192 rows 93 and 132, 16384 153 and 169, 32768 288
+// and 276, 65536 515 and 454; one prompt with no prefix: 16384 51 and 48, 32768 77 and 54.
 constexpr long long kJoinRows = 16384;
 
 // Blocks of a launch for each lane.
