@@ -27,20 +27,24 @@ struct PageTable {
 
 // The sequence that new token `tok` belongs to by the cumulative counts cu[0..B]
 // (the last b with cu[b] <= tok; -1 for rows outside all sequences), where it
-// begins and how many new tokens it has.  Warp-wide: 32 probes a level.
+// begins and how many new tokens it has.  Warp-wide: 32 probes a level.  kPastL1: for a
+// kernel that reads the list before its wait for the kernel before it, when an SM's L1
+// may still hold what another call's list said.
+template <bool kPastL1 = false>
 __device__ __forceinline__ int find_sequence(const int32_t *cu, int B, int tok, int lane, int *begin, int *count) {
+    auto at = [](const int32_t *p) { return kPastL1 ? __ldcg(p) : __ldg(p); };
     int lo = 0, n = B;
     for (;;) {
         const int step = (n + 31) >> 5;
-        const int at = lane * step;
-        const bool ok = at < n && __ldg(cu + lo + at) <= tok;
+        const int mine = lane * step;
+        const bool ok = mine < n && at(cu + lo + mine) <= tok;
         const int k = __popc(__ballot_sync(0xffffffffu, ok));
         if (k == 0) return -1;
         lo += (k - 1) * step;
         if (step == 1) break;
         n = min(step, n - (k - 1) * step);
     }
-    const int c0 = __ldg(cu + lo), c1 = __ldg(cu + lo + 1);
+    const int c0 = at(cu + lo), c1 = at(cu + lo + 1);
     if (tok < c0 || tok >= c1) return -1;
     *begin = c0;
     *count = c1 - c0;

@@ -492,7 +492,7 @@ __device__ __forceinline__ long long own_keys(const JoinArgs &a, int b, int *beg
         *begin = *count = 0;
         return 0;
     }
-    return min(max(static_cast<long long>(__ldg(a.kv_len + b)), 0ll), a.most);
+    return min(max(static_cast<long long>(__ldcg(a.kv_len + b)), 0ll), a.most);
 }
 
 // A part of one token's rows, for all its heads.
@@ -575,9 +575,9 @@ __global__ void __launch_bounds__(128) join_row_kernel(const JoinArgs a) {
     if (row >= static_cast<long long>(a.R) * a.N) return;
     const int tok = static_cast<int>(row / a.N), h = static_cast<int>(row - static_cast<long long>(tok) * a.N);
     int begin, count;
-    const int b = find_sequence(a.cu, a.B, tok, lane, &begin, &count);
-    // inputs, as the search: before the wait
-    const int all = min(max(__ldg(a.cu + a.B), 0), a.R);
+    const int b = find_sequence<true>(a.cu, a.B, tok, lane, &begin, &count);
+    // inputs, as the search: before the wait, and past L1
+    const int all = min(max(__ldcg(a.cu + a.B), 0), a.R);
     const long long len = own_keys(a, b, &begin, &count);
     wait_for_previous();
     if (b < 0) return;
@@ -643,9 +643,9 @@ __global__ void __launch_bounds__(128) join_token_kernel(const JoinArgs a) {
     const int tok = static_cast<int>(unit / blocks), h0 = static_cast<int>(unit - static_cast<long long>(tok) * blocks) * kJoinHeads;
     if (tok >= a.R) return;
     int begin, count;
-    const int b = find_sequence(a.cu, a.B, tok, lane, &begin, &count);
-    // inputs, as the search: before the wait
-    const int all = min(max(__ldg(a.cu + a.B), 0), a.R);
+    const int b = find_sequence<true>(a.cu, a.B, tok, lane, &begin, &count);
+    // inputs, as the search: before the wait, and past L1
+    const int all = min(max(__ldcg(a.cu + a.B), 0), a.R);
     const long long len = own_keys(a, b, &begin, &count);
     wait_for_previous();
     if (b < 0) return;

@@ -460,3 +460,34 @@ def test_append_then_attend_decodes_like_one_causal_attention(cuda_dev):
             assert np.abs(f64(lse)[:, at:at + n[s]] - wl).max() <= 2.0 ** -5
             within(o[at:at + n[s]], wo, "bf16", (2.0 ** -8 + 2.0 ** -4) * a, "decode")
             at += n[s]
+
+
+@pytest.mark.parametrize("N,Nkv", [(10, 5), (21, 7), (4, 1)])
+def test_lists_that_change_between_calls(cuda_dev, N, Nkv):
+    """A decode loop on the device: one small launch between two calls moves the lengths and
+    the counts on in place, and every call sees the new ones on all SMs, also on those that
+    the launches between left alone (the lanes of 5 or 7 KV heads do not use every SM)."""
+    B, steps = 40, 24
+    c = Call(23, [2] * B, [3 + 7 * b % 150 + steps for b in range(B)], 260, N, Nkv, 64, 16)
+    c.run(cuda_dev)
+    q, k, v, pages, table, cu, kv_len = c.dev
+    full = kv_len.clone()
+    lists = torch.cat([cu, kv_len])
+    cu, kv_len = lists[:B + 1], lists[B + 1:]
+    # kinds of rows move too: sequence 0 has between 1 and 3 of the new tokens, the next the rest of 4
+    after = []
+    for i in range(steps):
+        want = torch.cat([c.cu.to(cuda_dev), full - i])
+        want[1] = 1 + i % 3
+        after.append(want)
+    ws = torch.empty(F.cp_prefix_attn_workspace_size(2 * B, B, 3, 260, N, Nkv, 64, 16, table.shape[1]), dtype=torch.uint8,
+                     device=cuda_dev)
+    outs = [(torch.empty_like(q), torch.empty(N, 2 * B, device=cuda_dev)) for _ in range(steps)]
+    for i in range(steps):
+        lists.copy_(after[i])
+        F.cp_prefix_attn_fwd(q, k, v, pages, 260, table, cu, kv_len, 3, o=outs[i][0], lse=outs[i][1], workspace=ws)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        new = after[i][:B + 1].clone(), after[i][B + 1:].clone()  # lists of their own, never changed
+        o, lse = F.cp_prefix_attn_fwd(q, k, v, pages, 260, table, *new, 3)
+        assert torch.equal(o, outs[i][0]) and torch.equal(lse, outs[i][1]), i
