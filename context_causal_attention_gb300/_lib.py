@@ -118,6 +118,14 @@ def lib():
     L.cp_prefix_attn_fwd.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i64, i64, i64, i64, i64, f32,
                                      vp, i32, vp, vp, sz, vp]
     L.cp_selftest_stalled_prefix_attn.argtypes = L.cp_prefix_attn_fwd.argtypes[:-1] + [ctypes.c_uint64, vp]
+    L.cp_cache_plan.argtypes = [vp, vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp]
+    L.cp_cache_append_at.argtypes = [vp, vp, vp, i64, i64, i64, i32, i64, i64, i64, i64, vp, vp, i32, f32, rp, vp, vp,
+                                     i64, i64, vp, vp, vp, vp]
+    L.cp_cache_keep.argtypes = [vp, i64, i64, i64, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64, vp, vp, vp]
+    L.cp_tree_plan.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp, vp, vp]
+    L.cp_tree_attn_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
+    L.cp_tree_attn_fwd.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, i64, i64, i64, i64,
+                                   i64, f32, vp, i32, vp, vp, sz, vp]
     for name in header_symbols():
         if name not in ("cp_status_string", "cp_version", "cp_last_cuda_error"):
             getattr(L, name).restype = ctypes.c_int

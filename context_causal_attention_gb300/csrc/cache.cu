@@ -5,7 +5,8 @@
 // n_b + j, position pos_base + i, and slot i % page_size of page
 // table[b][i / page_size].  K: norm, rotation, bf16, into that slot; V: bf16,
 // into the same slot of the other cache; Q: norm, rotation, bf16, in place
-// order.  Norm and rotation as in rope.cu.
+// order.  Norm and rotation as in rope.cu.  cp_cache_append_at takes slots and positions as
+// lists instead (drafted tokens of a tree: siblings share a position).
 //
 // Memory-bound where there are many tokens and latency-bound at one token for
 // each sequence, so one launch does all three tensors: a warp takes a token
@@ -43,6 +44,7 @@ struct AppendArgs {
     RopeDev rope;
     PageTable pt;
     const int32_t *cu, *kv_len;
+    const int32_t *slots, *pos;  // kAt: of each row
     long long tokens, pos_base;
     int group, chunks, hpu;
 };
@@ -55,10 +57,19 @@ __device__ __forceinline__ long long slot_of(const AppendArgs &a, int b, int tok
     return slot;
 }
 
+// Row tok's slot as its list gives it, or -1 (none, or out of range and reported), and its position.
+__device__ __forceinline__ long long slot_in_list(const AppendArgs &a, int tok, long long *pos) {
+    *pos = __ldg(a.pos + tok);
+    const long long slot = __ldg(a.slots + tok), all = static_cast<long long>(a.pt.n_pages) << a.pt.shift;
+    if (slot >= -1 && slot < all) return slot;
+    atomicExch(&g_cache_status, static_cast<int>(CP_ERR_PAGE));
+    return -1;
+}
+
 // A unit is `group` tokens in a row with all their heads, or (group 1) `hpu` heads
 // of one token.  The rows of q, k and v of a token make one list, so that four rows
 // of a lane are in flight whichever tensor they belong to.
-template <typename T, int D, int kOrder>
+template <typename T, int D, int kOrder, bool kAt>
 __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs a) {
     using Map = LaneMap<D, kOrder>;
     constexpr int kU = sizeof(T) == 2 ? 4 : 2;
@@ -75,7 +86,9 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs a)
         const int last = min(first + a.hpu, all);
         // lane i looks up token tok0 + i
         long long idx = 0, slot = -1;
-        if (a.group == 1) {
+        if (kAt) {
+            if (lane < a.group && tok0 + lane < a.tokens) slot = slot_in_list(a, tok0 + lane, &idx);
+        } else if (a.group == 1) {
             int begin, count;
             const int b = find_sequence(a.cu, a.pt.B, tok0, lane, &begin, &count);
             if (b < 0) continue;  // a row behind the last sequence
@@ -146,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs a)
     }
 }
 
-template <typename T, int D, int kOrder>
+template <typename T, int D, int kOrder, bool kAt>
 cp_status launch_append(AppendArgs &a, cudaStream_t stream) {
     constexpr int rows = LaneMap<D, kOrder>::kRows;
     const int heads = a.heads[0] + a.heads[1] + a.heads[2], most = (heads + rows - 1) / rows;
@@ -164,7 +177,7 @@ cp_status launch_append(AppendArgs &a, cudaStream_t stream) {
     a.chunks = (heads + a.hpu - 1) / a.hpu;
     const long long blocks = ((a.tokens + a.group - 1) / a.group * a.chunks + kWarps - 1) / kWarps;
     const long long cap = static_cast<long long>(sm_count()) * 4;
-    append_kernel<T, D, kOrder><<<static_cast<unsigned>(blocks < cap ? blocks : cap), kThreads, 0, stream>>>(a);
+    append_kernel<T, D, kOrder, kAt><<<static_cast<unsigned>(blocks < cap ? blocks : cap), kThreads, 0, stream>>>(a);
     return last_launch_status();
 }
 
@@ -181,6 +194,10 @@ cp_status read_cache_device_status(int *code, bool clear) {
     return CP_OK;
 }
 
+cp_status cache_status_word(int **p) {
+    return cuda_status(cudaGetSymbolAddress(reinterpret_cast<void **>(p), g_cache_status));
+}
+
 cp_status check_pages(int64_t n_pages, int64_t page_size, int64_t B, int64_t max_pages, int64_t Nkv, int64_t D) {
     if (n_pages < 1 || n_pages > INT32_MAX || B < 1 || B > kMaxSequences || max_pages < 1 || max_pages > INT32_MAX ||
         Nkv < 1 || Nkv > 65535)
@@ -195,13 +212,17 @@ cp_status check_pages(int64_t n_pages, int64_t page_size, int64_t B, int64_t max
 
 using namespace cpattn;
 
-extern "C" cp_status cp_cache_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
-                                     int64_t v_stride, cp_dtype dtype, int64_t R, int64_t N, int64_t Nkv, int64_t D,
-                                     const void *wq, const void *wk, cp_dtype w_dtype, float eps, const cp_rope *rope,
-                                     int64_t pos_base, void *k_cache, void *v_cache, int64_t n_pages,
-                                     int64_t page_size, const int32_t *table, int64_t B, int64_t max_pages,
-                                     const int32_t *cu_new, const int32_t *kv_len, void *q_out, cudaStream_t stream) {
-    if (!k || !v || !k_cache || !v_cache || !table || !cu_new || !kv_len || (N > 0 && (!q || !q_out)))
+namespace {
+// cp_cache_append, or with kAt cp_cache_append_at (slots and pos in the place of the lists that the slots follow from).
+template <bool kAt>
+cp_status append_call(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                      cp_dtype dtype, int64_t R, int64_t N, int64_t Nkv, int64_t D, const void *wq, const void *wk,
+                      cp_dtype w_dtype, float eps, const cp_rope *rope, int64_t pos_base, void *k_cache, void *v_cache,
+                      int64_t n_pages, int64_t page_size, const int32_t *table, int64_t B, int64_t max_pages,
+                      const int32_t *cu_new, const int32_t *kv_len, const int32_t *slots, const int32_t *pos, void *q_out,
+                      cudaStream_t stream) {
+    if (!k || !v || !k_cache || !v_cache || (N > 0 && (!q || !q_out)) ||
+        (kAt ? !slots || !pos : !table || !cu_new || !kv_len))
         return CP_ERR_NULL;
     if (R < 1 || R > INT32_MAX / 2 || N < 0 || N > 65535) return CP_ERR_SHAPE;
     cp_status st = check_pages(n_pages, page_size, B, max_pages, Nkv, D);
@@ -217,7 +238,8 @@ extern "C" cp_status cp_cache_append(const void *q, const void *k, const void *v
     if ((N && q_stride * es % 16) || k_stride * es % 16 || v_stride * es % 16 || misaligned(q) || misaligned(k) ||
         misaligned(v) || misaligned(k_cache) || misaligned(v_cache) || misaligned(q_out) || misaligned(wq) ||
         misaligned(wk) || (reinterpret_cast<uintptr_t>(table) & 3u) || (reinterpret_cast<uintptr_t>(cu_new) & 3u) ||
-        (reinterpret_cast<uintptr_t>(kv_len) & 3u))
+        (reinterpret_cast<uintptr_t>(kv_len) & 3u) || (reinterpret_cast<uintptr_t>(slots) & 3u) ||
+        (reinterpret_cast<uintptr_t>(pos) & 3u))
         return CP_ERR_ALIGNMENT;
     const char *kc = static_cast<const char *>(k_cache), *vc = static_cast<const char *>(v_cache);
     const int64_t cache = n_pages * page_size * Nkv * D * 2;
@@ -257,14 +279,39 @@ extern "C" cp_status cp_cache_append(const void *q, const void *k, const void *v
     a.pt.shift = __builtin_ctzll(static_cast<unsigned long long>(page_size));
     a.cu = cu_new;
     a.kv_len = kv_len;
+    a.slots = slots;
+    a.pos = pos;
     a.tokens = R;
     a.pos_base = pos_base;
     const bool inter = rope && rope->order == CP_ROPE_INTERLEAVED;
     if (dtype == CP_BF16) {
         using T = __nv_bfloat16;
-        if (D == 128) return inter ? launch_append<T, 128, 1>(a, stream) : launch_append<T, 128, 0>(a, stream);
-        return inter ? launch_append<T, 64, 1>(a, stream) : launch_append<T, 64, 0>(a, stream);
+        if (D == 128) return inter ? launch_append<T, 128, 1, kAt>(a, stream) : launch_append<T, 128, 0, kAt>(a, stream);
+        return inter ? launch_append<T, 64, 1, kAt>(a, stream) : launch_append<T, 64, 0, kAt>(a, stream);
     }
-    if (D == 128) return inter ? launch_append<float, 128, 1>(a, stream) : launch_append<float, 128, 0>(a, stream);
-    return inter ? launch_append<float, 64, 1>(a, stream) : launch_append<float, 64, 0>(a, stream);
+    if (D == 128) return inter ? launch_append<float, 128, 1, kAt>(a, stream) : launch_append<float, 128, 0, kAt>(a, stream);
+    return inter ? launch_append<float, 64, 1, kAt>(a, stream) : launch_append<float, 64, 0, kAt>(a, stream);
+}
+}  // namespace
+
+extern "C" cp_status cp_cache_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                     int64_t v_stride, cp_dtype dtype, int64_t R, int64_t N, int64_t Nkv, int64_t D,
+                                     const void *wq, const void *wk, cp_dtype w_dtype, float eps, const cp_rope *rope,
+                                     int64_t pos_base, void *k_cache, void *v_cache, int64_t n_pages,
+                                     int64_t page_size, const int32_t *table, int64_t B, int64_t max_pages,
+                                     const int32_t *cu_new, const int32_t *kv_len, void *q_out, cudaStream_t stream) {
+    return append_call<false>(q, k, v, q_stride, k_stride, v_stride, dtype, R, N, Nkv, D, wq, wk, w_dtype, eps, rope,
+                              pos_base, k_cache, v_cache, n_pages, page_size, table, B, max_pages, cu_new, kv_len,
+                              nullptr, nullptr, q_out, stream);
+}
+
+extern "C" cp_status cp_cache_append_at(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                        int64_t v_stride, cp_dtype dtype, int64_t R, int64_t N, int64_t Nkv, int64_t D,
+                                        const void *wq, const void *wk, cp_dtype w_dtype, float eps,
+                                        const cp_rope *rope, void *k_cache, void *v_cache, int64_t n_pages,
+                                        int64_t page_size, const int32_t *slots, const int32_t *pos, void *q_out,
+                                        cudaStream_t stream) {
+    return append_call<true>(q, k, v, q_stride, k_stride, v_stride, dtype, R, N, Nkv, D, wq, wk, w_dtype, eps, rope, 0,
+                             k_cache, v_cache, n_pages, page_size, nullptr, 1, 1, nullptr, nullptr, slots, pos, q_out,
+                             stream);
 }

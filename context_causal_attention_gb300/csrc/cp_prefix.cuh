@@ -63,6 +63,9 @@ struct PrefixArgs {
     float2 *slot_ml;      // [slots][TM]: exponent, sum
     float *slot_o;        // [slots][TM][D], not divided by the sum
     int slots;            // of a lane
+    // trees of drafted tokens (kTree): bit i of row r, whether it sees its sequence's new token i
+    const uint32_t *mask;  // [R][words]
+    int words;
 };
 
 // A bad list never hides that a wait ran out.
@@ -256,12 +259,31 @@ struct Piece {
     int keys;             // keys of the problem
     int off;              // rows of token i see keys [0, off + i] (prefix: all)
     int k0, k1;           // key tiles [k0, k1), may be none
+    int tree;             // new tokens of a sequence whose rows go by their masks, 0 else
 };
 
 // Keys that row `row` of the problem sees: [0, limit).
 __device__ __forceinline__ int row_limit(const PrefixArgs &a, const Piece &x, int row) {
     return x.b < 0 ? x.keys
                    : min(x.keys, max(0, x.off + static_cast<int>(fdiv(static_cast<uint32_t>(row), a.div_g)) + 1));
+}
+
+// Keys key .. key + 31 of a tree's piece that the row of its token `tok` sees, as bits: all cached keys,
+// of the step's new tokens (key off + i is token i) those of the row's mask, none behind.
+__device__ __forceinline__ uint32_t tree_bits(const PrefixArgs &a, const Piece &x, int tok, int key) {
+    const int i = key - x.off, w = i >> 5;
+    if (i <= -32) return 0xffffffffu;
+    const uint32_t *m = a.mask + static_cast<long long>(x.tok0 + tok) * a.words;
+    const uint32_t lo = w < 0 ? 0xffffffffu : (w < a.words ? __ldcg(m + w) : 0u);
+    const uint32_t hi = w + 1 < a.words ? __ldcg(m + w + 1) : 0u;
+    const uint32_t bits = __funnelshift_r(lo, hi, i & 31);
+    const int left = x.tree - i;
+    return left >= 32 ? bits : (left > 0 ? bits & ((1u << left) - 1u) : 0u);
+}
+// The same of a row that sees the keys below `limit`.
+__device__ __forceinline__ uint32_t limit_bits(int limit, int key) {
+    const int n = limit - key;
+    return n >= 32 ? 0xffffffffu : (n > 0 ? (1u << n) - 1u : 0u);
 }
 
 // Where a block's share begins: the item and the place in it.
@@ -310,7 +332,7 @@ __device__ __forceinline__ void find_start(const PrefixArgs &a, const Line &line
 // step is a few additions.  The walk and the piece it has come to lie in shared
 // memory: they are looked at once in many tiles, and the registers of the tile
 // loops are scarce.
-template <int TM, int KT>
+template <int TM, int KT, bool kTree>
 struct Walk {
     Problem p;
     Start s;
@@ -345,8 +367,10 @@ struct Walk {
         x.rows = p.n * a.G;
         x.keys = static_cast<int>(p.keys);
         x.off = x.keys - p.n;
+        x.tree = kTree && s.b >= 0 && p.n <= 32 * a.words ? p.n : 0;
         const long long n1 = min(s.n0 + left, p.key_tiles);
-        const long long need = (static_cast<long long>(row_limit(a, x, min(x.row0 + TM, x.rows) - 1)) + KT - 1) / KT;
+        const int last = kTree && x.tree ? x.keys : row_limit(a, x, min(x.row0 + TM, x.rows) - 1);
+        const long long need = (static_cast<long long>(last) + KT - 1) / KT;
         // the part [n0, n1) of the nominal length, scaled to the tiles that the rows need
         x.k0 = static_cast<int>(s.n0 == 0 ? 0 : s.n0 * need / p.key_tiles);
         x.k1 = static_cast<int>(n1 == p.key_tiles ? need : n1 * need / p.key_tiles);

@@ -71,7 +71,7 @@ struct TcCfg {
     static_assert(kOffMisc % 16 == 0, "tensor memory's address is left on 16 bytes");
     static constexpr int kOffMl = (kOffMisc + 16 + 15) & ~15;        // [128] (m, l) of the second half
     static constexpr int kOffWalk = kOffMl + 128 * 8;   // [warps]
-    static constexpr int kSmem = kOffWalk + kWalks * static_cast<int>(sizeof(Walk<kTcTM, kTcKT>)) + 1024;  // + alignment slack
+    static constexpr int kSmem = kOffWalk + kWalks * static_cast<int>(sizeof(Walk<kTcTM, kTcKT, false>)) + 1024;  // + alignment slack
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -84,6 +84,13 @@ __device__ __forceinline__ void hide_columns(int c0, int lim, uint32_t (&h)[64])
 #pragma unroll
     for (int c = 0; c < 64; ++c)
         if (c0 + c >= lim) h[c] = 0xff800000u;
+}
+
+// The same by bits: word w of `seen` says it of columns 32 w .. 32 w + 31.
+__device__ __forceinline__ void hide_columns(uint32_t w0, uint32_t w1, uint32_t (&h)[64]) {
+#pragma unroll
+    for (int c = 0; c < 64; ++c)
+        if (!((c < 32 ? w0 : w1) >> (c & 31) & 1u)) h[c] = 0xff800000u;
 }
 
 // One lane of the warp (non-zero there), the same at every call.
@@ -177,8 +184,8 @@ __device__ __forceinline__ void tc_init(uint8_t *smem, const CUtensorMap &tmK, c
 }
 
 // A block's share, behind the scan of its line.  tma: the pages are copied by TMA,
-// else by cp.async.
-template <int D, bool tma>
+// else by cp.async.  kTree: rows of drafted trees go by their masks.
+template <int D, bool tma, bool kTree>
 __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMap &tmV, const PrefixArgs &a,
                                         uint8_t *smem) {
     using C = TcCfg<D>;
@@ -205,7 +212,8 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
     const uint32_t tmem = *tmem_slot;
     uint8_t *sQ = smem + C::kOffQ, *sK = smem + C::kOffK, *sV = smem + C::kOffV;
 
-    Walk<kTcTM, kTcKT> &walk = reinterpret_cast<Walk<kTcTM, kTcKT> *>(smem + C::kOffWalk)[warp];
+    using Walker = Walk<kTcTM, kTcKT, kTree>;
+    Walker &walk = reinterpret_cast<Walker *>(smem + C::kOffWalk)[warp];
     const Piece &x = walk.x;
     walk.begin(a, line, start, t1 - t0);
     if (warp == 0 || warp == 2) {
@@ -409,26 +417,38 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
             // counted from the current tile: keys of the problem, that this row sees, that all rows see
             int past = x.keys - (x.k0 + begin) * 128;
             int limit = (valid ? row_limit(a, x, row) : x.keys) - (x.k0 + begin) * 128;
-            int whole = row_limit(a, x, first_row) - (x.k0 + begin) * 128;
+            int whole = (kTree && x.tree ? max(x.off, 0) : row_limit(a, x, first_row)) - (x.k0 + begin) * 128;
+            const int tok = static_cast<int>(fdiv(static_cast<uint32_t>(valid ? row : x.row0), a.div_g));
             float m_run = -INFINITY, l_run = 0.f;
             for (int n = begin; n < all;) {
+                const bool mask = whole < 128;
+                uint32_t seen[4];  // the tile's columns that this row sees
+                if (kTree && mask) {
+                    const int key = x.keys - past;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        seen[w] = x.tree && valid ? tree_bits(a, x, tok, key + 32 * w) : limit_bits(limit, 32 * w);
+                }
+                // Scores that the row does not see become -inf: columns 0 .. 63 of a tile or 64 .. 127.
+                auto hide = [&](int upper, uint32_t (&h)[64]) {
+                    if (kTree) hide_columns(seen[2 * upper], seen[2 * upper + 1], h);
+                    else hide_columns(64 * upper, limit, h);
+                };
                 if (!dry && !mbar_wait_warp(s_full + half, tiles & 1u, abort_flag, a.timeout_ns)) { ok = false; break; }
                 // The halves take turns at the exponentials: left alone they fall into
                 // step, and the tensor cores wait while both compute and the other way round.
                 if (!dry && !my_turn()) { ok = false; break; }
                 tc_fence_after();
-                const bool mask = whole < 128;
-                const int lim = limit;
                 uint32_t sa[64], sb[64], pa[32], pb[32];
                 tmem_ld64_nowait(tS, sa);
                 tmem_wait_ld(sa);
                 tmem_ld64_nowait(tS + 64, sb);
-                if (mask) hide_columns(0, lim, sa);
+                if (mask) hide(0, sa);
                 const bool first = !__all_sync(0xffffffffu, m_run != -INFINITY);
                 if (first) {
                     // rows without a running maximum yet: set it
                     tmem_wait_ld(sb);
-                    if (mask) hide_columns(64, lim, sb);
+                    if (mask) hide(1, sb);
                     if (m_run == -INFINITY) {
                         const float top = row_max128(sa, sb) * sl2;
                         if (top > -INFINITY) m_run = ceilf(top);
@@ -438,7 +458,7 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                 const float s0 = exp_pack64(sa, sl2, neg_m, pa);
                 tmem_wait_ld(sb);  // columns 64..127 are read: P may overwrite them
                 if (!dry) tmem_st32_nowait(tS + 64, pa);
-                if (mask && !first) hide_columns(64, lim, sb);
+                if (mask && !first) hide(1, sb);
                 const float s1 = exp_pack64(sb, sl2, neg_m, pb);
                 if (!dry) tmem_st32_nowait(tS + 96, pb);
                 float sum = s0 + s1;
@@ -449,7 +469,7 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                     // rare: the scores grew by more than 2^64 over the running maximum.
                     // Columns 0..63 of S are still in tensor memory, 64..127 in sb.
                     tmem_ld64(tS, sa);
-                    if (mask) hide_columns(0, lim, sa);
+                    if (mask) hide(0, sa);
                     float f = 1.f;
                     if (big) {
                         const float m_new = ceilf(row_max128(sa, sb) * sl2), d = m_run - m_new;
@@ -569,7 +589,7 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
     if (tid == 0 && *abort_flag) report(a.status, CP_ERR_DEVICE_TIMEOUT);
 }
 
-template <int D, bool tma>
+template <int D, bool tma, bool kTree>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PrefixArgs a) {
@@ -583,7 +603,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     launch_dependents();
     scan_line<kTcTM, kTcKT>(a, line, nullptr, 0);
     if (blockIdx.x == 0 && blockIdx.y == 0) leave_places<kTcTM, kTcKT>(a, line);
-    tc_work<D, tma>(tmK, tmV, a, smem);
+    tc_work<D, tma, kTree>(tmK, tmV, a, smem);
 }
 
 }  // namespace

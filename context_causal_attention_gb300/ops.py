@@ -23,7 +23,8 @@ __all__ = [
     "cp_allgather_attention_fwd", "cp_ulysses_attention_fwd",
     "cp_device_status", "cp_version", "cp_rope_freqs", "cp_rope_phases", "cp_rope_fwd", "cp_rope_bwd",
     "cp_qk_norm_rope_fwd", "cp_qk_norm_rope_bwd_workspace_size", "cp_qk_norm_rope_bwd", "cp_cache_append",
-    "cp_prefix_attn_workspace_size", "cp_prefix_attn_fwd",
+    "cp_prefix_attn_workspace_size", "cp_prefix_attn_fwd", "cp_cache_plan", "cp_cache_append_at", "cp_cache_keep",
+    "cp_tree_plan", "cp_tree_attn_workspace_size", "cp_tree_attn_fwd", "CpCaches",
     "CP_BF16", "CP_F32", "CP_ZIGZAG", "CP_CONTIGUOUS", "CP_SEQ_TO_HEAD", "CP_HEAD_TO_SEQ", "CP_RANK_ORDER",
     "CP_GLOBAL_ORDER", "CP_RING_PREFETCH", "CP_RING_FUSED_MERGE", "CP_RING_TF32", "CP_ROPE_HALF",
     "CP_ROPE_INTERLEAVED", "CP_ROPE_PLAIN", "CP_ROPE_LINEAR", "CP_ROPE_BASE", "CP_ROPE_BY_PARTS", "CpRope", "CpError",
@@ -639,13 +640,8 @@ def _check_cache(k_cache, v_cache, table, cu_new, kv_len):
     return (*shape, *tab)
 
 
-def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=None, q_out=None, wq=None, wk=None,
-                    eps=1e-6, pos_base=0, stream=None):
-    """Append the new tokens' k, v [R,Nkv,D] to the pages of their sequences,
-    k normed (wk) and rotated (rope) on the way; q [R,N,D], if given, likewise into
-    q_out bf16 [R,N,D].  kv_len counts each sequence's tokens after the call.
-    Returns q_out (None without q)."""
-    n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
+def _append_rows(k, v, q, q_out, Nkv, D, stream):
+    """(R, N, strides of q, k and v, q_out) of the new tokens' rows."""
     shape, dtype = k.shape, k.dtype
     if len(shape) != 3 or v.shape != shape or shape[1] != Nkv or shape[2] != D or v.dtype is not dtype:
         raise ValueError("k and v must be [R, Nkv, D] of the cache's heads, of one dtype")
@@ -661,6 +657,17 @@ def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=
             raise ValueError("q_out must be contiguous bf16 [R, N, D]")
     elif q_out is not None:
         raise ValueError("q_out without q")
+    return R, N, qs, ks, vs, q_out
+
+
+def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=None, q_out=None, wq=None, wk=None,
+                    eps=1e-6, pos_base=0, stream=None):
+    """Append the new tokens' k, v [R,Nkv,D] to the pages of their sequences,
+    k normed (wk) and rotated (rope) on the way; q [R,N,D], if given, likewise into
+    q_out bf16 [R,N,D].  kv_len counts each sequence's tokens after the call.
+    Returns q_out (None without q)."""
+    n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
+    R, N, qs, ks, vs, q_out = _append_rows(k, v, q, q_out, Nkv, D, stream)
     wd = _check_weights(wq, wk, D)
     dev = _here(q, k, v, k_cache, v_cache, table, cu_new, kv_len, wq, wk, None if rope is None else rope.freqs, q_out)
     st = _lib.lib().cp_cache_append(_addr(q), _addr(k), _addr(v), qs, ks, vs, _dtype_code(k), R, N, Nkv, D, _addr(wq),
@@ -671,6 +678,131 @@ def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=
     return q_out
 
 
+def _check_list(t, shape, what):
+    """A list that a call reads or writes: contiguous int32 of `shape`."""
+    if t.shape != shape or t.dtype is not torch.int32 or not t.is_contiguous():
+        raise ValueError("%s must be contiguous int32 %s" % (what, list(shape)))
+
+
+def _list_out(t, shape, what, device, stream):
+    if t is None:
+        return _new(shape, torch.int32, device, stream)
+    _check_list(t, shape, what)
+    return t
+
+
+def cp_cache_plan(kv_had, kv_keep, n_new, table, free_pages, n_free, page_size, R, pos_base=0, kv_len=None, cu_new=None,
+                  slots=None, pos=None, n_free_out=None, stream=None):
+    """Pages and slots of a step from the sequences' lengths (see the C header): page numbers go between
+    table [B,max_pages] and the stack free_pages [n_pages].  Returns (kv_len [B], cu_new [B+1], slots [R],
+    pos [R], n_free_out [2]), all int32."""
+    tab, n_pages = table.shape, free_pages.shape
+    if len(tab) != 2 or len(n_pages) != 1:
+        raise ValueError("expected table [B, max_pages] and free_pages [n_pages]")
+    B = tab[0]
+    for t, shape, what in ((table, tab, "table"), (free_pages, n_pages, "free_pages"), (kv_had, (B,), "kv_had"),
+                           (kv_keep, (B,), "kv_keep"), (n_new, (B,), "n_new")):
+        _check_list(t, shape, what)
+    if n_free.dtype is not torch.int32 or n_free.numel() < 1 or not n_free.is_contiguous():
+        raise ValueError("n_free must be contiguous int32 [1] or [2]")
+    dev = table.device
+    kv_len = _list_out(kv_len, (B,), "kv_len", dev, stream)
+    cu_new = _list_out(cu_new, (B + 1,), "cu_new", dev, stream)
+    slots, pos = _list_out(slots, (R,), "slots", dev, stream), _list_out(pos, (R,), "pos", dev, stream)
+    n_free_out = _list_out(n_free_out, (2,), "n_free_out", dev, stream)
+    cur = _here(kv_had, kv_keep, n_new, table, free_pages, n_free, kv_len, cu_new, slots, pos, n_free_out)
+    st = _lib.lib().cp_cache_plan(_addr(kv_had), _addr(kv_keep), _addr(n_new), B, _addr(table), tab[1], page_size,
+                                  _addr(free_pages), n_pages[0], _addr(n_free), pos_base, R, _addr(kv_len),
+                                  _addr(cu_new), _addr(slots), _addr(pos), _addr(n_free_out), _raw_stream(stream, cur))
+    _lib.check("cp_cache_plan", st)
+    return kv_len, cu_new, slots, pos, n_free_out
+
+
+def cp_cache_append_at(k, v, k_cache, v_cache, slots, pos, rope=None, q=None, q_out=None, wq=None, wk=None, eps=1e-6,
+                       stream=None):
+    """cp_cache_append with the rows' slots and positions, int32 [R] each (slot -1: the row is skipped).
+    Returns q_out (None without q)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("the caches must be [n_pages, page_size, Nkv, D], both alike")
+    if k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16:
+        raise TypeError("the caches must be bf16")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("tensor must be contiguous")
+    n_pages, page, Nkv, D = shape
+    R, N, qs, ks, vs, q_out = _append_rows(k, v, q, q_out, Nkv, D, stream)
+    _check_list(slots, (R,), "slots")
+    _check_list(pos, (R,), "pos")
+    wd = _check_weights(wq, wk, D)
+    dev = _here(q, k, v, k_cache, v_cache, slots, pos, wq, wk, None if rope is None else rope.freqs, q_out)
+    st = _lib.lib().cp_cache_append_at(_addr(q), _addr(k), _addr(v), qs, ks, vs, _dtype_code(k), R, N, Nkv, D, _addr(wq),
+                                       _addr(wk), wd, eps, None if rope is None else rope._ref, _addr(k_cache),
+                                       _addr(v_cache), n_pages, page, _addr(slots), _addr(pos), _addr(q_out),
+                                       _raw_stream(stream, dev))
+    _lib.check("cp_cache_append_at", st)
+    return q_out
+
+
+class CpCaches:
+    """The caches of all layers (K and V of each, in any order), for cp_cache_keep: bf16
+    [n_pages, page_size, Nkv, D] each, all alike.  Made once and kept by the caller."""
+
+    def __init__(self, caches):
+        caches = tuple(caches)
+        if not caches or len(caches[0].shape) != 4:
+            raise ValueError("expected caches [n_pages, page_size, Nkv, D]")
+        for c in caches:
+            if c.dtype is not torch.bfloat16:
+                raise TypeError("the caches must be bf16")
+            if c.shape != caches[0].shape or c.device != caches[0].device or not c.is_contiguous():
+                raise ValueError("the caches must be contiguous, all alike, on one device")
+        self._caches = caches
+        self._ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+
+    # read only: calls use the addresses above
+    caches = property(lambda self: self._caches)
+
+
+def cp_cache_keep(caches, table, cu_new, kv_len, kept, n_kept, R=None, kv_keep=None, stream=None):
+    """Move the accepted tokens kept [B,max_kept] (n_kept [B] of each sequence; below zero: all stay) of the step's
+    new tokens together, in every one of `caches` (a CpCaches, or a list of tensors); R: the step's rows.
+    Returns kv_keep int32 [B], the tokens that stay."""
+    if not isinstance(caches, CpCaches):
+        caches = CpCaches(caches)
+    n_pages, page, Nkv, D = caches.caches[0].shape
+    tab = table.shape
+    if len(tab) != 2 or len(kept.shape) != 2:
+        raise ValueError("expected table [B, max_pages] and kept [B, max_kept]")
+    B = tab[0]
+    for t, shape, what in ((table, tab, "table"), (cu_new, (B + 1,), "cu_new"), (kv_len, (B,), "kv_len"),
+                           (kept, (B, kept.shape[1]), "kept"), (n_kept, (B,), "n_kept")):
+        _check_list(t, shape, what)
+    kv_keep = _list_out(kv_keep, (B,), "kv_keep", table.device, stream)
+    dev = _here(caches.caches[0], table, cu_new, kv_len, kept, n_kept, kv_keep)
+    st = _lib.lib().cp_cache_keep(caches._ptrs, len(caches.caches), n_pages, page, Nkv, D, _addr(table), B, tab[1],
+                                  _addr(cu_new), _addr(kv_len), (1 << 30) - 1 if R is None else R, _addr(kept),
+                                  kept.shape[1], _addr(n_kept), _addr(kv_keep), _raw_stream(stream, dev))
+    _lib.check("cp_cache_keep", st)
+    return kv_keep
+
+
+def cp_tree_plan(parent, cu_new, kv_len, words, pos_base=0, mask=None, pos=None, stream=None):
+    """Ancestors and positions of drafted trees from each row's parent [R] among its sequence's new tokens (-1: it
+    follows the cached ones) -> (mask int32 [R,words], pos int32 [R]); see the C header."""
+    if len(parent.shape) != 1 or len(kv_len.shape) != 1:
+        raise ValueError("expected parent [R] and kv_len [B]")
+    R, B = parent.shape[0], kv_len.shape[0]
+    for t, shape, what in ((parent, (R,), "parent"), (cu_new, (B + 1,), "cu_new"), (kv_len, (B,), "kv_len")):
+        _check_list(t, shape, what)
+    mask = _list_out(mask, (R, words), "mask", parent.device, stream)
+    pos = _list_out(pos, (R,), "pos", parent.device, stream)
+    dev = _here(parent, cu_new, kv_len, mask, pos)
+    st = _lib.lib().cp_tree_plan(_addr(parent), _addr(cu_new), _addr(kv_len), B, R, words, pos_base, _addr(mask),
+                                 _addr(pos), _raw_stream(stream, dev))
+    _lib.check("cp_tree_plan", st)
+    return mask, pos
+
+
 def cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page_size, max_pages):
     n = ctypes.c_size_t(0)
     _lib.check("cp_prefix_attn_workspace_size",
@@ -679,8 +811,16 @@ def cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page_siz
     return n.value
 
 
+def cp_tree_attn_workspace_size(R, B, max_new, words, prefix_len, N, Nkv, D, page_size, max_pages):
+    n = ctypes.c_size_t(0)
+    _lib.check("cp_tree_attn_workspace_size",
+               _lib.lib().cp_tree_attn_workspace_size(R, B, max_new, words, prefix_len, N, Nkv, D, page_size, max_pages,
+                                                      ctypes.byref(n)))
+    return n.value
+
+
 def _prefix_call(name, more, q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale,
-                 o_dtype, o, lse, workspace, stream):
+                 o_dtype, o, lse, workspace, stream, mask=None):
     n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
     if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be contiguous bf16 [R, N, D]")
@@ -700,13 +840,20 @@ def _prefix_call(name, more, q, k_cache, v_cache, prefix_pages, prefix_len, tabl
         lse = _new((N, R), torch.float32, q.device, stream)
     elif lse.shape != (N, R) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [N, R]")
+    tree = ()
+    if mask is not None:
+        if len(mask.shape) != 2:
+            raise ValueError("mask must be [R, words]")
+        _check_list(mask, (R, mask.shape[1]), "mask")
+        tree = (_addr(mask), mask.shape[1])
     if workspace is None:
-        workspace = _scratch(max(256, cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page,
-                                                                    max_pages)), q.device, stream)
-    dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, o, lse, workspace)
+        need = (cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page, max_pages) if mask is None else
+                cp_tree_attn_workspace_size(R, B, max_new, mask.shape[1], prefix_len, N, Nkv, D, page, max_pages))
+        workspace = _scratch(max(256, need), q.device, stream)
+    dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, mask, o, lse, workspace)
     st = getattr(_lib.lib(), name)(_addr(q), _addr(k_cache), _addr(v_cache), n_pages, page, _addr(prefix_pages),
-                                   prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), max_new, R, N,
-                                   Nkv, D, scale, _addr(o), _dtype_code(o), _addr(lse), _addr(workspace),
+                                   prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), *tree, max_new,
+                                   R, N, Nkv, D, scale, _addr(o), _dtype_code(o), _addr(lse), _addr(workspace),
                                    workspace.numel() * workspace.element_size(), *more, _raw_stream(stream, dev))
     _lib.check(name, st)
     return o, lse
@@ -719,6 +866,16 @@ def cp_prefix_attn_fwd(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_
     largest number of new tokens of a sequence (chooses the tiles only)."""
     return _prefix_call("cp_prefix_attn_fwd", (), q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len,
                         max_new, scale, o_dtype, o, lse, workspace, stream)
+
+
+def cp_tree_attn_fwd(q, k_cache, v_cache, mask, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale=None,
+                     o_dtype=CP_BF16, o=None, lse=None, workspace=None, stream=None):
+    """cp_prefix_attn_fwd for drafted trees: of its sequence's new tokens a row sees those whose bits its row of
+    mask int32 [R,words] has (cp_tree_plan) -> (o [R,N,D], lse fp32 [N,R])."""
+    if mask is None:
+        raise ValueError("mask must be contiguous int32 [R, words]")
+    return _prefix_call("cp_tree_attn_fwd", (), q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len,
+                        max_new, scale, o_dtype, o, lse, workspace, stream, mask)
 
 
 def cp_selftest_stalled_prefix_attn(timeout_ns, q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len,

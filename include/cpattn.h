@@ -620,6 +620,110 @@ cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, const void *v_c
                              cudaStream_t stream);
 
 /*
+ * cp_cache_plan -- the pages and slots of a step, from the sequences' lengths (no counterpart on the
+ * pages).  Sequence b has pages for kv_had[b] tokens, of which the first kv_keep[b] stay (all, without
+ * rejected drafts; none, when it has ended), and gets n_new[b] new ones:
+ *   kv_len[b] = kv_keep[b] + n_new[b], cu_new = running sum of n_new.
+ * The pages behind ceil(kv_len / page_size) are pushed on the stack of free pages, in the order of (sequence,
+ * index); then the missing ones are popped in the same order and written into the table.  Row r of sequence
+ * b (r = cu_new[b] + j) gets own index i = kv_keep[b] + j,
+ *   slots[r] = table[b][i / page_size] * page_size + i % page_size,  pos[r] = pos_base + i;
+ * rows from cu_new[B] up to R get slot -1 and position 0.  The results feed cp_cache_append(_at) and the
+ * attention calls as they are; the next step's kv_had is this step's kv_len.
+ *   kv_had, kv_keep, n_new : device int32 [B]
+ *   table      : device int32 [B][max_pages]; new pages are written, the others read
+ *   free_pages : device int32 [n_pages], the stack; n_free[0] (device int32) of them lie on it.  Entries
+ *                behind the new top are unspecified.
+ *   R          : rows of slots and pos, at least the sum of n_new
+ *   kv_len     : device int32 [B], may be kv_had or kv_keep;  cu_new : device int32 [B+1]
+ *   slots, pos : device int32 [R]
+ *   n_free_out : device int32 [2], may be n_free: {free pages, 0}; where too few pages are free, {free pages,
+ *                pages lacking}, and nothing is handed out or given back: cu_new is 0, every slot -1, kv_len is
+ *                kv_had, stack and table stay
+ * All lists apart from one another otherwise (CP_ERR_ARGUMENT else).  A count below zero, kv_keep over
+ * kv_had, a length past the table, more than R new tokens or a stack that does not fit n_pages sets the device
+ * status word to CP_ERR_PAGE and hands nothing out (n_free_out[1] = -1); so does a page number out of range, whose
+ * rows get slot -1.  Sizes as for cp_cache_append.
+ */
+cp_status cp_cache_plan(const int32_t *kv_had, const int32_t *kv_keep, const int32_t *n_new, int64_t B, int32_t *table,
+                        int64_t max_pages, int64_t page_size, int32_t *free_pages, int64_t n_pages,
+                        const int32_t *n_free, int64_t pos_base, int64_t R, int32_t *kv_len, int32_t *cu_new,
+                        int32_t *slots, int32_t *pos, int32_t *n_free_out, cudaStream_t stream);
+
+/*
+ * cp_cache_append_at -- cp_cache_append with the slot and the position of every row given as lists, for
+ * tokens whose position is not their index (drafted trees: siblings share one).
+ *   slots : device int32 [R], the row's slot (page * page_size + offset), -1: the row is skipped, in
+ *           q_out too.  A slot out of range is skipped and sets the device status word to CP_ERR_PAGE.
+ *           Two rows must not share a slot.
+ *   pos   : device int32 [R], any value (read without a rotation too)
+ * Everything else as for cp_cache_append.
+ */
+cp_status cp_cache_append_at(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, cp_dtype dtype, int64_t R, int64_t N, int64_t Nkv, int64_t D,
+                             const void *wq, const void *wk, cp_dtype w_dtype, float eps, const cp_rope *rope,
+                             void *k_cache, void *v_cache, int64_t n_pages, int64_t page_size, const int32_t *slots,
+                             const int32_t *pos, void *q_out, cudaStream_t stream);
+
+/*
+ * cp_cache_keep -- after a drafted tree has been verified: the accepted branch's rows, moved together behind the
+ * cached tokens in the caches of all layers.  In each cache the row of own index first + kept[b][j] goes to
+ * first + j (j < n_kept[b], first = kv_len[b] - n_b), and
+ *   kv_keep[b] = first + n_kept[b], or kv_len[b] where n_kept[b] < 0 (all new tokens stay: a prompt, single tokens).
+ *   caches : host array of n_caches (1 .. 256) device pointers, each bf16 [n_pages][page_size][Nkv][D], apart
+ *            from one another: K and V of every layer
+ *   table, cu_new, kv_len, B, max_pages : of the step, as cp_cache_append and the attention read them
+ *   R      : the step's rows (cu_new is checked against it)
+ *   kept   : device int32 [B][max_kept] (max_kept 1 .. 512), rising, each below n_b
+ *   n_kept : device int32 [B], up to n_b and max_kept
+ *   kv_keep: device int32 [B], written, apart from the lists that are read: the next cp_cache_plan's kv_keep,
+ *            beside kv_had = kv_len
+ * A path ends before its first entry that does not rise, is out of range, or whose page number is; an n_kept out of
+ * range keeps nothing; where cu_new or kv_len makes no sense kv_keep is kv_len.  Each sets the device status
+ * word to CP_ERR_PAGE.
+ */
+cp_status cp_cache_keep(void *const *caches, int64_t n_caches, int64_t n_pages, int64_t page_size, int64_t Nkv,
+                        int64_t D, const int32_t *table, int64_t B, int64_t max_pages, const int32_t *cu_new,
+                        const int32_t *kv_len, int64_t R, const int32_t *kept, int64_t max_kept, const int32_t *n_kept,
+                        int32_t *kv_keep, cudaStream_t stream);
+
+/*
+ * cp_tree_plan -- ancestors and positions of drafted trees.  The new tokens of sequence b (rows cu_new[b]
+ * .. cu_new[b+1]-1) form trees: parent[r] is the place among them of row r's parent, below its own place, or -1
+ * for a token that follows the cached ones.
+ *   mask[r] : bits of r's ancestors and of r itself, bit i % 32 of word i / 32 for new token i
+ *   pos[r]  : pos_base + kv_len[b] - n_b + depth, the depth of a token without a parent being 0
+ * A sequence of more than 32 words new tokens is a prompt: its positions count up, its parents are not
+ * read and its mask rows not written.
+ *   parent : device int32 [R];  cu_new [B+1], kv_len [B] as for cp_cache_append
+ *   mask   : device int32 [R][words], words 1 .. 16;  pos : device int32 [R]; rows from cu_new[B] on stay.
+ *            Apart from one another and from the lists that are read (CP_ERR_ARGUMENT else)
+ * A parent out of range counts as -1 and sets the device status word to CP_ERR_PAGE; so do counts that make no
+ * sense, whose rows stay.
+ */
+cp_status cp_tree_plan(const int32_t *parent, const int32_t *cu_new, const int32_t *kv_len, int64_t B, int64_t R,
+                       int64_t words, int64_t pos_base, int32_t *mask, int32_t *pos, cudaStream_t stream);
+
+/*
+ * cp_tree_attn_workspace_size / cp_tree_attn_fwd -- cp_prefix_attn_fwd for drafted trees: a row sees the prefix, the
+ * kv_len[b] - n_b cached tokens of its sequence, and those of its sequence's new tokens whose bits its mask
+ * has (cp_tree_plan's, or any others; bits from n_b on are not looked at).
+ *   mask : device int32 [R][words], words 1 .. 16.  Sequences of more than 32 words new tokens are prompts, causal as
+ *          in cp_prefix_attn_fwd, their mask rows not read: trees and prompts mix in one batch.
+ * Everything else as for cp_prefix_attn_fwd, but that a NaN or infinity in any V row of a sequence's own keys may
+ * reach its other rows (also one that no row's mask has).
+ */
+cp_status cp_tree_attn_workspace_size(int64_t R, int64_t B, int64_t max_new, int64_t words, int64_t prefix_len,
+                                      int64_t N, int64_t Nkv, int64_t D, int64_t page_size, int64_t max_pages,
+                                      size_t *bytes);
+cp_status cp_tree_attn_fwd(const void *q, const void *k_cache, const void *v_cache, int64_t n_pages, int64_t page_size,
+                           const int32_t *prefix_pages, int64_t prefix_len, const int32_t *table, int64_t B,
+                           int64_t max_pages, const int32_t *cu_new, const int32_t *kv_len, const int32_t *mask,
+                           int64_t words, int64_t max_new, int64_t R, int64_t N, int64_t Nkv, int64_t D, float scale,
+                           void *o, cp_dtype o_dtype, float *lse, void *workspace, size_t ws_bytes,
+                           cudaStream_t stream);
+
+/*
  * cp_selftest_stalled_producer -- failure-detection self-test of the bounded
  * device-side waits (no counterpart on the pages).  Launches the attention
  * kernel on a [1][128][1][64] problem (q, k, v device bf16 [128][64], pos
