@@ -25,8 +25,9 @@ namespace cpattn {
 namespace {
 
 // ---------------------------------------------------------------- pages of a step
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanBlocks = 8;  // of the cluster, at most
+constexpr int kPlanThreads = 1024;  // of a block, at most
+constexpr int kPlanBlocks = 8;      // of the cluster, at most
+constexpr int kRowsEach = 4;        // neighbouring rows of a thread
 
 struct PlanArgs {
     const int32_t *had, *keep, *n_new;
@@ -35,6 +36,7 @@ struct PlanArgs {
     int B, max_pages, n_pages, shift, R;
     long long pos_base;
     int32_t *kv_len, *cu, *slots, *pos, *n_free_out;
+    int vectors;  // slots and pos lie on 16 bytes
     int *status;
 };
 
@@ -44,6 +46,16 @@ __device__ __forceinline__ int cluster_rank() {
     int r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
+}
+
+// A barrier of the cluster, behind which its writes so far are seen.
+__device__ __forceinline__ void all_read(int blocks) {
+    if (blocks == 1) {
+        __syncthreads();
+    } else {
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 // The last entry of sums[0 .. n - 1] (non-decreasing, sums[0] = 0) that is at most v.
@@ -64,7 +76,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     __shared__ long long warp_sum[kPlanThreads / 32][3];
     wait_for_previous();
     launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, each = (a.B + kPlanThreads - 1) / kPlanThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, each = (a.B + blockDim.x - 1) / blockDim.x;
     const int P1 = (1 << a.shift) - 1, blocks = gridDim.x, rank = cluster_rank();
     const long long most = static_cast<long long>(a.max_pages) << a.shift;
     const int free0 = __ldcg(a.n_free);
@@ -112,7 +124,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         long long v[3], w[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-            const long long mine = lane < kPlanThreads / 32 ? warp_sum[lane][i] : 0;
+            const long long mine = lane < blockDim.x / 32 ? warp_sum[lane][i] : 0;
             v[i] = lane < warp ? mine : 0;
             w[i] = mine;
         }
@@ -131,11 +143,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     }
     if (all[0] > a.R || free0 + all[2] > a.n_pages) bad = true;
     const long long lacking = all[1] - (free0 + all[2]);
-    const int gx = rank * kPlanThreads + tid, step = blocks * kPlanThreads;
+    const int gx = rank * blockDim.x + tid, step = blocks * blockDim.x;
     if (bad || lacking > 0) {
         // nothing is handed out: no new rows, the lengths and pages as they were
-        cluster_arrive();
-        cluster_wait();
+        all_read(blocks);
         for (int r = gx; r < a.R; r += step) {
             a.slots[r] = -1;
             a.pos[r] = 0;
@@ -184,26 +195,49 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         a.free_pages[free0 + k] = __ldcg(a.table + static_cast<long long>(b) * a.max_pages + owned[b] - n + k - gives[b]);
     }
     // every block has read the lists, and what was given lies on the stack
-    cluster_arrive();
-    cluster_wait();
+    all_read(blocks);
     bool wrong = false;
     for (int k = gx; k < taken; k += step) {
         const int b = place_in(takes, a.B, k), page = __ldcg(a.free_pages + top - 1 - k);
         wrong |= page < 0 || page >= a.n_pages;
         a.table[static_cast<long long>(b) * a.max_pages + owned[b] + k - takes[b]] = page;
     }
-    for (int r = gx; r < a.R; r += step) {
-        int slot = -1, at = 0;
-        if (r < total) {
-            const int b = place_in(rows, a.B, r), i = stays[b] + r - rows[b], e = i >> a.shift;
-            const int page = e < owned[b] ? __ldcg(a.table + static_cast<long long>(b) * a.max_pages + e)
-                                          : __ldcg(a.free_pages + top - 1 - (takes[b] + e - owned[b]));
-            at = static_cast<int>(a.pos_base + i);
-            if (page >= 0 && page < a.n_pages) slot = (page << a.shift) + (i & P1);
-            else wrong = true;
+    for (int r0 = gx * kRowsEach; r0 < a.R; r0 += step * kRowsEach) {
+        int slot[kRowsEach], at[kRowsEach], page[kRowsEach];
+        int b = r0 < total ? place_in(rows, a.B, r0) : 0;
+#pragma unroll
+        for (int k = 0; k < kRowsEach; ++k) {
+            const int r = r0 + k;
+            slot[k] = -1;
+            at[k] = 0;
+            if (r < total) {
+                while (b + 1 < a.B && rows[b + 1] <= r) ++b;
+                const int i = stays[b] + r - rows[b], e = i >> a.shift;
+                const int32_t *where = e < owned[b] ? a.table + static_cast<long long>(b) * a.max_pages + e
+                                                    : a.free_pages + (top - 1 - (takes[b] + e - owned[b]));
+                page[k] = __ldcg(where);
+                at[k] = static_cast<int>(a.pos_base + i);
+                slot[k] = i & P1;
+            }
         }
-        a.slots[r] = slot;
-        a.pos[r] = at;
+#pragma unroll
+        for (int k = 0; k < kRowsEach; ++k)
+            if (r0 + k < total) {
+                const bool fine = page[k] >= 0 && page[k] < a.n_pages;
+                slot[k] = fine ? (page[k] << a.shift) + slot[k] : -1;
+                wrong |= !fine;
+            }
+        if (a.vectors && r0 + kRowsEach <= a.R) {
+            *reinterpret_cast<int4 *>(a.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(a.pos + r0) = make_int4(at[0], at[1], at[2], at[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kRowsEach; ++k)
+                if (r0 + k < a.R) {
+                    a.slots[r0 + k] = slot[k];
+                    a.pos[r0 + k] = at[k];
+                }
+        }
     }
     if (wrong) atomicExch(a.status, static_cast<int>(CP_ERR_PAGE));
     if (rank == 0) {
@@ -227,7 +261,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 constexpr int kKeepThreads = 256;
 constexpr int kMaxCaches = 256;  // K and V of 128 layers: their addresses are launch arguments
 constexpr int kMaxKept = 512;    // tokens of a path: as many as a mask's row holds
-constexpr int kAhead = 8;        // rows in flight of a thread
+constexpr int kAhead = 4;        // rows in flight of a thread, of each of two columns
 
 struct KeepArgs {
     PageTable pt;
@@ -245,6 +279,10 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
     wait_for_previous();
     launch_dependents();
     const int b = blockIdx.x, tid = threadIdx.x;
+    const int32_t *path = a.kept + static_cast<long long>(b) * a.most;
+    // (the beginning of the path is read beside the counts that say how long it is)
+    const int at0 = tid < a.most ? __ldcg(path + tid) : 0;
+    const int last0 = tid && tid < a.most ? __ldcg(path + tid - 1) : -1;
     const int begin = __ldcg(a.cu + b), n = __ldcg(a.cu + b + 1) - begin, len = __ldcg(a.kv_len + b);
     int count = __ldcg(a.n_kept + b);
     const bool senseless = begin < 0 || n < 0 || n > a.R - begin || len < n;  // the lists
@@ -256,8 +294,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
     __syncthreads();
     // the kept tokens, rising; the first that is not ends the path
     for (int j = tid; j < count; j += kKeepThreads) {
-        const int32_t *path = a.kept + static_cast<long long>(b) * a.most;
-        const int at = __ldcg(path + j), last = j ? __ldcg(path + j - 1) : -1;
+        const int at = j == tid ? at0 : __ldcg(path + j), last = j == tid ? last0 : __ldcg(path + j - 1);
         const bool fine = at > last && last >= -1 && at < n;
         const long long s = fine ? a.pt.slot(b, static_cast<long long>(first) + at) : -1;
         const long long t = fine ? a.pt.slot(b, static_cast<long long>(first) + j) : -1;
@@ -272,20 +309,29 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
     count = end;
     if (bad) atomicExch(a.status, static_cast<int>(CP_ERR_PAGE));
     if (blockIdx.y == 0 && tid == 0) a.kv_keep[b] = whole ? len : first + count;
+    // the tokens that stay where they are come first: the path rises
+    int j1 = 0;
+    while (j1 < count && from[j1] == to[j1]) ++j1;
     const int u1 = min((static_cast<int>(blockIdx.y) + 1) * a.units, a.caches * a.cols);
-    for (int u = blockIdx.y * a.units + tid; u < u1; u += kKeepThreads) {
-        const int c = u / a.cols, piece = u - c * a.cols;
-        uint4 *cache = a.cache[c] + piece;
-        for (int j0 = 0; j0 < count; j0 += kAhead) {
-            uint4 v[kAhead];
+    for (int u = blockIdx.y * a.units + tid; u < u1; u += 2 * kKeepThreads) {
+        uint4 *column[2];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (j0 + k < count && from[j0 + k] != to[j0 + k])
-                    v[k] = __ldcg(cache + static_cast<long long>(from[j0 + k]) * a.cols);
+        for (int i = 0; i < 2; ++i) {
+            const int v = u + i * kKeepThreads, c = v < u1 ? v / a.cols : 0;
+            column[i] = v < u1 ? a.cache[c] + (v - c * a.cols) : nullptr;
+        }
+        for (int j0 = j1; j0 < count; j0 += kAhead) {
+            uint4 v[2][kAhead];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (j0 + k < count && from[j0 + k] != to[j0 + k])
-                    cache[static_cast<long long>(to[j0 + k]) * a.cols] = v[k];
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (column[i] && j0 + k < count) v[i][k] = __ldcg(column[i] + static_cast<long long>(from[j0 + k]) * a.cols);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (column[i] && j0 + k < count) column[i][static_cast<long long>(to[j0 + k]) * a.cols] = v[i][k];
         }
     }
 }
@@ -347,11 +393,17 @@ extern "C" cp_status cp_cache_plan(const int32_t *kv_had, const int32_t *kv_keep
     static const cudaError_t err =
         cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSequences * 5 * 4);
     if (err != cudaSuccess) return cuda_status(err);
-    int blocks = 1;
-    while (blocks < kPlanBlocks && static_cast<int64_t>(blocks) * kPlanThreads < R) blocks *= 2;
+    a.vectors = aligned16(slots) && aligned16(pos);
+    // Four sequences a thread at most, and a thread for four rows: up to 2048 rows by a larger block, up to 16384 by more
+    // blocks, each of which forms all sums, then by larger ones again.
+    int threads = 128, blocks = 1;
+    auto rows = [&] { return static_cast<int64_t>(blocks) * threads * kRowsEach; };
+    while (threads < kPlanThreads && (threads * 4 < B || (threads < 512 && rows() < R))) threads *= 2;
+    while (blocks < kPlanBlocks && rows() < R) blocks *= 2;
+    while (threads < kPlanThreads && rows() < R) threads *= 2;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(blocks);
-    c.blockDim = dim3(kPlanThreads);
+    c.blockDim = dim3(threads);
     c.dynamicSmemBytes = smem;
     c.stream = stream;
     cudaLaunchAttribute at[2] = {};
@@ -408,8 +460,13 @@ extern "C" cp_status cp_cache_keep(void *const *caches, int64_t n_caches, int64_
     a.cols = static_cast<int>(Nkv * D / 8);
     if ((st = cache_status_word(&a.status)) != CP_OK) return st;
     const int64_t all = n_caches * a.cols;
-    const int64_t rounds = (all + kKeepThreads * 4096 - 1) / (kKeepThreads * 4096);
-    a.units = static_cast<int>(kKeepThreads * rounds);
+    // As many rounds of two columns a thread as leave about four blocks an SM (what a block does first costs it
+    // three loads in a row).
+    const int64_t pairs = (all + 2 * kKeepThreads - 1) / (2 * kKeepThreads);
+    int64_t most = (4LL * sm_count() + B - 1) / B;
+    most = most < pairs ? most : pairs;
+    most = most < 4096 ? most : 4096;
+    a.units = static_cast<int>((pairs + most - 1) / most * 2 * kKeepThreads);
     const int64_t parts = (all + a.units - 1) / a.units;
     return launch(keep_kernel, dim3(static_cast<unsigned>(B), static_cast<unsigned>(parts)), kKeepThreads, 0, stream, a);
 }
