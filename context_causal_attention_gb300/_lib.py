@@ -126,11 +126,20 @@ def lib():
     L.cp_tree_attn_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
     L.cp_tree_attn_fwd.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, i64, i64, i64, i64,
                                    i64, f32, vp, i32, vp, vp, sz, vp]
+    L.cp_packed_call.argtypes = [i32, ctypes.c_char_p]  # csrc/packed.cu
+    L.cp_packed_call.restype = ctypes.c_int
     for name in header_symbols():
         if name not in ("cp_status_string", "cp_version", "cp_last_cuda_error"):
             getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
+
+
+def packed(which, fn, layout, *words):
+    """A call with its arguments in one array (csrc/packed.cu); `layout` packs them (no pointer: 0)."""
+    status = (_lib or lib()).cp_packed_call(which, layout(*words))
+    if status != CP_OK:
+        check(fn, status)
 
 
 def check(fn, status):

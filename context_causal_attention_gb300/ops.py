@@ -8,6 +8,7 @@ orders the streams.  All arithmetic happens in the CUDA library.
 """
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -423,7 +424,8 @@ class CpRope:
         if freqs.dtype != torch.int64 or not freqs.is_contiguous() or 2 * freqs.numel() < rot_dim:
             raise ValueError("freqs must be contiguous int64 [rot_dim / 2]")
         self._freqs, self._rest = freqs, (rot_dim, order, amplitude)
-        self._ref = ctypes.byref(RopeStruct(freqs.data_ptr(), rot_dim, order, amplitude))
+        self._struct = RopeStruct(freqs.data_ptr(), rot_dim, order, amplitude)
+        self._ref, self._at = ctypes.byref(self._struct), ctypes.addressof(self._struct)
 
     # read only: calls use the struct above
     freqs = property(lambda self: self._freqs)
@@ -640,17 +642,32 @@ def _check_cache(k_cache, v_cache, table, cu_new, kv_len):
     return (*shape, *tab)
 
 
+def _token_step(t, R, H, D):
+    """Elements between the tokens of [R, H, D], whose head rows are dense (as _head_rows)."""
+    a, b, c = t.stride()
+    if c != 1 or (b != D and H > 1):
+        raise ValueError("the head rows of a token must be dense")
+    if R == 1:
+        return H * D
+    if a == 0:
+        raise ValueError("tokens must lie at one distance from one another")
+    return a
+
+
 def _append_rows(k, v, q, q_out, Nkv, D, stream):
     """(R, N, strides of q, k and v, q_out) of the new tokens' rows."""
     shape, dtype = k.shape, k.dtype
     if len(shape) != 3 or v.shape != shape or shape[1] != Nkv or shape[2] != D or v.dtype is not dtype:
         raise ValueError("k and v must be [R, Nkv, D] of the cache's heads, of one dtype")
-    ks, vs = _head_rows(k)[0], _head_rows(v)[0]
     R, qs, N = shape[0], 0, 0
+    ks, vs = _token_step(k, R, Nkv, D), _token_step(v, R, Nkv, D)
     if q is not None:
-        qs, lead, N, Dq = _head_rows(q)
-        if lead != shape[:1] or Dq != D or q.dtype is not dtype:
+        if q.dim() != 3:
             raise ValueError("q must be [R, N, D] of k's tokens and dtype")
+        Rq, N, Dq = q.shape
+        if Rq != R or Dq != D or q.dtype is not dtype:
+            raise ValueError("q must be [R, N, D] of k's tokens and dtype")
+        qs = _token_step(q, R, N, D)
         if q_out is None:
             q_out = _new((R, N, D), torch.bfloat16, q.device, stream)
         elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous():
@@ -678,17 +695,34 @@ def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=
     return q_out
 
 
-def _check_list(t, shape, what):
-    """A list that a call reads or writes: contiguous int32 of `shape`."""
-    if t.shape != shape or t.dtype is not torch.int32 or not t.is_contiguous():
-        raise ValueError("%s must be contiguous int32 %s" % (what, list(shape)))
+_I32, _BF16 = torch.int32, torch.bfloat16
+_at = torch.Tensor.data_ptr
+
+# The arguments of the calls that go in one array (csrc/packed.cu), in the header's order.
+_PLAN_WORDS = struct.Struct("18q").pack
+_APPEND_AT_WORDS = struct.Struct("14qd9q").pack
+_KEEP_WORDS = struct.Struct("17q").pack
+_TREE_WORDS = struct.Struct("10q").pack
+_ATTN_WORDS = struct.Struct("19qd6q").pack
 
 
-def _list_out(t, shape, what, device, stream):
+def _list(t, n, dev, what):
+    """Address of a list that a call reads or writes: n contiguous int32 on device `dev`.  (One that is missing is the
+    library's to refuse.)"""
     if t is None:
-        return _new(shape, torch.int32, device, stream)
-    _check_list(t, shape, what)
-    return t
+        return 0
+    if t.dtype is not _I32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous int32 of %d values" % (what, n))
+    if t.get_device() != dev:
+        raise ValueError("the tensors of a call must be on one device")
+    return _at(t)
+
+
+def _stream_here(stream, dev):
+    """_raw_stream, where `dev` is the current device."""
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensor must be on the current CUDA device")
+    return _raw_stream(stream, dev)
 
 
 def cp_cache_plan(kv_had, kv_keep, n_new, table, free_pages, n_free, page_size, R, pos_base=0, kv_len=None, cu_new=None,
@@ -696,25 +730,26 @@ def cp_cache_plan(kv_had, kv_keep, n_new, table, free_pages, n_free, page_size, 
     """Pages and slots of a step from the sequences' lengths (see the C header): page numbers go between
     table [B,max_pages] and the stack free_pages [n_pages].  Returns (kv_len [B], cu_new [B+1], slots [R],
     pos [R], n_free_out [2]), all int32."""
-    tab, n_pages = table.shape, free_pages.shape
-    if len(tab) != 2 or len(n_pages) != 1:
-        raise ValueError("expected table [B, max_pages] and free_pages [n_pages]")
-    B = tab[0]
-    for t, shape, what in ((table, tab, "table"), (free_pages, n_pages, "free_pages"), (kv_had, (B,), "kv_had"),
-                           (kv_keep, (B,), "kv_keep"), (n_new, (B,), "n_new")):
-        _check_list(t, shape, what)
-    if n_free.dtype is not torch.int32 or n_free.numel() < 1 or not n_free.is_contiguous():
-        raise ValueError("n_free must be contiguous int32 [1] or [2]")
-    dev = table.device
-    kv_len = _list_out(kv_len, (B,), "kv_len", dev, stream)
-    cu_new = _list_out(cu_new, (B + 1,), "cu_new", dev, stream)
-    slots, pos = _list_out(slots, (R,), "slots", dev, stream), _list_out(pos, (R,), "pos", dev, stream)
-    n_free_out = _list_out(n_free_out, (2,), "n_free_out", dev, stream)
-    cur = _here(kv_had, kv_keep, n_new, table, free_pages, n_free, kv_len, cu_new, slots, pos, n_free_out)
-    st = _lib.lib().cp_cache_plan(_addr(kv_had), _addr(kv_keep), _addr(n_new), B, _addr(table), tab[1], page_size,
-                                  _addr(free_pages), n_pages[0], _addr(n_free), pos_base, R, _addr(kv_len),
-                                  _addr(cu_new), _addr(slots), _addr(pos), _addr(n_free_out), _raw_stream(stream, cur))
-    _lib.check("cp_cache_plan", st)
+    if table.dim() != 2:
+        raise ValueError("expected table [B, max_pages]")
+    B, most = table.shape
+    n_pages, dev = free_pages.numel(), table.get_device()
+    if kv_len is None:
+        kv_len = _new(B, _I32, table.device, stream)
+    if cu_new is None:
+        cu_new = _new(B + 1, _I32, table.device, stream)
+    if slots is None:
+        slots = _new(R, _I32, table.device, stream)
+    if pos is None:
+        pos = _new(R, _I32, table.device, stream)
+    if n_free_out is None:
+        n_free_out = _new(2, _I32, table.device, stream)
+    _lib.packed(0, "cp_cache_plan", _PLAN_WORDS, _list(kv_had, B, dev, "kv_had"), _list(kv_keep, B, dev, "kv_keep"),
+                _list(n_new, B, dev, "n_new"), B, _list(table, B * most, dev, "table"), most, page_size,
+                _list(free_pages, n_pages, dev, "free_pages"), n_pages, _list(n_free, n_free.numel(), dev, "n_free"),
+                pos_base, R, _list(kv_len, B, dev, "kv_len"), _list(cu_new, B + 1, dev, "cu_new"),
+                _list(slots, R, dev, "slots"), _list(pos, R, dev, "pos"), _list(n_free_out, 2, dev, "n_free_out"),
+                _stream_here(stream, dev))
     return kv_len, cu_new, slots, pos, n_free_out
 
 
@@ -725,21 +760,21 @@ def cp_cache_append_at(k, v, k_cache, v_cache, slots, pos, rope=None, q=None, q_
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("the caches must be [n_pages, page_size, Nkv, D], both alike")
-    if k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16:
+    if k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16:
         raise TypeError("the caches must be bf16")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("tensor must be contiguous")
     n_pages, page, Nkv, D = shape
     R, N, qs, ks, vs, q_out = _append_rows(k, v, q, q_out, Nkv, D, stream)
-    _check_list(slots, (R,), "slots")
-    _check_list(pos, (R,), "pos")
     wd = _check_weights(wq, wk, D)
-    dev = _here(q, k, v, k_cache, v_cache, slots, pos, wq, wk, None if rope is None else rope.freqs, q_out)
-    st = _lib.lib().cp_cache_append_at(_addr(q), _addr(k), _addr(v), qs, ks, vs, _dtype_code(k), R, N, Nkv, D, _addr(wq),
-                                       _addr(wk), wd, eps, None if rope is None else rope._ref, _addr(k_cache),
-                                       _addr(v_cache), n_pages, page, _addr(slots), _addr(pos), _addr(q_out),
-                                       _raw_stream(stream, dev))
-    _lib.check("cp_cache_append_at", st)
+    dev = k.get_device()
+    slots, pos = _list(slots, R, dev, "slots"), _list(pos, R, dev, "pos")
+    _here(q, k, v, k_cache, v_cache, wq, wk, None if rope is None else rope._freqs, q_out)
+    _lib.packed(1, "cp_cache_append_at", _APPEND_AT_WORDS, 0 if q is None else _at(q), _at(k), _at(v), qs, ks, vs,
+                _dtype_code(k), R, N, Nkv, D, 0 if wq is None else _at(wq), 0 if wk is None else _at(wk), wd, eps,
+                0 if rope is None else rope._at, _at(k_cache), _at(v_cache), n_pages, page,
+                slots, pos, 0 if q_out is None else _at(q_out),
+                _raw_stream(stream, dev))
     return q_out
 
 
@@ -758,6 +793,7 @@ class CpCaches:
                 raise ValueError("the caches must be contiguous, all alike, on one device")
         self._caches = caches
         self._ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+        self._at, self._sizes = ctypes.addressof(self._ptrs), (len(caches), *caches[0].shape)
 
     # read only: calls use the addresses above
     caches = property(lambda self: self._caches)
@@ -769,37 +805,30 @@ def cp_cache_keep(caches, table, cu_new, kv_len, kept, n_kept, R=None, kv_keep=N
     Returns kv_keep int32 [B], the tokens that stay."""
     if not isinstance(caches, CpCaches):
         caches = CpCaches(caches)
-    n_pages, page, Nkv, D = caches.caches[0].shape
-    tab = table.shape
-    if len(tab) != 2 or len(kept.shape) != 2:
+    if table.dim() != 2 or kept.dim() != 2:
         raise ValueError("expected table [B, max_pages] and kept [B, max_kept]")
-    B = tab[0]
-    for t, shape, what in ((table, tab, "table"), (cu_new, (B + 1,), "cu_new"), (kv_len, (B,), "kv_len"),
-                           (kept, (B, kept.shape[1]), "kept"), (n_kept, (B,), "n_kept")):
-        _check_list(t, shape, what)
-    kv_keep = _list_out(kv_keep, (B,), "kv_keep", table.device, stream)
-    dev = _here(caches.caches[0], table, cu_new, kv_len, kept, n_kept, kv_keep)
-    st = _lib.lib().cp_cache_keep(caches._ptrs, len(caches.caches), n_pages, page, Nkv, D, _addr(table), B, tab[1],
-                                  _addr(cu_new), _addr(kv_len), (1 << 30) - 1 if R is None else R, _addr(kept),
-                                  kept.shape[1], _addr(n_kept), _addr(kv_keep), _raw_stream(stream, dev))
-    _lib.check("cp_cache_keep", st)
+    B, max_pages = table.shape
+    most, dev = kept.shape[1], caches.caches[0].get_device()
+    if kv_keep is None:
+        kv_keep = _new(B, _I32, table.device, stream)
+    _lib.packed(2, "cp_cache_keep", _KEEP_WORDS, caches._at, *caches._sizes, _list(table, B * max_pages, dev, "table"), B,
+                max_pages, _list(cu_new, B + 1, dev, "cu_new"), _list(kv_len, B, dev, "kv_len"),
+                (1 << 30) - 1 if R is None else R, _list(kept, B * most, dev, "kept"), most,
+                _list(n_kept, B, dev, "n_kept"), _list(kv_keep, B, dev, "kv_keep"), _stream_here(stream, dev))
     return kv_keep
 
 
 def cp_tree_plan(parent, cu_new, kv_len, words, pos_base=0, mask=None, pos=None, stream=None):
     """Ancestors and positions of drafted trees from each row's parent [R] among its sequence's new tokens (-1: it
     follows the cached ones) -> (mask int32 [R,words], pos int32 [R]); see the C header."""
-    if len(parent.shape) != 1 or len(kv_len.shape) != 1:
-        raise ValueError("expected parent [R] and kv_len [B]")
-    R, B = parent.shape[0], kv_len.shape[0]
-    for t, shape, what in ((parent, (R,), "parent"), (cu_new, (B + 1,), "cu_new"), (kv_len, (B,), "kv_len")):
-        _check_list(t, shape, what)
-    mask = _list_out(mask, (R, words), "mask", parent.device, stream)
-    pos = _list_out(pos, (R,), "pos", parent.device, stream)
-    dev = _here(parent, cu_new, kv_len, mask, pos)
-    st = _lib.lib().cp_tree_plan(_addr(parent), _addr(cu_new), _addr(kv_len), B, R, words, pos_base, _addr(mask),
-                                 _addr(pos), _raw_stream(stream, dev))
-    _lib.check("cp_tree_plan", st)
+    R, B, dev = parent.numel(), kv_len.numel(), parent.get_device()
+    if mask is None:
+        mask = _new((R, words), _I32, parent.device, stream)
+    if pos is None:
+        pos = _new(R, _I32, parent.device, stream)
+    _lib.packed(3, "cp_tree_plan", _TREE_WORDS, _list(parent, R, dev, "parent"), _list(cu_new, B + 1, dev, "cu_new"),
+                _list(kv_len, B, dev, "kv_len"), B, R, words, pos_base, _list(mask, R * words, dev, "mask"),
+                _list(pos, R, dev, "pos"), _stream_here(stream, dev))
     return mask, pos
 
 
@@ -819,9 +848,9 @@ def cp_tree_attn_workspace_size(R, B, max_new, words, prefix_len, N, Nkv, D, pag
     return n.value
 
 
-def _prefix_call(name, more, q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale,
-                 o_dtype, o, lse, workspace, stream, mask=None):
-    n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
+def _attn_rows(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, scale, o_dtype, o, lse, stream):
+    """What the attention calls over the cache check and make: (sizes of the cache and its lists, R, N, scale, o, lse)."""
+    n_pages, page, Nkv, D, B, max_pages = sizes = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
     if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be contiguous bf16 [R, N, D]")
     R, N = q.shape[0], q.shape[1]
@@ -840,20 +869,20 @@ def _prefix_call(name, more, q, k_cache, v_cache, prefix_pages, prefix_len, tabl
         lse = _new((N, R), torch.float32, q.device, stream)
     elif lse.shape != (N, R) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [N, R]")
-    tree = ()
-    if mask is not None:
-        if len(mask.shape) != 2:
-            raise ValueError("mask must be [R, words]")
-        _check_list(mask, (R, mask.shape[1]), "mask")
-        tree = (_addr(mask), mask.shape[1])
+    return sizes, R, N, scale, o, lse
+
+
+def _prefix_call(name, more, q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale,
+                 o_dtype, o, lse, workspace, stream):
+    (n_pages, page, Nkv, D, B, max_pages), R, N, scale, o, lse = _attn_rows(
+        q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, scale, o_dtype, o, lse, stream)
     if workspace is None:
-        need = (cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page, max_pages) if mask is None else
-                cp_tree_attn_workspace_size(R, B, max_new, mask.shape[1], prefix_len, N, Nkv, D, page, max_pages))
-        workspace = _scratch(max(256, need), q.device, stream)
-    dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, mask, o, lse, workspace)
+        workspace = _scratch(max(256, cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page,
+                                                                    max_pages)), q.device, stream)
+    dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, o, lse, workspace)
     st = getattr(_lib.lib(), name)(_addr(q), _addr(k_cache), _addr(v_cache), n_pages, page, _addr(prefix_pages),
-                                   prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), *tree, max_new,
-                                   R, N, Nkv, D, scale, _addr(o), _dtype_code(o), _addr(lse), _addr(workspace),
+                                   prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), max_new, R, N,
+                                   Nkv, D, scale, _addr(o), _dtype_code(o), _addr(lse), _addr(workspace),
                                    workspace.numel() * workspace.element_size(), *more, _raw_stream(stream, dev))
     _lib.check(name, st)
     return o, lse
@@ -872,10 +901,22 @@ def cp_tree_attn_fwd(q, k_cache, v_cache, mask, prefix_pages, prefix_len, table,
                      o_dtype=CP_BF16, o=None, lse=None, workspace=None, stream=None):
     """cp_prefix_attn_fwd for drafted trees: of its sequence's new tokens a row sees those whose bits its row of
     mask int32 [R,words] has (cp_tree_plan) -> (o [R,N,D], lse fp32 [N,R])."""
-    if mask is None:
+    if mask is None or mask.dim() != 2:
         raise ValueError("mask must be contiguous int32 [R, words]")
-    return _prefix_call("cp_tree_attn_fwd", (), q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len,
-                        max_new, scale, o_dtype, o, lse, workspace, stream, mask)
+    (n_pages, page, Nkv, D, B, max_pages), R, N, scale, o, lse = _attn_rows(
+        q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, scale, o_dtype, o, lse, stream)
+    words = mask.shape[1]
+    mask = _list(mask, R * words, q.get_device(), "mask")
+    if workspace is None:
+        workspace = _scratch(max(256, cp_tree_attn_workspace_size(R, B, max_new, words, prefix_len, N, Nkv, D, page,
+                                                                  max_pages)), q.device, stream)
+    dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, o, lse, workspace)
+    _lib.packed(4, "cp_tree_attn_fwd", _ATTN_WORDS, _at(q), _at(k_cache), _at(v_cache), n_pages, page,
+                0 if prefix_pages is None else _at(prefix_pages), prefix_len, _at(table), B, max_pages, _at(cu_new),
+                _at(kv_len), mask, words, max_new, R, N, Nkv, D, scale, _at(o),
+                _dtype_code(o), _at(lse), _at(workspace), workspace.numel() * workspace.element_size(),
+                _raw_stream(stream, dev))
+    return o, lse
 
 
 def cp_selftest_stalled_prefix_attn(timeout_ns, q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len,
