@@ -5,11 +5,14 @@ tensors to pointers, sizes and stream handles.  There is no fallback: if the
 library is missing or fails to load, every call raises.
 """
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libcpattn.so")
+BIND_PATH = os.path.join(HERE, "_build", "_cpbind.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "cpattn.h")
 
 CP_OK = 0
@@ -41,6 +44,7 @@ class CpError(RuntimeError):
 
 
 _lib = None
+_bind = None
 
 
 def header_symbols():
@@ -126,8 +130,6 @@ def lib():
     L.cp_tree_attn_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
     L.cp_tree_attn_fwd.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, i64, i64, i64, i64,
                                    i64, f32, vp, i32, vp, vp, sz, vp]
-    L.cp_packed_call.argtypes = [i32, ctypes.c_char_p]  # csrc/packed.cu
-    L.cp_packed_call.restype = ctypes.c_int
     for name in header_symbols():
         if name not in ("cp_status_string", "cp_version", "cp_last_cuda_error"):
             getattr(L, name).restype = ctypes.c_int
@@ -135,11 +137,19 @@ def lib():
     return L
 
 
-def packed(which, fn, layout, *words):
-    """A call with its arguments in one array (csrc/packed.cu); `layout` packs them (no pointer: 0)."""
-    status = (_lib or lib()).cp_packed_call(which, layout(*words))
-    if status != CP_OK:
-        check(fn, status)
+def bind():
+    """Load the module of the short calls (csrc/bind.cpp), beside the library."""
+    global _bind
+    if _bind is None:
+        import torch  # noqa: F401  (its libraries come first)
+
+        lib()
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError("_cpbind.so not built (expected at %s); run __graft_entry__.build()" % BIND_PATH)
+        loader = importlib.machinery.ExtensionFileLoader("_cpbind", BIND_PATH)
+        _bind = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_cpbind", BIND_PATH, loader=loader))
+        loader.exec_module(_bind)
+    return _bind
 
 
 def check(fn, status):

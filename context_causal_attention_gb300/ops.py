@@ -8,7 +8,6 @@ orders the streams.  All arithmetic happens in the CUDA library.
 """
 import ctypes
 import math
-import struct
 
 import torch
 
@@ -642,41 +641,6 @@ def _check_cache(k_cache, v_cache, table, cu_new, kv_len):
     return (*shape, *tab)
 
 
-def _token_step(t, R, H, D):
-    """Elements between the tokens of [R, H, D], whose head rows are dense (as _head_rows)."""
-    a, b, c = t.stride()
-    if c != 1 or (b != D and H > 1):
-        raise ValueError("the head rows of a token must be dense")
-    if R == 1:
-        return H * D
-    if a == 0:
-        raise ValueError("tokens must lie at one distance from one another")
-    return a
-
-
-def _append_rows(k, v, q, q_out, Nkv, D, stream):
-    """(R, N, strides of q, k and v, q_out) of the new tokens' rows."""
-    shape, dtype = k.shape, k.dtype
-    if len(shape) != 3 or v.shape != shape or shape[1] != Nkv or shape[2] != D or v.dtype is not dtype:
-        raise ValueError("k and v must be [R, Nkv, D] of the cache's heads, of one dtype")
-    R, qs, N = shape[0], 0, 0
-    ks, vs = _token_step(k, R, Nkv, D), _token_step(v, R, Nkv, D)
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [R, N, D] of k's tokens and dtype")
-        Rq, N, Dq = q.shape
-        if Rq != R or Dq != D or q.dtype is not dtype:
-            raise ValueError("q must be [R, N, D] of k's tokens and dtype")
-        qs = _token_step(q, R, N, D)
-        if q_out is None:
-            q_out = _new((R, N, D), torch.bfloat16, q.device, stream)
-        elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous bf16 [R, N, D]")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    return R, N, qs, ks, vs, q_out
-
-
 def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=None, q_out=None, wq=None, wk=None,
                     eps=1e-6, pos_base=0, stream=None):
     """Append the new tokens' k, v [R,Nkv,D] to the pages of their sequences,
@@ -684,7 +648,21 @@ def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=
     q_out bf16 [R,N,D].  kv_len counts each sequence's tokens after the call.
     Returns q_out (None without q)."""
     n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
-    R, N, qs, ks, vs, q_out = _append_rows(k, v, q, q_out, Nkv, D, stream)
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or v.shape != shape or shape[1] != Nkv or shape[2] != D or v.dtype is not dtype:
+        raise ValueError("k and v must be [R, Nkv, D] of the cache's heads, of one dtype")
+    ks, vs = _head_rows(k)[0], _head_rows(v)[0]
+    R, qs, N = shape[0], 0, 0
+    if q is not None:
+        qs, lead, N, Dq = _head_rows(q)
+        if lead != shape[:1] or Dq != D or q.dtype is not dtype:
+            raise ValueError("q must be [R, N, D] of k's tokens and dtype")
+        if q_out is None:
+            q_out = _new((R, N, D), torch.bfloat16, q.device, stream)
+        elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous bf16 [R, N, D]")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
     wd = _check_weights(wq, wk, D)
     dev = _here(q, k, v, k_cache, v_cache, table, cu_new, kv_len, wq, wk, None if rope is None else rope.freqs, q_out)
     st = _lib.lib().cp_cache_append(_addr(q), _addr(k), _addr(v), qs, ks, vs, _dtype_code(k), R, N, Nkv, D, _addr(wq),
@@ -695,34 +673,11 @@ def cp_cache_append(k, v, k_cache, v_cache, table, cu_new, kv_len, rope=None, q=
     return q_out
 
 
-_I32, _BF16 = torch.int32, torch.bfloat16
-_at = torch.Tensor.data_ptr
-
-# The arguments of the calls that go in one array (csrc/packed.cu), in the header's order.
-_PLAN_WORDS = struct.Struct("18q").pack
-_APPEND_AT_WORDS = struct.Struct("14qd9q").pack
-_KEEP_WORDS = struct.Struct("17q").pack
-_TREE_WORDS = struct.Struct("10q").pack
-_ATTN_WORDS = struct.Struct("19qd6q").pack
+_I32 = torch.int32
 
 
-def _list(t, n, dev, what):
-    """Address of a list that a call reads or writes: n contiguous int32 on device `dev`.  (One that is missing is the
-    library's to refuse.)"""
-    if t is None:
-        return 0
-    if t.dtype is not _I32 or t.numel() != n or not t.is_contiguous():
-        raise ValueError("%s must be contiguous int32 of %d values" % (what, n))
-    if t.get_device() != dev:
-        raise ValueError("the tensors of a call must be on one device")
-    return _at(t)
-
-
-def _stream_here(stream, dev):
-    """_raw_stream, where `dev` is the current device."""
-    if dev != torch.cuda.current_device():
-        raise ValueError("tensor must be on the current CUDA device")
-    return _raw_stream(stream, dev)
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def cp_cache_plan(kv_had, kv_keep, n_new, table, free_pages, n_free, page_size, R, pos_base=0, kv_len=None, cu_new=None,
@@ -730,26 +685,20 @@ def cp_cache_plan(kv_had, kv_keep, n_new, table, free_pages, n_free, page_size, 
     """Pages and slots of a step from the sequences' lengths (see the C header): page numbers go between
     table [B,max_pages] and the stack free_pages [n_pages].  Returns (kv_len [B], cu_new [B+1], slots [R],
     pos [R], n_free_out [2]), all int32."""
-    if table.dim() != 2:
-        raise ValueError("expected table [B, max_pages]")
-    B, most = table.shape
-    n_pages, dev = free_pages.numel(), table.get_device()
     if kv_len is None:
-        kv_len = _new(B, _I32, table.device, stream)
+        kv_len = _new(table.shape[0], _I32, table.device, stream)
     if cu_new is None:
-        cu_new = _new(B + 1, _I32, table.device, stream)
+        cu_new = _new(table.shape[0] + 1, _I32, table.device, stream)
     if slots is None:
         slots = _new(R, _I32, table.device, stream)
     if pos is None:
         pos = _new(R, _I32, table.device, stream)
     if n_free_out is None:
         n_free_out = _new(2, _I32, table.device, stream)
-    _lib.packed(0, "cp_cache_plan", _PLAN_WORDS, _list(kv_had, B, dev, "kv_had"), _list(kv_keep, B, dev, "kv_keep"),
-                _list(n_new, B, dev, "n_new"), B, _list(table, B * most, dev, "table"), most, page_size,
-                _list(free_pages, n_pages, dev, "free_pages"), n_pages, _list(n_free, n_free.numel(), dev, "n_free"),
-                pos_base, R, _list(kv_len, B, dev, "kv_len"), _list(cu_new, B + 1, dev, "cu_new"),
-                _list(slots, R, dev, "slots"), _list(pos, R, dev, "pos"), _list(n_free_out, 2, dev, "n_free_out"),
-                _stream_here(stream, dev))
+    st = _lib.bind().cache_plan(table, free_pages, kv_had, kv_keep, n_new, n_free, page_size, R, pos_base, kv_len, cu_new,
+                                slots, pos, n_free_out, _handle(stream))
+    if st:
+        _lib.check("cp_cache_plan", st)
     return kv_len, cu_new, slots, pos, n_free_out
 
 
@@ -757,24 +706,12 @@ def cp_cache_append_at(k, v, k_cache, v_cache, slots, pos, rope=None, q=None, q_
                        stream=None):
     """cp_cache_append with the rows' slots and positions, int32 [R] each (slot -1: the row is skipped).
     Returns q_out (None without q)."""
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape:
-        raise ValueError("the caches must be [n_pages, page_size, Nkv, D], both alike")
-    if k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16:
-        raise TypeError("the caches must be bf16")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        raise ValueError("tensor must be contiguous")
-    n_pages, page, Nkv, D = shape
-    R, N, qs, ks, vs, q_out = _append_rows(k, v, q, q_out, Nkv, D, stream)
-    wd = _check_weights(wq, wk, D)
-    dev = k.get_device()
-    slots, pos = _list(slots, R, dev, "slots"), _list(pos, R, dev, "pos")
-    _here(q, k, v, k_cache, v_cache, wq, wk, None if rope is None else rope._freqs, q_out)
-    _lib.packed(1, "cp_cache_append_at", _APPEND_AT_WORDS, 0 if q is None else _at(q), _at(k), _at(v), qs, ks, vs,
-                _dtype_code(k), R, N, Nkv, D, 0 if wq is None else _at(wq), 0 if wk is None else _at(wk), wd, eps,
-                0 if rope is None else rope._at, _at(k_cache), _at(v_cache), n_pages, page,
-                slots, pos, 0 if q_out is None else _at(q_out),
-                _raw_stream(stream, dev))
+    if q is not None and q_out is None:
+        q_out = _new(q.shape, torch.bfloat16, q.device, stream)
+    at, freqs = (0, None) if rope is None else (rope._at, rope._freqs)
+    st = _lib.bind().cache_append_at(k, v, k_cache, v_cache, slots, pos, at, freqs, q, q_out, wq, wk, eps, _handle(stream))
+    if st:
+        _lib.check("cp_cache_append_at", st)
     return q_out
 
 
@@ -793,7 +730,7 @@ class CpCaches:
                 raise ValueError("the caches must be contiguous, all alike, on one device")
         self._caches = caches
         self._ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
-        self._at, self._sizes = ctypes.addressof(self._ptrs), (len(caches), *caches[0].shape)
+        self._words = (caches[0], ctypes.addressof(self._ptrs), len(caches), *caches[0].shape)
 
     # read only: calls use the addresses above
     caches = property(lambda self: self._caches)
@@ -805,30 +742,25 @@ def cp_cache_keep(caches, table, cu_new, kv_len, kept, n_kept, R=None, kv_keep=N
     Returns kv_keep int32 [B], the tokens that stay."""
     if not isinstance(caches, CpCaches):
         caches = CpCaches(caches)
-    if table.dim() != 2 or kept.dim() != 2:
-        raise ValueError("expected table [B, max_pages] and kept [B, max_kept]")
-    B, max_pages = table.shape
-    most, dev = kept.shape[1], caches.caches[0].get_device()
     if kv_keep is None:
-        kv_keep = _new(B, _I32, table.device, stream)
-    _lib.packed(2, "cp_cache_keep", _KEEP_WORDS, caches._at, *caches._sizes, _list(table, B * max_pages, dev, "table"), B,
-                max_pages, _list(cu_new, B + 1, dev, "cu_new"), _list(kv_len, B, dev, "kv_len"),
-                (1 << 30) - 1 if R is None else R, _list(kept, B * most, dev, "kept"), most,
-                _list(n_kept, B, dev, "n_kept"), _list(kv_keep, B, dev, "kv_keep"), _stream_here(stream, dev))
+        kv_keep = _new(table.shape[0], _I32, table.device, stream)
+    st = _lib.bind().cache_keep(*caches._words, table, cu_new, kv_len, (1 << 30) - 1 if R is None else R, kept, n_kept,
+                                kv_keep, _handle(stream))
+    if st:
+        _lib.check("cp_cache_keep", st)
     return kv_keep
 
 
 def cp_tree_plan(parent, cu_new, kv_len, words, pos_base=0, mask=None, pos=None, stream=None):
     """Ancestors and positions of drafted trees from each row's parent [R] among its sequence's new tokens (-1: it
     follows the cached ones) -> (mask int32 [R,words], pos int32 [R]); see the C header."""
-    R, B, dev = parent.numel(), kv_len.numel(), parent.get_device()
     if mask is None:
-        mask = _new((R, words), _I32, parent.device, stream)
+        mask = _new((parent.shape[0], words), _I32, parent.device, stream)
     if pos is None:
-        pos = _new(R, _I32, parent.device, stream)
-    _lib.packed(3, "cp_tree_plan", _TREE_WORDS, _list(parent, R, dev, "parent"), _list(cu_new, B + 1, dev, "cu_new"),
-                _list(kv_len, B, dev, "kv_len"), B, R, words, pos_base, _list(mask, R * words, dev, "mask"),
-                _list(pos, R, dev, "pos"), _stream_here(stream, dev))
+        pos = _new(parent.shape[0], _I32, parent.device, stream)
+    st = _lib.bind().tree_plan(parent, kv_len, cu_new, words, pos_base, mask, pos, _handle(stream))
+    if st:
+        _lib.check("cp_tree_plan", st)
     return mask, pos
 
 
@@ -848,9 +780,9 @@ def cp_tree_attn_workspace_size(R, B, max_new, words, prefix_len, N, Nkv, D, pag
     return n.value
 
 
-def _attn_rows(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, scale, o_dtype, o, lse, stream):
-    """What the attention calls over the cache check and make: (sizes of the cache and its lists, R, N, scale, o, lse)."""
-    n_pages, page, Nkv, D, B, max_pages = sizes = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
+def _prefix_call(name, more, q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale,
+                 o_dtype, o, lse, workspace, stream):
+    n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
     if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be contiguous bf16 [R, N, D]")
     R, N = q.shape[0], q.shape[1]
@@ -869,13 +801,6 @@ def _attn_rows(q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_
         lse = _new((N, R), torch.float32, q.device, stream)
     elif lse.shape != (N, R) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [N, R]")
-    return sizes, R, N, scale, o, lse
-
-
-def _prefix_call(name, more, q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale,
-                 o_dtype, o, lse, workspace, stream):
-    (n_pages, page, Nkv, D, B, max_pages), R, N, scale, o, lse = _attn_rows(
-        q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, scale, o_dtype, o, lse, stream)
     if workspace is None:
         workspace = _scratch(max(256, cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page,
                                                                     max_pages)), q.device, stream)
@@ -901,21 +826,22 @@ def cp_tree_attn_fwd(q, k_cache, v_cache, mask, prefix_pages, prefix_len, table,
                      o_dtype=CP_BF16, o=None, lse=None, workspace=None, stream=None):
     """cp_prefix_attn_fwd for drafted trees: of its sequence's new tokens a row sees those whose bits its row of
     mask int32 [R,words] has (cp_tree_plan) -> (o [R,N,D], lse fp32 [N,R])."""
-    if mask is None or mask.dim() != 2:
-        raise ValueError("mask must be contiguous int32 [R, words]")
-    (n_pages, page, Nkv, D, B, max_pages), R, N, scale, o, lse = _attn_rows(
-        q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, scale, o_dtype, o, lse, stream)
-    words = mask.shape[1]
-    mask = _list(mask, R * words, q.get_device(), "mask")
+    R, N, D = q.shape
+    if o is None:
+        o = _new((R, N, D), torch.float32 if o_dtype == CP_F32 else torch.bfloat16, q.device, stream)
+    if lse is None:
+        lse = _new((N, R), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = _scratch(max(256, cp_tree_attn_workspace_size(R, B, max_new, words, prefix_len, N, Nkv, D, page,
-                                                                  max_pages)), q.device, stream)
-    dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, o, lse, workspace)
-    _lib.packed(4, "cp_tree_attn_fwd", _ATTN_WORDS, _at(q), _at(k_cache), _at(v_cache), n_pages, page,
-                0 if prefix_pages is None else _at(prefix_pages), prefix_len, _at(table), B, max_pages, _at(cu_new),
-                _at(kv_len), mask, words, max_new, R, N, Nkv, D, scale, _at(o),
-                _dtype_code(o), _at(lse), _at(workspace), workspace.numel() * workspace.element_size(),
-                _raw_stream(stream, dev))
+        if mask is None or mask.dim() != 2 or k_cache.dim() != 4 or table.dim() != 2:
+            raise ValueError("expected mask [R, words], caches [n_pages, page_size, Nkv, D] and table [B, max_pages]")
+        B, max_pages = table.shape
+        workspace = _scratch(max(256, cp_tree_attn_workspace_size(R, B, max_new, mask.shape[1], prefix_len, N,
+                                                                  k_cache.shape[2], D, k_cache.shape[1], max_pages)),
+                             q.device, stream)
+    st = _lib.bind().tree_attn_fwd(q, k_cache, v_cache, mask, prefix_pages, prefix_len, table, cu_new, kv_len, max_new,
+                                   D ** -0.5 if scale is None else scale, o, lse, workspace, _handle(stream))
+    if st:
+        _lib.check("cp_tree_attn_fwd", st)
     return o, lse
 
 
