@@ -59,8 +59,8 @@ __device__ __forceinline__ long long slot_of(const AppendArgs &a, int b, int tok
 
 // Row tok's slot as its list gives it, or -1 (none, or out of range and reported), and its position.
 __device__ __forceinline__ long long slot_in_list(const AppendArgs &a, int tok, long long *pos) {
-    *pos = __ldg(a.pos + tok);
-    const long long slot = __ldg(a.slots + tok), all = static_cast<long long>(a.pt.n_pages) << a.pt.shift;
+    *pos = __ldcg(a.pos + tok);
+    const long long slot = __ldcg(a.slots + tok), all = static_cast<long long>(a.pt.n_pages) << a.pt.shift;
     if (slot >= -1 && slot < all) return slot;
     atomicExch(&g_cache_status, static_cast<int>(CP_ERR_PAGE));
     return -1;
@@ -76,6 +76,11 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs a)
     const int lane = threadIdx.x & 31, sub = lane / Map::L;
     const Map map(lane, a.rope.half);
     unsigned long long f[Map::kAng];
+    if (kAt) {
+        // its blocks may have started under the kernel that makes the lists or the rows
+        wait_for_previous();
+        launch_dependents();
+    }
     load_freqs(a.rope, lane, f);
     const int nq = a.heads[0], nk = a.heads[1], all = nq + 2 * nk;
     const long long units = (a.tokens + a.group - 1) / a.group * a.chunks;
@@ -177,7 +182,9 @@ cp_status launch_append(AppendArgs &a, cudaStream_t stream) {
     a.chunks = (heads + a.hpu - 1) / a.hpu;
     const long long blocks = ((a.tokens + a.group - 1) / a.group * a.chunks + kWarps - 1) / kWarps;
     const long long cap = static_cast<long long>(sm_count()) * 4;
-    append_kernel<T, D, kOrder, kAt><<<static_cast<unsigned>(blocks < cap ? blocks : cap), kThreads, 0, stream>>>(a);
+    const unsigned grid = static_cast<unsigned>(blocks < cap ? blocks : cap);
+    if (kAt) return launch(append_kernel<T, D, kOrder, kAt>, dim3(grid), kThreads, 0, stream, a);
+    append_kernel<T, D, kOrder, kAt><<<grid, kThreads, 0, stream>>>(a);
     return last_launch_status();
 }
 

@@ -48,9 +48,11 @@ extern "C" cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, cons
                                         const int32_t *kv_len, int64_t max_new, int64_t R, int64_t N, int64_t Nkv,
                                         int64_t D, float scale, void *o, cp_dtype o_dtype, float *lse,
                                         void *workspace, size_t ws_bytes, cudaStream_t stream) {
-    return prefix_call<false>(nullptr, 0, q, k_cache, v_cache, n_pages, page_size, prefix_pages, prefix_len, table, B,
-                              max_pages, cu_new, kv_len, max_new, R, N, Nkv, D, scale, o, o_dtype, lse, workspace,
-                              ws_bytes, 2000000000ull, false, stream);
+    Call c;
+    const cp_status st = check_call<false>(c, nullptr, 0, q, k_cache, v_cache, n_pages, page_size, prefix_pages,
+                                           prefix_len, table, B, max_pages, cu_new, kv_len, max_new, R, N, Nkv, D,
+                                           scale, o, o_dtype, lse, workspace, ws_bytes, 2000000000ull, false);
+    return st != CP_OK ? st : launch_line<false>(c, stream);
 }
 
 extern "C" cp_status cp_selftest_stalled_prefix_attn(
@@ -60,7 +62,9 @@ extern "C" cp_status cp_selftest_stalled_prefix_attn(
     float scale, void *o, cp_dtype o_dtype, float *lse, void *workspace, size_t ws_bytes, uint64_t timeout_ns,
     cudaStream_t stream) {
     if (timeout_ns < 1000000ull || timeout_ns > 2000000000ull) return CP_ERR_ARGUMENT;
-    return prefix_call<false>(nullptr, 0, q, k_cache, v_cache, n_pages, page_size, prefix_pages, prefix_len, table, B,
-                              max_pages, cu_new, kv_len, max_new, R, N, Nkv, D, scale, o, o_dtype, lse, workspace,
-                              ws_bytes, timeout_ns, true, stream);
+    Call c;
+    const cp_status st = check_call<false>(c, nullptr, 0, q, k_cache, v_cache, n_pages, page_size, prefix_pages,
+                                           prefix_len, table, B, max_pages, cu_new, kv_len, max_new, R, N, Nkv, D,
+                                           scale, o, o_dtype, lse, workspace, ws_bytes, timeout_ns, true);
+    return st != CP_OK ? st : launch_line<false>(c, stream);
 }

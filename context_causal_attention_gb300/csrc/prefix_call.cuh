@@ -856,14 +856,23 @@ cp_status check_sizes(int64_t R, int64_t B, int64_t max_new, int64_t P, int64_t 
     return CP_OK;
 }
 
-// cp_prefix_attn_fwd, or with kTree cp_tree_attn_fwd with its mask, with the limit of its waits; stalled: its loads
+// A call's arguments, checked.
+struct Call {
+    PrefixArgs a;
+    JoinArgs j;
+    Shape s;
+    uint8_t *workspace;
+    int D;
+};
+
+// cp_prefix_attn_fwd's, or with kTree cp_tree_attn_fwd's with its mask, with the limit of its waits; stalled: its loads
 // wait for a word that nothing sets.
 template <bool kTree>
-cp_status prefix_call(const int32_t *mask, int64_t words, const void *q, const void *k_cache, const void *v_cache,
+cp_status check_call(Call &c, const int32_t *mask, int64_t words, const void *q, const void *k_cache, const void *v_cache,
                       int64_t n_pages, int64_t page_size, const int32_t *prefix_pages, int64_t prefix_len, const int32_t *table, int64_t B,
                       int64_t max_pages, const int32_t *cu_new, const int32_t *kv_len, int64_t max_new, int64_t R,
                       int64_t N, int64_t Nkv, int64_t D, float scale, void *o, cp_dtype o_dtype, float *lse,
-                      void *workspace, size_t ws_bytes, uint64_t timeout_ns, bool stalled, cudaStream_t stream) {
+                      void *workspace, size_t ws_bytes, uint64_t timeout_ns, bool stalled) {
     if (!q || !k_cache || !v_cache || !table || !cu_new || !kv_len || !o || !lse || (prefix_len > 0 && !prefix_pages) ||
         (kTree && !mask))
         return CP_ERR_NULL;
@@ -880,7 +889,8 @@ cp_status prefix_call(const int32_t *mask, int64_t words, const void *q, const v
     if (!workspace || ws_bytes < s.bytes) return CP_ERR_WORKSPACE;
     if (odd(workspace, 256)) return CP_ERR_ALIGNMENT;
     if (s.slots[0] * s.lanes > INT32_MAX || s.slots[1] * s.lanes > INT32_MAX) return CP_ERR_SHAPE;
-    PrefixArgs a{};
+    PrefixArgs &a = c.a;
+    a = PrefixArgs{};
     if ((st = prefix_status_word(&a.status)) != CP_OK) return st;
     a.timeout_ns = timeout_ns;
     if (stalled) {
@@ -914,7 +924,8 @@ cp_status prefix_call(const int32_t *mask, int64_t words, const void *q, const v
     a.mask = reinterpret_cast<const uint32_t *>(mask);
     a.words = static_cast<int>(words);
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-    JoinArgs j{};
+    JoinArgs &j = c.j;
+    j = JoinArgs{};
     j.cu = cu_new;
     j.kv_len = kv_len;
     j.R = a.R, j.B = a.B, j.N = a.N, j.Nkv = a.Nkv, j.G = a.G;
@@ -923,8 +934,16 @@ cp_status prefix_call(const int32_t *mask, int64_t words, const void *q, const v
     j.o = o;
     j.o_bf16 = o_dtype == CP_BF16;
     j.lse = lse;
-    uint8_t *w = static_cast<uint8_t *>(workspace);
-    return D == 128 ? launch_call<128, kTree>(a, s, w, j, stream) : launch_call<64, kTree>(a, s, w, j, stream);
+    c.s = s;
+    c.workspace = static_cast<uint8_t *>(workspace);
+    c.D = static_cast<int>(D);
+    return CP_OK;
 }
+template <bool kTree>
+cp_status launch_line(const Call &c, cudaStream_t stream) {
+    return c.D == 128 ? launch_call<128, kTree>(c.a, c.s, c.workspace, c.j, stream)
+                      : launch_call<64, kTree>(c.a, c.s, c.workspace, c.j, stream);
+}
+
 }  // namespace
 }  // namespace cpattn

@@ -3,17 +3,19 @@
 // index wherever a key tile reaches into the step's new tokens).
 //
 // Ancestors.  mask_j = {j} + mask_parent(j).  A warp holds 32 tokens in a row, a token a lane, and follows the
-// parents among them by doubling (five rounds of shuffles, whatever the tree's shape); what is left of a token's
-// branch begins at one earlier token, whose row is taken over whole.  So the warps of a block, which works on one
-// sequence, come one after the other, and each row is read and written once: 16 short steps for 512 tokens.  Following
-// all parents by doubling through shared memory instead took 15.9 us for 300 trees of up to 500 tokens, this 9.4.
-// What bounds it is the latency of the launch and of two loads that hang on one another (counts, parents).
+// parents among them by doubling (five rounds of shuffles, whatever the tree's shape): each token then knows its branch
+// among these 32, one word of its mask, and the earlier token that the branch hangs on.  From there it goes from
+// word to word, 16 steps for 512 tokens at most, two reads of shared memory each, all tokens side by side.  300 trees of
+// up to 500 tokens take 5.2 us in a graph so; 9.4 where the warps came one after the other and took whole rows over,
+// 15.9 by doubling through shared memory over the whole tree.  What bounds it is the latency of the launch and of
+// two loads that hang on one another (counts, parents).
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "cp_internal.h"
 #include "prefix_call.cuh"
+#include "tree_cluster.cuh"
 
 namespace cpattn {
 namespace {
@@ -30,7 +32,7 @@ struct TreeArgs {
 };
 
 __global__ void tree_kernel(const TreeArgs a) {
-    extern __shared__ __align__(16) uint32_t shared[];
+    extern __shared__ uint32_t shared[];
     wait_for_previous();
     launch_dependents();
     const int b = blockIdx.x, tid = threadIdx.x, wide = 32 * a.words;
@@ -46,8 +48,10 @@ __global__ void tree_kernel(const TreeArgs a) {
         for (int j = tid; j < n; j += blockDim.x) a.pos[begin + j] = static_cast<int32_t>(first + j);
         return;
     }
-    uint32_t *bits = shared;  // [32 words][words]
-    int *depth = reinterpret_cast<int *>(bits + wide * a.words);
+    // rows an odd number of words apart, so that neighbouring tokens' are on different banks
+    const int stride = a.words | 1;
+    uint32_t *bits = shared, *word = bits + wide * stride;  // [32 words][stride], [32 words]
+    int *hangs = reinterpret_cast<int *>(word + wide), *depth = hangs + wide;
     const int lane = tid & 31, warp = tid >> 5, at = 32 * warp;
     int up = -1;
     if (tid < n) {
@@ -67,35 +71,109 @@ __global__ void tree_kernel(const TreeArgs a) {
         top = __shfl_sync(0xffffffffu, top, top);
     }
     const int before = __shfl_sync(0xffffffffu, up, top);  // the earlier token that it hangs on, or -1
-    for (int i = tid; i < wide * a.words; i += blockDim.x) bits[i] = 0;
+    word[tid] = own;
+    hangs[tid] = before;
+    depth[tid] = edges;
+    for (int w = 0; w < a.words; ++w) bits[tid * stride + w] = 0;
     __syncthreads();
-    const int warps = (n + 31) >> 5;
-    for (int k = 0; k < warps; ++k) {
-        if (k == warp) {
-            if (before >= 0) edges += 1 + depth[before];
-            depth[tid] = edges;
-            bits[tid * a.words + k] = own;
-            // the rows of the earlier tokens, eight at a time, four lanes each
-            for (int w0 = 0; w0 < k; w0 += 4) {
-                const int w = w0 + (lane & 3);
-                uint32_t v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int from = __shfl_sync(0xffffffffu, before, 8 * i + (lane >> 2));
-                    v[i] = w < k && from >= 0 ? bits[from * a.words + w] : 0u;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (w < k) bits[(at + 8 * i + (lane >> 2)) * a.words + w] = v[i];
-            }
+    if (tid < n) {
+        // (each token's earlier ones are in an earlier word than it: the walk ends)
+        int e = tid, sum = edges;
+        for (;;) {
+            bits[tid * stride + (e >> 5)] = word[e];
+            e = hangs[e];
+            if (e < 0) break;
+            sum += 1 + depth[e];
         }
-        __syncthreads();
+        a.pos[begin + tid] = static_cast<int32_t>(first + sum);
     }
-    if (tid < n) a.pos[begin + tid] = static_cast<int32_t>(first + edges);
+    __syncthreads();
     uint32_t *to = a.mask + static_cast<long long>(begin) * a.words;
-    const int all = n * a.words, fours = (reinterpret_cast<uintptr_t>(to) & 15u) == 0 ? all >> 2 : 0;
-    for (int i = tid; i < fours; i += blockDim.x) reinterpret_cast<uint4 *>(to)[i] = reinterpret_cast<uint4 *>(bits)[i];
-    for (int i = 4 * fours + tid; i < all; i += blockDim.x) to[i] = bits[i];
+    if (a.words == 1) {
+        if (tid < n) to[tid] = bits[tid];
+        return;
+    }
+    for (int i = tid; i < n * a.words; i += blockDim.x) {
+        const int j = i / a.words;
+        to[i] = bits[j * stride + i - j * a.words];
+    }
+}
+
+// ---------------------------------------------------------------- few sequences
+template <int D>
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute (&at)[2], int items, int blocks, cudaStream_t stream) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(static_cast<unsigned>(items * blocks));
+    c.blockDim = dim3(kClThreads);
+    c.dynamicSmemBytes = ClCfg<D>::kSmem;
+    c.stream = stream;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(blocks);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = 2;
+    return c;
+}
+
+// How many clusters of each size the GPU holds at once (all GPUs of a process are alike); 0 of all if it has none.
+struct AtOnce {
+    int clusters[kClMost + 1];
+};
+template <int D>
+const AtOnce &clusters_at_once() {
+    static AtOnce most{};
+    static std::once_flag once;
+    std::call_once(once, [] {
+        const void *f = reinterpret_cast<const void *>(tree_cluster_kernel<D>);
+        if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, ClCfg<D>::kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+            cudaGetLastError();
+            return;
+        }
+        for (int i = 1; i <= kClMost; ++i) {
+            cudaLaunchAttribute at[2] = {};
+            cudaLaunchConfig_t c = cluster_config<D>(at, 1, i, nullptr);
+            c.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, f, &c) == cudaSuccess) most.clusters[i] = n;
+            else cudaGetLastError();
+        }
+    });
+    return most;
+}
+
+// Blocks of a cluster, or 0 where the line of prefix_call.cuh takes the call.  As many blocks as let all items run at
+// once; the line where that is one, or where the longest sequence that the table can hold would make a
+// block's share too many tiles of 128 keys: clusters are quick to begin and to end, the line shares the keys of
+// ragged sequences evenly and reads a prefix once.  Clusters and line, us (16 tokens, 32 / 8 heads of 128, pages of 32, own keys
+// up to the figure): one sequence of 500 13.5 and 15.5, of 4096 16.9 and 19.3, of 16000 (10 tiles) 26.6 and 25.4; four of
+// 4096 (8 tiles) 23 and 30, ragged 22 and 25, of 16000 (31) 54 and 64, ragged 52 and 48; nine of 4096 (16)
+// 36 and 51, ragged 35 and 36.  Up to 16 rows the line has its narrow tiles: four tokens of one sequence of 4000 keys
+// (3 tiles) 14.4 and 15.8, of two (4.5) 17.2 and 15.7, of four (8) 19.4 and 16.8.  A prefix is read once for each
+// sequence: two sequences of 500 behind 500 keys 13.5 and 18.1, behind 4000 (5) 21.8 and 20.4, four of 4000 behind 4000 (16) 29 and 26.
+// At D = 64 (16 / 4 heads) a tile costs half: four of 4000 behind 4000 (9) 19 and 25, behind 16000 (22) 36 and 30; four tokens
+// of eight sequences of 4000 (8) 15.8 and 16.0, of sixteen (16) 24 and 20.
+template <int D>
+int cluster_blocks(const ClusterArgs &c, int64_t max_new) {
+    const PrefixArgs &a = c.p;
+    const long long items = static_cast<long long>(a.B) * c.tiles * a.Nkv;
+    const AtOnce &most = clusters_at_once<D>();
+    const long long keys = a.P + (static_cast<long long>(a.own.max_pages) << a.own.shift);
+    const int tiles = (D == 64 ? 2 : 1) * (a.P > 0 ? 8 : max_new * a.G <= kTcRows ? 4 : 16);
+    for (int i = kClMost; i >= 2; --i)
+        if (items <= most.clusters[i]) return keys <= 128LL * i * tiles ? i : 0;
+    return 0;
+}
+
+template <int D>
+cp_status launch_clusters(const ClusterArgs &a, int blocks, cudaStream_t stream) {
+    cudaLaunchAttribute at[2] = {};
+    const cudaLaunchConfig_t c = cluster_config<D>(at, a.p.B * a.tiles * a.p.Nkv, blocks, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&c, tree_cluster_kernel<D>, a);
+    if (e != cudaSuccess) cudaGetLastError();
+    return cuda_status(e);
 }
 
 }  // namespace
@@ -127,7 +205,7 @@ extern "C" cp_status cp_tree_plan(const int32_t *parent, const int32_t *cu_new, 
     const cp_status st = prefix_status_word(&a.status);
     if (st != CP_OK) return st;
     const int wide = 32 * a.words;
-    return launch(tree_kernel, dim3(static_cast<unsigned>(B)), wide, static_cast<size_t>(wide) * (1 + a.words) * 4,
+    return launch(tree_kernel, dim3(static_cast<unsigned>(B)), wide, static_cast<size_t>(wide) * (3 + (a.words | 1)) * 4,
                   stream, a);
 }
 
@@ -150,7 +228,13 @@ extern "C" cp_status cp_tree_attn_fwd(const void *q, const void *k_cache, const 
                                       cp_dtype o_dtype, float *lse, void *workspace, size_t ws_bytes,
                                       cudaStream_t stream) {
     if (words < 1 || words > kMaxWords) return CP_ERR_SHAPE;
-    return prefix_call<true>(mask, words, q, k_cache, v_cache, n_pages, page_size, prefix_pages, prefix_len, table, B,
-                             max_pages, cu_new, kv_len, max_new, R, N, Nkv, D, scale, o, o_dtype, lse, workspace,
-                             ws_bytes, 2000000000ull, false, stream);
+    Call c;
+    const cp_status st = check_call<true>(c, mask, words, q, k_cache, v_cache, n_pages, page_size, prefix_pages,
+                                          prefix_len, table, B, max_pages, cu_new, kv_len, max_new, R, N, Nkv, D,
+                                          scale, o, o_dtype, lse, workspace, ws_bytes, 2000000000ull, false);
+    if (st != CP_OK) return st;
+    ClusterArgs few{c.a, static_cast<int>((max_new * c.a.G + 127) / 128), o, o_dtype == CP_BF16, lse};
+    const int blocks = D == 128 ? cluster_blocks<128>(few, max_new) : cluster_blocks<64>(few, max_new);
+    if (blocks) return D == 128 ? launch_clusters<128>(few, blocks, stream) : launch_clusters<64>(few, blocks, stream);
+    return launch_line<true>(c, stream);
 }

@@ -40,7 +40,11 @@ class TreeCall(Call):
             r += n
         self.mask = torch.from_numpy(mask)
 
-    def run(self, dev, hint=None, **kw):
+    def run(self, dev, hint=None, form=None, **kw):
+        if form == "line":
+            # a table for more tokens than a cluster takes: the same call by the line's kernels
+            wide = 140000 // self.b.page
+            self.table = torch.cat([self.table, torch.full((len(self.new), wide), -3, dtype=torch.int32)], 1)
         self.dev = [t.to(dev) for t in (self.q, self.k, self.v, self.mask, self.pages, self.table, self.cu, self.kv_len)]
         return self.again(hint, **kw)
 
@@ -90,14 +94,15 @@ CASES = {
 
 @pytest.mark.parametrize("name", sorted(CASES))
 @pytest.mark.parametrize("kind", ["random", "any", "chain"])
-def test_against_64_bits(cuda_dev, name, kind):
+@pytest.mark.parametrize("form", ["as_chosen", "line"])
+def test_against_64_bits(cuda_dev, name, kind, form):
     new, length, prefix, N, Nkv, D, page, words, pad = CASES[name]
     c = TreeCall(len(name), new, length, prefix, N, Nkv, D, page, words, kind, pad)
     dt = "fp32" if kind == "any" else "bf16"
     T_ = {"bf16": torch.bfloat16, "fp32": torch.float32}[dt]
     o = torch.full((c.R, N, D), 7.0, dtype=T_, device=cuda_dev)
     lse = torch.full((N, c.R), 7.0, device=cuda_dev)
-    c.run(cuda_dev, o=o, lse=lse)
+    c.run(cuda_dev, form=form, o=o, lse=lse)
     c.check(o, lse, dt, name)
     assert (o[c.rows:] == 7).all() and (lse[:, c.rows:] == 7).all()
 
@@ -116,22 +121,24 @@ def test_a_chain_is_the_prefix_attention(cuda_dev, name):
 
 @pytest.mark.parametrize("garbage", [float("nan"), float("inf"), 3e38])
 @pytest.mark.parametrize("name", ["narrow", "half_tile_prefix", "wide", "with_prompts", "one"])
-def test_what_unused_slots_hold_does_not_matter(cuda_dev, name, garbage):
+@pytest.mark.parametrize("form", ["as_chosen", "line"])
+def test_what_unused_slots_hold_does_not_matter(cuda_dev, name, garbage, form):
     new, length, prefix, N, Nkv, D, page, words, pad = CASES[name]
     clean = TreeCall(3, new, length, prefix, N, Nkv, D, page, words, "random", pad)
     dirty = TreeCall(3, new, length, prefix, N, Nkv, D, page, words, "random", pad, garbage=garbage)
     n = clean.rows
-    a, b = clean.run(cuda_dev), dirty.run(cuda_dev)
+    a, b = clean.run(cuda_dev, form=form), dirty.run(cuda_dev, form=form)
     assert torch.equal(a[0][:n], b[0][:n]) and torch.equal(a[1][:, :n], b[1][:, :n])
 
 
+@pytest.mark.parametrize("form", ["as_chosen", "line"])
 @pytest.mark.parametrize("name", ["narrow", "half_tile_prefix", "wide"])
-def test_keys_that_a_row_does_not_see_are_hidden_whatever_they_hold(cuda_dev, name):
+def test_keys_that_a_row_does_not_see_are_hidden_whatever_they_hold(cuda_dev, name, form):
     """NaN, infinities and the lowest value in drafted K rows: rows that do not see them keep their values (to the
     tolerance that test_gpu_prefix.py derives for rows beside a row of NaN)."""
     new, length, prefix, N, Nkv, D, page, words, pad = CASES[name]
     c = TreeCall(8, new, length, prefix, N, Nkv, D, page, words, "star", pad)
-    good = [t.clone() for t in c.run(cuda_dev, o_dtype=F.CP_F32)]
+    good = [t.clone() for t in c.run(cuda_dev, form=form, o_dtype=F.CP_F32)]
     size = torch.from_numpy(c.want()[2]).to(cuda_dev)
     keep = torch.ones(c.rows, dtype=torch.bool)
     r = 0
@@ -172,21 +179,23 @@ def test_rows_that_see_nothing(cuda_dev):
 
 @pytest.mark.parametrize("gain", [30.0, 300.0])
 @pytest.mark.parametrize("N", [2, 16])
-def test_large_scores(cuda_dev, gain, N):
+@pytest.mark.parametrize("form", ["as_chosen", "line"])
+def test_large_scores(cuda_dev, gain, N, form):
     c = TreeCall(6, [7, 12], [500, 900], 700, N, 2, 64, 16, 1, gain=gain)
     for s, m in enumerate(c.b.length):
         at = c.b.slots(s, 0, m)
         k = c.k.view(-1, 2, 64)
         k[at] = (k[at].float() * torch.linspace(0.01, 1, max(m, 1)).view(-1, 1, 1)).to(torch.bfloat16)
-    o, lse = c.run(cuda_dev, o_dtype=F.CP_F32)
+    o, lse = c.run(cuda_dev, form=form, o_dtype=F.CP_F32)
     c.check(o, lse, "fp32", "gain", gain)
 
 
+@pytest.mark.parametrize("form", ["as_chosen", "line"])
 @pytest.mark.parametrize("name", ["narrow_edges", "half_tile_prefix", "wide", "with_prompts"])
-def test_same_bits_twice_on_a_stream_and_by_graph(cuda_dev, name):
+def test_same_bits_twice_on_a_stream_and_by_graph(cuda_dev, name, form):
     new, length, prefix, N, Nkv, D, page, words, pad = CASES[name]
     c = TreeCall(7, new, length, prefix, N, Nkv, D, page, words, "random", pad)
-    a = [t.clone() for t in c.run(cuda_dev)]
+    a = [t.clone() for t in c.run(cuda_dev, form=form)]
     n = c.rows
     same = lambda x, y: torch.equal(x[0][:n], y[0][:n]) and torch.equal(x[1][:, :n], y[1][:, :n])  # noqa: E731
     for _ in range(5):
@@ -296,9 +305,10 @@ def test_outputs_and_workspace_stay_in_bounds(cuda_dev):
 
 @pytest.mark.parametrize("what", ["page", "prefix_page", "length", "negative_length", "counts", "counts_past_rows"])
 @pytest.mark.parametrize("N", [4, 32])
-def test_bad_lists_are_reported(cuda_dev, what, N):
+@pytest.mark.parametrize("form", ["as_chosen", "line"])
+def test_bad_lists_are_reported(cuda_dev, what, N, form):
     c = TreeCall(9, [2, 3], [50, 40], 70, N, 2, 64, 16, 1)
-    good = [t.clone() for t in c.run(cuda_dev)]
+    good = [t.clone() for t in c.run(cuda_dev, form=form)]
     if what == "page":
         c.table[0, 1] = c.b.total + 5
     elif what == "prefix_page":
