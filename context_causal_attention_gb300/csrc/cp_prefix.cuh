@@ -468,8 +468,11 @@ __device__ __forceinline__ void copy_rows(uint32_t at, uint32_t sw, const char *
 // filled with zeros.  TMA tiles of a small page are slower: a copy of 16 rows of
 // 128 bytes holds the TMA unit for about 90 cycles, which ends at 3.4 TB/s over
 // the GPU with two issuing warps and 4.4 with four, where this reaches 5.9.
-// (The loop over 16-row groups is not unrolled: a block copies few tiles, and code
-// that is read for the first time costs more than the loop.)
+// A tile of nothing but keys is copied without a look at its rows, all addresses formed first: a warp's 128 rows of 256 bytes
+// took 2400 clk in the loop over 16-row groups, which was a tile's time (64 sequences of 4096 keys, 16 tokens of 32 / 8
+// heads each, pages of 16: 229 us, 216 so; heads of 64: 171 and 135; 64 single tokens behind 32768 keys as before).
+// That loop, for the tiles at the end of the keys or with a bad page, is not unrolled: code that is read for the
+// first time costs more than the loop.
 template <int D, int KT, int kAtom>  // KT: a multiple of 16, here also a part of a tile
 __device__ __forceinline__ void copy_tile(const PrefixArgs &a, const Piece &x, const PageWindow &win,
                                           const __nv_bfloat16 *cache, uint32_t dst, int key0, int lane) {
@@ -481,6 +484,16 @@ __device__ __forceinline__ void copy_tile(const PrefixArgs &a, const Piece &x, c
     const uint32_t sw = ((c & 7) ^ r) << 4;
     // lane g looks up the rows 16 g .. 16 g + 15: where they begin, -1 for none (a bad page or no keys)
     const int mine = win.rows16(a, key0 + 16 * (lane % (KT / 16)), x.keys);
+    if (x.keys - key0 >= KT && __all_sync(0xffffffffu, mine >= 0)) {
+        // a tile of nothing but keys
+        const char *src[KT / 16];
+#pragma unroll
+        for (int g = 0; g < KT / 16; ++g)
+            src[g] = lane_src + static_cast<long long>(__shfl_sync(0xffffffffu, mine, g)) * row_bytes;
+#pragma unroll
+        for (int g = 0; g < KT / 16; ++g) copy_rows<kRpi, 0>(at + g * (16 * 128), sw, src[g], step);
+        return;
+    }
 #pragma unroll 2
     for (int g = 0; g < KT / 16; ++g, at += 16 * 128) {
         const int left = x.keys - key0 - 16 * g, row = __shfl_sync(0xffffffffu, mine, g);
