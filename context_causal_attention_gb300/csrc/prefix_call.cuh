@@ -276,7 +276,8 @@ __device__ __forceinline__ void mma_work(const PrefixArgs &a, uint8_t *smem) {
                         if (masked && hidden) s[n][e] = -INFINITY;
                     }
                 // the maximum is an integer, set by the first keys that a row sees and
-                // moved only when a weight would pass 2^30: rescaling is exact and rare
+                // moved only when a weight would pass 2^30: rescaling is exact and rare (trees: the maximum
+                // itself, so that the weight of a row's only key is 1)
                 const float top0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
                 const float top1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
                 if (__any_sync(0xffffffffu, top0 > m[0] + 30.f || top1 > m[1] + 30.f)) {
@@ -286,7 +287,7 @@ __device__ __forceinline__ void mma_work(const PrefixArgs &a, uint8_t *smem) {
                         top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
                         top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
                         if (top[h] > m[h] + 30.f) {
-                            const float mn = ceilf(top[h]), f = fast_exp2(m[h] - mn);  // 0 from -inf
+                            const float mn = kTree ? top[h] : ceilf(top[h]), f = fast_exp2(m[h] - mn);  // 0 from -inf
                             m[h] = mn;
                             l[h] *= f;
 #pragma unroll

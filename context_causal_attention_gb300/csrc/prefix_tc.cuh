@@ -15,7 +15,8 @@
 //               in tensor memory (512 columns: S0 | S1 | O0 | O1).
 //   warps 4-7   softmax of rows 0..127, warps 8-11 of rows 128..255: one thread
 //               a row, in the log2 domain with an integer running maximum that
-//               moves only when a tile's sum passes 2^64 (as in attn.cu).
+//               moves only when a tile's sum passes 2^64 (as in attn.cu).  Trees (kTree) take the
+//               maximum itself: the weight of a row's only key is 1 then, and its output that key's value.
 // The two halves keep the tensor cores and the exponentials busy in turn.  In a
 // tile of up to 128 rows both hold the same rows and take the key tiles in turn;
 // the first half joins the two results at the end (with one half alone the scores,
@@ -451,7 +452,7 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                     if (mask) hide(1, sb);
                     if (m_run == -INFINITY) {
                         const float top = row_max128(sa, sb) * sl2;
-                        if (top > -INFINITY) m_run = ceilf(top);
+                        if (top > -INFINITY) m_run = kTree ? top : ceilf(top);
                     }
                 }
                 const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
@@ -472,8 +473,8 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                     if (mask) hide(0, sa);
                     float f = 1.f;
                     if (big) {
-                        const float m_new = ceilf(row_max128(sa, sb) * sl2), d = m_run - m_new;
-                        f = d >= -126.f ? __int_as_float((127 + static_cast<int>(d)) << 23) : 0.f;
+                        const float top = row_max128(sa, sb) * sl2, m_new = kTree ? top : ceilf(top), d = m_run - m_new;
+                        f = kTree ? fast_exp2(d) : d >= -126.f ? __int_as_float((127 + static_cast<int>(d)) << 23) : 0.f;
                         l_run *= f;
                         m_run = m_new;
                     }

@@ -10,7 +10,8 @@
 // Inside a block, as in prefix_tc.cuh: two halves of four softmax warps take the key tiles in turn, S = Q K^T and
 // O += P V on tcgen05 with S, P and O in tensor memory (S0 | S1 | O0 | O1), a thread a row.  K and V come by 16-byte
 // cp.async whatever the page's size, Q is gathered by the softmax warps.  A row's maximum is looked for before its
-// weights are formed (integer, and moved only when a weight would pass 2^30), so nothing is computed twice.
+// weights are formed (and moved only when a weight would pass 2^30), so nothing is computed twice.  It is the score itself, not
+// a whole number above it: the weight of a row's only key is 1 then, and its output that key's value.
 // A tile's code is a loop over 64 columns, not unrolled over 128: a block goes through two to thirty tiles, and code
 // that is read for the first time costs more than the loop (a tree of 27 tokens over 4096 keys takes 15.6 us so, 17.0 with
 // the weights of 128 columns in a row and the maximum looked for only when their sum asks for it).
@@ -318,10 +319,9 @@ __global__ void __launch_bounds__(kClThreads, 1) tree_cluster_kernel(const __gri
                 if (__any_sync(0xffffffffu, top > m + 30.f)) {
                     float f = 1.f;
                     if (top > m + 30.f) {
-                        const float m_new = ceilf(top), d = m - m_new;
-                        f = d >= -126.f ? __int_as_float((127 + static_cast<int>(d)) << 23) : 0.f;
+                        f = fast_exp2(m - top);  // 0 from -inf
                         l *= f;
-                        m = m_new;
+                        m = top;
                     }
                     // O is quiet: its last product was issued before these scores
 #pragma unroll 1
