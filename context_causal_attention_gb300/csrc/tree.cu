@@ -155,6 +155,10 @@ const AtOnce &clusters_at_once() {
 // sequence: two sequences of 500 behind 500 keys 13.5 and 18.1, behind 4000 (5) 21.8 and 20.4, four of 4000 behind 4000 (16) 29 and 26.
 // At D = 64 (16 / 4 heads) a tile costs half: four of 4000 behind 4000 (9) 19 and 25, behind 16000 (22) 36 and 30; four tokens
 // of eight sequences of 4000 (8) 15.8 and 16.0, of sixteen (16) 24 and 20.
+// With more items than two blocks each would find room for, a block an item still saves the line's beginning, partials
+// and join while its turns are few and short (16 tokens, 8 KV heads): 16 sequences of 500 keys 17.7 and 37, of 4096 55 and
+// 75, ragged 47 and 50; 20 of 4096 98 and 88 (eight blocks go a second time), ragged 50 and 56; 64 of 4096 212 and
+// 216, ragged 113 and 127; 300 of 500, ragged, 178 and 169.  At D = 64 32 of 4096 69 and 82, 64 138 and 128.
 template <int D>
 int cluster_blocks(const ClusterArgs &c, int64_t max_new) {
     const PrefixArgs &a = c.p;
@@ -164,6 +168,8 @@ int cluster_blocks(const ClusterArgs &c, int64_t max_new) {
     const int tiles = (D == 64 ? 2 : 1) * (a.P > 0 ? 8 : max_new * a.G <= kTcRows ? 4 : 16);
     for (int i = kClMost; i >= 2; --i)
         if (items <= most.clusters[i]) return keys <= 128LL * i * tiles ? i : 0;
+    if (most.clusters[1] && a.P == 0 && max_new * a.G > kTcRows && items <= (D == 64 ? 256 : 512) && keys <= 128LL * 48)
+        return 1;
     return 0;
 }
 

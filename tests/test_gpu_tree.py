@@ -86,6 +86,9 @@ CASES = {
     "one_kv_head": ([9, 3], [9, 300], 77, 40, 1, 64, 256, 1, 0),
     "no_groups": ([13, 6], [200, 13], 500, 16, 16, 64, 16, 1, 0),
     "odd_groups": ([11, 2, 30], [90, 2, 400], 257, 21, 3, 128, 128, 1, 0),
+    # one block an item: more items than SMs, and fewer
+    "blocks": ([9 + i % 20 for i in range(30)], [9 + i % 20 + 37 * i % 300 for i in range(30)], 0, 32, 8, 128, 16, 1, 1),
+    "blocks_few": ([5 + 7 * i % 60 for i in range(22)], [70 + 91 * i % 900 for i in range(22)], 0, 16, 4, 64, 32, 2, 0),
     "many": ([1 + i % 6 for i in range(200)], [10 + 7 * i % 300 for i in range(200)], 130, 8, 2, 64, 16, 1, 0),
     "many_wide": ([5 + 13 * i % 60 for i in range(150)], [70 + 37 * i % 700 for i in range(150)], 0, 8, 1, 128, 64, 2, 0),
     "most_sequences": ([1 + i % 2 for i in range(4096)], [2 + i % 40 for i in range(4096)], 30, 2, 1, 64, 16, 1, 0),
