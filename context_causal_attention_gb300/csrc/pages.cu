@@ -16,6 +16,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 
 #include "cp_internal.h"
 #include "cp_paged.cuh"
@@ -26,7 +27,7 @@ namespace {
 
 // ---------------------------------------------------------------- pages of a step
 constexpr int kPlanThreads = 1024;  // of a block, at most
-constexpr int kPlanBlocks = 8;      // of the cluster, at most
+constexpr int kPlanBlocks = 16;     // of the cluster, at most (8 where the GPU has no room for one of 16)
 constexpr int kRowsEach = 4;        // neighbouring rows of a thread
 
 struct PlanArgs {
@@ -73,7 +74,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     extern __shared__ int sums[];
     // of the B sequences: new tokens before it, pages taken before it, given before it, tokens that stay, pages had
     int *rows = sums, *takes = rows + a.B, *gives = takes + a.B, *stays = gives + a.B, *owned = stays + a.B;
-    __shared__ long long warp_sum[kPlanThreads / 32][3];
+    __shared__ float warp_size[kPlanThreads / 32];
+    __shared__ int warp_sum[kPlanThreads / 32][3];
     wait_for_previous();
     launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, each = (a.B + blockDim.x - 1) / blockDim.x;
@@ -81,7 +83,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     const long long most = static_cast<long long>(a.max_pages) << a.shift;
     const int free0 = __ldcg(a.n_free);
     int had[4], keep[4], fresh[4];
-    long long t[3] = {0, 0, 0};
+    int t[3] = {0, 0, 0};
+    float size = 0.f;  // of the three together: whether 32 bits hold them
     bool bad = free0 < 0 || free0 > a.n_pages;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -104,45 +107,55 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         t[0] += fresh[k];
         t[1] += max(move, 0);
         t[2] += max(-move, 0);
+        size += static_cast<float>(fresh[k]) + static_cast<float>(abs(move));
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) size += __shfl_xor_sync(0xffffffffu, size, o);
+    if (lane == 0) warp_size[warp] = size;
     bad = __syncthreads_or(bad);
-    long long before[3] = {t[0], t[1], t[2]};
+    int before[3] = {t[0], t[1], t[2]};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-            const long long v = __shfl_up_sync(0xffffffffu, before[i], o);
+            const int v = __shfl_up_sync(0xffffffffu, before[i], o);
             if (lane >= o) before[i] += v;
         }
     }
     if (lane == 31)
         for (int i = 0; i < 3; ++i) warp_sum[warp][i] = before[i];
     __syncthreads();
-    long long all[3] = {0, 0, 0};
+    int all[3] = {0, 0, 0};
     {
         // the warps before this one, and all of them
-        long long v[3], w[3];
+        int v[3], w[3];
+        size = lane < blockDim.x / 32 ? warp_size[lane] : 0.f;
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-            const long long mine = lane < blockDim.x / 32 ? warp_sum[lane][i] : 0;
+            const int mine = lane < blockDim.x / 32 ? warp_sum[lane][i] : 0;
             v[i] = lane < warp ? mine : 0;
             w[i] = mine;
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        for (int o = 16; o > 0; o >>= 1) {
+            size += __shfl_xor_sync(0xffffffffu, size, o);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
                 w[i] += __shfl_xor_sync(0xffffffffu, w[i], o);
             }
+        }
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             before[i] += v[i] - t[i];
             all[i] = w[i];
         }
     }
-    if (all[0] > a.R || free0 + all[2] > a.n_pages) bad = true;
-    const long long lacking = all[1] - (free0 + all[2]);
+    // (an fp32 sum of 8192 terms is off by less than its 1000th part: each sum is below 2^31 then; where they are not, R
+    // or the stack is too small for them)
+    const bool huge = !(size < 0x1.8p30f);
+    bad |= huge || all[0] > a.R || all[2] > a.n_pages - free0;
+    const int lacking = all[1] - (free0 + all[2]);
     const int gx = rank * blockDim.x + tid, step = blocks * blockDim.x;
     if (bad || lacking > 0) {
         // nothing is handed out: no new rows, the lengths and pages as they were
@@ -163,21 +176,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
             if (tid == 0) {
                 a.cu[a.B] = 0;
                 a.n_free_out[0] = free0;
-                a.n_free_out[1] = bad ? -1 : static_cast<int>(min(lacking, static_cast<long long>(INT32_MAX)));
+                a.n_free_out[1] = bad ? -1 : lacking;
                 if (bad) atomicExch(a.status, static_cast<int>(CP_ERR_PAGE));
             }
         }
         return;
     }
-    const int total = static_cast<int>(all[0]), taken = static_cast<int>(all[1]), given = static_cast<int>(all[2]);
+    const int total = all[0], taken = all[1], given = all[2];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int b = tid * each + k;
         if (k < each && b < a.B) {
             const int pages = (had[k] + P1) >> a.shift, move = ((keep[k] + fresh[k] + P1) >> a.shift) - pages;
-            rows[b] = static_cast<int>(before[0]);
-            takes[b] = static_cast<int>(before[1]);
-            gives[b] = static_cast<int>(before[2]);
+            rows[b] = before[0];
+            takes[b] = before[1];
+            gives[b] = before[2];
             stays[b] = keep[k];
             owned[b] = pages;
             before[0] += fresh[k];
@@ -342,6 +355,20 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
 using namespace cpattn;
 
 namespace {
+// A launch of one cluster (`at`: room for its attributes).
+cudaLaunchConfig_t plan_config(cudaLaunchAttribute *at, int blocks, int threads, size_t smem, cudaStream_t stream) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(blocks);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = blocks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return c;
+}
 bool odd4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 }  // namespace
 
@@ -390,8 +417,18 @@ extern "C" cp_status cp_cache_plan(const int32_t *kv_had, const int32_t *kv_keep
     a.kv_len = kv_len, a.cu = cu_new, a.slots = slots, a.pos = pos, a.n_free_out = n_free_out;
     if ((st = cache_status_word(&a.status)) != CP_OK) return st;
     const size_t smem = static_cast<size_t>(B) * 5 * 4;
-    static const cudaError_t err =
-        cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSequences * 5 * 4);
+    static int room = 0;  // blocks of the largest cluster
+    static cudaError_t err = cudaSuccess;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSequences * 5 * 4);
+        if (err == cudaSuccess) err = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        cudaLaunchAttribute at{};
+        const cudaLaunchConfig_t c = plan_config(&at, kPlanBlocks, kPlanThreads, kMaxSequences * 5 * 4, nullptr);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, plan_kernel, &c) != cudaSuccess) cudaGetLastError();
+        room = n > 0 ? kPlanBlocks : 8;
+    });
     if (err != cudaSuccess) return cuda_status(err);
     a.vectors = aligned16(slots) && aligned16(pos);
     // Four sequences a thread at most, and a thread for four rows: up to 2048 rows by a larger block, up to 16384 by more
@@ -399,20 +436,12 @@ extern "C" cp_status cp_cache_plan(const int32_t *kv_had, const int32_t *kv_keep
     int threads = 128, blocks = 1;
     auto rows = [&] { return static_cast<int64_t>(blocks) * threads * kRowsEach; };
     while (threads < kPlanThreads && (threads * 4 < B || (threads < 512 && rows() < R))) threads *= 2;
-    while (blocks < kPlanBlocks && rows() < R) blocks *= 2;
+    while (blocks < room && rows() < R) blocks *= 2;
     while (threads < kPlanThreads && rows() < R) threads *= 2;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3(blocks);
-    c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
-    c.stream = stream;
     cudaLaunchAttribute at[2] = {};
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = blocks;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    c.attrs = at;
+    cudaLaunchConfig_t c = plan_config(at, blocks, threads, smem, stream);
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     c.numAttrs = 2;
     const cudaError_t e = cudaLaunchKernelEx(&c, plan_kernel, a);
     if (e != cudaSuccess) cudaGetLastError();
