@@ -16,10 +16,12 @@ struct PageTable {
     const int32_t *table;  // [B][max_pages]
     int B, max_pages, n_pages;
     int shift;  // log2 of the tokens of a page
-    // Slot (page * page_size + offset) of own index idx of sequence b, or -1.
+    // Slot (page * page_size + offset) of own index idx of sequence b, or -1.  kPastL1: see find_sequence().
+    template <bool kPastL1 = false>
     __device__ __forceinline__ long long slot(int b, long long idx) const {
         if (idx < 0 || (idx >> shift) >= max_pages) return -1;
-        const int page = __ldg(table + static_cast<long long>(b) * max_pages + (idx >> shift));
+        const int32_t *entry = table + static_cast<long long>(b) * max_pages + (idx >> shift);
+        const int page = kPastL1 ? __ldcg(entry) : __ldg(entry);
         if (page < 0 || page >= n_pages) return -1;
         return (static_cast<long long>(page) << shift) + (idx & ((1 << shift) - 1));
     }
@@ -28,8 +30,8 @@ struct PageTable {
 // The sequence that new token `tok` belongs to by the cumulative counts cu[0..B]
 // (the last b with cu[b] <= tok; -1 for rows outside all sequences), where it
 // begins and how many new tokens it has.  Warp-wide: 32 probes a level.  kPastL1: for a
-// kernel that reads the list before its wait for the kernel before it, when an SM's L1
-// may still hold what another call's list said.
+// kernel that starts under the one before it, when an SM's L1 may still hold what another
+// call's list said.
 template <bool kPastL1 = false>
 __device__ __forceinline__ int find_sequence(const int32_t *cu, int B, int tok, int lane, int *begin, int *count) {
     auto at = [](const int32_t *p) { return kPastL1 ? __ldcg(p) : __ldg(p); };

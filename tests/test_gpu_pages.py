@@ -498,3 +498,51 @@ def test_keep_in_a_graph_and_on_another_stream(cuda_dev):
     got = F.cp_cache_keep(handle, *lists, stream=s)
     s.synchronize()
     b.check(got)
+
+
+def test_keep_follows_pages_that_move_between_calls(cuda_dev):
+    """Plans and keeps in turns in one graph: every plan hands other pages to the sequences, and the keep that starts
+    under it reads that plan's table, lengths and counts."""
+    B, page, width, n_pages, steps, most, Nkv, D = 9, 16, 8, 60, 12, 6, 2, 64
+    g = np.random.default_rng(63)
+    s = Step(63, [0] * B, [0] * B, [0] * B, page, width, n_pages, 0)
+    new = [[int(g.integers(1, 60)) for _ in range(B)] for _ in range(steps)]
+    n_kept = [[min(n, int(g.integers(0, most + 1))) for n in row] for row in new]
+    kept = [[sorted(g.choice(n, k, replace=False).tolist()) + [-1] * (most - k) for n, k in zip(a, b)]
+            for a, b in zip(new, n_kept)]
+    for row in n_kept:  # and a step that ends in an empty sequence for some
+        row[3] = 0
+    t = torch.Generator().manual_seed(63)
+    caches = [torch.randn(n_pages, page, Nkv, D, generator=t).to(torch.bfloat16).to(cuda_dev) for _ in range(4)]
+    before = [c.clone() for c in caches]
+    first = [c.flatten(0, 1).clone() for c in caches]
+    table, stack = i32(s.table, cuda_dev), i32(s.stack, cuda_dev)
+    had, keep, n_free = i32([0] * B, cuda_dev), i32([0] * B, cuda_dev), i32([n_pages, 0], cuda_dev)
+    lists = [[i32(x[i], cuda_dev) for x in (new, kept, n_kept)] for i in range(steps)]
+    cu, R = i32([0] * (B + 1), cuda_dev), 60 * B
+    rows = [i32([0] * R, cuda_dev) for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for n, k, c in lists:
+            F.cp_cache_plan(had, keep, n, table, stack, n_free, page, R, 0, kv_len=had, cu_new=cu, slots=rows[0],
+                            pos=rows[1], n_free_out=n_free)
+            F.cp_cache_keep(caches, table, cu, had, k, c, kv_keep=keep)
+    graph.replay()
+    h, m, nf, tb, st = [0] * B, [0] * B, n_pages, [list(r) for r in s.table], list(s.stack)
+    moved = 0
+    for i in range(steps):
+        old = [list(r) for r in tb]
+        r = T.plan(h, m, new[i], tb, st, nf, page, R, 0)
+        assert r["n_free"][1] == 0
+        h, nf = r["kv_len"], r["n_free"][0]
+        moved += tb != old
+        at = lambda b, j: tb[b][j // page] * page + j % page  # noqa: E731
+        pairs = [(at(b, h[b] - new[i][b] + x), at(b, h[b] - new[i][b] + j))
+                 for b in range(B) for j, x in enumerate(kept[i][b][:n_kept[i][b]])]
+        source, target = [x for x, _ in pairs], [y for _, y in pairs]
+        for c in first:
+            c[target] = c[source]
+        m = [h[b] - new[i][b] + n_kept[i][b] for b in range(B)]
+    assert moved > steps // 2 and keep.tolist() == m and n_free.tolist() == [nf, 0]
+    for c, w, o in zip(caches, first, before):
+        assert torch.equal(c.flatten(0, 1), w) and not torch.equal(c, o)
