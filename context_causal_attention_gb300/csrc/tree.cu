@@ -1,6 +1,7 @@
 // tree.cu -- trees of drafted tokens: their ancestors and positions (cp_tree_plan), and attention over the paged cache by
-// them (cp_tree_attn_fwd: the kernels of prefix_call.cuh and prefix_tc.cuh, with a row's mask in the place of its
-// index wherever a key tile reaches into the step's new tokens).
+// them (cp_tree_attn_fwd: a block an item, tree_block.cuh, a cluster an item, tree_cluster.cuh, or the line of
+// prefix_call.cuh and prefix_tc.cuh, with a row's mask in the place of its index wherever a key tile reaches into the
+// step's new tokens).
 //
 // Ancestors.  mask_j = {j} + mask_parent(j).  A warp holds 32 tokens in a row, a token a lane, and follows the
 // parents among them by doubling (five rounds of shuffles, whatever the tree's shape): each token then knows its branch
@@ -15,6 +16,7 @@
 
 #include "cp_internal.h"
 #include "prefix_call.cuh"
+#include "tree_block.cuh"
 #include "tree_cluster.cuh"
 
 namespace cpattn {
@@ -132,7 +134,7 @@ const AtOnce &clusters_at_once() {
             cudaGetLastError();
             return;
         }
-        for (int i = 1; i <= kClMost; ++i) {
+        for (int i = 2; i <= kClMost; ++i) {
             cudaLaunchAttribute at[2] = {};
             cudaLaunchConfig_t c = cluster_config<D>(at, 1, i, nullptr);
             c.numAttrs = 1;
@@ -144,33 +146,54 @@ const AtOnce &clusters_at_once() {
     return most;
 }
 
-// Blocks of a cluster, or 0 where the line of prefix_call.cuh takes the call.  As many blocks as let all items run at
-// once; the line where that is one, or where the longest sequence that the table can hold would make a
-// block's share too many tiles of 128 keys: clusters are quick to begin and to end, the line shares the keys of
-// ragged sequences evenly and reads a prefix once.  Clusters and line, us (16 tokens, 32 / 8 heads of 128, pages of 32, own keys
-// up to the figure): one sequence of 500 13.5 and 15.5, of 4096 16.9 and 19.3, of 16000 (10 tiles) 26.6 and 25.4; four of
-// 4096 (8 tiles) 23 and 30, ragged 22 and 25, of 16000 (31) 54 and 64, ragged 52 and 48; nine of 4096 (16)
-// 36 and 51, ragged 35 and 36.  Up to 16 rows the line has its narrow tiles: four tokens of one sequence of 4000 keys
+// Blocks of a cluster of tree_cluster.cuh, or 0 where it does not take the call: clusters are quick to begin and to
+// end, the line of prefix_call.cuh shares the keys of ragged sequences evenly and reads a prefix once, and a block an item
+// (tree_block.cuh) needs no join.  As many blocks as let all items run at once, two at least; not where the longest
+// sequence that the table can hold would make a block's share too many tiles of 128 keys.  Clusters and line, us
+// (16 tokens, 32 / 8 heads of 128, pages of 32, own keys up to the figure): one sequence of 4096 16.9 and 19.3, of 16000 (10
+// tiles) 26.6 and 25.4; four of 4096 (8 tiles) 23 and 30, ragged 22 and 25, of 16000 (31) 54 and 64, ragged 52 and 48; nine of
+// 4096 (16) 36 and 51, ragged 35 and 36.  Up to 16 rows the line has its narrow tiles: four tokens of one sequence of 4000 keys
 // (3 tiles) 14.4 and 15.8, of two (4.5) 17.2 and 15.7, of four (8) 19.4 and 16.8.  A prefix is read once for each
-// sequence: two sequences of 500 behind 500 keys 13.5 and 18.1, behind 4000 (5) 21.8 and 20.4, four of 4000 behind 4000 (16) 29 and 26.
-// At D = 64 (16 / 4 heads) a tile costs half: four of 4000 behind 4000 (9) 19 and 25, behind 16000 (22) 36 and 30; four tokens
-// of eight sequences of 4000 (8) 15.8 and 16.0, of sixteen (16) 24 and 20.
-// With more items than two blocks each would find room for, a block an item still saves the line's beginning, partials
-// and join while its turns are few and short (16 tokens, 8 KV heads): 16 sequences of 500 keys 17.7 and 37, of 4096 55 and
-// 75, ragged 47 and 50; 20 of 4096 98 and 88 (eight blocks go a second time), ragged 50 and 56; 64 of 4096 212 and
-// 216, ragged 113 and 127; 300 of 500, ragged, 178 and 169.  At D = 64 32 of 4096 69 and 82, 64 138 and 128.
+// sequence: two sequences of 500 behind 4000 (5) 21.8 and 20.4, four of 4000 behind 4000 (16) 29 and 26.  At D = 64 (16 / 4
+// heads) a tile costs half: four of 4000 behind 4000 (9) 19 and 25, behind 16000 (22) 36 and 30; four tokens of eight
+// sequences of 4000 (8) 15.8 and 16.0, of sixteen (16) 24 and 20.
+// Up to 640 keys a block an item is quicker, as it needs no meeting of blocks: one sequence of 16 tokens behind 30 keys 5.6
+// us and 13.0, behind 500 10.8 and 13.4, 800 12.8 both, 1200 16.5 and 12.6; nine 6.0 and 11.8, 11.1 and 15.2, 13.2 and
+// 15.0, 16.9 and 15.3; at D = 64 two of 500 9.8 and 10.5, of 800 11.6 and 10.1.
 template <int D>
-int cluster_blocks(const ClusterArgs &c, int64_t max_new) {
+int cluster_blocks(const ClusterArgs &c, int64_t rows) {
     const PrefixArgs &a = c.p;
     const long long items = static_cast<long long>(a.B) * c.tiles * a.Nkv;
     const AtOnce &most = clusters_at_once<D>();
     const long long keys = a.P + (static_cast<long long>(a.own.max_pages) << a.own.shift);
-    const int tiles = (D == 64 ? 2 : 1) * (a.P > 0 ? 8 : max_new * a.G <= kTcRows ? 4 : 16);
+    if (keys <= 640) return 0;
+    const int tiles = (D == 64 ? 2 : 1) * (a.P > 0 ? 8 : rows <= kTcRows ? 4 : 16);
     for (int i = kClMost; i >= 2; --i)
         if (items <= most.clusters[i]) return keys <= 128LL * i * tiles ? i : 0;
-    if (most.clusters[1] && a.P == 0 && max_new * a.G > kTcRows && items <= (D == 64 ? 256 : 512) && keys <= 128LL * 48)
-        return 1;
     return 0;
+}
+
+// Whether a block an item (tree_block.cuh), two on an SM, takes the call, rather than the line.  A tile of 64
+// keys takes a block 0.75 us at both D, so the longest sequence that the table holds takes 0.75 k, k its tiles, and all
+// items together, half as long on average, items k / 2 x 0.75 / 304 at best (measured 1.3 times that: half of the time
+// memory is what they wait for).  The line reads the keys once for 256 rows, a prefix once for all sequences,
+// whatever the lengths, at 5 TB/s (6.5 by its narrow tiles), and takes 20 us (13) and 0.05 us (0.03) an item of its own
+// besides.  Block and line, us (16 tokens, 32 / 8 heads of 128, pages of 16, own keys up to the figure, ragged): 16 sequences of 4096
+// 48 and 50, of 8000 87 and 71 (not ragged 94 and 113), 32 of 8000 109 and 115, 64 of 4096 86 and 126, of 16000 314 and 349; 300 of
+// 500 78 and 175, of 1000 117 and 220; 27 tokens of 100 of 1000 58 and 97, 60 tokens of 60 59 and 80, 120 of 60 of 2000
+// 163 both.  Single tokens of 20 sequences of 500 11.1 and 15.9, of 4000 47 and 38, 64 of 4000 89 and 102, not ragged of 32000 1187 and
+// 1238.  Behind a prefix of 500 64 of 1000 44 and 103, 200 of 300 81 and 162, of 2000 79 and 116, 184 and 192.  At D = 64 (16 /
+// 4 heads) 40 of 4000 43 and 36, 64 49 and 58, 200 99 and 118.
+template <int D>
+bool items_pay(const ClusterArgs &c, int64_t rows) {
+    const PrefixArgs &a = c.p;
+    const double own = static_cast<double>(static_cast<long long>(a.own.max_pages) << a.own.shift), tile = 0.75;
+    const double items = static_cast<double>(a.B) * c.tiles * a.Nkv, shared = static_cast<double>(a.B) * a.Nkv * ((rows + 255) / 256);
+    if (items > 1e9) return false;  // (a launch has fewer than 2^31 blocks)
+    const double longest = (a.P + own) / kBlKeys * tile, all = items * (a.P + own / 2) / kBlKeys * 1.3 * tile / (2 * sm_count());
+    const double bytes = shared * own / 2 * 4 * D;
+    const double line = rows <= kTcRows ? 13 + bytes / 6.5e6 + 0.03 * shared : 20 + bytes / 5e6 + 0.05 * shared;
+    return longest <= line && all <= line;
 }
 
 template <int D>
@@ -180,6 +203,24 @@ cp_status launch_clusters(const ClusterArgs &a, int blocks, cudaStream_t stream)
     const cudaError_t e = cudaLaunchKernelEx(&c, tree_cluster_kernel<D>, a);
     if (e != cudaSuccess) cudaGetLastError();
     return cuda_status(e);
+}
+
+// A block an item, two on an SM; the longest sequences' first where they do not all run at once and the order is
+// worth what finding it costs each block, 6 ns a sequence, against a quarter of the longest item's time: 64
+// sequences of up to 4096 keys 86 us and 101 without, 32 tokens of 32 of 2000 40 and 50; 150 of 1000 68 and 60.
+template <int D>
+cp_status launch_items(const ClusterArgs &a, cudaStream_t stream) {
+    static cudaError_t err = cudaSuccess;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(tree_block_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BlCfg<D>::kSmem);
+    });
+    if (err != cudaSuccess) return cuda_status(err);
+    const int64_t items = static_cast<int64_t>(a.p.B) * a.tiles * a.p.Nkv, at_once = 2LL * sm_count();
+    const double keys = static_cast<double>(a.p.P + (static_cast<long long>(a.p.own.max_pages) << a.p.own.shift));
+    const bool order = a.p.B <= kBlThreads && items > at_once && 0.006 * a.p.B * items / at_once < 0.75 / 4 * keys / kBlKeys;
+    const BlockArgs x{a, order};
+    return launch(tree_block_kernel<D>, dim3(static_cast<unsigned>(items)), kBlThreads, BlCfg<D>::kSmem, stream, x);
 }
 
 }  // namespace
@@ -239,8 +280,12 @@ extern "C" cp_status cp_tree_attn_fwd(const void *q, const void *k_cache, const 
                                           prefix_len, table, B, max_pages, cu_new, kv_len, max_new, R, N, Nkv, D,
                                           scale, o, o_dtype, lse, workspace, ws_bytes, 2000000000ull, false);
     if (st != CP_OK) return st;
-    ClusterArgs few{c.a, static_cast<int>((max_new * c.a.G + 127) / 128), o, o_dtype == CP_BF16, lse};
-    const int blocks = D == 128 ? cluster_blocks<128>(few, max_new) : cluster_blocks<64>(few, max_new);
+    const int64_t rows = max_new * c.a.G;  // of an item, about
+    auto form = [&](int tile) { return ClusterArgs{c.a, static_cast<int>((rows + tile - 1) / tile), o, o_dtype == CP_BF16, lse}; };
+    const ClusterArgs few = form(128), many = form(kBlRows);
+    const int blocks = D == 128 ? cluster_blocks<128>(few, rows) : cluster_blocks<64>(few, rows);
     if (blocks) return D == 128 ? launch_clusters<128>(few, blocks, stream) : launch_clusters<64>(few, blocks, stream);
+    if (D == 128 ? items_pay<128>(many, rows) : items_pay<64>(many, rows))
+        return D == 128 ? launch_items<128>(many, stream) : launch_items<64>(many, stream);
     return launch_line<true>(c, stream);
 }

@@ -41,9 +41,9 @@ class TreeCall(Call):
         self.mask = torch.from_numpy(mask)
 
     def run(self, dev, hint=None, form=None, **kw):
-        if form == "line":
-            # a table for more tokens than a cluster takes: the same call by the line's kernels
-            wide = 140000 // self.b.page
+        if form in ("clusters", "line"):
+            # a table for more tokens than a block an item takes, or than a cluster: the same call by other kernels
+            wide = (140000 if form == "line" else 700) // self.b.page
             self.table = torch.cat([self.table, torch.full((len(self.new), wide), -3, dtype=torch.int32)], 1)
         self.dev = [t.to(dev) for t in (self.q, self.k, self.v, self.mask, self.pages, self.table, self.cu, self.kv_len)]
         return self.again(hint, **kw)
@@ -86,9 +86,10 @@ CASES = {
     "one_kv_head": ([9, 3], [9, 300], 77, 40, 1, 64, 256, 1, 0),
     "no_groups": ([13, 6], [200, 13], 500, 16, 16, 64, 16, 1, 0),
     "odd_groups": ([11, 2, 30], [90, 2, 400], 257, 21, 3, 128, 128, 1, 0),
-    # one block an item: more items than SMs, and fewer
+    # more items than find room at once, the longest first, and fewer
     "blocks": ([9 + i % 20 for i in range(30)], [9 + i % 20 + 37 * i % 300 for i in range(30)], 0, 32, 8, 128, 16, 1, 1),
     "blocks_few": ([5 + 7 * i % 60 for i in range(22)], [70 + 91 * i % 900 for i in range(22)], 0, 16, 4, 64, 32, 2, 0),
+    "blocks_equal": ([9] * 40 + [1, 0] * 20, [300, 9] * 20 + [300, 0] * 20, 70, 32, 8, 64, 16, 1, 2),
     "many": ([1 + i % 6 for i in range(200)], [10 + 7 * i % 300 for i in range(200)], 130, 8, 2, 64, 16, 1, 0),
     "many_wide": ([5 + 13 * i % 60 for i in range(150)], [70 + 37 * i % 700 for i in range(150)], 0, 8, 1, 128, 64, 2, 0),
     "most_sequences": ([1 + i % 2 for i in range(4096)], [2 + i % 40 for i in range(4096)], 30, 2, 1, 64, 16, 1, 0),
@@ -97,7 +98,7 @@ CASES = {
 
 @pytest.mark.parametrize("name", sorted(CASES))
 @pytest.mark.parametrize("kind", ["random", "any", "chain"])
-@pytest.mark.parametrize("form", ["as_chosen", "line"])
+@pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
 def test_against_64_bits(cuda_dev, name, kind, form):
     new, length, prefix, N, Nkv, D, page, words, pad = CASES[name]
     c = TreeCall(len(name), new, length, prefix, N, Nkv, D, page, words, kind, pad)
@@ -124,7 +125,7 @@ def test_a_chain_is_the_prefix_attention(cuda_dev, name):
 
 @pytest.mark.parametrize("garbage", [float("nan"), float("inf"), 3e38])
 @pytest.mark.parametrize("name", ["narrow", "half_tile_prefix", "wide", "with_prompts", "one"])
-@pytest.mark.parametrize("form", ["as_chosen", "line"])
+@pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
 def test_what_unused_slots_hold_does_not_matter(cuda_dev, name, garbage, form):
     new, length, prefix, N, Nkv, D, page, words, pad = CASES[name]
     clean = TreeCall(3, new, length, prefix, N, Nkv, D, page, words, "random", pad)
@@ -134,7 +135,7 @@ def test_what_unused_slots_hold_does_not_matter(cuda_dev, name, garbage, form):
     assert torch.equal(a[0][:n], b[0][:n]) and torch.equal(a[1][:, :n], b[1][:, :n])
 
 
-@pytest.mark.parametrize("form", ["as_chosen", "line"])
+@pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
 @pytest.mark.parametrize("name", ["narrow", "half_tile_prefix", "wide"])
 def test_keys_that_a_row_does_not_see_are_hidden_whatever_they_hold(cuda_dev, name, form):
     """NaN, infinities and the lowest value in drafted K rows: rows that do not see them keep their values (to the
@@ -180,7 +181,7 @@ def test_rows_that_see_nothing(cuda_dev):
         assert (o[:6] == 0).all()
 
 
-@pytest.mark.parametrize("form", ["as_chosen", "line"])
+@pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
 @pytest.mark.parametrize("N,n", [(2, 5), (16, 30), (32, 60)])
 def test_a_row_that_sees_one_key_gives_its_value(cuda_dev, N, n, form):
     """One weight, whatever its score: o is that key's value to the bit."""
@@ -194,7 +195,7 @@ def test_a_row_that_sees_one_key_gives_its_value(cuda_dev, N, n, form):
 
 @pytest.mark.parametrize("gain", [30.0, 300.0])
 @pytest.mark.parametrize("N", [2, 16])
-@pytest.mark.parametrize("form", ["as_chosen", "line"])
+@pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
 def test_large_scores(cuda_dev, gain, N, form):
     c = TreeCall(6, [7, 12], [500, 900], 700, N, 2, 64, 16, 1, gain=gain)
     for s, m in enumerate(c.b.length):
@@ -205,7 +206,7 @@ def test_large_scores(cuda_dev, gain, N, form):
     c.check(o, lse, "fp32", "gain", gain)
 
 
-@pytest.mark.parametrize("form", ["as_chosen", "line"])
+@pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
 @pytest.mark.parametrize("name", ["narrow_edges", "half_tile_prefix", "wide", "with_prompts"])
 def test_same_bits_twice_on_a_stream_and_by_graph(cuda_dev, name, form):
     new, length, prefix, N, Nkv, D, page, words, pad = CASES[name]
@@ -320,7 +321,7 @@ def test_outputs_and_workspace_stay_in_bounds(cuda_dev):
 
 @pytest.mark.parametrize("what", ["page", "prefix_page", "length", "negative_length", "counts", "counts_past_rows"])
 @pytest.mark.parametrize("N", [4, 32])
-@pytest.mark.parametrize("form", ["as_chosen", "line"])
+@pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
 def test_bad_lists_are_reported(cuda_dev, what, N, form):
     c = TreeCall(9, [2, 3], [50, 40], 70, N, 2, 64, 16, 1)
     good = [t.clone() for t in c.run(cuda_dev, form=form)]
@@ -341,7 +342,7 @@ def test_bad_lists_are_reported(cuda_dev, what, N, form):
     assert F.cp_device_status() == 11
     assert F.cp_device_status() == 0
     if what in ("page", "length", "negative_length"):
-        if form == "as_chosen":  # (a cluster sees one sequence)
+        if form != "line":  # (a block or a cluster sees one sequence)
             assert torch.equal(o[2:], good[0][2:]) and torch.equal(lse[:, 2:], good[1][:, 2:])
         # The line is cut in other places where the first sequence has another length, and a piece's weights are rounded
         # relative to the piece's own maximum: off by half a step of themselves either way, so within the same bounds.
