@@ -55,6 +55,19 @@ struct BlCfg {
     static_assert(kSmem + 1024 <= 228 * 1024 / 2 && kStages * kTile >= kAtomQ, "shared memory budget");
 };
 
+// Whether the phase of parity `parity` is over, without a wait.
+__device__ __forceinline__ bool mbar_test(const uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 struct BlockArgs {
     ClusterArgs c;
     int longest_first;  // the order of the items: the longest sequences' first (B up to kBlThreads)
@@ -257,12 +270,14 @@ __global__ void __launch_bounds__(kBlThreads, 2) tree_block_kernel(const __grid_
                     seen1 = tree ? tree_bits(a, x, tok, key + 32) : limit_bits(limit, key + 32);
                 }
                 const uint32_t it = kv + j, tS = tmem + lane_off + (it & 1u) * 64;
-                ok = mbar_wait_warp(s_full + (it & 1u), (it >> 1) & 1u, abort_flag, a.timeout_ns);
+                // (the product before last has ended, as these scores came behind it; each phase is seen.  Both barriers are
+                // asked at once: a wait for one that is over costs 130 clk of a tile's 1200)
+                const uint32_t ph = (it >> 1) & 1u;
+                const bool there = mbar_test(s_full + (it & 1u), ph) & (j < 2 || mbar_test(o_full + (it & 1u), ph ^ 1u));
+                ok = __all_sync(0xffffffffu, there) ||
+                     (mbar_wait_warp(s_full + (it & 1u), ph, abort_flag, a.timeout_ns) && (j < 2 || ended(it - 2)));
                 if (!ok) break;
                 if (busy) {
-                    // (the product before last has ended, as these scores came behind it; each phase is seen)
-                    ok = j < 2 || ended(it - 2);
-                    if (!ok) break;
                     tc_fence_after();
                     uint32_t h[64], pk[32];
                     tmem_ld64(tS, h);
