@@ -473,7 +473,8 @@ __device__ __forceinline__ void copy_rows(uint32_t at, uint32_t sw, const char *
 // heads each, pages of 16: 229 us, 216 so; heads of 64: 171 and 135; 64 single tokens behind 32768 keys as before).
 // That loop, for the tiles at the end of the keys or with a bad page, is not unrolled: code that is read for the
 // first time costs more than the loop.
-template <int D, int KT, int kAtom>  // KT: a multiple of 16, here also a part of a tile
+// kEnds: 16-row groups without a key are left as they are, for products that end with the keys' last group.
+template <int D, int KT, int kAtom, bool kEnds = false>  // KT: a multiple of 16, here also a part of a tile
 __device__ __forceinline__ void copy_tile(const PrefixArgs &a, const Piece &x, const PageWindow &win,
                                           const __nv_bfloat16 *cache, uint32_t dst, int key0, int lane) {
     constexpr int kChunks = D / 8, kRpi = 32 / kChunks;  // 16-byte chunks of a row, rows of an instruction
@@ -497,6 +498,7 @@ __device__ __forceinline__ void copy_tile(const PrefixArgs &a, const Piece &x, c
 #pragma unroll 2
     for (int g = 0; g < KT / 16; ++g, at += 16 * 128) {
         const int left = x.keys - key0 - 16 * g, row = __shfl_sync(0xffffffffu, mine, g);
+        if (kEnds && left <= 0) break;
         const bool there = row >= 0;
         const char *src = lane_src + (there ? row : 0) * row_bytes;
         if (there && left >= 16) {

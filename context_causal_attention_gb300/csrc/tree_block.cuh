@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kBlThreads, 2) tree_block_kernel(const __grid_
                 win.advance(key >> a.own.shift, lane);
                 const uint32_t it = kv + j, st = it % C::kStages;
                 if (!mbar_wait_warp(empty + st, ((it / C::kStages) & 1u) ^ 1u, abort_flag, a.timeout_ns)) break;
-                copy_tile<D, kBlKeys, C::kAtom>(a, y, win, cache, ring + st * C::kTile, key, lane);
+                copy_tile<D, kBlKeys, C::kAtom, true>(a, y, win, cache, ring + st * C::kTile, key, lane);
                 copies_arrive(full + st);
             }
         } else if (warp == 3) {
@@ -223,9 +223,11 @@ __global__ void __launch_bounds__(kBlThreads, 2) tree_block_kernel(const __grid_
                 if (!ok) break;
                 tc_fence_after();
                 fence_async_shared();
+                const bool pre = j < prefix_tiles;
+                const int left = (pre ? prefix : x.keys) - (j - (pre ? 0 : prefix_tiles)) * kBlKeys;
 #pragma unroll
                 for (int k = 0; k < kBlKeys / 16; ++k)
-                    mma_ts(tO, tmem + (it & 1u) * 64 + 8 * k, dv + st * kStageDesc + 128 * k, kIdescPV, j > 0 || k > 0, lead);
+                    if (16 * k < left) mma_ts(tO, tmem + (it & 1u) * 64 + 8 * k, dv + st * kStageDesc + 128 * k, kIdescPV, j > 0 || k > 0, lead);
                 commit(v_empty + st, lead);
                 commit(o_full + (it & 1u), lead);
             }

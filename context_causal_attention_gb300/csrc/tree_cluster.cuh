@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kClThreads, 1) tree_cluster_kernel(const __gri
                 win.advance(key >> a.own.shift, lane);
                 const uint32_t it = kv + j, st = it % stages;
                 if (!mbar_wait_warp(empty + st, ((it / stages) & 1u) ^ 1u, abort_flag, a.timeout_ns)) break;
-                copy_tile<D, 128, C::kAtom>(a, y, win, warp ? a.v : a.k, ring + st * C::kTile, key, lane);
+                copy_tile<D, 128, C::kAtom, true>(a, y, win, warp ? a.v : a.k, ring + st * C::kTile, key, lane);
                 copies_arrive(full + st);
             }
         } else if (warp < 4) {
@@ -237,9 +237,11 @@ __global__ void __launch_bounds__(kClThreads, 1) tree_cluster_kernel(const __gri
                 ++mine;
                 tc_fence_after();
                 fence_async_shared();
+                const bool pre = k0 + j < prefix_tiles;
+                const int left = (pre ? prefix : x.keys) - (k0 + j - (pre ? 0 : prefix_tiles)) * 128;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    mma_ts(tO, tP + 8 * k, dv + st * kStageDesc + 128 * k, kIdescPV, j > i || k > 0, lead);
+                    if (16 * k < left) mma_ts(tO, tP + 8 * k, dv + st * kStageDesc + 128 * k, kIdescPV, j > i || k > 0, lead);
                 commit(v_empty + st, lead);
                 return true;
             };
@@ -417,26 +419,16 @@ __global__ void __launch_bounds__(kClThreads, 1) tree_cluster_kernel(const __gri
         const int pieces = twice ? 2 * blocks : blocks, by = twice;
         for (int i = rank + blocks * warp; i < rows; i += blocks * (kClThreads / 32)) {
             constexpr int kV = D / 32;
-            const float2 ml = lane < pieces ? ld_cluster2(at_rank(ml_at + ((lane & by) * 64 + i) * 8, lane >> by))
-                                            : make_float2(-INFINITY, 0.f);
-            float top = ml.x;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
-            float sum = w * ml.y;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             const uint32_t chunk = kV == 4 ? lane : lane >> 1;
             const uint32_t from = o_at + i * D * 4 + ((chunk ^ (i & (D / 4 - 1))) << 4) + (kV == 4 ? 0 : (lane & 1) * 8);
-            float acc[kV];
+            const float2 ml = lane < pieces ? ld_cluster2(at_rank(ml_at + ((lane & by) * 64 + i) * 8, lane >> by))
+                                            : make_float2(-INFINITY, 0.f);
+            // eight pieces' rows on their way together, the first ones beside the sums
+            constexpr int kAtOnce = 8;
+            float v[kAtOnce][kV];
+            auto fetch = [&](int r0) {
 #pragma unroll
-            for (int e = 0; e < kV; ++e) acc[e] = 0.f;
-            // four pieces' rows on their way together
-            for (int r0 = 0; r0 < pieces; r0 += 4) {
-                float v[4][kV], f[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    f[r] = __shfl_sync(0xffffffffu, w, r0 + r);  // (0 behind the last)
+                for (int r = 0; r < kAtOnce; ++r)
                     // (64 rows further the swizzle is the same)
                     if (r0 + r < pieces) {
                         const uint32_t at = at_rank(from + ((r0 + r) & by) * 64 * D * 4, (r0 + r) >> by);
@@ -448,12 +440,29 @@ __global__ void __launch_bounds__(kClThreads, 1) tree_cluster_kernel(const __gri
                             v[r][0] = y.x, v[r][1] = y.y;
                         }
                     }
+            };
+            fetch(0);
+            float top = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
+            float sum = w * ml.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            float acc[kV];
+#pragma unroll
+            for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+            for (int r0 = 0;;) {
+#pragma unroll
+                for (int r = 0; r < kAtOnce; ++r) {
+                    const float f = __shfl_sync(0xffffffffu, w, r0 + r);  // (0 behind the last)
+                    if (f != 0.f)                                         // (a piece that saw nothing may hold anything)
+#pragma unroll
+                        for (int e = 0; e < kV; ++e) acc[e] += f * v[r][e];
                 }
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (f[r] != 0.f)  // (a piece that saw nothing may hold anything)
-#pragma unroll
-                        for (int e = 0; e < kV; ++e) acc[e] += f[r] * v[r][e];
+                r0 += kAtOnce;
+                if (r0 >= pieces) break;
+                fetch(r0);
             }
             const float inv = top == -INFINITY ? 0.f : 1.f / sum;
             const int at = x.row0 + i, tok = static_cast<int>(fdiv(static_cast<uint32_t>(at), a.div_g));
