@@ -150,16 +150,15 @@ const AtOnce &clusters_at_once() {
 // end, the line of prefix_call.cuh shares the keys of ragged sequences evenly and reads a prefix once, and a block an item
 // (tree_block.cuh) needs no join.  As many blocks as let all items run at once, two at least; not where the longest
 // sequence that the table can hold would make a block's share too many tiles of 128 keys.  Clusters and line, us
-// (16 tokens, 32 / 8 heads of 128, pages of 32, own keys up to the figure): one sequence of 4096 16.9 and 19.3, of 16000 (10
-// tiles) 26.6 and 25.4; four of 4096 (8 tiles) 23 and 30, ragged 22 and 25, of 16000 (31) 54 and 64, ragged 52 and 48; nine of
-// 4096 (16) 36 and 51, ragged 35 and 36.  Up to 16 rows the line has its narrow tiles: four tokens of one sequence of 4000 keys
-// (3 tiles) 14.4 and 15.8, of two (4.5) 17.2 and 15.7, of four (8) 19.4 and 16.8.  A prefix is read once for each
-// sequence: two sequences of 500 behind 4000 (5) 21.8 and 20.4, four of 4000 behind 4000 (16) 29 and 26.  At D = 64 (16 / 4
-// heads) a tile costs half: four of 4000 behind 4000 (9) 19 and 25, behind 16000 (22) 36 and 30; four tokens of eight
-// sequences of 4000 (8) 15.8 and 16.0, of sixteen (16) 24 and 20.
-// Up to 640 keys a block an item is quicker, as it needs no meeting of blocks: one sequence of 16 tokens behind 30 keys 5.6
-// us and 13.0, behind 500 10.8 and 13.4, 800 12.8 both, 1200 16.5 and 12.6; nine 6.0 and 11.8, 11.1 and 15.2, 13.2 and
-// 15.0, 16.9 and 15.3; at D = 64 two of 500 9.8 and 10.5, of 800 11.6 and 10.1.
+// (16 tokens, 32 / 8 heads of 128, pages of 32, own keys up to the figure): one sequence of 4096 13.6 and 19.3, of 16000
+// 20.6 and 24.3; four of 4096 18.8 and 30, of 8000 31 and 40, ragged 26 and 32, of 16000 (31 tiles) 51 and 62, ragged 45 and 49;
+// seven of 6000 (24) 38 and 52, ragged 32 and 29; nine of 4096 (16) 35 and 50, ragged 27 and 34.  At D = 64 (16 / 4 heads) 16 of
+// 4000 ragged 19 and 24, of 8000 (31) 31 both, four of 32000 (31) 38 and 32.  Up to 16 rows the line has its narrow tiles:
+// four tokens of two sequences of 4000 keys, ragged, 13.1 and 15.9, of four (8) 14.8 and 17.3; at D = 64 of 16 (16) 17.9 and
+// 18.6.  A prefix is read once for each sequence: two of 500 behind 8000 20 and 25, four of 4000 behind 4000 (16) 24 and 32,
+// at D = 64 behind 16000 (39) 27 and 28.
+// Up to 640 keys a block an item is quicker, as it needs no meeting of blocks: one sequence of 16 tokens behind 500 keys
+// 9.9 us and 11.5, behind 800 12.8 and 11.4; nine 10.3 and 13.2, 13.2 and 13.8; at D = 64 two of 500 9.1 and 8.7.
 template <int D>
 int cluster_blocks(const ClusterArgs &c, int64_t rows) {
     const PrefixArgs &a = c.p;
@@ -167,29 +166,32 @@ int cluster_blocks(const ClusterArgs &c, int64_t rows) {
     const AtOnce &most = clusters_at_once<D>();
     const long long keys = a.P + (static_cast<long long>(a.own.max_pages) << a.own.shift);
     if (keys <= 640) return 0;
-    const int tiles = (D == 64 ? 2 : 1) * (a.P > 0 ? 8 : rows <= kTcRows ? 4 : 16);
+    const int tiles = a.P > 0 ? (D == 64 ? 32 : 16) : rows <= kTcRows ? 16 : 32;
     for (int i = kClMost; i >= 2; --i)
         if (items <= most.clusters[i]) return keys <= 128LL * i * tiles ? i : 0;
     return 0;
 }
 
 // Whether a block an item (tree_block.cuh), two on an SM, takes the call, rather than the line.  A tile of 64
-// keys takes a block 0.75 us at both D, so the longest sequence that the table holds takes 0.75 k, k its tiles, and all
+// keys takes a block 0.75 us, so the longest sequence that the table holds takes 0.75 k, k its tiles, and all
 // items together, half as long on average, items k / 2 x 0.75 / 304 at best (measured 1.3 times that: half of the time
 // memory is what they wait for).  The line reads the keys once for 256 rows, a prefix once for all sequences,
 // whatever the lengths, at 5 TB/s (6.5 by its narrow tiles), and takes 20 us (13) and 0.05 us (0.03) an item of its own
 // besides.  Block and line, us (16 tokens, 32 / 8 heads of 128, pages of 16, own keys up to the figure, ragged): 16 sequences of 4096
-// 48 and 50, of 8000 87 and 71 (not ragged 94 and 113), 32 of 8000 109 and 115, 64 of 4096 86 and 126, of 16000 314 and 349; 300 of
-// 500 78 and 175, of 1000 117 and 220; 27 tokens of 100 of 1000 58 and 97, 60 tokens of 60 59 and 80, 120 of 60 of 2000
-// 163 both.  Single tokens of 20 sequences of 500 11.1 and 15.9, of 4000 47 and 38, 64 of 4000 89 and 102, not ragged of 32000 1187 and
-// 1238.  Behind a prefix of 500 64 of 1000 44 and 103, 200 of 300 81 and 162, of 2000 79 and 116, 184 and 192.  At D = 64 (16 /
-// 4 heads) 40 of 4000 43 and 36, 64 49 and 58, 200 99 and 118.
+// 47 and 50, of 8000 87 and 71 (not ragged 94 and 113), 32 of 8000 109 and 115, 64 of 4096 85 and 126, of 8000 159 and 200; 300 of
+// 500 78 and 175, of 1000 117 and 220; 27 tokens of 100 of 1000 58 and 97, 60 tokens of 60 59 and 81, 120 of 60 of 2000
+// 163 both.  Single tokens of 20 sequences of 500 11.2 and 16.1, of 4000 47 and 38, 64 of 4000 87 and 102.  Behind a prefix
+// of 500 64 of 1000 44 and 103, 200 of 300 81 and 162, of 2000 79 and 116, 184 and 192.  At D = 64 (16 / 4 heads) 40 of
+// 4000 40 and 36, 64 47 and 58, 200 95 and 118.
+// Beyond 8192 keys the line gains by itself (64 of 16000 310 and 349), and one long sequence among short ones would leave
+// a block alone with it.
+constexpr int kBlMost = 8192;
 template <int D>
 bool items_pay(const ClusterArgs &c, int64_t rows) {
     const PrefixArgs &a = c.p;
     const double own = static_cast<double>(static_cast<long long>(a.own.max_pages) << a.own.shift), tile = 0.75;
     const double items = static_cast<double>(a.B) * c.tiles * a.Nkv, shared = static_cast<double>(a.B) * a.Nkv * ((rows + 255) / 256);
-    if (items > 1e9) return false;  // (a launch has fewer than 2^31 blocks)
+    if (a.P + own > kBlMost || items > 1e9) return false;  // (a launch has fewer than 2^31 blocks)
     const double longest = (a.P + own) / kBlKeys * tile, all = items * (a.P + own / 2) / kBlKeys * 1.3 * tile / (2 * sm_count());
     const double bytes = shared * own / 2 * 4 * D;
     const double line = rows <= kTcRows ? 13 + bytes / 6.5e6 + 0.03 * shared : 20 + bytes / 5e6 + 0.05 * shared;
