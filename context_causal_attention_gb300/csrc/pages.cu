@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 }
 
 // ---------------------------------------------------------------- the accepted branch
-constexpr int kKeepThreads = 64;
+constexpr int kKeepThreads = 128;
 constexpr int kMaxCaches = 256;  // K and V of 128 layers: their addresses are launch arguments
 constexpr int kMaxKept = 512;    // tokens of a path: as many as a mask's row holds
 constexpr int kAhead = 4;        // rows in flight of a thread, of each of two columns
@@ -489,13 +489,13 @@ extern "C" cp_status cp_cache_keep(void *const *caches, int64_t n_caches, int64_
     a.cols = static_cast<int>(Nkv * D / 8);
     if ((st = cache_status_word(&a.status)) != CP_OK) return st;
     const int64_t all = n_caches * a.cols;
-    // As many rounds of two columns a thread as leave about twelve small blocks an SM: what a block does first costs
+    // As many rounds of two columns a thread as leave about eight small blocks an SM: what a block does first costs
     // it three loads in a row, which others' copies have to cover.  A small call needs many blocks, each soon begun.
-    // (Up to 6 of 16 tokens of 64 sequences in 32 layers, and of 27 tokens of one in 16: 12 blocks of 64 threads 8.4 and
-    // 2.7 us in a graph, 8 of 128 threads 8.7 and 2.8, 4 of 256 9.5 and 3.2, 2 of 512 10.9; with six rows in flight 9.2
-    // and 3.1.)
+    // (Up to 6 of 16 tokens of 64 sequences in 32 layers, and of 27 tokens of one in 16, us in a graph: 8 blocks of 128
+    // threads 8.7 and 2.9, call after call with other data 9.1; 4 of 256 threads 9.6 and 3.2, 9.5; 2 of 256 10.2, 10.4; 12 of
+    // 64 8.5 and 2.8, but 11.1; with six rows in flight 8.6 and 3.1.)
     const int64_t pairs = (all + 2 * kKeepThreads - 1) / (2 * kKeepThreads);
-    int64_t most = (12LL * sm_count() + B - 1) / B;
+    int64_t most = (8LL * sm_count() + B - 1) / B;
     most = most < pairs ? most : pairs;
     most = most < 4096 ? most : 4096;
     a.units = static_cast<int>((pairs + most - 1) / most * 2 * kKeepThreads);
