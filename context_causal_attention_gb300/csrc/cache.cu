@@ -6,7 +6,8 @@
 // table[b][i / page_size].  K: norm, rotation, bf16, into that slot; V: bf16,
 // into the same slot of the other cache; Q: norm, rotation, bf16, in place
 // order.  Norm and rotation as in rope.cu.  cp_cache_append_at takes slots and positions as
-// lists instead (drafted tokens of a tree: siblings share a position).
+// lists instead (drafted tokens of a tree: siblings share a position): 16 of them for each of 64 sequences, 32 / 8
+// heads of 128, normed and rotated, take 6.5 us in a graph, 3.7 at the copy's rate; slot, row and phase follow one another.
 //
 // Memory-bound where there are many tokens and latency-bound at one token for
 // each sequence, so one launch does all three tensors: a warp takes a token

@@ -6,11 +6,13 @@
 // running sums over the sequences (new tokens, pages taken, pages given), which every block of one cluster forms
 // for itself (4096 sequences at most: four a thread); then each new row, and each moved page, looks for its
 // sequence in the sums in shared memory.  Results may overwrite the lists they come from, so they are written behind a
-// barrier of the cluster.  What bounds it is latency: the launch, the lists, the barrier, a page number.
+// barrier of the cluster.  What bounds it is latency: the launch, the lists, the barrier, a page number.  In a graph 64
+// sequences of one token take 3.7 us, 1000 of up to 60 tokens 6.4 (8.5 by sums of 64 bits in a cluster of 8).
 //
 // cp_cache_keep.  Row j of the kept path comes from row path_j >= j of the step, so a thread that takes 16
 // bytes of all rows of one sequence in one cache, in rising order, never overwrites what it still has to read, and
-// no thread waits for another.  Bound by memory where there are many layers and sequences.
+// no thread waits for another.  Bound by the latency of scattered rows: up to 6 of 16 tokens of 64 sequences in 32 layers,
+// 10.5 MB read and as much written at rows of 2 KB, take 8.7 us in a graph (3.1 at the copy's rate).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -46,8 +46,8 @@ namespace {
 
 constexpr int kTcThreads = 384;
 // Pages of this many tokens or more are copied by TMA, smaller ones by cp.async
-// (see copy_tile).  64 rows over 32768 keys in pages of 16 take 62.6 us by TMA and 60.5
-// by cp.async; prompts over pages of 64 359.5 by TMA and 367.7 by cp.async.
+// (see copy_tile).  Prompts and trees over 16384 keys in pages of 128 take 1063 us by TMA and
+// 1095 by cp.async, 64 trees of 16 rows in pages of 64 129 and 124.
 constexpr int kTmaPage = 64;
 
 template <int D>

@@ -1,8 +1,8 @@
 // tree_cluster.cuh -- the tree attention of few sequences: one launch of thread-block clusters, without a plan of
 // the work, partials in global memory or a second launch.
 //
-// Few sequences are latency: the line of prefix_call.cuh (its scan, the search of a block's place, the partials' way
-// through global memory, the join) takes 16 of a call's 20 us where the keys take 3.  Here a cluster of up to 16 blocks
+// Few sequences are latency: a tree of 27 tokens over 4096 keys takes 19 us by the line of prefix_call.cuh (its scan, the
+// search of a block's place, the partials' way through global memory, the join) and 12 so, where the keys take 3.  Here a cluster of up to 16 blocks
 // takes one item -- 128 rows (tokens x the G query heads of a KV head) of one sequence -- and its blocks an equal share
 // of the item's key tiles each, first the prefix's and then the sequence's own.  Where a block works follows from
 // its index alone, and the blocks join their partials through each other's shared memory.
@@ -13,8 +13,9 @@
 // weights are formed (and moved only when a weight would pass 2^30), so nothing is computed twice.  It is the score itself, not
 // a whole number above it: the weight of a row's only key is 1 then, and its output that key's value.
 // A tile's code is a loop over 64 columns, not unrolled over 128: a block goes through two to thirty tiles, and code
-// that is read for the first time costs more than the loop (a tree of 27 tokens over 4096 keys takes 15.6 us so, 17.0 with
-// the weights of 128 columns in a row and the maximum looked for only when their sum asks for it).
+// that is read for the first time costs more than the loop (1.4 us less than with the weights of 128 columns in a row and
+// the maximum looked for only when their sum asks for it).  16-key groups behind the last key are neither copied nor
+// multiplied: the block with the end of the sequence was the one that all others waited for (2 us).
 //
 // All of S is read before P overwrites it: the upper 64 columns' weights are stored over columns 96 .. 127, which
 // have been read, then the lower ones' over 64 .. 95.
