@@ -180,7 +180,7 @@ int cluster_blocks(const ClusterArgs &c, int64_t rows) {
 // besides.  Block and line, us (16 tokens, 32 / 8 heads of 128, pages of 16, own keys up to the figure, ragged): 16 sequences of 4096
 // 47 and 50, of 8000 87 and 71 (not ragged 94 and 113), 32 of 8000 109 and 115, 64 of 4096 85 and 126, of 8000 159 and 200; 300 of
 // 500 78 and 175, of 1000 117 and 220; 27 tokens of 100 of 1000 58 and 97, 60 tokens of 60 59 and 81, 120 of 60 of 2000
-// 163 both.  Single tokens of 20 sequences of 500 11.2 and 16.1, of 4000 47 and 38, 64 of 4000 87 and 102.  Behind a prefix
+// 163 both, 500 of 8 of 1000 not ragged 152 and 138; a prompt of 1000 tokens 30 and 47, four 92 and 117.  Single tokens of 20 sequences of 500 11.2 and 16.1, of 4000 47 and 38, 64 of 4000 87 and 102.  Behind a prefix
 // of 500 64 of 1000 44 and 103, 200 of 300 81 and 162, of 2000 79 and 116, 184 and 192.  At D = 64 (16 / 4 heads) 40 of
 // 4000 40 and 36, 64 47 and 58, 200 95 and 118.
 // Beyond 8192 keys the line gains by itself (64 of 16000 310 and 349), and one long sequence among short ones would leave
