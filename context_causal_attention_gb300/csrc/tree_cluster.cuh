@@ -77,15 +77,11 @@ __device__ __forceinline__ uint32_t cluster_size32() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-// By all threads of all blocks of the cluster: what they wrote before is seen behind it.
+// By all threads of all blocks of the cluster: what they wrote before is seen behind it, and what they read before is read
+// from what stood there before it (also a value that nobody waits for, as those of the join's pieces of weight 0).
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-// The same without the last: all threads have come here.
-__device__ __forceinline__ void cluster_meet() {
-    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-    asm volatile("barrier.cluster.wait;" ::: "memory");
 }
 // Address of this block's shared address `a` in block `rank` of the cluster.
 __device__ __forceinline__ uint32_t at_rank(uint32_t a, uint32_t rank) {
@@ -482,7 +478,7 @@ __global__ void __launch_bounds__(kClThreads, 1) tree_cluster_kernel(const __gri
                 c.lse[static_cast<long long>(head) * a.R + x.tok0 + tok] =
                     top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
         }
-        cluster_meet();  // nothing of this block is read any more
+        cluster_sync();  // nothing of this block is read any more
     }
     // no copy lands and no product runs when the block is gone
     copies_drain();

@@ -302,6 +302,33 @@ def test_any_hint_is_right(cuda_dev, hint):
     c.check(*c.run(cuda_dev, hint=hint))
 
 
+# new tokens, own lengths, prefix, N, Nkv, D, page, words: items of several row tiles (trees and prompts), and few key tiles
+# for many blocks
+ROW_TILES = {
+    "trees_128": ([100, 70, 33], [900, 70, 1500], 0, 8, 1, 128, 16, 4),
+    "prompt_128": ([300, 5], [300, 700], 130, 16, 2, 128, 64, 1),
+    "trees_64": ([64, 200, 1], [2000, 200, 64], 0, 8, 1, 64, 32, 8),
+    "prompt_64": ([400, 20], [1000, 90], 77, 6, 1, 64, 16, 1),
+    "two_tiles_of_keys": ([150, 40], [150, 170], 0, 8, 2, 128, 16, 1),
+    "one_tile_of_keys": ([90, 3], [90, 100], 0, 8, 2, 64, 16, 3),
+}
+
+
+@pytest.mark.parametrize("hint", [1, 20, None])
+@pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
+@pytest.mark.parametrize("name", sorted(ROW_TILES))
+def test_any_hint_is_right_in_every_form(cuda_dev, name, form, hint):
+    """Fewer row tiles than an item has: its block, or its cluster, takes one behind the other, over shared memory that
+    other blocks have just read.  The same bits every time."""
+    new, length, prefix, N, Nkv, D, page, words = ROW_TILES[name]
+    c = TreeCall(31, new, length, prefix, N, Nkv, D, page, words, pad=1)
+    o, lse = (t.clone() for t in c.run(cuda_dev, hint=hint, form=form))
+    c.check(o, lse)
+    for _ in range(20):
+        o2, lse2 = c.again(hint=hint)
+        assert torch.equal(o[:c.rows], o2[:c.rows]) and torch.equal(lse[:, :c.rows], lse2[:, :c.rows])
+
+
 def test_outputs_and_workspace_stay_in_bounds(cuda_dev):
     c = TreeCall(8, [3, 40, 1], [3, 300, 77], 130, 6, 2, 64, 16, 2, pad=2)
     c.run(cuda_dev)

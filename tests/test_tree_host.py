@@ -1,12 +1,15 @@
 """What the calls of the page plan, the storing by slots, the drafted trees and the kept branch refuse on the
 host before anything is launched, and the tests' own plain forms (no GPU needed)."""
 import ctypes
+import glob
+import os
 
 import numpy as np
 import pytest
 import torch
 
 import tree_ref as T
+from conftest import ROOT
 from context_causal_attention_gb300 import ops as F
 
 FAKE = 1 << 20  # aligned, never read
@@ -182,3 +185,13 @@ def test_plain_branches():
     assert np.nonzero(seen[6])[0].tolist() == [0, 1, 3, 6]
     words = T.packed(np.eye(40, dtype=bool), 2)
     assert words[31].tolist() == [-2 ** 31, 0] and words[33].tolist() == [0, 2]
+
+
+def test_cluster_barriers_order_what_was_read_before_them():
+    """Blocks of a cluster read each other's shared memory and then overwrite it or end: a barrier between that arrives
+    without release orders none of those reads."""
+    sources = glob.glob(os.path.join(ROOT, "context_causal_attention_gb300", "csrc", "*.cu*"))
+    assert len(sources) > 20
+    for path in sources:
+        with open(path) as f:
+            assert "barrier.cluster.arrive.relaxed" not in f.read(), path
