@@ -193,6 +193,53 @@ def test_a_row_that_sees_one_key_gives_its_value(cuda_dev, N, n, form):
     assert torch.equal(o.cpu(), v)
 
 
+@pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["narrow", "half_tile_prefix", "half_tile", "wide", "with_prompts", "blocks", "no_groups"])
+def test_a_query_that_is_not_a_number_stays_alone(cuda_dev, name, value, form):
+    """A query row of NaN (or of infinities of both signs): NaN in its own o and lse alone.  Other rows within what
+    test_gpu_prefix.py derives for rows beside such a one."""
+    new, length, prefix, N, Nkv, D, page, words, pad = CASES[name]
+    c = TreeCall(13, new, length, prefix, N, Nkv, D, page, words, "any", pad)
+    n = c.rows
+    good = [t.clone() for t in c.run(cuda_dev, form=form, o_dtype=F.CP_F32)]
+    size = torch.from_numpy(c.want()[2]).to(cuda_dev)
+    at = [(r, (7 * r) % N) for r in range(0, n, 11)]
+    for r, h in at:
+        c.q[r, h] = value
+        c.q[r, h, ::2] *= -1
+    o, lse = c.run(cuda_dev, o_dtype=F.CP_F32)
+    sick = torch.zeros((n, N), dtype=torch.bool, device=cuda_dev)
+    for r, h in at:
+        sick[r, h] = True
+    sick &= ~torch.isneginf(good[1][:, :n].T)  # a row that sees no key has no score
+    assert sick.any()
+    o, lse, wo, wl = o[:n], lse[:, :n].T, good[0][:n], good[1][:, :n].T
+    assert torch.isnan(o[sick]).all() and torch.isnan(lse[sick]).all()
+    assert ((o[~sick] - wo[~sick]).abs() <= (2.0 ** -17 + 2.0 ** -21) * size[~sick]).all()
+    same = torch.isneginf(wl) & torch.isneginf(lse)
+    assert ((lse - wl).abs() <= 2.0 ** -17)[~sick & ~same].all()
+
+
+# few sequences of as many tiles a block as a cluster is given (17 to 32 of 128 keys), and many over whole tiles of keys
+LONG = {
+    "shares_of_a_cluster": ([12, 20, 3, 1, 16, 9, 20, 0, 7], [8190, 5000, 7000, 4097, 300, 6500, 20, 900, 7300], 0, 16, 8, 64, 16, 1),
+    "shares_of_a_cluster_128": ([20, 9, 40, 33], [15000, 9000, 12345, 16000], 0, 4, 4, 128, 64, 2),
+    "shares_with_a_prefix": ([5, 17, 11, 2], [4000, 3900, 77, 1], 12000, 16, 8, 64, 32, 1),
+    "blocks": ([7 + 5 * i % 24 for i in range(12)], [3000 - 211 * i % 2300 for i in range(12)], 0, 16, 8, 128, 32, 1),
+    "blocks_64": ([30 - 7 * i % 25 for i in range(16)], [2990 - 333 * i % 2700 for i in range(16)], 0, 16, 8, 64, 16, 1),
+}
+
+
+@pytest.mark.parametrize("kind", ["random", "any"])
+@pytest.mark.parametrize("name", sorted(LONG))
+def test_long_sequences(cuda_dev, name, kind):
+    new, length, prefix, N, Nkv, D, page, words = LONG[name]
+    c = TreeCall(17, new, length, prefix, N, Nkv, D, page, words, kind)
+    o, lse = c.run(cuda_dev, o_dtype=F.CP_F32)
+    c.check(o, lse, "fp32", name)
+
+
 @pytest.mark.parametrize("gain", [30.0, 300.0])
 @pytest.mark.parametrize("N", [2, 16])
 @pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
