@@ -250,6 +250,16 @@ __device__ __forceinline__ float2 left_ml(float m, float l) {
     return make_float2(m == -INFINITY && l != l ? INFINITY : m, l);
 }
 
+// The sum l of a row of trees relative to its maximum m, as a piece leaves it.  m is the largest score itself, but rounded,
+// where the weights come from the scores by one rounding (a fused product and difference): a row's only key has the weight
+// 1 + r with |r| <= |m| 2^-24 (half a step of m times ln 2, and less) + 2^-21 (the exponential), while the weight that
+// its value was multiplied by, in bf16, is 1 for |r| < 2^-9.  A sum that near 1 is one key's, beside others that weigh no
+// more than r together: it becomes 1, and the output that key's value itself, for |m| up to 2^15; lse moves by no
+// more than |m| 2^-24 + 2^-21.
+__device__ __forceinline__ float sum_of_one(float m, float l) {
+    return fabsf(l - 1.f) <= fminf(fmaf(fabsf(m), 0x1p-24f, 0x1p-21f), 0x1.fp-10f) ? 1.f : l;
+}
+
 // A stretch of one item that a block works on.
 struct Piece {
     int b;                // sequence, -1: the prefix

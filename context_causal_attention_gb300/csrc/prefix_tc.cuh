@@ -16,7 +16,7 @@
 //   warps 4-7   softmax of rows 0..127, warps 8-11 of rows 128..255: one thread
 //               a row, in the log2 domain with an integer running maximum that
 //               moves only when a tile's sum passes 2^64 (as in attn.cu).  Trees (kTree) take the
-//               maximum itself: the weight of a row's only key is 1 then, and its output that key's value.
+//               maximum itself: the output of a row that sees one key is that key's value (sum_of_one).
 // The two halves keep the tensor cores and the exponentials busy in turn.  In a
 // tile of up to 128 rows both hold the same rows and take the key tiles in turn;
 // the first half joins the two results at the end (with one half alone the scores,
@@ -576,7 +576,7 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
                                      __uint_as_float(ov[e + 6]), __uint_as_float(ov[e + 7]));
                 }
             }
-            if (write) a.slot_ml[at] = left_ml(m_run, l_run);
+            if (write) a.slot_ml[at] = left_ml(m_run, kTree ? sum_of_one(m_run, l_run) : l_run);
             if (!paired || join) ++other;
         }
     }

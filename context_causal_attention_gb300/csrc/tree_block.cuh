@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kBlThreads, 2) tree_block_kernel(const __grid_
             if (busy) ok = ok && (tiles < 2 || ended(kv + tiles - 2)) && (tiles < 1 || ended(kv + tiles - 1));
             if (ok && busy) {
                 tc_fence_after();
-                const float2 ml = left_ml(m, l);
+                const float2 ml = left_ml(m, sum_of_one(m, l));
                 const bool none = ml.x == -INFINITY;
                 const float inv = none ? 0.f : 1.f / ml.y;
                 const int head = kvh * a.G + row - tok * a.G;

@@ -11,7 +11,7 @@
 // O += P V on tcgen05 with S, P and O in tensor memory (S0 | S1 | O0 | O1), a thread a row.  K and V come by 16-byte
 // cp.async whatever the page's size, Q is gathered by the softmax warps.  A row's maximum is looked for before its
 // weights are formed (and moved only when a weight would pass 2^30), so nothing is computed twice.  It is the score itself, not
-// a whole number above it: the weight of a row's only key is 1 then, and its output that key's value.
+// a whole number above it: the output of a row that sees one key is that key's value then (sum_of_one).
 // A tile's code is a loop over 64 columns, not unrolled over 128: a block goes through two to thirty tiles, and code
 // that is read for the first time costs more than the loop (1.4 us less than with the weights of 128 columns in a row and
 // the maximum looked for only when their sum asks for it).  16-key groups behind the last key are neither copied nor
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kClThreads, 1) tree_cluster_kernel(const __gri
             tc_fence_after();
             if (twice) {
                 const bool left = ok && half < tiles;
-                if ((in_tile >> 6) == half) ml_s[in_tile] = left ? left_ml(m, l) : make_float2(-INFINITY, 0.f);
+                if ((in_tile >> 6) == half) ml_s[in_tile] = left ? left_ml(m, sum_of_one(m, l)) : make_float2(-INFINITY, 0.f);
                 if (left && busy) {
 #pragma unroll 1
                     for (int e = 0; e < D; e += 32) {
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kClThreads, 1) tree_cluster_kernel(const __gri
                 const float f0 = h0.x == -INFINITY ? 0.f : fast_exp2(h0.x - top);
                 const float f1 = h1.x == -INFINITY ? 0.f : fast_exp2(h1.x - top);
                 const float sum = f0 * h0.y + f1 * h1.y;  // (NaN where a half's is, also one of all NaN, without exponent)
-                if (half == 0) ml_s[in_tile] = ok && tiles > 0 ? left_ml(top, sum) : make_float2(-INFINITY, 0.f);
+                if (half == 0) ml_s[in_tile] = ok && tiles > 0 ? left_ml(top, sum_of_one(top, sum)) : make_float2(-INFINITY, 0.f);
                 if (ok && tiles > 0 && busy) {
 #pragma unroll 1
                     for (int e = half * (D / 2); e < (half + 1) * (D / 2); e += 32) {

@@ -712,7 +712,7 @@ cp_status cp_tree_plan(const int32_t *parent, const int32_t *cu_new, const int32
  *          in cp_prefix_attn_fwd, their mask rows not read: trees and prompts mix in one batch.
  * max_pages says how long a sequence may be, which chooses how the work is cut (every length is right): a table no
  * wider than the step needs is worth up to half of the time where it holds a few thousand tokens a sequence.
- * A row that sees one key gets that key's value itself.
+ * A row that sees one key gets that key's value itself, for scores scale <q, k> up to 2^14 in size.
  * Everything else as for cp_prefix_attn_fwd, but that a NaN or infinity in any V row of a sequence's own keys may
  * reach its other rows (also one that no row's mask has).
  */

@@ -194,6 +194,21 @@ def test_a_row_that_sees_one_key_gives_its_value(cuda_dev, N, n, form):
 
 
 @pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
+@pytest.mark.parametrize("gain", [1.0, 40.0, 3000.0])
+@pytest.mark.parametrize("N,n,D", [(2, 5, 64), (16, 30, 64), (32, 60, 64), (8, 25, 128)])
+def test_a_row_that_sees_one_key_gives_its_value_in_32_bits(cuda_dev, N, n, D, gain, form):
+    """The same for fp32 outputs, which show what a bf16 one rounds away, up to the scores that the header names; lse is the
+    score, to the rounding of its products' sum, of its multiplication and of itself (as check() derives)."""
+    c = TreeCall(19, [n, 3], [n, 3], 0, N, 2, D, 16, 2, "roots", gain=gain)
+    o, lse = c.run(cuda_dev, form=form, o_dtype=F.CP_F32)
+    assert np.abs(f64(lse)).max() < 2 ** 14  # of the one key: lse is the score
+    at = c.b.slots(0, 0, n) + c.b.slots(1, 0, 3)
+    v = c.v.view(-1, 2, D)[at].repeat_interleave(N // 2, 1)
+    assert torch.equal(o.cpu(), v.float())
+    c.check(o, lse, "fp32", gain=gain)
+
+
+@pytest.mark.parametrize("form", ["as_chosen", "clusters", "line"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("name", ["narrow", "half_tile_prefix", "half_tile", "wide", "with_prompts", "blocks", "no_groups"])
 def test_a_query_that_is_not_a_number_stays_alone(cuda_dev, name, value, form):
