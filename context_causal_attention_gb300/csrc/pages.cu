@@ -203,15 +203,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     __syncthreads();
     const int top = free0 + given;
     auto last_of = [&](const int *s, int b, int end) { return b + 1 < a.B ? s[b + 1] : end; };
-    // The last given page of a sequence is its last one.
+    bool wrong = false;
+    // The last given page of a sequence is its last one.  (A page number out of range goes on the stack as it is: told here,
+    // by the step that puts it there, and again by the one that pops it.)
     for (int k = gx; k < given; k += step) {
         const int b = place_in(gives, a.B, k);
         const int n = last_of(gives, b, given) - gives[b];
-        a.free_pages[free0 + k] = __ldcg(a.table + static_cast<long long>(b) * a.max_pages + owned[b] - n + k - gives[b]);
+        const int page = __ldcg(a.table + static_cast<long long>(b) * a.max_pages + owned[b] - n + k - gives[b]);
+        wrong |= page < 0 || page >= a.n_pages;
+        a.free_pages[free0 + k] = page;
     }
     // every block has read the lists, and what was given lies on the stack
     all_read(blocks);
-    bool wrong = false;
     for (int k = gx; k < taken; k += step) {
         const int b = place_in(takes, a.B, k), page = __ldcg(a.free_pages + top - 1 - k);
         wrong |= page < 0 || page >= a.n_pages;

@@ -642,8 +642,9 @@ cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, const void *v_c
  *                kv_had, stack and table stay
  * All lists apart from one another otherwise (CP_ERR_ARGUMENT else).  A count below zero, kv_keep over
  * kv_had, a length past the table, more than R new tokens or a stack that does not fit n_pages sets the device
- * status word to CP_ERR_PAGE and hands nothing out (n_free_out[1] = -1); so does a page number out of range, whose
- * rows get slot -1.  Sizes as for cp_cache_append.
+ * status word to CP_ERR_PAGE and hands nothing out (n_free_out[1] = -1).  A page number out of range that the step
+ * meets, in the table or on the stack, sets the status word too, but the step goes on: its rows get slot -1, a
+ * page that is given back or taken moves as it is, and n_free_out[1] stays 0.  Sizes as for cp_cache_append.
  */
 cp_status cp_cache_plan(const int32_t *kv_had, const int32_t *kv_keep, const int32_t *n_new, int64_t B, int32_t *table,
                         int64_t max_pages, int64_t page_size, int32_t *free_pages, int64_t n_pages,

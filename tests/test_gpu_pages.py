@@ -156,6 +156,24 @@ def test_plan_reports_lists_out_of_range(cuda_dev, what):
     assert set(got["slots"]) == {-1} and got["table"] == s.table and got["stack"] == s.stack
 
 
+@pytest.mark.parametrize("bad", [-1, 999, -2 ** 31, 2 ** 31 - 1])
+@pytest.mark.parametrize("taken", [False, True])
+def test_plan_reports_bad_pages_that_are_given_back(cuda_dev, bad, taken):
+    """A page number out of range in the table of a sequence that gives it back: the step that puts it on the stack
+    says so, whether or not the same step hands it on."""
+    s = Step(22, [40, 33, 5], [10, 33, 5], [0, 40 if taken else 1, 0], 16, 6, 0, 0, 2)
+    s.table[0][2] = bad  # pages 1 and 2 of sequence 0 go back
+    got = s.call(cuda_dev)
+    assert F.cp_device_status() == 11
+    assert F.cp_device_status() == 0
+    assert got["kv_len"] == [10, 73 if taken else 34, 5]
+    if not taken:
+        assert got["slots"][0] == s.table[1][2] * 16 + 1 and got["n_free"] == [2, 0]
+    else:
+        # the page was pushed last and popped first: own indexes 48 to 63 of sequence 1 have no slot
+        assert got["n_free"] == [0, 0] and [r for r, x in enumerate(got["slots"][:40]) if x < 0] == list(range(15, 31))
+
+
 def test_plan_over_many_steps_in_a_graph(cuda_dev):
     """One captured call, replayed with new lengths: its own results are the next step's lists; every page is
     handed out once."""
