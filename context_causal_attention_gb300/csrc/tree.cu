@@ -38,13 +38,13 @@ __global__ void tree_kernel(const TreeArgs a) {
     wait_for_previous();
     launch_dependents();
     const int b = blockIdx.x, tid = threadIdx.x, wide = 32 * a.words;
-    const int begin = __ldcg(a.cu + b), n = __ldcg(a.cu + b + 1) - begin;
-    // counts that make no sense: nothing is read or written by them
-    if (begin < 0 || n < 0 || n > a.R - begin) {
+    const int begin = __ldcg(a.cu + b), end = __ldcg(a.cu + b + 1), length = __ldcg(a.kv_len + b), n = end - begin;
+    // counts that make no sense, also fewer tokens than new ones: nothing is read or written by them
+    if (begin < 0 || end < begin || end > a.R || length < n) {
         if (tid == 0) report(a.status, CP_ERR_PAGE);
         return;
     }
-    const long long first = a.pos_base + __ldcg(a.kv_len + b) - n;  // position of a token of depth 0
+    const long long first = a.pos_base + length - n;  // position of a token of depth 0
     if (n > wide) {
         // a prompt: its tokens follow one another
         for (int j = tid; j < n; j += blockDim.x) a.pos[begin + j] = static_cast<int32_t>(first + j);

@@ -700,7 +700,7 @@ cp_status cp_cache_keep(void *const *caches, int64_t n_caches, int64_t n_pages, 
  *   mask   : device int32 [R][words], words 1 .. 16;  pos : device int32 [R]; rows from cu_new[B] on stay.
  *            Apart from one another and from the lists that are read (CP_ERR_ARGUMENT else)
  * A parent out of range counts as -1 and sets the device status word to CP_ERR_PAGE; so do counts that make no
- * sense, whose rows stay.
+ * sense, kv_len[b] below n_b among them, whose rows stay.
  */
 cp_status cp_tree_plan(const int32_t *parent, const int32_t *cu_new, const int32_t *kv_len, int64_t B, int64_t R,
                        int64_t words, int64_t pos_base, int32_t *mask, int32_t *pos, cudaStream_t stream);

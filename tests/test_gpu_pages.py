@@ -293,6 +293,22 @@ def test_tree_plan_reports_lists_out_of_range(cuda_dev, what):
         assert mask == [9] * 6 and pos == [9] * 6
 
 
+@pytest.mark.parametrize("what,length", [("short", 2), ("none", 0), ("negative", -7), ("lowest", -2 ** 31)])
+@pytest.mark.parametrize("n", [3, 40])
+def test_tree_plan_reports_lengths_below_the_new_tokens(cuda_dev, what, length, n):
+    """A tree (or a prompt) of more new tokens than its sequence has: its rows stay, as cp_cache_keep keeps nothing of it."""
+    parent, cu = [-1, 0, 1] + [-1, 0, 0] * 14, [0, 3, 3 + n, 6 + n]
+    rows = 6 + n
+    mask = torch.full((rows, 1), 9, dtype=torch.int32, device=cuda_dev)
+    pos = torch.full((rows,), 9, dtype=torch.int32, device=cuda_dev)
+    parent[3 + n:] = [-1, 0, 1]
+    F.cp_tree_plan(i32(parent, cuda_dev), i32(cu, cuda_dev), i32([13, length, 3], cuda_dev), 1, 100, mask=mask, pos=pos)
+    assert F.cp_device_status() == 11
+    assert F.cp_device_status() == 0
+    mask, pos = mask.flatten().tolist(), pos.tolist()
+    assert mask == [1, 3, 7] + [9] * n + [1, 3, 7] and pos == [110, 111, 112] + [9] * n + [100, 101, 102]
+
+
 # ------------------------------------------------------------------ storing by slots
 @pytest.mark.parametrize("name,rows,N,Nkv,D,page", [("one", 1, 4, 1, 64, 16), ("odd", 37, 15, 3, 128, 64),
                                                     ("no_q", 200, 0, 2, 128, 256), ("units", 5000, 2, 1, 64, 16),
