@@ -101,7 +101,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const long long len = static_cast<long long>(keep[k]) + fresh[k];
-        if (fresh[k] < 0 || keep[k] < 0 || had[k] < keep[k] || len > most || had[k] > most) {
+        // (the last new position, pos_base + len - 1, has to fit 32 bits)
+        const bool far = fresh[k] > 0 && a.pos_base + len > 1ll << 31;
+        if (fresh[k] < 0 || keep[k] < 0 || had[k] < keep[k] || len > most || had[k] > most || far) {
             bad = true;
             continue;
         }

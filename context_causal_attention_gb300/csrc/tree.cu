@@ -39,8 +39,9 @@ __global__ void tree_kernel(const TreeArgs a) {
     launch_dependents();
     const int b = blockIdx.x, tid = threadIdx.x, wide = 32 * a.words;
     const int begin = __ldcg(a.cu + b), end = __ldcg(a.cu + b + 1), length = __ldcg(a.kv_len + b), n = end - begin;
-    // counts that make no sense, also fewer tokens than new ones: nothing is read or written by them
-    if (begin < 0 || end < begin || end > a.R || length < n) {
+    // counts that make no sense, also fewer tokens than new ones, or positions that 32 bits do not hold: nothing is read or
+    // written by them
+    if (begin < 0 || end < begin || end > a.R || length < n || (n && a.pos_base + length > 1ll << 31)) {
         if (tid == 0) report(a.status, CP_ERR_PAGE);
         return;
     }

@@ -641,10 +641,11 @@ cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, const void *v_c
  *                pages lacking}, and nothing is handed out or given back: cu_new is 0, every slot -1, kv_len is
  *                kv_had, stack and table stay
  * All lists apart from one another otherwise (CP_ERR_ARGUMENT else).  A count below zero, kv_keep over
- * kv_had, a length past the table, more than R new tokens or a stack that does not fit n_pages sets the device
- * status word to CP_ERR_PAGE and hands nothing out (n_free_out[1] = -1).  A page number out of range that the step
- * meets, in the table or on the stack, sets the status word too, but the step goes on: its rows get slot -1, a
- * page that is given back or taken moves as it is, and n_free_out[1] stays 0.  Sizes as for cp_cache_append.
+ * kv_had, a length past the table, a new position past 32 bits, more than R new tokens or a stack that does not fit
+ * n_pages sets the device status word to CP_ERR_PAGE and hands nothing out (n_free_out[1] = -1).  A page number out of
+ * range that the step meets, in the table or on the stack, sets the status word too, but the step goes on: its rows
+ * get slot -1, a page that is given back or taken moves as it is, and n_free_out[1] stays 0.  Sizes as for
+ * cp_cache_append.
  */
 cp_status cp_cache_plan(const int32_t *kv_had, const int32_t *kv_keep, const int32_t *n_new, int64_t B, int32_t *table,
                         int64_t max_pages, int64_t page_size, int32_t *free_pages, int64_t n_pages,
@@ -700,7 +701,7 @@ cp_status cp_cache_keep(void *const *caches, int64_t n_caches, int64_t n_pages, 
  *   mask   : device int32 [R][words], words 1 .. 16;  pos : device int32 [R]; rows from cu_new[B] on stay.
  *            Apart from one another and from the lists that are read (CP_ERR_ARGUMENT else)
  * A parent out of range counts as -1 and sets the device status word to CP_ERR_PAGE; so do counts that make no
- * sense, kv_len[b] below n_b among them, whose rows stay.
+ * sense, whose rows stay: kv_len[b] below n_b among them, and new tokens behind position 2^31 - 1.
  */
 cp_status cp_tree_plan(const int32_t *parent, const int32_t *cu_new, const int32_t *kv_len, int64_t B, int64_t R,
                        int64_t words, int64_t pos_base, int32_t *mask, int32_t *pos, cudaStream_t stream);

@@ -174,6 +174,22 @@ def test_plan_reports_bad_pages_that_are_given_back(cuda_dev, bad, taken):
         assert got["n_free"] == [0, 0] and [r for r, x in enumerate(got["slots"][:40]) if x < 0] == list(range(15, 31))
 
 
+@pytest.mark.parametrize("base,first", [(2 ** 31 - 60, 0), (2 ** 31 - 59, 1), (2 ** 31 - 1, 1)])
+def test_plan_reports_positions_past_32_bits(cuda_dev, base, first):
+    """The last new position is base + 59: beyond 32 bits nothing is handed out.  (A longer sequence without new tokens
+    has no new position.)"""
+    s = Step(23, [20, 40, 64], [18, 40, 64], [3, 20, 0], 16, 4, 6, base, 2)
+    got = s.call(cuda_dev)
+    assert F.cp_device_status() == (11 if first else 0)
+    if not first:
+        same(got, s.want())
+        assert max(got["pos"]) == 2 ** 31 - 1
+        return
+    assert F.cp_device_status() == 0
+    assert got["n_free"] == [s.n_free, -1] and got["cu"] == [0] * 4 and got["kv_len"] == s.had
+    assert set(got["slots"]) == {-1} and got["table"] == s.table and got["stack"] == s.stack
+
+
 def test_plan_over_many_steps_in_a_graph(cuda_dev):
     """One captured call, replayed with new lengths: its own results are the next step's lists; every page is
     handed out once."""
@@ -307,6 +323,19 @@ def test_tree_plan_reports_lengths_below_the_new_tokens(cuda_dev, what, length, 
     assert F.cp_device_status() == 0
     mask, pos = mask.flatten().tolist(), pos.tolist()
     assert mask == [1, 3, 7] + [9] * n + [1, 3, 7] and pos == [110, 111, 112] + [9] * n + [100, 101, 102]
+
+
+@pytest.mark.parametrize("n", [6, 40])
+@pytest.mark.parametrize("base,bad", [(2 ** 31 - 90, 0), (2 ** 31 - 89, 1)])
+def test_tree_plan_reports_positions_past_32_bits(cuda_dev, n, base, bad):
+    """A sequence of 90 tokens: its last position is base + 89, beyond 32 bits its rows stay."""
+    parent = [j - 1 for j in range(n)]
+    mask = torch.full((n, 1), 9, dtype=torch.int32, device=cuda_dev)
+    pos = torch.full((n,), 9, dtype=torch.int32, device=cuda_dev)
+    F.cp_tree_plan(i32(parent, cuda_dev), i32([0, n], cuda_dev), i32([90], cuda_dev), 1, base, mask=mask, pos=pos)
+    assert F.cp_device_status() == (11 if bad else 0)
+    assert F.cp_device_status() == 0
+    assert pos.tolist() == ([9] * n if bad else list(range(2 ** 31 - n, 2 ** 31)))
 
 
 # ------------------------------------------------------------------ storing by slots
