@@ -1,5 +1,5 @@
-// cp_hold.cuh -- failure injection for the self-tests of the tf32, backward and
-// shared-prefix kernels: a bounded wait on a flag that nothing sets.
+// cp_hold.cuh -- failure injection for the self-tests of the tf32, backward,
+// shared-prefix and tree kernels: a bounded wait on a flag that nothing sets.
 #pragma once
 #include <cstdint>
 

@@ -270,18 +270,18 @@ extern "C" cp_status cp_tree_attn_workspace_size(int64_t R, int64_t B, int64_t m
     return CP_OK;
 }
 
-extern "C" cp_status cp_tree_attn_fwd(const void *q, const void *k_cache, const void *v_cache, int64_t n_pages,
-                                      int64_t page_size, const int32_t *prefix_pages, int64_t prefix_len,
-                                      const int32_t *table, int64_t B, int64_t max_pages, const int32_t *cu_new,
-                                      const int32_t *kv_len, const int32_t *mask, int64_t words, int64_t max_new,
-                                      int64_t R, int64_t N, int64_t Nkv, int64_t D, float scale, void *o,
-                                      cp_dtype o_dtype, float *lse, void *workspace, size_t ws_bytes,
-                                      cudaStream_t stream) {
+namespace {
+// cp_tree_attn_fwd, with the limit of its waits; stalled: its loads wait for a word that nothing sets.
+cp_status tree_call(const void *q, const void *k_cache, const void *v_cache, int64_t n_pages, int64_t page_size,
+                    const int32_t *prefix_pages, int64_t prefix_len, const int32_t *table, int64_t B, int64_t max_pages,
+                    const int32_t *cu_new, const int32_t *kv_len, const int32_t *mask, int64_t words, int64_t max_new,
+                    int64_t R, int64_t N, int64_t Nkv, int64_t D, float scale, void *o, cp_dtype o_dtype, float *lse,
+                    void *workspace, size_t ws_bytes, uint64_t timeout_ns, bool stalled, cudaStream_t stream) {
     if (words < 1 || words > kMaxWords) return CP_ERR_SHAPE;
     Call c;
     const cp_status st = check_call<true>(c, mask, words, q, k_cache, v_cache, n_pages, page_size, prefix_pages,
                                           prefix_len, table, B, max_pages, cu_new, kv_len, max_new, R, N, Nkv, D,
-                                          scale, o, o_dtype, lse, workspace, ws_bytes, 2000000000ull, false);
+                                          scale, o, o_dtype, lse, workspace, ws_bytes, timeout_ns, stalled);
     if (st != CP_OK) return st;
     const int64_t rows = max_new * c.a.G;  // of an item, about
     auto form = [&](int tile) { return ClusterArgs{c.a, static_cast<int>((rows + tile - 1) / tile), o, o_dtype == CP_BF16, lse}; };
@@ -291,4 +291,31 @@ extern "C" cp_status cp_tree_attn_fwd(const void *q, const void *k_cache, const 
     if (D == 128 ? items_pay<128>(many, rows) : items_pay<64>(many, rows))
         return D == 128 ? launch_items<128>(many, stream) : launch_items<64>(many, stream);
     return launch_line<true>(c, stream);
+}
+}  // namespace
+
+extern "C" cp_status cp_tree_attn_fwd(const void *q, const void *k_cache, const void *v_cache, int64_t n_pages,
+                                      int64_t page_size, const int32_t *prefix_pages, int64_t prefix_len,
+                                      const int32_t *table, int64_t B, int64_t max_pages, const int32_t *cu_new,
+                                      const int32_t *kv_len, const int32_t *mask, int64_t words, int64_t max_new,
+                                      int64_t R, int64_t N, int64_t Nkv, int64_t D, float scale, void *o,
+                                      cp_dtype o_dtype, float *lse, void *workspace, size_t ws_bytes,
+                                      cudaStream_t stream) {
+    return tree_call(q, k_cache, v_cache, n_pages, page_size, prefix_pages, prefix_len, table, B, max_pages, cu_new,
+                     kv_len, mask, words, max_new, R, N, Nkv, D, scale, o, o_dtype, lse, workspace, ws_bytes,
+                     2000000000ull, false, stream);
+}
+
+extern "C" cp_status cp_selftest_stalled_tree_attn(const void *q, const void *k_cache, const void *v_cache,
+                                                   int64_t n_pages, int64_t page_size, const int32_t *prefix_pages,
+                                                   int64_t prefix_len, const int32_t *table, int64_t B,
+                                                   int64_t max_pages, const int32_t *cu_new, const int32_t *kv_len,
+                                                   const int32_t *mask, int64_t words, int64_t max_new, int64_t R,
+                                                   int64_t N, int64_t Nkv, int64_t D, float scale, void *o,
+                                                   cp_dtype o_dtype, float *lse, void *workspace, size_t ws_bytes,
+                                                   uint64_t timeout_ns, cudaStream_t stream) {
+    if (timeout_ns < 1000000ull || timeout_ns > 2000000000ull) return CP_ERR_ARGUMENT;
+    return tree_call(q, k_cache, v_cache, n_pages, page_size, prefix_pages, prefix_len, table, B, max_pages, cu_new,
+                     kv_len, mask, words, max_new, R, N, Nkv, D, scale, o, o_dtype, lse, workspace, ws_bytes,
+                     timeout_ns, true, stream);
 }

@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kBlThreads, 2) tree_block_kernel(const __grid_
             PageWindow win{};
             Piece y = x;
             int segment = -1;
-            for (int j = 0; j < tiles; ++j) {
+            const int loads = tiles && released(a, abort_flag) ? tiles : 0;
+            for (int j = 0; j < loads; ++j) {
                 const bool pre = j < prefix_tiles;
                 const int key = (j - (pre ? 0 : prefix_tiles)) * kBlKeys;
                 if (segment != pre) {

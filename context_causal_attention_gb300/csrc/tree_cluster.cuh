@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kClThreads, 1) tree_cluster_kernel(const __gri
             PageWindow win{};
             Piece y = x;
             int segment = -1;
-            for (int j = 0; j < tiles; ++j) {
+            const int loads = tiles && released(a, abort_flag) ? tiles : 0;
+            for (int j = 0; j < loads; ++j) {
                 const bool pre = k0 + j < prefix_tiles;
                 const int key = (k0 + j - (pre ? 0 : prefix_tiles)) * 128;
                 if (segment != pre) {

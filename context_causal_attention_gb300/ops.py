@@ -781,11 +781,16 @@ def cp_tree_attn_workspace_size(R, B, max_new, words, prefix_len, N, Nkv, D, pag
 
 
 def _prefix_call(name, more, q, k_cache, v_cache, prefix_pages, prefix_len, table, cu_new, kv_len, max_new, scale,
-                 o_dtype, o, lse, workspace, stream):
+                 o_dtype, o, lse, workspace, stream, mask=None):
+    """A call of the shared-prefix attention, or with `mask` of the tree attention, through ctypes."""
     n_pages, page, Nkv, D, B, max_pages = _check_cache(k_cache, v_cache, table, cu_new, kv_len)
     if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be contiguous bf16 [R, N, D]")
     R, N = q.shape[0], q.shape[1]
+    if mask is not None and (mask.dim() != 2 or mask.dtype != torch.int32 or mask.shape[0] != R or
+                             not mask.is_contiguous()):
+        raise ValueError("mask must be contiguous int32 [R, words]")
+    masked = () if mask is None else (_addr(mask), mask.shape[1])
     # (a list that is missing is the library's to refuse)
     if prefix_len and prefix_pages is not None and (prefix_pages.dtype != torch.int32 or
                                                     not prefix_pages.is_contiguous() or
@@ -804,10 +809,10 @@ def _prefix_call(name, more, q, k_cache, v_cache, prefix_pages, prefix_len, tabl
     if workspace is None:
         workspace = _scratch(max(256, cp_prefix_attn_workspace_size(R, B, max_new, prefix_len, N, Nkv, D, page,
                                                                     max_pages)), q.device, stream)
-    dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, o, lse, workspace)
+    dev = _here(q, k_cache, v_cache, prefix_pages, table, cu_new, kv_len, mask, o, lse, workspace)
     st = getattr(_lib.lib(), name)(_addr(q), _addr(k_cache), _addr(v_cache), n_pages, page, _addr(prefix_pages),
-                                   prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), max_new, R, N,
-                                   Nkv, D, scale, _addr(o), _dtype_code(o), _addr(lse), _addr(workspace),
+                                   prefix_len, _addr(table), B, max_pages, _addr(cu_new), _addr(kv_len), *masked,
+                                   max_new, R, N, Nkv, D, scale, _addr(o), _dtype_code(o), _addr(lse), _addr(workspace),
                                    workspace.numel() * workspace.element_size(), *more, _raw_stream(stream, dev))
     _lib.check(name, st)
     return o, lse
@@ -851,6 +856,15 @@ def cp_selftest_stalled_prefix_attn(timeout_ns, q, k_cache, v_cache, prefix_page
     that nothing sets (see the C header); read the outcome with cp_device_status."""
     _prefix_call("cp_selftest_stalled_prefix_attn", (int(timeout_ns),), q, k_cache, v_cache, prefix_pages, prefix_len,
                  table, cu_new, kv_len, max_new, None, CP_BF16, None, None, workspace, stream)
+
+
+def cp_selftest_stalled_tree_attn(timeout_ns, q, k_cache, v_cache, mask, prefix_pages, prefix_len, table, cu_new, kv_len,
+                                  max_new, workspace=None, stream=None):
+    """The same of the tree attention, with the kernels that cp_tree_attn_fwd takes for these arguments."""
+    if mask is None:
+        raise ValueError("mask must be contiguous int32 [R, words]")
+    _prefix_call("cp_selftest_stalled_tree_attn", (int(timeout_ns),), q, k_cache, v_cache, prefix_pages, prefix_len,
+                 table, cu_new, kv_len, max_new, None, CP_BF16, None, None, workspace, stream, mask)
 
 
 def cp_selftest_stalled_producer(q, k, v, pos, o, lse, timeout_ns, stream=None):

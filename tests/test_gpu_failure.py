@@ -112,6 +112,40 @@ def test_prefix_attention_gives_up_a_stalled_wait(cuda_dev, form, D):
     assert F.cp_device_status() == 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form", ["items", "items_of_many_tiles", "items_ordered", "clusters", "clusters_of_many_tiles",
+                                  "clusters_few_tiles", "line_narrow", "line_wide"])
+def test_tree_attention_gives_up_a_stalled_wait(cuda_dev, form, D):
+    """The tree attention's own kernels (a block an item, a cluster an item: their blocks still meet when all of them
+    have given up) and the line's: as above."""
+    from test_gpu_tree import TreeCall
+    new, length, prefix, hint, wide = {
+        "items": ([20, 9], [300, 90], 100, 20, 0),
+        "items_of_many_tiles": ([60, 200, 3], [300, 200, 90], 0, 1, 0),
+        "items_ordered": ([3 + i % 9 for i in range(100)], [700 + 9 * i for i in range(100)], 0, 11, 0),
+        "clusters": ([20, 9], [300, 1900], 100, 20, 0),
+        "clusters_of_many_tiles": ([60, 200, 3], [300, 2000, 90], 0, 1, 0),
+        "clusters_few_tiles": ([5, 40], [90, 40], 0, 40, 700),
+        "line_narrow": ([1, 2], [300, 200], 0, 2, 140000),
+        "line_wide": ([40, 9], [300, 900], 500, 40, 140000)}[form]
+    c = TreeCall(23, new, length, prefix, 16, 4, D, 16, 2)
+    c.table = torch.cat([c.table, torch.full((len(new), wide // 16), -3, dtype=torch.int32)], 1)
+    o, lse = c.run(cuda_dev, hint=hint)
+    c.check(o, lse)
+    assert F.cp_device_status() == 0
+    q, k, v, mask, pages, table, cu, kv_len = c.dev
+    need = F.cp_tree_attn_workspace_size(c.R, len(new), hint, 2, prefix, 16, 4, D, 16, table.shape[1])
+    ws = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device=cuda_dev)
+    lists = (q, k, v, mask, pages, prefix, table, cu, kv_len, hint)
+    F.cp_selftest_stalled_tree_attn(10_000_000, *lists, workspace=ws[256:256 + need])
+    assert F.cp_device_status() == CP_ERR_DEVICE_TIMEOUT
+    assert F.cp_device_status() == 0
+    o2, lse2 = F.cp_tree_attn_fwd(*lists, workspace=ws[256:256 + need])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert (ws[:256] == 0xA5).all() and (ws[256 + need:] == 0xA5).all()
+    assert F.cp_device_status() == 0
+
+
 @pytest.mark.parametrize("order", ["wait_first", "list_first"])
 def test_a_bad_list_does_not_hide_a_wait_that_ran_out(cuda_dev, order):
     """A stalled call and calls with a page number out of range (the append's and the

@@ -126,6 +126,21 @@ def test_tree_attention_refusals(cplib):
     assert cplib.cp_tree_attn_workspace_size(64, 4, 8, 2, 32, 4, 2, 64, 16, 8, None) == 1
 
 
+def test_stalled_tree_attention_checks_as_the_call_does(cplib):
+    def call(ns=10_000_000, **c):
+        return cplib.cp_selftest_stalled_tree_attn(*args(ATTN, **c)[:-1], ns, None)
+
+    for ns in (0, 999_999, 2_000_000_001):
+        assert call(ns) == 10, ns
+    assert call(q=None) == 1 and call(mask=None) == 1 and call(words=17) == 2 and call(ws_bytes=1) == 6
+    assert call(q=FAR[0] + 8) == 5
+    i32, bf = lambda *s: torch.zeros(*s, dtype=torch.int32), lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    for mask in (None, i32(6, 1), i32(5), i32(5, 2).float(), i32(2, 5).t()):
+        with pytest.raises(ValueError):
+            F.cp_selftest_stalled_tree_attn(10_000_000, bf(5, 4, 64), bf(4, 16, 2, 64), bf(4, 16, 2, 64), mask, None, 0,
+                                            i32(3, 2), i32(4), i32(3), 2)
+
+
 def test_binding_refusals(cplib):
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
