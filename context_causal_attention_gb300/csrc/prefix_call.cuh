@@ -108,7 +108,7 @@ struct MmaCfg {
     static constexpr int kOffBar = (kOffStart + static_cast<int>(sizeof(Start)) + 15) & ~15;
     static constexpr int kOffMisc = kOffBar + kStages * 16 + kGroups * 8;
     static constexpr int kOffWalk = (kOffMisc + 16 + 15) & ~15;  // [warps]
-    static constexpr int kSmem = kOffWalk + kMmaThreads / 32 * static_cast<int>(sizeof(Walk<kTM, kKT, false>)) + 1024;  // + alignment slack
+    static constexpr int kSmem = kOffWalk + kMmaThreads / 32 * static_cast<int>(sizeof(Walk<kTM, kKT, true>)) + 1024;  // + alignment slack
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -170,7 +170,7 @@ __device__ __forceinline__ void mma_work(const PrefixArgs &a, uint8_t *smem) {
 
     using Walker = Walk<kTM, kKT, kTree>;
     Walker &walk = reinterpret_cast<Walker *>(smem + C::kOffWalk)[warp];
-    const Piece &x = walk.x;
+    const auto &x = walk.x;
     walk.begin(a, line, start, t1 - t0);
     if (warp < kLoaders) {
         // -------------------------------------------------------- loads
@@ -229,7 +229,7 @@ __device__ __forceinline__ void mma_work(const PrefixArgs &a, uint8_t *smem) {
             const int lim0 = x.row0 + g < x.rows ? row_limit(a, x, x.row0 + g) : 0;
             const int lim1 = x.row0 + g + 8 < x.rows ? row_limit(a, x, x.row0 + g + 8) : 0;
             // tiles from the first that some row does not see whole on are masked
-            const int whole = kTree && x.tree ? max(x.off, 0) : (x.row0 + kTM <= x.rows ? row_limit(a, x, x.row0) : 0);
+            const int whole = tree_of(x) ? max(x.off, 0) : (x.row0 + kTM <= x.rows ? row_limit(a, x, x.row0) : 0);
             const int tok0 = static_cast<int>(fdiv(static_cast<uint32_t>(min(x.row0 + g, x.rows - 1)), a.div_g));
             const int tok1 = static_cast<int>(fdiv(static_cast<uint32_t>(min(x.row0 + g + 8, x.rows - 1)), a.div_g));
             float o[D / 8][4];
@@ -262,9 +262,11 @@ __device__ __forceinline__ void mma_work(const PrefixArgs &a, uint8_t *smem) {
                 const int kb = kt * kKT + key0 + 2 * t4;
                 const bool masked = whole - kt * kKT < kKT;
                 uint32_t seen0 = 0, seen1 = 0;  // from key kb on
-                if (kTree && masked) {
-                    seen0 = x.tree ? tree_bits(a, x, tok0, kb) : limit_bits(lim0, kb);
-                    seen1 = x.tree ? tree_bits(a, x, tok1, kb) : limit_bits(lim1, kb);
+                if constexpr (kTree) {
+                    if (masked) {
+                        seen0 = x.tree ? tree_bits(a, x, tok0, kb) : limit_bits(lim0, kb);
+                        seen1 = x.tree ? tree_bits(a, x, tok1, kb) : limit_bits(lim1, kb);
+                    }
                 }
 #pragma unroll
                 for (int n = 0; n < 2; ++n)

@@ -72,7 +72,7 @@ struct TcCfg {
     static_assert(kOffMisc % 16 == 0, "tensor memory's address is left on 16 bytes");
     static constexpr int kOffMl = (kOffMisc + 16 + 15) & ~15;        // [128] (m, l) of the second half
     static constexpr int kOffWalk = kOffMl + 128 * 8;   // [warps]
-    static constexpr int kSmem = kOffWalk + kWalks * static_cast<int>(sizeof(Walk<kTcTM, kTcKT, false>)) + 1024;  // + alignment slack
+    static constexpr int kSmem = kOffWalk + kWalks * static_cast<int>(sizeof(Walk<kTcTM, kTcKT, true>)) + 1024;  // + alignment slack
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -215,7 +215,7 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
 
     using Walker = Walk<kTcTM, kTcKT, kTree>;
     Walker &walk = reinterpret_cast<Walker *>(smem + C::kOffWalk)[warp];
-    const Piece &x = walk.x;
+    const auto &x = walk.x;
     walk.begin(a, line, start, t1 - t0);
     if (warp == 0 || warp == 2) {
         // -------------------------------------------------------- loads: K by warp 0, Q and V by warp 2
@@ -418,17 +418,18 @@ __device__ __forceinline__ void tc_work(const CUtensorMap &tmK, const CUtensorMa
             // counted from the current tile: keys of the problem, that this row sees, that all rows see
             int past = x.keys - (x.k0 + begin) * 128;
             int limit = (valid ? row_limit(a, x, row) : x.keys) - (x.k0 + begin) * 128;
-            int whole = (kTree && x.tree ? max(x.off, 0) : row_limit(a, x, first_row)) - (x.k0 + begin) * 128;
+            int whole = (tree_of(x) ? max(x.off, 0) : row_limit(a, x, first_row)) - (x.k0 + begin) * 128;
             const int tok = static_cast<int>(fdiv(static_cast<uint32_t>(valid ? row : x.row0), a.div_g));
             float m_run = -INFINITY, l_run = 0.f;
             for (int n = begin; n < all;) {
                 const bool mask = whole < 128;
                 uint32_t seen[4];  // the tile's columns that this row sees
-                if (kTree && mask) {
+                if constexpr (kTree) {
                     const int key = x.keys - past;
+                    if (mask)
 #pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        seen[w] = x.tree && valid ? tree_bits(a, x, tok, key + 32 * w) : limit_bits(limit, 32 * w);
+                        for (int w = 0; w < 4; ++w)
+                            seen[w] = x.tree && valid ? tree_bits(a, x, tok, key + 32 * w) : limit_bits(limit, 32 * w);
                 }
                 // Scores that the row does not see become -inf: columns 0 .. 63 of a tile or 64 .. 127.
                 auto hide = [&](int upper, uint32_t (&h)[64]) {

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kBlThreads, 2) tree_block_kernel(const __grid_
         length = length < 0 ? 0 : most;
         if (tid == 0) report(a.status, CP_ERR_PAGE);
     }
-    Piece x{};
+    TreePiece x{};
     x.b = b;
     x.kvh = kvh;
     x.tok0 = c0;

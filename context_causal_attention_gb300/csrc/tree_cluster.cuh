@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kClThreads, 1) tree_cluster_kernel(const __gri
         length = length < 0 ? 0 : most;
         if (tid == 0) report(a.status, CP_ERR_PAGE);
     }
-    Piece x{};
+    TreePiece x{};
     x.b = b;
     x.kvh = kvh;
     x.tok0 = c0;
