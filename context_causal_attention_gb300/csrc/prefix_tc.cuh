@@ -45,9 +45,12 @@ namespace cpattn {
 namespace {
 
 constexpr int kTcThreads = 384;
-// Pages of this many tokens or more are copied by TMA, smaller ones by cp.async
-// (see copy_tile).  Prompts and trees over 16384 keys in pages of 128 take 1063 us by TMA and
-// 1095 by cp.async, 64 trees of 16 rows in pages of 64 129 and 124.
+// Pages of this many tokens or more are copied by TMA, smaller ones by cp.async (see copy_tile).  By TMA and by cp.async, us
+// (32 / 8 heads of 128): 8 prompts of 512 over 16384 keys in pages of 64 908 and 945, of 128 905 and 940, 2000 tokens of a
+// prompt of 6000 164 and 169, 166 and 169, 64 single tokens over 32768 keys 75.0 and 76.4, 74.5 and 76.3.  Of little more
+// rows than that a tile's copies are what is waited for and cp.async is quicker: 64 x 4 tokens over 32768 keys 165 and 159, 160 and
+// 159, trees of 16 tokens of 64 sequences of up to 4096 142 and 136, 140 and 136, of 60 tokens of 24 over 16384 367 and 351
+// in both pages: the page alone decides, for the longest calls.
 constexpr int kTmaPage = 64;
 
 template <int D>

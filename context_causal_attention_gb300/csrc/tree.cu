@@ -148,18 +148,26 @@ const AtOnce &clusters_at_once() {
 }
 
 // Blocks of a cluster of tree_cluster.cuh, or 0 where it does not take the call: clusters are quick to begin and to
-// end, the line of prefix_call.cuh shares the keys of ragged sequences evenly and reads a prefix once, and a block an item
-// (tree_block.cuh) needs no join.  As many blocks as let all items run at once, two at least; not where the longest
-// sequence that the table can hold would make a block's share too many tiles of 128 keys.  Clusters and line, us
-// (16 tokens, 32 / 8 heads of 128, pages of 32, own keys up to the figure): one sequence of 4096 13.6 and 19.3, of 16000
-// 20.6 and 24.3; four of 4096 18.8 and 30, of 8000 31 and 40, ragged 26 and 32, of 16000 (31 tiles) 51 and 62, ragged 45 and 49;
-// seven of 6000 (24) 38 and 52, ragged 32 and 29; nine of 4096 (16) 35 and 50, ragged 27 and 34.  At D = 64 (16 / 4 heads) 16 of
-// 4000 ragged 19 and 24, of 8000 (31) 31 both, four of 32000 (31) 38 and 32.  Up to 16 rows the line has its narrow tiles:
-// four tokens of two sequences of 4000 keys, ragged, 13.1 and 15.9, of four (8) 14.8 and 17.3; at D = 64 of 16 (16) 17.9 and
-// 18.6.  A prefix is read once for each sequence: two of 500 behind 8000 20 and 25, four of 4000 behind 4000 (16) 24 and 32,
-// at D = 64 behind 16000 (39) 27 and 28.
-// Up to 640 keys a block an item is quicker, as it needs no meeting of blocks: one sequence of 16 tokens behind 500 keys
-// 9.9 us and 11.5, behind 800 12.8 and 11.4; nine 10.3 and 13.2, 13.2 and 13.8; at D = 64 two of 500 9.1 and 8.7.
+// end, the line of prefix_call.cuh shares the keys of ragged sequences evenly and reads a prefix once, and a block an
+// item (tree_block.cuh) needs no join.  As many blocks as let all items run at once, two at least; not where the
+// longest sequence that the table can hold would make a block's share more tiles of 128 keys than `tiles`.
+// Clusters and line in us (16 tokens, pages of 32; 32 / 8 heads at D = 128, 16 / 4 at 64; all sequences of the figure,
+// and up to it; tables as wide as the longest):
+//   D = 128   1 of 4096   14.7 18.7               9 of 4096   33.7 48.1, 27.5 36.4
+//             1 of 16000  23.0 28.0               9 of 8000   55.4 72.1, 42.8 45.4
+//             4 of 8000   31.3 39.8, 27.8 34.6    7 of 6000   39.0 51.9, 33.8 37.2
+//             4 of 16000  51.3 60.6, 44.9 47.3 (31 tiles)
+//   D = 64    8 of 8000   20.4 28.7, 19.2 23.2    16 of 4000  20.6 29.7, 19.4 23.6
+//             8 of 16000  32.3 39.9, 31.5 31.3    16 of 8000  32.9 40.6, 31.0 27.1 (31 tiles)
+//             4 of 24000  31.2 34.4, 30.2 26.6    4 of 32000 (beyond the limit) 38.6 39.6, 37.9 30.5
+// Near the limit ragged sequences would be better off by the line, by up to 15%, and others worse by as much or more:
+// which it is the host does not see.  Up to 16 rows the line has its narrow tiles and the limit is lower: four tokens of
+// up to 4000 keys of two sequences 14.2 and 19.0, of four 16.8 and 20.7, at D = 64 of 16 18.2 and 17.9 (all of 4000
+// 19.0, 23.0).  A prefix is read once for each sequence, and the limit is lower at D = 128: two of 500 behind 8000 22.0
+// and 24.8, four of 4000 behind 4000 26.6 and 37.2, at D = 64 behind 16000 27.1 and 30.0.
+// Up to 640 keys a block an item is quicker, as it needs no meeting of blocks.  Blocks and clusters: one sequence of 500
+// keys 8.7 and 12.0, of 640 9.8 and 11.5, of 800 11.6 and 11.2, of 1300 16.2 and 11.2; nine of 640 10.8 and 14.7, of
+// 800 12.7 and 15.2, of 1300 17.6 and 17.7; at D = 64 two of 500 8.0 and 9.2, of 640 8.9 and 8.7, of 1300 14.9 and 8.5.
 template <int D>
 int cluster_blocks(const ClusterArgs &c, int64_t rows) {
     const PrefixArgs &a = c.p;
@@ -173,19 +181,24 @@ int cluster_blocks(const ClusterArgs &c, int64_t rows) {
     return 0;
 }
 
-// Whether a block an item (tree_block.cuh), two on an SM, takes the call, rather than the line.  A tile of 64
-// keys takes a block 0.75 us, so the longest sequence that the table holds takes 0.75 k, k its tiles, and all
-// items together, half as long on average, items k / 2 x 0.75 / 304 at best (measured 1.3 times that: half of the time
-// memory is what they wait for).  The line reads the keys once for 256 rows, a prefix once for all sequences,
-// whatever the lengths, at 5 TB/s (6.5 by its narrow tiles), and takes 20 us (13) and 0.05 us (0.03) an item of its own
-// besides.  Block and line, us (16 tokens, 32 / 8 heads of 128, pages of 16, own keys up to the figure, ragged): 16 sequences of 4096
-// 47 and 50, of 8000 87 and 71 (not ragged 94 and 113), 32 of 8000 109 and 115, 64 of 4096 85 and 126, of 8000 159 and 200; 300 of
-// 500 78 and 175, of 1000 117 and 220; 27 tokens of 100 of 1000 58 and 97, 60 tokens of 60 59 and 81, 120 of 60 of 2000
-// 163 both, 500 of 8 of 1000 not ragged 152 and 138; a prompt of 1000 tokens 30 and 47, four 92 and 117.  Single tokens of 20 sequences of 500 11.2 and 16.1, of 4000 47 and 38, 64 of 4000 87 and 102.  Behind a prefix
-// of 500 64 of 1000 44 and 103, 200 of 300 81 and 162, of 2000 79 and 116, 184 and 192.  At D = 64 (16 / 4 heads) 40 of
-// 4000 40 and 36, 64 47 and 58, 200 95 and 118.
-// Beyond 8192 keys the line gains by itself (64 of 16000 310 and 349), and one long sequence among short ones would leave
-// a block alone with it.
+// Whether a block an item (tree_block.cuh), two on an SM, takes the call, rather than the line.  A tile of 64 keys takes
+// a block 0.75 us, so the longest sequence that the table holds takes 0.75 k, k its tiles, and all items together, half
+// as long on average, items k / 2 x 0.75 / 304 at best (measured 1.3 times that: half of the time memory is what they
+// wait for).  The line reads the keys once for 256 rows, a prefix once for all sequences, whatever the lengths, at
+// 5 TB/s (6.5 by its narrow tiles), and takes 20 us (13) and 0.05 us (0.03) an item of its own besides.
+// Block and line in us (16 tokens, 32 / 8 heads of 128, pages of 16, own keys up to the figure, tables as wide):
+//   16 of 4096   47  55    64 of 8000    153 192    300 of 500    83 199    27 tokens, 100 of 1000  77 117
+//   32 of 8000  106 122    64 all of it  307 369    300 of 1000  115 236    60 tokens, 60 of 60     39  76
+//   1 token, 20 of 500 11 17, 64 of 4000 84 93; prompts of 1000: one 27 46, four 84 111, eight 159 185; 500 tokens of
+//   eight prompts of 1000 108 123, 200 of 16 99 118; behind a prefix of 500 64 of 1000 43 110, 200 of 300 82 208, behind
+//   one of 2000 64 of 1000 79 126; at D = 64 (16 / 4 heads) 64 of 4000 46 64, 200 of 4000 93 126.
+// and where it takes the line: 16 of 8000 83 64 (all of it 95 113), 1 token of 20 of 4000 45 37, 60 tokens, 120 of
+//   2000 243 235.
+// The estimates know neither the rows' own work nor which tokens are a prompt's, and are wrong in places: the block is
+// taken for trees of 500 tokens of eight sequences of 1000 keys (152 138) and for 500 tokens of four prompts of 2000
+// (108 94), the line for 200 of 300 behind 2000 (191 264) and 40 of 4000 at D = 64 (42 46).
+// Beyond 8192 keys the line is taken as one long sequence among short ones would leave a block alone with it (64 of
+// 16000 are quicker by blocks, 324 372).
 constexpr int kBlMost = 8192;
 template <int D>
 bool items_pay(const ClusterArgs &c, int64_t rows) {

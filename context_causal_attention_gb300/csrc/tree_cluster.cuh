@@ -2,10 +2,10 @@
 // the work, partials in global memory or a second launch.
 //
 // Few sequences are latency: a tree of 27 tokens over 4096 keys takes 19 us by the line of prefix_call.cuh (its scan, the
-// search of a block's place, the partials' way through global memory, the join) and 12 so, where the keys take 3.  Here a cluster of up to 16 blocks
-// takes one item -- 128 rows (tokens x the G query heads of a KV head) of one sequence -- and its blocks an equal share
-// of the item's key tiles each, first the prefix's and then the sequence's own.  Where a block works follows from
-// its index alone, and the blocks join their partials through each other's shared memory.
+// search of a block's place, the partials' way through global memory, the join) and 13 so, where the keys take 3.  Here
+// a cluster of up to 16 blocks takes one item -- 128 rows (tokens x the G query heads of a KV head) of one sequence --
+// and its blocks an equal share of the item's key tiles each, first the prefix's and then the sequence's own.  Where a
+// block works follows from its index alone, and the blocks join their partials through each other's shared memory.
 //
 // Inside a block, as in prefix_tc.cuh: two halves of four softmax warps take the key tiles in turn, S = Q K^T and
 // O += P V on tcgen05 with S, P and O in tensor memory (S0 | S1 | O0 | O1), a thread a row.  K and V come by 16-byte
@@ -79,6 +79,7 @@ __device__ __forceinline__ uint32_t cluster_size32() {
 }
 // By all threads of all blocks of the cluster: what they wrote before is seen behind it, and what they read before is read
 // from what stood there before it (also a value that nobody waits for, as those of the join's pieces of weight 0).
+// The release is 0.6 us of the 13 at the end of a row tile, before the results' stores as well as behind them.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");

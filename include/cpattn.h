@@ -646,6 +646,9 @@ cp_status cp_prefix_attn_fwd(const void *q, const void *k_cache, const void *v_c
  * range that the step meets, in the table or on the stack, sets the status word too, but the step goes on: its rows
  * get slot -1, a page that is given back or taken moves as it is, and n_free_out[1] stays 0.  Sizes as for
  * cp_cache_append.
+ * This call and the four below let a kernel that follows them with programmatic stream serialization start before
+ * they end: as behind any such kernel it waits for them itself (cudaGridDependencySynchronize) before it touches what
+ * they read or write.  Kernels launched without it are behind them as always.
  */
 cp_status cp_cache_plan(const int32_t *kv_had, const int32_t *kv_keep, const int32_t *n_new, int64_t B, int32_t *table,
                         int64_t max_pages, int64_t page_size, int32_t *free_pages, int64_t n_pages,
@@ -716,7 +719,8 @@ cp_status cp_tree_plan(const int32_t *parent, const int32_t *cu_new, const int32
  * wider than the step needs is worth up to half of the time where it holds a few thousand tokens a sequence.
  * A row that sees one key gets that key's value itself, for scores scale <q, k> up to 2^14 in size.
  * Everything else as for cp_prefix_attn_fwd, but that a NaN or infinity in any V row of a sequence's own keys may
- * reach its other rows (also one that no row's mask has).
+ * reach its other rows (also one that no row's mask has), and that kernels behind it may start early as behind
+ * cp_cache_plan.
  */
 cp_status cp_tree_attn_workspace_size(int64_t R, int64_t B, int64_t max_new, int64_t words, int64_t prefix_len,
                                       int64_t N, int64_t Nkv, int64_t D, int64_t page_size, int64_t max_pages,
